@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -21,7 +22,9 @@ FMT = {"fp16": 0, "bf16": 1, "fp32": 2}
 VARIANT = {"auto": 0, "online": 1, "certified": 2, "online_lazy": 3}
 DTYPE = {torch.bfloat16: 0, torch.float16: 1}
 STATUS = {0: "CLIS_OK", 1: "CLIS_ERR_INVALID_ARG", 2: "CLIS_ERR_UNSUPPORTED", 3: "CLIS_ERR_MISALIGNED",
-          4: "CLIS_ERR_WORKSPACE", 5: "CLIS_ERR_CUDA", 6: "CLIS_ERR_TIMEOUT"}
+          4: "CLIS_ERR_WORKSPACE", 5: "CLIS_ERR_CUDA", 6: "CLIS_ERR_TIMEOUT", 7: "CLIS_ERR_DATA"}
+# Bits of the device error word that the calls around a paged cache set (include/clis.h).
+PAGED_INDEX_BIT, PAGED_POOL_BIT, PAGED_LENGTH_BIT = 1 << 16, 1 << 17, 1 << 18
 
 
 class ClisError(RuntimeError):
@@ -44,6 +47,20 @@ class Cert(ctypes.Structure):
 
 
 CERT_WORDS = ctypes.sizeof(Cert) // 4  # a certificate is 8 32-bit words
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "B", "Hq", "Hk", "N", "d", "pairs", "axes", "interleaved", "inverse",
+        "q_sb", "q_sh", "q_sn", "k_sb", "k_sh", "k_sn", "qo_sb", "qo_sh", "qo_sn", "ko_sb", "ko_sh", "ko_sn",
+        "p_sb", "p_sn", "p_sa", "dtype")]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "S", "T", "H", "Hkv", "d", "page_size", "num_pages", "width", "q_st", "q_sh", "o_st", "o_sh",
+        "kc_sp", "kc_sh", "kc_sn", "vc_sp", "vc_sh", "vc_sn", "bt_ss", "dtype")]
+
 
 _lib = None
 
@@ -112,6 +129,17 @@ def load_library():
     lib.clis_host_plan_wait.restype = i32
     lib.clis_host_plan_destroy.argtypes = [vp]
     lib.clis_host_plan_destroy.restype = i32
+    rp, pp, i64 = ctypes.POINTER(RopeDesc), ctypes.POINTER(PagedDesc), ctypes.c_int64
+    lib.clis_rope.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.clis_rope.restype = i32
+    lib.clis_paged_plan.argtypes = [pp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+    lib.clis_paged_plan.restype = i32
+    lib.clis_paged_append.argtypes = [pp, rp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.clis_paged_append.restype = i32
+    lib.clis_attn_paged_workspace_size.argtypes = [pp, i64, ctypes.POINTER(sz)]
+    lib.clis_attn_paged_workspace_size.restype = i32
+    lib.clis_attn_fwd_paged.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, i64, f32, i32, vp, sz, vp]
+    lib.clis_attn_fwd_paged.restype = i32
     _lib = lib
     return lib
 
@@ -451,15 +479,19 @@ class AttentionFunction(torch.autograd.Function):
         return dq, dk, dv, None, None, None
 
 
-def attention_autograd(q, k, v, softmax_scale: float | None = None, causal: bool = False, variant: str = "auto"):
-    """Differentiable CLiS attention (training): o = attention(q, k, v)."""
+def attention_autograd(q, k, v, softmax_scale: float | None = None, causal: bool = False, variant: str = "auto",
+                       rope: Rope | None = None):
+    """Differentiable CLiS attention (training): o = attention(q, k, v).  With
+    ``rope``, of the rotated q and k; gradients are with respect to the given ones."""
+    if rope is not None:
+        q, k = rope_autograd(q, k, *rope)
     return AttentionFunction.apply(q, k, v, softmax_scale, causal, variant)
 
 
 def clis_get_device_error() -> int:
     code = ctypes.c_uint32(0)
     st = load_library().clis_get_device_error(ctypes.byref(code))
-    if st not in (0, 6):
+    if st not in (0, 6, 7):
         raise ClisError("clis_get_device_error", st)
     return code.value
 
@@ -534,8 +566,11 @@ def grouped_query_views(q, k, v, out=None):
 
 def attention(q, k, v, softmax_scale: float | None = None, causal: bool = False,
               variant: str = "auto", return_certs: bool = False, device=None, out=None,
-              groups: int | None = None, non_blocking: bool = False, pv: str = "bf16"):
+              groups: int | None = None, non_blocking: bool = False, pv: str = "bf16", rope: Rope | None = None):
     """CLiS attention forward: certification pre-pass, then the fused kernel.
+
+    ``rope`` (device tensors): q and k are rotated by their positions first
+    (:func:`rope_qk`); the certificate is that of the rotated heads.
 
     q, k, v: bf16 or fp16 [B, H, N, d].  Device tensors are processed in place
     on the current stream.  Host tensors (pinned for overlap) go through the
@@ -567,6 +602,8 @@ def attention(q, k, v, softmax_scale: float | None = None, causal: bool = False,
     """
     if pv not in ("bf16", "fp8"):
         raise ValueError(f"pv must be 'bf16' or 'fp8', not {pv!r}")
+    if rope is not None:
+        q, k = rope_qk(q, k, *rope)
     if k.shape[1] != q.shape[1]:
         if q.device.type == "cpu":
             raise ValueError("grouped key/value heads take device tensors")
@@ -716,6 +753,366 @@ def host_done_event(device=None):
     waits for it (``stream.wait_event(...)``) is ordered after that call's
     output, and ``.synchronize()`` waits for it on the host."""
     return _host_done.get(torch.device(device or "cuda:0"))
+
+
+# ------------------------------------------------------- rotary positions
+
+
+class Rope(NamedTuple):
+    """Rotary positions: ``positions`` int32 [B, N, axes] (or [N, axes], shared by
+    the batch), ``inv_freq`` float64 [pairs] (radians per position of each pair)
+    and ``axis`` int32 [pairs] (which of a token's positions turns the pair);
+    pairs are elements (p, p + pairs) of a row, or (2p, 2p + 1) if
+    ``interleaved``.  Elements from 2 * pairs on pass through."""
+    positions: torch.Tensor
+    inv_freq: torch.Tensor
+    axis: torch.Tensor
+    interleaved: bool = False
+
+
+def _check(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(device, stream=None):
+    """(context that makes ``device`` current if it is not, raw stream handle)."""
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device), (stream or torch.cuda.current_stream(device)).cuda_stream
+    return None, (stream or torch.cuda.current_stream()).cuda_stream
+
+
+def _call(name: str, device, stream, *args) -> None:
+    """The library's ``name`` on ``device`` and ``stream`` (default: current)."""
+    ctx, raw = _on(device, stream)
+    fn = getattr(load_library(), name)
+    if ctx is None:
+        st = fn(*args, raw)
+    else:
+        with ctx:
+            st = fn(*args, raw)
+    if st != 0:
+        raise ClisError(name, st)
+
+
+def _check_rope_table(positions, inv_freq, axis, device) -> None:
+    _check(positions.dtype == torch.int32, "positions must be int32")
+    _check(inv_freq.dtype == torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous(),
+           "inv_freq must be a contiguous float64 tensor [pairs]")
+    _check(axis.dtype == torch.int32 and axis.shape == inv_freq.shape and axis.is_contiguous(),
+           "axis must be a contiguous int32 tensor [pairs]")
+    _check(positions.device == device and inv_freq.device == device and axis.device == device,
+           "positions, inv_freq and axis must be on the device of q")
+
+
+def clis_rope(q, k, positions, inv_freq, axis, interleaved: bool = False, inverse: bool = False, q_out=None,
+              k_out=None, stream=None):
+    """q [B, H, N, d] and k [B, H_kv, N, d] (or None) rotated by their positions
+    (see :class:`Rope`), or back with ``inverse``; returns (q', k').  q_out and
+    k_out may be q and k themselves."""
+    _check(q.is_cuda and q.dim() == 4 and q.dtype in DTYPE and q.stride(-1) == 1,
+           "q must be a bfloat16 or float16 device tensor [B, H, N, d] with a contiguous last dimension")
+    B, H, N, d = q.shape
+    dev = q.device
+    if positions.dim() == 2:
+        positions = positions[None]
+    _check(positions.dim() == 3 and positions.shape[0] in (1, B) and positions.shape[1] == N,
+           "positions must be [B, N, axes] or [N, axes]")
+    _check_rope_table(positions, inv_freq, axis, dev)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    pairs = [("q_out", q_out, q)]
+    Hk = 0
+    if k is not None:
+        _check(k.dim() == 4 and k.dtype == q.dtype and k.device == dev and k.stride(-1) == 1
+               and k.shape[0] == B and k.shape[2:] == q.shape[2:], "k must match q in all but its number of heads")
+        Hk = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        pairs.append(("k_out", k_out, k))
+    for name, t, like in pairs:
+        _check(t.shape == like.shape and t.dtype == q.dtype and t.device == dev and t.stride(-1) == 1,
+               f"{name} must have its input's shape, dtype and device and a contiguous last dimension")
+    qs, os, zero = q.stride(), q_out.stride(), (0, 0, 0)
+    ks, kos = (k.stride(), k_out.stride()) if k is not None else (zero, zero)
+    ps = positions.stride()
+    desc = RopeDesc(B, H, Hk, N, d, inv_freq.numel(), positions.shape[2], int(bool(interleaved)), int(bool(inverse)),
+                    qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], os[0], os[1], os[2], kos[0], kos[1], kos[2],
+                    ps[0] if positions.shape[0] > 1 else 0, ps[1], ps[2], DTYPE[q.dtype])
+    _call("clis_rope", dev, stream, desc, q.data_ptr(), k.data_ptr() if k is not None else None, q_out.data_ptr(),
+          k_out.data_ptr() if k is not None else None, positions.data_ptr(), inv_freq.data_ptr(), axis.data_ptr())
+    return q_out, (k_out if k is not None else None)
+
+
+def rope_qk(q, k, positions, inv_freq, axis, interleaved: bool = False):
+    """(q', k'): q and k (or None) rotated by their positions; see :class:`Rope`."""
+    return clis_rope(q, k, positions, inv_freq, axis, interleaved)
+
+
+rope = rope_qk
+
+
+class RopeFunction(torch.autograd.Function):
+    """Rotation of q and k; the gradient is the rotation back (itself
+    differentiable).  The angles carry no gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, axis, interleaved, inverse):
+        ctx.save_for_backward(positions, inv_freq, axis)
+        ctx.interleaved, ctx.inverse = interleaved, inverse
+        ctx.set_materialize_grads(False)
+        return clis_rope(q, k, positions, inv_freq, axis, interleaved, inverse)
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        need = [g.contiguous() if g is not None and n else None for g, n in zip((gq, gk), ctx.needs_input_grad)]
+        some = [g for g in need if g is not None]
+        if not some:
+            return (None,) * 7
+        back = RopeFunction.apply(some[0], some[1] if len(some) > 1 else None, *ctx.saved_tensors, ctx.interleaved,
+                                  not ctx.inverse)
+        back = iter(back)
+        return tuple(next(back) if g is not None else None for g in need) + (None,) * 5
+
+
+def rope_autograd(q, k, positions, inv_freq, axis, interleaved: bool = False):
+    """Differentiable :func:`rope_qk` (training)."""
+    return RopeFunction.apply(q, k, positions, inv_freq, axis, bool(interleaved), False)
+
+
+# -------------------------------------------------- paged key/value cache
+
+
+class PagedPlan(NamedTuple):
+    """What :func:`paged_plan` derives from a step's lengths: ``cu_q`` int32 [S + 1],
+    ``kv_len`` int32 [S], ``slots`` int64 [T], ``positions`` int32 [T], ``ring_state``
+    int64 [2] (head and tail of the ring of free pages after the step)."""
+    cu_q: torch.Tensor
+    kv_len: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    ring_state: torch.Tensor
+
+
+def _check_int(t, dtype, shape, device, name: str) -> None:
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on the same device")
+
+
+def clis_paged_plan(ctx_len, new_len, block_table, ring, ring_state, page_size: int, num_tokens: int,
+                    num_pages: int | None = None, stream=None) -> PagedPlan:
+    """Block tables, slots and positions of a step from the lengths of its
+    sequences, on the GPU: ctx_len, new_len int32 [S] (cached and new tokens; new
+    < 0: the sequence is finished and gives its pages back), block_table int32
+    [S, width] (completed in place), ring int32 [ring size] (free pages; pages
+    given back are written into it), ring_state int64 [2] (its head and tail,
+    not changed).  num_tokens: rows of the packed batch, at least the sum of the
+    new tokens.  num_pages: pages of the cache (default: the ring's size)."""
+    dev = ctx_len.device
+    _check(ctx_len.is_cuda and ctx_len.dim() == 1, "ctx_len must be an int32 device tensor [S]")
+    S = ctx_len.shape[0]
+    _check_int(ctx_len, torch.int32, ctx_len.shape, dev, "ctx_len")
+    _check_int(new_len, torch.int32, ctx_len.shape, dev, "new_len")
+    _check_int(ring_state, torch.int64, (2,), dev, "ring_state")
+    _check(ring.dim() == 1, "ring must be an int32 tensor [ring size]")
+    _check_int(ring, torch.int32, ring.shape, dev, "ring")
+    _check(block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.device == dev
+           and block_table.shape[0] == S and block_table.stride(1) == 1,
+           "block_table must be an int32 tensor [S, width] with contiguous rows on the same device")
+    T = int(num_tokens)
+    _check(T >= 0, "num_tokens must not be negative")
+    # One allocation for the five outputs: 8-byte values first.
+    buf = torch.empty(2 + T + (2 * S + 1 + T + 1) // 2 + 1, dtype=torch.int64, device=dev)
+    state, slots, small = buf[:2], buf[2:2 + T], buf[2 + T:].view(torch.int32)
+    cu, kv, pos = small[:S + 1], small[S + 1:2 * S + 1], small[2 * S + 1:2 * S + 1 + T]
+    desc = PagedDesc(S, T, 0, 0, 0, int(page_size), ring.shape[0] if num_pages is None else int(num_pages),
+                     block_table.shape[1])
+    desc.bt_ss = block_table.stride(0) if S > 1 else block_table.shape[1]
+    at = buf.data_ptr()
+    at32 = at + 8 * (2 + T)
+    _call("clis_paged_plan", dev, stream, desc, ctx_len.data_ptr(), new_len.data_ptr(), block_table.data_ptr(),
+          ring.data_ptr(), ring.shape[0], ring_state.data_ptr(), at, at32, at32 + 4 * (S + 1), at + 16,
+          at32 + 4 * (2 * S + 1))
+    return PagedPlan(cu, kv, slots, pos, state)
+
+
+paged_plan = clis_paged_plan
+
+
+def _cache_desc(k_cache, v_cache, T: int, H: int, d: int, dtype, device) -> PagedDesc:
+    _check(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[3] == d,
+           "k_cache and v_cache must be [pages, H_kv, page_size, d]")
+    _check(k_cache.dtype == dtype and v_cache.dtype == dtype, "the caches must have the dtype of q, k and v")
+    _check(k_cache.device == device and v_cache.device == device, "the caches must be on the device of q, k and v")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    _check(ks[3] == 1 and vs[3] == 1, "the caches must have a contiguous last dimension")
+    pages, Hkv, page = k_cache.shape[:3]
+    return PagedDesc(0, T, H, Hkv, d, page, pages, 1, 0, 0, 0, 0, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], 0,
+                     DTYPE[dtype])
+
+
+def clis_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, inv_freq=None, axis=None,
+                      interleaved: bool = False, q_out=None, stream=None):
+    """Writes k, v [T, H_kv, d] into the caches [pages, H_kv, page_size, d] at their
+    slots (int64 [T], page * page_size + row; negative: nowhere; distinct),
+    rotated by ``positions`` (int32 [T, axes] or [T]) if given, and returns q
+    [T, H, d] rotated by them (None without q).  Any strides with a contiguous last
+    dimension; q_out may be q."""
+    _check(k.is_cuda and k.dim() == 3 and k.dtype in DTYPE and k.stride(2) == 1,
+           "k must be a bfloat16 or float16 device tensor [T, H_kv, d] with a contiguous last dimension")
+    T, Hk, d = k.shape
+    dev = k.device
+    _check(v.shape == k.shape and v.dtype == k.dtype and v.device == dev and v.stride(2) == 1, "v must match k")
+    H = Hk
+    if q is not None:
+        _check(positions is not None, "q is rotated: positions are needed")
+        _check(q.dim() == 3 and q.shape[0] == T and q.shape[2] == d and q.dtype == k.dtype and q.device == dev
+               and q.stride(2) == 1, "q must match k in all but its number of heads")
+        H = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        _check(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.device == dev and q_out.stride(2) == 1,
+               "q_out must match q")
+    desc = _cache_desc(k_cache, v_cache, T, H, d, k.dtype, dev)
+    _check(desc.Hkv == Hk, "the caches must have k's number of heads")
+    _check_int(slots, torch.int64, (T,), dev, "slots")
+    ks, vs = k.stride(), v.stride()
+    r = RopeDesc(1, 0 if q is None else H, Hk, T, d, dtype=DTYPE[k.dtype])
+    r.k_sh, r.k_sn = ks[1], ks[0]
+    ptrs = (None, None, None)
+    if positions is not None:
+        if positions.dim() == 1:
+            positions = positions[:, None]
+        _check(positions.dim() == 2 and positions.shape[0] == T, "positions must be [T, axes] or [T]")
+        _check(inv_freq is not None and axis is not None, "positions need inv_freq and axis")
+        _check_rope_table(positions, inv_freq, axis, dev)
+        r.pairs, r.axes, r.interleaved = inv_freq.numel(), positions.shape[1], int(bool(interleaved))
+        r.p_sn, r.p_sa = positions.stride()
+        ptrs = (positions.data_ptr(), inv_freq.data_ptr(), axis.data_ptr())
+        _check(r.pairs > 0, "inv_freq is empty")
+    if q is not None:
+        (r.q_sn, r.q_sh), (r.qo_sn, r.qo_sh) = q.stride()[:2], q_out.stride()[:2]
+    _call("clis_paged_append", dev, stream, desc, r, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          vs[0], vs[1], None if q is None else q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          slots.data_ptr(), *ptrs)
+    return q_out if q is not None else None
+
+
+paged_append = clis_paged_append
+
+
+def clis_attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: int, scale_log2: float,
+                        causal: bool = True, out=None, lse2=None, workspace=None, stream=None):
+    """Attention of the new tokens q [T, H, d] (those of sequence s are rows cu_q[s] ..
+    cu_q[s + 1] - 1) over their sequences' cached keys; returns ``out``.  ``lse2``:
+    optional float32 [T, H].  Rows that belong to no sequence are not written."""
+    _check(q.is_cuda and q.dim() == 3 and q.dtype in DTYPE and q.stride(2) == 1,
+           "q must be a bfloat16 or float16 device tensor [T, H, d] with a contiguous last dimension")
+    T, H, d = q.shape
+    dev = q.device
+    desc = _cache_desc(k_cache, v_cache, T, H, d, q.dtype, dev)
+    _check(block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.device == dev
+           and block_table.stride(1) == 1, "block_table must be an int32 tensor [S, width] with contiguous rows")
+    S, width = block_table.shape
+    _check_int(cu_q, torch.int32, (S + 1,), dev, "cu_q")
+    _check_int(kv_len, torch.int32, (S,), dev, "kv_len")
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    _check(out.shape == q.shape and out.dtype == q.dtype and out.device == dev and out.stride(2) == 1,
+           "out must match q")
+    if lse2 is not None:
+        _check_int(lse2, torch.float32, (T, H), dev, "lse2")
+    desc.S, desc.width, desc.bt_ss = S, width, block_table.stride(0) if S > 1 else 0
+    (desc.q_st, desc.q_sh), (desc.o_st, desc.o_sh) = q.stride()[:2], out.stride()[:2]
+    n = ctypes.c_size_t(0)
+    ctx, raw = _on(dev, stream)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
+        lib = load_library()
+        st = lib.clis_attn_paged_workspace_size(desc, max_q, n)
+        if st != 0:
+            raise ClisError("clis_attn_paged_workspace_size", st)
+        if workspace is None:
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+            if stream is not None:  # allocated on the current stream, used on the given one
+                workspace.record_stream(stream)
+        _check(workspace.device == dev and workspace.is_contiguous(),
+               "the workspace must be contiguous and on the device of q")
+        st = lib.clis_attn_fwd_paged(desc, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                     block_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
+                                     None if lse2 is None else lse2.data_ptr(), max_q, float(scale_log2),
+                                     int(bool(causal)), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), raw)
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
+    if st != 0:
+        raise ClisError("clis_attn_fwd_paged", st)
+    return out
+
+
+def attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: int | None = None,
+                    softmax_scale: float | None = None, causal: bool = True, out=None, return_lse: bool = False):
+    """Attention of new tokens over a paged cache: any mix of single tokens, drafted
+    tokens and chunks in one call (grouped-query heads by q's and the caches'
+    head counts).  max_q: the most new tokens of a sequence (default: all rows of q).
+    With ``return_lse``: (out, lse2 float32 [T, H])."""
+    T = q.shape[0]
+    lse2 = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+    o = clis_attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max(1, T if max_q is None else int(max_q)),
+                            scale_log2_for(q.shape[-1], softmax_scale), causal, out, lse2)
+    return (o, lse2) if return_lse else o
+
+
+class PagedCache:
+    """Paged key/value cache of a model's layers with its block tables and its ring
+    of free pages, all on the device: a step is :meth:`begin` with the new tokens
+    of each sequence, then :meth:`attend` once per layer.  Nothing is read back,
+    so a step can be captured in a graph and replayed with other lengths.
+
+        cache = PagedCache(layers=2, num_pages=4096, num_kv_heads=8, d=128, max_seqs=64, max_len=32768)
+        plan = cache.begin(new_len, num_tokens)          # int32 [max_seqs], rows of the packed batch
+        for i in range(2):
+            o = cache.attend(i, q[i], k[i], v[i], plan, max_q, rope=(inv_freq, axis, False))
+    """
+
+    def __init__(self, layers: int, num_pages: int, num_kv_heads: int, d: int, max_seqs: int, max_len: int,
+                 page_size: int = 64, dtype=torch.bfloat16, device="cuda"):
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        shape = (layers, num_pages, num_kv_heads, page_size, d)
+        self.k, self.v = (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
+        self.page_size = page_size
+        self.block_table = torch.full((max_seqs, -(-max_len // page_size)), -1, dtype=torch.int32, device=dev)
+        self.ring = torch.arange(num_pages, dtype=torch.int32, device=dev)
+        self.ring_state = torch.tensor([0, num_pages], dtype=torch.int64, device=dev)
+        self.lens = torch.zeros(max_seqs, dtype=torch.int32, device=dev)
+
+    def begin(self, new_len, num_tokens: int) -> PagedPlan:
+        """Plan of a step that adds new_len[s] tokens to sequence s (0: not part of
+        the step, negative: finished, its pages are free again), ``num_tokens``
+        rows in all (rows behind the last token are padding)."""
+        plan = clis_paged_plan(self.lens, new_len, self.block_table, self.ring, self.ring_state, self.page_size,
+                               num_tokens)
+        self.lens.copy_(plan.kv_len)
+        self.ring_state.copy_(plan.ring_state)
+        return plan
+
+    def attend(self, layer: int, q, k, v, plan: PagedPlan, max_q: int | None = None, rope=None, positions=None,
+               softmax_scale: float | None = None, causal: bool = True, out=None):
+        """Writes the step's k, v [T, H_kv, d] of ``layer`` into the cache and returns
+        the attention of q [T, H, d] over it.  ``rope``: (inv_freq, axis,
+        interleaved) rotates q and k by ``positions`` (int32 [T, axes], default
+        the tokens' places in their sequences)."""
+        kc, vc = self.k[layer], self.v[layer]
+        if rope is not None:
+            q = clis_paged_append(k, v, kc, vc, plan.slots, q=q, positions=plan.positions if positions is None else positions,
+                                  inv_freq=rope[0], axis=rope[1], interleaved=rope[2] if len(rope) > 2 else False)
+        else:
+            clis_paged_append(k, v, kc, vc, plan.slots)
+        return attention_paged(q, kc, vc, self.block_table, plan.cu_q, plan.kv_len, max_q, softmax_scale, causal, out)
 
 
 load_library()

@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "clis_internal.h"
+#include "paged_internal.h"
 
 namespace {
 
@@ -477,6 +478,7 @@ const char *clis_status_string(clis_status_t s)
     case CLIS_ERR_WORKSPACE: return "workspace missing or too small";
     case CLIS_ERR_CUDA: return "CUDA call or kernel launch failed";
     case CLIS_ERR_TIMEOUT: return "a kernel pipeline wait timed out";
+    case CLIS_ERR_DATA: return "device data out of range";
     }
     return "unknown status";
 }
@@ -565,14 +567,23 @@ clis_status_t clis_get_device_error(uint32_t *code)
     clis_status_t st = clis::read_device_error(&fwd);
     if (st == CLIS_ERR_CUDA) return st;
     if (clis::read_bwd_error(&bwd) != CLIS_OK) return CLIS_ERR_CUDA;
-    *code = fwd | bwd;
-    return *code ? CLIS_ERR_TIMEOUT : CLIS_OK;
+    uint32_t rot = 0, plan = 0, dec = 0, chunk = 0;
+    if (clis::read_rot_error(&rot) != CLIS_OK || clis::read_plan_error(&plan) != CLIS_OK ||
+        clis::read_decode_error(&dec) != CLIS_OK || clis::read_chunk_error(&chunk) != CLIS_OK)
+        return CLIS_ERR_CUDA;
+    *code = fwd | bwd | rot | plan | dec | chunk;
+    if (*code & ~(CLIS_PAGED_INDEX_BIT | CLIS_PAGED_POOL_BIT | CLIS_PAGED_LENGTH_BIT)) return CLIS_ERR_TIMEOUT;
+    return *code ? CLIS_ERR_DATA : CLIS_OK;
 }
 
 clis_status_t clis_clear_device_error(void)
 {
     clis_status_t st = clis::clear_device_error();
-    return st != CLIS_OK ? st : clis::clear_bwd_error();
+    if (st == CLIS_OK) st = clis::clear_bwd_error();
+    if (st == CLIS_OK) st = clis::clear_rot_error();
+    if (st == CLIS_OK) st = clis::clear_plan_error();
+    if (st == CLIS_OK) st = clis::clear_decode_error();
+    return st != CLIS_OK ? st : clis::clear_chunk_error();
 }
 
 clis_status_t clis_debug_wait_selftest(uint32_t limit_us, clis_stream_t stream)

@@ -1,0 +1,698 @@
+// paged_decode.cu -- attention of a few new query rows per sequence (single
+// tokens, drafted tokens) over a paged key/value cache.
+//
+//   x_ij = scale_log2 * q_i . k_j,  o_i = sum_j 2^(x_ij - m_i) v_j / sum_j 2^(x_ij - m_i)
+//
+// over the keys j < visible(i), with the running shift m_i raised only when a
+// row's maximum outgrew it by 2^8 (the rescale is then rare).
+//
+// Bound: the cache's bytes.  All n * g query rows of a (sequence, key/value
+// head) pair share each key and value that is loaded, in one m16n8k16 row tile
+// (MT = 1) or two (MT = 2); 16 rows cost 64 flops per byte of cache, far below
+// what even the warp-level matrix instructions deliver, so the tensor cores of
+// the chunk kernel would gain nothing here.
+//
+//  * Work: paged_sched.h lays all items' 64-key units end to end and gives
+//    every block an equal run, so ragged lengths balance; an item that crosses
+//    a cut leaves partial results (unnormalised o, m, l) that
+//    paged_decode_join_kernel adds in a fixed order.
+//  * Loads: each of the block's four warps takes 16 of a unit's 64 keys and runs
+//    its own ring of cp.async stages: no block-wide barrier inside an item, and
+//    the ring runs on into the next item, so item ends do not drain it.  Rows
+//    past the length are filled with zeros by the copy itself: what a page
+//    holds behind the last key is never multiplied (0 * NaN would be NaN).
+//  * P is rounded to the data type (bf16: off by up to 2^-8 of each weight) as
+//    the matrix instructions take it; the row sum adds the unrounded values,
+//    and o, m, l stay in fp32.
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "clis_internal.h"
+#include "paged_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace clis {
+
+__device__ unsigned int g_decode_error_word = 0;
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTileKeys = kDecodeKeys / kWarps;  // 16 keys per warp and unit
+constexpr float kTau = 8.0f;
+constexpr int kJoinThreads = 512;
+
+template <int D>
+struct DCfg {
+    static constexpr int NST = D == 128 ? 3 : 6;
+    static constexpr int ROW = D * 2;                   // bytes of a row
+    static constexpr int HALF = kTileKeys * ROW;        // K (or V) of a stage
+    static constexpr int STAGE = 2 * HALF;
+    static constexpr int RING = kWarps * NST * STAGE;
+    static constexpr int OPITCH = D + 8;                // floats per row of the merge buffer
+    static constexpr int MERGE = 16 * OPITCH * 4;
+    static constexpr int SMEM = RING + MERGE;
+};
+
+struct DecodeParams {
+    PagedArgs a;
+    int g, rows_max, least;
+    int strict;  // no chunk kernel follows: a sequence of more rows is an error
+    float *part_o;   // [2 * blocks][rows_max][D]
+    float2 *part_ml; // [2 * blocks][rows_max]
+    int4 *meta;      // [blocks] {parts, sequence, head, 0} of the item the block starts and does not finish
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t *r)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t *r)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <int DT>
+__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
+{
+    if (DT)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Clears the non-finite halves of a pair; true if there was one.
+template <int DT>
+__device__ __forceinline__ bool scrub(uint32_t &u)
+{
+    constexpr uint32_t E = DT ? 0x7C00u : 0x7F80u;
+    uint32_t keep = 0xFFFFFFFFu;
+    if ((u & E) == E) keep &= 0xFFFF0000u;
+    if (((u >> 16) & E) == E) keep &= 0x0000FFFFu;
+    u &= keep;
+    return keep != 0xFFFFFFFFu;
+}
+
+__device__ __forceinline__ SeqLen seq_len(const PagedArgs &a, int s)
+{
+    return clip_seq(__ldg(a.cu_q + s), __ldg(a.cu_q + s + 1), __ldg(a.kv_len + s), a.T, a.width << a.page_shift);
+}
+
+// Position in the block's run: unit j of item (s, h).
+struct Pos {
+    int s, h, j, units;
+    SeqLen q;
+    uint32_t left;  // units of the run from this one on
+
+    __device__ __forceinline__ void set(const PagedArgs &a, int seq)
+    {
+        s = seq;
+        q = seq_len(a, s);
+        units = decode_units(q);
+    }
+    // The next item of the run (there is one if units are left).
+    __device__ __forceinline__ void next_item(const PagedArgs &a, int g, int rows_max)
+    {
+        j = 0;
+        if (++h < a.Hkv) return;
+        h = 0;
+        int n = s + 1;
+        while (n < a.S) {
+            set(a, n);
+            if (is_decode(q, g, rows_max)) return;
+            ++n;
+        }
+        left = 0;  // not reached while the run's units are counted alike
+    }
+};
+
+template <int D, int DT, int MT>
+__global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeParams p)
+{
+    using C = DCfg<D>;
+    const PagedArgs &a = p.a;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t s_sum[kWarps];
+    __shared__ int s_seq;
+    __shared__ uint32_t s_rel;
+    __shared__ float s_m[kWarps][MT * 16], s_l[kWarps][MT * 16];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c = blockIdx.x;
+    unsigned int bad = 0;
+
+    // ---- this block's run of units
+    const int per = (a.S + kThreads - 1) / kThreads;
+    const int sb = min(a.S, tid * per), se = min(a.S, sb + per);
+    uint32_t mine = 0;
+    for (int s = sb; s < se; s++) {
+        const SeqLen q = seq_len(a, s);
+        if (q.bad) bad |= CLIS_PAGED_LENGTH_BIT;
+        if (is_decode(q, p.g, p.rows_max)) mine += static_cast<uint32_t>(a.Hkv) * decode_units(q);
+        else if (p.strict && q.n > 0) bad |= CLIS_PAGED_LENGTH_BIT;
+    }
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    uint32_t U = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp) before += s_sum[w];
+        U += s_sum[w];
+    }
+    const uint32_t excl = before + incl - mine;
+    const int nb = decode_blocks(U, gridDim.x, p.least);
+    if (c >= nb) {  // nothing for this block (U = 0 included)
+        if (tid == 0) p.meta[c] = make_int4(0, 0, 0, 0);
+        if (bad && c == 0) atomicOr(&g_decode_error_word, bad);
+        return;
+    }
+    const uint32_t u0 = decode_cut(U, nb, c), u1 = decode_cut(U, nb, c + 1);
+    if (u0 >= excl && u0 < excl + mine) {
+        uint32_t rel = u0 - excl;
+        for (int s = sb; s < se; s++) {
+            const SeqLen q = seq_len(a, s);
+            if (!is_decode(q, p.g, p.rows_max)) continue;
+            const uint32_t w = static_cast<uint32_t>(a.Hkv) * decode_units(q);
+            if (rel < w) {
+                s_seq = s;
+                s_rel = rel;
+                break;
+            }
+            rel -= w;
+        }
+    }
+    __syncthreads();
+
+    Pos cur;
+    cur.set(a, s_seq);
+    cur.h = static_cast<int>(s_rel / cur.units);
+    cur.j = static_cast<int>(s_rel % cur.units);
+    cur.left = u1 - u0;
+
+    // ---- loader: one stage per unit, `ld` runs NST - 1 units ahead of `cur`
+    constexpr int CPR = D / 8;         // 16-byte chunks per row
+    constexpr int RPI = 32 / CPR;      // rows per copy instruction
+    constexpr int NCP = kTileKeys / RPI;
+    const uint32_t ring = smem_u32(smem) + warp * C::NST * C::STAGE;
+    const int key_mask = (1 << a.page_shift) - 1;
+    const int lrow = lane / CPR, lchunk = lane % CPR;
+    Pos ld = cur;
+    int ld_stage = 0;
+    // Page of key (lane & 15) of the tile that the loader is at, read one unit ahead.
+    auto page_at = [&](const Pos &q) -> int {
+        const int key = q.j * kDecodeKeys + warp * kTileKeys + (lane & 15);
+        if (q.left == 0 || key >= q.q.kv) return -2;  // nothing to load
+        return __ldg(a.block_table + q.s * a.bt_s + (key >> a.page_shift));
+    };
+    int page = page_at(ld);
+    auto load_step = [&]() {
+        if (ld.left > 0) {
+            if (page != -2 && (page < 0 || page >= a.num_pages)) {
+                bad |= CLIS_PAGED_INDEX_BIT;
+                page = -2;  // its keys read as zeros
+            }
+            const uint32_t dst = ring + ld_stage * C::STAGE;
+            const int key0 = ld.j * kDecodeKeys + warp * kTileKeys;
+#pragma unroll
+            for (int i = 0; i < NCP; i++) {
+                const int row = i * RPI + lrow;
+                const int pg = __shfl_sync(~0u, page, row);
+                const bool ok = pg >= 0;
+                const int64_t pi = ok ? pg : 0;
+                const int in = ok ? (key0 + row) & key_mask : 0;
+                const uint16_t *ks = a.kc + pi * a.kc_sp + ld.h * a.kc_sh + in * a.kc_sn + lchunk * 8;
+                const uint16_t *vs = a.vc + pi * a.vc_sp + ld.h * a.vc_sh + in * a.vc_sn + lchunk * 8;
+                const uint32_t at = row * C::ROW + ((lchunk ^ (row & 7)) << 4);
+                cp_async16(dst + at, ks, ok ? 16 : 0);
+                cp_async16(dst + C::HALF + at, vs, ok ? 16 : 0);
+            }
+            ld_stage = ld_stage + 1 == C::NST ? 0 : ld_stage + 1;
+            ld.left--;
+            if (++ld.j == ld.units && ld.left > 0) ld.next_item(a, p.g, p.rows_max);
+            page = page_at(ld);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < C::NST - 1; i++) load_step();
+
+    const float sl2 = a.scale_log2;
+    const int r4 = lane >> 2, c2 = (lane & 3) * 2;
+    int stage = 0;
+    float *merge = reinterpret_cast<float *>(smem + C::RING);
+
+    if (tid == 0 && c < nb) p.meta[c] = make_int4(0, 0, 0, 0);
+
+    while (cur.left > 0) {
+        // ---- one item, units j0 .. j1 - 1 of it
+        const int j0 = cur.j;
+        const int j1 = static_cast<int>(min(static_cast<uint32_t>(cur.units), j0 + cur.left));
+        const int n = cur.q.n, kv = cur.q.kv, R = n * p.g, q0 = cur.q.q0;
+        const int lim0 = visible_keys(n, kv, 0, a.causal);  // keys that every row sees
+
+        uint32_t qf[MT][D / 16][4];
+        int lim[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+                const int row = mt * 16 + hf * 8 + r4;
+                const bool ok = row < R;
+                const int tok = ok ? row / p.g : 0, hd = cur.h * p.g + (ok ? row - tok * p.g : 0);
+                lim[mt][hf] = ok ? visible_keys(n, kv, tok, a.causal) : 0;
+                const uint16_t *src = a.q + static_cast<int64_t>(q0 + tok) * a.q_st + hd * a.q_sh + c2;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++) {
+                    qf[mt][ks][hf] = ok ? __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16)) : 0u;
+                    qf[mt][ks][hf + 2] = ok ? __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16 + 8)) : 0u;
+                }
+            }
+        float o[MT][D / 8][4];
+        float m_run[MT][2], l_run[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+            m_run[mt][0] = m_run[mt][1] = -INFINITY;
+            l_run[mt][0] = l_run[mt][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 8; i++) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
+        }
+        bool dirty = false;
+
+        for (int j = j0; j < j1; j++) {
+            cp_async_wait<C::NST - 2>();
+            __syncwarp();
+            load_step();  // into the stage that the previous unit has been read from
+            const int key0 = j * kDecodeKeys + warp * kTileKeys;
+            const uint32_t sK = ring + stage * C::STAGE, sV = sK + C::HALF;
+            stage = stage + 1 == C::NST ? 0 : stage + 1;
+            if (key0 >= kv) continue;
+
+            // S = Q K^T: 16 rows x 16 keys per row tile
+            float s[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) s[mt][i][0] = s[mt][i][1] = s[mt][i][2] = s[mt][i][3] = 0.f;
+            {
+                const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+                const uint32_t base = sK + kr * C::ROW;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++) {
+                    uint32_t kf[4];
+                    ldsm4(base + (((ks * 2 + kc) ^ (kr & 7)) << 4), kf);
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++) {
+                        mma16816<DT>(s[mt][0], qf[mt][ks], kf[0], kf[1]);
+                        mma16816<DT>(s[mt][1], qf[mt][ks], kf[2], kf[3]);
+                    }
+                }
+            }
+            const bool edge = key0 + kTileKeys > lim0;  // some row does not see some key
+            if (edge) {
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            if (key0 + i * 8 + c2 + (e & 1) >= lim[mt][e >> 1]) s[mt][i][e] = -INFINITY;
+            }
+            float mx[MT][2];
+            bool grow = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    float v = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
+                                    fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
+                    mx[mt][hf] = v * sl2;
+                    grow |= mx[mt][hf] > m_run[mt][hf] + kTau;
+                }
+            if (__any_sync(~0u, grow)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++) {
+                        if (mx[mt][hf] > m_run[mt][hf] + kTau) {
+                            const float al = ex2_approx(m_run[mt][hf] - mx[mt][hf]);
+                            m_run[mt][hf] = mx[mt][hf];
+                            l_run[mt][hf] *= al;
+#pragma unroll
+                            for (int i = 0; i < D / 8; i++) {
+                                o[mt][i][2 * hf] *= al;
+                                o[mt][i][2 * hf + 1] *= al;
+                            }
+                        }
+                    }
+            }
+            uint32_t pf[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    const float ns = m_run[mt][hf] == -INFINITY ? 0.f : -m_run[mt][hf];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const float p0 = ex2_approx(fmaf(s[mt][i][2 * hf], sl2, ns));
+                        const float p1 = ex2_approx(fmaf(s[mt][i][2 * hf + 1], sl2, ns));
+                        l_run[mt][hf] += p0 + p1;
+                        pf[mt][2 * i + hf] = pack2<DT>(p0, p1);
+                    }
+                }
+            // O += P V
+            {
+                const int vr = lane & 15, vc = lane >> 4;
+                const uint32_t base = sV + vr * C::ROW;
+                auto pv = [&](bool clean) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++) {
+                        uint32_t vf[4];
+                        ldsm4_t(base + (((i * 2 + vc) ^ (vr & 7)) << 4), vf);
+                        if (clean)
+#pragma unroll
+                            for (int e = 0; e < 4; e++) dirty |= scrub<DT>(vf[e]);
+#pragma unroll
+                        for (int mt = 0; mt < MT; mt++) {
+                            mma16816<DT>(o[mt][2 * i], pf[mt], vf[0], vf[1]);
+                            mma16816<DT>(o[mt][2 * i + 1], pf[mt], vf[2], vf[3]);
+                        }
+                    }
+                };
+                // Where a key is masked for some rows only, a non-finite v of it must
+                // not reach them as 0 * inf: it is left out of the product and added to
+                // the rows that see it at the end.
+                if (edge && lim0 < kv) pv(true);
+                else pv(false);
+            }
+        }
+
+        // ---- join the four warps; rows in shared memory, columns in turns
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+                float l = l_run[mt][hf];
+                l += __shfl_xor_sync(~0u, l, 1);
+                l += __shfl_xor_sync(~0u, l, 2);
+                if ((lane & 3) == 0) {
+                    s_m[warp][mt * 16 + hf * 8 + r4] = m_run[mt][hf];
+                    s_l[warp][mt * 16 + hf * 8 + r4] = l;
+                }
+            }
+        const bool any_dirty = __syncthreads_or(dirty);
+        const bool whole = j0 == 0 && j1 == cur.units;
+        const int slot = 2 * c + (j0 == 0 ? 1 : 0);
+#pragma unroll 1
+        for (int mt = 0; mt < MT; mt++) {
+            if (mt * 16 >= R) break;
+            // A warp none of whose keys a row sees has l = 0 there and adds nothing.
+            float wgt[2];
+            bool none[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+                const int row = mt * 16 + hf * 8 + r4;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_m[w][row]);
+                none[hf] = s_l[warp][row] == 0.f;
+                wgt[hf] = ex2_approx(s_m[warp][row] - M);
+            }
+            auto add_quarter = [&](auto QD, int t) {
+                constexpr int qd = decltype(QD)::value;
+#pragma unroll
+                for (int i = 0; i < D / 8 / kWarps; i++) {
+                    constexpr int first = qd * (D / 8 / kWarps);
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++) {
+                        float2 *d2 =
+                            reinterpret_cast<float2 *>(merge + (hf * 8 + r4) * C::OPITCH + (first + i) * 8 + c2);
+                        // (MT is 1 or 2: selected without indexing registers by mt)
+                        const float x0 = MT == 2 && mt ? o[MT - 1][first + i][2 * hf] : o[0][first + i][2 * hf];
+                        const float x1 = MT == 2 && mt ? o[MT - 1][first + i][2 * hf + 1] : o[0][first + i][2 * hf + 1];
+                        float2 v = none[hf] ? make_float2(0.f, 0.f) : make_float2(x0 * wgt[hf], x1 * wgt[hf]);
+                        if (t > 0) {
+                            const float2 u = *d2;
+                            v.x += u.x;
+                            v.y += u.y;
+                        }
+                        *d2 = v;
+                    }
+                }
+            };
+#pragma unroll 1
+            for (int t = 0; t < kWarps; t++) {
+                switch ((warp + t) & (kWarps - 1)) {
+                case 0: add_quarter(std::integral_constant<int, 0>{}, t); break;
+                case 1: add_quarter(std::integral_constant<int, 1>{}, t); break;
+                case 2: add_quarter(std::integral_constant<int, 2>{}, t); break;
+                default: add_quarter(std::integral_constant<int, 3>{}, t); break;
+                }
+                __syncthreads();
+            }
+            // ---- write: 8 columns of a row per thread and turn
+            for (int it = tid; it < 16 * (D / 8); it += kThreads) {
+                const int rr = it / (D / 8), c8 = (it % (D / 8)) * 8;
+                const int row = mt * 16 + rr;
+                if (row >= R) continue;
+                float M = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_m[w][row]);
+#pragma unroll
+                for (int w = 0; w < kWarps; w++)
+                    if (s_l[w][row] != 0.f) l += ex2_approx(s_m[w][row] - M) * s_l[w][row];
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[e] = merge[rr * C::OPITCH + c8 + e];
+                const int tok = row / p.g, hd = cur.h * p.g + (row - tok * p.g);
+                if (any_dirty) {
+                    // Non-finite values of keys that this row sees and that were left out.
+                    const int see = min(visible_keys(n, kv, tok, a.causal), j1 * kDecodeKeys);
+                    for (int key = max(lim0 / kTileKeys * kTileKeys, j0 * kDecodeKeys); key < see; key++) {
+                        const int pg = __ldg(a.block_table + cur.s * a.bt_s + (key >> a.page_shift));
+                        if (pg < 0 || pg >= a.num_pages) continue;
+                        const uint16_t *vs = a.vc + static_cast<int64_t>(pg) * a.vc_sp + cur.h * a.vc_sh +
+                                             static_cast<int64_t>(key & key_mask) * a.vc_sn + c8;
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const float x = elem_lo<DT>(__ldg(vs + e));
+                            if (!isfinite(x)) v[e] += x;
+                        }
+                    }
+                }
+                if (whole) {
+                    const float inv = 1.f / l;
+                    uint4 u = make_uint4(0u, 0u, 0u, 0u);  // a row that sees no key
+                    if (l != 0.f)
+                        u = make_uint4(pack2<DT>(v[0] * inv, v[1] * inv), pack2<DT>(v[2] * inv, v[3] * inv),
+                                       pack2<DT>(v[4] * inv, v[5] * inv), pack2<DT>(v[6] * inv, v[7] * inv));
+                    *reinterpret_cast<uint4 *>(a.o + static_cast<int64_t>(q0 + tok) * a.o_st + hd * a.o_sh + c8) = u;
+                    if (c8 == 0 && a.lse2)
+                        a.lse2[static_cast<int64_t>(q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
+                } else {
+                    float4 *d4 = reinterpret_cast<float4 *>(
+                        p.part_o + (static_cast<int64_t>(slot) * p.rows_max + row) * D + c8);
+                    d4[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    d4[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    if (c8 == 0) p.part_ml[static_cast<int64_t>(slot) * p.rows_max + row] = make_float2(M, l);
+                }
+            }
+            __syncthreads();
+        }
+        if (!whole && j0 == 0 && tid == 0) {
+            // The item's remaining units lie in the next blocks' runs; how many blocks:
+            const uint32_t end = u1 - cur.left + cur.units - 1;  // the item's last unit
+            int ce = static_cast<int>(static_cast<uint64_t>(end) * static_cast<uint32_t>(nb) / U);
+            while (ce > c && decode_cut(U, nb, ce) > end) ce--;
+            while (ce + 1 < nb && decode_cut(U, nb, ce + 1) <= end) ce++;
+            p.meta[c] = make_int4(ce - c + 1, cur.s, cur.h, 0);
+        }
+        cur.left -= j1 - j0;
+        cur.j = j1;
+        if (cur.left > 0) cur.next_item(a, p.g, p.rows_max);
+    }
+    cp_async_wait<0>();
+    if (bad) atomicOr(&g_decode_error_word, bad);
+}
+
+// Adds the partial results of the item that block c of the decode kernel
+// started and did not finish: its own and those at the start of the following
+// blocks, in that order per group of warps (fixed, so reruns agree bit for bit).
+template <int D, int DT>
+__global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const DecodeParams p)
+{
+    constexpr int V = D / 32;  // columns per lane
+    __shared__ float s_o[kJoinThreads / 32][D];
+    __shared__ float s_l[kJoinThreads / 32];
+    const PagedArgs &a = p.a;
+    const int c = blockIdx.x;
+    const int4 mt = p.meta[c];
+    const int K = mt.x;
+    if (K == 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const SeqLen q = seq_len(a, mt.y);
+    const int R = q.n * p.g;
+    // Warps: rows x groups of parts.
+    constexpr int W = kJoinThreads / 32;
+    int rows = 1;
+    while (rows < R && rows < W) rows *= 2;
+    const int groups = W / rows;
+    const int wr = warp % rows, grp = warp / rows;
+    auto slot_of = [&](int k) -> int64_t { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
+    for (int rb = 0; rb < R; rb += rows) {
+        const int row = rb + wr;
+        float M = -INFINITY, l = 0.f;
+        float o[V];
+#pragma unroll
+        for (int e = 0; e < V; e++) o[e] = 0.f;
+        if (row < R) {
+            for (int k = lane; k < K; k += 32) {
+                const float2 ml = p.part_ml[slot_of(k) * p.rows_max + row];
+                if (ml.y != 0.f) M = fmaxf(M, ml.x);
+            }
+#pragma unroll
+            for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
+#pragma unroll 4
+            for (int k = grp; k < K; k += groups) {
+                const int64_t at = slot_of(k) * p.rows_max + row;
+                const float2 ml = p.part_ml[at];
+                const float w = ml.y == 0.f ? 0.f : ex2_approx(ml.x - M);
+                float x[V];
+                if (V == 4) {
+                    const float4 u = *reinterpret_cast<const float4 *>(p.part_o + at * D + lane * 4);
+                    x[0] = u.x; x[1] = u.y; x[2 % V] = u.z; x[3 % V] = u.w;
+                } else {
+                    const float2 u = *reinterpret_cast<const float2 *>(p.part_o + at * D + lane * 2);
+                    x[0] = u.x; x[1] = u.y;
+                }
+                if (ml.y != 0.f) {
+                    l = fmaf(w, ml.y, l);
+#pragma unroll
+                    for (int e = 0; e < V; e++) o[e] = fmaf(w, x[e], o[e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; e++) s_o[warp][lane * V + e] = o[e];
+        if (lane == 0) s_l[warp] = l;
+        __syncthreads();
+        if (grp == 0 && row < R) {
+            for (int g2 = 1; g2 < groups; g2++) {
+                l += s_l[wr + g2 * rows];
+#pragma unroll
+                for (int e = 0; e < V; e++) o[e] += s_o[wr + g2 * rows][lane * V + e];
+            }
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            const int tok = row / p.g, hd = mt.z * p.g + (row - tok * p.g);
+            uint16_t *dst = a.o + static_cast<int64_t>(q.q0 + tok) * a.o_st + hd * a.o_sh + lane * V;
+#pragma unroll
+            for (int e = 0; e < V; e += 2)
+                *reinterpret_cast<uint32_t *>(dst + e) = l != 0.f ? pack2<DT>(o[e] * inv, o[e + 1] * inv) : 0u;
+            if (lane == 0 && a.lse2)
+                a.lse2[static_cast<int64_t>(q.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int DT, int MT>
+clis_status_t launch_impl(const DecodeParams &p, int grid, cudaStream_t stream)
+{
+    if (cudaFuncSetAttribute(paged_decode_kernel<D, DT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             DCfg<D>::SMEM) != cudaSuccess)
+        return CLIS_ERR_CUDA;
+    paged_decode_kernel<D, DT, MT><<<grid, kThreads, DCfg<D>::SMEM, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
+    paged_decode_join_kernel<D, DT><<<grid, kJoinThreads, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+
+int paged_decode_row_tiles(int64_t max_q, int g)
+{
+    // Rows of the largest sequence if it is small; else those of single tokens.
+    const int64_t rows = max_q * g <= 2 * 16 ? max_q * g : g;
+    return rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+}
+
+size_t paged_decode_workspace(int d, int row_tiles, int nsm)
+{
+    if (row_tiles == 0) return 0;
+    const size_t slots = 2 * 2 * static_cast<size_t>(nsm), rows = 16 * static_cast<size_t>(row_tiles);
+    return up256(2 * static_cast<size_t>(nsm) * sizeof(int4)) + up256(slots * rows * sizeof(float2)) +
+           up256(slots * rows * d * sizeof(float));
+}
+
+clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, void *workspace, int nsm,
+                                  cudaStream_t stream)
+{
+    const int grid = 2 * nsm;  // two blocks fit an SM
+    const size_t slots = 2 * static_cast<size_t>(grid), rows = 16 * static_cast<size_t>(row_tiles);
+    DecodeParams p;
+    p.a = a;
+    p.g = a.H / a.Hkv;
+    p.rows_max = static_cast<int>(rows);
+    p.least = 4;
+    p.strict = strict;
+    char *w = static_cast<char *>(workspace);
+    p.meta = reinterpret_cast<int4 *>(w);
+    w += up256(grid * sizeof(int4));
+    p.part_ml = reinterpret_cast<float2 *>(w);
+    w += up256(slots * rows * sizeof(float2));
+    p.part_o = reinterpret_cast<float *>(w);
+    const bool f16 = a.dtype == CLIS_DT_FP16;
+    if (a.d == 128) {
+        if (row_tiles == 1) return f16 ? launch_impl<128, 1, 1>(p, grid, stream) : launch_impl<128, 0, 1>(p, grid, stream);
+        return f16 ? launch_impl<128, 1, 2>(p, grid, stream) : launch_impl<128, 0, 2>(p, grid, stream);
+    }
+    if (row_tiles == 1) return f16 ? launch_impl<64, 1, 1>(p, grid, stream) : launch_impl<64, 0, 1>(p, grid, stream);
+    return f16 ? launch_impl<64, 1, 2>(p, grid, stream) : launch_impl<64, 0, 2>(p, grid, stream);
+}
+
+clis_status_t read_decode_error(uint32_t *code)
+{
+    return cudaMemcpyFromSymbol(code, g_decode_error_word, sizeof *code) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
+}
+
+clis_status_t clear_decode_error()
+{
+    const unsigned int z = 0;
+    return cudaMemcpyToSymbol(g_decode_error_word, &z, sizeof z) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
+}
+
+}  // namespace clis

@@ -54,7 +54,8 @@ typedef enum {
     CLIS_ERR_MISALIGNED = 3,   /* pointer not 16-byte aligned or stride not a multiple of 8 elements */
     CLIS_ERR_WORKSPACE = 4,    /* workspace null or smaller than clis_certify_workspace_size() */
     CLIS_ERR_CUDA = 5,         /* a CUDA runtime/driver call or a kernel launch failed */
-    CLIS_ERR_TIMEOUT = 6       /* a kernel pipeline wait exceeded its limit (device error word) */
+    CLIS_ERR_TIMEOUT = 6,      /* a kernel pipeline wait exceeded its limit (device error word) */
+    CLIS_ERR_DATA = 7          /* device data (lengths, page numbers, slots) out of range (device error word) */
 } clis_status_t;
 
 /* Floating-point formats whose exp2 overflow limits Figure 3 tabulates (FP16,
@@ -455,13 +456,168 @@ CLIS_API clis_status_t clis_attn_bwd(const clis_shape_t *shape, const void *q, c
                                      float scale_log2, int causal, void *workspace,
                                      size_t ws_bytes, clis_stream_t stream);
 
+/* Rotary positions with up to four axes (text: one; images and video: height
+ * and width, or time, height and width) for q and k, before clis_certify and the
+ * attention calls.  The paper rotates q and k of its video models before the
+ * path it describes; here it is one launch over both tensors.  Pair p of a row
+ * turns by the angle a = position[b, n, axis[p]] * inv_freq[p]:
+ *   (y0, y1) = (x0 cos a - x1 sin a, x1 cos a + x0 sin a),
+ * p < pairs; pairs are elements (p, p + pairs) of a row, or (2p, 2p + 1) when
+ * interleaved; elements from 2 * pairs on are copied.  inverse = 1 turns back:
+ * the gradient of the rotation.  Angles are exact to fp32 for positions of any
+ * size and sign; products are rounded once, to the data type.
+ *   B, Hq, Hk, N, d   q [B, Hq, N, d], k [B, Hk, N, d]; d 64 or 128
+ *   pairs             a multiple of 8, 8 .. d / 2
+ *   axes              1 .. 4
+ *   q_s*, k_s*        strides of q and k (may be 0: broadcast); qo_s*, ko_s* of
+ *                     the outputs, which must not alias
+ *   p_sb, p_sn, p_sa  strides of positions (int32), any */
+typedef struct {
+    int64_t B, Hq, Hk, N, d;
+    int64_t pairs, axes, interleaved, inverse;
+    int64_t q_sb, q_sh, q_sn, k_sb, k_sh, k_sn;
+    int64_t qo_sb, qo_sh, qo_sn, ko_sb, ko_sh, ko_sn;
+    int64_t p_sb, p_sn, p_sa;
+    int64_t dtype;
+} clis_rope_t;
+
+/*   q, k        device inputs (k may be NULL when Hk = 0)
+ *   q_out, k_out  device outputs; the input itself with its own strides is
+ *               allowed (in place), any other overlap is not
+ *   positions   device int32
+ *   inv_freq    device double [pairs], finite, radians per position
+ *   axis        device int32 [pairs], 0 .. axes - 1 (another value turns nothing
+ *               and sets CLIS_PAGED_INDEX_BIT in the device error word)
+ * Empty tensors launch nothing.  Errors as for clis_attn_fwd. */
+CLIS_API clis_status_t clis_rope(const clis_rope_t *desc, const void *q, const void *k, void *q_out, void *k_out,
+                                 const int32_t *positions, const double *inv_freq, const int32_t *axis,
+                                 clis_stream_t stream);
+
+/* A paged key/value cache and a batch of sequences that use it.
+ *
+ * The cache is k_cache, v_cache [num_pages, Hkv, page_size, d] with strides kc_s*
+ * and vc_s* (d contiguous; a [num_pages, page_size, Hkv, d] cache is the same
+ * with other strides).  Key j of sequence s lies in page block_table[s * bt_ss +
+ * j / page_size], row j % page_size.  New tokens of all sequences are packed:
+ * those of sequence s are rows cu_q[s] .. cu_q[s + 1] - 1 of q [T, H, d].
+ *   S          sequences, at most 16384
+ *   T          rows of q, k, v, o (rows from cu_q[S] on belong to no sequence)
+ *   H, Hkv     query and key/value heads, H a multiple of Hkv, H / Hkv <= 128
+ *   d          64 or 128
+ *   page_size  a power of two, 8 .. 65536
+ *   width      block-table columns
+ * Lengths, tables, slots and page numbers live on the device, so one captured
+ * graph serves every step; what is out of range there is not followed: it sets
+ * a bit in the device error word (CLIS_PAGED_*) and reads as zeros, is not
+ * written, or is brought into range. */
+typedef struct {
+    int64_t S, T, H, Hkv, d;
+    int64_t page_size, num_pages, width;
+    int64_t q_st, q_sh, o_st, o_sh;
+    int64_t kc_sp, kc_sh, kc_sn, vc_sp, vc_sh, vc_sn;
+    int64_t bt_ss;
+    int64_t dtype;
+} clis_paged_t;
+
+/* Bits of the device error word: a page number, slot or axis out of range; the
+ * ring of free pages ran out (or its counters contradict its size); a length
+ * out of range. */
+#define CLIS_PAGED_INDEX_BIT (1u << 16)
+#define CLIS_PAGED_POOL_BIT (1u << 17)
+#define CLIS_PAGED_LENGTH_BIT (1u << 18)
+
+/* Plan of a step from the lengths of its sequences, all on the device: pages
+ * for the new tokens, block tables, slots and positions.
+ *   S, T, width, bt_ss, page_size, num_pages  as in clis_paged_t (no other
+ *                field is read)
+ *   ctx_len      int32 [S]: tokens of each sequence that are in the cache
+ *   new_len      int32 [S]: tokens that this step adds; negative: the sequence
+ *                is finished and gives its pages back
+ *   block_table  int32 in/out: its first ceil(ctx / page_size) columns of a row
+ *                are read, the following ones that the step needs are written
+ *   ring         int32 [ring_size] in/out: free pages, those from state_in[0] (head)
+ *                up to state_in[1] (tail), both counted without end and taken
+ *                modulo ring_size; ring_size >= num_pages holds every page.
+ *                Pages are taken from the head on in the order of the sequences,
+ *                pages given back are written from the tail on.
+ *   state_in, state_out  int64 [2]: head and tail before and after; different
+ *                memory
+ *   cu_q         int32 out [S + 1]: prefix sums of the new tokens
+ *   kv_len       int32 out [S]: ctx + new (0 for a finished sequence)
+ *   slots        int64 out [T]: page * page_size + row of each new token in
+ *                packed order; -1 for rows behind the last, and where the ring
+ *                had no page
+ *   positions    int32 out [T]: the token's place in its sequence (0 behind the last)
+ * Outputs must not overlap each other or the inputs.  The same inputs give the
+ * same outputs bit for bit.  One launch.  Errors: CLIS_ERR_INVALID_ARG (null
+ * pointers, sizes, state_out == state_in), CLIS_ERR_UNSUPPORTED (S > 16384, T or
+ * width * page_size beyond 2^30), CLIS_ERR_MISALIGNED. */
+CLIS_API clis_status_t clis_paged_plan(const clis_paged_t *desc, const int32_t *ctx_len, const int32_t *new_len,
+                                       int32_t *block_table, int32_t *ring, int64_t ring_size, const int64_t *state_in,
+                                       int64_t *state_out, int32_t *cu_q, int32_t *kv_len, int64_t *slots,
+                                       int32_t *positions, clis_stream_t stream);
+
+/* New keys and values into the cache, rotated on the way, and q rotated beside
+ * them, in one launch.
+ *   rope       desc for the rotation: N = T, B = 1, Hq = H (0: no q), Hk = Hkv, d,
+ *              strides of q, q_out, k and positions (ko_s* are ignored: k goes to
+ *              the cache); dtype as in desc; inverse must be 0
+ *   v_st, v_sh strides of v [T, Hkv, d]
+ *   slots      device int64 [T]: row t goes to page slots[t] / page_size, row
+ *              slots[t] % page_size; negative: nowhere (padding).  Slots >= 0
+ *              must be distinct; for equal ones it is not specified which row's
+ *              pieces stay.
+ *   positions, inv_freq, axis  as for clis_rope; pairs = 0: no rotation, and the
+ *              three may be NULL (then q must be NULL too)
+ * q_out may be q (in place); the caches must not overlap q, k or v. */
+CLIS_API clis_status_t clis_paged_append(const clis_paged_t *desc, const clis_rope_t *rope, const void *q, const void *k,
+                                         const void *v, int64_t v_st, int64_t v_sh, void *q_out, void *k_cache,
+                                         void *v_cache, const int64_t *slots, const int32_t *positions,
+                                         const double *inv_freq, const int32_t *axis, clis_stream_t stream);
+
+/* Workspace bytes of clis_attn_fwd_paged for this shape and max_q (on the
+ * current device: it depends on the number of SMs). */
+CLIS_API clis_status_t clis_attn_paged_workspace_size(const clis_paged_t *desc, int64_t max_q, size_t *bytes);
+
+/* Attention of the new tokens of every sequence over its cached keys (the new
+ * tokens' own among them: append first).  The n = cu_q[s + 1] - cu_q[s] new
+ * tokens are the last of the kv_len[s] tokens:
+ *   o_i = sum_j 2^(x_ij) v_j / sum_j 2^(x_ij),  x_ij = scale_log2 * q_i . k_j,
+ * over the keys j < kv_len[s] of head h / (H / Hkv) and, if causal, j <= kv_len[s] - n
+ * + i.  Any mix of single tokens, drafted tokens and long chunks is one call;
+ * sequences of few rows (n * H / Hkv up to 16, or 32) run a kernel bound by the
+ * cache's bytes, the others one bound by the tensor cores.  The softmax is
+ * online with a lazily raised shift, as CLIS_ONLINE_LAZY: a certificate would
+ * have to read all keys first, which for a few query rows is the whole cost.
+ *   q          device [T, H, d] (q_st, q_sh)
+ *   k_cache, v_cache, block_table, cu_q (int32 [S + 1], from 0 on, not falling),
+ *              kv_len (int32 [S]): see clis_paged_t
+ *   o          device out [T, H, d] (o_st, o_sh; must not alias).  Rows that
+ *              belong to no sequence are left as they are; a row that sees no
+ *              key becomes 0 (lse2: -inf).
+ *   lse2       optional device fp32 out [T * H], index t * H + h
+ *   max_q      no sequence has more new tokens than this (T is always valid); a
+ *              sequence that does may be left out, with CLIS_PAGED_LENGTH_BIT
+ *   workspace  device scratch of clis_attn_paged_workspace_size() bytes, 256-byte
+ *              aligned; contents need no initialisation; not shared by calls that
+ *              may run at the same time
+ * What pages hold behind the last key has no effect, whatever it is, nor have
+ * non-finite keys or values on rows that do not see them.  Results do not
+ * depend on timing: reruns agree bit for bit.  S = 0 or T = 0 launches nothing.
+ * Errors as for clis_attn_fwd; CLIS_ERR_WORKSPACE. */
+CLIS_API clis_status_t clis_attn_fwd_paged(const clis_paged_t *desc, const void *q, const void *k_cache,
+                                           const void *v_cache, const int32_t *block_table, const int32_t *cu_q,
+                                           const int32_t *kv_len, void *o, float *lse2, int64_t max_q, float scale_log2,
+                                           int causal, void *workspace, size_t ws_bytes, clis_stream_t stream);
+
 /* Static description of a status code (never NULL). */
 CLIS_API const char *clis_status_string(clis_status_t status);
 
 /* Reads the device error word of the current device (synchronises the
  * device).  *code = 0 when no kernel recorded a fault; otherwise bit flags of
- * the pipeline waits that timed out.  Returns CLIS_ERR_TIMEOUT if *code != 0,
- * CLIS_ERR_CUDA if the read failed. */
+ * the pipeline waits that timed out and CLIS_PAGED_* bits.  Returns
+ * CLIS_ERR_DATA if *code holds CLIS_PAGED_* bits alone, CLIS_ERR_TIMEOUT if it
+ * holds others, CLIS_ERR_CUDA if the read failed. */
 CLIS_API clis_status_t clis_get_device_error(uint32_t *code);
 
 /* Resets the device error word of the current device to 0 (synchronous). */

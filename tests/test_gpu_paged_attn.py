@@ -1,0 +1,270 @@
+"""Attention over a paged cache against 64-bit softmax: every mix of single tokens, drafted
+tokens and chunks, at the sizes where tiles, pages and rows end inside one another."""
+import math
+
+import pytest
+import torch
+
+from certified_fixed_stabilizer_gb300 import clis
+from paged_util import check_attention, make_batch
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(autouse=True)
+def clean_error_word():
+    clis.clis_clear_device_error()
+    yield
+    assert clis.clis_get_device_error() == 0
+
+
+def run(b, causal=True, max_q=None, **kw):
+    return clis.attention_paged(b["q"], b["k_cache"], b["v_cache"], b["block_table"], b["cu_q"], b["kv_len"],
+                                b["max_q"] if max_q is None else max_q, causal=causal, return_lse=True, **kw)
+
+
+# (ctx, new, H, Hkv, d, page, dtype, causal)
+DECODE = [
+    ([0], [1], 4, 4, 128, 16, BF, True),                       # one token, nothing cached before it
+    ([1], [1], 8, 1, 64, 8, FP, True),
+    ([15], [1], 4, 2, 128, 16, BF, True),                      # a page exactly full
+    ([16], [1], 4, 2, 128, 16, FP, True),
+    ([62, 63, 64, 65], [1, 1, 1, 1], 8, 2, 128, 64, BF, True),  # around one 64-key unit
+    ([299], [1], 32, 8, 128, 16, BF, True),
+    ([5000], [1], 32, 8, 128, 16, BF, True),                   # keys shared out over many blocks
+    ([5000], [1], 5, 1, 64, 32, FP, True),
+    ([100, 0, 7000, 31, 900], [1, 1, 1, 1, 1], 16, 4, 128, 16, FP, True),  # ragged
+    ([100, 3, 700], [3, 0, 5], 12, 4, 64, 128, BF, True),      # drafted tokens, one sequence without any
+    ([100, 3, 700], [4, 4, 4], 12, 4, 128, 8, BF, False),      # no mask among the new tokens
+    ([2000, 10], [2, 2], 16, 1, 128, 256, BF, True),           # 32 rows
+    ([513], [5], 6, 1, 128, 32, FP, True),                     # 30 rows
+    ([40] * 40, [1] * 40, 6, 2, 64, 16, BF, True),             # more sequences than warps
+]
+CHUNK = [
+    ([0], [33], 1, 1, 128, 16, BF, True),                      # one short prompt
+    ([0], [128], 4, 4, 64, 64, FP, True),
+    ([0], [129], 4, 2, 128, 128, BF, True),
+    ([127], [257], 8, 2, 128, 8, FP, True),
+    ([1000], [100], 8, 1, 128, 16, BF, True),
+    ([1000], [100], 8, 1, 64, 16, BF, False),
+    ([3000], [300], 5, 1, 128, 32, BF, True),                  # 25 tokens of 5 heads per row tile
+    ([3000, 17], [40, 300], 3, 1, 64, 256, FP, True),          # 42 tokens of 3 heads
+    ([500], [70], 128, 1, 128, 64, BF, True),                  # one token per row tile
+    ([500], [40], 64, 1, 64, 64, BF, True),
+    ([0, 300, 64, 0], [700, 1, 200, 65], 8, 4, 128, 16, BF, True),   # mixed
+    ([900, 0, 20, 2000, 5], [1, 512, 0, 1, 300], 8, 2, 64, 32, FP, True),
+    ([0], [2000], 16, 2, 128, 64, BF, True),                   # triangular costs
+    ([127, 128, 129], [128, 128, 128], 2, 2, 128, 128, BF, False),
+]
+
+
+@pytest.mark.parametrize("ctx,new,H,Hkv,d,page,dtype,causal", DECODE + CHUNK)
+def test_against_64_bits(ctx, new, H, Hkv, d, page, dtype, causal):
+    b = make_batch(ctx, new, H, Hkv, d, page, dtype, seed=len(ctx) + d + page)
+    o, lse2 = run(b, causal)
+    check_attention(o, lse2, b, causal)
+    o2, lse3 = run(b, causal)
+    assert torch.equal(o, o2) and torch.equal(lse2, lse3)  # reruns agree bit for bit
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("ctx,new", [([700, 40], [1, 1]), ([300, 90], [150, 1])])
+def test_strides(ctx, new, dtype):
+    """q and o inside wider buffers and head-major, caches as [pages, page, H_kv, d]."""
+    b = make_batch(ctx, new, 8, 2, 128, 32, dtype, seed=3, layout="nhd")
+    want, _ = run(b)
+    check_attention(want, None, b)
+    T = b["q"].shape[0]
+    wide = torch.randn(T, 12, 136, device="cuda").to(dtype)
+    wide[:, 2:10, :128] = b["q"]
+    out = torch.full((8, T, 128), 7.0, dtype=dtype, device="cuda").transpose(0, 1)
+    got, _ = run({**b, "q": wide[:, 2:10, :128]}, out=out)
+    assert got is out and torch.equal(got, want)
+    head_major = b["q"].transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(run({**b, "q": head_major})[0], want)
+    # heads that share one row of q (stride 0)
+    shared = b["q"][:, :1].expand(-1, 8, -1)
+    assert torch.equal(run({**b, "q": shared})[0], run({**b, "q": shared.contiguous()})[0])
+
+
+@pytest.mark.parametrize("new", [[1, 2, 0], [1, 140, 0]])
+def test_rows_of_no_sequence_stay(new):
+    b = make_batch([50, 60, 70], new, 4, 2, 64, 16, BF, seed=5, extra_rows=37)
+    T = b["q"].shape[0]
+    out = torch.full((T, 4, 64), 3.0, dtype=BF, device="cuda")
+    o, lse2 = run(b, out=out)
+    check_attention(o, lse2, b)
+    assert (o[sum(new):] == 3.0).all()
+
+
+@pytest.mark.parametrize("max_q,H", [(1, 4), (64, 4)])
+def test_rows_without_keys(max_q, H):
+    """kv_len 0, and kv_len below the number of new tokens (its first tokens see nothing)."""
+    for n, kv in ((1, 0), (max_q, 0), (max_q, max_q // 2)):
+        b = make_batch([64], [n], H, 2, 128, 16, BF, seed=2)
+        b["kv_len"] = torch.tensor([kv], dtype=torch.int32, device="cuda")
+        o, lse2 = run(b)
+        blind = n - kv
+        assert (o[:blind] == 0).all() and (lse2[:blind] == -math.inf).all()
+        if kv:
+            seen = {**b, "ctx": [0], "new": [kv], "q": b["q"][blind:], "keys": [b["keys"][0][:kv]],
+                    "vals": [b["vals"][0][:kv]]}
+            check_attention(o[blind:], lse2[blind:], seen)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("ctx,new,H,Hkv,d", [([200], [4], 8, 2, 128), ([100], [90], 4, 1, 128), ([0], [300], 2, 2, 64),
+                                             ([5000], [4], 4, 1, 64)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_masked_values_that_are_not_finite(bad, ctx, new, H, Hkv, d, dtype):
+    """A key or value of a later token that is not finite reaches the rows that see it, and no other."""
+    b = make_batch(ctx, new, H, Hkv, d, 16, dtype, seed=7)
+    clean, clean_lse = run(b)
+    at = ctx[0] + new[0] - 2          # the last token but one: seen by the last two
+    page, row = b["block_table"][0, at // 16].item(), at % 16
+    vc = b["v_cache"].clone()
+    vc[page, :, row, 5] = bad
+    o, lse2 = run({**b, "v_cache": vc})
+    assert torch.equal(lse2, clean_lse)
+    assert torch.equal(o[:-2], clean[:-2])
+    rest = [c for c in range(d) if c != 5]
+    assert torch.equal(o[-2:, :, rest], clean[-2:, :, rest])
+    hit = o[-2:, :, 5].float()
+    assert torch.isnan(hit).all() if math.isnan(bad) else (hit == bad).all()
+    kc = b["k_cache"].clone()
+    kc[page, :, row, 5] = float("nan")
+    o, lse2 = run({**b, "k_cache": kc})
+    assert torch.equal(o[:-2], clean[:-2]) and torch.isnan(o[-2:].float()).all() and torch.isnan(lse2[-2:]).all()
+
+
+def test_a_key_that_is_not_finite_seen_by_all():
+    """NaN keys make NaN rows, not rows without keys, also where a whole tile is NaN."""
+    for new in ([1], [40]):
+        b = make_batch([300], new, 4, 2, 128, 16, BF, seed=11)
+        b["k_cache"][b["block_table"][0, :16].long()] = float("nan")  # the first 256 keys
+        o, lse2 = run(b)
+        assert torch.isnan(o.float()).all() and torch.isnan(lse2).all()
+
+
+def test_max_q_only_chooses_the_kernel():
+    """The decode kernel's and the chunk kernel's results agree to rounding; T is always a valid max_q."""
+    b = make_batch([300, 900, 64], [1, 2, 1], 8, 2, 128, 16, BF, seed=13)
+    for mq in (2, 4, 100, 10 ** 9):
+        check_attention(*run(b, max_q=mq), b, what=f"max_q {mq}")
+
+
+def test_large_scores_raise_the_shift_often():
+    """Scores that grow along the keys: the running shift is raised again and again."""
+    for new in ([1], [100]):
+        b = make_batch([1500], new, 4, 1, 128, 32, BF, seed=17)
+        n = 1500 + new[0]
+        ramp = torch.linspace(0.05, 3.0, n, device="cuda")[:, None, None]
+        # keys along one direction, longer and longer; queries along the same direction
+        e = torch.zeros(128, device="cuda")
+        e[:8] = 1.0
+        keys = (ramp * e).to(BF)
+        b["keys"] = [keys]
+        for i in range(-(-n // 32)):
+            m = min(32, n - 32 * i)
+            b["k_cache"][b["block_table"][0, i].item(), :, :m] = keys[32 * i:32 * i + m].transpose(0, 1)
+        b["q"] = (10 * e).to(BF).expand(new[0], 4, 128).contiguous()
+        o, lse2 = run(b)
+        check_attention(o, lse2, b)
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 elements: the page offset needs 64 bits."""
+    pages, page, d = 70000, 256, 128
+    kc = torch.empty((pages, 2, page, d), dtype=BF, device="cuda")  # 4.6e9 elements, 9.2 GB
+    vc = torch.empty_like(kc)
+    for new in ([1], [80]):
+        n = 600 + new[0]
+        b = make_batch([600], new, 4, 2, d, page, BF, seed=19, poison=False)
+        ids = [pages - 1, pages - 7, 40000]
+        for i, p in enumerate(ids):
+            src = b["block_table"][0, i].item()
+            kc[p], vc[p] = b["k_cache"][src], b["v_cache"][src]
+        b["block_table"][0, :3] = torch.tensor(ids, dtype=torch.int32)
+        check_attention(*run({**b, "k_cache": kc, "v_cache": vc}), b)
+        assert n <= 3 * page
+
+
+def test_other_stream_and_captured_graph():
+    """A captured call replayed with other lengths; two graphs with workspaces of their own."""
+    b = make_batch([700, 300], [1, 1], 8, 2, 128, 16, BF, seed=23)
+    c = make_batch([40, 500], [90, 1], 8, 2, 128, 16, BF, seed=24)
+    want = [run(x) for x in (b, c)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [run(x) for x in (b, c)]
+    torch.cuda.current_stream().wait_stream(side)
+    for (o, l), (o2, l2) in zip(want, got):
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+    graphs = []
+    for x in (b, c):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r = run(x)
+        graphs.append((g, r))
+    for (g, r), w in zip(graphs, want):
+        r[0].zero_()
+    for g, r in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for (g, r), w in zip(graphs, want):
+        assert torch.equal(r[0], w[0]) and torch.equal(r[1], w[1])
+    # other lengths in the same buffers
+    b["kv_len"].copy_(torch.tensor([333, 17], dtype=torch.int32))
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    short = {**b, "ctx": [332, 16], "keys": [b["keys"][0][:333], b["keys"][1][:17]],
+             "vals": [b["vals"][0][:333], b["vals"][1][:17]]}
+    check_attention(*graphs[0][1], short)
+
+
+def test_bad_pages_and_lengths_are_recorded():
+    for new in ([2], [80]):
+        b = make_batch([100], new, 4, 2, 128, 16, BF, seed=29)
+        b["block_table"][0, 1] = b["k_cache"].shape[0]      # one page out of range: zeros
+        o, _ = run(b)
+        assert torch.isfinite(o.float()).all()
+        assert clis.clis_get_device_error() == clis.PAGED_INDEX_BIT
+        clis.clis_clear_device_error()
+        zero = {**b, "keys": [b["keys"][0].clone()], "vals": [b["vals"][0].clone()]}
+        zero["keys"][0][16:32] = 0
+        zero["vals"][0][16:32] = 0
+        check_attention(o, None, zero)
+        b["block_table"][0, 1] = -5
+        run(b)
+        assert clis.clis_get_device_error() == clis.PAGED_INDEX_BIT
+        clis.clis_clear_device_error()
+        # a length beyond the block table, prefix sums beyond T: brought into range
+        b = make_batch([100], new, 4, 2, 128, 16, BF, seed=29, poison=False)
+        b["block_table"].clamp_(min=0)
+        b["kv_len"].fill_(10 ** 9)
+        b["cu_q"][1] = 10 ** 6
+        run(b)
+        assert clis.clis_get_device_error() & clis.PAGED_LENGTH_BIT
+        clis.clis_clear_device_error()
+
+
+def test_more_tokens_than_max_q_is_recorded():
+    b = make_batch([10, 10], [1, 9], 4, 1, 64, 16, BF, seed=31)
+    run(b, max_q=4)
+    assert clis.clis_get_device_error() == clis.PAGED_LENGTH_BIT
+    clis.clis_clear_device_error()
+
+
+def test_empty_batches():
+    b = make_batch([10], [1], 4, 2, 64, 16, BF, seed=1)
+    o = clis.attention_paged(b["q"][:0], b["k_cache"], b["v_cache"], b["block_table"], torch.zeros(2, dtype=torch.int32, device="cuda"),
+                             b["kv_len"])
+    assert o.shape == (0, 4, 64)
+    none = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+    out = torch.full((1, 4, 64), 2.0, dtype=BF, device="cuda")
+    clis.attention_paged(b["q"], b["k_cache"], b["v_cache"], none, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                         none[:, 0].contiguous(), out=out)
+    assert (out == 2.0).all()
