@@ -162,13 +162,23 @@ struct Split {
     bool chunk;     // the chunk kernel is launched
 };
 
-Split split_of(const clis_paged_t *p, int64_t max_q)
+Split split_of(const clis_paged_t *p, int64_t max_q, int nsm)
 {
     const int g = static_cast<int>(p->H / p->Hkv);
     const int64_t mq = max_q < p->T ? max_q : p->T;
     Split s;
     s.row_tiles = clis::paged_decode_row_tiles(mq, g);
     s.chunk = mq * g > 16 * s.row_tiles;
+    // A batch with chunks whose caches are small as a whole leaves its single tokens
+    // to the chunk kernel too: at 12 sequences of up to 8,000 keys (d = 128, 8
+    // key/value heads) that took 110 us, the decode kernel first 136 us.  Above, the
+    // decode kernel's higher share of the bandwidth counts: 64 sequences of up to
+    // 16,000 keys took 383 us and 374 us, at d = 64 276 us and 231 us (a key tile
+    // has half the bytes there, but takes almost as long).  The limit is on what
+    // the block table can hold, which the host knows.
+    const int64_t tiles = p->d == 128 ? 128 : 32;
+    const int64_t per = (p->width * p->page_size + clis::kChunkKeys - 1) / clis::kChunkKeys;
+    if (s.chunk && p->S * p->Hkv * per <= tiles * nsm) s.row_tiles = 0;
     return s;
 }
 
@@ -341,7 +351,7 @@ clis_status_t clis_attn_paged_workspace_size(const clis_paged_t *desc, int64_t m
     if (desc->S == 0 || desc->T == 0) return CLIS_OK;
     int nsm = 0;
     if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
-    const Split s = split_of(desc, max_q);
+    const Split s = split_of(desc, max_q, nsm);
     *bytes = clis::paged_decode_workspace(static_cast<int>(desc->d), s.row_tiles, nsm) +
              (s.chunk ? clis::paged_chunk_workspace(attn_args(desc), nsm) : 0);
     return CLIS_OK;
@@ -364,7 +374,7 @@ clis_status_t clis_attn_fwd_paged(const clis_paged_t *desc, const void *q, const
         return CLIS_ERR_MISALIGNED;
     int nsm = 0;
     if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
-    const Split s = split_of(desc, max_q);
+    const Split s = split_of(desc, max_q, nsm);
     clis::PagedArgs a = attn_args(desc);
     const size_t dec = clis::paged_decode_workspace(a.d, s.row_tiles, nsm);
     const size_t need = dec + (s.chunk ? clis::paged_chunk_workspace(a, nsm) : 0);
@@ -381,13 +391,13 @@ clis_status_t clis_attn_fwd_paged(const clis_paged_t *desc, const void *q, const
     a.scale_log2 = scale_log2;
     a.causal = causal;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (s.row_tiles > 0) {
-        const clis_status_t e = clis::launch_paged_decode(a, s.row_tiles, !s.chunk, workspace, nsm, cs);
-        if (e != CLIS_OK) return e;
-    }
-    if (s.chunk)
-        return clis::launch_paged_chunk(a, 16 * s.row_tiles, static_cast<char *>(workspace) + dec, nsm, cs);
-    return CLIS_OK;
+    void *cws = static_cast<char *>(workspace) + dec;
+    clis_status_t e = CLIS_OK;
+    if (s.chunk) e = clis::launch_paged_chunk_schedule(a, 16 * s.row_tiles, cws, nsm, cs);
+    if (e == CLIS_OK && s.row_tiles > 0)
+        e = clis::launch_paged_decode(a, s.row_tiles, !s.chunk, s.chunk, workspace, nsm, cs);
+    if (e == CLIS_OK && s.chunk) e = clis::launch_paged_chunk(a, 16 * s.row_tiles, cws, nsm, cs);
+    return e;
 }
 
 }  // extern "C"

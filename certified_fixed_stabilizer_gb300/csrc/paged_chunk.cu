@@ -23,9 +23,27 @@
 //                   taken out of the product (0 * NaN would reach every row) and
 //                   added by the epilogue to the rows that see them
 //
-// A one-block kernel first writes the list of work tiles (the lengths live on
-// the device); block i takes tiles i, 2 G - 1 - i, 2 G + i, ... (G blocks), which
-// evens out costs that rise or fall along the list.  Every wait is bounded.
+// A one-block kernel first lists the items and where each block's run of them
+// starts (the lengths live on the device).  Runs are equal in cost.  An item that
+// crosses a cut is computed in parts; two parts are joined by the block that
+// finishes last (an arrival count per item; nobody waits), more by
+// paged_chunk_join_kernel.  Either way the parts are added in the order of the
+// keys, so results do not depend on who was last.
+//
+// An item with a single row tile (few tokens, or the last of a sequence) would
+// leave one softmax group idle and the other's chain score -> weight -> product
+// bare.  There the groups take turns at the key tiles: the even ones go through S0,
+// O0, the odd ones through S1, O1, and the epilogue adds the two.
+//
+// A key tile's weights are computed with the shift as it is, beside the tile's
+// maximum, and the maximum is looked at afterwards: it is off the chain score ->
+// weight -> product unless it outgrew the shift, and then the tile's weights are
+// computed again.  (Handing the weights over in two halves, so that the first
+// half's product runs beside the second half's weights, was slower: 1.5 instead of
+// 1.4 us a key tile; what bounds a step is the MMA warp, which the tensor pipe
+// outruns at every wait and commit.)
+//
+// Every wait is bounded.
 #include <cuda_bf16.h>
 
 #include "clis_internal.h"
@@ -42,7 +60,10 @@ constexpr int BM = kChunkRows, BN = kChunkKeys;
 constexpr int kThreads = 512;
 constexpr int kNStageMax = 8;
 constexpr float kTau = 8.0f;
-constexpr int kSchedThreads = 1024;
+constexpr int kSchedThreads = 512;
+// Items of three parts or more: every block but the last adds at most one part to
+// the items' number, so there are at most (grid - 1) / 2 of them.
+int max_joins(int grid) { return (grid - 1) / 2 + 1; }
 
 // Error-word bits of waits that gave up (the forward kernel's meanings).
 constexpr unsigned kErrProducer = 1u << 0, kErrMma = 1u << 1, kErrSoftmax = 1u << 2, kErrEpilogue = 1u << 3,
@@ -63,12 +84,16 @@ struct ChunkParams {
     PagedArgs a;
     int g, tpt;           // query heads per key/value head; tokens per row tile
     int rows_small;       // sequences of up to so many rows are the decode kernel's
-    int slots, least;     // places for tiles when keys are shared out; key tiles per part
+    int grid, least;      // blocks; cost of a block's run, at least
     int box_rows;         // rows of a K/V TMA box: min(page size, 128)
-    ChunkTile *tiles;
-    int *count;           // {tiles, first work tile of a sequence whose keys are shared out: 0/1}
-    float *part_o;        // [slots'][256][D]
-    float2 *part_ml;      // [slots'][256]
+    ChunkItem *items;
+    unsigned long long *head;  // {items, total cost, blocks that take part}
+    int *run_first;       // [grid] first item of each block's run
+    int *arrived;         // [grid] parts done of the item that the block starts and does not finish
+    int2 *join;           // [max_joins] {parts, item} of items of three parts or more
+    int *joins;           // their number
+    float *part_o;        // [2 * grid][D / 4][256][4]: slot 2 c + 1 if block c starts the item, 2 c if it goes on with it
+    float2 *part_ml;      // [2 * grid][256]
 };
 
 struct __align__(8) Ctl {
@@ -82,6 +107,7 @@ struct __align__(8) Ctl {
     float epi_l[2][BM], epi_shift[2][BM];
     int dirty[8];  // per work tile (mod 8): non-finite values were taken out
     uint32_t tmem_base;
+    int last;  // epilogue: the item's other parts are done
     int abort_flag;
 };
 
@@ -92,96 +118,149 @@ __device__ __forceinline__ SeqLen seq_len(const PagedArgs &a, int s)
 
 // ------------------------------------------------------------------ schedule
 
-__global__ void __launch_bounds__(kSchedThreads) paged_chunk_schedule_kernel(const ChunkParams p)
+__device__ __forceinline__ ChunkItem load_item(const ChunkParams &p, int i)
 {
-    extern __shared__ int s_first[];  // [S + 1] first tile of each sequence
-    __shared__ unsigned long long s_total, s_items;
-    __shared__ int s_warp[kSchedThreads / 32];
-    const PagedArgs &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned int bad = 0;
-    if (tid == 0) s_total = s_items = 0;
-    __syncthreads();
-    unsigned long long total = 0, items = 0;
-    for (int s = tid; s < a.S; s += kSchedThreads) {
-        const SeqLen q = seq_len(a, s);
-        if (q.bad) bad |= CLIS_PAGED_LENGTH_BIT;
-        if (q.n == 0 || is_decode(q, p.g, p.rows_small)) continue;
-        const unsigned long long it = static_cast<unsigned long long>(a.Hkv) * chunk_q_tiles(q.n, p.g);
-        items += it;
-        total += it * chunk_max_cost(q);
-    }
-    // (integer sums: the order in which they are added does not matter)
-    if (items) {
-        atomicAdd(&s_items, items);
-        atomicAdd(&s_total, total);
-    }
-    __syncthreads();
-    const int len = chunk_part_len(s_total, s_items, p.slots, p.least);
-    const int per = (a.S + kSchedThreads - 1) / kSchedThreads;
-    const int s0 = min(a.S, tid * per), s1 = min(a.S, s0 + per);
-    auto tiles_of = [&](int s) -> int {
-        const SeqLen q = seq_len(a, s);
-        if (q.n == 0 || is_decode(q, p.g, p.rows_small)) return 0;
-        return a.Hkv * chunk_q_tiles(q.n, p.g) * chunk_parts(q, len);
-    };
-    int mine = 0;
-    for (int s = s0; s < s1; s++) mine += tiles_of(s);
-    int incl = mine;
+    union { int4 v[3]; ChunkItem c; } u;
+    const int4 *src = reinterpret_cast<const int4 *>(p.items + i);
+    u.v[0] = src[0];
+    u.v[1] = src[1];
+    u.v[2] = src[2];
+    return u.c;
+}
+
+// Exclusive prefix sum over the block's threads; the total in *total.
+template <typename T>
+__device__ __forceinline__ T block_scan(T mine, T *s_warp, T *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(~0u, incl, o);
+        const T up = __shfl_up_sync(~0u, incl, o);
         if (lane >= o) incl += up;
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    int run = incl - mine;
-    for (int w = 0; w < warp; w++) run += s_warp[w];
-    for (int s = s0; s < s1; s++) {
-        s_first[s] = run;
-        run += tiles_of(s);
+    T before = 0, all = 0;
+    for (int w = 0; w < kSchedThreads / 32; w++) {
+        if (w < warp) before += s_warp[w];
+        all += s_warp[w];
     }
-    if (s0 < a.S && s1 == a.S) s_first[a.S] = run;
     __syncthreads();
-    const int W = s_first[a.S];
-    for (int t = tid; t < W; t += kSchedThreads) {
-        int lo = 0, hi = a.S;  // s_first[lo] <= t < s_first[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_first[mid] <= t) lo = mid;
+    *total = all;
+    return before + incl - mine;
+}
+
+__global__ void __launch_bounds__(kSchedThreads) paged_chunk_schedule_kernel(const ChunkParams p)
+{
+    extern __shared__ int s_first[];  // [S + 1] first item of each sequence
+    __shared__ unsigned long long s_warp[kSchedThreads / 32];
+    __shared__ int s_joins;
+    const PagedArgs &a = p.a;
+    const int tid = threadIdx.x;
+    const bool causal = a.causal != 0;
+    unsigned int bad = 0;
+    pdl_launch();  // the decode kernel does not read what is written here
+    for (int c = tid; c < p.grid; c += kSchedThreads) p.arrived[c] = 0;
+    if (tid == 0) s_joins = 0;  // (read after the scans' barriers)
+
+    const int per = (a.S + kSchedThreads - 1) / kSchedThreads;
+    const int s0 = min(a.S, tid * per), s1 = min(a.S, s0 + per);
+    auto items_of = [&](const SeqLen &q) -> int {
+        return q.n == 0 || is_decode(q, p.g, p.rows_small) ? 0 : a.Hkv * chunk_q_tiles(q.n, p.g);
+    };
+    unsigned long long mine = 0, all;
+    for (int s = s0; s < s1; s++) {
+        const SeqLen q = seq_len(a, s);
+        if (q.bad) bad |= CLIS_PAGED_LENGTH_BIT;
+        mine += items_of(q);
+    }
+    unsigned long long run = block_scan(mine, s_warp, &all);
+    for (int s = s0; s < s1; s++) {
+        s_first[s] = static_cast<int>(run);
+        run += items_of(seq_len(a, s));
+    }
+    const int W = static_cast<int>(all);
+    if (tid == 0) s_first[a.S] = W;
+    __syncthreads();
+
+    // Costs: a run of consecutive items per thread, then over the threads.
+    const int iper = (W + kSchedThreads - 1) / kSchedThreads;
+    const int i0 = min(W, tid * iper), i1 = min(W, i0 + iper);
+    int seq = 0;
+    if (i0 < i1) {  // the sequence of item i0
+        int hi = a.S;
+        while (hi - seq > 1) {
+            const int mid = (seq + hi) >> 1;
+            if (s_first[mid] <= i0) seq = mid;
             else hi = mid;
         }
-        const SeqLen q = seq_len(a, lo);
-        p.tiles[t] = chunk_tile(q, lo, p.g, chunk_parts(q, len), t - s_first[lo], a.causal != 0);
     }
-    if (tid == 0) *p.count = W;
+    auto item_at = [&](int i, int &s) -> ChunkItem {
+        while (s_first[s + 1] <= i) s++;
+        return chunk_item(seq_len(a, s), s, p.g, i - s_first[s], causal);
+    };
+    mine = 0;
+    for (int i = i0, s = seq; i < i1; i++) {
+        const ChunkItem t = item_at(i, s);
+        mine += chunk_cost(t.n_kv, t.nt);
+    }
+    unsigned long long U;
+    unsigned long long first = block_scan(mine, s_warp, &U);
+    const int nb = chunk_blocks(U, p.grid, p.least);
+    const ChunkCuts cuts = chunk_cuts(U, nb);
+    for (int i = i0, s = seq; i < i1; i++) {
+        ChunkItem t = item_at(i, s);
+        t.first = first;
+        p.items[i] = t;
+        first += chunk_cost(t.n_kv, t.nt);
+        // Blocks whose runs start in this item.
+        int c = chunk_block_of(cuts, t.first);
+        if (cuts.cut(c) < t.first) c++;
+        for (; c < nb && cuts.cut(c) < first; c++) p.run_first[c] = i;
+        const ChunkOwners o = chunk_owners(t, cuts);
+        // (the order of the list does not matter: it only says which block joins what)
+        if (o.count > 2) p.join[atomicAdd(&s_joins, 1)] = make_int2(o.count, i);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        p.head[0] = W;
+        p.head[1] = U;
+        p.head[2] = nb;
+        *p.joins = s_joins;
+    }
     if (bad) atomicOr(&g_chunk_error_word, bad);
 }
 
-// i-th tile of this block (-1: no more).
-__device__ __forceinline__ int tile_at(int i, int W)
+// A block's run of items.
+struct Run {
+    int first, items;      // its first item; items in all
+    unsigned long long lo, hi;
+    ChunkCuts cuts;
+};
+
+// One item of the run: the key tiles [start, start + n) of it are this block's.
+struct Work {
+    ChunkItem t;
+    int start, n;
+    bool whole;
+};
+
+__device__ __forceinline__ bool load_work(const ChunkParams &p, const Run &r, int i, Work &k)
 {
-    const int G = gridDim.x;
-    const int t = i * G + ((i & 1) ? G - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
-    if (i * static_cast<int64_t>(G) >= W) return -1;
-    return t < W ? t : -2;  // -2: this round has no tile for the block
+    k.t = load_item(p, i);
+    const ChunkRange g = chunk_range(k.t, r.lo, r.hi);
+    k.start = g.t0;
+    k.n = g.t1 - g.t0;
+    k.whole = g.t0 == 0 && g.t1 == k.t.n_kv;
+    return k.t.first < r.hi;  // false: behind the run
 }
 
-__device__ __forceinline__ ChunkTile load_tile(const ChunkParams &p, int t)
-{
-    union { int4 v[3]; ChunkTile c; } u;
-    const int4 *src = reinterpret_cast<const int4 *>(p.tiles + t);
-    u.v[0] = __ldg(src);
-    u.v[1] = __ldg(src + 1);
-    u.v[2] = __ldg(src + 2);
-    return u.c;
-}
-
-// Loop over this block's work tiles; `w` counts them.
-#define CLIS_FOR_TILES(T)                                                  \
-    for (int i_ = 0, t_; (t_ = tile_at(i_, W)) != -1; ++i_)                \
-        if (t_ >= 0)                                                       \
-            if (const ChunkTile T = load_tile(p, t_); true)
+// Loop over the block's items that have key tiles in its run.
+#define CLIS_FOR_WORK(K)                                                              \
+    Work K;                                                                           \
+    for (int i_ = R.first; i_ < R.items && load_work(p, R, i_, K); ++i_)              \
+        if (K.n > 0)
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
 {
@@ -197,7 +276,7 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
 // ----------------------------------------------------------------- producers
 
 template <int D>
-__device__ void q_producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *tm_q, uint32_t sQ0, int W)
+__device__ void q_producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *tm_q, uint32_t sQ0, const Run &R)
 {
     using C = Cfg<D>;
     volatile int *ab = &c.abort_flag;
@@ -205,8 +284,9 @@ __device__ void q_producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap 
     const bool leader = elect_one();
     const uint64_t pol = policy_evict_first();
     int wt[2] = {0, 0};
-    CLIS_FOR_TILES(T)
+    CLIS_FOR_WORK(K)
     {
+        const ChunkItem &T = K.t;
 #pragma unroll
         for (int t = 0; t < 2; t++) {
             if (t >= T.nt) break;
@@ -231,7 +311,7 @@ abort:
 
 template <int D>
 __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
-                              uint32_t sKV, int W)
+                              uint32_t sKV, const Run &R)
 {
     using C = Cfg<D>;
     const PagedArgs &a = p.a;
@@ -243,20 +323,21 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
     const uint64_t pol = policy_evict_last();
     uint32_t it = 0, gq = 0;
     unsigned int bad = 0;
-    CLIS_FOR_TILES(T)
+    CLIS_FOR_WORK(K)
     {
+        const ChunkItem &T = K.t;
         // Page of the lane's rows of key tile kt; -2: behind the last key, not loaded.
         auto page_of = [&](int kt) -> int {
             const int key = kt * BN + lane * p.box_rows;
             if (lane >= npg || key >= T.kv) return -2;
             return __ldg(a.block_table + T.s * a.bt_s + (key >> a.page_shift));
         };
-        int pg_k = page_of(T.start), pg_v = -2;
+        int pg_k = page_of(K.start), pg_v = -2;
         // Groups of loads as the MMA warp needs them: {K_0}, {V_0, K_1}, ..., {V_{n-1}}.
-        for (int gi = 0; gi <= T.n_kv; gi++) {
-            const bool has_v = gi > 0, has_k = gi < T.n_kv;
+        for (int gi = 0; gi <= K.n; gi++) {
+            const bool has_v = gi > 0, has_k = gi < K.n;
             const int nl = (has_v ? 1 : 0) + (has_k ? 1 : 0);
-            const int pg_next = gi + 1 < T.n_kv ? page_of(T.start + gi + 1) : -2;
+            const int pg_next = gi + 1 < K.n ? page_of(K.start + gi + 1) : -2;
             for (int l = 0; l < nl; l++) {
                 const uint32_t li = it + l;
                 if (!mbar_wait_warp(smem_u32(&c.kv_empty[li % C::NSTAGE]), ((li / C::NSTAGE) & 1) ^ 1, ab, err,
@@ -278,7 +359,7 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
                     pg = static_cast<int>(a.num_pages);  // out of the map: its rows read as zeros
                 }
                 const uint32_t slot = (it + (is_v ? 0 : nl - 1)) % C::NSTAGE;
-                const int key = (T.start + (is_v ? gi - 1 : gi)) * BN + lane * p.box_rows;
+                const int key = (K.start + (is_v ? gi - 1 : gi)) * BN + lane * p.box_rows;
                 const uint32_t dst = sKV + slot * C::TILE_BYTES + lane * box_bytes;
                 const CUtensorMap *tm = is_v ? tm_v : tm_k;
 #pragma unroll
@@ -327,7 +408,7 @@ __device__ __forceinline__ bool scrub(uint32_t &u)
 }
 
 template <int D, int DT>
-__device__ void edge_role(const ChunkParams &p, Ctl &c, uint32_t sKV, int W)
+__device__ void edge_role(const ChunkParams &p, Ctl &c, uint32_t sKV, const Run &R)
 {
     using C = Cfg<D>;
     volatile int *ab = &c.abort_flag;
@@ -335,12 +416,13 @@ __device__ void edge_role(const ChunkParams &p, Ctl &c, uint32_t sKV, int W)
     const int lane = threadIdx.x & 31;
     uint32_t it = 0, gq = 0, nedge = 0;
     int w = 0;
-    CLIS_FOR_TILES(T)
+    CLIS_FOR_WORK(K)
     {
+        const ChunkItem &T = K.t;
         const int first = chunk_first_masked(T, p.a.causal != 0);
         bool dirty = false;
-        for (int j = 0; j < T.n_kv; j++) {
-            const int kt = T.start + j;
+        for (int j = 0; j < K.n; j++) {
+            const int kt = K.start + j;
             if (kt < first) continue;
             // V_j is in load group j + 1 and in ring slot 2 j + 1 of the work tile's
             // (K_0, V_0, K_1, V_1, ...).  The MMA warp, which waits for every group,
@@ -388,8 +470,8 @@ __device__ void edge_role(const ChunkParams &p, Ctl &c, uint32_t sKV, int W)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c.edge_ok));
         }
-        it += 2 * T.n_kv;
-        gq += T.n_kv + 1;
+        it += 2 * K.n;
+        gq += K.n + 1;
         ++w;
     }
 }
@@ -417,26 +499,48 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint6
         umma_ts(o_tmem, p_tmem + kk * 8, vd + ((kk * 2048) >> 4), IDESC_O, (accumulate | kk) ? 1u : 0u);
 }
 
+// O_t (+)= P_t V_j, in the MMA role's loop: the group is a compile-time constant, so
+// that addresses and descriptors stay in uniform registers.
+#define CLIS_PRODUCT(t, fresh, frees)                                                                               \
+    do {                                                                                                            \
+        if (!mbar_wait_warp(smem_u32(&c.p_full[t]), (steps >> (t)) & 1, ab, err, kErrMma)) goto abort;               \
+        if (fresh)                                                                                                  \
+            if (!mbar_wait_warp(smem_u32(&c.o_free[t]), (items & 1) ^ 1, ab, err, kErrMma)) goto abort;              \
+        tc_fence_after();                                                                                           \
+        if (leader) {                                                                                               \
+            issue_pv<D, DT>(tmem + ((t) ? C::TM_O1 : C::TM_O0), tmem + ((t) ? C::TM_S1 : C::TM_S0), vd,              \
+                            (fresh) ? 0u : 1u);                                                                     \
+            umma_commit(smem_u32(&c.pv_done[t]));                                                                   \
+            if (frees) umma_commit(smem_u32(&c.kv_empty[vs]));                                                      \
+        }                                                                                                           \
+        __syncwarp();                                                                                               \
+        steps ^= 1u << (t);                                                                                         \
+    } while (0)
+
 template <int D, int DT>
-__device__ void mma_role(const ChunkParams &p, Ctl &c, uint32_t tmem, uint32_t sQ0, uint32_t sKV, int W)
+__device__ void mma_role(const ChunkParams &p, Ctl &c, uint32_t tmem, uint32_t sQ0, uint32_t sKV, const Run &R)
 {
     using C = Cfg<D>;
     volatile int *ab = &c.abort_flag;
     unsigned *err = &g_chunk_error_word;
     const bool leader = elect_one();
     uint32_t it = 0, gq = 0, nedge = 0;
-    uint32_t wt[2] = {0, 0}, gt[2] = {0, 0};  // per row tile: work tiles, steps
+    uint32_t items = 0;             // parities: of the items,
+    uint32_t steps = 0, q_par = 0;  // of each group's steps and Q tiles (bit t)
     const uint64_t qd0 = sdesc_sw128(sQ0, 16, 1024);
     const uint64_t qd1 = sdesc_sw128(sQ0 + C::TILE_BYTES, 16, 1024);
     const uint64_t kvd_k = sdesc_sw128(sKV, 16, 1024);
     const uint64_t kvd_v = sdesc_sw128(sKV, C::BOX_BYTES, 1024);
     auto stage_off = [](uint32_t s) -> uint64_t { return (s * C::TILE_BYTES) >> 4; };
-    CLIS_FOR_TILES(T)
+    CLIS_FOR_WORK(K)
     {
+        const ChunkItem &T = K.t;
         const int nt = T.nt;
         const int first = chunk_first_masked(T, p.a.causal != 0);
-        for (int t = 0; t < nt; t++)
-            if (!mbar_wait_warp(smem_u32(&c.q_full[t]), wt[t] & 1, ab, err, kErrMma)) goto abort;
+        for (int t = 0; t < nt; t++) {
+            if (!mbar_wait_warp(smem_u32(&c.q_full[t]), (q_par >> t) & 1, ab, err, kErrMma)) goto abort;
+            q_par ^= 1u << t;
+        }
         {
             const uint32_t ks = it % C::NSTAGE;
             if (!mbar_wait_warp(smem_u32(&c.kv_full[gq % C::NSTAGE]), (gq / C::NSTAGE) & 1, ab, err, kErrMma))
@@ -452,53 +556,63 @@ __device__ void mma_role(const ChunkParams &p, Ctl &c, uint32_t tmem, uint32_t s
                     umma_commit(smem_u32(&c.s_full[1]));
                 }
                 umma_commit(smem_u32(&c.kv_empty[ks]));
-                if (T.n_kv == 1)
+                if (K.n == 1)
                     for (int t = 0; t < nt; t++) umma_commit(smem_u32(&c.q_empty[t]));
             }
             __syncwarp();
             ++it;
         }
-        for (int j = 0; j < T.n_kv; j++) {
-            const bool has_next = j + 1 < T.n_kv;
+        for (int j = 0; j < K.n; j++) {
+            const bool has_next = j + 1 < K.n;
             const uint32_t vs = it % C::NSTAGE;
             if (!mbar_wait_warp(smem_u32(&c.kv_full[gq % C::NSTAGE]), (gq / C::NSTAGE) & 1, ab, err, kErrMma))
                 goto abort;
             ++gq;
-            const bool edge = T.start + j >= first;
+            const bool edge = K.start + j >= first;
             if (edge && leader) mbar_arrive(smem_u32(&c.edge_go));
+            const uint64_t vd = kvd_v + stage_off(vs);
+            const uint32_t kns = (it + 1) % C::NSTAGE;
+            const uint64_t kd = kvd_k + stage_off(kns);
+            const bool last_k = j + 1 == K.n - 1;  // K_{j+1} is the item's last key tile
             if (edge) {
                 if (!mbar_wait_warp(smem_u32(&c.edge_ok), nedge & 1, ab, err, kErrMma)) goto abort;
                 ++nedge;
             }
-            const uint64_t vd = kvd_v + stage_off(vs);
-            const uint32_t kns = (it + 1) % C::NSTAGE;
-            const uint64_t kd = kvd_k + stage_off(kns);
+            if (nt == 2) {
 #pragma unroll
-            for (int t = 0; t < 2; t++) {
-                if (t >= nt) break;
-                const bool last = t == nt - 1;
-                if (!mbar_wait_warp(smem_u32(&c.p_full[t]), gt[t] & 1, ab, err, kErrMma)) goto abort;
-                if (j == 0)
-                    if (!mbar_wait_warp(smem_u32(&c.o_free[t]), (wt[t] & 1) ^ 1, ab, err, kErrMma)) goto abort;
-                tc_fence_after();
-                if (leader) {
-                    issue_pv<D, DT>(tmem + (t ? C::TM_O1 : C::TM_O0), tmem + (t ? C::TM_S1 : C::TM_S0), vd,
-                                    j > 0 ? 1u : 0u);
-                    umma_commit(smem_u32(&c.pv_done[t]));
-                    if (last) umma_commit(smem_u32(&c.kv_empty[vs]));
+                for (int t = 0; t < 2; t++) {
+                    CLIS_PRODUCT(t, j == 0, t == 1);
                     if (has_next) {
-                        issue_qk<D, DT>(tmem + (t ? C::TM_S1 : C::TM_S0), t ? qd1 : qd0, kd);
-                        umma_commit(smem_u32(&c.s_full[t]));
-                        if (last) umma_commit(smem_u32(&c.kv_empty[kns]));
-                        if (j + 1 == T.n_kv - 1) umma_commit(smem_u32(&c.q_empty[t]));
+                        if (leader) {
+                            issue_qk<D, DT>(tmem + (t ? C::TM_S1 : C::TM_S0), t ? qd1 : qd0, kd);
+                            umma_commit(smem_u32(&c.s_full[t]));
+                            if (t == 1) umma_commit(smem_u32(&c.kv_empty[kns]));
+                            if (last_k) umma_commit(smem_u32(&c.q_empty[t]));
+                        }
+                        __syncwarp();
                     }
                 }
-                __syncwarp();
-                ++gt[t];
+            } else {
+                // One row tile: the other group's next scores first (its last product was
+                // issued before), then this group's product.
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    if ((j & 1) != t) continue;
+                    if (has_next) {
+                        if (leader) {
+                            issue_qk<D, DT>(tmem + (t ? C::TM_S0 : C::TM_S1), qd0, kd);
+                            umma_commit(smem_u32(&c.s_full[t ^ 1]));
+                            umma_commit(smem_u32(&c.kv_empty[kns]));
+                            if (last_k) umma_commit(smem_u32(&c.q_empty[0]));
+                        }
+                        __syncwarp();
+                    }
+                    CLIS_PRODUCT(t, j < 2, true);
+                }
             }
             it += has_next ? 2 : 1;
         }
-        for (int t = 0; t < nt; t++) ++wt[t];
+        ++items;
     }
     return;
 abort:
@@ -509,8 +623,34 @@ abort:
 
 // ------------------------------------------------------------------- softmax
 
+// Weights of a row's 128 scores for a shift, p = 2^(scale_log2 s - shift), packed in
+// pairs over the first 64 columns of the scores, all of which have been read;
+// returns their sum (before rounding).
+template <int DT>
+__device__ __forceinline__ float weights128(const uint32_t *s, float sl2, float nshift, uint32_t tP)
+{
+    const float2 sc2 = make_float2(sl2, sl2), sh2 = make_float2(nshift, nshift);
+    float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c32 = 0; c32 < BN / 32; c32++) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+            const float2 x = ffma2(
+                make_float2(__uint_as_float(s[c32 * 32 + 2 * e]), __uint_as_float(s[c32 * 32 + 2 * e + 1])), sc2, sh2);
+            const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            if (e & 1) lb = fadd2(lb, pp);
+            else la = fadd2(la, pp);
+            pk[e] = pack2<DT>(pp.x, pp.y);
+        }
+        tmem_st16(tP + c32 * 16, pk);
+    }
+    const float2 l = fadd2(la, lb);
+    return l.x + l.y;
+}
+
 template <int D, int DT>
-__device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int warp, int lane, int W)
+__device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int warp, int lane, const Run &R)
 {
     using C = Cfg<D>;
     volatile int *ab = &c.abort_flag;
@@ -525,14 +665,18 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
     const int row_tok = rl / p.g;  // token within the row tile
     uint32_t g = 0;
     int w = 0;
-    CLIS_FOR_TILES(T)
+    CLIS_FOR_WORK(K)
     {
-        if (t >= T.nt) continue;
-        const int tok = T.tok0 + t * p.tpt + row_tok;
-        const bool row_ok = row_tok < p.tpt && tok < T.n && !T.masked;
+        const ChunkItem &T = K.t;
+        const bool single = T.nt == 1;  // the groups share the row tile, key tiles in turn
+        const int tok = T.tok0 + (single ? 0 : t * p.tpt) + row_tok;
+        const bool row_ok = row_tok < p.tpt && tok < T.n;
         const int lim = row_ok ? visible_keys(T.n, T.kv, tok, p.a.causal) : 0;  // keys [0, lim) are visible
+        const int step = single ? 2 : 1;
         float m_run = -INFINITY, l_run = 0.f;
-        for (int j = 0; j < T.n_kv; j++) {
+        bool begun = false;  // O holds a product of this item
+#pragma unroll 1
+        for (int j = single ? t : 0; j < K.n; j += step) {
             if (!mbar_wait(smem_u32(&c.s_full[t]), g & 1, ab, err, kErrSoftmax)) return;
             tc_fence_after();
             uint32_t s[BN];
@@ -541,12 +685,13 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
             tmem_ld32(tS + 64, s + 64);
             tmem_ld32(tS + 96, s + 96);
             tmem_wait_ld();
-            const int key0 = (T.start + j) * BN;
+            const int key0 = (K.start + j) * BN;
             if (key0 + BN > lim) {
 #pragma unroll
                 for (int cc = 0; cc < BN; cc++)
                     if (key0 + cc >= lim) s[cc] = 0xFF800000u;  // -inf
             }
+            float l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int cc = 0; cc < BN; cc += 8) {
@@ -555,56 +700,39 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
                     mx[q4] = fmax3(mx[q4], __uint_as_float(s[cc + 2 * q4]), __uint_as_float(s[cc + 2 * q4 + 1]));
             }
             const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-            float alpha = 1.f;
-            const bool grow = m_tile > m_run + kTau;
-            if (grow) {
-                if (j > 0) alpha = ex2_approx(m_run - m_tile);
-                m_run = m_tile;
-            }
-            const bool rescale = j > 0 && __any_sync(0xFFFFFFFFu, grow);
-            const float nshift = (m_run == -INFINITY) ? 0.f : -m_run;
-            const float2 sc2 = make_float2(sl2, sl2), sh2 = make_float2(nshift, nshift);
-            float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c32 = 0; c32 < BN / 32; c32++) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; e++) {
-                    const float2 x = ffma2(make_float2(__uint_as_float(s[c32 * 32 + 2 * e]),
-                                                       __uint_as_float(s[c32 * 32 + 2 * e + 1])),
-                                           sc2, sh2);
-                    const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                    if (e & 1) lb = fadd2(lb, pp);
-                    else la = fadd2(la, pp);
-                    pk[e] = pack2<DT>(pp.x, pp.y);
-                }
-                tmem_st16(tS + c32 * 16, pk);
-            }
-            const float2 lab = fadd2(la, lb);
-            l_run = l_run * alpha + (lab.x + lab.y);
-            if (rescale) {
-                // O of the warp's rows shrinks to the new shift once the previous product
-                // is in it, before this step's arrival lets the next one start.
-                if (!mbar_wait(smem_u32(&c.pv_done[t]), (g - 1) & 1, ab, err, kErrSoftmax)) return;
-                tc_fence_after();
-                const float2 a2 = make_float2(alpha, alpha);
+            const bool grow = m_tile > m_run + kTau;  // always true where a row's first visible key is
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                // Raise the shift, compute the tile's weights again, and shrink O once the
+                // last product is in it.
+                const float alpha = grow ? ex2_approx(m_run - m_tile) : 1.f;
+                if (grow) m_run = m_tile;
+                l_run *= alpha;
+                l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
+                if (begun) {
+                    if (!mbar_wait(smem_u32(&c.pv_done[t]), (g - 1) & 1, ab, err, kErrSoftmax)) return;
+                    tc_fence_after();
+                    const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll 1
-                for (int c32 = 0; c32 < D / 32; c32++) {
-                    uint32_t r[32];
-                    tmem_ld32(tO + c32 * 32, r);
-                    tmem_wait_ld();
+                    for (int c16 = 0; c16 < D / 16; c16++) {
+                        uint32_t r[16];
+                        tmem_ld16(tO + c16 * 16, r);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 o2 = fmul2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), a2);
-                        r[e] = __float_as_uint(o2.x);
-                        r[e + 1] = __float_as_uint(o2.y);
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 o2 = fmul2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), a2);
+                            r[e] = __float_as_uint(o2.x);
+                            r[e + 1] = __float_as_uint(o2.y);
+                        }
+                        tmem_st16(tO + c16 * 16, r);
                     }
-                    tmem_st32(tO + c32 * 32, r);
                 }
             }
+            l_run += l;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_u32(&c.p_full[t]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.p_full[t]));  // one arrival per warp
+            begun = true;
             ++g;
         }
         // Row sum and shift for the epilogue, which must have read the previous ones.
@@ -618,8 +746,70 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
 
 // ------------------------------------------------------------------ epilogue
 
+// Adds to 16 columns of an output row the non-finite values of the keys [from, see).
+template <int DT>
+__device__ __forceinline__ void add_not_finite(float *o, const ChunkItem &T, int from, int see, int col, const ChunkParams &p)
+{
+    const PagedArgs &a = p.a;
+#pragma unroll 1
+    for (int key = from; key < see; key++) {
+        const int pg = __ldg(a.block_table + T.s * a.bt_s + (key >> a.page_shift));
+        if (pg < 0 || pg >= a.num_pages) continue;
+        const uint32_t *vs = reinterpret_cast<const uint32_t *>(
+            a.vc + static_cast<int64_t>(pg) * a.vc_sp + T.h * a.vc_sh +
+            static_cast<int64_t>(key & ((1 << a.page_shift) - 1)) * a.vc_sn + col);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const uint32_t u = __ldg(vs + e);
+            const float lo = elem_lo<DT>(u), hi = elem_hi<DT>(u);
+            if (!isfinite(lo)) o[2 * e] += lo;
+            if (!isfinite(hi)) o[2 * e + 1] += hi;
+        }
+    }
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// The same barrier; true in all threads if `bad` in one.
+__device__ __forceinline__ bool epilogue_any(bool bad)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "selp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(bad ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
+// Partial result of place `slot` [D / 4][256][4] (a warp's rows lie side by side).
+template <int D>
+__device__ __forceinline__ float4 *part_at(const ChunkParams &p, int64_t slot, int c4, int r)
+{
+    return reinterpret_cast<float4 *>(p.part_o) + (slot * (D / 4) + c4) * (2 * BM) + r;
+}
+
+// 16 columns of an output row; inv = 1 / l, none: the row sees no key.
+template <int DT>
+__device__ __forceinline__ void store16(uint16_t *dst, const float *o, float inv, bool none, uint64_t pol)
+{
+    uint32_t pk[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) pk[e] = none ? 0u : pack2<DT>(o[2 * e] * inv, o[2 * e + 1] * inv);
+    st_global_v4_hint(dst, make_uint4(pk[0], pk[1], pk[2], pk[3]), pol);
+    st_global_v4_hint(dst + 8, make_uint4(pk[4], pk[5], pk[6], pk[7]), pol);
+}
+
 template <int D, int DT>
-__device__ void epilogue_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int warp, int lane, int W)
+__device__ void epilogue_role(const ChunkParams &p, Ctl &c, uint32_t tmem, uint32_t sKV, int warp, int lane, const Run &R)
 {
     using C = Cfg<D>;
     const PagedArgs &a = p.a;
@@ -629,82 +819,210 @@ __device__ void epilogue_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int w
     const int rl = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const int row_tok = rl / p.g, row_head = rl - row_tok * p.g;
-    const uint64_t pol_o = policy_evict_first();
-    uint32_t gt[2] = {0, 0}, wt[2] = {0, 0};
+    const bool lead = rl == 0;
+    const uint64_t pol = policy_evict_first();
+    uint32_t g0 = 0, g1 = 0;  // steps of the two groups
     int w = 0;
-    CLIS_FOR_TILES(T)
+    CLIS_FOR_WORK(K)
     {
+        const ChunkItem &T = K.t;
         const int first = chunk_first_masked(T, a.causal != 0);
-        const bool edges = T.start + T.n_kv > first;
+        const bool edges = K.start + K.n > first;
+        ChunkOwners own = {static_cast<int>(blockIdx.x), 1};
+        if (!K.whole) own = chunk_owners(T, R.cuts);
+        const int me = static_cast<int>(blockIdx.x) - own.c;
+        // The second of two parts done already (the usual case: the first part is the
+        // last work of its block, the second the first of the next block): the first
+        // need not go through memory.
+        bool direct = false;
+        if (own.count == 2 && me == 0) {
+            if (lead) {
+                int n;
+                asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(n) : "l"(p.arrived + own.c) : "memory");
+                c.last = n == 1;
+            }
+            epilogue_barrier();
+            direct = c.last != 0;
+            epilogue_barrier();  // (c.last is written again below or by the next item)
+        }
+        const bool to_memory = own.count > 1 && !direct;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (K.start == 0 ? 1 : 0);
+        const int64_t slot0 = 2 * own.c + 1, slot1 = 2 * (own.c + 1);  // the two parts' places
+
+        // A single row tile's own values are the sum of both groups'.
+        const bool single = T.nt == 1;
+        float w_even = 1.f, w_odd = 0.f;
+        bool has_odd = false;
+        auto own16 = [&](uint32_t tO, int c16, float *o) {
+            uint32_t x[16];
+            tmem_ld16(tO + c16 * 16, x);
+            tmem_wait_ld();
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-            if (t >= T.nt) break;
-            gt[t] += T.n_kv;
-            if (!mbar_wait(smem_u32(&c.epi_full[t]), wt[t] & 1, ab, err, kErrEpilogue)) return;
-            if (!mbar_wait(smem_u32(&c.pv_done[t]), (gt[t] - 1) & 1, ab, err, kErrEpilogue)) return;
+            for (int e = 0; e < 16; e++) o[e] = __uint_as_float(x[e]);
+            if (has_odd) {
+                tmem_ld16(tO + (C::TM_O1 - C::TM_O0) + c16 * 16, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e++) o[e] = fmaf(w_odd, __uint_as_float(x[e]), w_even * o[e]);
+            }
+        };
+        // Joins the two parts of row tile t: the first from TMEM (staged = the place of
+        // the second in shared memory) or, with staged = 0, both from memory.
+        auto join_rows = [&](int t, uint32_t staged, float l0, float m0, int key_from, int see) {
+            const int r = t * BM + rl, tok = T.tok0 + t * p.tpt + row_tok;
+            const bool row_ok = row_tok < p.tpt && tok < T.n;
+            float2 a0 = make_float2(m0, l0), a1 = make_float2(-INFINITY, 0.f);
+            if (row_ok) {
+                if (!staged) a0 = __ldcg(p.part_ml + slot0 * (2 * BM) + r);
+                a1 = __ldcg(p.part_ml + slot1 * (2 * BM) + r);
+            }
+            // (a part none of whose keys the row sees adds nothing)
+            const bool any0 = a0.y != 0.f, any1 = a1.y != 0.f;
+            const float M = !any0 ? a1.x : !any1 ? a0.x : fmaxf(a0.x, a1.x);
+            const float w0 = any0 ? ex2_approx(a0.x - M) : 0.f, w1 = any1 ? ex2_approx(a1.x - M) : 0.f;
+            float l = any0 ? w0 * a0.y : 0.f;
+            if (any1) l = fmaf(w1, a1.y, l);
+            const int hd = T.h * p.g + row_head;
+            uint16_t *orow = a.o + static_cast<int64_t>(T.q0 + tok) * a.o_st + hd * a.o_sh;
+            const uint32_t tO = tmem + (t ? C::TM_O1 : C::TM_O0) + lane_off;
+            const float inv = 1.f / l;
+#pragma unroll 1
+            for (int c16 = 0; c16 < D / 16; c16++) {
+                float o[16];
+                if (staged) {
+                    own16(tO, c16, o);
+                    if (key_from >= 0) add_not_finite<DT>(o, T, key_from, see, c16 * 16, p);
+                }
+                if (!row_ok) continue;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    if (!staged) {
+                        const float4 x = __ldcg(part_at<D>(p, slot0, c16 * 4 + e, r));
+                        o[4 * e] = x.x; o[4 * e + 1] = x.y; o[4 * e + 2] = x.z; o[4 * e + 3] = x.w;
+                    }
+                    float4 y;
+                    if (staged) {
+                        const uint4 u = lds128(staged + ((t * (D / 4) + c16 * 4 + e) * BM + rl) * 16);
+                        y = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+                    } else {
+                        y = __ldcg(part_at<D>(p, slot1, c16 * 4 + e, r));
+                    }
+                    const float yy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int f = 0; f < 4; f++) {
+                        const float x = any0 ? w0 * o[4 * e + f] : 0.f;
+                        o[4 * e + f] = any1 ? fmaf(w1, yy[f], x) : x;
+                    }
+                }
+                store16<DT>(orow + c16 * 16, o, inv, l == 0.f, pol);
+            }
+            if (row_ok && a.lse2) a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
+        };
+
+#pragma unroll 1
+        for (int t = 0; t < T.nt; t++) {
+            bool ok;
+            if (single) {
+                g0 += (K.n + 1) / 2;
+                g1 += K.n / 2;
+                ok = mbar_wait(smem_u32(&c.epi_full[0]), w & 1, ab, err, kErrEpilogue) &&
+                     mbar_wait(smem_u32(&c.epi_full[1]), w & 1, ab, err, kErrEpilogue) &&
+                     mbar_wait(smem_u32(&c.pv_done[0]), (g0 - 1) & 1, ab, err, kErrEpilogue) &&
+                     (K.n < 2 || mbar_wait(smem_u32(&c.pv_done[1]), (g1 - 1) & 1, ab, err, kErrEpilogue));
+            } else {
+                const uint32_t steps = t ? g1 += K.n : g0 += K.n;
+                ok = mbar_wait(smem_u32(&c.epi_full[t]), w & 1, ab, err, kErrEpilogue) &&
+                     mbar_wait(smem_u32(&c.pv_done[t]), (steps - 1) & 1, ab, err, kErrEpilogue);
+            }
+            // A wait that gave up ends all four warps together: one that went on would
+            // stay at the barriers of a later item.
+            if (epilogue_any(!ok)) return;
             tc_fence_after();
             const bool dirty = edges && *reinterpret_cast<volatile int *>(&c.dirty[w & 7]) != 0;
             const uint32_t tO = tmem + (t ? C::TM_O1 : C::TM_O0) + lane_off;
             const int tok = T.tok0 + t * p.tpt + row_tok;
             const bool row_ok = row_tok < p.tpt && tok < T.n;
-            const float l = c.epi_l[t][rl], shift = c.epi_shift[t][rl];
-            const float inv = 1.f / l;
-            const int see = min(visible_keys(T.n, T.kv, tok, a.causal), (T.start + T.n_kv) * BN);
-            const int hd = T.h * p.g + row_head;
-            uint16_t *orow = a.o + static_cast<int64_t>(T.q0 + tok) * a.o_st + hd * a.o_sh;
-            const int64_t prow = static_cast<int64_t>(t_) * (2 * BM) + t * BM + rl;
+            float l = c.epi_l[t][rl], shift = c.epi_shift[t][rl];
+            if (single) {
+                const float l1 = c.epi_l[1][rl], m1 = c.epi_shift[1][rl];
+                const float M = l == 0.f ? m1 : l1 == 0.f ? shift : fmaxf(shift, m1);
+                has_odd = K.n > 1;
+                w_even = l == 0.f ? 0.f : ex2_approx(shift - M);  // (a group none of whose keys the row sees adds nothing)
+                w_odd = l1 == 0.f ? 0.f : ex2_approx(m1 - M);
+                l = (l == 0.f ? 0.f : w_even * l) + (l1 == 0.f ? 0.f : w_odd * l1);
+                shift = M;
+            }
+            // Non-finite values of keys from key_from on that the row sees were left out of
+            // the product (-1: none were).
+            const int key_from = dirty ? max(first, K.start) * BN : -1;
+            const int see = row_ok ? min(visible_keys(T.n, T.kv, tok, a.causal), (K.start + K.n) * BN) : 0;
+            if (direct) {
+                if (t == 0) {
+                    // The block's last work: once every product is done the K/V ring is free,
+                    // and the other part is staged there, each thread its own row.
+                    if (T.nt == 2) {
+                        const bool ok1 = mbar_wait(smem_u32(&c.epi_full[1]), w & 1, ab, err, kErrEpilogue) &&
+                                         mbar_wait(smem_u32(&c.pv_done[1]), (g1 + K.n - 1) & 1, ab, err, kErrEpilogue);
+                        if (epilogue_any(!ok1)) return;
+                    }
+                    for (int u = 0; u < T.nt; u++) {
+                        const int rtok = T.tok0 + u * p.tpt + row_tok;
+                        if (row_tok >= p.tpt || rtok >= T.n) continue;  // never written
+#pragma unroll 8
+                        for (int c4 = 0; c4 < D / 4; c4++)
+                            cp_async16(sKV + ((u * (D / 4) + c4) * BM + rl) * 16, part_at<D>(p, slot1, c4, u * BM + rl));
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                }
+                join_rows(t, sKV, l, shift, key_from, see);
+            } else {
+                const int hd = T.h * p.g + row_head;
+                const float inv = 1.f / l;
+                uint16_t *orow = a.o + static_cast<int64_t>(T.q0 + tok) * a.o_st + hd * a.o_sh;
 #pragma unroll 1
-            for (int c32 = 0; c32 < D / 32; c32++) {
-                uint32_t r[32];
-                tmem_ld32(tO + c32 * 32, r);
-                tmem_wait_ld();
-                if (!row_ok) continue;
-                if (dirty && !T.masked) {
-                    // Non-finite values of keys that this row sees and that were left out.
-#pragma unroll 1
-                    for (int key = max(first, T.start) * BN; key < see; key++) {
-                        const int pg = __ldg(a.block_table + T.s * a.bt_s + (key >> a.page_shift));
-                        if (pg < 0 || pg >= a.num_pages) continue;
-                        const uint16_t *vs = a.vc + static_cast<int64_t>(pg) * a.vc_sp + T.h * a.vc_sh +
-                                             static_cast<int64_t>(key & ((1 << a.page_shift) - 1)) * a.vc_sn + c32 * 32;
+                for (int c16 = 0; c16 < D / 16; c16++) {
+                    float o[16];
+                    own16(tO, c16, o);
+                    if (c16 == D / 16 - 1) {  // O has been read: the next item's products may start
+                        tc_fence_before();
+                        mbar_arrive(smem_u32(&c.o_free[t]));
+                        if (single) mbar_arrive(smem_u32(&c.o_free[1]));
+                    }
+                    if (!row_ok) continue;
+                    if (key_from >= 0) add_not_finite<DT>(o, T, key_from, see, c16 * 16, p);
+                    if (to_memory) {
 #pragma unroll
-                        for (int e = 0; e < 32; e++) {
-                            const float x = elem_lo<DT>(__ldg(vs + e));
-                            if (!isfinite(x)) r[e] = __float_as_uint(__uint_as_float(r[e]) + x);
-                        }
+                        for (int e = 0; e < 4; e++)
+                            __stcg(part_at<D>(p, slot, c16 * 4 + e, t * BM + rl),
+                                   make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                    } else {
+                        store16<DT>(orow + c16 * 16, o, inv, l == 0.f, pol);
                     }
                 }
-                if (T.parts > 1) {
-                    float4 *d4 = reinterpret_cast<float4 *>(p.part_o + prow * D + c32 * 32);
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        d4[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                                            __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-                } else {
-                    uint32_t pk[16];
-                    const float2 inv2 = make_float2(inv, inv);
-#pragma unroll
-                    for (int e = 0; e < 16; e++) {
-                        const float2 o2 =
-                            fmul2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), inv2);
-                        pk[e] = l == 0.f ? 0u : pack2<DT>(o2.x, o2.y);  // a row that sees no key
-                    }
-                    uint4 *dst = reinterpret_cast<uint4 *>(orow + c32 * 32);
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        st_global_v4_hint(dst + e,
-                                          make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]), pol_o);
+                if (row_ok) {
+                    if (to_memory)
+                        __stcg(p.part_ml + slot * (2 * BM) + t * BM + rl, make_float2(shift, l));
+                    else if (a.lse2)
+                        a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : shift + log2f(l);
                 }
             }
-            if (row_ok) {
-                if (T.parts > 1)
-                    p.part_ml[prow] = make_float2(shift, l);
-                else if (a.lse2)
-                    a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : shift + log2f(l);
+            if (direct) {  // (the block's last item: nobody waits for it any more)
+                tc_fence_before();
+                mbar_arrive(smem_u32(&c.o_free[t]));
+                if (single) mbar_arrive(smem_u32(&c.o_free[1]));
             }
-            tc_fence_before();
-            mbar_arrive(smem_u32(&c.o_free[t]));
-            ++wt[t];
+        }
+        if (to_memory && own.count == 2) {
+            // Announce the part; the block that completes the count joins them all.
+            __threadfence();
+            epilogue_barrier();
+            if (lead) c.last = atomicAdd(p.arrived + own.c, 1) == 1;
+            epilogue_barrier();
+            if (c.last) {
+                __threadfence();
+                for (int t = 0; t < T.nt; t++) join_rows(t, 0u, 0.f, 0.f, -1, 0);
+            }
+            epilogue_barrier();
         }
         ++w;
     }
@@ -725,14 +1043,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sKV = sbase + 2 * C::TILE_BYTES;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int W = __ldg(p.count);
-
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; t++) {
             mbar_init(smem_u32(&ctl.q_full[t]), 1);
             mbar_init(smem_u32(&ctl.q_empty[t]), 1);
             mbar_init(smem_u32(&ctl.s_full[t]), 1);
-            mbar_init(smem_u32(&ctl.p_full[t]), BM);
+            mbar_init(smem_u32(&ctl.p_full[t]), BM / 32);
             mbar_init(smem_u32(&ctl.pv_done[t]), 1);
             mbar_init(smem_u32(&ctl.o_free[t]), BM);
             mbar_init(smem_u32(&ctl.epi_full[t]), BM);
@@ -761,20 +1077,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
 
+    pdl_wait();
+    pdl_launch();
+    Run R;
+    {
+        const int nb = static_cast<int>(p.head[2]);
+        const unsigned long long U = p.head[1];
+        const int c = blockIdx.x;
+        R.items = c < nb ? static_cast<int>(p.head[0]) : 0;  // no items: nothing to do
+        R.first = c < nb ? p.run_first[c] : 0;
+        R.cuts = chunk_cuts(U, nb);
+        R.lo = R.cuts.cut(c);
+        R.hi = R.cuts.cut(c + 1);
+    }
+
     // Register split (launch: 512 threads x 128 = 65536): softmax 2 x 128 x 176,
     // epilogue 128 x 80, the other four warps 128 x 80.
     if (warp < 8) {
         setmaxnreg_inc<176>();
-        softmax_role<D, DT>(p, ctl, tmem, warp, lane, W);
+        softmax_role<D, DT>(p, ctl, tmem, warp, lane, R);
     } else if (warp < 12) {
         setmaxnreg_dec<80>();
-        epilogue_role<D, DT>(p, ctl, tmem, warp, lane, W);
+        epilogue_role<D, DT>(p, ctl, tmem, sKV, warp, lane, R);
     } else {
         setmaxnreg_dec<80>();
-        if (warp == 12) producer_role<D>(p, ctl, &tm_k, &tm_v, sKV, W);
-        if (warp == 13) mma_role<D, DT>(p, ctl, tmem, sQ0, sKV, W);
-        if (warp == 14) q_producer_role<D>(p, ctl, &tm_q, sQ0, W);
-        if (warp == 15) edge_role<D, DT>(p, ctl, sKV, W);
+        if (warp == 12) producer_role<D>(p, ctl, &tm_k, &tm_v, sKV, R);
+        if (warp == 13) mma_role<D, DT>(p, ctl, tmem, sQ0, sKV, R);
+        if (warp == 14) q_producer_role<D>(p, ctl, &tm_q, sQ0, R);
+        if (warp == 15) edge_role<D, DT>(p, ctl, sKV, R);
     }
 
     tc_fence_before();
@@ -785,62 +1115,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the parts of work tiles whose keys were shared out: a warp per row, the
-// parts in order (fixed, so reruns agree bit for bit).
+// Adds the partial results of items of three parts or more: part 0 in place
+// 2 c + 1, part k in place 2 (c + k), c the block that started the item.  A block
+// takes 32 rows (lane = row) and 16 columns, its warps every eighth part; sums
+// over parts run in a fixed order.
+constexpr int kJoinWarps = 8;
+
 template <int D, int DT>
-__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const ChunkParams p)
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_chunk_join_kernel(const ChunkParams p)
 {
-    constexpr int V = D / 32;
     const PagedArgs &a = p.a;
-    const int t = blockIdx.x;
-    if (t >= __ldg(p.count)) return;
-    const ChunkTile T = load_tile(p, t);
-    if (T.parts == 1 || T.part != 0) return;
+    __shared__ float s_o[kJoinWarps][16][33], s_m[kJoinWarps][32], s_l[kJoinWarps][32];
+    pdl_wait();
+    if (static_cast<int>(blockIdx.x) >= *p.joins) return;
+    const int2 jn = p.join[blockIdx.x];
+    const int parts = jn.x;
+    const ChunkItem T = load_item(p, jn.y);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nqt = chunk_q_tiles(T.n, p.g);
-    const int rows = p.tpt * p.g;
-    for (int r = blockIdx.y * 8 + warp; r < 2 * BM; r += gridDim.y * 8) {
-        const int tile = r / BM, rl = r % BM;
-        const int rt = rl / p.g, tok = T.tok0 + tile * p.tpt + rt;
-        if (tile >= T.nt || rl >= rows || tok >= T.n) continue;
-        float M = -INFINITY;
-        for (int k = lane; k < T.parts; k += 32) {
-            const float2 ml = p.part_ml[(static_cast<int64_t>(t) + static_cast<int64_t>(k) * nqt) * (2 * BM) + r];
-            if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    const int r = blockIdx.y * 32 + lane, tile = r / BM, rl = r % BM, c16 = blockIdx.z;
+    if (blockIdx.y * 32 / BM >= T.nt) return;
+    const int rt = rl / p.g, tok = T.tok0 + tile * p.tpt + rt;
+    const bool row_ok = rt < p.tpt && tok < T.n;  // (other rows' partial results were never written)
+    const int nb = static_cast<int>(p.head[2]);
+    const int c = chunk_owners(T, chunk_cuts(p.head[1], nb)).c;
+    float M = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+    for (int e = 0; e < 16; e++) o[e] = 0.f;
+    if (row_ok) {
+#pragma unroll 2
+        for (int k = warp; k < parts; k += kJoinWarps) {
+            const int64_t s = k == 0 ? 2 * c + 1 : 2 * (c + k);
+            const float2 ml = p.part_ml[s * (2 * BM) + r];
+            float4 u[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) u[e] = *part_at<D>(p, s, c16 * 4 + e, r);
+            if (ml.y == 0.f) continue;  // a part none of whose keys the row sees adds nothing
+            const float m = fmaxf(M, ml.x);
+            const bool none = l == 0.f;
+            const float w0 = none ? 0.f : ex2_approx(M - m), w = ex2_approx(ml.x - m);
+            M = m;
+            l = none ? w * ml.y : fmaf(l, w0, w * ml.y);
+            const float x[16] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w,
+                                 u[2].x, u[2].y, u[2].z, u[2].w, u[3].x, u[3].y, u[3].z, u[3].w};
+#pragma unroll
+            for (int e = 0; e < 16; e++) o[e] = none ? w * x[e] : fmaf(o[e], w0, w * x[e]);
         }
-#pragma unroll
-        for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
-        float l = 0.f, o[V];
-#pragma unroll
-        for (int e = 0; e < V; e++) o[e] = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < T.parts; k++) {
-            const int64_t at = (static_cast<int64_t>(t) + static_cast<int64_t>(k) * nqt) * (2 * BM) + r;
-            const float2 ml = p.part_ml[at];
-            if (ml.y == 0.f) continue;
-            const float w = ex2_approx(ml.x - M);
-            l = fmaf(w, ml.y, l);
-            if (V == 4) {
-                const float4 u = *reinterpret_cast<const float4 *>(p.part_o + at * D + lane * 4);
-                o[0] = fmaf(w, u.x, o[0]);
-                o[1] = fmaf(w, u.y, o[1]);
-                o[2 % V] = fmaf(w, u.z, o[2 % V]);
-                o[3 % V] = fmaf(w, u.w, o[3 % V]);
-            } else {
-                const float2 u = *reinterpret_cast<const float2 *>(p.part_o + at * D + lane * 2);
-                o[0] = fmaf(w, u.x, o[0]);
-                o[1] = fmaf(w, u.y, o[1]);
-            }
-        }
-        const float inv = 1.f / l;
-        const int hd = T.h * p.g + (rl - rt * p.g);
-        uint16_t *dst = a.o + static_cast<int64_t>(T.q0 + tok) * a.o_st + hd * a.o_sh + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; e += 2)
-            *reinterpret_cast<uint32_t *>(dst + e) = l == 0.f ? 0u : pack2<DT>(o[e] * inv, o[e + 1] * inv);
-        if (lane == 0 && a.lse2)
-            a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
     }
+#pragma unroll
+    for (int e = 0; e < 16; e++) s_o[warp][e][lane] = o[e];
+    s_m[warp][lane] = M;
+    s_l[warp][lane] = l;
+    __syncthreads();
+    if (warp >= 2 || !row_ok) return;
+    // Warps 0 and 1: eight columns each, over the warps' sums in order.
+    M = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; w++)
+        if (s_l[w][lane] != 0.f) M = fmaxf(M, s_m[w][lane]);
+#pragma unroll
+    for (int e = 0; e < 8; e++) o[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; w++) {
+        const float lw = s_l[w][lane];
+        if (lw == 0.f) continue;
+        const float g = ex2_approx(s_m[w][lane] - M);
+        l = fmaf(g, lw, l);
+#pragma unroll
+        for (int e = 0; e < 8; e++) o[e] = fmaf(g, s_o[w][warp * 8 + e][lane], o[e]);
+    }
+    const float inv = 1.f / l;
+    const int hd = T.h * p.g + (rl - rt * p.g);
+    uint32_t pk[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) pk[e] = l == 0.f ? 0u : pack2<DT>(o[2 * e] * inv, o[2 * e + 1] * inv);
+    *reinterpret_cast<uint4 *>(a.o + static_cast<int64_t>(T.q0 + tok) * a.o_st + hd * a.o_sh + c16 * 16 + warp * 8) =
+        make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    if (c16 == 0 && warp == 0 && a.lse2)
+        a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
 }
 
 // ------------------------------------------------------------------ host side
@@ -879,36 +1231,20 @@ bool encode(CUtensorMap *map, const void *base, int dtype, int rank, const cuuin
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// Work tiles if no keys are shared out, at most.
+// Items, at most (each sequence rounds its query tiles up).
 int64_t max_items(const PagedArgs &a)
 {
     const int g = a.H / a.Hkv;
     return static_cast<int64_t>(a.Hkv) * (a.T / chunk_tokens(g) + static_cast<int64_t>(a.S) + 1);
 }
 
-// Places for tiles when keys are shared out (a few rounds of the grid).
-int part_places(int nsm) { return 2 * nsm; }
-
-// Tiles whose keys are shared out, at most: chunk_part_len cuts the work into
-// `places` pieces, and each of fewer than `places` work tiles adds at most one.
-int64_t max_parts(const PagedArgs &a, int nsm)
-{
-    const int64_t places = part_places(nsm), items = max_items(a);
-    return places + (items < places ? items : places);
-}
-
 template <int D, int DT>
-clis_status_t launch_impl(const ChunkParams &p, int nsm, cudaStream_t stream)
+clis_status_t launch_impl(const ChunkParams &p, cudaStream_t stream)
 {
     using C = Cfg<D>;
     const PagedArgs &a = p.a;
     if (cudaFuncSetAttribute(paged_chunk_kernel<D, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
         cudaSuccess)
-        return CLIS_ERR_CUDA;
-    const size_t sched_smem = sizeof(int) * (static_cast<size_t>(a.S) + 1);
-    if (sched_smem > 48 * 1024 &&
-        cudaFuncSetAttribute(paged_chunk_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(sched_smem)) != cudaSuccess)
         return CLIS_ERR_CUDA;
     CUtensorMap mq, mk, mv;
     {
@@ -924,47 +1260,77 @@ clis_status_t launch_impl(const ChunkParams &p, int nsm, cudaStream_t stream)
         const int64_t ks[3] = {a.kc_sn, a.kc_sh, a.kc_sp}, vs[3] = {a.vc_sn, a.vc_sh, a.vc_sp};
         if (!encode(&mk, a.kc, DT, 4, dims, ks, box) || !encode(&mv, a.vc, DT, 4, dims, vs, box)) return CLIS_ERR_CUDA;
     }
-    paged_chunk_schedule_kernel<<<1, kSchedThreads, sched_smem, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
-    const int64_t tiles = max_items(a) + max_parts(a, nsm);
-    const int grid = static_cast<int>(tiles < nsm ? tiles : nsm);
-    paged_chunk_kernel<D, DT><<<grid, kThreads, C::SMEM_BYTES, stream>>>(mq, mk, mv, p);
-    if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
-    paged_chunk_join_kernel<D, DT><<<dim3(static_cast<unsigned>(max_parts(a, nsm)), 8), 256, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
+    if (launch_pdl(paged_chunk_kernel<D, DT>, dim3(p.grid), kThreads, C::SMEM_BYTES, stream, mq, mk, mv, p) != cudaSuccess)
+        return CLIS_ERR_CUDA;
+    const int64_t items = max_items(a);
+    const int joins = static_cast<int>(items < max_joins(p.grid) ? items : max_joins(p.grid));
+    if (launch_pdl(paged_chunk_join_kernel<D, DT>, dim3(joins, 2 * BM / 32, D / 16), 32 * kJoinWarps, 0, stream, p) !=
+        cudaSuccess)
+        return CLIS_ERR_CUDA;
+    return CLIS_OK;
 }
 
 }  // namespace
 
 size_t paged_chunk_workspace(const PagedArgs &a, int nsm)
 {
-    const size_t parts = static_cast<size_t>(max_parts(a, nsm));
-    return 256 + up256(static_cast<size_t>(max_items(a) + max_parts(a, nsm)) * sizeof(ChunkTile)) +
-           up256(parts * 2 * BM * sizeof(float2)) + up256(parts * 2 * BM * a.d * sizeof(float));
+    const size_t grid = static_cast<size_t>(nsm);
+    return 256 + 2 * up256(grid * sizeof(int)) + up256(max_joins(nsm) * sizeof(int2)) +
+           up256(static_cast<size_t>(max_items(a)) * sizeof(ChunkItem)) + up256(2 * grid * 2 * BM * sizeof(float2)) +
+           up256(2 * grid * 2 * BM * a.d * sizeof(float));
 }
 
-clis_status_t launch_paged_chunk(const PagedArgs &a, int rows_small, void *workspace, int nsm, cudaStream_t stream)
+namespace {
+
+ChunkParams chunk_params(const PagedArgs &a, int rows_small, void *workspace, int nsm)
 {
     ChunkParams p;
     p.a = a;
     p.g = a.H / a.Hkv;
     p.tpt = BM / p.g;
     p.rows_small = rows_small;
-    p.slots = part_places(nsm);
-    p.least = 4;
+    p.grid = nsm;
+    p.least = 2 * kChunkOverhead;
     p.box_rows = imin(1 << a.page_shift, BN);
+    const size_t grid = static_cast<size_t>(nsm);
     char *w = static_cast<char *>(workspace);
-    p.count = reinterpret_cast<int *>(w);
+    p.head = reinterpret_cast<unsigned long long *>(w);
+    p.joins = reinterpret_cast<int *>(w + 128);
     w += 256;
-    p.tiles = reinterpret_cast<ChunkTile *>(w);
-    const size_t parts = static_cast<size_t>(max_parts(a, nsm));
-    w += up256(static_cast<size_t>(max_items(a) + max_parts(a, nsm)) * sizeof(ChunkTile));
+    p.run_first = reinterpret_cast<int *>(w);
+    w += up256(grid * sizeof(int));
+    p.arrived = reinterpret_cast<int *>(w);
+    w += up256(grid * sizeof(int));
+    p.join = reinterpret_cast<int2 *>(w);
+    w += up256(max_joins(nsm) * sizeof(int2));
+    p.items = reinterpret_cast<ChunkItem *>(w);
+    w += up256(static_cast<size_t>(max_items(a)) * sizeof(ChunkItem));
     p.part_ml = reinterpret_cast<float2 *>(w);
-    w += up256(parts * 2 * BM * sizeof(float2));
+    w += up256(2 * grid * 2 * BM * sizeof(float2));
     p.part_o = reinterpret_cast<float *>(w);
+    return p;
+}
+
+}  // namespace
+
+clis_status_t launch_paged_chunk_schedule(const PagedArgs &a, int rows_small, void *workspace, int nsm,
+                                          cudaStream_t stream)
+{
+    const ChunkParams p = chunk_params(a, rows_small, workspace, nsm);
+    const size_t smem = sizeof(int) * (static_cast<size_t>(a.S) + 1);
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(paged_chunk_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(smem)) != cudaSuccess)
+        return CLIS_ERR_CUDA;
+    paged_chunk_schedule_kernel<<<1, kSchedThreads, smem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
+}
+
+clis_status_t launch_paged_chunk(const PagedArgs &a, int rows_small, void *workspace, int nsm, cudaStream_t stream)
+{
+    const ChunkParams p = chunk_params(a, rows_small, workspace, nsm);
     const bool f16 = a.dtype == CLIS_DT_FP16;
-    if (a.d == 128) return f16 ? launch_impl<128, 1>(p, nsm, stream) : launch_impl<128, 0>(p, nsm, stream);
-    return f16 ? launch_impl<64, 1>(p, nsm, stream) : launch_impl<64, 0>(p, nsm, stream);
+    if (a.d == 128) return f16 ? launch_impl<128, 1>(p, stream) : launch_impl<128, 0>(p, stream);
+    return f16 ? launch_impl<64, 1>(p, stream) : launch_impl<64, 0>(p, stream);
 }
 
 clis_status_t read_chunk_error(uint32_t *code)

@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c = blockIdx.x;
     unsigned int bad = 0;
+    pdl_launch();
 
     // ---- this block's run of units
     const int per = (a.S + kThreads - 1) / kThreads;
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     if (c >= nb) {  // nothing for this block (U = 0 included)
         if (tid == 0) p.meta[c] = make_int4(0, 0, 0, 0);
         if (bad && c == 0) atomicOr(&g_decode_error_word, bad);
+        pdl_wait();
         return;
     }
     const uint32_t u0 = decode_cut(U, nb, c), u1 = decode_cut(U, nb, c + 1);
@@ -545,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     }
     cp_async_wait<0>();
     if (bad) atomicOr(&g_decode_error_word, bad);
+    pdl_wait();  // (the schedule kernel, whose results only later kernels read)
 }
 
 // Adds the partial results of the item that block c of the decode kernel
@@ -558,6 +561,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
     __shared__ float s_l[kJoinThreads / 32];
     const PagedArgs &a = p.a;
     const int c = blockIdx.x;
+    pdl_wait();
+    pdl_launch();
     const int4 mt = p.meta[c];
     const int K = mt.x;
     if (K == 0) return;
@@ -628,15 +633,20 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
 }
 
 template <int D, int DT, int MT>
-clis_status_t launch_impl(const DecodeParams &p, int grid, cudaStream_t stream)
+clis_status_t launch_impl(const DecodeParams &p, int grid, bool after_schedule, cudaStream_t stream)
 {
     if (cudaFuncSetAttribute(paged_decode_kernel<D, DT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              DCfg<D>::SMEM) != cudaSuccess)
         return CLIS_ERR_CUDA;
-    paged_decode_kernel<D, DT, MT><<<grid, kThreads, DCfg<D>::SMEM, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
-    paged_decode_join_kernel<D, DT><<<grid, kJoinThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
+    if (after_schedule) {
+        if (launch_pdl(paged_decode_kernel<D, DT, MT>, dim3(grid), kThreads, DCfg<D>::SMEM, stream, p) != cudaSuccess)
+            return CLIS_ERR_CUDA;
+    } else {
+        paged_decode_kernel<D, DT, MT><<<grid, kThreads, DCfg<D>::SMEM, stream>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
+    }
+    return launch_pdl(paged_decode_join_kernel<D, DT>, dim3(grid), kJoinThreads, 0, stream, p) == cudaSuccess ? CLIS_OK
+                                                                                                     : CLIS_ERR_CUDA;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -658,8 +668,8 @@ size_t paged_decode_workspace(int d, int row_tiles, int nsm)
            up256(slots * rows * d * sizeof(float));
 }
 
-clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, void *workspace, int nsm,
-                                  cudaStream_t stream)
+clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, bool after_schedule, void *workspace,
+                                  int nsm, cudaStream_t stream)
 {
     const int grid = 2 * nsm;  // two blocks fit an SM
     const size_t slots = 2 * static_cast<size_t>(grid), rows = 16 * static_cast<size_t>(row_tiles);
@@ -675,13 +685,16 @@ clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict
     p.part_ml = reinterpret_cast<float2 *>(w);
     w += up256(slots * rows * sizeof(float2));
     p.part_o = reinterpret_cast<float *>(w);
-    const bool f16 = a.dtype == CLIS_DT_FP16;
+#define CLIS_DECODE(D, MT)                                                  \
+    return a.dtype == CLIS_DT_FP16 ? launch_impl<D, 1, MT>(p, grid, after_schedule, stream) \
+                                   : launch_impl<D, 0, MT>(p, grid, after_schedule, stream)
     if (a.d == 128) {
-        if (row_tiles == 1) return f16 ? launch_impl<128, 1, 1>(p, grid, stream) : launch_impl<128, 0, 1>(p, grid, stream);
-        return f16 ? launch_impl<128, 1, 2>(p, grid, stream) : launch_impl<128, 0, 2>(p, grid, stream);
+        if (row_tiles == 1) CLIS_DECODE(128, 1);
+        CLIS_DECODE(128, 2);
     }
-    if (row_tiles == 1) return f16 ? launch_impl<64, 1, 1>(p, grid, stream) : launch_impl<64, 0, 1>(p, grid, stream);
-    return f16 ? launch_impl<64, 1, 2>(p, grid, stream) : launch_impl<64, 0, 2>(p, grid, stream);
+    if (row_tiles == 1) CLIS_DECODE(64, 1);
+    CLIS_DECODE(64, 2);
+#undef CLIS_DECODE
 }
 
 clis_status_t read_decode_error(uint32_t *code)

@@ -70,15 +70,48 @@ struct PagedArgs {
     int causal;
 };
 
+#ifdef __CUDACC__
+// Programmatic dependent launch.  A kernel launched by launch_pdl may start while
+// the kernel before it in the stream still runs; pdl_wait returns once that
+// kernel has ended and its writes are visible.  Every kernel of a chain calls it,
+// so the end of one implies the end of all before it.  pdl_launch lets the next
+// kernel be set up (it changes nothing for correctness).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 // Row tiles (of 16 rows) per sequence that the decode kernel is built for, when
 // no sequence has more than max_q new tokens: 1, 2, or 0 (not used).
 int paged_decode_row_tiles(int64_t max_q, int g);
 size_t paged_decode_workspace(int d, int row_tiles, int nsm);
 // strict: no chunk kernel follows, a sequence of more rows is an error.
-clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, void *workspace, int nsm,
-                                  cudaStream_t stream);
+// after_schedule: launched behind launch_paged_chunk_schedule, whose results it
+// does not read.
+clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, bool after_schedule, void *workspace,
+                                  int nsm, cudaStream_t stream);
 size_t paged_chunk_workspace(const PagedArgs &a, int nsm);
 // Sequences of at most rows_small query rows are left to the decode kernel.
+// Schedule first, then (with rows_small > 0) the decode kernel, then the chunk kernel:
+// each of these kernels but the first may be set up while the one before it
+// still runs, and waits for it before it reads its results.
+clis_status_t launch_paged_chunk_schedule(const PagedArgs &a, int rows_small, void *workspace, int nsm,
+                                          cudaStream_t stream);
 clis_status_t launch_paged_chunk(const PagedArgs &a, int rows_small, void *workspace, int nsm, cudaStream_t stream);
 
 // Device error words of these kernels (CLIS_PAGED_* bits and wait bits), one

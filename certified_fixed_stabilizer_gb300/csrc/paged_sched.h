@@ -77,78 +77,127 @@ CLIS_HD uint32_t decode_cut(uint32_t U, int blocks, int c)
 
 // ------------------------------------------------------------- chunk kernel
 //
-// A row tile is up to 128 query rows: tpt = 128 / g tokens of all g heads.  A
-// work tile is two row tiles of one (sequence, key/value head) against a range
-// of 128-key tiles.  When there are too few work tiles to fill the GPU the
-// keys of each are split into `parts` ranges, joined afterwards.
+// A row tile is up to 128 query rows: 128 / g tokens of all g heads.  An item is
+// two row tiles of one (sequence, key/value head) against the keys they see, in
+// tiles of 128.  Items in order (sequence, head, query tile) are laid end to end,
+// each as long as its cost, and cut into equal runs, one per block; an item that
+// crosses a cut is joined from the blocks' partial results.
+//
+// Cost of a key tile: 3 with two row tiles (1.45 us), 2 with one (two key tiles are
+// worked on at a time, but their bytes come no faster), and per item what loading
+// Q, filling the pipeline and writing the output take (about 4.5 us).
 constexpr int kChunkRows = 128;
 constexpr int kChunkKeys = 128;
+constexpr int kChunkOverhead = 9;
 
-struct __attribute__((aligned(16))) ChunkTile {
+struct __attribute__((aligned(16))) ChunkItem {
     int q0, n, kv, s;        // the sequence
-    int h, tok0, start, n_kv;  // head, first token, first key tile, key tiles
-    int parts, part, nt, masked;  // row tiles in use; masked: an empty range (no key of it counts)
+    int h, tok0, n_kv, nt;   // head, first token, key tiles, row tiles in use
+    uint64_t first;          // cost of the items before it
+    uint64_t pad;
 };
 
-CLIS_HD int chunk_tokens(int g) { return 2 * (kChunkRows / g); }  // tokens per work tile
+CLIS_HD int chunk_tokens(int g) { return 2 * (kChunkRows / g); }  // tokens per item
 CLIS_HD int chunk_q_tiles(int n, int g) { return ceil_div(n, chunk_tokens(g)); }
 
-// Key tiles of work tile qt, at least one (its output must be written).
-CLIS_HD int chunk_cost(const SeqLen &s, int g, int qt, bool causal)
+// Item r (0-based) of sequence seq; at least one key tile (its output must be written).
+CLIS_HD ChunkItem chunk_item(const SeqLen &s, int seq, int g, int r, bool causal)
 {
-    const int last = imin(s.n, (qt + 1) * chunk_tokens(g)) - 1;
-    return imax(1, ceil_div(visible_keys(s.n, s.kv, last, causal), kChunkKeys));
-}
-
-CLIS_HD int chunk_max_cost(const SeqLen &s) { return imax(1, ceil_div(s.kv, kChunkKeys)); }
-
-// Key tiles a part should have: `total` tiles of work in `items` work tiles, for
-// `slots` places; with enough work tiles nothing is split.
-CLIS_HD int chunk_part_len(uint64_t total, uint64_t items, int slots, int least)
-{
-    if (items >= static_cast<uint64_t>(slots)) return 1 << 30;
-    const uint64_t len = (total + slots - 1) / slots;
-    return len < static_cast<uint64_t>(least) ? least : static_cast<int>(len > (1u << 30) ? (1u << 30) : len);
-}
-
-CLIS_HD int chunk_parts(const SeqLen &s, int part_len) { return ceil_div(chunk_max_cost(s), part_len); }
-
-// Tile r (0-based) of sequence s: head-major, then part, then query tile, so that
-// tiles that read the same keys run side by side.
-CLIS_HD ChunkTile chunk_tile(const SeqLen &s, int seq, int g, int parts, int r, bool causal)
-{
-    ChunkTile t;
+    ChunkItem t;
     const int nqt = chunk_q_tiles(s.n, g);
     t.q0 = s.q0;
     t.n = s.n;
     t.kv = s.kv;
     t.s = seq;
-    t.h = r / (nqt * parts);
-    const int rem = r - t.h * nqt * parts;
-    t.part = rem / nqt;
-    const int qt = rem - t.part * nqt;
-    t.parts = parts;
-    t.tok0 = qt * chunk_tokens(g);
+    t.h = r / nqt;
+    t.tok0 = (r - t.h * nqt) * chunk_tokens(g);
+    const int last = imin(s.n, t.tok0 + chunk_tokens(g)) - 1;
+    t.n_kv = imax(1, ceil_div(visible_keys(s.n, s.kv, last, causal), kChunkKeys));
     t.nt = s.n - t.tok0 > kChunkRows / g ? 2 : 1;
-    const int cost = chunk_cost(s, g, qt, causal);
-    t.start = static_cast<int>(static_cast<int64_t>(cost) * t.part / parts);
-    const int end = static_cast<int>(static_cast<int64_t>(cost) * (t.part + 1) / parts);
-    t.n_kv = end - t.start;
-    t.masked = 0;
-    if (t.n_kv == 0) {  // an empty part still takes its place: one tile, none of whose keys counts
-        t.n_kv = 1;
-        t.masked = 1;
-        if (t.start >= cost) t.start = cost - 1;
-    }
+    t.first = 0;
+    t.pad = 0;
     return t;
 }
 
-// First key tile of the work tile that some of its rows see only in part: from
-// there on masked places lie among the keys.
-CLIS_HD int chunk_first_masked(const ChunkTile &t, bool causal)
+CLIS_HD uint64_t chunk_cost(int n_kv, int nt) { return kChunkOverhead + static_cast<uint64_t>(n_kv) * (nt + 1); }
+
+// Blocks that take part, for a total cost of U: every run is `least` or longer (if
+// U is), which must be at least a key tile's cost, so that no run within an item
+// is without a key tile of it.
+CLIS_HD int chunk_blocks(uint64_t U, int grid, int least)
 {
-    const int full = t.masked ? 0 : visible_keys(t.n, t.kv, t.tok0, causal);
-    return full / kChunkKeys;
+    const uint64_t want = U / least;
+    return want >= static_cast<uint64_t>(grid) ? grid : want > 0 ? static_cast<int>(want) : U > 0 ? 1 : 0;
+}
+
+// The cuts: run c is [cut(c), cut(c + 1)), cut(c) = floor(U c / blocks).
+struct ChunkCuts {
+    uint64_t run;  // U / blocks
+    uint32_t rem, blocks;
+    CLIS_HD uint64_t cut(int c) const { return run * c + rem * static_cast<uint32_t>(c) / blocks; }  // rem c < blocks^2
+};
+
+CLIS_HD ChunkCuts chunk_cuts(uint64_t U, int blocks)
+{
+    ChunkCuts k;
+    k.blocks = blocks > 0 ? blocks : 1;
+    k.run = U / k.blocks;
+    k.rem = static_cast<uint32_t>(U % k.blocks);
+    return k;
+}
+
+// Block whose run holds place x < U.
+CLIS_HD int chunk_block_of(const ChunkCuts &k, uint64_t x)
+{
+    const uint64_t g = k.run > 0 ? x / k.run : x;
+    int c = static_cast<int>(g < k.blocks ? g : k.blocks - 1);
+    while (c > 0 && k.cut(c) > x) c--;
+    while (c + 1 < static_cast<int>(k.blocks) && k.cut(c + 1) <= x) c++;
+    return c;
+}
+
+// Key tile that place x (0 .. cost) of an item falls on.
+CLIS_HD int chunk_tile_of(uint64_t x, int n_kv, int nt)
+{
+    if (x <= kChunkOverhead) return 0;
+    const uint64_t t = static_cast<uint32_t>(x - kChunkOverhead) / static_cast<uint32_t>(nt + 1);  // (a cost is below 2^32)
+    return t < static_cast<uint64_t>(n_kv) ? static_cast<int>(t) : n_kv;
+}
+
+// Key tiles [t0, t1) of an item that the run [lo, hi) takes.
+struct ChunkRange {
+    int t0, t1;
+};
+
+CLIS_HD ChunkRange chunk_range(const ChunkItem &t, uint64_t lo, uint64_t hi)
+{
+    ChunkRange r;
+    r.t0 = lo > t.first ? chunk_tile_of(lo - t.first, t.n_kv, t.nt) : 0;
+    r.t1 = hi > t.first ? chunk_tile_of(hi - t.first, t.n_kv, t.nt) : 0;
+    return r;
+}
+
+// Blocks among which the item is shared out: the first with a key tile of it, and
+// how many.
+struct ChunkOwners {
+    int c, count;
+};
+
+CLIS_HD ChunkOwners chunk_owners(const ChunkItem &t, const ChunkCuts &k)
+{
+    int c = chunk_block_of(k, t.first);
+    while (c + 1 < static_cast<int>(k.blocks) && chunk_range(t, k.cut(c), k.cut(c + 1)).t1 == 0) c++;
+    ChunkOwners o;
+    o.c = c;
+    o.count = chunk_block_of(k, t.first + chunk_cost(t.n_kv, t.nt) - 1) - c + 1;
+    return o;
+}
+
+// First key tile of the item that some of its rows see only in part: from there
+// on masked places lie among the keys.
+CLIS_HD int chunk_first_masked(const ChunkItem &t, bool causal)
+{
+    return visible_keys(t.n, t.kv, t.tok0, causal) / kChunkKeys;
 }
 
 }  // namespace clis

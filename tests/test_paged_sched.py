@@ -39,68 +39,91 @@ static int decode(int S, const int *cu, const int *kv, int T, int cap, int g, in
     }
     return at == U ? 0 : 6;
 }
-static int chunk(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_small, int Hkv, int places, int least,
-                 int causal, long long max_items, long long max_parts)
+static int chunk(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_small, int Hkv, int grid, int least,
+                 int causal, long long max_items)
 {
-    unsigned long long total = 0, items = 0;
+    std::vector<ChunkItem> items;
+    unsigned long long U = 0;
     for (int s = 0; s < S; s++) {
         SeqLen q = clip_seq(cu[s], cu[s + 1], kv[s], T, cap);
         if (q.n == 0 || is_decode(q, g, rows_small)) continue;
-        unsigned long long it = (unsigned long long)Hkv * chunk_q_tiles(q.n, g);
-        items += it;
-        total += it * chunk_max_cost(q);
-    }
-    if ((long long)items > max_items) return 11;
-    int len = chunk_part_len(total, items, places, least);
-    long long W = 0, shared = 0;
-    for (int s = 0; s < S; s++) {
-        SeqLen q = clip_seq(cu[s], cu[s + 1], kv[s], T, cap);
-        if (q.n == 0 || is_decode(q, g, rows_small)) continue;
-        int parts = chunk_parts(q, len), nqt = chunk_q_tiles(q.n, g), tpt = kChunkRows / g;
-        // key tiles seen: [head][query tile], counted
-        std::vector<int> next(Hkv * nqt, 0);
+        int nqt = chunk_q_tiles(q.n, g), tpt = kChunkRows / g;
         std::vector<char> row(q.n, 0);
-        for (int r = 0; r < Hkv * nqt * parts; r++, W++) {
-            ChunkTile t = chunk_tile(q, s, g, parts, r, causal);
-            if (parts > 1) { shared++; if (W >= max_parts) return 12; }
-            if (t.h < 0 || t.h >= Hkv || t.part < 0 || t.part >= parts || t.tok0 < 0 || t.tok0 >= q.n) return 13;
-            if (t.n_kv < 1 || t.start < 0) return 14;
-            int qt = t.tok0 / (2 * tpt);
+        for (int r = 0; r < Hkv * nqt; r++) {
+            ChunkItem t = chunk_item(q, s, g, r, causal);
+            if (t.h != r / nqt || t.tok0 != (r % nqt) * 2 * tpt || t.tok0 >= q.n || t.n_kv < 1) return 13;
             if (t.nt != (q.n - t.tok0 > tpt ? 2 : 1)) return 15;
-            int cost = chunk_cost(q, g, qt, causal);
-            if (t.start + t.n_kv > cost) return 16;
-            if ((long long)(cost - 1) * kChunkKeys >= (q.kv > 0 ? q.kv : 1)) return 17;
-            // r's place among the parts of its work tile: later parts lie nqt tiles apart
-            if (r != (t.h * parts + t.part) * nqt + qt) return 18;
-            if (!t.masked) {
-                if (next[t.h * nqt + qt] != t.start) return 19;
-                next[t.h * nqt + qt] += t.n_kv;
-            }
+            if ((long long)(t.n_kv - 1) * kChunkKeys >= (q.kv > 0 ? q.kv : 1)) return 17;  // a tile without keys
             int first = chunk_first_masked(t, causal);
-            for (int i = 0; i < 2 * tpt; i++) {
-                int tok = t.tok0 + i;
-                if (tok >= q.n) break;
-                if (t.h == 0 && t.part == 0) row[tok]++;
-                int lim = visible_keys(q.n, q.kv, tok, causal);
+            for (int i = 0; i < 2 * tpt && t.tok0 + i < q.n; i++) {
+                if (t.h == 0) row[t.tok0 + i]++;
+                int lim = visible_keys(q.n, q.kv, t.tok0 + i, causal);
                 if (lim < 0 || lim > q.kv) return 20;
-                if (lim > cost * kChunkKeys) return 21;          // a visible key beyond the work tile
-                if (!t.masked && first * kChunkKeys > lim) return 22;  // a tile before `first` is masked in part
+                if (lim > (long long)t.n_kv * kChunkKeys) return 21;  // a visible key beyond the item
+                if ((long long)first * kChunkKeys > lim) return 22;    // a tile before `first` is masked in part
             }
+            t.first = U;
+            U += chunk_cost(t.n_kv, t.nt);
+            items.push_back(t);
         }
-        for (int h = 0; h < Hkv; h++)
-            for (int qt = 0; qt < nqt; qt++)
-                if (next[h * nqt + qt] != chunk_cost(q, g, qt, causal)) return 23;
         for (int i = 0; i < q.n; i++)
             if (row[i] != 1) return 24;
     }
-    if (W > max_items + max_parts) return 25;
+    if ((long long)items.size() > max_items) return 11;
+    int nb = chunk_blocks(U, grid, least);
+    if (nb > grid || (U > 0) != (nb > 0)) return 12;
+    ChunkCuts cuts = chunk_cuts(U, nb);
+    std::vector<int> first(nb, -1), starts(nb, -1);
+    for (size_t i = 0; i < items.size(); i++) {   // as the schedule kernel finds them
+        const ChunkItem &t = items[i];
+        unsigned long long end = t.first + chunk_cost(t.n_kv, t.nt);
+        int c = chunk_block_of(cuts, t.first);
+        if (cuts.cut(c) < t.first) c++;
+        for (; c < nb && cuts.cut(c) < end; c++) {
+            if (first[c] != -1) return 26;
+            first[c] = i;
+        }
+        ChunkOwners o = chunk_owners(t, cuts);
+        if (o.c < 0 || o.count < 1 || o.c + o.count > nb) return 27;
+        if (o.count > 1) {
+            if (starts[o.c] != -1) return 28;     // two unfinished items started by one block
+            starts[o.c] = i;
+        }
+    }
+    std::vector<int> next(items.size(), 0), parts(items.size(), 0), begun(items.size(), -1), last(items.size(), -1);
+    for (int c = 0; c < nb; c++) {
+        unsigned long long lo = cuts.cut(c), hi = cuts.cut(c + 1);
+        if (hi <= lo || (c == 0 && lo) || (c == nb - 1 && hi != U) || first[c] < 0) return 29;
+        int go = 0, start = 0;
+        for (size_t i = first[c]; i < items.size() && items[i].first < hi; i++) {
+            ChunkRange r = chunk_range(items[i], lo, hi);
+            if (r.t1 <= r.t0) continue;
+            if (r.t0 != next[i] || r.t1 > items[i].n_kv) return 19;
+            next[i] = r.t1;
+            parts[i]++;
+            if (begun[i] < 0) begun[i] = c;
+            else if (last[i] != c - 1) return 30;  // parts lie in consecutive blocks
+            last[i] = c;
+            if (r.t0 > 0) go++;                                   // place 2 c
+            else if (r.t1 < items[i].n_kv) start++;                // place 2 c + 1
+        }
+        if (go > 1 || start > 1) return 31;        // one place of each kind per block
+    }
+    for (size_t i = 0; i < items.size(); i++) {
+        if (next[i] != items[i].n_kv) return 23;
+        ChunkOwners o = chunk_owners(items[i], cuts);
+        if (o.c != begun[i] || o.count != parts[i]) return 32;
+    }
+    int many = 0;
+    for (int n : parts) many += n > 2;
+    if (many > (grid - 1) / 2 + 1) return 33;      // items joined by the join kernel: its list and its grid
     return 0;
 }
 extern "C" int check_decode(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_max, int Hkv, int grid, int least)
 { return decode(S, cu, kv, T, cap, g, rows_max, Hkv, grid, least); }
-extern "C" int check_chunk(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_small, int Hkv, int places, int least,
-                           int causal, long long max_items, long long max_parts)
-{ return chunk(S, cu, kv, T, cap, g, rows_small, Hkv, places, least, causal, max_items, max_parts); }
+extern "C" int check_chunk(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_small, int Hkv, int grid, int least,
+                           int causal, long long max_items)
+{ return chunk(S, cu, kv, T, cap, g, rows_small, Hkv, grid, least, causal, max_items); }
 """
 
 
@@ -111,11 +134,11 @@ def lib(tmp_path_factory):
         pytest.skip("no g++")
     d = tmp_path_factory.mktemp("sched")
     src = d / "h.cpp"
-    src.write_text(HARNESS % HEADER)
+    src.write_text(HARNESS.replace("%s", HEADER, 1))
     so = d / "h.so"
     subprocess.run([gxx, "-std=c++17", "-O1", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
     L = ctypes.CDLL(str(so))
-    L.check_chunk.argtypes = [ctypes.c_int] + [ctypes.POINTER(ctypes.c_int)] * 2 + [ctypes.c_int] * 8 + [ctypes.c_longlong] * 2
+    L.check_chunk.argtypes = [ctypes.c_int] + [ctypes.POINTER(ctypes.c_int)] * 2 + [ctypes.c_int] * 8 + [ctypes.c_longlong]
     return L
 
 
@@ -134,9 +157,8 @@ def check(lib, ctx, new, g, Hkv, causal=1, sms=152, cap=None, cu=None, kv=None):
                 assert lib.check_decode(S, ints(cu), ints(kv), T, cap, g, rows, Hkv, 2 * sms, least) == 0
         tokens = 2 * (128 // g)
         items = Hkv * (T // tokens + S + 1)
-        places = 2 * sms
-        parts = places + min(items, places)
-        assert lib.check_chunk(S, ints(cu), ints(kv), T, cap, g, rows, Hkv, places, 4, causal, items, parts) == 0
+        for least in (4, 16):
+            assert lib.check_chunk(S, ints(cu), ints(kv), T, cap, g, rows, Hkv, sms, least, causal, items) == 0
 
 
 def test_random_batches(lib):
