@@ -21,7 +21,7 @@ _BINDING_NAMES = {
     "clis_attn_chunk_finalize", "clis_v_e4m3_size", "clis_v_to_e4m3", "clis_attn_fwd_fp8pv", "clis_attn_fwd_chunk_fp8pv",
     "clis_attn_bwd", "clis_attn_bwd_workspace_size", "attention_bwd", "attention_fwd_lse", "attention_autograd",
     "AttentionFunction", "host_done_event", "grouped_query_views", "clis_attention_host",
-    "HostPlan", "Rope", "RopeDesc", "PagedDesc", "clis_rope", "rope", "rope_qk", "rope_autograd", "RopeFunction",
+    "HostPlan", "Rope", "RopeDesc", "PagedDesc", "clis_rope", "rope", "rope_qk", "rope_autograd",
     "PagedPlan", "clis_paged_plan", "paged_plan", "clis_paged_append", "paged_append", "clis_attn_fwd_paged",
     "attention_paged", "PagedCache", "PAGED_INDEX_BIT", "PAGED_POOL_BIT", "PAGED_LENGTH_BIT",
 }

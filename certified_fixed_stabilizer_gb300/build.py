@@ -1,4 +1,5 @@
-"""Builds libclis.so (CUDA for sm_103a) in-tree with nvcc.
+"""Builds libclis.so (CUDA for sm_103a) in-tree with nvcc, and _clis_torch.so, the
+torch binding of the calls around a paged cache, with the C++ compiler.
 
 Each translation unit is compiled in parallel to an object file, then linked
 into ``certified_fixed_stabilizer_gb300/_lib/libclis.so``.  The CUDA runtime is
@@ -17,6 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libclis.so")
+TORCH_EXT = os.path.join(OUT_DIR, "_clis_torch.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["clis_api.cu", "certify.cu", "attn_fwd.cu", "attn_bwd.cu", "host_attention.cu", "rope.cu",
@@ -45,10 +47,41 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    """csrc/binding.cpp against the installed torch's headers."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    obj = os.path.join(OBJ_DIR, "binding.o")
+    cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-w",
+           *[f"-I{d}" for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+                                sysconfig.get_paths()["include"])],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling binding.cpp failed:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_EXT + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, f"-L{OUT_DIR}", "-lclis", f"-L{lib}", "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking the torch binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_EXT)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(TORCH_EXT)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_EXT))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(HERE, "..", "include", "clis.h"))
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
@@ -59,14 +92,17 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(OBJ_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
+        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

@@ -8,6 +8,7 @@ importing this module raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 from typing import NamedTuple
@@ -63,6 +64,7 @@ class PagedDesc(ctypes.Structure):
 
 
 _lib = None
+_native = None  # the torch binding of the calls around a paged cache (csrc/binding.cpp)
 
 
 def library_path() -> str:
@@ -70,8 +72,9 @@ def library_path() -> str:
 
 
 def load_library():
-    """Load libclis.so (building it first when nvcc is available and it is stale)."""
-    global _lib
+    """Load libclis.so and its torch binding (building them first when nvcc is available
+    and they are stale)."""
+    global _lib, _native
     if _lib is not None:
         return _lib
     path = _build.LIB
@@ -140,6 +143,10 @@ def load_library():
     lib.clis_attn_paged_workspace_size.restype = i32
     lib.clis_attn_fwd_paged.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, i64, f32, i32, vp, sz, vp]
     lib.clis_attn_fwd_paged.restype = i32
+    spec = importlib.util.spec_from_file_location("_clis_torch", _build.TORCH_EXT)
+    _native = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_native)
+    _native.set_error_class(ClisError)
     _lib = lib
     return lib
 
@@ -770,39 +777,8 @@ class Rope(NamedTuple):
     interleaved: bool = False
 
 
-def _check(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
-def _on(device, stream=None):
-    """(context that makes ``device`` current if it is not, raw stream handle)."""
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device), (stream or torch.cuda.current_stream(device)).cuda_stream
-    return None, (stream or torch.cuda.current_stream()).cuda_stream
-
-
-def _call(name: str, device, stream, *args) -> None:
-    """The library's ``name`` on ``device`` and ``stream`` (default: current)."""
-    ctx, raw = _on(device, stream)
-    fn = getattr(load_library(), name)
-    if ctx is None:
-        st = fn(*args, raw)
-    else:
-        with ctx:
-            st = fn(*args, raw)
-    if st != 0:
-        raise ClisError(name, st)
-
-
-def _check_rope_table(positions, inv_freq, axis, device) -> None:
-    _check(positions.dtype == torch.int32, "positions must be int32")
-    _check(inv_freq.dtype == torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous(),
-           "inv_freq must be a contiguous float64 tensor [pairs]")
-    _check(axis.dtype == torch.int32 and axis.shape == inv_freq.shape and axis.is_contiguous(),
-           "axis must be a contiguous int32 tensor [pairs]")
-    _check(positions.device == device and inv_freq.device == device and axis.device == device,
-           "positions, inv_freq and axis must be on the device of q")
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def clis_rope(q, k, positions, inv_freq, axis, interleaved: bool = False, inverse: bool = False, q_out=None,
@@ -810,74 +786,20 @@ def clis_rope(q, k, positions, inv_freq, axis, interleaved: bool = False, invers
     """q [B, H, N, d] and k [B, H_kv, N, d] (or None) rotated by their positions
     (see :class:`Rope`), or back with ``inverse``; returns (q', k').  q_out and
     k_out may be q and k themselves."""
-    _check(q.is_cuda and q.dim() == 4 and q.dtype in DTYPE and q.stride(-1) == 1,
-           "q must be a bfloat16 or float16 device tensor [B, H, N, d] with a contiguous last dimension")
-    B, H, N, d = q.shape
-    dev = q.device
-    if positions.dim() == 2:
-        positions = positions[None]
-    _check(positions.dim() == 3 and positions.shape[0] in (1, B) and positions.shape[1] == N,
-           "positions must be [B, N, axes] or [N, axes]")
-    _check_rope_table(positions, inv_freq, axis, dev)
-    if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    pairs = [("q_out", q_out, q)]
-    Hk = 0
-    if k is not None:
-        _check(k.dim() == 4 and k.dtype == q.dtype and k.device == dev and k.stride(-1) == 1
-               and k.shape[0] == B and k.shape[2:] == q.shape[2:], "k must match q in all but its number of heads")
-        Hk = k.shape[1]
-        if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        pairs.append(("k_out", k_out, k))
-    for name, t, like in pairs:
-        _check(t.shape == like.shape and t.dtype == q.dtype and t.device == dev and t.stride(-1) == 1,
-               f"{name} must have its input's shape, dtype and device and a contiguous last dimension")
-    qs, os, zero = q.stride(), q_out.stride(), (0, 0, 0)
-    ks, kos = (k.stride(), k_out.stride()) if k is not None else (zero, zero)
-    ps = positions.stride()
-    desc = RopeDesc(B, H, Hk, N, d, inv_freq.numel(), positions.shape[2], int(bool(interleaved)), int(bool(inverse)),
-                    qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], os[0], os[1], os[2], kos[0], kos[1], kos[2],
-                    ps[0] if positions.shape[0] > 1 else 0, ps[1], ps[2], DTYPE[q.dtype])
-    _call("clis_rope", dev, stream, desc, q.data_ptr(), k.data_ptr() if k is not None else None, q_out.data_ptr(),
-          k_out.data_ptr() if k is not None else None, positions.data_ptr(), inv_freq.data_ptr(), axis.data_ptr())
-    return q_out, (k_out if k is not None else None)
+    return _native.rope(q, k, positions, inv_freq, axis, interleaved, inverse, q_out, k_out, _raw(stream))
 
 
-def rope_qk(q, k, positions, inv_freq, axis, interleaved: bool = False):
+def rope(q, k, positions, inv_freq, axis, interleaved: bool = False):
     """(q', k'): q and k (or None) rotated by their positions; see :class:`Rope`."""
-    return clis_rope(q, k, positions, inv_freq, axis, interleaved)
+    return _native.rope(q, k, positions, inv_freq, axis, interleaved, False, None, None, None)
 
 
-rope = rope_qk
-
-
-class RopeFunction(torch.autograd.Function):
-    """Rotation of q and k; the gradient is the rotation back (itself
-    differentiable).  The angles carry no gradient."""
-
-    @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, axis, interleaved, inverse):
-        ctx.save_for_backward(positions, inv_freq, axis)
-        ctx.interleaved, ctx.inverse = interleaved, inverse
-        ctx.set_materialize_grads(False)
-        return clis_rope(q, k, positions, inv_freq, axis, interleaved, inverse)
-
-    @staticmethod
-    def backward(ctx, gq, gk):
-        need = [g.contiguous() if g is not None and n else None for g, n in zip((gq, gk), ctx.needs_input_grad)]
-        some = [g for g in need if g is not None]
-        if not some:
-            return (None,) * 7
-        back = RopeFunction.apply(some[0], some[1] if len(some) > 1 else None, *ctx.saved_tensors, ctx.interleaved,
-                                  not ctx.inverse)
-        back = iter(back)
-        return tuple(next(back) if g is not None else None for g in need) + (None,) * 5
+rope_qk = rope  # (for the functions that have an argument of that name)
 
 
 def rope_autograd(q, k, positions, inv_freq, axis, interleaved: bool = False):
-    """Differentiable :func:`rope_qk` (training)."""
-    return RopeFunction.apply(q, k, positions, inv_freq, axis, bool(interleaved), False)
+    """Differentiable :func:`rope` (training): the gradient is the rotation back."""
+    return _native.rope_autograd(q, k, positions, inv_freq, axis, interleaved)
 
 
 # -------------------------------------------------- paged key/value cache
@@ -894,11 +816,6 @@ class PagedPlan(NamedTuple):
     ring_state: torch.Tensor
 
 
-def _check_int(t, dtype, shape, device, name: str) -> None:
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on the same device")
-
-
 def clis_paged_plan(ctx_len, new_len, block_table, ring, ring_state, page_size: int, num_tokens: int,
                     num_pages: int | None = None, stream=None) -> PagedPlan:
     """Block tables, slots and positions of a step from the lengths of its
@@ -908,47 +825,11 @@ def clis_paged_plan(ctx_len, new_len, block_table, ring, ring_state, page_size: 
     given back are written into it), ring_state int64 [2] (its head and tail,
     not changed).  num_tokens: rows of the packed batch, at least the sum of the
     new tokens.  num_pages: pages of the cache (default: the ring's size)."""
-    dev = ctx_len.device
-    _check(ctx_len.is_cuda and ctx_len.dim() == 1, "ctx_len must be an int32 device tensor [S]")
-    S = ctx_len.shape[0]
-    _check_int(ctx_len, torch.int32, ctx_len.shape, dev, "ctx_len")
-    _check_int(new_len, torch.int32, ctx_len.shape, dev, "new_len")
-    _check_int(ring_state, torch.int64, (2,), dev, "ring_state")
-    _check(ring.dim() == 1, "ring must be an int32 tensor [ring size]")
-    _check_int(ring, torch.int32, ring.shape, dev, "ring")
-    _check(block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.device == dev
-           and block_table.shape[0] == S and block_table.stride(1) == 1,
-           "block_table must be an int32 tensor [S, width] with contiguous rows on the same device")
-    T = int(num_tokens)
-    _check(T >= 0, "num_tokens must not be negative")
-    # One allocation for the five outputs: 8-byte values first.
-    buf = torch.empty(2 + T + (2 * S + 1 + T + 1) // 2 + 1, dtype=torch.int64, device=dev)
-    state, slots, small = buf[:2], buf[2:2 + T], buf[2 + T:].view(torch.int32)
-    cu, kv, pos = small[:S + 1], small[S + 1:2 * S + 1], small[2 * S + 1:2 * S + 1 + T]
-    desc = PagedDesc(S, T, 0, 0, 0, int(page_size), ring.shape[0] if num_pages is None else int(num_pages),
-                     block_table.shape[1])
-    desc.bt_ss = block_table.stride(0) if S > 1 else block_table.shape[1]
-    at = buf.data_ptr()
-    at32 = at + 8 * (2 + T)
-    _call("clis_paged_plan", dev, stream, desc, ctx_len.data_ptr(), new_len.data_ptr(), block_table.data_ptr(),
-          ring.data_ptr(), ring.shape[0], ring_state.data_ptr(), at, at32, at32 + 4 * (S + 1), at + 16,
-          at32 + 4 * (2 * S + 1))
-    return PagedPlan(cu, kv, slots, pos, state)
+    return PagedPlan(*_native.paged_plan(ctx_len, new_len, block_table, ring, ring_state, page_size, num_tokens, num_pages,
+                                         _raw(stream)))
 
 
 paged_plan = clis_paged_plan
-
-
-def _cache_desc(k_cache, v_cache, T: int, H: int, d: int, dtype, device) -> PagedDesc:
-    _check(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[3] == d,
-           "k_cache and v_cache must be [pages, H_kv, page_size, d]")
-    _check(k_cache.dtype == dtype and v_cache.dtype == dtype, "the caches must have the dtype of q, k and v")
-    _check(k_cache.device == device and v_cache.device == device, "the caches must be on the device of q, k and v")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    _check(ks[3] == 1 and vs[3] == 1, "the caches must have a contiguous last dimension")
-    pages, Hkv, page = k_cache.shape[:3]
-    return PagedDesc(0, T, H, Hkv, d, page, pages, 1, 0, 0, 0, 0, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], 0,
-                     DTYPE[dtype])
 
 
 def clis_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, inv_freq=None, axis=None,
@@ -958,44 +839,8 @@ def clis_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, inv
     rotated by ``positions`` (int32 [T, axes] or [T]) if given, and returns q
     [T, H, d] rotated by them (None without q).  Any strides with a contiguous last
     dimension; q_out may be q."""
-    _check(k.is_cuda and k.dim() == 3 and k.dtype in DTYPE and k.stride(2) == 1,
-           "k must be a bfloat16 or float16 device tensor [T, H_kv, d] with a contiguous last dimension")
-    T, Hk, d = k.shape
-    dev = k.device
-    _check(v.shape == k.shape and v.dtype == k.dtype and v.device == dev and v.stride(2) == 1, "v must match k")
-    H = Hk
-    if q is not None:
-        _check(positions is not None, "q is rotated: positions are needed")
-        _check(q.dim() == 3 and q.shape[0] == T and q.shape[2] == d and q.dtype == k.dtype and q.device == dev
-               and q.stride(2) == 1, "q must match k in all but its number of heads")
-        H = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _check(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.device == dev and q_out.stride(2) == 1,
-               "q_out must match q")
-    desc = _cache_desc(k_cache, v_cache, T, H, d, k.dtype, dev)
-    _check(desc.Hkv == Hk, "the caches must have k's number of heads")
-    _check_int(slots, torch.int64, (T,), dev, "slots")
-    ks, vs = k.stride(), v.stride()
-    r = RopeDesc(1, 0 if q is None else H, Hk, T, d, dtype=DTYPE[k.dtype])
-    r.k_sh, r.k_sn = ks[1], ks[0]
-    ptrs = (None, None, None)
-    if positions is not None:
-        if positions.dim() == 1:
-            positions = positions[:, None]
-        _check(positions.dim() == 2 and positions.shape[0] == T, "positions must be [T, axes] or [T]")
-        _check(inv_freq is not None and axis is not None, "positions need inv_freq and axis")
-        _check_rope_table(positions, inv_freq, axis, dev)
-        r.pairs, r.axes, r.interleaved = inv_freq.numel(), positions.shape[1], int(bool(interleaved))
-        r.p_sn, r.p_sa = positions.stride()
-        ptrs = (positions.data_ptr(), inv_freq.data_ptr(), axis.data_ptr())
-        _check(r.pairs > 0, "inv_freq is empty")
-    if q is not None:
-        (r.q_sn, r.q_sh), (r.qo_sn, r.qo_sh) = q.stride()[:2], q_out.stride()[:2]
-    _call("clis_paged_append", dev, stream, desc, r, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          vs[0], vs[1], None if q is None else q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          slots.data_ptr(), *ptrs)
-    return q_out if q is not None else None
+    return _native.paged_append(k, v, k_cache, v_cache, slots, q, positions, inv_freq, axis, interleaved, q_out,
+                                _raw(stream))
 
 
 paged_append = clis_paged_append
@@ -1006,50 +851,8 @@ def clis_attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: i
     """Attention of the new tokens q [T, H, d] (those of sequence s are rows cu_q[s] ..
     cu_q[s + 1] - 1) over their sequences' cached keys; returns ``out``.  ``lse2``:
     optional float32 [T, H].  Rows that belong to no sequence are not written."""
-    _check(q.is_cuda and q.dim() == 3 and q.dtype in DTYPE and q.stride(2) == 1,
-           "q must be a bfloat16 or float16 device tensor [T, H, d] with a contiguous last dimension")
-    T, H, d = q.shape
-    dev = q.device
-    desc = _cache_desc(k_cache, v_cache, T, H, d, q.dtype, dev)
-    _check(block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.device == dev
-           and block_table.stride(1) == 1, "block_table must be an int32 tensor [S, width] with contiguous rows")
-    S, width = block_table.shape
-    _check_int(cu_q, torch.int32, (S + 1,), dev, "cu_q")
-    _check_int(kv_len, torch.int32, (S,), dev, "kv_len")
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    _check(out.shape == q.shape and out.dtype == q.dtype and out.device == dev and out.stride(2) == 1,
-           "out must match q")
-    if lse2 is not None:
-        _check_int(lse2, torch.float32, (T, H), dev, "lse2")
-    desc.S, desc.width, desc.bt_ss = S, width, block_table.stride(0) if S > 1 else 0
-    (desc.q_st, desc.q_sh), (desc.o_st, desc.o_sh) = q.stride()[:2], out.stride()[:2]
-    n = ctypes.c_size_t(0)
-    ctx, raw = _on(dev, stream)
-    if ctx is not None:
-        ctx.__enter__()
-    try:
-        lib = load_library()
-        st = lib.clis_attn_paged_workspace_size(desc, max_q, n)
-        if st != 0:
-            raise ClisError("clis_attn_paged_workspace_size", st)
-        if workspace is None:
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-            if stream is not None:  # allocated on the current stream, used on the given one
-                workspace.record_stream(stream)
-        _check(workspace.device == dev and workspace.is_contiguous(),
-               "the workspace must be contiguous and on the device of q")
-        st = lib.clis_attn_fwd_paged(desc, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                     block_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
-                                     None if lse2 is None else lse2.data_ptr(), max_q, float(scale_log2),
-                                     int(bool(causal)), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), raw)
-    finally:
-        if ctx is not None:
-            ctx.__exit__(None, None, None)
-    if st != 0:
-        raise ClisError("clis_attn_fwd_paged", st)
-    return out
+    return _native.attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, scale_log2, causal, out, lse2,
+                                   workspace, _raw(stream))
 
 
 def attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: int | None = None,
@@ -1058,10 +861,9 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: int |
     tokens and chunks in one call (grouped-query heads by q's and the caches'
     head counts).  max_q: the most new tokens of a sequence (default: all rows of q).
     With ``return_lse``: (out, lse2 float32 [T, H])."""
-    T = q.shape[0]
     lse2 = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
-    o = clis_attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max(1, T if max_q is None else int(max_q)),
-                            scale_log2_for(q.shape[-1], softmax_scale), causal, out, lse2)
+    o = _native.attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q or max(1, q.shape[0]),
+                                scale_log2_for(q.shape[-1], softmax_scale), causal, out, lse2, None, None)
     return (o, lse2) if return_lse else o
 
 
