@@ -124,7 +124,7 @@ clis_status_t check_attn(const clis_paged_t *p, int64_t max_q)
     if (overlapping(p->d, od, 2)) return CLIS_ERR_INVALID_ARG;
     // Work units and tiles are counted in 32 bits.
     const double per = static_cast<double>(p->width) * static_cast<double>(p->page_size);
-    if (static_cast<double>(p->S) * static_cast<double>(p->Hkv) * (per / clis::kDecodeKeys + 1) >= 4.0e9)
+    if (static_cast<double>(p->S) * static_cast<double>(p->Hkv) * (per / 64 + 1) >= 4.0e9)
         return CLIS_ERR_UNSUPPORTED;
     const int64_t tpc = clis::chunk_tokens(static_cast<int>(p->H / p->Hkv));
     if (static_cast<double>(p->Hkv) * (static_cast<double>(p->T) / tpc + p->S + 1) >= 1.0e9) return CLIS_ERR_UNSUPPORTED;

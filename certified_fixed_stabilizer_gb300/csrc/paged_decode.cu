@@ -16,8 +16,8 @@
 //    every block an equal run, so ragged lengths balance; an item that crosses
 //    a cut leaves partial results (unnormalised o, m, l) that
 //    paged_decode_join_kernel adds in a fixed order.
-//  * Loads: each of the block's four warps takes 16 of a unit's 64 keys and runs
-//    its own ring of cp.async stages: no block-wide barrier inside an item, and
+//  * Loads: each of the block's four warps takes a quarter of a unit's keys (16 of
+//    64 at d = 128, 32 of 128 at d = 64: 8 KB either way) and runs its own ring of cp.async stages: no block-wide barrier inside an item, and
 //    the ring runs on into the next item, so item ends do not drain it.  Rows
 //    past the length are filled with zeros by the copy itself: what a page
 //    holds behind the last key is never multiplied (0 * NaN would be NaN).
@@ -40,19 +40,20 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTileKeys = kDecodeKeys / kWarps;  // 16 keys per warp and unit
 constexpr float kTau = 8.0f;
 constexpr int kJoinThreads = 512;
 
 template <int D>
 struct DCfg {
-    static constexpr int NST = D == 128 ? 3 : 6;
+    static constexpr int KEYS = decode_keys(D);         // per unit
+    static constexpr int TK = KEYS / kWarps;            // 16 or 32 keys per warp and unit
+    static constexpr int NST = 3;
     static constexpr int ROW = D * 2;                   // bytes of a row
-    static constexpr int HALF = kTileKeys * ROW;        // K (or V) of a stage
+    static constexpr int HALF = TK * ROW;               // K (or V) of a stage
     static constexpr int STAGE = 2 * HALF;
     static constexpr int RING = kWarps * NST * STAGE;
     static constexpr int OPITCH = D + 8;                // floats per row of the merge buffer
-    static constexpr int MERGE = 16 * OPITCH * 4;
+    static constexpr int MERGE = 16 * OPITCH * 4;       // (also holds Q, see below)
     static constexpr int SMEM = RING + MERGE;
 };
 
@@ -62,7 +63,7 @@ struct DecodeParams {
     int strict;  // no chunk kernel follows: a sequence of more rows is an error
     float *part_o;   // [2 * blocks][rows_max][D]
     float2 *part_ml; // [2 * blocks][rows_max]
-    int4 *meta;      // [blocks] {parts, sequence, head, 0} of the item the block starts and does not finish
+    int4 *meta;      // [blocks] {parts, first row of q, new tokens, head} of the item the block starts and does not finish
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
@@ -134,7 +135,7 @@ struct Pos {
     {
         s = seq;
         q = seq_len(a, s);
-        units = decode_units(q);
+        units = decode_units(q, decode_keys(a.d));
     }
     // The next item of the run (there is one if units are left).
     __device__ __forceinline__ void next_item(const PagedArgs &a, int g, int rows_max)
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     for (int s = sb; s < se; s++) {
         const SeqLen q = seq_len(a, s);
         if (q.bad) bad |= CLIS_PAGED_LENGTH_BIT;
-        if (is_decode(q, p.g, p.rows_max)) mine += static_cast<uint32_t>(a.Hkv) * decode_units(q);
+        if (is_decode(q, p.g, p.rows_max)) mine += static_cast<uint32_t>(a.Hkv) * decode_units(q, C::KEYS);
         else if (p.strict && q.n > 0) bad |= CLIS_PAGED_LENGTH_BIT;
     }
     uint32_t incl = mine;
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
         for (int s = sb; s < se; s++) {
             const SeqLen q = seq_len(a, s);
             if (!is_decode(q, p.g, p.rows_max)) continue;
-            const uint32_t w = static_cast<uint32_t>(a.Hkv) * decode_units(q);
+            const uint32_t w = static_cast<uint32_t>(a.Hkv) * decode_units(q, C::KEYS);
             if (rel < w) {
                 s_seq = s;
                 s_rel = rel;
@@ -225,15 +226,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     // ---- loader: one stage per unit, `ld` runs NST - 1 units ahead of `cur`
     constexpr int CPR = D / 8;         // 16-byte chunks per row
     constexpr int RPI = 32 / CPR;      // rows per copy instruction
-    constexpr int NCP = kTileKeys / RPI;
+    constexpr int NCP = C::TK / RPI;
     const uint32_t ring = smem_u32(smem) + warp * C::NST * C::STAGE;
     const int key_mask = (1 << a.page_shift) - 1;
     const int lrow = lane / CPR, lchunk = lane % CPR;
     Pos ld = cur;
     int ld_stage = 0;
-    // Page of key (lane & 15) of the tile that the loader is at, read one unit ahead.
+    // Page of the lane's key of the tile that the loader is at, read one unit ahead.
     auto page_at = [&](const Pos &q) -> int {
-        const int key = q.j * kDecodeKeys + warp * kTileKeys + (lane & 15);
+        const int key = q.j * C::KEYS + warp * C::TK + (lane & (C::TK - 1));
         if (q.left == 0 || key >= q.q.kv) return -2;  // nothing to load
         return __ldg(a.block_table + q.s * a.bt_s + (key >> a.page_shift));
     };
@@ -245,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                 page = -2;  // its keys read as zeros
             }
             const uint32_t dst = ring + ld_stage * C::STAGE;
-            const int key0 = ld.j * kDecodeKeys + warp * kTileKeys;
-#pragma unroll
+            const int key0 = ld.j * C::KEYS + warp * C::TK;
+#pragma unroll (MT * D == 256 ? 1 : NCP)
             for (int i = 0; i < NCP; i++) {
                 const int row = i * RPI + lrow;
                 const int pg = __shfl_sync(~0u, page, row);
@@ -283,8 +284,24 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
         const int n = cur.q.n, kv = cur.q.kv, R = n * p.g, q0 = cur.q.q0;
         const int lim0 = visible_keys(n, kv, 0, a.causal);  // keys that every row sees
 
-        uint32_t qf[MT][D / 16][4];
+        // Q as operand fragments; with two row tiles at d = 128 they would take 64 more
+        // registers than there are and stay in the merge buffer (32 rows, swizzled).
+        constexpr bool QREG = MT * D <= 128;
+        uint32_t qf[QREG ? MT : 1][QREG ? D / 16 : 1][4];
+        const uint32_t sQ = smem_u32(merge);
         int lim[MT][2];
+        if constexpr (!QREG) {
+            for (int i = tid; i < 32 * (D / 8); i += kThreads) {
+                const int row = i / (D / 8), c8 = i % (D / 8);
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                if (row < R) {
+                    const int tok = row / p.g, hd = cur.h * p.g + row - tok * p.g;
+                    u = __ldg(reinterpret_cast<const uint4 *>(a.q + static_cast<int64_t>(q0 + tok) * a.q_st + hd * a.q_sh) + c8);
+                }
+                *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(merge) + row * C::ROW + ((c8 ^ (row & 7)) << 4)) = u;
+            }
+            __syncthreads();
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; mt++)
 #pragma unroll
@@ -293,11 +310,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                 const bool ok = row < R;
                 const int tok = ok ? row / p.g : 0, hd = cur.h * p.g + (ok ? row - tok * p.g : 0);
                 lim[mt][hf] = ok ? visible_keys(n, kv, tok, a.causal) : 0;
+                if constexpr (QREG) {
                 const uint16_t *src = a.q + static_cast<int64_t>(q0 + tok) * a.q_st + hd * a.q_sh + c2;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ks++) {
                     qf[mt][ks][hf] = ok ? __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16)) : 0u;
                     qf[mt][ks][hf + 2] = ok ? __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16 + 8)) : 0u;
+                }
                 }
             }
         float o[MT][D / 8][4];
@@ -315,37 +334,52 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
             cp_async_wait<C::NST - 2>();
             __syncwarp();
             load_step();  // into the stage that the previous unit has been read from
-            const int key0 = j * kDecodeKeys + warp * kTileKeys;
+            const int key0 = j * C::KEYS + warp * C::TK;
             const uint32_t sK = ring + stage * C::STAGE, sV = sK + C::HALF;
             stage = stage + 1 == C::NST ? 0 : stage + 1;
             if (key0 >= kv) continue;
 
-            // S = Q K^T: 16 rows x 16 keys per row tile
-            float s[MT][2][4];
+            // S = Q K^T: 16 rows x TK keys per row tile
+            constexpr int NB = C::TK / 8, KB = C::TK / 16;  // key blocks of 8 and of 16
+            float s[MT][NB][4];
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                for (int i = 0; i < 2; i++) s[mt][i][0] = s[mt][i][1] = s[mt][i][2] = s[mt][i][3] = 0.f;
+                for (int i = 0; i < NB; i++) s[mt][i][0] = s[mt][i][1] = s[mt][i][2] = s[mt][i][3] = 0.f;
             {
                 const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+                const int qr = lane & 15, qc = lane >> 4;
                 const uint32_t base = sK + kr * C::ROW;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ks++) {
-                    uint32_t kf[4];
-                    ldsm4(base + (((ks * 2 + kc) ^ (kr & 7)) << 4), kf);
+                    uint32_t qm[MT][4];
 #pragma unroll
                     for (int mt = 0; mt < MT; mt++) {
-                        mma16816<DT>(s[mt][0], qf[mt][ks], kf[0], kf[1]);
-                        mma16816<DT>(s[mt][1], qf[mt][ks], kf[2], kf[3]);
+                        if constexpr (QREG) {
+#pragma unroll
+                            for (int e = 0; e < 4; e++) qm[mt][e] = qf[mt][ks][e];
+                        } else {
+                            ldsm4(sQ + (mt * 16 + qr) * C::ROW + (((ks * 2 + qc) ^ (qr & 7)) << 4), qm[mt]);
+                        }
+                    }
+#pragma unroll
+                    for (int kb = 0; kb < KB; kb++) {
+                        uint32_t kf[4];
+                        ldsm4(base + kb * 16 * C::ROW + (((ks * 2 + kc) ^ (kr & 7)) << 4), kf);
+#pragma unroll
+                        for (int mt = 0; mt < MT; mt++) {
+                            mma16816<DT>(s[mt][2 * kb], qm[mt], kf[0], kf[1]);
+                            mma16816<DT>(s[mt][2 * kb + 1], qm[mt], kf[2], kf[3]);
+                        }
                     }
                 }
             }
-            const bool edge = key0 + kTileKeys > lim0;  // some row does not see some key
+            const bool edge = key0 + C::TK > lim0;  // some row does not see some key
             if (edge) {
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                    for (int i = 0; i < 2; i++)
+                    for (int i = 0; i < NB; i++)
 #pragma unroll
                         for (int e = 0; e < 4; e++)
                             if (key0 + i * 8 + c2 + (e & 1) >= lim[mt][e >> 1]) s[mt][i][e] = -INFINITY;
@@ -356,8 +390,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
-                    float v = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
-                                    fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+                    float v = fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]);
+#pragma unroll
+                    for (int i = 1; i < NB; i++) v = fmax3(v, s[mt][i][2 * hf], s[mt][i][2 * hf + 1]);
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
                     mx[mt][hf] = v * sl2;
@@ -380,18 +415,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                         }
                     }
             }
-            uint32_t pf[MT][4];
+            uint32_t pf[MT][KB][4];
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
                     const float ns = m_run[mt][hf] == -INFINITY ? 0.f : -m_run[mt][hf];
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
+                    for (int i = 0; i < NB; i++) {
                         const float p0 = ex2_approx(fmaf(s[mt][i][2 * hf], sl2, ns));
                         const float p1 = ex2_approx(fmaf(s[mt][i][2 * hf + 1], sl2, ns));
                         l_run[mt][hf] += p0 + p1;
-                        pf[mt][2 * i + hf] = pack2<DT>(p0, p1);
+                        pf[mt][i >> 1][2 * (i & 1) + hf] = pack2<DT>(p0, p1);
                     }
                 }
             // O += P V
@@ -400,18 +435,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                 const uint32_t base = sV + vr * C::ROW;
                 auto pv = [&](bool clean) {
 #pragma unroll
-                    for (int i = 0; i < D / 16; i++) {
-                        uint32_t vf[4];
-                        ldsm4_t(base + (((i * 2 + vc) ^ (vr & 7)) << 4), vf);
-                        if (clean)
+                    for (int kb = 0; kb < KB; kb++)
 #pragma unroll
-                            for (int e = 0; e < 4; e++) dirty |= scrub<DT>(vf[e]);
+                        for (int i = 0; i < D / 16; i++) {
+                            uint32_t vf[4];
+                            ldsm4_t(base + kb * 16 * C::ROW + (((i * 2 + vc) ^ (vr & 7)) << 4), vf);
+                            if (clean)
 #pragma unroll
-                        for (int mt = 0; mt < MT; mt++) {
-                            mma16816<DT>(o[mt][2 * i], pf[mt], vf[0], vf[1]);
-                            mma16816<DT>(o[mt][2 * i + 1], pf[mt], vf[2], vf[3]);
+                                for (int e = 0; e < 4; e++) dirty |= scrub<DT>(vf[e]);
+#pragma unroll
+                            for (int mt = 0; mt < MT; mt++) {
+                                mma16816<DT>(o[mt][2 * i], pf[mt][kb], vf[0], vf[1]);
+                                mma16816<DT>(o[mt][2 * i + 1], pf[mt][kb], vf[2], vf[3]);
+                            }
                         }
-                    }
                 };
                 // Where a key is masked for some rows only, a non-finite v of it must
                 // not reach them as 0 * inf: it is left out of the product and added to
@@ -501,8 +538,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                 const int tok = row / p.g, hd = cur.h * p.g + (row - tok * p.g);
                 if (any_dirty) {
                     // Non-finite values of keys that this row sees and that were left out.
-                    const int see = min(visible_keys(n, kv, tok, a.causal), j1 * kDecodeKeys);
-                    for (int key = max(lim0 / kTileKeys * kTileKeys, j0 * kDecodeKeys); key < see; key++) {
+                    const int see = min(visible_keys(n, kv, tok, a.causal), j1 * C::KEYS);
+                    for (int key = max(lim0 / C::TK * C::TK, j0 * C::KEYS); key < see; key++) {
                         const int pg = __ldg(a.block_table + cur.s * a.bt_s + (key >> a.page_shift));
                         if (pg < 0 || pg >= a.num_pages) continue;
                         const uint16_t *vs = a.vc + static_cast<int64_t>(pg) * a.vc_sp + cur.h * a.vc_sh +
@@ -539,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
             int ce = static_cast<int>(static_cast<uint64_t>(end) * static_cast<uint32_t>(nb) / U);
             while (ce > c && decode_cut(U, nb, ce) > end) ce--;
             while (ce + 1 < nb && decode_cut(U, nb, ce + 1) <= end) ce++;
-            p.meta[c] = make_int4(ce - c + 1, cur.s, cur.h, 0);
+            p.meta[c] = make_int4(ce - c + 1, q0, n, cur.h);
         }
         cur.left -= j1 - j0;
         cur.j = j1;
@@ -550,85 +587,68 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     pdl_wait();  // (the schedule kernel, whose results only later kernels read)
 }
 
-// Adds the partial results of the item that block c of the decode kernel
-// started and did not finish: its own and those at the start of the following
-// blocks, in that order per group of warps (fixed, so reruns agree bit for bit).
+// Adds the partial results of the item that block c of the decode kernel started
+// and did not finish: its own and those at the start of the following blocks.  A
+// thread takes four columns of a row; where an item's rows leave threads over,
+// groups of threads take every so-many-th part (a fixed order, so reruns agree
+// bit for bit).
 template <int D, int DT>
 __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const DecodeParams p)
 {
-    constexpr int V = D / 32;  // columns per lane
-    __shared__ float s_o[kJoinThreads / 32][D];
-    __shared__ float s_l[kJoinThreads / 32];
+    constexpr int TPR = D / 4;  // threads per row
+    __shared__ float4 s_o[kJoinThreads];
+    __shared__ float2 s_ml[kJoinThreads];
     const PagedArgs &a = p.a;
-    const int c = blockIdx.x;
+    const int c = blockIdx.x, tid = threadIdx.x;
     pdl_wait();
     pdl_launch();
     const int4 mt = p.meta[c];
-    const int K = mt.x;
+    const int K = mt.x, q0 = mt.y, R = mt.z * p.g;
     if (K == 0) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const SeqLen q = seq_len(a, mt.y);
-    const int R = q.n * p.g;
-    // Warps: rows x groups of parts.
-    constexpr int W = kJoinThreads / 32;
     int rows = 1;
-    while (rows < R && rows < W) rows *= 2;
-    const int groups = W / rows;
-    const int wr = warp % rows, grp = warp / rows;
-    auto slot_of = [&](int k) -> int64_t { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
+    while (rows < R && rows < kJoinThreads / TPR) rows *= 2;
+    const int groups = kJoinThreads / TPR / rows;
+    const int c4 = tid % TPR, wr = tid / TPR % rows, grp = tid / TPR / rows;
     for (int rb = 0; rb < R; rb += rows) {
         const int row = rb + wr;
         float M = -INFINITY, l = 0.f;
-        float o[V];
-#pragma unroll
-        for (int e = 0; e < V; e++) o[e] = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float2 ml, float4 x) {
+            if (ml.y == 0.f) return;  // a part none of whose keys the row sees
+            const float m = fmaxf(M, ml.x), w = ex2_approx(ml.x - m);
+            const bool none = l == 0.f;
+            const float w0 = none ? 0.f : ex2_approx(M - m);
+            M = m;
+            l = none ? w * ml.y : fmaf(l, w0, w * ml.y);
+            o.x = none ? w * x.x : fmaf(o.x, w0, w * x.x);
+            o.y = none ? w * x.y : fmaf(o.y, w0, w * x.y);
+            o.z = none ? w * x.z : fmaf(o.z, w0, w * x.z);
+            o.w = none ? w * x.w : fmaf(o.w, w0, w * x.w);
+        };
         if (row < R) {
-            for (int k = lane; k < K; k += 32) {
-                const float2 ml = p.part_ml[slot_of(k) * p.rows_max + row];
-                if (ml.y != 0.f) M = fmaxf(M, ml.x);
-            }
-#pragma unroll
-            for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, s));
 #pragma unroll 4
             for (int k = grp; k < K; k += groups) {
-                const int64_t at = slot_of(k) * p.rows_max + row;
-                const float2 ml = p.part_ml[at];
-                const float w = ml.y == 0.f ? 0.f : ex2_approx(ml.x - M);
-                float x[V];
-                if (V == 4) {
-                    const float4 u = *reinterpret_cast<const float4 *>(p.part_o + at * D + lane * 4);
-                    x[0] = u.x; x[1] = u.y; x[2 % V] = u.z; x[3 % V] = u.w;
-                } else {
-                    const float2 u = *reinterpret_cast<const float2 *>(p.part_o + at * D + lane * 2);
-                    x[0] = u.x; x[1] = u.y;
-                }
-                if (ml.y != 0.f) {
-                    l = fmaf(w, ml.y, l);
-#pragma unroll
-                    for (int e = 0; e < V; e++) o[e] = fmaf(w, x[e], o[e]);
-                }
+                const int64_t at = static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * p.rows_max + row;
+                add(p.part_ml[at], reinterpret_cast<const float4 *>(p.part_o + at * D)[c4]);
             }
         }
-#pragma unroll
-        for (int e = 0; e < V; e++) s_o[warp][lane * V + e] = o[e];
-        if (lane == 0) s_l[warp] = l;
-        __syncthreads();
+        if (groups > 1) {
+            s_o[tid] = o;
+            s_ml[tid] = make_float2(M, l);
+            __syncthreads();
+            if (grp == 0)
+                for (int g2 = 1; g2 < groups; g2++) add(s_ml[tid + g2 * rows * TPR], s_o[tid + g2 * rows * TPR]);
+            __syncthreads();
+        }
         if (grp == 0 && row < R) {
-            for (int g2 = 1; g2 < groups; g2++) {
-                l += s_l[wr + g2 * rows];
-#pragma unroll
-                for (int e = 0; e < V; e++) o[e] += s_o[wr + g2 * rows][lane * V + e];
-            }
-            const float inv = l != 0.f ? 1.f / l : 0.f;
-            const int tok = row / p.g, hd = mt.z * p.g + (row - tok * p.g);
-            uint16_t *dst = a.o + static_cast<int64_t>(q.q0 + tok) * a.o_st + hd * a.o_sh + lane * V;
-#pragma unroll
-            for (int e = 0; e < V; e += 2)
-                *reinterpret_cast<uint32_t *>(dst + e) = l != 0.f ? pack2<DT>(o[e] * inv, o[e + 1] * inv) : 0u;
-            if (lane == 0 && a.lse2)
-                a.lse2[static_cast<int64_t>(q.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
+            const float inv = 1.f / l;
+            const int tok = row / p.g, hd = mt.w * p.g + (row - tok * p.g);
+            uint2 u = make_uint2(0u, 0u);  // a row that sees no key
+            if (l != 0.f) u = make_uint2(pack2<DT>(o.x * inv, o.y * inv), pack2<DT>(o.z * inv, o.w * inv));
+            *reinterpret_cast<uint2 *>(a.o + static_cast<int64_t>(q0 + tok) * a.o_st + hd * a.o_sh + c4 * 4) = u;
+            if (c4 == 0 && a.lse2)
+                a.lse2[static_cast<int64_t>(q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
         }
-        __syncthreads();
     }
 }
 
@@ -677,7 +697,7 @@ clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict
     p.a = a;
     p.g = a.H / a.Hkv;
     p.rows_max = static_cast<int>(rows);
-    p.least = 4;
+    p.least = 2;  // units per block at least: one token over 301 keys 13.7 us with 1 or 2, 14.5 with 4, 18.7 with 8
     p.strict = strict;
     char *w = static_cast<char *>(workspace);
     p.meta = reinterpret_cast<int4 *>(w);

@@ -49,11 +49,11 @@ CLIS_HD int visible_keys(int n, int kv, int t, bool causal)
 // ------------------------------------------------------------ decode kernel
 //
 // Items are (sequence, key/value head), sequence-major; an item costs one unit
-// per kDecodeKeys keys (at least one: its output must be written).  The units
+// per decode_keys(d) keys (at least one: its output must be written).  The units
 // of all items, laid end to end, are cut into as many equal runs as there are
 // blocks, so ragged batches balance to one unit, and an item that crosses a cut
 // is joined from partial results afterwards.
-constexpr int kDecodeKeys = 64;
+CLIS_HD constexpr int decode_keys(int d) { return d == 128 ? 64 : 128; }  // the same bytes
 
 CLIS_HD bool is_decode(const SeqLen &s, int g, int rows_max)
 {
@@ -61,7 +61,7 @@ CLIS_HD bool is_decode(const SeqLen &s, int g, int rows_max)
     return s.n > 0 && s.n <= rows_max && s.n * g <= rows_max;
 }
 
-CLIS_HD int decode_units(const SeqLen &s) { return imax(1, ceil_div(s.kv, kDecodeKeys)); }
+CLIS_HD int decode_units(const SeqLen &s, int keys) { return imax(1, ceil_div(s.kv, keys)); }
 
 // Blocks that take part, for U units: every run holds at least `least` units.
 CLIS_HD int decode_blocks(uint32_t U, int grid, int least)

@@ -16,7 +16,11 @@
 // Bound: HBM bytes (each row read once and written once; sin and cos are
 // computed once for a token and group of heads, not per head).  A thread owns
 // 16 elements (8 pairs) of a row and walks a group of heads with the eight
-// angles in registers; loads of four heads are in flight at a time.
+// angles in registers; loads of four heads are in flight at a time, the first
+// of them while the angles are computed.  480p video q and k (671 MB read and
+// written) take 102.7 us, 6.5 TB/s, 96% of the measured copy rate; a chunk of
+// 8,192 tokens into a cache (201 MB) 39.8 us, 5.1 TB/s: its 768 blocks fill the
+// GPU 1.7 times.
 #include <cuda_bf16.h>
 
 #include "clis_internal.h"
@@ -34,18 +38,22 @@ constexpr int kMaxPairs = 64;  // d / 2 at d = 128
 constexpr int kMaxAxes = 4;
 constexpr int kHeadBatch = 4;  // heads whose loads are in flight together
 
+// The eight pairs in u0, u1 by the angles cs, sn.  Interleaved: `first` and `second`
+// say whether u0's and u1's pairs turn (what does not turn is not multiplied by 1
+// and 0: an inf beside it would make a NaN).
 template <int DT>
-__device__ __forceinline__ void rotate8(uint4 &u0, uint4 &u1, const float *cs, const float *sn, bool interleaved)
+__device__ __forceinline__ void rotate8(uint4 &u0, uint4 &u1, const float *cs, const float *sn, bool interleaved,
+                                        bool first, bool second)
 {
     uint32_t a[4] = {u0.x, u0.y, u0.z, u0.w}, b[4] = {u1.x, u1.y, u1.z, u1.w};
     if (interleaved) {
-        // a holds pairs 0..3 as (x0, x1) words, b pairs 4..7.
+        // a holds the first four pairs as (x0, x1) words, b the other four.
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             const float x0 = elem_lo<DT>(a[e]), x1 = elem_hi<DT>(a[e]);
-            a[e] = pack2<DT>(fmaf(x0, cs[e], -x1 * sn[e]), fmaf(x1, cs[e], x0 * sn[e]));
+            if (first) a[e] = pack2<DT>(fmaf(x0, cs[e], -x1 * sn[e]), fmaf(x1, cs[e], x0 * sn[e]));
             const float z0 = elem_lo<DT>(b[e]), z1 = elem_hi<DT>(b[e]);
-            b[e] = pack2<DT>(fmaf(z0, cs[4 + e], -z1 * sn[4 + e]), fmaf(z1, cs[4 + e], z0 * sn[4 + e]));
+            if (second) b[e] = pack2<DT>(fmaf(z0, cs[4 + e], -z1 * sn[4 + e]), fmaf(z1, cs[4 + e], z0 * sn[4 + e]));
         }
     } else {
         // a holds x0 of pairs 0..7, b their x1.
@@ -62,11 +70,60 @@ __device__ __forceinline__ void rotate8(uint4 &u0, uint4 &u1, const float *cs, c
 }
 
 // NC: 16-element chunks per row (d / 16).  hg: heads per block row of the grid.
+// The first heads are loaded before the angles are computed, so that the chain
+// frequency -> turn -> sin, cos runs beside them.
 template <int DT, int NC, bool APPEND>
-__global__ void __launch_bounds__(kRotThreads) rot_kernel(const RotArgs a, const int hg)
+__global__ void __launch_bounds__(kRotThreads, 3) rot_kernel(const RotArgs a, const int hg)
 {
     __shared__ unsigned long long s_step[kMaxPairs];
     __shared__ int s_axis[kMaxPairs];
+    const int idx = blockIdx.x * kRotThreads + threadIdx.x;
+    const bool live = idx < a.B * a.N * NC;
+    const int tok = live ? idx / NC : 0, ch = idx % NC;
+    const int b = tok / a.N, n = tok - b * a.N;
+
+    // The thread's two 8-element vectors of a row and how many of their pairs turn.
+    // Halves: x0 and x1 of pairs 8 ch .. 8 ch + 7.  Interleaved: pairs 4 ch .. 4 ch + 3
+    // from the row's first half and as many from its second (a warp's accesses then
+    // fill whole 128-byte lines).
+    const bool inter = a.interleaved != 0;
+    const bool rot = ch * 8 < a.pairs;  // (halves)
+    const int e0 = inter || rot ? ch * 8 : ch * 16;
+    const int e1 = inter ? NC * 8 + ch * 8 : rot ? a.pairs + ch * 8 : ch * 16 + 8;
+    const int p0 = inter ? ch * 4 : ch * 8, p1 = inter ? NC * 4 + ch * 4 : ch * 8 + 4;  // pairs of angles 0-3, 4-7
+    const bool turn0 = p0 < a.pairs, turn1 = p1 < a.pairs;  // (pairs is a multiple of 8)
+
+    const int heads = a.Hq + (APPEND ? 2 : 1) * a.Hk;
+    const int h0 = blockIdx.y * hg, h1 = live ? min(h0 + hg, heads) : h0;
+    auto source = [&](int h) -> const uint16_t * {
+        if (h < a.Hq) return a.q + b * a.q_sb + h * a.q_sh + n * a.q_sn;
+        if (!APPEND || h < a.Hq + a.Hk) return a.k + b * a.k_sb + (h - a.Hq) * a.k_sh + n * a.k_sn;
+        return a.v + (h - a.Hq - a.Hk) * a.v_sh + n * a.v_sn;
+    };
+    uint4 u0[kHeadBatch], u1[kHeadBatch];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < kHeadBatch; i++) {
+            if (h + i >= h1) continue;
+            const uint16_t *src = source(h + i);
+            u0[i] = *reinterpret_cast<const uint4 *>(src + e0);
+            u1[i] = *reinterpret_cast<const uint4 *>(src + e1);
+        }
+    };
+    load(h0);
+    int pos[kMaxAxes];
+#pragma unroll
+    for (int x = 0; x < kMaxAxes; x++)
+        pos[x] = x < a.axes && a.pairs > 0 ? __ldg(a.pos + b * a.p_sb + n * a.p_sn + x * a.p_sa) : 0;
+    int64_t page = 0, in_page = 0;
+    bool write_kv = true;
+    if (APPEND) {
+        const int64_t slot = live ? __ldg(a.slots + n) : -1;
+        write_kv = slot >= 0 && slot < a.num_slots;
+        if (slot >= a.num_slots) atomicOr(&g_rot_error_word, CLIS_PAGED_INDEX_BIT);
+        page = slot >> a.page_shift;
+        in_page = slot & ((int64_t(1) << a.page_shift) - 1);
+    }
     for (int i = threadIdx.x; i < a.pairs; i += kRotThreads) {
         // Frequency as a fraction of a turn per position, 64-bit fixed point.
         double t = a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
@@ -77,84 +134,48 @@ __global__ void __launch_bounds__(kRotThreads) rot_kernel(const RotArgs a, const
         s_axis[i] = ax;
     }
     __syncthreads();
-    const int idx = blockIdx.x * kRotThreads + threadIdx.x;
-    const int tok = idx / NC, ch = idx % NC;
-    if (tok >= a.B * a.N) return;
-    const int b = tok / a.N, n = tok - b * a.N;
-
-    const bool rot = ch * 8 < a.pairs;  // pairs is a multiple of 8
     float cs[8], sn[8];
-    if (rot) {
-        int pos[kMaxAxes];
-        const int32_t *pp = a.pos + b * a.p_sb + n * a.p_sn;
 #pragma unroll
-        for (int x = 0; x < kMaxAxes; x++) pos[x] = x < a.axes ? __ldg(pp + x * a.p_sa) : 0;
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const int ax = s_axis[ch * 8 + e];
-            // (an axis index out of range turns by nothing)
-            const int p = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : ax == 3 ? pos[3] : 0;
-            const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(p)) * s_step[ch * 8 + e];
-            sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn[e], &cs[e]);
-            if (a.inverse) sn[e] = -sn[e];
-        }
+    for (int e = 0; e < 8; e++) {
+        cs[e] = 1.f;
+        sn[e] = 0.f;
+        if (e < 4 ? !turn0 : !turn1) continue;
+        const int pr = e < 4 ? p0 + e : p1 + e - 4;
+        const int ax = s_axis[pr];
+        // (an axis index out of range turns by nothing)
+        const int p = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : ax == 3 ? pos[3] : 0;
+        const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(p)) * s_step[pr];
+        sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn[e], &cs[e]);
+        if (a.inverse) sn[e] = -sn[e];
     }
-    // The thread's two 8-element vectors of a row.
-    const bool halves = rot && !a.interleaved;
-    const int e0 = halves ? ch * 8 : ch * 16;
-    const int e1 = halves ? a.pairs + ch * 8 : ch * 16 + 8;
-
-    const int heads = a.Hq + (APPEND ? 2 : 1) * a.Hk;
-    const int h0 = blockIdx.y * hg, h1 = min(h0 + hg, heads);
-    int64_t page = 0, in_page = 0;
-    bool write_kv = true;
-    if (APPEND) {
-        const int64_t slot = __ldg(a.slots + n);
-        write_kv = slot >= 0 && slot < a.num_slots;
-        if (slot >= a.num_slots) atomicOr(&g_rot_error_word, CLIS_PAGED_INDEX_BIT);
-        page = slot >> a.page_shift;
-        in_page = slot & ((int64_t(1) << a.page_shift) - 1);
-    }
+    const bool turns = turn0 || turn1;
+#pragma unroll 1
     for (int h = h0; h < h1; h += kHeadBatch) {
-        uint4 u0[kHeadBatch], u1[kHeadBatch];
-        uint16_t *dst[kHeadBatch];
-        bool turn[kHeadBatch];
 #pragma unroll
         for (int i = 0; i < kHeadBatch; i++) {
             const int hh = h + i;
-            dst[i] = nullptr;
-            turn[i] = rot;
             if (hh >= h1) continue;
-            const uint16_t *src;
+            uint16_t *dst;
+            bool turn = turns;
             if (hh < a.Hq) {
-                src = a.q + b * a.q_sb + hh * a.q_sh + n * a.q_sn;
-                dst[i] = a.qo + b * a.qo_sb + hh * a.qo_sh + n * a.qo_sn;
-            } else if (!APPEND || hh < a.Hq + a.Hk) {
-                const int kh = hh - a.Hq;
-                src = a.k + b * a.k_sb + kh * a.k_sh + n * a.k_sn;
-                dst[i] = APPEND ? a.ko + page * a.ko_sb + kh * a.ko_sh + in_page * a.ko_sn
-                                : a.ko + b * a.ko_sb + kh * a.ko_sh + n * a.ko_sn;
+                dst = a.qo + b * a.qo_sb + hh * a.qo_sh + n * a.qo_sn;
+            } else if (!APPEND) {
+                dst = a.ko + b * a.ko_sb + (hh - a.Hq) * a.ko_sh + n * a.ko_sn;
             } else {
-                const int vh = hh - a.Hq - a.Hk;
-                src = a.v + vh * a.v_sh + n * a.v_sn;
-                dst[i] = a.vo + page * a.vo_sb + vh * a.vo_sh + in_page * a.vo_sn;
-                turn[i] = false;
+                if (!write_kv) continue;
+                const int kh = hh - a.Hq;
+                if (kh < a.Hk) {
+                    dst = a.ko + page * a.ko_sb + kh * a.ko_sh + in_page * a.ko_sn;
+                } else {  // v is copied as it is
+                    dst = a.vo + page * a.vo_sb + (kh - a.Hk) * a.vo_sh + in_page * a.vo_sn;
+                    turn = false;
+                }
             }
-            if (APPEND && hh >= a.Hq && !write_kv) {
-                dst[i] = nullptr;
-                continue;
-            }
-            // v is copied, not rotated, so any split of its row will do.
-            u0[i] = *reinterpret_cast<const uint4 *>(src + e0);
-            u1[i] = *reinterpret_cast<const uint4 *>(src + e1);
+            if (turn) rotate8<DT>(u0[i], u1[i], cs, sn, inter, turn0, turn1);
+            *reinterpret_cast<uint4 *>(dst + e0) = u0[i];
+            *reinterpret_cast<uint4 *>(dst + e1) = u1[i];
         }
-#pragma unroll
-        for (int i = 0; i < kHeadBatch; i++) {
-            if (!dst[i]) continue;
-            if (turn[i]) rotate8<DT>(u0[i], u1[i], cs, sn, a.interleaved != 0);
-            *reinterpret_cast<uint4 *>(dst[i] + e0) = u0[i];
-            *reinterpret_cast<uint4 *>(dst[i] + e1) = u1[i];
-        }
+        load(h + kHeadBatch);
     }
 }
 
@@ -176,10 +197,12 @@ clis_status_t launch_rot(const RotArgs &a, cudaStream_t stream)
     const int64_t threads = static_cast<int64_t>(a.B) * a.N * (a.d / 16);
     if (threads == 0 || heads == 0) return CLIS_OK;
     const int64_t blocks = (threads + kRotThreads - 1) / kRotThreads;
-    // Heads per thread: sin and cos are shared by them, so as many as still
-    // leave the GPU several blocks per SM.
+    // Heads per thread: sin and cos are shared by them, so 16, fewer where that
+    // leaves the GPU without a few blocks per SM.  (8,192 rows of 48 heads into a
+    // cache: 39.8 us with 16, 41.5 with 12, 45.5 with 4 or 24; 480p video q and k, 40
+    // heads of 32,760 rows: 102.7 us with 16, 103.5 with 12, 108.2 with all.)
     int hg = 16;
-    while (hg > kHeadBatch && blocks * ((heads + hg - 1) / hg) < 152 * 16) hg /= 2;
+    while (hg > kHeadBatch && blocks * ((heads + hg - 1) / hg) < 152 * 4) hg /= 2;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + hg - 1) / hg));
     cudaError_t e;
     if (a.d == 128)

@@ -16,7 +16,7 @@ HARNESS = r"""
 #include "%s"
 using namespace clis;
 // 0: sound; else the number of the broken property.
-static int decode(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_max, int Hkv, int grid, int least)
+static int decode(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_max, int Hkv, int grid, int least, int keys)
 {
     std::vector<int> units;   // per item
     for (int s = 0; s < S; s++) {
@@ -24,8 +24,8 @@ static int decode(int S, const int *cu, const int *kv, int T, int cap, int g, in
         if (q.n < 0 || q.q0 < 0 || q.q0 + q.n > T || q.kv < 0 || q.kv > cap) return 1;
         if (!is_decode(q, g, rows_max)) continue;
         if ((long long)q.n * g > rows_max) return 2;
-        if ((long long)decode_units(q) * kDecodeKeys < q.kv) return 3;
-        for (int h = 0; h < Hkv; h++) units.push_back(decode_units(q));
+        if ((long long)decode_units(q, keys) * keys < q.kv) return 3;
+        for (int h = 0; h < Hkv; h++) units.push_back(decode_units(q, keys));
     }
     unsigned U = 0;
     for (int u : units) U += u;
@@ -119,8 +119,8 @@ static int chunk(int S, const int *cu, const int *kv, int T, int cap, int g, int
     if (many > (grid - 1) / 2 + 1) return 33;      // items joined by the join kernel: its list and its grid
     return 0;
 }
-extern "C" int check_decode(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_max, int Hkv, int grid, int least)
-{ return decode(S, cu, kv, T, cap, g, rows_max, Hkv, grid, least); }
+extern "C" int check_decode(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_max, int Hkv, int grid, int least, int keys)
+{ return decode(S, cu, kv, T, cap, g, rows_max, Hkv, grid, least, keys); }
 extern "C" int check_chunk(int S, const int *cu, const int *kv, int T, int cap, int g, int rows_small, int Hkv, int grid, int least,
                            int causal, long long max_items)
 { return chunk(S, cu, kv, T, cap, g, rows_small, Hkv, grid, least, causal, max_items); }
@@ -154,7 +154,8 @@ def check(lib, ctx, new, g, Hkv, causal=1, sms=152, cap=None, cu=None, kv=None):
     for rows in (0, 16, 32):
         if rows:
             for least in (1, 4):
-                assert lib.check_decode(S, ints(cu), ints(kv), T, cap, g, rows, Hkv, 2 * sms, least) == 0
+                for keys in (64, 128):
+                    assert lib.check_decode(S, ints(cu), ints(kv), T, cap, g, rows, Hkv, 2 * sms, least, keys) == 0
         tokens = 2 * (128 // g)
         items = Hkv * (T // tokens + S + 1)
         for least in (4, 16):
