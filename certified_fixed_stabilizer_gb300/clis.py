@@ -798,7 +798,9 @@ rope_qk = rope  # (for the functions that have an argument of that name)
 
 
 def rope_autograd(q, k, positions, inv_freq, axis, interleaved: bool = False):
-    """Differentiable :func:`rope` (training): the gradient is the rotation back."""
+    """Differentiable :func:`rope` (training): the gradient is the rotation back.
+    A backward pass may be captured in a graph while no eager graph of the same
+    leaves is alive (torch ties a leaf's gradient to the stream of its first use)."""
     return _native.rope_autograd(q, k, positions, inv_freq, axis, interleaved)
 
 

@@ -79,6 +79,10 @@ void check_like(const Tensor &t, const Tensor &like, const char *name)
                       name, " must have its input's shape, dtype and device and a contiguous last dimension");
 }
 
+// Stride of a dimension; one of size 1 is never stepped over, and torch leaves
+// anything in its stride: it gets the row length, which passes every check.
+int64_t st(const Tensor &t, int64_t i) { return t.size(i) == 1 ? t.size(t.dim() - 1) : t.stride(i); }
+
 Tensor empty_as(const Tensor &t) { return at::empty(t.sizes(), t.options().requires_grad(false)); }
 
 // -------------------------------------------------------------------- rotary
@@ -121,11 +125,11 @@ Rotated rope(const Tensor &q, const std::optional<Tensor> &k, const Tensor &posi
     d.axes = positions.size(-1);
     d.interleaved = interleaved;
     d.inverse = inverse;
-    d.q_sb = q.stride(0), d.q_sh = q.stride(1), d.q_sn = q.stride(2);
-    d.qo_sb = r.q.stride(0), d.qo_sh = r.q.stride(1), d.qo_sn = r.q.stride(2);
+    d.q_sb = st(q, 0), d.q_sh = st(q, 1), d.q_sn = st(q, 2);
+    d.qo_sb = st(r.q, 0), d.qo_sh = st(r.q, 1), d.qo_sn = st(r.q, 2);
     if (k) {
-        d.k_sb = k->stride(0), d.k_sh = k->stride(1), d.k_sn = k->stride(2);
-        d.ko_sb = r.k.stride(0), d.ko_sh = r.k.stride(1), d.ko_sn = r.k.stride(2);
+        d.k_sb = st(*k, 0), d.k_sh = st(*k, 1), d.k_sn = st(*k, 2);
+        d.ko_sb = st(r.k, 0), d.ko_sh = st(r.k, 1), d.ko_sn = st(r.k, 2);
     }
     d.p_sb = shared || positions.size(0) == 1 ? 0 : positions.stride(0);
     d.p_sn = positions.stride(-2), d.p_sa = positions.stride(-1);
@@ -161,8 +165,13 @@ struct RopeNode : torch::autograd::Function<RopeNode> {
         const bool interleaved = ctx->saved_data["interleaved"].toBool(), inverse = ctx->saved_data["inverse"].toBool();
         torch::autograd::variable_list out(7);
         std::vector<std::pair<int, Tensor>> need;
-        for (size_t i = 0; i < grads.size(); i++)
-            if (grads[i].defined()) need.emplace_back(static_cast<int>(i), grads[i].contiguous());
+        for (size_t i = 0; i < grads.size(); i++) {
+            if (!grads[i].defined() || !ctx->needs_input_grad(i)) continue;
+            // Gradients come in any layout: expanded, or a contiguous piece at an odd offset.
+            Tensor g = grads[i].contiguous();
+            if (reinterpret_cast<uintptr_t>(g.data_ptr()) & 15) g = g.clone();
+            need.emplace_back(static_cast<int>(i), g);
+        }
         if (need.empty()) return out;
         const std::optional<Tensor> second = need.size() > 1 ? std::optional<Tensor>(need[1].second) : std::nullopt;
         if (at::GradMode::is_enabled()) {
@@ -232,8 +241,8 @@ clis_paged_t cache_desc(const Tensor &kc, const Tensor &vc, const Tensor &like)
     d.page_size = kc.size(2);
     d.num_pages = kc.size(0);
     d.width = 1;
-    d.kc_sp = kc.stride(0), d.kc_sh = kc.stride(1), d.kc_sn = kc.stride(2);
-    d.vc_sp = vc.stride(0), d.vc_sh = vc.stride(1), d.vc_sn = vc.stride(2);
+    d.kc_sp = st(kc, 0), d.kc_sh = st(kc, 1), d.kc_sn = st(kc, 2);
+    d.vc_sp = st(vc, 0), d.vc_sh = st(vc, 1), d.vc_sn = st(vc, 2);
     d.dtype = dtype_of(like);
     return d;
 }
@@ -260,7 +269,7 @@ std::optional<Tensor> append(const Tensor &k, const Tensor &v, const Tensor &kc,
     r.N = T;
     r.d = d;
     r.dtype = desc.dtype;
-    r.k_sh = k.stride(1), r.k_sn = k.stride(0);
+    r.k_sh = st(k, 1), r.k_sn = st(k, 0);
     if (q) {
         TORCH_CHECK_VALUE(positions.has_value(), "q is rotated: positions are needed");
         TORCH_CHECK_VALUE(q->dim() == 3 && q->size(0) == T && q->size(2) == d && q->scalar_type() == k.scalar_type() &&
@@ -269,8 +278,8 @@ std::optional<Tensor> append(const Tensor &k, const Tensor &v, const Tensor &kc,
         desc.H = r.Hq = q->size(1);
         if (q_out) check_like(*q_out, *q, "q_out");
         else q_out = empty_as(*q);
-        r.q_sh = q->stride(1), r.q_sn = q->stride(0);
-        r.qo_sh = q_out->stride(1), r.qo_sn = q_out->stride(0);
+        r.q_sh = st(*q, 1), r.q_sn = st(*q, 0);
+        r.qo_sh = st(*q_out, 1), r.qo_sn = st(*q_out, 0);
     }
     if (positions) {
         TORCH_CHECK_VALUE((positions->dim() == 1 || positions->dim() == 2) && positions->size(0) == T,
@@ -285,7 +294,7 @@ std::optional<Tensor> append(const Tensor &k, const Tensor &v, const Tensor &kc,
         r.p_sa = positions->dim() == 2 ? positions->stride(1) : 0;
     }
     ok("clis_paged_append",
-       clis_paged_append(&desc, &r, q ? q->data_ptr() : nullptr, k.data_ptr(), v.data_ptr(), v.stride(0), v.stride(1),
+       clis_paged_append(&desc, &r, q ? q->data_ptr() : nullptr, k.data_ptr(), v.data_ptr(), st(v, 0), st(v, 1),
                          q ? q_out->data_ptr() : nullptr, kc.data_ptr(), vc.data_ptr(),
                          static_cast<const int64_t *>(slots.data_ptr()),
                          positions ? static_cast<const int32_t *>(positions->data_ptr()) : nullptr,
@@ -314,8 +323,8 @@ Tensor attention(const Tensor &q, const Tensor &kc, const Tensor &vc, const Tens
     Place at_(q, raw);
     if (out) check_like(*out, q, "out");
     else out = empty_as(q);
-    d.q_st = q.stride(0), d.q_sh = q.stride(1);
-    d.o_st = out->stride(0), d.o_sh = out->stride(1);
+    d.q_st = st(q, 0), d.q_sh = st(q, 1);
+    d.o_st = st(*out, 0), d.o_sh = st(*out, 1);
     size_t need = 0;
     ok("clis_attn_paged_workspace_size", clis_attn_paged_workspace_size(&d, max_q, &need));
     if (!workspace) {

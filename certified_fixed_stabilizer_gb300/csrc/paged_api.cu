@@ -10,6 +10,9 @@ namespace {
 
 constexpr int64_t kMaxN = (int64_t(1) << 31) - 1024;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
+// Keys of a sequence: a block works on at most one item's at a time, 1.5 us per 128
+// of them, while other warps wait for it with a limit of 2 s.
+constexpr int64_t kMaxKeys = int64_t(1) << 26;
 constexpr int64_t kMaxSeqs = 16384;
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -91,7 +94,7 @@ clis_status_t check_table(const clis_paged_t *p)
     if (p->S < 0 || p->T < 0 || p->width < 1 || p->num_pages < 1 || p->bt_ss < 0 || p->page_size < 1)
         return CLIS_ERR_INVALID_ARG;
     if (page_shift(p->page_size) < 0 || p->S > kMaxSeqs || p->T > kMaxTokens || p->num_pages > kMaxN) return CLIS_ERR_UNSUPPORTED;
-    if (p->width > kMaxTokens / p->page_size || p->bt_ss >= (int64_t(1) << 38)) return CLIS_ERR_UNSUPPORTED;
+    if (p->width > kMaxKeys / p->page_size || p->bt_ss >= (int64_t(1) << 38)) return CLIS_ERR_UNSUPPORTED;
     return CLIS_OK;
 }
 

@@ -505,7 +505,8 @@ CLIS_API clis_status_t clis_rope(const clis_rope_t *desc, const void *q, const v
  *   H, Hkv     query and key/value heads, H a multiple of Hkv, H / Hkv <= 128
  *   d          64 or 128
  *   page_size  a power of two, 8 .. 65536
- *   width      block-table columns
+ *   width      block-table columns; width * page_size (keys of a sequence, at
+ *              most) up to 2^26
  * Lengths, tables, slots and page numbers live on the device, so one captured
  * graph serves every step; what is out of range there is not followed: it sets
  * a bit in the device error word (CLIS_PAGED_*) and reads as zeros, is not
@@ -550,8 +551,8 @@ typedef struct {
  *   positions    int32 out [T]: the token's place in its sequence (0 behind the last)
  * Outputs must not overlap each other or the inputs.  The same inputs give the
  * same outputs bit for bit.  One launch.  Errors: CLIS_ERR_INVALID_ARG (null
- * pointers, sizes, state_out == state_in), CLIS_ERR_UNSUPPORTED (S > 16384, T or
- * width * page_size beyond 2^30), CLIS_ERR_MISALIGNED. */
+ * pointers, sizes, state_out == state_in), CLIS_ERR_UNSUPPORTED (S > 16384, T
+ * beyond 2^30), CLIS_ERR_MISALIGNED. */
 CLIS_API clis_status_t clis_paged_plan(const clis_paged_t *desc, const int32_t *ctx_len, const int32_t *new_len,
                                        int32_t *block_table, int32_t *ring, int64_t ring_size, const int64_t *state_in,
                                        int64_t *state_out, int32_t *cu_q, int32_t *kv_len, int64_t *slots,
@@ -584,9 +585,10 @@ CLIS_API clis_status_t clis_attn_paged_workspace_size(const clis_paged_t *desc, 
  * tokens are the last of the kv_len[s] tokens:
  *   o_i = sum_j 2^(x_ij) v_j / sum_j 2^(x_ij),  x_ij = scale_log2 * q_i . k_j,
  * over the keys j < kv_len[s] of head h / (H / Hkv) and, if causal, j <= kv_len[s] - n
- * + i.  Any mix of single tokens, drafted tokens and long chunks is one call;
+ * + i.  Any mix of single tokens, drafted tokens and long chunks is one call:
  * sequences of few rows (n * H / Hkv up to 16, or 32) run a kernel bound by the
- * cache's bytes, the others one bound by the tensor cores.  The softmax is
+ * cache's bytes, the others one bound by the tensor cores (which takes them all
+ * where the batch is small).  The softmax is
  * online with a lazily raised shift, as CLIS_ONLINE_LAZY: a certificate would
  * have to read all keys first, which for a few query rows is the whole cost.
  *   q          device [T, H, d] (q_st, q_sh)

@@ -148,6 +148,42 @@ def test_a_key_that_is_not_finite_seen_by_all():
         assert torch.isnan(o.float()).all() and torch.isnan(lse2).all()
 
 
+def test_many_sequences():
+    """More sequences than threads of the kernels that list the work."""
+    new = [1 if i % 3 else 0 for i in range(1100)]
+    b = make_batch([(7 * i) % 90 for i in range(1100)], new, 4, 2, 64, 8, BF, seed=37)
+    check_attention(*run(b), b, what="single tokens")
+    new[550] = 40
+    new[1099] = 33
+    b = make_batch([(7 * i) % 90 for i in range(1100)], new, 4, 2, 64, 8, BF, seed=38)
+    check_attention(*run(b), b, what="with chunks")
+
+
+@pytest.mark.parametrize("Hkv,g,n,ctx,dtype", [(8, 4, 640, 8000, BF), (4, 2, 1200, 5000, FP), (1, 8, 60, 30000, BF),
+                                               (2, 4, 500, 20000, BF), (16, 8, 16, 3000, BF), (8, 4, 9, 60000, FP)])
+def test_parts_join_alike_whoever_is_last(Hkv, g, n, ctx, dtype):
+    """Items as long as one to many blocks' runs: their parts end at about the same time, and reruns
+    agree bit for bit whichever block joins them."""
+    b = make_batch([ctx], [n], Hkv * g, Hkv, 128, 64, dtype, seed=41)
+    o, lse2 = run(b)
+    check_attention(o, lse2, b)
+    for _ in range(20):
+        o2, l2 = run(b)
+        assert torch.equal(o, o2) and torch.equal(lse2, l2)
+
+
+def test_sizes_of_one_with_odd_strides():
+    """Dimensions of size 1 whose strides are not multiples of anything (torch leaves them as they are)."""
+    b = make_batch([37], [1], 2, 1, 64, 16, BF, seed=43)
+    want, _ = run(b)
+    q = torch.empty(7 + 128, dtype=BF, device="cuda")[:128].as_strided((1, 2, 64), (3, 64, 1))
+    q.copy_(b["q"])
+    kc = b["k_cache"].as_strided(b["k_cache"].shape, (b["k_cache"].stride(0), 5, 64, 1))
+    vc = b["v_cache"].as_strided(b["v_cache"].shape, (b["v_cache"].stride(0), 1, 64, 1))
+    got, _ = run({**b, "q": q, "k_cache": kc, "v_cache": vc})
+    assert torch.equal(got, want)
+
+
 def test_max_q_only_chooses_the_kernel():
     """The decode kernel's and the chunk kernel's results agree to rounding; T is always a valid max_q."""
     b = make_batch([300, 900, 64], [1, 2, 1], 8, 2, 128, 16, BF, seed=13)

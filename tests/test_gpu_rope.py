@@ -148,6 +148,71 @@ def test_gradients(interleaved):
     assert torch.allclose(one.double(), dk.double().sum(1, keepdim=True), rtol=2 ** -7, atol=2 ** -6)
 
 
+def test_gradients_in_odd_layouts():
+    """A gradient that is a contiguous piece at an odd offset, one that is expanded, none at all; inputs
+    that need none."""
+    q0 = torch.randn(1, 2, 5, 64, device="cuda").to(BF)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")[:, None]
+    inv, axis = table(32, 1)
+    big = torch.randn(2 * 5 * 64 + 1, device="cuda").to(BF)
+    odd = big[1:].reshape(1, 2, 5, 64)
+    q, k = q0.clone().requires_grad_(), q0.clone()
+    yq, yk = clis.rope_autograd(q, k, pos, inv, axis)
+    (dq,) = torch.autograd.grad(yq, q, odd)
+    check(dq, turned(odd, pos, inv, axis, False, -1.0), odd)
+    q, k = q0.clone().requires_grad_(), q0.clone().requires_grad_()
+    yq, yk = clis.rope_autograd(q, k, pos, inv, axis)
+    dq, dk = torch.autograd.grad(yk, (q, k), odd.expand(1, 2, 5, 64), allow_unused=True)
+    assert dq is None
+    check(dk, turned(odd, pos, inv, axis, False, -1.0), odd)
+    with torch.no_grad():
+        y, _ = clis.rope_autograd(q, None, pos, inv, axis)
+    assert not y.requires_grad
+
+
+def test_not_finite_elements_stay_in_their_pairs():
+    """An inf or NaN reaches its own pair and nothing else, the elements that pass through least of all."""
+    inv, axis = table(16, 1)
+    pos = torch.arange(1, 4, dtype=torch.int32, device="cuda")[:, None]
+    for inter in (False, True):
+        x = torch.ones(1, 1, 3, 64, device="cuda").to(BF)
+        x[..., 40] = float("inf")
+        x[..., 3] = float("nan")
+        y, _ = clis.rope(x, None, pos, inv, axis, inter)
+        mate = 2 if inter else 19
+        bad = {3, mate, 40}
+        rest = [c for c in range(64) if c not in bad]
+        assert torch.isfinite(y[..., rest].float()).all() and torch.isnan(y[..., [3, mate]].float()).all()
+        assert torch.isinf(y[..., 40].float()).all()
+
+
+def test_training_step_captured():
+    """Forward and backward of the rotation in one captured graph (no eager graph of the leaf alive: torch
+    would tie the leaf's gradient to that graph's stream, which is not being captured)."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q = torch.randn((1, 4, 33, 64), generator=g, device="cuda").to(BF).requires_grad_()
+    gq = torch.randn((1, 4, 33, 64), generator=g, device="cuda").to(BF)
+    pos = torch.arange(33, dtype=torch.int32, device="cuda")[:, None]
+    inv, axis = table(32, 1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            y, _ = clis.rope_autograd(q, None, pos, inv, axis)
+            torch.autograd.grad(y, q, gq)
+            del y
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, _ = clis.rope_autograd(q, None, pos, inv, axis)
+        (dq,) = torch.autograd.grad(y, q, gq)
+    pos.add_(5)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(y.detach(), turned(q.detach(), pos, inv, axis, False), q.detach())
+    check(dq, turned(gq, pos, inv, axis, False, -1.0), gq)
+
+
 def test_attention_with_rope():
     """attention and attention_autograd rotate q and k first."""
     g = torch.Generator(device="cuda").manual_seed(5)

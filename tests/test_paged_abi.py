@@ -72,7 +72,7 @@ def test_rope_refusals():
 TABLE = [(dict(S=-1), INVALID), (dict(T=-1), INVALID), (dict(width=0), INVALID), (dict(num_pages=0), INVALID),
          (dict(page_size=0), INVALID), (dict(page_size=4), UNSUPPORTED), (dict(page_size=24), UNSUPPORTED),
          (dict(page_size=1 << 17), UNSUPPORTED), (dict(S=16385), UNSUPPORTED), (dict(T=(1 << 30) + 1), UNSUPPORTED),
-         (dict(width=1 << 27), UNSUPPORTED), (dict(num_pages=1 << 31), UNSUPPORTED), (dict(bt_ss=-8), INVALID)]
+         (dict(width=(1 << 22) + 1, bt_ss=1 << 23), UNSUPPORTED), (dict(num_pages=1 << 31), UNSUPPORTED), (dict(bt_ss=-8), INVALID)]
 
 
 def test_plan_refusals():
@@ -118,7 +118,7 @@ def test_attention_refusals():
         assert attn(paged_desc(**kw)) == st, kw
     for kw, st in ((dict(q_st=64), INVALID), (dict(q_st=516), MISALIGNED), (dict(o_sh=0), INVALID), (dict(o_st=0), INVALID),
                    (dict(o_st=256), INVALID), (dict(o_sh=64), INVALID), (dict(H=258, Hkv=2, o_st=1 << 20), UNSUPPORTED),
-                   (dict(S=16384, Hkv=4096, H=4096, o_st=1 << 20, width=1 << 20, bt_ss=1 << 20), UNSUPPORTED)):
+                   (dict(S=16384, Hkv=4096, H=4096, o_st=1 << 20, width=1 << 20, bt_ss=1 << 20, kc_sp=1 << 24, vc_sp=1 << 24), UNSUPPORTED)):
         assert attn(paged_desc(**kw)) == st, kw
     assert attn(paged_desc(), max_q=0) == INVALID
     for scale in (0.0, -1.0, float("inf"), float("nan")):
