@@ -420,6 +420,9 @@ __device__ void edge_role(const ChunkParams &p, Ctl &c, uint32_t sKV, const Run 
     {
         const ChunkItem &T = K.t;
         const int first = chunk_first_masked(T, p.a.causal != 0);
+        // Keys that all rows, and that some row of the item sees.
+        const int lim_all = visible_keys(T.n, T.kv, T.tok0, p.a.causal);
+        const int lim_any = visible_keys(T.n, T.kv, min(T.n, T.tok0 + 2 * p.tpt) - 1, p.a.causal);
         bool dirty = false;
         for (int j = 0; j < K.n; j++) {
             const int kt = K.start + j;
@@ -435,30 +438,31 @@ __device__ void edge_role(const ChunkParams &p, Ctl &c, uint32_t sKV, const Run 
             ++nedge;
             if (!mbar_wait_warp(smem_u32(&c.kv_full[grp % C::NSTAGE]), (grp / C::NSTAGE) & 1, ab, err, kErrEdge)) return;
             const uint32_t base = sKV + (vs % C::NSTAGE) * C::TILE_BYTES;
-            const int live = min(BN, T.kv - kt * BN);  // rows that hold keys (may be <= 0)
-            // Rows of 128 bytes, two boxes at d = 128; the swizzle permutes 16-byte
-            // pieces within a row, so a row is a row.
-            if (p.a.causal) {
-#pragma unroll 4
-                for (int i = lane; i < C::NBOX * BN * 8; i += 32) {
-                    const int row = (i >> 3) & (BN - 1);
-                    const uint32_t at = base + i * 16;
-                    if (row < live) {
-                        uint4 u = lds128(at);
-                        const bool d0 = scrub<DT>(u.x), d1 = scrub<DT>(u.y), d2 = scrub<DT>(u.z), d3 = scrub<DT>(u.w);
+            // Rows [0, lo) are keys that every row of the item sees: left alone.  Rows [lo, hi)
+            // are seen by some: scrubbed.  Rows from hi on are seen by none, or hold no key:
+            // zeros.  (One warp: only what has to be touched is.  Going over all of the tile
+            // took 4 us, in every item.)
+            const int lo = min(max(lim_all - kt * BN, 0), BN), hi = min(max(lim_any - kt * BN, lo), BN);
+            // (the swizzle permutes 16-byte pieces within a 128-byte row: a row is a row)
+            for (int bx = 0; bx < C::NBOX; bx++) {
+                const uint32_t box = base + bx * C::BOX_BYTES;
+                for (int i0 = lo * 8; i0 < hi * 8; i0 += 4 * 32) {
+                    uint4 u[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (i0 + e * 32 + lane < hi * 8) u[e] = lds128(box + (i0 + e * 32 + lane) * 16);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        if (i0 + e * 32 + lane >= hi * 8) continue;
+                        const bool d0 = scrub<DT>(u[e].x), d1 = scrub<DT>(u[e].y), d2 = scrub<DT>(u[e].z), d3 = scrub<DT>(u[e].w);
                         if (d0 | d1 | d2 | d3) {
-                            sts128(at, u);
+                            sts128(box + (i0 + e * 32 + lane) * 16, u[e]);
                             dirty = true;
                         }
-                    } else {
-                        sts128(at, make_uint4(0u, 0u, 0u, 0u));
                     }
                 }
-            } else {
-                const int from = max(live, 0) * 8;
-                for (int bx = 0; bx < C::NBOX; bx++)
-                    for (int i = from + lane; i < BN * 8; i += 32)
-                        sts128(base + bx * C::BOX_BYTES + i * 16, make_uint4(0u, 0u, 0u, 0u));
+#pragma unroll 4
+                for (int i = hi * 8 + lane; i < BN * 8; i += 32) sts128(box + i * 16, make_uint4(0u, 0u, 0u, 0u));
             }
             const bool any = __any_sync(~0u, dirty);
             if (lane == 0) {
@@ -919,6 +923,27 @@ __device__ void epilogue_role(const ChunkParams &p, Ctl &c, uint32_t tmem, uint3
             if (row_ok && a.lse2) a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
         };
 
+        // Row sum and shift of row tile t (a single row tile's: of both groups).
+        auto row_sums = [&](int t, float &l, float &shift) {
+            l = c.epi_l[t][rl];
+            shift = c.epi_shift[t][rl];
+            if (single) {
+                const float l1 = c.epi_l[1][rl], m1 = c.epi_shift[1][rl];
+                const float M = l == 0.f ? m1 : l1 == 0.f ? shift : fmaxf(shift, m1);
+                has_odd = K.n > 1;
+                w_even = l == 0.f ? 0.f : ex2_approx(shift - M);  // (a group none of whose keys the row sees adds nothing)
+                w_odd = l1 == 0.f ? 0.f : ex2_approx(m1 - M);
+                l = (l == 0.f ? 0.f : w_even * l) + (l1 == 0.f ? 0.f : w_odd * l1);
+                shift = M;
+            }
+        };
+        // Non-finite values of keys from here on that a row sees were left out of the
+        // product (-1: none were); to be asked once the products are done.
+        auto left_out = [&]() -> int {
+            return edges && *reinterpret_cast<volatile int *>(&c.dirty[w & 7]) != 0 ? max(first, K.start) * BN : -1;
+        };
+        auto seen = [&](int tok) { return min(visible_keys(T.n, T.kv, tok, a.causal), (K.start + K.n) * BN); };
+
 #pragma unroll 1
         for (int t = 0; t < T.nt; t++) {
             bool ok;
@@ -938,91 +963,76 @@ __device__ void epilogue_role(const ChunkParams &p, Ctl &c, uint32_t tmem, uint3
             // stay at the barriers of a later item.
             if (epilogue_any(!ok)) return;
             tc_fence_after();
-            const bool dirty = edges && *reinterpret_cast<volatile int *>(&c.dirty[w & 7]) != 0;
+            if (direct) continue;  // (below, with both row tiles done)
             const uint32_t tO = tmem + (t ? C::TM_O1 : C::TM_O0) + lane_off;
             const int tok = T.tok0 + t * p.tpt + row_tok;
             const bool row_ok = row_tok < p.tpt && tok < T.n;
-            float l = c.epi_l[t][rl], shift = c.epi_shift[t][rl];
-            if (single) {
-                const float l1 = c.epi_l[1][rl], m1 = c.epi_shift[1][rl];
-                const float M = l == 0.f ? m1 : l1 == 0.f ? shift : fmaxf(shift, m1);
-                has_odd = K.n > 1;
-                w_even = l == 0.f ? 0.f : ex2_approx(shift - M);  // (a group none of whose keys the row sees adds nothing)
-                w_odd = l1 == 0.f ? 0.f : ex2_approx(m1 - M);
-                l = (l == 0.f ? 0.f : w_even * l) + (l1 == 0.f ? 0.f : w_odd * l1);
-                shift = M;
-            }
-            // Non-finite values of keys from key_from on that the row sees were left out of
-            // the product (-1: none were).
-            const int key_from = dirty ? max(first, K.start) * BN : -1;
-            const int see = row_ok ? min(visible_keys(T.n, T.kv, tok, a.causal), (K.start + K.n) * BN) : 0;
-            if (direct) {
-                if (t == 0) {
-                    // The block's last work: once every product is done the K/V ring is free,
-                    // and the other part is staged there, each thread its own row.
-                    if (T.nt == 2) {
-                        const bool ok1 = mbar_wait(smem_u32(&c.epi_full[1]), w & 1, ab, err, kErrEpilogue) &&
-                                         mbar_wait(smem_u32(&c.pv_done[1]), (g1 + K.n - 1) & 1, ab, err, kErrEpilogue);
-                        if (epilogue_any(!ok1)) return;
-                    }
-                    for (int u = 0; u < T.nt; u++) {
-                        const int rtok = T.tok0 + u * p.tpt + row_tok;
-                        if (row_tok >= p.tpt || rtok >= T.n) continue;  // never written
-#pragma unroll 8
-                        for (int c4 = 0; c4 < D / 4; c4++)
-                            cp_async16(sKV + ((u * (D / 4) + c4) * BM + rl) * 16, part_at<D>(p, slot1, c4, u * BM + rl));
-                    }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                }
-                join_rows(t, sKV, l, shift, key_from, see);
-            } else {
-                const int hd = T.h * p.g + row_head;
-                const float inv = 1.f / l;
-                uint16_t *orow = a.o + static_cast<int64_t>(T.q0 + tok) * a.o_st + hd * a.o_sh;
+            float l, shift;
+            row_sums(t, l, shift);
+            const int key_from = left_out();
+            const int see = row_ok ? seen(tok) : 0;
+            const int hd = T.h * p.g + row_head;
+            const float inv = 1.f / l;
+            uint16_t *orow = a.o + static_cast<int64_t>(T.q0 + tok) * a.o_st + hd * a.o_sh;
 #pragma unroll 1
-                for (int c16 = 0; c16 < D / 16; c16++) {
-                    float o[16];
-                    own16(tO, c16, o);
-                    if (c16 == D / 16 - 1) {  // O has been read: the next item's products may start
-                        tc_fence_before();
-                        mbar_arrive(smem_u32(&c.o_free[t]));
-                        if (single) mbar_arrive(smem_u32(&c.o_free[1]));
-                    }
-                    if (!row_ok) continue;
-                    if (key_from >= 0) add_not_finite<DT>(o, T, key_from, see, c16 * 16, p);
-                    if (to_memory) {
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            __stcg(part_at<D>(p, slot, c16 * 4 + e, t * BM + rl),
-                                   make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
-                    } else {
-                        store16<DT>(orow + c16 * 16, o, inv, l == 0.f, pol);
-                    }
+            for (int c16 = 0; c16 < D / 16; c16++) {
+                float o[16];
+                own16(tO, c16, o);
+                if (c16 == D / 16 - 1) {  // O has been read: the next item's products may start
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&c.o_free[t]));
+                    if (single) mbar_arrive(smem_u32(&c.o_free[1]));
                 }
-                if (row_ok) {
-                    if (to_memory)
-                        __stcg(p.part_ml + slot * (2 * BM) + t * BM + rl, make_float2(shift, l));
-                    else if (a.lse2)
-                        a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : shift + log2f(l);
+                if (!row_ok) continue;
+                if (key_from >= 0) add_not_finite<DT>(o, T, key_from, see, c16 * 16, p);
+                if (to_memory) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        __stcg(part_at<D>(p, slot, c16 * 4 + e, t * BM + rl),
+                               make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                } else {
+                    store16<DT>(orow + c16 * 16, o, inv, l == 0.f, pol);
                 }
             }
-            if (direct) {  // (the block's last item: nobody waits for it any more)
-                tc_fence_before();
-                mbar_arrive(smem_u32(&c.o_free[t]));
-                if (single) mbar_arrive(smem_u32(&c.o_free[1]));
+            if (row_ok) {
+                if (to_memory)
+                    __stcg(p.part_ml + slot * (2 * BM) + t * BM + rl, make_float2(shift, l));
+                else if (a.lse2)
+                    a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : shift + log2f(l);
             }
         }
+        // Who joins two parts: this block if the other part is done.
+        bool joins = direct;
         if (to_memory && own.count == 2) {
-            // Announce the part; the block that completes the count joins them all.
             __threadfence();
             epilogue_barrier();
             if (lead) c.last = atomicAdd(p.arrived + own.c, 1) == 1;
             epilogue_barrier();
-            if (c.last) {
-                __threadfence();
-                for (int t = 0; t < T.nt; t++) join_rows(t, 0u, 0.f, 0.f, -1, 0);
-            }
+            joins = c.last != 0;
+            if (joins) __threadfence();
             epilogue_barrier();
+        }
+        if (joins && me == 0) {
+            // The block's last work: its own part is still in TMEM, and the K/V ring, free
+            // after the last product, takes the other part, each thread its own row.
+            tc_fence_after();
+            for (int t = 0; t < T.nt; t++) {
+                if (row_tok >= p.tpt || T.tok0 + t * p.tpt + row_tok >= T.n) continue;  // never written
+#pragma unroll 8
+                for (int c4 = 0; c4 < D / 4; c4++)
+                    cp_async16(sKV + ((t * (D / 4) + c4) * BM + rl) * 16, part_at<D>(p, slot1, c4, t * BM + rl));
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+            for (int t = 0; t < T.nt; t++) {
+                const int tok = T.tok0 + t * p.tpt + row_tok;
+                float l, shift;
+                row_sums(t, l, shift);
+                join_rows(t, sKV, l, shift, left_out(), row_tok < p.tpt && tok < T.n ? seen(tok) : 0);
+            }
+        } else if (joins) {
+#pragma unroll 1
+            for (int t = 0; t < T.nt; t++) join_rows(t, 0u, 0.f, 0.f, -1, 0);
         }
         ++w;
     }
