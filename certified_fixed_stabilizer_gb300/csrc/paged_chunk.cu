@@ -60,7 +60,7 @@ constexpr int BM = kChunkRows, BN = kChunkKeys;
 constexpr int kThreads = 512;
 constexpr int kNStageMax = 8;
 constexpr float kTau = 8.0f;
-constexpr int kSchedThreads = 512;
+constexpr int kSchedThreads = 256;
 // Items of three parts or more: every block but the last adds at most one part to
 // the items' number, so there are at most (grid - 1) / 2 of them.
 int max_joins(int grid) { return (grid - 1) / 2 + 1; }
@@ -695,7 +695,8 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
                 for (int cc = 0; cc < BN; cc++)
                     if (key0 + cc >= lim) s[cc] = 0xFF800000u;  // -inf
             }
-            float l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
+            float l = 0.f;
+            if (begun) l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int cc = 0; cc < BN; cc += 8) {
@@ -705,8 +706,8 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
             }
             const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
             const bool grow = m_tile > m_run + kTau;  // always true where a row's first visible key is
-            if (__any_sync(0xFFFFFFFFu, grow)) {
-                // Raise the shift, compute the tile's weights again, and shrink O once the
+            if (__any_sync(0xFFFFFFFFu, grow) || !begun) {
+                // Raise the shift, compute the tile's weights (again), and shrink O once the
                 // last product is in it.
                 const float alpha = grow ? ex2_approx(m_run - m_tile) : 1.f;
                 if (grow) m_run = m_tile;

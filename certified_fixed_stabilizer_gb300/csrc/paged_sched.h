@@ -137,19 +137,25 @@ struct ChunkCuts {
     CLIS_HD uint64_t cut(int c) const { return run * c + rem * static_cast<uint32_t>(c) / blocks; }  // rem c < blocks^2
 };
 
+// (64-bit division is slow on the GPU, and costs are mostly below 2^32)
+CLIS_HD uint64_t chunk_div(uint64_t a, uint64_t b)
+{
+    return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 CLIS_HD ChunkCuts chunk_cuts(uint64_t U, int blocks)
 {
     ChunkCuts k;
     k.blocks = blocks > 0 ? blocks : 1;
-    k.run = U / k.blocks;
-    k.rem = static_cast<uint32_t>(U % k.blocks);
+    k.run = chunk_div(U, k.blocks);
+    k.rem = static_cast<uint32_t>(U - k.run * k.blocks);
     return k;
 }
 
 // Block whose run holds place x < U.
 CLIS_HD int chunk_block_of(const ChunkCuts &k, uint64_t x)
 {
-    const uint64_t g = k.run > 0 ? x / k.run : x;
+    const uint64_t g = k.run > 0 ? chunk_div(x, k.run) : x;
     int c = static_cast<int>(g < k.blocks ? g : k.blocks - 1);
     while (c > 0 && k.cut(c) > x) c--;
     while (c + 1 < static_cast<int>(k.blocks) && k.cut(c + 1) <= x) c++;
