@@ -127,7 +127,7 @@ clis_status_t check_attn(const clis_paged_t *p, int64_t max_q)
     if (overlapping(p->d, od, 2)) return CLIS_ERR_INVALID_ARG;
     // Work units and tiles are counted in 32 bits.
     const double per = static_cast<double>(p->width) * static_cast<double>(p->page_size);
-    if (static_cast<double>(p->S) * static_cast<double>(p->Hkv) * (per / 64 + 1) >= 4.0e9)
+    if (static_cast<double>(p->S) * static_cast<double>(p->Hkv) * (per / 16 + 1) >= 4.0e9)
         return CLIS_ERR_UNSUPPORTED;
     const int64_t tpc = clis::chunk_tokens(static_cast<int>(p->H / p->Hkv));
     if (static_cast<double>(p->Hkv) * (static_cast<double>(p->T) / tpc + p->S + 1) >= 1.0e9) return CLIS_ERR_UNSUPPORTED;
@@ -170,7 +170,7 @@ Split split_of(const clis_paged_t *p, int64_t max_q, int nsm)
     const int g = static_cast<int>(p->H / p->Hkv);
     const int64_t mq = max_q < p->T ? max_q : p->T;
     Split s;
-    s.row_tiles = clis::paged_decode_row_tiles(mq, g);
+    s.row_tiles = clis::paged_decode_row_tiles(mq, g, static_cast<int>(p->d));
     s.chunk = mq * g > 16 * s.row_tiles;
     // A batch with chunks whose caches are small as a whole leaves its single tokens
     // to the chunk kernel too: at 12 sequences of up to 8,000 keys (d = 128, 8

@@ -12,21 +12,21 @@
 // what even the warp-level matrix instructions deliver, so the tensor cores of
 // the chunk kernel would gain nothing here.
 //
-//  * Work: paged_sched.h lays all items' 64-key units end to end and gives
-//    every block an equal run, so ragged lengths balance; an item that crosses
-//    a cut leaves partial results (unnormalised o, m, l) that
-//    paged_decode_join_kernel adds in a fixed order.
-//  * Loads: each of the block's four warps takes a quarter of a unit's keys (16 of
-//    64 at d = 128, 32 of 128 at d = 64: 8 KB either way) and runs its own ring of cp.async stages: no block-wide barrier inside an item, and
-//    the ring runs on into the next item, so item ends do not drain it.  Rows
-//    past the length are filled with zeros by the copy itself: what a page
-//    holds behind the last key is never multiplied (0 * NaN would be NaN).
+//  * Work: paged_sched.h lays all items' units (16 keys, 32 at d = 64) end to end
+//    and gives every warp an equal run, so ragged lengths balance; an item that
+//    crosses a cut leaves partial results (unnormalised o, m, l) that
+//    paged_decode_join_kernel adds in a fixed order.  A warp works alone: no
+//    barrier, and items that end inside its run are written from registers.
+//    (With a block of four warps per item, which then had to join its warps'
+//    results, 1,000 sequences of 70 keys took 140 us.)
+//  * Loads: each warp runs its own ring of cp.async stages of 8 KB, on into the next
+//    item, so item ends do not drain it.  Rows past the length are filled with
+//    zeros by the copy itself: what a page holds behind the last key is never
+//    multiplied (0 * NaN would be NaN).
 //  * P is rounded to the data type (bf16: off by up to 2^-8 of each weight) as
 //    the matrix instructions take it; the row sum adds the unrounded values,
 //    and o, m, l stay in fp32.
 #include <cuda_bf16.h>
-
-#include <type_traits>
 
 #include "clis_internal.h"
 #include "paged_internal.h"
@@ -45,25 +45,22 @@ constexpr int kJoinThreads = 512;
 
 template <int D>
 struct DCfg {
-    static constexpr int KEYS = decode_keys(D);         // per unit
-    static constexpr int TK = KEYS / kWarps;            // 16 or 32 keys per warp and unit
+    static constexpr int TK = decode_keys(D);           // keys per unit
     static constexpr int NST = 3;
     static constexpr int ROW = D * 2;                   // bytes of a row
     static constexpr int HALF = TK * ROW;               // K (or V) of a stage
     static constexpr int STAGE = 2 * HALF;
-    static constexpr int RING = kWarps * NST * STAGE;
-    static constexpr int OPITCH = D + 8;                // floats per row of the merge buffer
-    static constexpr int MERGE = 16 * OPITCH * 4;       // (also holds Q, see below)
-    static constexpr int SMEM = RING + MERGE;
+    static constexpr int SMEM = kWarps * NST * STAGE;
 };
 
 struct DecodeParams {
     PagedArgs a;
     int g, rows_max, least;
+    int workers;     // warps of the grid
     int strict;  // no chunk kernel follows: a sequence of more rows is an error
-    float *part_o;   // [2 * blocks][rows_max][D]
-    float2 *part_ml; // [2 * blocks][rows_max]
-    int4 *meta;      // [blocks] {parts, first row of q, new tokens, head} of the item the block starts and does not finish
+    float *part_o;   // [2 * workers][rows_max][D]: place 2 c + 1 if worker c starts the item, 2 c if it goes on with it
+    float2 *part_ml; // [2 * workers][rows_max]
+    int4 *meta;      // [workers] {parts, first row of q, new tokens, head} of the item the worker starts and does not finish
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
@@ -160,22 +157,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     const PagedArgs &a = p.a;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t s_sum[kWarps];
-    __shared__ int s_seq;
-    __shared__ uint32_t s_rel;
-    __shared__ float s_m[kWarps][MT * 16], s_l[kWarps][MT * 16];
+    __shared__ int s_seq[kWarps];
+    __shared__ uint32_t s_rel[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int c = blockIdx.x;
     unsigned int bad = 0;
     pdl_launch();
 
-    // ---- this block's run of units
+    // ---- the four warps' runs of units (neighbouring runs go to different blocks)
     const int per = (a.S + kThreads - 1) / kThreads;
     const int sb = min(a.S, tid * per), se = min(a.S, sb + per);
     uint32_t mine = 0;
     for (int s = sb; s < se; s++) {
         const SeqLen q = seq_len(a, s);
         if (q.bad) bad |= CLIS_PAGED_LENGTH_BIT;
-        if (is_decode(q, p.g, p.rows_max)) mine += static_cast<uint32_t>(a.Hkv) * decode_units(q, C::KEYS);
+        if (is_decode(q, p.g, p.rows_max)) mine += static_cast<uint32_t>(a.Hkv) * decode_units(q, C::TK);
         else if (p.strict && q.n > 0) bad |= CLIS_PAGED_LENGTH_BIT;
     }
     uint32_t incl = mine;
@@ -193,34 +188,40 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
         U += s_sum[w];
     }
     const uint32_t excl = before + incl - mine;
-    const int nb = decode_blocks(U, gridDim.x, p.least);
-    if (c >= nb) {  // nothing for this block (U = 0 included)
-        if (tid == 0) p.meta[c] = make_int4(0, 0, 0, 0);
-        if (bad && c == 0) atomicOr(&g_decode_error_word, bad);
+    const int nb = decode_workers(U, p.workers, p.least);
+    for (int w = 0; w < kWarps; w++) {
+        const int cw = w * gridDim.x + blockIdx.x;
+        if (cw >= nb) break;
+        const uint32_t u = decode_cut(U, nb, cw);
+        if (u < excl || u >= excl + mine) continue;
+        uint32_t rel = u - excl;
+        for (int s = sb; s < se; s++) {
+            const SeqLen q = seq_len(a, s);
+            if (!is_decode(q, p.g, p.rows_max)) continue;
+            const uint32_t n = static_cast<uint32_t>(a.Hkv) * decode_units(q, C::TK);
+            if (rel < n) {
+                s_seq[w] = s;
+                s_rel[w] = rel;
+                break;
+            }
+            rel -= n;
+        }
+    }
+    __syncthreads();
+    const int c = warp * gridDim.x + blockIdx.x;  // this worker
+    if (lane == 0) p.meta[c] = make_int4(0, 0, 0, 0);
+    if (bad && blockIdx.x == 0) atomicOr(&g_decode_error_word, bad);
+    bad = 0;
+    if (c >= nb) {  // nothing for this warp (U = 0 included)
         pdl_wait();
         return;
     }
     const uint32_t u0 = decode_cut(U, nb, c), u1 = decode_cut(U, nb, c + 1);
-    if (u0 >= excl && u0 < excl + mine) {
-        uint32_t rel = u0 - excl;
-        for (int s = sb; s < se; s++) {
-            const SeqLen q = seq_len(a, s);
-            if (!is_decode(q, p.g, p.rows_max)) continue;
-            const uint32_t w = static_cast<uint32_t>(a.Hkv) * decode_units(q, C::KEYS);
-            if (rel < w) {
-                s_seq = s;
-                s_rel = rel;
-                break;
-            }
-            rel -= w;
-        }
-    }
-    __syncthreads();
 
     Pos cur;
-    cur.set(a, s_seq);
-    cur.h = static_cast<int>(s_rel / cur.units);
-    cur.j = static_cast<int>(s_rel % cur.units);
+    cur.set(a, s_seq[warp]);
+    cur.h = static_cast<int>(s_rel[warp] / cur.units);
+    cur.j = static_cast<int>(s_rel[warp] % cur.units);
     cur.left = u1 - u0;
 
     // ---- loader: one stage per unit, `ld` runs NST - 1 units ahead of `cur`
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     int ld_stage = 0;
     // Page of the lane's key of the tile that the loader is at, read one unit ahead.
     auto page_at = [&](const Pos &q) -> int {
-        const int key = q.j * C::KEYS + warp * C::TK + (lane & (C::TK - 1));
+        const int key = q.j * C::TK + (lane & (C::TK - 1));
         if (q.left == 0 || key >= q.q.kv) return -2;  // nothing to load
         return __ldg(a.block_table + q.s * a.bt_s + (key >> a.page_shift));
     };
@@ -246,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                 page = -2;  // its keys read as zeros
             }
             const uint32_t dst = ring + ld_stage * C::STAGE;
-            const int key0 = ld.j * C::KEYS + warp * C::TK;
-#pragma unroll (MT * D == 256 ? 1 : NCP)
+            const int key0 = ld.j * C::TK;
+#pragma unroll
             for (int i = 0; i < NCP; i++) {
                 const int row = i * RPI + lrow;
                 const int pg = __shfl_sync(~0u, page, row);
@@ -273,9 +274,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     const float sl2 = a.scale_log2;
     const int r4 = lane >> 2, c2 = (lane & 3) * 2;
     int stage = 0;
-    float *merge = reinterpret_cast<float *>(smem + C::RING);
-
-    if (tid == 0 && c < nb) p.meta[c] = make_int4(0, 0, 0, 0);
 
     while (cur.left > 0) {
         // ---- one item, units j0 .. j1 - 1 of it
@@ -284,24 +282,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
         const int n = cur.q.n, kv = cur.q.kv, R = n * p.g, q0 = cur.q.q0;
         const int lim0 = visible_keys(n, kv, 0, a.causal);  // keys that every row sees
 
-        // Q as operand fragments; with two row tiles at d = 128 they would take 64 more
-        // registers than there are and stay in the merge buffer (32 rows, swizzled).
-        constexpr bool QREG = MT * D <= 128;
-        uint32_t qf[QREG ? MT : 1][QREG ? D / 16 : 1][4];
-        const uint32_t sQ = smem_u32(merge);
+        uint32_t qf[MT][D / 16][4];
         int lim[MT][2];
-        if constexpr (!QREG) {
-            for (int i = tid; i < 32 * (D / 8); i += kThreads) {
-                const int row = i / (D / 8), c8 = i % (D / 8);
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (row < R) {
-                    const int tok = row / p.g, hd = cur.h * p.g + row - tok * p.g;
-                    u = __ldg(reinterpret_cast<const uint4 *>(a.q + static_cast<int64_t>(q0 + tok) * a.q_st + hd * a.q_sh) + c8);
-                }
-                *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(merge) + row * C::ROW + ((c8 ^ (row & 7)) << 4)) = u;
-            }
-            __syncthreads();
-        }
 #pragma unroll
         for (int mt = 0; mt < MT; mt++)
 #pragma unroll
@@ -310,13 +292,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                 const bool ok = row < R;
                 const int tok = ok ? row / p.g : 0, hd = cur.h * p.g + (ok ? row - tok * p.g : 0);
                 lim[mt][hf] = ok ? visible_keys(n, kv, tok, a.causal) : 0;
-                if constexpr (QREG) {
                 const uint16_t *src = a.q + static_cast<int64_t>(q0 + tok) * a.q_st + hd * a.q_sh + c2;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ks++) {
                     qf[mt][ks][hf] = ok ? __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16)) : 0u;
                     qf[mt][ks][hf + 2] = ok ? __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16 + 8)) : 0u;
-                }
                 }
             }
         float o[MT][D / 8][4];
@@ -334,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
             cp_async_wait<C::NST - 2>();
             __syncwarp();
             load_step();  // into the stage that the previous unit has been read from
-            const int key0 = j * C::KEYS + warp * C::TK;
+            const int key0 = j * C::TK;
             const uint32_t sK = ring + stage * C::STAGE, sV = sK + C::HALF;
             stage = stage + 1 == C::NST ? 0 : stage + 1;
             if (key0 >= kv) continue;
@@ -348,28 +328,17 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                 for (int i = 0; i < NB; i++) s[mt][i][0] = s[mt][i][1] = s[mt][i][2] = s[mt][i][3] = 0.f;
             {
                 const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
-                const int qr = lane & 15, qc = lane >> 4;
                 const uint32_t base = sK + kr * C::ROW;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ks++) {
-                    uint32_t qm[MT][4];
-#pragma unroll
-                    for (int mt = 0; mt < MT; mt++) {
-                        if constexpr (QREG) {
-#pragma unroll
-                            for (int e = 0; e < 4; e++) qm[mt][e] = qf[mt][ks][e];
-                        } else {
-                            ldsm4(sQ + (mt * 16 + qr) * C::ROW + (((ks * 2 + qc) ^ (qr & 7)) << 4), qm[mt]);
-                        }
-                    }
 #pragma unroll
                     for (int kb = 0; kb < KB; kb++) {
                         uint32_t kf[4];
                         ldsm4(base + kb * 16 * C::ROW + (((ks * 2 + kc) ^ (kr & 7)) << 4), kf);
 #pragma unroll
                         for (int mt = 0; mt < MT; mt++) {
-                            mma16816<DT>(s[mt][2 * kb], qm[mt], kf[0], kf[1]);
-                            mma16816<DT>(s[mt][2 * kb + 1], qm[mt], kf[2], kf[3]);
+                            mma16816<DT>(s[mt][2 * kb], qf[mt][ks], kf[0], kf[1]);
+                            mma16816<DT>(s[mt][2 * kb + 1], qf[mt][ks], kf[2], kf[3]);
                         }
                     }
                 }
@@ -458,120 +427,58 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
             }
         }
 
-        // ---- join the four warps; rows in shared memory, columns in turns
+        // ---- write the rows: final, or partial
+        const bool any_dirty = __any_sync(~0u, dirty);
+        const bool whole = j0 == 0 && j1 == cur.units;
+        const int64_t slot = 2 * static_cast<int64_t>(c) + (j0 == 0 ? 1 : 0);
 #pragma unroll
         for (int mt = 0; mt < MT; mt++)
 #pragma unroll
             for (int hf = 0; hf < 2; hf++) {
+                const int row = mt * 16 + hf * 8 + r4;
                 float l = l_run[mt][hf];
                 l += __shfl_xor_sync(~0u, l, 1);
                 l += __shfl_xor_sync(~0u, l, 2);
-                if ((lane & 3) == 0) {
-                    s_m[warp][mt * 16 + hf * 8 + r4] = m_run[mt][hf];
-                    s_l[warp][mt * 16 + hf * 8 + r4] = l;
-                }
-            }
-        const bool any_dirty = __syncthreads_or(dirty);
-        const bool whole = j0 == 0 && j1 == cur.units;
-        const int slot = 2 * c + (j0 == 0 ? 1 : 0);
-#pragma unroll 1
-        for (int mt = 0; mt < MT; mt++) {
-            if (mt * 16 >= R) break;
-            // A warp none of whose keys a row sees has l = 0 there and adds nothing.
-            float wgt[2];
-            bool none[2];
-#pragma unroll
-            for (int hf = 0; hf < 2; hf++) {
-                const int row = mt * 16 + hf * 8 + r4;
-                float M = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_m[w][row]);
-                none[hf] = s_l[warp][row] == 0.f;
-                wgt[hf] = ex2_approx(s_m[warp][row] - M);
-            }
-            auto add_quarter = [&](auto QD, int t) {
-                constexpr int qd = decltype(QD)::value;
-#pragma unroll
-                for (int i = 0; i < D / 8 / kWarps; i++) {
-                    constexpr int first = qd * (D / 8 / kWarps);
-#pragma unroll
-                    for (int hf = 0; hf < 2; hf++) {
-                        float2 *d2 =
-                            reinterpret_cast<float2 *>(merge + (hf * 8 + r4) * C::OPITCH + (first + i) * 8 + c2);
-                        // (MT is 1 or 2: selected without indexing registers by mt)
-                        const float x0 = MT == 2 && mt ? o[MT - 1][first + i][2 * hf] : o[0][first + i][2 * hf];
-                        const float x1 = MT == 2 && mt ? o[MT - 1][first + i][2 * hf + 1] : o[0][first + i][2 * hf + 1];
-                        float2 v = none[hf] ? make_float2(0.f, 0.f) : make_float2(x0 * wgt[hf], x1 * wgt[hf]);
-                        if (t > 0) {
-                            const float2 u = *d2;
-                            v.x += u.x;
-                            v.y += u.y;
-                        }
-                        *d2 = v;
-                    }
-                }
-            };
-#pragma unroll 1
-            for (int t = 0; t < kWarps; t++) {
-                switch ((warp + t) & (kWarps - 1)) {
-                case 0: add_quarter(std::integral_constant<int, 0>{}, t); break;
-                case 1: add_quarter(std::integral_constant<int, 1>{}, t); break;
-                case 2: add_quarter(std::integral_constant<int, 2>{}, t); break;
-                default: add_quarter(std::integral_constant<int, 3>{}, t); break;
-                }
-                __syncthreads();
-            }
-            // ---- write: 8 columns of a row per thread and turn
-            for (int it = tid; it < 16 * (D / 8); it += kThreads) {
-                const int rr = it / (D / 8), c8 = (it % (D / 8)) * 8;
-                const int row = mt * 16 + rr;
                 if (row >= R) continue;
-                float M = -INFINITY, l = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_m[w][row]);
-#pragma unroll
-                for (int w = 0; w < kWarps; w++)
-                    if (s_l[w][row] != 0.f) l += ex2_approx(s_m[w][row] - M) * s_l[w][row];
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; e++) v[e] = merge[rr * C::OPITCH + c8 + e];
                 const int tok = row / p.g, hd = cur.h * p.g + (row - tok * p.g);
                 if (any_dirty) {
                     // Non-finite values of keys that this row sees and that were left out.
-                    const int see = min(visible_keys(n, kv, tok, a.causal), j1 * C::KEYS);
-                    for (int key = max(lim0 / C::TK * C::TK, j0 * C::KEYS); key < see; key++) {
+                    const int see = min(lim[mt][hf], j1 * C::TK);
+#pragma unroll 1
+                    for (int key = max(lim0 / C::TK * C::TK, j0 * C::TK); key < see; key++) {
                         const int pg = __ldg(a.block_table + cur.s * a.bt_s + (key >> a.page_shift));
                         if (pg < 0 || pg >= a.num_pages) continue;
                         const uint16_t *vs = a.vc + static_cast<int64_t>(pg) * a.vc_sp + cur.h * a.vc_sh +
-                                             static_cast<int64_t>(key & key_mask) * a.vc_sn + c8;
+                                             static_cast<int64_t>(key & key_mask) * a.vc_sn + c2;
 #pragma unroll
-                        for (int e = 0; e < 8; e++) {
-                            const float x = elem_lo<DT>(__ldg(vs + e));
-                            if (!isfinite(x)) v[e] += x;
+                        for (int i = 0; i < D / 8; i++) {
+                            const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(vs + i * 8));
+                            const float x0 = elem_lo<DT>(u), x1 = elem_hi<DT>(u);
+                            if (!isfinite(x0)) o[mt][i][2 * hf] += x0;
+                            if (!isfinite(x1)) o[mt][i][2 * hf + 1] += x1;
                         }
                     }
                 }
+                const float m = m_run[mt][hf];
                 if (whole) {
                     const float inv = 1.f / l;
-                    uint4 u = make_uint4(0u, 0u, 0u, 0u);  // a row that sees no key
-                    if (l != 0.f)
-                        u = make_uint4(pack2<DT>(v[0] * inv, v[1] * inv), pack2<DT>(v[2] * inv, v[3] * inv),
-                                       pack2<DT>(v[4] * inv, v[5] * inv), pack2<DT>(v[6] * inv, v[7] * inv));
-                    *reinterpret_cast<uint4 *>(a.o + static_cast<int64_t>(q0 + tok) * a.o_st + hd * a.o_sh + c8) = u;
-                    if (c8 == 0 && a.lse2)
-                        a.lse2[static_cast<int64_t>(q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
+                    uint16_t *dst = a.o + static_cast<int64_t>(q0 + tok) * a.o_st + hd * a.o_sh + c2;
+#pragma unroll
+                    for (int i = 0; i < D / 8; i++)  // (zeros for a row that sees no key)
+                        *reinterpret_cast<uint32_t *>(dst + i * 8) =
+                            l == 0.f ? 0u : pack2<DT>(o[mt][i][2 * hf] * inv, o[mt][i][2 * hf + 1] * inv);
+                    if ((lane & 3) == 0 && a.lse2)
+                        a.lse2[static_cast<int64_t>(q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : m + log2f(l);
                 } else {
-                    float4 *d4 = reinterpret_cast<float4 *>(
-                        p.part_o + (static_cast<int64_t>(slot) * p.rows_max + row) * D + c8);
-                    d4[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    d4[1] = make_float4(v[4], v[5], v[6], v[7]);
-                    if (c8 == 0) p.part_ml[static_cast<int64_t>(slot) * p.rows_max + row] = make_float2(M, l);
+                    float *dst = p.part_o + (slot * p.rows_max + row) * D + c2;
+#pragma unroll
+                    for (int i = 0; i < D / 8; i++)
+                        *reinterpret_cast<float2 *>(dst + i * 8) = make_float2(o[mt][i][2 * hf], o[mt][i][2 * hf + 1]);
+                    if ((lane & 3) == 0) p.part_ml[slot * p.rows_max + row] = make_float2(m, l);
                 }
             }
-            __syncthreads();
-        }
-        if (!whole && j0 == 0 && tid == 0) {
-            // The item's remaining units lie in the next blocks' runs; how many blocks:
+        if (!whole && j0 == 0 && lane == 0) {
+            // The item's remaining units lie in the next workers' runs; how many workers:
             const uint32_t end = u1 - cur.left + cur.units - 1;  // the item's last unit
             int ce = static_cast<int>(static_cast<uint64_t>(end) * static_cast<uint32_t>(nb) / U);
             while (ce > c && decode_cut(U, nb, ce) > end) ce--;
@@ -587,67 +494,101 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     pdl_wait();  // (the schedule kernel, whose results only later kernels read)
 }
 
-// Adds the partial results of the item that block c of the decode kernel started
-// and did not finish: its own and those at the start of the following blocks.  A
-// thread takes four columns of a row; where an item's rows leave threads over,
-// groups of threads take every so-many-th part (a fixed order, so reruns agree
-// bit for bit).
+// Adds the partial results of the items that workers of the decode kernel started
+// and did not finish: worker c's own and those at the start of the following
+// workers' runs, a few, or a hundred where there are few sequences.  A block looks
+// after kJoinEach neighbouring workers; its warps share out the rows of the items
+// that those started, and where there are fewer rows than warps the parts of each
+// row too (by counts alone, and added in a fixed order: reruns agree bit for bit).
+// blockIdx.y: where an item has many rows, blocks take turns.
+constexpr int kJoinEach = 8;
+
 template <int D, int DT>
 __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const DecodeParams p)
 {
-    constexpr int TPR = D / 4;  // threads per row
-    __shared__ float4 s_o[kJoinThreads];
-    __shared__ float2 s_ml[kJoinThreads];
+    constexpr int V = D / 32, W = kJoinThreads / 32, B = 8;  // columns per lane, warps, loads in flight
+    __shared__ int4 s_meta[kJoinEach];
+    __shared__ float s_o[W][D];
+    __shared__ float2 s_ml[W];
     const PagedArgs &a = p.a;
-    const int c = blockIdx.x, tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c0 = blockIdx.x * kJoinEach;
     pdl_wait();
     pdl_launch();
-    const int4 mt = p.meta[c];
-    const int K = mt.x, q0 = mt.y, R = mt.z * p.g;
-    if (K == 0) return;
-    int rows = 1;
-    while (rows < R && rows < kJoinThreads / TPR) rows *= 2;
-    const int groups = kJoinThreads / TPR / rows;
-    const int c4 = tid % TPR, wr = tid / TPR % rows, grp = tid / TPR / rows;
-    for (int rb = 0; rb < R; rb += rows) {
-        const int row = rb + wr;
-        float M = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float2 ml, float4 x) {
-            if (ml.y == 0.f) return;  // a part none of whose keys the row sees
-            const float m = fmaxf(M, ml.x), w = ex2_approx(ml.x - m);
+    if (tid < kJoinEach) s_meta[tid] = c0 + tid < p.workers ? p.meta[c0 + tid] : make_int4(0, 0, 0, 0);
+    __syncthreads();
+    int rows = 0;
+#pragma unroll
+    for (int i = 0; i < kJoinEach; i++) rows += s_meta[i].x ? s_meta[i].z * p.g : 0;
+    int per = W;  // warps per row
+    while (per > 1 && rows * per > W) per /= 2;
+    for (int r0 = blockIdx.y * (W / per); r0 < rows; r0 += gridDim.y * (W / per)) {
+        const int sub = warp % per;
+        int row = r0 + warp / per, i = 0;
+        const bool live = row < rows;
+        if (live)
+            while (true) {  // the item that the row belongs to
+                const int n = s_meta[i].x ? s_meta[i].z * p.g : 0;
+                if (row < n) break;
+                row -= n;
+                i++;
+            }
+        const int4 mt = s_meta[live ? i : 0];
+        const int c = c0 + i;
+        float M = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+        for (int e = 0; e < V; e++) o[e] = 0.f;
+        auto add = [&](float m1, float l1, const float *x) {
+            if (l1 == 0.f) return;  // a part none of whose keys the row sees
+            const float m = fmaxf(M, m1), w = ex2_approx(m1 - m);
             const bool none = l == 0.f;
             const float w0 = none ? 0.f : ex2_approx(M - m);
             M = m;
-            l = none ? w * ml.y : fmaf(l, w0, w * ml.y);
-            o.x = none ? w * x.x : fmaf(o.x, w0, w * x.x);
-            o.y = none ? w * x.y : fmaf(o.y, w0, w * x.y);
-            o.z = none ? w * x.z : fmaf(o.z, w0, w * x.z);
-            o.w = none ? w * x.w : fmaf(o.w, w0, w * x.w);
+            l = none ? w * l1 : fmaf(l, w0, w * l1);
+#pragma unroll
+            for (int e = 0; e < V; e++) o[e] = none ? w * x[e] : fmaf(o[e], w0, w * x[e]);
         };
-        if (row < R) {
-#pragma unroll 4
-            for (int k = grp; k < K; k += groups) {
-                const int64_t at = static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * p.rows_max + row;
-                add(p.part_ml[at], reinterpret_cast<const float4 *>(p.part_o + at * D)[c4]);
+        if (live) {
+            for (int k0 = sub; k0 < mt.x; k0 += B * per) {
+                float2 ml[B];
+                float x[B][V];
+#pragma unroll
+                for (int e = 0; e < B; e++) {
+                    const int k = k0 + e * per;
+                    ml[e] = make_float2(0.f, 0.f);
+                    if (k >= mt.x) continue;
+                    const int64_t at = static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * p.rows_max + row;
+                    ml[e] = p.part_ml[at];
+                    if constexpr (V == 4) {
+                        const float4 u = reinterpret_cast<const float4 *>(p.part_o + at * D)[lane];
+                        x[e][0] = u.x; x[e][1] = u.y; x[e][2] = u.z; x[e][3] = u.w;
+                    } else {
+                        const float2 u = reinterpret_cast<const float2 *>(p.part_o + at * D)[lane];
+                        x[e][0] = u.x; x[e][1] = u.y;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < B; e++) add(ml[e].x, ml[e].y, x[e]);
             }
         }
-        if (groups > 1) {
-            s_o[tid] = o;
-            s_ml[tid] = make_float2(M, l);
+        if (per > 1) {
+#pragma unroll
+            for (int e = 0; e < V; e++) s_o[warp][lane * V + e] = o[e];
+            if (lane == 0) s_ml[warp] = make_float2(M, l);
             __syncthreads();
-            if (grp == 0)
-                for (int g2 = 1; g2 < groups; g2++) add(s_ml[tid + g2 * rows * TPR], s_o[tid + g2 * rows * TPR]);
+            if (sub == 0)
+                for (int w = 1; w < per; w++) add(s_ml[warp + w].x, s_ml[warp + w].y, &s_o[warp + w][lane * V]);
             __syncthreads();
         }
-        if (grp == 0 && row < R) {
+        if (live && sub == 0) {
             const float inv = 1.f / l;
             const int tok = row / p.g, hd = mt.w * p.g + (row - tok * p.g);
-            uint2 u = make_uint2(0u, 0u);  // a row that sees no key
-            if (l != 0.f) u = make_uint2(pack2<DT>(o.x * inv, o.y * inv), pack2<DT>(o.z * inv, o.w * inv));
-            *reinterpret_cast<uint2 *>(a.o + static_cast<int64_t>(q0 + tok) * a.o_st + hd * a.o_sh + c4 * 4) = u;
-            if (c4 == 0 && a.lse2)
-                a.lse2[static_cast<int64_t>(q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
+            uint16_t *dst = a.o + static_cast<int64_t>(mt.y + tok) * a.o_st + hd * a.o_sh + lane * V;
+#pragma unroll
+            for (int e = 0; e < V; e += 2)  // (zeros for a row that sees no key)
+                *reinterpret_cast<uint32_t *>(dst + e) = l == 0.f ? 0u : pack2<DT>(o[e] * inv, o[e + 1] * inv);
+            if (lane == 0 && a.lse2)
+                a.lse2[static_cast<int64_t>(mt.y + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
         }
     }
 }
@@ -665,53 +606,56 @@ clis_status_t launch_impl(const DecodeParams &p, int grid, bool after_schedule, 
         paged_decode_kernel<D, DT, MT><<<grid, kThreads, DCfg<D>::SMEM, stream>>>(p);
         if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
     }
-    return launch_pdl(paged_decode_join_kernel<D, DT>, dim3(grid), kJoinThreads, 0, stream, p) == cudaSuccess ? CLIS_OK
-                                                                                                     : CLIS_ERR_CUDA;
+    return launch_pdl(paged_decode_join_kernel<D, DT>, dim3((p.workers + kJoinEach - 1) / kJoinEach, p.rows_max / 8), kJoinThreads, 0,
+                      stream, p) == cudaSuccess
+               ? CLIS_OK
+               : CLIS_ERR_CUDA;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
-int paged_decode_row_tiles(int64_t max_q, int g)
+int paged_decode_row_tiles(int64_t max_q, int g, int d)
 {
-    // Rows of the largest sequence if it is small; else those of single tokens.
-    const int64_t rows = max_q * g <= 2 * 16 ? max_q * g : g;
-    return rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+    // Rows of the largest sequence if it is small; else those of single tokens.  Two
+    // row tiles at d = 128 would spill registers (64 sequences of 8,000 keys and 32
+    // rows: 661 us, the chunk kernel 415 us): not built.
+    const int most = d == 64 ? 32 : 16;
+    const int64_t rows = max_q <= most && max_q * g <= most ? max_q * g : g;
+    return rows <= 16 ? 1 : rows <= most ? 2 : 0;
 }
 
 size_t paged_decode_workspace(int d, int row_tiles, int nsm)
 {
     if (row_tiles == 0) return 0;
-    const size_t slots = 2 * 2 * static_cast<size_t>(nsm), rows = 16 * static_cast<size_t>(row_tiles);
-    return up256(2 * static_cast<size_t>(nsm) * sizeof(int4)) + up256(slots * rows * sizeof(float2)) +
-           up256(slots * rows * d * sizeof(float));
+    const size_t workers = 2 * static_cast<size_t>(nsm) * kWarps, rows = 16 * static_cast<size_t>(row_tiles);
+    return up256(workers * sizeof(int4)) + up256(2 * workers * rows * sizeof(float2)) +
+           up256(2 * workers * rows * d * sizeof(float));
 }
 
 clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, bool after_schedule, void *workspace,
                                   int nsm, cudaStream_t stream)
 {
     const int grid = 2 * nsm;  // two blocks fit an SM
-    const size_t slots = 2 * static_cast<size_t>(grid), rows = 16 * static_cast<size_t>(row_tiles);
+    const size_t workers = static_cast<size_t>(grid) * kWarps, rows = 16 * static_cast<size_t>(row_tiles);
     DecodeParams p;
     p.a = a;
     p.g = a.H / a.Hkv;
     p.rows_max = static_cast<int>(rows);
-    p.least = 2;  // units per block at least: one token over 301 keys 13.7 us with 1 or 2, 14.5 with 4, 18.7 with 8
+    p.least = 2;  // units of a worker's run: one token over 301 keys 12.8 us with 2, 14 with 1 or 4, 16.5 with 8
+    p.workers = static_cast<int>(workers);
     p.strict = strict;
     char *w = static_cast<char *>(workspace);
     p.meta = reinterpret_cast<int4 *>(w);
-    w += up256(grid * sizeof(int4));
+    w += up256(workers * sizeof(int4));
     p.part_ml = reinterpret_cast<float2 *>(w);
-    w += up256(slots * rows * sizeof(float2));
+    w += up256(2 * workers * rows * sizeof(float2));
     p.part_o = reinterpret_cast<float *>(w);
 #define CLIS_DECODE(D, MT)                                                  \
     return a.dtype == CLIS_DT_FP16 ? launch_impl<D, 1, MT>(p, grid, after_schedule, stream) \
                                    : launch_impl<D, 0, MT>(p, grid, after_schedule, stream)
-    if (a.d == 128) {
-        if (row_tiles == 1) CLIS_DECODE(128, 1);
-        CLIS_DECODE(128, 2);
-    }
+    if (a.d == 128) CLIS_DECODE(128, 1);
     if (row_tiles == 1) CLIS_DECODE(64, 1);
     CLIS_DECODE(64, 2);
 #undef CLIS_DECODE

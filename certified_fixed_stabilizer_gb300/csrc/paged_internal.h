@@ -97,8 +97,8 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem
 #endif
 
 // Row tiles (of 16 rows) per sequence that the decode kernel is built for, when
-// no sequence has more than max_q new tokens: 1, 2, or 0 (not used).
-int paged_decode_row_tiles(int64_t max_q, int g);
+// no sequence has more than max_q new tokens: 1, 2 (d = 64), or 0 (not used).
+int paged_decode_row_tiles(int64_t max_q, int g, int d);
 size_t paged_decode_workspace(int d, int row_tiles, int nsm);
 // strict: no chunk kernel follows, a sequence of more rows is an error.
 // after_schedule: launched behind launch_paged_chunk_schedule, whose results it

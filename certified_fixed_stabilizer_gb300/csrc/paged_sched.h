@@ -51,9 +51,9 @@ CLIS_HD int visible_keys(int n, int kv, int t, bool causal)
 // Items are (sequence, key/value head), sequence-major; an item costs one unit
 // per decode_keys(d) keys (at least one: its output must be written).  The units
 // of all items, laid end to end, are cut into as many equal runs as there are
-// blocks, so ragged batches balance to one unit, and an item that crosses a cut
-// is joined from partial results afterwards.
-CLIS_HD constexpr int decode_keys(int d) { return d == 128 ? 64 : 128; }  // the same bytes
+// workers (warps), so ragged batches balance to one unit, and an item that crosses
+// a cut is joined from partial results afterwards.
+CLIS_HD constexpr int decode_keys(int d) { return d == 128 ? 16 : 32; }  // the same bytes
 
 CLIS_HD bool is_decode(const SeqLen &s, int g, int rows_max)
 {
@@ -63,8 +63,8 @@ CLIS_HD bool is_decode(const SeqLen &s, int g, int rows_max)
 
 CLIS_HD int decode_units(const SeqLen &s, int keys) { return imax(1, ceil_div(s.kv, keys)); }
 
-// Blocks that take part, for U units: every run holds at least `least` units.
-CLIS_HD int decode_blocks(uint32_t U, int grid, int least)
+// Workers that take part, for U units.
+CLIS_HD int decode_workers(uint32_t U, int grid, int least)
 {
     const uint32_t want = (U + least - 1) / least;
     return want < static_cast<uint32_t>(grid) ? static_cast<int>(want) : grid;
