@@ -71,7 +71,7 @@ def _link_binding(obj: str) -> None:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = TORCH_EXT + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, f"-L{OUT_DIR}", "-lclis", f"-L{lib}", "-ltorch_python",
-           "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+           "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"linking the torch binding failed:\n{r.stdout}\n{r.stderr}")

@@ -854,7 +854,7 @@ def clis_attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: i
     cu_q[s + 1] - 1) over their sequences' cached keys; returns ``out``.  ``lse2``:
     optional float32 [T, H].  Rows that belong to no sequence are not written."""
     return _native.attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, scale_log2, causal, out, lse2,
-                                   workspace, _raw(stream))
+                                   False, workspace, _raw(stream))[0]
 
 
 def attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: int | None = None,
@@ -863,10 +863,9 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: int |
     tokens and chunks in one call (grouped-query heads by q's and the caches'
     head counts).  max_q: the most new tokens of a sequence (default: all rows of q).
     With ``return_lse``: (out, lse2 float32 [T, H])."""
-    lse2 = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
-    o = _native.attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q or max(1, q.shape[0]),
-                                scale_log2_for(q.shape[-1], softmax_scale), causal, out, lse2, None, None)
-    return (o, lse2) if return_lse else o
+    r = _native.attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q or max(1, q.shape[0]),
+                                scale_log2_for(q.shape[-1], softmax_scale), causal, out, None, return_lse, None, None)
+    return r if return_lse else r[0]
 
 
 class PagedCache:

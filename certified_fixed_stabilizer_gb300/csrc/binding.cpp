@@ -5,7 +5,7 @@
 // These calls are made once or more per layer and token, and at a few tokens the
 // kernels take a few microseconds: marshalled in Python a call took 25 to 35 us of
 // host time, here it takes about 5.  Everything that computes is in libclis.so.
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -83,7 +83,14 @@ void check_like(const Tensor &t, const Tensor &like, const char *name)
 // anything in its stride: it gets the row length, which passes every check.
 int64_t st(const Tensor &t, int64_t i) { return t.size(i) == 1 ? t.size(t.dim() - 1) : t.stride(i); }
 
-Tensor empty_as(const Tensor &t) { return at::empty(t.sizes(), t.options().requires_grad(false)); }
+// New tensors straight from the CUDA allocator (the dispatcher on the way to it costs
+// as much again).
+Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const at::Device &dev)
+{
+    return at::detail::empty_cuda(sizes, type, dev, std::nullopt);
+}
+
+Tensor empty_as(const Tensor &t) { return empty(t.sizes(), t.scalar_type(), t.device()); }
 
 // -------------------------------------------------------------------- rotary
 
@@ -206,9 +213,8 @@ std::vector<Tensor> plan(const Tensor &ctx_len, const Tensor &new_len, const Ten
                       "block_table must be an int32 tensor [S, width] with contiguous rows on the same device");
     TORCH_CHECK_VALUE(T >= 0, "num_tokens must not be negative");
     Place at_(ctx_len, raw);
-    const auto o32 = ctx_len.options(), o64 = o32.dtype(at::kLong);
-    Tensor cu = at::empty({S + 1}, o32), kv = at::empty({S}, o32), slots = at::empty({T}, o64), pos = at::empty({T}, o32),
-           state = at::empty({2}, o64);
+    Tensor cu = empty({S + 1}, at::kInt, dev), kv = empty({S}, at::kInt, dev), slots = empty({T}, at::kLong, dev),
+           pos = empty({T}, at::kInt, dev), state = empty({2}, at::kLong, dev);
     clis_paged_t d = {};
     d.S = S;
     d.T = T;
@@ -303,9 +309,11 @@ std::optional<Tensor> append(const Tensor &k, const Tensor &v, const Tensor &kc,
     return q ? q_out : std::nullopt;
 }
 
-Tensor attention(const Tensor &q, const Tensor &kc, const Tensor &vc, const Tensor &table, const Tensor &cu,
-                 const Tensor &kv, int64_t max_q, double scale_log2, bool causal, std::optional<Tensor> out,
-                 const std::optional<Tensor> &lse2, std::optional<Tensor> workspace, std::optional<uintptr_t> raw)
+// with_lse: lse2 is allocated if it is not given.
+std::vector<Tensor> attention(const Tensor &q, const Tensor &kc, const Tensor &vc, const Tensor &table, const Tensor &cu,
+                              const Tensor &kv, int64_t max_q, double scale_log2, bool causal, std::optional<Tensor> out,
+                              std::optional<Tensor> lse2, bool with_lse, std::optional<Tensor> workspace,
+                              std::optional<uintptr_t> raw)
 {
     TORCH_CHECK_VALUE(q.is_cuda() && q.dim() == 3 && elem(q) && q.stride(2) == 1,
                       "q must be a bfloat16 or float16 device tensor [T, H, d] with a contiguous last dimension");
@@ -323,12 +331,13 @@ Tensor attention(const Tensor &q, const Tensor &kc, const Tensor &vc, const Tens
     Place at_(q, raw);
     if (out) check_like(*out, q, "out");
     else out = empty_as(q);
+    if (with_lse && !lse2) lse2 = empty({d.T, d.H}, at::kFloat, dev);
     d.q_st = st(q, 0), d.q_sh = st(q, 1);
     d.o_st = st(*out, 0), d.o_sh = st(*out, 1);
     size_t need = 0;
     ok("clis_attn_paged_workspace_size", clis_attn_paged_workspace_size(&d, max_q, &need));
     if (!workspace) {
-        workspace = at::empty({static_cast<int64_t>(need)}, q.options().dtype(at::kByte).requires_grad(false));
+        workspace = empty({static_cast<int64_t>(need)}, at::kByte, dev);
         if (raw && need)  // allocated on the current stream, used on the given one
             workspace->record_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*raw), dev.index()));
     }
@@ -339,7 +348,7 @@ Tensor attention(const Tensor &q, const Tensor &kc, const Tensor &vc, const Tens
                            static_cast<const int32_t *>(cu.data_ptr()), static_cast<const int32_t *>(kv.data_ptr()),
                            out->data_ptr(), lse2 ? static_cast<float *>(lse2->data_ptr()) : nullptr, max_q,
                            static_cast<float>(scale_log2), causal, workspace->data_ptr(), workspace->nbytes(), at_.stream));
-    return *out;
+    return {*out, lse2 ? *lse2 : Tensor()};
 }
 
 // -------------------------------------------------------------- Python objects
@@ -469,11 +478,11 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n)
 
 PyObject *py_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    return call(n, 13, [&] {
-        return THPVariable_Wrap(attention(tensor(a[0], "q"), tensor(a[1], "k_cache"), tensor(a[2], "v_cache"),
-                                          tensor(a[3], "block_table"), tensor(a[4], "cu_q"), tensor(a[5], "kv_len"),
-                                          integer(a[6]), real(a[7]), truth(a[8]), maybe(a[9], "out"), maybe(a[10], "lse2"),
-                                          maybe(a[11], "workspace"), stream_of(a[12])));
+    return call(n, 14, [&] {
+        return wrap(attention(tensor(a[0], "q"), tensor(a[1], "k_cache"), tensor(a[2], "v_cache"), tensor(a[3], "block_table"),
+                              tensor(a[4], "cu_q"), tensor(a[5], "kv_len"), integer(a[6]), real(a[7]), truth(a[8]),
+                              maybe(a[9], "out"), maybe(a[10], "lse2"), truth(a[11]), maybe(a[12], "workspace"),
+                              stream_of(a[13])));
     });
 }
 

@@ -172,16 +172,18 @@ Split split_of(const clis_paged_t *p, int64_t max_q, int nsm)
     Split s;
     s.row_tiles = clis::paged_decode_row_tiles(mq, g, static_cast<int>(p->d));
     s.chunk = mq * g > 16 * s.row_tiles;
-    // A batch with chunks whose caches are small as a whole leaves its single tokens
-    // to the chunk kernel too: at 12 sequences of up to 8,000 keys (d = 128, 8
-    // key/value heads) that took 110 us, the decode kernel first 136 us.  Above, the
-    // decode kernel's higher share of the bandwidth counts: 64 sequences of up to
-    // 16,000 keys took 383 us and 374 us, at d = 64 276 us and 231 us (a key tile
-    // has half the bytes there, but takes almost as long).  The limit is on what
-    // the block table can hold, which the host knows.
-    const int64_t tiles = p->d == 128 ? 128 : 32;
+    // A batch with chunks leaves its single tokens to the chunk kernel too where they
+    // are few items (sequence, key/value head): an item costs that kernel some 5 us of
+    // one SM, the decode kernel's launches cost the batch 25 us.  (8 key/value heads,
+    // one chunk: 12 sequences of up to 8,000 keys 98 us against 127 with both, 64 of
+    // 16,000 362 against 384; 100 of 600 104 against 80, 300 of 300 206 against 102.)
+    // At d = 64 a key tile has half the bytes but takes almost as long, so the total
+    // length counts too (24 sequences of up to 8,000 keys 84 us against 94, 40 119
+    // against 112, 64 of 16,000 260 against 219): at most 96 tiles per SM by what the
+    // block table can hold, which the host knows.
+    const int64_t items = p->S * p->Hkv;
     const int64_t per = (p->width * p->page_size + clis::kChunkKeys - 1) / clis::kChunkKeys;
-    if (s.chunk && p->S * p->Hkv * per <= tiles * nsm) s.row_tiles = 0;
+    if (s.chunk && items <= 4 * nsm && (p->d == 128 || items * per <= 96 * nsm)) s.row_tiles = 0;
     return s;
 }
 
