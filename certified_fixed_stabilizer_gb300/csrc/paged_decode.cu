@@ -41,7 +41,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kTau = 8.0f;
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 
 template <int D>
 struct DCfg {
@@ -520,8 +520,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
     int rows = 0;
 #pragma unroll
     for (int i = 0; i < kJoinEach; i++) rows += s_meta[i].x ? s_meta[i].z * p.g : 0;
-    int per = W;  // warps per row
-    while (per > 1 && rows * per > W) per /= 2;
+    const int mine = (rows + gridDim.y - 1) / gridDim.y;  // rows of this block
+    int per = W;                                          // warps per row
+    while (per > 1 && mine * per > W) per /= 2;
     for (int r0 = blockIdx.y * (W / per); r0 < rows; r0 += gridDim.y * (W / per)) {
         const int sub = warp % per;
         int row = r0 + warp / per, i = 0;
@@ -606,7 +607,7 @@ clis_status_t launch_impl(const DecodeParams &p, int grid, bool after_schedule, 
         paged_decode_kernel<D, DT, MT><<<grid, kThreads, DCfg<D>::SMEM, stream>>>(p);
         if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
     }
-    return launch_pdl(paged_decode_join_kernel<D, DT>, dim3((p.workers + kJoinEach - 1) / kJoinEach, p.rows_max / 8), kJoinThreads, 0,
+    return launch_pdl(paged_decode_join_kernel<D, DT>, dim3((p.workers + kJoinEach - 1) / kJoinEach, p.rows_max / 4), kJoinThreads, 0,
                       stream, p) == cudaSuccess
                ? CLIS_OK
                : CLIS_ERR_CUDA;
