@@ -26,6 +26,9 @@
 //  * P is rounded to the data type (bf16: off by up to 2^-8 of each weight) as
 //    the matrix instructions take it; the row sum adds the unrounded values,
 //    and o, m, l stay in fp32.
+//
+// 64 requests of 1,000 to 16,000 keys (8 key/value heads, d = 128, 2.13 GB): 306 us
+// and 5 us for the join, 6.8 TB/s, the measured copy rate.
 #include <cuda_bf16.h>
 
 #include "clis_internal.h"

@@ -159,6 +159,35 @@ def test_many_sequences():
     check_attention(*run(b), b, what="with chunks")
 
 
+def test_the_most_sequences():
+    """16,384 sequences, nearly all of them without a token in this step."""
+    ctx, new = [0] * 16384, [0] * 16384
+    for s, c, n in ((0, 100, 1), (7, 0, 1), (511, 300, 60), (9000, 64, 1), (16383, 33, 2)):
+        ctx[s], new[s] = c, n
+    b = make_batch(ctx, new, 4, 2, 64, 16, BF, seed=39)
+    check_attention(*run(b), b)
+    new[511] = 1
+    b = make_batch(ctx, new, 4, 2, 64, 16, BF, seed=40)
+    check_attention(*run(b), b)
+
+
+def test_calls_at_once():
+    """Calls on several streams at the same time, each with its own workspace."""
+    bs = [make_batch([900, 40], [1, n], 8, 2, 128, 16, BF, seed=50 + i) for i, n in enumerate((1, 90, 3, 200))]
+    want = [run(b) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        for b, s in zip(bs, streams):
+            with torch.cuda.stream(s):
+                got.append(run(b))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 4][0]) and torch.equal(l, want[i % 4][1])
+
+
 @pytest.mark.parametrize("Hkv,g,n,ctx,dtype", [(8, 4, 640, 8000, BF), (4, 2, 1200, 5000, FP), (1, 8, 60, 30000, BF),
                                                (2, 4, 500, 20000, BF), (16, 8, 16, 3000, BF), (8, 4, 9, 60000, FP)])
 def test_parts_join_alike_whoever_is_last(Hkv, g, n, ctx, dtype):

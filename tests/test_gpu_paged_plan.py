@@ -48,7 +48,7 @@ def host_plan(ctx, new, table, ring, head, tail, page, T):
 
 
 @pytest.mark.parametrize("S,page,big,seed", [(1, 8, 30, 0), (1, 16, 5000, 1), (5, 64, 300, 2), (33, 8, 100, 3), (700, 16, 90, 4),
-                                            (1024, 32, 700, 5), (3000, 16, 40, 6)])
+                                            (1024, 32, 700, 5), (3000, 16, 40, 6), (16384, 8, 20, 7)])
 def test_against_a_host_loop(S, page, big, seed):
     rng = random.Random(seed)
     ctx = [rng.choice([0, page, rng.randint(0, big), rng.randint(0, 10 * page)]) for _ in range(S)]
