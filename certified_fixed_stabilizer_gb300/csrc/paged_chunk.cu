@@ -44,7 +44,7 @@
 // which takes only a few products in advance.)
 //
 // 2,048 tokens behind 30,011 (32 query and 8 key/value heads, d = 128): 690 us, 1,510
-// TFLOP/s, the tensor pipe active 61% of the time; a key tile takes 1.45 us, of which
+// TFLOP/s, the tensor pipe active 66% of the time; a key tile takes 1.45 us, of which
 // the chain of one row tile is 1.4 (scores 0.28, weights 0.6, product 0.28, and the
 // barriers between them).
 //
@@ -1143,72 +1143,77 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_chunk_join_kernel(const
     const PagedArgs &a = p.a;
     __shared__ float s_o[kJoinWarps][16][33], s_m[kJoinWarps][32], s_l[kJoinWarps][32];
     pdl_wait();
-    if (static_cast<int>(blockIdx.x) >= *p.joins) return;
-    const int2 jn = p.join[blockIdx.x];
-    const int parts = jn.x;
-    const ChunkItem T = load_item(p, jn.y);
+    const int joins = *p.joins;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = blockIdx.y * 32 + lane, tile = r / BM, rl = r % BM, c16 = blockIdx.z;
-    if (blockIdx.y * 32 / BM >= T.nt) return;
-    const int rt = rl / p.g, tok = T.tok0 + tile * p.tpt + rt;
-    const bool row_ok = rt < p.tpt && tok < T.n;  // (other rows' partial results were never written)
-    const int nb = static_cast<int>(p.head[2]);
-    const int c = chunk_owners(T, chunk_cuts(p.head[1], nb)).c;
-    float M = -INFINITY, l = 0.f, o[16];
+    const int rt = rl / p.g;
+    for (int i = blockIdx.x; i < joins; i += gridDim.x) {
+        const int2 jn = p.join[i];
+        const int parts = jn.x;
+        const ChunkItem T = load_item(p, jn.y);
+        if (static_cast<int>(blockIdx.y) * 32 / BM >= T.nt) continue;
+        const int tok = T.tok0 + tile * p.tpt + rt;
+        const bool row_ok = rt < p.tpt && tok < T.n;  // (other rows' partial results were never written)
+        const int nb = static_cast<int>(p.head[2]);
+        const int c = chunk_owners(T, chunk_cuts(p.head[1], nb)).c;
+        float M = -INFINITY, l = 0.f, o[16];
 #pragma unroll
-    for (int e = 0; e < 16; e++) o[e] = 0.f;
-    if (row_ok) {
+        for (int e = 0; e < 16; e++) o[e] = 0.f;
+        if (row_ok) {
 #pragma unroll 2
-        for (int k = warp; k < parts; k += kJoinWarps) {
-            const int64_t s = k == 0 ? 2 * c + 1 : 2 * (c + k);
-            const float2 ml = p.part_ml[s * (2 * BM) + r];
-            float4 u[4];
+            for (int k = warp; k < parts; k += kJoinWarps) {
+                const int64_t s = k == 0 ? 2 * c + 1 : 2 * (c + k);
+                const float2 ml = p.part_ml[s * (2 * BM) + r];
+                float4 u[4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) u[e] = *part_at<D>(p, s, c16 * 4 + e, r);
-            if (ml.y == 0.f) continue;  // a part none of whose keys the row sees adds nothing
-            const float m = fmaxf(M, ml.x);
-            const bool none = l == 0.f;
-            const float w0 = none ? 0.f : ex2_approx(M - m), w = ex2_approx(ml.x - m);
-            M = m;
-            l = none ? w * ml.y : fmaf(l, w0, w * ml.y);
-            const float x[16] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w,
-                                 u[2].x, u[2].y, u[2].z, u[2].w, u[3].x, u[3].y, u[3].z, u[3].w};
+                for (int e = 0; e < 4; e++) u[e] = *part_at<D>(p, s, c16 * 4 + e, r);
+                if (ml.y == 0.f) continue;  // a part none of whose keys the row sees adds nothing
+                const float m = fmaxf(M, ml.x);
+                const bool none = l == 0.f;
+                const float w0 = none ? 0.f : ex2_approx(M - m), w = ex2_approx(ml.x - m);
+                M = m;
+                l = none ? w * ml.y : fmaf(l, w0, w * ml.y);
+                const float x[16] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w,
+                                     u[2].x, u[2].y, u[2].z, u[2].w, u[3].x, u[3].y, u[3].z, u[3].w};
 #pragma unroll
-            for (int e = 0; e < 16; e++) o[e] = none ? w * x[e] : fmaf(o[e], w0, w * x[e]);
+                for (int e = 0; e < 16; e++) o[e] = none ? w * x[e] : fmaf(o[e], w0, w * x[e]);
+            }
         }
+#pragma unroll
+        for (int e = 0; e < 16; e++) s_o[warp][e][lane] = o[e];
+        s_m[warp][lane] = M;
+        s_l[warp][lane] = l;
+        __syncthreads();
+        if (warp < 2 && row_ok) {
+            // Warps 0 and 1: eight columns each, over the warps' sums in order.
+            M = -INFINITY;
+            l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; w++)
+                if (s_l[w][lane] != 0.f) M = fmaxf(M, s_m[w][lane]);
+#pragma unroll
+            for (int e = 0; e < 8; e++) o[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; w++) {
+                const float lw = s_l[w][lane];
+                if (lw == 0.f) continue;
+                const float g = ex2_approx(s_m[w][lane] - M);
+                l = fmaf(g, lw, l);
+#pragma unroll
+                for (int e = 0; e < 8; e++) o[e] = fmaf(g, s_o[w][warp * 8 + e][lane], o[e]);
+            }
+            const float inv = 1.f / l;
+            const int hd = T.h * p.g + (rl - rt * p.g);
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) pk[e] = l == 0.f ? 0u : pack2<DT>(o[2 * e] * inv, o[2 * e + 1] * inv);
+            *reinterpret_cast<uint4 *>(a.o + static_cast<int64_t>(T.q0 + tok) * a.o_st + hd * a.o_sh + c16 * 16 + warp * 8) =
+                make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            if (c16 == 0 && warp == 0 && a.lse2)
+                a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
+        }
+        __syncthreads();  // (the sums are written again)
     }
-#pragma unroll
-    for (int e = 0; e < 16; e++) s_o[warp][e][lane] = o[e];
-    s_m[warp][lane] = M;
-    s_l[warp][lane] = l;
-    __syncthreads();
-    if (warp >= 2 || !row_ok) return;
-    // Warps 0 and 1: eight columns each, over the warps' sums in order.
-    M = -INFINITY;
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; w++)
-        if (s_l[w][lane] != 0.f) M = fmaxf(M, s_m[w][lane]);
-#pragma unroll
-    for (int e = 0; e < 8; e++) o[e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; w++) {
-        const float lw = s_l[w][lane];
-        if (lw == 0.f) continue;
-        const float g = ex2_approx(s_m[w][lane] - M);
-        l = fmaf(g, lw, l);
-#pragma unroll
-        for (int e = 0; e < 8; e++) o[e] = fmaf(g, s_o[w][warp * 8 + e][lane], o[e]);
-    }
-    const float inv = 1.f / l;
-    const int hd = T.h * p.g + (rl - rt * p.g);
-    uint32_t pk[4];
-#pragma unroll
-    for (int e = 0; e < 4; e++) pk[e] = l == 0.f ? 0u : pack2<DT>(o[2 * e] * inv, o[2 * e + 1] * inv);
-    *reinterpret_cast<uint4 *>(a.o + static_cast<int64_t>(T.q0 + tok) * a.o_st + hd * a.o_sh + c16 * 16 + warp * 8) =
-        make_uint4(pk[0], pk[1], pk[2], pk[3]);
-    if (c16 == 0 && warp == 0 && a.lse2)
-        a.lse2[static_cast<int64_t>(T.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1278,8 +1283,9 @@ clis_status_t launch_impl(const ChunkParams &p, cudaStream_t stream)
     }
     if (launch_pdl(paged_chunk_kernel<D, DT>, dim3(p.grid), kThreads, C::SMEM_BYTES, stream, mq, mk, mv, p) != cudaSuccess)
         return CLIS_ERR_CUDA;
-    const int64_t items = max_items(a);
-    const int joins = static_cast<int>(items < max_joins(p.grid) ? items : max_joins(p.grid));
+    // One wave of blocks over the list; mostly it is short or empty.
+    const int64_t items = max_items(a), wave = p.grid / 8;
+    const int joins = static_cast<int>(imin(max_joins(p.grid), static_cast<int>(items < wave ? items : wave > 1 ? wave : 1)));
     if (launch_pdl(paged_chunk_join_kernel<D, DT>, dim3(joins, 2 * BM / 32, D / 16), 32 * kJoinWarps, 0, stream, p) !=
         cudaSuccess)
         return CLIS_ERR_CUDA;
