@@ -8,13 +8,13 @@
 // row's maximum outgrew it by 2^8.
 //
 // Bound: the tensor cores (4 d flops per row and visible key), then exp2 on the
-// MUFU.  A work tile is two 128-row tiles; a row tile packs 128 / g tokens of
-// all g query heads of one key/value head, so each key tile that is loaded
-// serves every head that shares it.  The pipeline of one persistent block:
+// MUFU.  An item is two 128-row tiles against the keys they see; a row tile packs
+// 128 / g tokens of all g query heads of one key/value head, so each key tile that
+// is loaded serves every head that shares it.  The pipeline of one persistent block:
 //
 //   warps 0-3, 4-7  softmax of row tile 0, 1 (thread = row)
-//   warps 8-11      epilogue: O / l, or a partial result where the keys of a
-//                   work tile are shared out
+//   warps 8-11      epilogue: O / l, or a partial result of an item that other
+//                   blocks compute parts of
 //   warp 12         TMA producer of K and V: 128-key tiles gathered page by page
 //   warp 13         MMA issuer, owns TMEM
 //   warp 14         TMA producer of Q
@@ -110,7 +110,7 @@ struct __align__(8) Ctl {
     uint64_t edge_ok;  // and is ready for the product
     uint64_t drain;
     float epi_l[2][BM], epi_shift[2][BM];
-    int dirty[8];  // per work tile (mod 8): non-finite values were taken out
+    int dirty[8];  // per item (mod 8): non-finite values were taken out
     uint32_t tmem_base;
     int last;  // epilogue: the item's other parts are done
     int abort_flag;
@@ -432,7 +432,7 @@ __device__ void edge_role(const ChunkParams &p, Ctl &c, uint32_t sKV, const Run 
         for (int j = 0; j < K.n; j++) {
             const int kt = K.start + j;
             if (kt < first) continue;
-            // V_j is in load group j + 1 and in ring slot 2 j + 1 of the work tile's
+            // V_j is in load group j + 1 and in ring slot 2 j + 1 of the item's
             // (K_0, V_0, K_1, V_1, ...).  The MMA warp, which waits for every group,
             // says when it has arrived; this warp skips groups, and a barrier whose
             // phases are skipped cannot be told apart by parity.  Once it is said, the

@@ -203,8 +203,9 @@ clis_status_t launch_paged_plan(const PlanArgs &a, cudaStream_t stream)
         cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
         return CLIS_ERR_CUDA;
-    // About four tokens a thread, one block per SM at most.
-    int64_t blocks = (static_cast<int64_t>(a.T) + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+    // About two tokens a thread, one block per SM at most (90,000 tokens: 8.5 us a call with
+    // one or two, 10.3 with four).
+    int64_t blocks = (static_cast<int64_t>(a.T) + 2 * kPlanThreads - 1) / (2 * kPlanThreads);
     blocks = blocks < 1 ? 1 : blocks > 152 ? 152 : blocks;
     paged_plan_kernel<<<static_cast<unsigned>(blocks), kPlanThreads, smem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
