@@ -18,9 +18,11 @@
 // 16 elements (8 pairs) of a row and walks a group of heads with the eight
 // angles in registers; loads of four heads are in flight at a time, the first
 // of them while the angles are computed.  480p video q and k (671 MB read and
-// written) take 102.7 us, 6.5 TB/s, 96% of the measured copy rate; a chunk of
-// 8,192 tokens into a cache (201 MB) 39.8 us, 5.1 TB/s: its 768 blocks fill the
-// GPU 1.7 times.
+// written) take 102.6 us, 6.5 TB/s (a plain copy of as many bytes 104.6); a chunk
+// of 8,192 tokens into a cache (201 MB) 39.3 us, 5.1 TB/s (a plain copy 37.0: what
+// fits the L2 twice over does not reach the rate of long copies).  More loads in
+// flight make it slower (blocks of 128 threads, 8 an SM: 45.2; two heads a thread
+// at a time, 5 blocks an SM: 50.2; eight, 2 blocks: 39.9).
 #include <cuda_bf16.h>
 
 #include "clis_internal.h"
