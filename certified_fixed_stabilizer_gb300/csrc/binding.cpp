@@ -40,15 +40,26 @@ void ok(const char *fn, clis_status_t st)
 }
 
 // The tensor's device made current for the call, and the stream: the given one or
-// the device's current one.
+// the device's current one.  What a call with a given stream allocates belongs to
+// that stream: a block of the current stream's may still be in use there by work
+// that was queued before its last tensor was dropped.
 struct Place {
     c10::cuda::CUDAGuard guard;
+    c10::cuda::CUDAStream current;
+    c10::cuda::OptionalCUDAStreamGuard given;
     clis_stream_t stream;
     Place(const Tensor &t, std::optional<uintptr_t> raw)
-        : guard(t.device()),
-          stream(reinterpret_cast<clis_stream_t>(raw ? *raw : reinterpret_cast<uintptr_t>(
-                                                                    c10::cuda::getCurrentCUDAStream(t.device().index()).stream())))
+        : guard(t.device()), current(c10::cuda::getCurrentCUDAStream(t.device().index())),
+          stream(reinterpret_cast<clis_stream_t>(raw ? *raw : reinterpret_cast<uintptr_t>(current.stream())))
     {
+        if (raw && reinterpret_cast<cudaStream_t>(*raw) != current.stream())
+            given.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*raw), t.device().index()));
+    }
+    // A result, which the caller may read on the current stream and drop.
+    Tensor result(Tensor t) const
+    {
+        if (given.current_stream()) t.record_stream(current);
+        return t;
     }
 };
 
@@ -116,10 +127,10 @@ Rotated rope(const Tensor &q, const std::optional<Tensor> &k, const Tensor &posi
                           "k must match q in all but its number of heads");
     Place at_(q, raw);
     Rotated r;
-    r.q = q_out ? *q_out : empty_as(q);
+    r.q = q_out ? *q_out : at_.result(empty_as(q));
     if (q_out) check_like(r.q, q, "q_out");
     if (k) {
-        r.k = k_out ? *k_out : empty_as(*k);
+        r.k = k_out ? *k_out : at_.result(empty_as(*k));
         if (k_out) check_like(r.k, *k, "k_out");
     }
     clis_rope_t d = {};
@@ -226,7 +237,7 @@ std::vector<Tensor> plan(const Tensor &ctx_len, const Tensor &new_len, const Ten
     auto i64 = [](const Tensor &t) { return static_cast<int64_t *>(t.data_ptr()); };
     ok("clis_paged_plan", clis_paged_plan(&d, i32(ctx_len), i32(new_len), i32(table), i32(ring), ring.size(0),
                                           i64(ring_state), i64(state), i32(cu), i32(kv), i64(slots), i32(pos), at_.stream));
-    return {cu, kv, slots, pos, state};
+    return {at_.result(cu), at_.result(kv), at_.result(slots), at_.result(pos), at_.result(state)};
 }
 
 // --------------------------------------------------------- cache and attention
@@ -283,7 +294,7 @@ std::optional<Tensor> append(const Tensor &k, const Tensor &v, const Tensor &kc,
                           "q must match k in all but its number of heads");
         desc.H = r.Hq = q->size(1);
         if (q_out) check_like(*q_out, *q, "q_out");
-        else q_out = empty_as(*q);
+        else q_out = at_.result(empty_as(*q));
         r.q_sh = st(*q, 1), r.q_sn = st(*q, 0);
         r.qo_sh = st(*q_out, 1), r.qo_sn = st(*q_out, 0);
     }
@@ -330,17 +341,13 @@ std::vector<Tensor> attention(const Tensor &q, const Tensor &kc, const Tensor &v
     if (lse2) check_ints(*lse2, at::kFloat, {d.T, d.H}, dev, "lse2");
     Place at_(q, raw);
     if (out) check_like(*out, q, "out");
-    else out = empty_as(q);
-    if (with_lse && !lse2) lse2 = empty({d.T, d.H}, at::kFloat, dev);
+    else out = at_.result(empty_as(q));
+    if (with_lse && !lse2) lse2 = at_.result(empty({d.T, d.H}, at::kFloat, dev));
     d.q_st = st(q, 0), d.q_sh = st(q, 1);
     d.o_st = st(*out, 0), d.o_sh = st(*out, 1);
     size_t need = 0;
     ok("clis_attn_paged_workspace_size", clis_attn_paged_workspace_size(&d, max_q, &need));
-    if (!workspace) {
-        workspace = empty({static_cast<int64_t>(need)}, at::kByte, dev);
-        if (raw && need)  // allocated on the current stream, used on the given one
-            workspace->record_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*raw), dev.index()));
-    }
+    if (!workspace) workspace = empty({static_cast<int64_t>(need)}, at::kByte, dev);
     TORCH_CHECK_VALUE(workspace->device() == dev && workspace->is_contiguous(),
                       "the workspace must be contiguous and on the device of q");
     ok("clis_attn_fwd_paged",

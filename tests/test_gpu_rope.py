@@ -317,3 +317,60 @@ def test_append_past_32_bits():
     clis.paged_append(k, v, kc, vc, slots)
     for t, s in enumerate(slots.tolist()):
         assert torch.equal(kc[s // page, :, s % page], k[t]) and torch.equal(vc[s // page, :, s % page], v[t])
+
+
+def busy(n):
+    """Some milliseconds of work on the current stream."""
+    a = torch.randn((4096, 4096), device="cuda")
+    b = torch.empty_like(a)
+    for _ in range(n):
+        torch.mm(a, a, out=b)
+
+
+@pytest.mark.parametrize("op", ["rope", "append", "attention", "plan"])
+def test_given_stream_leaves_memory_that_is_still_read(op):
+    """A tensor is dropped while a copy of it waits on the current stream: its memory is
+    free for that stream's next calls, but not for a call on another stream."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    T, H, d = 5003, 8, 128
+    side = torch.cuda.Stream()
+    if op == "plan":
+        lens = [torch.tensor([n], dtype=torch.int32, device="cuda") for n in (0, 300_007)]
+        bt = torch.full((1, 1200), -1, dtype=torch.int32, device="cuda")
+        ring = torch.arange(1200, dtype=torch.int32, device="cuda")
+        state = torch.tensor([0, 1200], dtype=torch.int64, device="cuda")
+        like = torch.empty(300_007, dtype=torch.int64, device="cuda")
+        call = lambda s: clis.paged_plan(*lens, bt, ring, state, 256, 300_007, stream=s).slots
+    else:
+        like = torch.randn((T, H, d), generator=g, device="cuda").to(BF)
+        q = like.clone()
+        kc, vc = (torch.randn((20, 2, 256, d), generator=g, device="cuda").to(BF) for _ in range(2))
+        pos = torch.arange(T, device="cuda", dtype=torch.int32)[:, None]
+        inv, axis = table(64, 1)
+        cu, kv = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, T], [T]))
+        bt = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+        slots = torch.arange(T, device="cuda")
+        k, v = (torch.randn((T, 2, d), generator=g, device="cuda").to(BF) for _ in range(2))
+        if op == "rope":
+            call = lambda s: clis.clis_rope(q[None].transpose(1, 2), None, pos, inv, axis, stream=s)[0]
+        elif op == "append":
+            call = lambda s: clis.paged_append(k, v, kc, vc, slots, q=q, positions=pos, inv_freq=inv, axis=axis, stream=s)
+        else:
+            call = lambda s: clis.clis_attn_fwd_paged(q, kc, vc, bt, cu, kv, T, 0.1, stream=s)
+    busy(1)
+    want = call(None).clone()
+    side.wait_stream(torch.cuda.current_stream())
+    call(side)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        x = torch.full_like(like, 7)
+        y = torch.empty_like(x)
+        torch.cuda.synchronize()
+        busy(40)
+        y.copy_(x)
+        del x
+        got = call(side)
+        torch.cuda.synchronize()
+        assert (y == 7).all(), "the dropped tensor's memory was written before it was read"
+        assert torch.equal(got, want)
+        del got, y
