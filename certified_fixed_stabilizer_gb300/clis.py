@@ -896,7 +896,9 @@ class PagedCache:
     def begin(self, new_len, num_tokens: int) -> PagedPlan:
         """Plan of a step that adds new_len[s] tokens to sequence s (0: not part of
         the step, negative: finished, its pages are free again), ``num_tokens``
-        rows in all (rows behind the last token are padding)."""
+        rows in all (rows behind the last token are padding).  A sequence that too few
+        pages are left for stays as it was (PAGED_POOL_BIT in the device error word; its
+        rows of the step mean nothing): bring its tokens again when others have finished."""
         plan = clis_paged_plan(self.lens, new_len, self.block_table, self.ring, self.ring_state, self.page_size,
                                num_tokens)
         self.lens.copy_(plan.kv_len)

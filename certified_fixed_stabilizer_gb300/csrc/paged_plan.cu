@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 // Sums saturate here, so that lengths beyond any sense cannot wrap around.
-constexpr uint32_t kCap = 1u << 30;
+constexpr uint32_t kCap = (1u << 31) - 1;  // (beyond any number of rows)
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kCap); }  // a, b <= kCap
 
@@ -132,13 +132,22 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
     const int64_t avail = held < 0 || held > F ? 0 : held;
     const uint32_t hm = static_cast<uint32_t>(((head % F) + F) % F), tm = static_cast<uint32_t>(((tail % F) + F) % F);
     const uint32_t Fu = static_cast<uint32_t>(F);
-    // The i-th page taken in this step (-1: the ring has none left).
+    // A sequence that the ring has too few pages for, or the batch too few rows, stays as
+    // it was, and those behind it take no page either: `served` are served whatever they
+    // need, the others only if they need no page and their rows are there.
+    int served = a.S;
+    if (taken > avail) served = find(s_taken, a.S, static_cast<uint32_t>(avail));
+    if (tokens > static_cast<uint32_t>(a.T)) served = min(served, find(s_tok, a.S, static_cast<uint32_t>(a.T)));
+    const uint32_t used = s_taken[served];  // <= avail
+    auto fits = [&](int s, const Seq &q) {
+        return s < served || q.n == 0 ||
+               (q.need == q.have && s_tok[s] + static_cast<uint32_t>(q.n) <= static_cast<uint32_t>(a.T));
+    };
+    // The i-th page taken in this step, i < used.
     auto fresh = [&](uint32_t i) -> int {
-        if (i >= avail) {
-            bad |= CLIS_PAGED_POOL_BIT;
-            return -1;
-        }
-        return __ldg(a.ring + (hm + i) % Fu);
+        const int page = __ldg(a.ring + (hm + i) % Fu);
+        if (page < 0 || page >= a.num_pages) bad |= CLIS_PAGED_INDEX_BIT;
+        return page;
     };
 
     const uint32_t gtid = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
@@ -146,16 +155,17 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
         a.cu_q[s] = min(s_tok[s], static_cast<uint32_t>(a.T));
         if (s < static_cast<uint32_t>(a.S)) {
             const Seq q = read_seq(a, s);
-            a.kv_len[s] = q.gone ? 0 : q.ctx + q.n;
+            a.kv_len[s] = q.gone ? 0 : fits(s, q) ? q.ctx + q.n : q.ctx;
         }
     }
     if (gtid == 0) {
         if (tokens > static_cast<uint32_t>(a.T)) bad |= CLIS_PAGED_LENGTH_BIT;
-        a.state_out[0] = head + min(static_cast<int64_t>(taken), avail);
+        if (taken > avail) bad |= CLIS_PAGED_POOL_BIT;
+        a.state_out[0] = head + used;
         a.state_out[1] = tail + min(static_cast<int64_t>(back), F - avail);
     }
     // Pages taken go into the block tables behind the pages held.
-    for (uint32_t i = gtid; i < taken; i += step) {
+    for (uint32_t i = gtid; i < used; i += step) {
         const int s = find(s_taken, a.S, i);
         const Seq q = read_seq(a, s);
         a.block_table[s * a.bt_s + q.have + (i - s_taken[s])] = fresh(i);
@@ -168,7 +178,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
             bad |= CLIS_PAGED_POOL_BIT;
             continue;
         }
-        a.ring[(tm + i) % Fu] = a.block_table[s * a.bt_s + (i - s_back[s])];
+        const int page = a.block_table[s * a.bt_s + (i - s_back[s])];
+        if (page < 0 || page >= a.num_pages) bad |= CLIS_PAGED_INDEX_BIT;
+        a.ring[(tm + i) % Fu] = page;
     }
     // Slots and positions; rows behind the last sequence get slot -1, position 0.
     const int mask = (1 << a.page_shift) - 1;
@@ -179,14 +191,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
             const int s = find(s_tok, a.S, t);
             const Seq q = read_seq(a, s);
             pos = q.ctx + static_cast<int>(t - s_tok[s]);
-            const int col = pos >> a.page_shift;
-            // A page held is read from the table, a page taken from the ring: this
-            // launch writes the latter's table entry, the former's it leaves alone.
-            const int page = col < q.have ? a.block_table[s * a.bt_s + col] : fresh(s_taken[s] + (col - q.have));
-            if (page >= 0 && page < a.num_pages)
-                slot = (static_cast<int64_t>(page) << a.page_shift) + (pos & mask);
-            else if (col < q.have || page >= 0)
-                bad |= CLIS_PAGED_INDEX_BIT;
+            if (fits(s, q)) {
+                const int col = pos >> a.page_shift;
+                // A page held is read from the table, a page taken from the ring: this
+                // launch writes the latter's table entry, the former's it leaves alone.
+                const int page = col < q.have ? a.block_table[s * a.bt_s + col] : fresh(s_taken[s] + (col - q.have));
+                if (page >= 0 && page < a.num_pages) slot = (static_cast<int64_t>(page) << a.page_shift) + (pos & mask);
+                else bad |= CLIS_PAGED_INDEX_BIT;
+            }
         }
         a.slots[t] = slot;
         a.pos[t] = pos;

@@ -544,11 +544,16 @@ typedef struct {
  *   state_in, state_out  int64 [2]: head and tail before and after; different
  *                memory
  *   cu_q         int32 out [S + 1]: prefix sums of the new tokens
- *   kv_len       int32 out [S]: ctx + new (0 for a finished sequence)
+ *   kv_len       int32 out [S]: ctx + new (0 for a finished sequence; ctx for one
+ *                that cannot be served)
  *   slots        int64 out [T]: page * page_size + row of each new token in
- *                packed order; -1 for rows behind the last, and where the ring
- *                had no page
+ *                packed order; -1 for rows behind the last and of sequences that
+ *                cannot be served
  *   positions    int32 out [T]: the token's place in its sequence (0 behind the last)
+ * A sequence for which the ring has too few pages (CLIS_PAGED_POOL_BIT) or the batch
+ * too few rows (CLIS_PAGED_LENGTH_BIT) stays as it was: it takes no page and none of
+ * its new tokens gets a slot, nor do those of later sequences that need a page.  Their
+ * rows of this step mean nothing; their tokens can be brought again in a later one.
  * Outputs must not overlap each other or the inputs.  The same inputs give the
  * same outputs bit for bit.  One launch.  Errors: CLIS_ERR_INVALID_ARG (null
  * pointers, sizes, state_out == state_in), CLIS_ERR_UNSUPPORTED (S > 16384, T

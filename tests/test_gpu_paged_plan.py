@@ -190,3 +190,84 @@ def test_step_captured_and_replayed():
         torch.cuda.synchronize()
         assert torch.equal(out, w)
     assert torch.equal(cache.lens, eager.lens) and torch.equal(cache.block_table, eager.block_table)
+
+
+@pytest.mark.parametrize("S,page,seed", [(1, 8, 0), (6, 16, 1), (40, 8, 2), (900, 8, 3), (2000, 16, 4)])
+@pytest.mark.parametrize("short", ["pages", "rows", "both"])
+def test_what_cannot_be_served_stays_as_it_was(S, page, seed, short):
+    """Too few free pages, or rows: the sequences from the first that lacks any on take no page, and those of
+    them that need one (or rows that are not there) keep their length; nothing of them is written."""
+    rng = random.Random(seed)
+    ctx = [rng.randint(0, 6 * page) for _ in range(S)]
+    new = [rng.choice([0, 1, 2, page, 3 * page, -1]) if S > 1 else 2 * page + 1 for _ in range(S)]
+    have = [-(-c // page) for c in ctx]
+    take = [max(0, -(-(c + max(n, 0)) // page) - h) for h, c, n in zip(have, ctx, new)]
+    free = sum(take) * 2 // 3 if short != "rows" else sum(take) + 3
+    T = sum(max(n, 0) for n in new)
+    T = T * 3 // 5 if short != "pages" else T + 2
+    pages, width = sum(have) + free, 12
+    table, at = [[-1] * width for _ in range(S)], 0
+    for s in range(S):
+        table[s][:have[s]] = range(at, at + have[s])
+        at += have[s]
+    head = 5
+    size = pages + 1
+    ring = [-1] * size
+    for i in range(free):
+        ring[(head + i) % size] = at + i
+    bt, dring = i32(table), i32(ring)
+    p = clis.paged_plan(i32(ctx), i32(new), bt, dring, torch.tensor([head, head + free], dtype=torch.int64, device="cuda"),
+                        page, T, num_pages=pages)
+    cu, kv, slots, used, tail, first = [0], [], [-1] * T, 0, head + free, None
+    for s in range(S):
+        n = max(new[s], 0)
+        rows, room = cu[-1] + n <= T, used + take[s] <= free
+        if first is None and n > 0 and not (rows and room):
+            first = s
+        ok = n == 0 or (rows and (first is None or take[s] == 0))
+        if new[s] < 0:
+            for i in range(have[s]):
+                ring[tail % size] = table[s][i]
+                tail += 1
+        elif ok:
+            for i in range(take[s]):
+                table[s][have[s] + i] = ring[(head + used + i) % size]
+            used += take[s]
+            for j in range(n):
+                slots[cu[-1] + j] = table[s][(ctx[s] + j) // page] * page + (ctx[s] + j) % page
+        kv.append(0 if new[s] < 0 else ctx[s] + n if ok else ctx[s])
+        cu.append(cu[-1] + n)
+    assert first is not None
+    bit = (clis.PAGED_POOL_BIT if short != "rows" else 0) | (clis.PAGED_LENGTH_BIT if short != "pages" else 0)
+    assert clis.clis_get_device_error() == bit
+    clis.clis_clear_device_error()
+    assert p.cu_q.tolist() == [min(c, T) for c in cu] and p.kv_len.tolist() == kv and p.slots.tolist() == slots
+    assert p.ring_state.tolist() == [head + used, tail] and bt.tolist() == table and dring.tolist() == ring
+
+
+def test_a_full_cache_goes_on():
+    """Tokens that no page was left for are brought again once another sequence has finished; no page is lost."""
+    cache = clis.PagedCache(1, num_pages=6, num_kv_heads=1, d=64, max_seqs=3, max_len=64, page_size=8)
+    cache.begin(i32([16, 16, 8]), 40)
+    plan = cache.begin(i32([1, 9, 1]), 11)          # one page is left: for the first sequence
+    assert clis.clis_get_device_error() == clis.PAGED_POOL_BIT
+    clis.clis_clear_device_error()
+    assert cache.lens.tolist() == [17, 16, 8] and plan.slots.tolist()[1:] == [-1] * 10
+    plan = cache.begin(i32([-1, 0, 0]), 0)
+    plan = cache.begin(i32([0, 9, 1]), 10)
+    assert cache.lens.tolist() == [0, 25, 9] and min(plan.slots.tolist()) >= 0
+    cache.begin(i32([0, -1, -1]), 0)
+    head, tail = cache.ring_state.tolist()
+    assert tail - head == 6 and sorted(cache.ring.tolist()) == list(range(6))
+
+
+def test_what_is_no_page_is_recorded():
+    """In the ring, or given back."""
+    state = torch.tensor([0, 2], dtype=torch.int64, device="cuda")
+    for page in (-1, 4):
+        p = clis.paged_plan(i32([0]), i32([9]), i32([[-1, -1]]), i32([3, page, 0, 0]), state, 8, 9)
+        assert clis.clis_get_device_error() == clis.PAGED_INDEX_BIT and p.slots.tolist() == [24 + i for i in range(8)] + [-1]
+        clis.clis_clear_device_error()
+        clis.paged_plan(i32([9]), i32([-1]), i32([[1, page]]), i32([3, 2, 0, 0]), state, 8, 0)
+        assert clis.clis_get_device_error() == clis.PAGED_INDEX_BIT
+        clis.clis_clear_device_error()
