@@ -898,7 +898,9 @@ class PagedCache:
         the step, negative: finished, its pages are free again), ``num_tokens``
         rows in all (rows behind the last token are padding).  A sequence that too few
         pages are left for stays as it was (PAGED_POOL_BIT in the device error word; its
-        rows of the step mean nothing): bring its tokens again when others have finished."""
+        rows of the step mean nothing): bring its tokens again when others have finished.
+        So does one that would outgrow ``max_len``, rounded up to pages (PAGED_LENGTH_BIT);
+        the others go on as if it had not taken part."""
         plan = clis_paged_plan(self.lens, new_len, self.block_table, self.ring, self.ring_state, self.page_size,
                                num_tokens)
         self.lens.copy_(plan.kv_len)

@@ -37,10 +37,13 @@ __device__ __forceinline__ Sums add(const Sums &a, const Sums &b)
     return {sat_add(a.tok, b.tok), sat_add(a.taken, b.taken), sat_add(a.back, b.back)};
 }
 
-// Lengths of one sequence, brought into the range a block-table row can hold.
+// Lengths of one sequence.  The cached one is brought into the range a block-table row
+// can hold; the new tokens are counted as given, because their rows are in the packed
+// batch whether they can be served or not.
 struct Seq {
     int ctx, n, have, need;  // have, need: pages held and pages wanted
-    bool gone, bad;
+    bool gone;
+    bool full;  // the block-table row cannot hold it: not served, takes no page
 };
 
 __device__ __forceinline__ Seq read_seq(const PlanArgs &a, int s)
@@ -51,10 +54,10 @@ __device__ __forceinline__ Seq read_seq(const PlanArgs &a, int s)
     const int c = __ldg(a.ctx_len + s), n = __ldg(a.new_len + s);
     q.gone = n < 0;
     q.ctx = min(max(c, 0), cap);
-    q.n = q.gone ? 0 : min(n, cap - q.ctx);
-    q.bad = c != q.ctx || (!q.gone && n != q.n);
+    q.n = q.gone ? 0 : n;
+    q.full = c != q.ctx || q.n > cap - q.ctx;
     q.have = (q.ctx >> a.page_shift) + ((q.ctx & mask) ? 1 : 0);
-    const int total = q.ctx + q.n;
+    const int total = q.full ? q.ctx : q.ctx + q.n;
     q.need = (total >> a.page_shift) + ((total & mask) ? 1 : 0);
     return q;
 }
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
     Sums mine = {0, 0, 0};
     for (int s = s0; s < s1; s++) {
         const Seq q = read_seq(a, s);
-        if (q.bad) bad |= CLIS_PAGED_LENGTH_BIT;
+        if (q.full) bad |= CLIS_PAGED_LENGTH_BIT;
         mine = add(mine, sums_of(q));
     }
     Sums incl = mine;
@@ -134,12 +137,15 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
     const uint32_t Fu = static_cast<uint32_t>(F);
     // A sequence that the ring has too few pages for, or the batch too few rows, stays as
     // it was, and those behind it take no page either: `served` are served whatever they
-    // need, the others only if they need no page and their rows are there.
+    // need, the others only if they need no page and their rows are there.  One whose
+    // block-table row is full stays as it was too, and is nobody else's concern: it wants
+    // no page, and its rows are counted.
     int served = a.S;
     if (taken > avail) served = find(s_taken, a.S, static_cast<uint32_t>(avail));
     if (tokens > static_cast<uint32_t>(a.T)) served = min(served, find(s_tok, a.S, static_cast<uint32_t>(a.T)));
     const uint32_t used = s_taken[served];  // <= avail
     auto fits = [&](int s, const Seq &q) {
+        if (q.full) return false;
         return s < served || q.n == 0 ||
                (q.need == q.have && s_tok[s] + static_cast<uint32_t>(q.n) <= static_cast<uint32_t>(a.T));
     };

@@ -554,6 +554,9 @@ typedef struct {
  * too few rows (CLIS_PAGED_LENGTH_BIT) stays as it was: it takes no page and none of
  * its new tokens gets a slot, nor do those of later sequences that need a page.  Their
  * rows of this step mean nothing; their tokens can be brought again in a later one.
+ * A sequence whose tokens the block-table row cannot hold (ctx + new beyond width *
+ * page_size, or ctx out of range: CLIS_PAGED_LENGTH_BIT) stays as it was too, and no
+ * other sequence is concerned: cu_q counts its rows as given.
  * Outputs must not overlap each other or the inputs.  The same inputs give the
  * same outputs bit for bit.  One launch.  Errors: CLIS_ERR_INVALID_ARG (null
  * pointers, sizes, state_out == state_in), CLIS_ERR_UNSUPPORTED (S > 16384, T

@@ -271,3 +271,85 @@ def test_what_is_no_page_is_recorded():
         clis.paged_plan(i32([9]), i32([-1]), i32([[1, page]]), i32([3, 2, 0, 0]), state, 8, 0)
         assert clis.clis_get_device_error() == clis.PAGED_INDEX_BIT
         clis.clis_clear_device_error()
+
+
+@pytest.mark.parametrize("S,page,seed", [(3, 8, 0), (7, 16, 1), (60, 8, 2), (1100, 16, 3)])
+def test_a_full_table_row_concerns_nobody_else(S, page, seed):
+    """Sequences that their block-table row cannot hold (or whose cached length is out of range), among others:
+    they take no page, get no slot and keep their length; the others' rows stay where they were packed."""
+    rng = random.Random(seed)
+    width = 4
+    cap = width * page
+    ctx = [rng.choice([cap, cap, cap - 1, rng.randint(0, cap), rng.randint(0, page), 0]) for _ in range(S)]
+    new = [rng.choice([1, 1, 2, cap + 1 - c if c else cap + 1, page, 0, -1]) for c in ctx]
+    ctx[1], new[1] = cap, 1
+    if S > 50:
+        ctx[40], ctx[41], new[40], new[41] = -3, cap + 5, 2, 1   # lengths that cannot be
+    held = [min(max(c, 0), cap) for c in ctx]
+    full = [c != h or max(n, 0) > cap - h for c, h, n in zip(ctx, held, new)]
+    have = [-(-c // page) for c in held]
+    take = [0 if f else -(-(c + max(n, 0)) // page) - h for f, c, n, h in zip(full, held, new, have)]
+    pages = sum(have) + sum(take) + 2
+    table, at = [[-1] * width for _ in range(S)], 0
+    for s in range(S):
+        table[s][:have[s]] = range(at, at + have[s])
+        at += have[s]
+    free = pages - at
+    ring = list(range(at, pages)) + [-1] * at
+    T = sum(max(n, 0) for n in new) + 3
+    bt, dring = i32(table), i32(ring)
+    p = clis.paged_plan(i32(ctx), i32(new), bt, dring, torch.tensor([0, free], dtype=torch.int64, device="cuda"), page, T)
+    assert clis.clis_get_device_error() == clis.PAGED_LENGTH_BIT
+    clis.clis_clear_device_error()
+    cu, kv, slots, head, tail = [0], [], [-1] * T, 0, free
+    for s in range(S):
+        n = max(new[s], 0)
+        if new[s] < 0:
+            for i in range(have[s]):
+                ring[tail % pages] = table[s][i]
+                tail += 1
+        elif not full[s]:
+            for i in range(take[s]):
+                table[s][have[s] + i] = ring[head]
+                head += 1
+            for j in range(n):
+                slots[cu[-1] + j] = table[s][(ctx[s] + j) // page] * page + (ctx[s] + j) % page
+        kv.append(0 if new[s] < 0 else held[s] if full[s] else ctx[s] + n)
+        cu.append(cu[-1] + n)
+    assert p.cu_q.tolist() == cu and p.kv_len.tolist() == kv and p.slots.tolist() == slots
+    assert p.ring_state.tolist() == [head, tail] and bt.tolist() == table and dring.tolist() == ring
+    pos = p.positions.tolist()
+    for s in range(S):
+        if not full[s]:
+            assert pos[cu[s]:cu[s + 1]] == list(range(ctx[s], ctx[s] + max(new[s], 0)))
+
+
+def test_a_sequence_at_its_end_leaves_the_others_alone():
+    """One of three sequences reaches max_len: the others' keys, values and outputs are those of a cache without it."""
+    H, Hk, d, page = 4, 2, 64, 8
+    g = torch.Generator(device="cuda").manual_seed(21)
+    cache = clis.PagedCache(1, num_pages=30, num_kv_heads=Hk, d=d, max_seqs=3, max_len=16, page_size=page)
+    hist = [[torch.zeros(0, Hk, d, dtype=torch.bfloat16, device="cuda")] * 2 for _ in range(3)]
+    lens = [0, 0, 0]
+    for new in ([5, 15, 9], [1, 1, 1], [2, 1, 1], [1, 3, 2]):
+        T = sum(new)
+        q, k, v = (torch.randn((T, h, d), generator=g, device="cuda").to(torch.bfloat16) for h in (H, Hk, Hk))
+        plan = cache.begin(i32(new), T)
+        o = cache.attend(0, q, k, v, plan, max(new))
+        stays = [c + n > 16 for c, n in zip(lens, new)]
+        assert clis.clis_get_device_error() == (clis.PAGED_LENGTH_BIT if any(stays) else 0)
+        clis.clis_clear_device_error()
+        at, rows, seqs = 0, [], []
+        ctx = list(lens)
+        for s, n in enumerate(new):
+            if not stays[s]:
+                hist[s] = [torch.cat((t, x[at:at + n])) for t, x in zip(hist[s], (k, v))]
+                rows += range(at, at + n)
+                seqs.append(s)
+                lens[s] += n
+            at += n
+        assert cache.lens.tolist() == lens
+        check_attention(o[rows], None, {"q": q[rows], "k_cache": cache.k[0], "ctx": [ctx[s] for s in seqs],
+                                        "new": [new[s] for s in seqs], "keys": [hist[s][0] for s in seqs],
+                                        "vals": [hist[s][1] for s in seqs]})
+    assert lens[1] == 16
