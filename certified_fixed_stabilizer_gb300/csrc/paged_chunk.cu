@@ -91,6 +91,7 @@ struct ChunkParams {
     int rows_small;       // sequences of up to so many rows are the decode kernel's
     int grid, least;      // blocks; cost of a block's run, at least
     int box_rows;         // rows of a K/V TMA box: min(page size, 128)
+    int list;             // places of the list of items
     ChunkItem *items;
     unsigned long long *head;  // {items, total cost, blocks that take part}
     int *run_first;       // [grid] first item of each block's run
@@ -171,9 +172,7 @@ __global__ void __launch_bounds__(kSchedThreads) paged_chunk_schedule_kernel(con
 
     const int per = (a.S + kSchedThreads - 1) / kSchedThreads;
     const int s0 = min(a.S, tid * per), s1 = min(a.S, s0 + per);
-    auto items_of = [&](const SeqLen &q) -> int {
-        return q.n == 0 || is_decode(q, p.g, p.rows_small) ? 0 : a.Hkv * chunk_q_tiles(q.n, p.g);
-    };
+    auto items_of = [&](const SeqLen &q) -> int { return chunk_items(q, p.g, p.rows_small, a.Hkv); };
     unsigned long long mine = 0, all;
     for (int s = s0; s < s1; s++) {
         const SeqLen q = seq_len(a, s);
@@ -182,10 +181,11 @@ __global__ void __launch_bounds__(kSchedThreads) paged_chunk_schedule_kernel(con
     }
     unsigned long long run = block_scan(mine, s_warp, &all);
     for (int s = s0; s < s1; s++) {
-        s_first[s] = static_cast<int>(run);
+        s_first[s] = chunk_place(run, p.list);
         run += items_of(seq_len(a, s));
     }
-    const int W = static_cast<int>(all);
+    const int W = chunk_place(all, p.list);
+    if (all > static_cast<unsigned long long>(W)) bad |= CLIS_PAGED_LENGTH_BIT;
     if (tid == 0) s_first[a.S] = W;
     __syncthreads();
 
@@ -1252,12 +1252,7 @@ bool encode(CUtensorMap *map, const void *base, int dtype, int rank, const cuuin
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// Items, at most (each sequence rounds its query tiles up).
-int64_t max_items(const PagedArgs &a)
-{
-    const int g = a.H / a.Hkv;
-    return static_cast<int64_t>(a.Hkv) * (a.T / chunk_tokens(g) + static_cast<int64_t>(a.S) + 1);
-}
+int64_t max_items(const PagedArgs &a) { return chunk_list(a.T, a.S, a.H / a.Hkv, a.Hkv); }
 
 template <int D, int DT>
 clis_status_t launch_impl(const ChunkParams &p, cudaStream_t stream)
@@ -1314,6 +1309,7 @@ ChunkParams chunk_params(const PagedArgs &a, int rows_small, void *workspace, in
     p.grid = nsm;
     p.least = 2 * kChunkOverhead;
     p.box_rows = imin(1 << a.page_shift, BN);
+    p.list = static_cast<int>(max_items(a));  // (below 10^9, which the entry point checks)
     const size_t grid = static_cast<size_t>(nsm);
     char *w = static_cast<char *>(workspace);
     p.head = reinterpret_cast<unsigned long long *>(w);

@@ -100,6 +100,27 @@ struct __attribute__((aligned(16))) ChunkItem {
 CLIS_HD int chunk_tokens(int g) { return 2 * (kChunkRows / g); }  // tokens per item
 CLIS_HD int chunk_q_tiles(int n, int g) { return ceil_div(n, chunk_tokens(g)); }
 
+// Items of a sequence (those of up to rows_small rows are the decode kernel's).
+CLIS_HD int chunk_items(const SeqLen &s, int g, int rows_small, int Hkv)
+{
+    return s.n == 0 || is_decode(s, g, rows_small) ? 0 : Hkv * chunk_q_tiles(s.n, g);
+}
+
+// Places of the list of items: what sequences of T tokens in all need at most (each
+// rounds its query tiles up).
+CLIS_HD int64_t chunk_list(int T, int S, int g, int Hkv)
+{
+    return static_cast<int64_t>(Hkv) * (T / chunk_tokens(g) + static_cast<int64_t>(S) + 1);
+}
+
+// Place of the list for the item behind `before` others.  Prefix sums that fall let
+// sequences share rows, and then more items follow than there are places: those are left
+// out (a sequence's first place is then the list's end).
+CLIS_HD int chunk_place(uint64_t before, int64_t list)
+{
+    return static_cast<int>(before < static_cast<uint64_t>(list) ? before : static_cast<uint64_t>(list));
+}
+
 // Item r (0-based) of sequence seq; at least one key tile (its output must be written).
 CLIS_HD ChunkItem chunk_item(const SeqLen &s, int seq, int g, int r, bool causal)
 {

@@ -1,5 +1,6 @@
 """Attention over a paged cache against 64-bit softmax: every mix of single tokens, drafted
 tokens and chunks, at the sizes where tiles, pages and rows end inside one another."""
+import ctypes
 import math
 
 import pytest
@@ -333,3 +334,26 @@ def test_empty_batches():
     clis.attention_paged(b["q"], b["k_cache"], b["v_cache"], none, torch.zeros(1, dtype=torch.int32, device="cuda"),
                          none[:, 0].contiguous(), out=out)
     assert (out == 2.0).all()
+
+
+def test_prefix_sums_that_fall_stay_inside_the_workspace():
+    """Sequences that share rows make more work items than T rows can: what is beyond the list is left out and
+    recorded, nothing behind the workspace is touched, and a sound call afterwards is what it was."""
+    S, T, H, Hkv, d = 64, 2048, 32, 8, 64
+    b = make_batch([0], [T], H, Hkv, d, 64, BF, seed=61)
+    want, want_lse = run(b)
+    desc = clis.PagedDesc(S=S, T=T, H=H, Hkv=Hkv, d=d, page_size=64, num_pages=b["k_cache"].shape[0], width=b["block_table"].shape[1],
+                          q_st=H * d, q_sh=d, o_st=H * d, o_sh=d, kc_sp=Hkv * 64 * d, kc_sh=64 * d, kc_sn=d, vc_sp=Hkv * 64 * d,
+                          vc_sh=64 * d, vc_sn=d, bt_ss=b["block_table"].shape[1], dtype=0)
+    need = ctypes.c_size_t()
+    assert clis.load_library().clis_attn_paged_workspace_size(desc, T, ctypes.byref(need)) == 0
+    ws = torch.full((need.value + (1 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    cu = torch.tensor([T * (s % 2) for s in range(S + 1)], dtype=torch.int32, device="cuda")
+    kv = torch.full((S,), 90, dtype=torch.int32, device="cuda")
+    bt = b["block_table"][:, :].expand(S, -1).contiguous()
+    clis.clis_attn_fwd_paged(b["q"], b["k_cache"], b["v_cache"], bt, cu, kv, T, clis.scale_log2_for(d), workspace=ws)
+    assert clis.clis_get_device_error() == clis.PAGED_LENGTH_BIT
+    clis.clis_clear_device_error()
+    assert (ws[need.value:] == 0x5A).all()
+    o, lse2 = run(b)
+    assert torch.equal(o, want) and torch.equal(lse2, want_lse)

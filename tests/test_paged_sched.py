@@ -190,3 +190,58 @@ def test_rows_without_keys(lib):
     """Fewer keys than new tokens: the first tokens see none."""
     for n, kv in ((1, 0), (200, 0), (300, 100), (300, 299)):
         check(lib, [0], [n], 4, 2, kv=[kv])
+
+
+LISTING = r"""
+#include <vector>
+#include "%s"
+using namespace clis;
+// The list of items as the schedule kernel writes it, and what its places hold; 0: sound.
+extern "C" int check_list(int S, const int *cu, int T, int g, int rows_small, int Hkv, long long *dropped)
+{
+    const long long list = chunk_list(T, S, g, Hkv);
+    std::vector<int> first(S + 1);
+    unsigned long long run = 0;
+    for (int s = 0; s < S; s++) {
+        first[s] = chunk_place(run, list);
+        run += chunk_items(clip_seq(cu[s], cu[s + 1], 100, T, 4096), g, rows_small, Hkv);
+    }
+    const int W = first[S] = chunk_place(run, list);
+    *dropped = (long long)run - W;
+    if (W < 0 || W > list) return 1;                       // written behind the list
+    for (int i = 0, s = 0; i < W; i++) {
+        while (s < S && first[s + 1] <= i) s++;
+        if (s >= S || first[s] > i) return 2;              // no sequence has this item
+        const SeqLen q = clip_seq(cu[s], cu[s + 1], 100, T, 4096);
+        const int r = i - first[s];
+        if (r >= chunk_items(q, g, rows_small, Hkv)) return 3;
+        const ChunkItem t = chunk_item(q, s, g, r, true);
+        if (t.h < 0 || t.h >= Hkv || t.tok0 >= q.n || t.q0 + t.tok0 >= T) return 4;
+    }
+    return 0;
+}
+"""
+
+
+def test_prefix_sums_that_fall_fit_the_list(tmp_path):
+    """Prefix sums that fall let sequences share rows: every second one may have all of T.  The list of items has
+    places for T rows in all; what does not fit is left out."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    src, so = tmp_path / "l.cpp", tmp_path / "l.so"
+    src.write_text(LISTING.replace("%s", HEADER, 1))
+    subprocess.run([gxx, "-std=c++17", "-O1", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
+    L = ctypes.CDLL(str(so))
+    rng = random.Random(8)
+    for S, T, Hkv in ((64, 2048, 8), (3, 15, 2), (16384, 300, 1), (1000, 999, 3), (2, 1 << 20, 16)):
+        for g in (1, 4, 7, 128):
+            for rows in (0, 16, 32):
+                for cu in ([T * (s % 2) for s in range(S + 1)], [rng.randint(-9, T + 9) for _ in range(S + 1)],
+                           sorted(rng.randint(0, T) for _ in range(S + 1))):
+                    dropped = ctypes.c_longlong(-1)
+                    assert L.check_list(S, ints(cu), T, g, rows, Hkv, ctypes.byref(dropped)) == 0
+                    if cu == sorted(cu):
+                        assert dropped.value == 0            # sound prefix sums always fit
+    L.check_list(64, ints([2048 * (s % 2) for s in range(65)]), 2048, 4, 16, 8, ctypes.byref(dropped))
+    assert dropped.value > 7000                              # (8,192 items for 776 places)
