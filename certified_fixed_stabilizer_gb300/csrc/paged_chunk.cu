@@ -331,18 +331,20 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
     CLIS_FOR_WORK(K)
     {
         const ChunkItem &T = K.t;
-        // Page of the lane's rows of key tile kt; -2: behind the last key, not loaded.
+        // Whether the lane has rows of key tile kt to load (none behind the last key), and
+        // their page.  What the table holds is looked at when it is used, a tile later (any
+        // number can stand there, so none can say that there is nothing to load).
+        auto has_rows = [&](int kt) { return lane < npg && kt * BN + lane * p.box_rows < T.kv; };
         auto page_of = [&](int kt) -> int {
-            const int key = kt * BN + lane * p.box_rows;
-            if (lane >= npg || key >= T.kv) return -2;
-            return __ldg(a.block_table + T.s * a.bt_s + (key >> a.page_shift));
+            return has_rows(kt) ? __ldg(a.block_table + T.s * a.bt_s + ((kt * BN + lane * p.box_rows) >> a.page_shift)) : -1;
         };
-        int pg_k = page_of(K.start), pg_v = -2;
+        int pg_k = page_of(K.start), pg_v = -1;
         // Groups of loads as the MMA warp needs them: {K_0}, {V_0, K_1}, ..., {V_{n-1}}.
         for (int gi = 0; gi <= K.n; gi++) {
             const bool has_v = gi > 0, has_k = gi < K.n;
             const int nl = (has_v ? 1 : 0) + (has_k ? 1 : 0);
-            const int pg_next = gi + 1 < K.n ? page_of(K.start + gi + 1) : -2;
+            const bool rows_v = has_v && has_rows(K.start + gi - 1), rows_k = has_k && has_rows(K.start + gi);
+            const int pg_next = gi + 1 < K.n ? page_of(K.start + gi + 1) : -1;
             for (int l = 0; l < nl; l++) {
                 const uint32_t li = it + l;
                 if (!mbar_wait_warp(smem_u32(&c.kv_empty[li % C::NSTAGE]), ((li / C::NSTAGE) & 1) ^ 1, ab, err,
@@ -350,15 +352,14 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
                     goto abort;
             }
             const uint32_t bar = smem_u32(&c.kv_full[gq % C::NSTAGE]);
-            const int live = __popc(__ballot_sync(~0u, has_v && pg_v != -2)) + __popc(__ballot_sync(~0u, has_k && pg_k != -2));
+            const int live = __popc(__ballot_sync(~0u, rows_v)) + __popc(__ballot_sync(~0u, rows_k));
             if (lane == 0) mbar_arrive_expect_tx(bar, live * C::NBOX * box_bytes);
             __syncwarp();
 #pragma unroll
             for (int l = 0; l < 2; l++) {
                 const bool is_v = l == 0;
-                if (is_v ? !has_v : !has_k) continue;
+                if (is_v ? !rows_v : !rows_k) continue;
                 int pg = is_v ? pg_v : pg_k;
-                if (pg == -2) continue;
                 if (pg < 0 || pg >= a.num_pages) {
                     bad |= CLIS_PAGED_INDEX_BIT;
                     pg = static_cast<int>(a.num_pages);  // out of the map: its rows read as zeros

@@ -236,18 +236,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     const int lrow = lane / CPR, lchunk = lane % CPR;
     Pos ld = cur;
     int ld_stage = 0;
-    // Page of the lane's key of the tile that the loader is at, read one unit ahead.
+    // Page of the lane's key of the tile that the loader is at, read one unit ahead.  What
+    // the table holds is looked at when it is used (any number can stand there, so none
+    // can say that there is no key: `lane_key` does).
+    auto lane_key = [&](const Pos &q) { return q.j * C::TK + (lane & (C::TK - 1)); };
     auto page_at = [&](const Pos &q) -> int {
-        const int key = q.j * C::TK + (lane & (C::TK - 1));
-        if (q.left == 0 || key >= q.q.kv) return -2;  // nothing to load
+        const int key = lane_key(q);
+        if (q.left == 0 || key >= q.q.kv) return -1;
         return __ldg(a.block_table + q.s * a.bt_s + (key >> a.page_shift));
     };
     int page = page_at(ld);
     auto load_step = [&]() {
         if (ld.left > 0) {
-            if (page != -2 && (page < 0 || page >= a.num_pages)) {
-                bad |= CLIS_PAGED_INDEX_BIT;
-                page = -2;  // its keys read as zeros
+            if (page < 0 || page >= a.num_pages) {
+                if (lane_key(ld) < ld.q.kv) bad |= CLIS_PAGED_INDEX_BIT;
+                page = -1;  // its keys read as zeros
             }
             const uint32_t dst = ring + ld_stage * C::STAGE;
             const int key0 = ld.j * C::TK;

@@ -357,3 +357,18 @@ def test_prefix_sums_that_fall_stay_inside_the_workspace():
     assert (ws[need.value:] == 0x5A).all()
     o, lse2 = run(b)
     assert torch.equal(o, want) and torch.equal(lse2, want_lse)
+
+
+@pytest.mark.parametrize("entry", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1])
+@pytest.mark.parametrize("new", [[2], [80]])
+def test_any_page_number_out_of_range_reads_as_zeros(new, entry):
+    """Whatever the block table holds for a visible key, a number that is no page is recorded and its keys and
+    values are zeros (in the ring of the chunk kernel the tile before has left others)."""
+    b = make_batch([300], new, 4, 2, 128, 16, BF, seed=29)
+    b["block_table"][0, 11] = entry
+    o, lse2 = run(b)
+    assert clis.clis_get_device_error() == clis.PAGED_INDEX_BIT
+    clis.clis_clear_device_error()
+    b["keys"][0][176:192] = 0
+    b["vals"][0][176:192] = 0
+    check_attention(o, lse2, b)
