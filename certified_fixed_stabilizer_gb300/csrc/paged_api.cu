@@ -11,7 +11,8 @@ namespace {
 constexpr int64_t kMaxN = (int64_t(1) << 31) - 1024;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 // Keys of a sequence: a block works on at most one item's at a time, 1.5 us per 128
-// of them, while other warps wait for it with a limit of 2 s.
+// of them (0.8 s), while other warps wait for it with a limit of 2 s.  Every warp follows
+// every item, so no wait spans more than one.
 constexpr int64_t kMaxKeys = int64_t(1) << 26;
 constexpr int64_t kMaxSeqs = 16384;
 

@@ -425,6 +425,11 @@ __device__ void edge_role(const ChunkParams &p, Ctl &c, uint32_t sKV, const Run 
     CLIS_FOR_WORK(K)
     {
         const ChunkItem &T = K.t;
+        // Items without an edge tile are followed too: a wait then spans one item, however
+        // many of them come first.  (Q of the next item is not loaded before this arrival, so
+        // this phase is the barrier's last.)
+        if (!mbar_wait_warp(smem_u32(&c.q_full[0]), w & 1, ab, err, kErrEdge)) return;
+        if (lane == 0) mbar_arrive(smem_u32(&c.q_empty[0]));
         const int first = chunk_first_masked(T, p.a.causal != 0);
         // Keys that all rows, and that some row of the item sees.
         const int lim_all = visible_keys(T.n, T.kv, T.tok0, p.a.causal);
@@ -1063,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; t++) {
             mbar_init(smem_u32(&ctl.q_full[t]), 1);
-            mbar_init(smem_u32(&ctl.q_empty[t]), 1);
+            mbar_init(smem_u32(&ctl.q_empty[t]), t == 0 ? 2 : 1);  // the first: products and the edge warp
             mbar_init(smem_u32(&ctl.s_full[t]), 1);
             mbar_init(smem_u32(&ctl.p_full[t]), BM / 32);
             mbar_init(smem_u32(&ctl.pv_done[t]), 1);

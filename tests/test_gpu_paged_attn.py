@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from certified_fixed_stabilizer_gb300 import clis
-from paged_util import check_attention, make_batch
+from paged_util import HALF_STEP, check_attention, make_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -372,3 +372,41 @@ def test_any_page_number_out_of_range_reads_as_zeros(new, entry):
     b["keys"][0][176:192] = 0
     b["vals"][0][176:192] = 0
     check_attention(o, lse2, b)
+
+
+def test_a_long_run_without_edge_tiles():
+    """Seconds of keys in whole tiles (no row has a masked place among them) before the last sequence's odd length:
+    no wait of the kernel spans more than one work item.  All block tables name one page 64 times over."""
+    S, n, g, Hkv, d, page, times = 332, 64, 4, 32, 64, 65536, 64
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    kc, vc = (torch.randn((1, Hkv, page, d), generator=gen, device="cuda").to(BF) for _ in range(2))
+    q = torch.randn((S * n, g * Hkv, d), generator=gen, device="cuda").to(BF)
+    bt = torch.zeros(S, times, dtype=torch.int32, device="cuda")
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda") * n
+    kv = torch.full((S,), page * times, dtype=torch.int32, device="cuda")
+    kv[-1] -= 1
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    o, lse2 = clis.attention_paged(q, kc, vc, bt, cu, kv, n, causal=False, return_lse=True)
+    end.record()
+    torch.cuda.synchronize()
+    assert clis.clis_get_device_error() == 0
+    print(f"{start.elapsed_time(end) / 1e3:.2f} s")
+    count = torch.full((page,), float(times), dtype=torch.float64, device="cuda")
+    u = HALF_STEP[BF]
+    for s in (0, S - 1):
+        if s:
+            count[-1] -= 1
+        for h in (0, Hkv - 1):
+            rows, heads = slice(s * n, s * n + n), slice(h * g, h * g + g)
+            x = q[rows, heads].double() @ kc[0, h].double().T / 8.0
+            m = x.amax(-1, keepdim=True)
+            p = torch.exp(x - m) * count
+            L = p.sum(-1, keepdim=True)
+            want, A = p @ vc[0, h].double() / L, p @ vc[0, h].double().abs() / L
+            # as check_attention, and 32-bit sums over 2^15 key tiles: 2^-24 each of a row sum, 2^-23 of an output in each
+            # of a tile's eight products (whose sum may be cut off instead of rounded)
+            tol = u * (want.abs() + A) * 1.01 + 2e-4 * A + want.abs() * (2.0 ** 15 * 2.0 ** -24 + 2.0 ** 18 * 2.0 ** -23)
+            assert ((o[rows, heads].double() - want).abs() <= tol).all(), (s, h)
+            e = (lse2[rows, heads].double() - (m + L.log())[..., 0] / math.log(2.0)).abs().max().item()
+            assert e <= 1.5e-4 + 2.0 ** 15 * 2.0 ** -24 / math.log(2.0) + 2.0 ** -23 * 30, (s, h, e)
