@@ -126,10 +126,10 @@ clis_status_t check_attn(const clis_paged_t *p, int64_t max_q)
     if (p->q_st < p->d) return CLIS_ERR_INVALID_ARG;
     const int64_t od[2][2] = {{p->T, p->o_st}, {p->H, p->o_sh}};
     if (overlapping(p->d, od, 2)) return CLIS_ERR_INVALID_ARG;
-    // Work units and tiles are counted in 32 bits.
-    const double per = static_cast<double>(p->width) * static_cast<double>(p->page_size);
-    if (static_cast<double>(p->S) * static_cast<double>(p->Hkv) * (per / 16 + 1) >= 4.0e9)
-        return CLIS_ERR_UNSUPPORTED;
+    // What the tables can hold, in the smallest of units (S Hkv is below 2^30, a row's keys
+    // are at most 2^26).
+    const uint64_t per = static_cast<uint64_t>(p->width) * p->page_size / clis::decode_keys(128);
+    if (per > 0 && static_cast<uint64_t>(p->S) * p->Hkv > clis::kMaxUnits / per) return CLIS_ERR_UNSUPPORTED;
     const int64_t tpc = clis::chunk_tokens(static_cast<int>(p->H / p->Hkv));
     if (static_cast<double>(p->Hkv) * (static_cast<double>(p->T) / tpc + p->S + 1) >= 1.0e9) return CLIS_ERR_UNSUPPORTED;
     return CLIS_OK;

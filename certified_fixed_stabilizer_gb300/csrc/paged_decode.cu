@@ -159,9 +159,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     using C = DCfg<D>;
     const PagedArgs &a = p.a;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t s_sum[kWarps];
+    __shared__ uint64_t s_sum[kWarps];
     __shared__ int s_seq[kWarps];
-    __shared__ uint32_t s_rel[kWarps];
+    __shared__ uint64_t s_rel[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned int bad = 0;
     pdl_launch();
@@ -169,39 +169,39 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     // ---- the four warps' runs of units (neighbouring runs go to different blocks)
     const int per = (a.S + kThreads - 1) / kThreads;
     const int sb = min(a.S, tid * per), se = min(a.S, sb + per);
-    uint32_t mine = 0;
+    uint64_t mine = 0;
     for (int s = sb; s < se; s++) {
         const SeqLen q = seq_len(a, s);
         if (q.bad) bad |= CLIS_PAGED_LENGTH_BIT;
-        if (is_decode(q, p.g, p.rows_max)) mine += static_cast<uint32_t>(a.Hkv) * decode_units(q, C::TK);
+        if (is_decode(q, p.g, p.rows_max)) mine += static_cast<uint64_t>(a.Hkv) * decode_units(q, C::TK);
         else if (p.strict && q.n > 0) bad |= CLIS_PAGED_LENGTH_BIT;
     }
-    uint32_t incl = mine;
+    uint64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t up = __shfl_up_sync(~0u, incl, o);
+        const uint64_t up = __shfl_up_sync(~0u, incl, o);
         if (lane >= o) incl += up;
     }
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
-    uint32_t U = 0, before = 0;
+    uint64_t U = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; w++) {
         if (w < warp) before += s_sum[w];
         U += s_sum[w];
     }
-    const uint32_t excl = before + incl - mine;
+    const uint64_t excl = before + incl - mine;
     const int nb = decode_workers(U, p.workers, p.least);
     for (int w = 0; w < kWarps; w++) {
         const int cw = w * gridDim.x + blockIdx.x;
         if (cw >= nb) break;
-        const uint32_t u = decode_cut(U, nb, cw);
+        const uint64_t u = decode_cut(U, nb, cw);
         if (u < excl || u >= excl + mine) continue;
-        uint32_t rel = u - excl;
+        uint64_t rel = u - excl;
         for (int s = sb; s < se; s++) {
             const SeqLen q = seq_len(a, s);
             if (!is_decode(q, p.g, p.rows_max)) continue;
-            const uint32_t n = static_cast<uint32_t>(a.Hkv) * decode_units(q, C::TK);
+            const uint64_t n = static_cast<uint64_t>(a.Hkv) * decode_units(q, C::TK);
             if (rel < n) {
                 s_seq[w] = s;
                 s_rel[w] = rel;
@@ -219,13 +219,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
         pdl_wait();
         return;
     }
-    const uint32_t u0 = decode_cut(U, nb, c), u1 = decode_cut(U, nb, c + 1);
+    const uint64_t u0 = decode_cut(U, nb, c), u1 = decode_cut(U, nb, c + 1);
 
     Pos cur;
     cur.set(a, s_seq[warp]);
-    cur.h = static_cast<int>(s_rel[warp] / cur.units);
-    cur.j = static_cast<int>(s_rel[warp] % cur.units);
-    cur.left = u1 - u0;
+    cur.h = static_cast<int>(div64(s_rel[warp], cur.units));
+    cur.j = static_cast<int>(s_rel[warp] - static_cast<uint64_t>(cur.h) * cur.units);
+    cur.left = static_cast<uint32_t>(u1 - u0);
 
     // ---- loader: one stage per unit, `ld` runs NST - 1 units ahead of `cur`
     constexpr int CPR = D / 8;         // 16-byte chunks per row
@@ -485,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
             }
         if (!whole && j0 == 0 && lane == 0) {
             // The item's remaining units lie in the next workers' runs; how many workers:
-            const uint32_t end = u1 - cur.left + cur.units - 1;  // the item's last unit
-            int ce = static_cast<int>(static_cast<uint64_t>(end) * static_cast<uint32_t>(nb) / U);
+            const uint64_t end = u1 - cur.left + cur.units - 1;  // the item's last unit
+            int ce = static_cast<int>(div64(end * static_cast<uint32_t>(nb), U));
             while (ce > c && decode_cut(U, nb, ce) > end) ce--;
             while (ce + 1 < nb && decode_cut(U, nb, ce + 1) <= end) ce++;
             p.meta[c] = make_int4(ce - c + 1, q0, n, cur.h);

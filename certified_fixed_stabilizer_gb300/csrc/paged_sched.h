@@ -63,16 +63,26 @@ CLIS_HD bool is_decode(const SeqLen &s, int g, int rows_max)
 
 CLIS_HD int decode_units(const SeqLen &s, int keys) { return imax(1, ceil_div(s.kv, keys)); }
 
-// Workers that take part, for U units.
-CLIS_HD int decode_workers(uint32_t U, int grid, int least)
+// 64-bit division is slow on the GPU, and units and costs are mostly below 2^32.
+CLIS_HD uint64_t div64(uint64_t a, uint64_t b)
 {
-    const uint32_t want = (U + least - 1) / least;
-    return want < static_cast<uint32_t>(grid) ? static_cast<int>(want) : grid;
+    return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
 
-CLIS_HD uint32_t decode_cut(uint32_t U, int blocks, int c)
+// Units of a batch, at most (the entry point checks what its tables can hold): a
+// worker's run then counts in 32 bits on any GPU of more than 16 SMs (8 workers each).
+constexpr uint64_t kMaxUnits = uint64_t(1) << 39;
+
+// Workers that take part, for U units.
+CLIS_HD int decode_workers(uint64_t U, int grid, int least)
 {
-    return static_cast<uint32_t>(static_cast<uint64_t>(U) * static_cast<uint32_t>(c) / static_cast<uint32_t>(blocks));
+    const uint64_t want = div64(U + least - 1, least);
+    return want < static_cast<uint64_t>(grid) ? static_cast<int>(want) : grid;
+}
+
+CLIS_HD uint64_t decode_cut(uint64_t U, int blocks, int c)  // (U c: below 2^39 times the workers)
+{
+    return div64(U * static_cast<uint32_t>(c), static_cast<uint32_t>(blocks));
 }
 
 // ------------------------------------------------------------- chunk kernel
@@ -158,17 +168,11 @@ struct ChunkCuts {
     CLIS_HD uint64_t cut(int c) const { return run * c + rem * static_cast<uint32_t>(c) / blocks; }  // rem c < blocks^2
 };
 
-// (64-bit division is slow on the GPU, and costs are mostly below 2^32)
-CLIS_HD uint64_t chunk_div(uint64_t a, uint64_t b)
-{
-    return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-}
-
 CLIS_HD ChunkCuts chunk_cuts(uint64_t U, int blocks)
 {
     ChunkCuts k;
     k.blocks = blocks > 0 ? blocks : 1;
-    k.run = chunk_div(U, k.blocks);
+    k.run = div64(U, k.blocks);
     k.rem = static_cast<uint32_t>(U - k.run * k.blocks);
     return k;
 }
@@ -176,7 +180,7 @@ CLIS_HD ChunkCuts chunk_cuts(uint64_t U, int blocks)
 // Block whose run holds place x < U.
 CLIS_HD int chunk_block_of(const ChunkCuts &k, uint64_t x)
 {
-    const uint64_t g = k.run > 0 ? chunk_div(x, k.run) : x;
+    const uint64_t g = k.run > 0 ? div64(x, k.run) : x;
     int c = static_cast<int>(g < k.blocks ? g : k.blocks - 1);
     while (c > 0 && k.cut(c) > x) c--;
     while (c + 1 < static_cast<int>(k.blocks) && k.cut(c + 1) <= x) c++;

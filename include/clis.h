@@ -507,6 +507,9 @@ CLIS_API clis_status_t clis_rope(const clis_rope_t *desc, const void *q, const v
  *   page_size  a power of two, 8 .. 65536
  *   width      block-table columns; width * page_size (keys of a sequence, at
  *              most) up to 2^26
+ * Attention also wants S * Hkv * width * page_size up to 2^43 (16,384 sequences of
+ * 2^26 keys and 8 heads) and Hkv * (S + 1 + T / t) below 10^9, with the 2 * (128 / (H /
+ * Hkv)) tokens t of a work item.
  * Lengths, tables, slots and page numbers live on the device, so one captured
  * graph serves every step; what is out of range there is not followed: it sets
  * a bit in the device error word (CLIS_PAGED_*) and reads as zeros, is not

@@ -410,3 +410,28 @@ def test_a_long_run_without_edge_tiles():
             assert ((o[rows, heads].double() - want).abs() <= tol).all(), (s, h)
             e = (lse2[rows, heads].double() - (m + L.log())[..., 0] / math.log(2.0)).abs().max().item()
             assert e <= 1.5e-4 + 2.0 ** 15 * 2.0 ** -24 / math.log(2.0) + 2.0 ** -23 * 30, (s, h, e)
+
+
+def test_the_largest_table():
+    """16,384 sequences whose table rows could hold 2^26 keys each, with 8 key/value heads; they hold a few."""
+    S, Hkv, d, page = 16384, 8, 64, 65536
+    g = torch.Generator(device="cuda").manual_seed(73)
+    kc, vc = (torch.randn((2, Hkv, page, d), generator=g, device="cuda").to(BF) for _ in range(2))
+    bt = torch.full((S, 1024), 0x3FFFFFFF, dtype=torch.int32, device="cuda")
+    bt[:, 0] = torch.arange(S, device="cuda") % 2
+    for n in (1, 3):                      # single tokens; few sequences with chunks among them
+        new = torch.ones(S, dtype=torch.int64) if n == 1 else torch.zeros(S, dtype=torch.int64)
+        if n > 1:
+            new[[5, 700, 16383]] = torch.tensor([40, 1, 130])
+        cu = torch.cat((torch.zeros(1, dtype=torch.int64), new.cumsum(0))).to(torch.int32).cuda()
+        kv = (torch.arange(S) % 37 + new).to(torch.int32).cuda()
+        T = int(new.sum())
+        q = torch.randn((T, Hkv, d), generator=g, device="cuda").to(BF)
+        o, lse2 = clis.attention_paged(q, kc, vc, bt, cu, kv, int(new.max()), return_lse=True)
+        for s in (0, 1, 5, 36, 700, 8191, 16382, 16383):
+            r, m, c = cu[s].item(), int(new[s]), s % 37
+            if m == 0:
+                continue
+            check_attention(o[r:r + m], lse2[r:r + m], {"q": q[r:r + m], "k_cache": kc, "ctx": [c], "new": [m],
+                                                       "keys": [kc[s % 2, :, :c + m].transpose(0, 1)],
+                                                       "vals": [vc[s % 2, :, :c + m].transpose(0, 1)]})

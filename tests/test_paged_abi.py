@@ -8,7 +8,7 @@ import torch
 from certified_fixed_stabilizer_gb300 import clis
 
 FAKE = 1 << 20  # never followed: every call below is refused, or has nothing to do
-OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = 0, 1, 2, 3, 4
+OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA = 0, 1, 2, 3, 4, 5
 
 
 def rope_desc(**kw):
@@ -158,3 +158,15 @@ def test_python_refusals():
         clis.paged_plan(axis, axis, pos[0], axis, axis.long()[:2], 16, 4)
     with pytest.raises(ValueError):
         clis.attention(cpu, cpu, cpu, rope=clis.Rope(pos, inv, axis))
+
+
+def test_the_sizes_together():
+    """The limits of clis_paged_t hold together as documented: sequences x key/value heads x a table row's keys up to 2^43."""
+    big = dict(S=16384, T=16384, H=8, Hkv=8, q_st=1024, o_st=1024, page_size=65536, width=1024, bt_ss=1024, num_pages=64,
+               kc_sn=128, kc_sh=1 << 23, kc_sp=1 << 26, vc_sn=128, vc_sh=1 << 23, vc_sp=1 << 26)
+    for d in (64, 128):
+        # (no workspace: refused for that, once all sizes have been accepted)
+        assert attn(paged_desc(**{**big, "d": d}), ws=None, ws_bytes=0) in (WORKSPACE, CUDA), d
+        assert attn(paged_desc(**{**big, "d": d, "width": 512, "Hkv": 16, "H": 16, "q_st": 2048, "o_st": 2048}), ws=None,
+                    ws_bytes=0) in (WORKSPACE, CUDA), d
+        assert attn(paged_desc(**{**big, "d": d, "Hkv": 9, "H": 9, "q_st": 2048, "o_st": 2048})) == UNSUPPORTED, d

@@ -245,3 +245,40 @@ def test_prefix_sums_that_fall_fit_the_list(tmp_path):
                         assert dropped.value == 0            # sound prefix sums always fit
     L.check_list(64, ints([2048 * (s % 2) for s in range(65)]), 2048, 4, 16, 8, ctypes.byref(dropped))
     assert dropped.value > 7000                              # (8,192 items for 776 places)
+
+
+MANY_UNITS = r"""
+#include "%s"
+using namespace clis;
+extern "C" int check_units(unsigned long long U, int workers)
+{
+    const int nb = decode_workers(U, workers, 2);
+    if (nb < 1 || nb > workers) return 1;
+    uint64_t at = 0;
+    for (int c = 0; c < nb; c++) {
+        const uint64_t a = decode_cut(U, nb, c), b = decode_cut(U, nb, c + 1);
+        if (a != at || b <= a) return 2;
+        if (b - a > 0xFFFFFFFFull) return 3;   // a run counts in 32 bits
+        at = b;
+    }
+    return at == U ? 0 : 4;
+}
+extern "C" unsigned long long max_units() { return kMaxUnits; }
+"""
+
+
+def test_units_past_32_bits(tmp_path):
+    """What the documented sizes can add up to is shared out without wrapping round."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    src, so = tmp_path / "u.cpp", tmp_path / "u.so"
+    src.write_text(MANY_UNITS.replace("%s", HEADER, 1))
+    subprocess.run([gxx, "-std=c++17", "-O1", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
+    L = ctypes.CDLL(str(so))
+    L.check_units.argtypes = [ctypes.c_ulonglong, ctypes.c_int]
+    L.max_units.restype = ctypes.c_ulonglong
+    assert L.max_units() >= 16384 * 8 * (2 ** 26 // 16)
+    for workers in (8 * 17, 8 * 152):
+        for U in (1, 2, 2433, 2 ** 32 - 1, 2 ** 32, 2 ** 32 + 1, 5 * 10 ** 9, 2 ** 39 - 1, 2 ** 39):
+            assert L.check_units(U, workers) == 0, (U, workers)
