@@ -78,32 +78,75 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, TORCH_EXT)
 
 
-def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(TORCH_EXT)):
+def _older(out: str, deps) -> bool:
+    if not os.path.exists(out):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_EXT))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(HERE, "..", "include", "clis.h"))
+    t = os.path.getmtime(out)
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+HEADER = os.path.join(HERE, "..", "include", "clis.h")
+
+
+def _stale() -> bool:
+    """libclis.so is missing or older than one of its sources."""
+    return _older(LIB, [HEADER, *(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "binding.cpp")])
+
+
+def _torch_tag() -> str:
+    """The torch and Python that a binding is built against: it only fits these."""
+    import sysconfig
+
+    import torch
+    return f"{torch.__version__} abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}"
+
+
+def _binding_stale() -> bool:
+    """_clis_torch.so is missing, older than its source, or built against another torch."""
+    if _older(TORCH_EXT, [HEADER, os.path.join(CSRC, "binding.cpp")]):
+        return True
+    try:
+        with open(TORCH_EXT + ".torch") as f:
+            return f.read() != _torch_tag()
+    except OSError:
+        return True
+
+
+def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """libclis.so, which needs no torch."""
     if not force and not verbose_ptxas and not _stale():
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(OBJ_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), SOURCES))
-        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding)
     return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    """_clis_torch.so (and libclis.so, which it links)."""
+    if force or _binding_stale():
+        os.makedirs(OBJ_DIR, exist_ok=True)
+        with cf.ThreadPoolExecutor(max_workers=1) as ex:
+            obj = ex.submit(_compile_binding)
+            build_library(force)
+            _link_binding(obj.result())
+        with open(TORCH_EXT + ".torch", "w") as f:
+            f.write(_torch_tag())
+    return TORCH_EXT
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    if verbose_ptxas:
+        build_library(True, True)
+    build_binding(force and not verbose_ptxas)
+    return build_library()
 
 
 if __name__ == "__main__":

@@ -64,7 +64,17 @@ class PagedDesc(ctypes.Structure):
 
 
 _lib = None
-_native = None  # the torch binding of the calls around a paged cache (csrc/binding.cpp)
+
+
+class _Unloaded:
+    """Stands for the torch binding of the calls around a paged cache (csrc/binding.cpp)
+    until the first of them loads it.  Everything else needs libclis.so alone."""
+
+    def __getattr__(self, name):
+        return getattr(load_binding(), name)
+
+
+_native = _Unloaded()
 
 
 def library_path() -> str:
@@ -72,14 +82,13 @@ def library_path() -> str:
 
 
 def load_library():
-    """Load libclis.so and its torch binding (building them first when nvcc is available
-    and they are stale)."""
-    global _lib, _native
+    """Load libclis.so (building it first when nvcc is available and it is stale)."""
+    global _lib
     if _lib is not None:
         return _lib
     path = _build.LIB
     if not os.path.exists(path) or _build._stale():
-        _build.build()
+        _build.build_library()
     lib = ctypes.CDLL(path)
     vp, i32, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     sp = ctypes.POINTER(Shape)
@@ -143,12 +152,23 @@ def load_library():
     lib.clis_attn_paged_workspace_size.restype = i32
     lib.clis_attn_fwd_paged.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, i64, f32, i32, vp, sz, vp]
     lib.clis_attn_fwd_paged.restype = i32
-    spec = importlib.util.spec_from_file_location("_clis_torch", _build.TORCH_EXT)
-    _native = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(_native)
-    _native.set_error_class(ClisError)
     _lib = lib
     return lib
+
+
+def load_binding():
+    """Load the torch binding of rope, paged_plan, paged_append and attention_paged
+    (building it first when it is missing, older than its source or built against another
+    torch; there is no fallback: without it these calls raise)."""
+    global _native
+    if isinstance(_native, _Unloaded):
+        path = _build.build_binding()
+        spec = importlib.util.spec_from_file_location("_clis_torch", path)
+        native = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(native)
+        native.set_error_class(ClisError)
+        _native = native
+    return _native
 
 
 def _ptr(t):
