@@ -597,7 +597,8 @@ def attention(q, k, v, softmax_scale: float | None = None, causal: bool = False,
     """CLiS attention forward: certification pre-pass, then the fused kernel.
 
     ``rope`` (device tensors): q and k are rotated by their positions first
-    (:func:`rope_qk`); the certificate is that of the rotated heads.
+    (:func:`rope_qk`); the certificate is that of the rotated heads.  No autograd graph is
+    recorded, with or without it: see :func:`attention_autograd`.
 
     q, k, v: bf16 or fp16 [B, H, N, d].  Device tensors are processed in place
     on the current stream.  Host tensors (pinned for overlap) go through the
@@ -810,7 +811,8 @@ def clis_rope(q, k, positions, inv_freq, axis, interleaved: bool = False, invers
 
 
 def rope(q, k, positions, inv_freq, axis, interleaved: bool = False):
-    """(q', k'): q and k (or None) rotated by their positions; see :class:`Rope`."""
+    """(q', k'): q and k (or None) rotated by their positions; see :class:`Rope`.  No
+    autograd graph is recorded, whatever q and k want: see :func:`rope_autograd`."""
     return _native.rope(q, k, positions, inv_freq, axis, interleaved, False, None, None, None)
 
 
@@ -818,7 +820,8 @@ rope_qk = rope  # (for the functions that have an argument of that name)
 
 
 def rope_autograd(q, k, positions, inv_freq, axis, interleaved: bool = False):
-    """Differentiable :func:`rope` (training): the gradient is the rotation back.
+    """Differentiable :func:`rope` (training): the gradient is the rotation back.  Only q
+    and k have one; an ``inv_freq`` that requires a gradient is refused (ValueError).
     A backward pass may be captured in a graph while no eager graph of the same
     leaves is alive (torch ties a leaf's gradient to the stream of its first use)."""
     return _native.rope_autograd(q, k, positions, inv_freq, axis, interleaved)

@@ -160,7 +160,7 @@ Rotated rope(const Tensor &q, const std::optional<Tensor> &k, const Tensor &posi
 }
 
 // The rotation as an autograd node: its gradient is the rotation back, itself
-// differentiable.  The angles carry no gradient.
+// differentiable.  The angles carry no gradient; an inv_freq that wants one is refused.
 struct RopeNode : torch::autograd::Function<RopeNode> {
     static torch::autograd::variable_list forward(torch::autograd::AutogradContext *ctx, const Tensor &q,
                                                   const std::optional<Tensor> &k, const Tensor &positions,
@@ -458,7 +458,10 @@ PyObject *py_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
 PyObject *py_rope_autograd(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return call(n, 6, [&] {
-        auto r = RopeNode::apply(tensor(a[0], "q"), maybe(a[1], "k"), tensor(a[2], "positions"), tensor(a[3], "inv_freq"),
+        const Tensor inv_freq = tensor(a[3], "inv_freq");
+        TORCH_CHECK_VALUE(!(inv_freq.requires_grad() && at::GradMode::is_enabled()),
+                          "inv_freq gets no gradient from the rotation: detach it");
+        auto r = RopeNode::apply(tensor(a[0], "q"), maybe(a[1], "k"), tensor(a[2], "positions"), inv_freq,
                                  tensor(a[4], "axis"), truth(a[5]), false);
         return wrap({r[0], r.size() > 1 ? r[1] : Tensor()});
     });

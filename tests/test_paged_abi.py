@@ -170,3 +170,16 @@ def test_the_sizes_together():
         assert attn(paged_desc(**{**big, "d": d, "width": 512, "Hkv": 16, "H": 16, "q_st": 2048, "o_st": 2048}), ws=None,
                     ws_bytes=0) in (WORKSPACE, CUDA), d
         assert attn(paged_desc(**{**big, "d": d, "Hkv": 9, "H": 9, "q_st": 2048, "o_st": 2048})) == UNSUPPORTED, d
+
+
+def test_angles_have_no_gradient():
+    """An inv_freq that wants a gradient would silently get none: refused (unless nothing is recorded anyway)."""
+    x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    pos, axis = torch.zeros(4, 1, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    inv = torch.ones(8, dtype=torch.float64, requires_grad=True)
+    with pytest.raises(ValueError, match="inv_freq gets no gradient"):
+        clis.rope_autograd(x, None, pos, inv, axis)
+    with pytest.raises(ValueError, match="inv_freq gets no gradient"):
+        clis.attention_autograd(x, x, x, rope=clis.Rope(pos, inv, axis))
+    with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):  # (the next check: these are host tensors)
+        clis.rope_autograd(x, None, pos, inv, axis)
