@@ -5,7 +5,10 @@
 //   x_ij = scale_log2 * q_i . k_j,  o_i = sum_j 2^(x_ij - m_i) v_j / sum_j 2^(x_ij - m_i)
 //
 // over the keys j < visible(i), with the running shift m_i raised only when a
-// row's maximum outgrew it by 2^8.
+// row's maximum outgrew it by 2^8.  The weights are rounded to the data type as the
+// tensor cores take them (off by up to 2^-8 of each in bf16, 2^-11 in fp16, where the
+// shift stands 2^7 below the maximum: weight_room in paged_sched.h); row sums add the
+// unrounded ones, and O, m and l stay in fp32.
 //
 // Bound: the tensor cores (4 d flops per row and visible key), then exp2 on the
 // MUFU.  An item is two 128-row tiles against the keys they see; a row tile packs
@@ -716,12 +719,13 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
                     mx[q4] = fmax3(mx[q4], __uint_as_float(s[cc + 2 * q4]), __uint_as_float(s[cc + 2 * q4 + 1]));
             }
             const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-            const bool grow = m_tile > m_run + kTau;  // always true where a row's first visible key is
+            const bool grow = m_tile > m_run + (kTau + weight_room(DT));  // always true where a row's first visible key is
             if (__any_sync(0xFFFFFFFFu, grow) || !begun) {
                 // Raise the shift, compute the tile's weights (again), and shrink O once the
                 // last product is in it.
-                const float alpha = grow ? ex2_approx(m_run - m_tile) : 1.f;
-                if (grow) m_run = m_tile;
+                const float m_new = m_tile - weight_room(DT);
+                const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
+                if (grow) m_run = m_new;
                 l_run *= alpha;
                 l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
                 if (begun) {

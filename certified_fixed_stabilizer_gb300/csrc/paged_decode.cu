@@ -23,9 +23,10 @@
 //    item, so item ends do not drain it.  Rows past the length are filled with
 //    zeros by the copy itself: what a page holds behind the last key is never
 //    multiplied (0 * NaN would be NaN).
-//  * P is rounded to the data type (bf16: off by up to 2^-8 of each weight) as
-//    the matrix instructions take it; the row sum adds the unrounded values,
-//    and o, m, l stay in fp32.
+//  * P is rounded to the data type as the matrix instructions take it (off by up to
+//    2^-8 of each weight in bf16, 2^-11 in fp16); the row sum adds the unrounded values,
+//    and o, m, l stay in fp32.  fp16 ends at 2^-24, so there the shift stands 2^7 below
+//    the row's maximum and weights reach up to 2^15 (weight_room in paged_sched.h).
 //
 // 64 requests of 1,000 to 16,000 keys (8 key/value heads, d = 128, 2.13 GB): 306 us
 // and 5 us for the join, 6.8 TB/s, the measured copy rate.
@@ -371,16 +372,17 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
                     mx[mt][hf] = v * sl2;
-                    grow |= mx[mt][hf] > m_run[mt][hf] + kTau;
+                    grow |= mx[mt][hf] > m_run[mt][hf] + (kTau + weight_room(DT));
                 }
             if (__any_sync(~0u, grow)) {
 #pragma unroll
                 for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                     for (int hf = 0; hf < 2; hf++) {
-                        if (mx[mt][hf] > m_run[mt][hf] + kTau) {
-                            const float al = ex2_approx(m_run[mt][hf] - mx[mt][hf]);
-                            m_run[mt][hf] = mx[mt][hf];
+                        if (mx[mt][hf] > m_run[mt][hf] + (kTau + weight_room(DT))) {
+                            const float m = mx[mt][hf] - weight_room(DT);
+                            const float al = ex2_approx(m_run[mt][hf] - m);
+                            m_run[mt][hf] = m;
                             l_run[mt][hf] *= al;
 #pragma unroll
                             for (int i = 0; i < D / 8; i++) {

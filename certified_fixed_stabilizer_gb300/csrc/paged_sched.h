@@ -46,6 +46,13 @@ CLIS_HD int visible_keys(int n, int kv, int t, bool causal)
     return causal ? imin(kv, imax(kv - n + t + 1, 0)) : kv;
 }
 
+// How far the shift of a row's weights 2^(x - shift) stands below the row's maximum
+// (dt: 0 bf16, 1 fp16), in powers of two.  fp16 holds 2^-24 to 65504: with the shift at
+// the maximum, many weights below 2^-25 of the largest vanish although the row sum counts
+// them (262,143 of 2^-25.5 are 0.5% of a row).  The maximum may outgrow the shift by 2^8
+// before it is raised; 2^7 more still fit, and weights down to 2^-32 count.
+CLIS_HD constexpr float weight_room(int dt) { return dt ? 7.f : 0.f; }
+
 // ------------------------------------------------------------ decode kernel
 //
 // Items are (sequence, key/value head), sequence-major; an item costs one unit

@@ -602,6 +602,9 @@ CLIS_API clis_status_t clis_attn_paged_workspace_size(const clis_paged_t *desc, 
  * where the batch is small).  The softmax is
  * online with a lazily raised shift, as CLIS_ONLINE_LAZY: a certificate would
  * have to read all keys first, which for a few query rows is the whole cost.
+ * Scores, row sums and outputs are held in fp32; the weights 2^(x_ij - shift) are rounded
+ * to the data type before they multiply v, as the dense calls do it: off by up to 2^-8
+ * of each in bf16, 2^-11 in fp16 (there at least 2^-32 of the row's largest).
  *   q          device [T, H, d] (q_st, q_sh)
  *   k_cache, v_cache, block_table, cu_q (int32 [S + 1], from 0 on, not falling),
  *              kv_len (int32 [S]): see clis_paged_t

@@ -435,3 +435,28 @@ def test_the_largest_table():
             check_attention(o[r:r + m], lse2[r:r + m], {"q": q[r:r + m], "k_cache": kc, "ctx": [c], "new": [m],
                                                        "keys": [kc[s % 2, :, :c + m].transpose(0, 1)],
                                                        "vals": [vc[s % 2, :, :c + m].transpose(0, 1)]})
+
+
+@pytest.mark.parametrize("S,n,H", [(1300, 1, 1), (320, 40, 4)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_many_small_weights_beside_a_large_one(S, n, H, dtype):
+    """One key far above 262,143 others, whose weights are 2^-25.5 of its own each: together 0.6%.  Enough sequences
+    that none is shared out, so that all of a row's weights are taken with one shift."""
+    d, page, N = 64, 65536, 262144
+    kc, vc = torch.zeros(4, 1, page, d, dtype=dtype, device="cuda"), torch.ones(4, 1, page, d, dtype=dtype, device="cuda")
+    q = torch.zeros(S * n, H, d, dtype=dtype, device="cuda")
+    q[..., 0] = 8.0
+    kc[0, 0, 0, 0] = 17.625
+    vc[0, 0, 0] = 0.0
+    bt = torch.arange(4, dtype=torch.int32, device="cuda").expand(S, 4).contiguous()
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda") * n
+    kv = torch.full((S,), N, dtype=torch.int32, device="cuda")
+    o = clis.attention_paged(q, kc, vc, bt, cu, kv, n, causal=False)
+    top = 8.0 * 17.625 / 8.0 / math.log(2.0)
+    L = 1.0 + (N - 1) * 2.0 ** -top
+    want = (N - 1) * 2.0 ** -top / L
+    u = HALF_STEP[dtype]
+    # as check_attention, with A = o here; weights below 2^-14 of 2^7 times the largest lose up to 2^-25: 2^-32 of it each
+    tol = 2 * u * want * 1.01 + 2e-4 * want + ((N - 1) / L * 2.0 ** -32 + 2.0 ** -25 if dtype == FP else 0)
+    err = (o.double() - want).abs().max().item()
+    assert err <= tol, f"off by {err:.2e} of {want:.2e}, {err / tol:.1f} times the bound"
