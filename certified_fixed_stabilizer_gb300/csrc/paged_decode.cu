@@ -307,11 +307,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                 }
             }
         float o[MT][D / 8][4];
-        float m_run[MT][2], l_run[MT][2];
+        float m_run[MT][2], l_run[MT][2], l_low[MT][2];  // l_low: what the last addition to l_run gained by rounding
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
             m_run[mt][0] = m_run[mt][1] = -INFINITY;
-            l_run[mt][0] = l_run[mt][1] = 0.f;
+            l_run[mt][0] = l_run[mt][1] = l_low[mt][0] = l_low[mt][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 8; i++) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
         }
@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                             const float al = ex2_approx(m_run[mt][hf] - m);
                             m_run[mt][hf] = m;
                             l_run[mt][hf] *= al;
+                            l_low[mt][hf] *= al;
 #pragma unroll
                             for (int i = 0; i < D / 8; i++) {
                                 o[mt][i][2 * hf] *= al;
@@ -398,13 +399,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
                     const float ns = m_run[mt][hf] == -INFINITY ? 0.f : -m_run[mt][hf];
+                    float l = 0.f;
 #pragma unroll
                     for (int i = 0; i < NB; i++) {
                         const float p0 = ex2_approx(fmaf(s[mt][i][2 * hf], sl2, ns));
                         const float p1 = ex2_approx(fmaf(s[mt][i][2 * hf + 1], sl2, ns));
-                        l_run[mt][hf] += p0 + p1;
+                        l += p0 + p1;
                         pf[mt][i >> 1][2 * (i & 1) + hf] = pack2<DT>(p0, p1);
                     }
+                    // Compensated: a run may be many thousands of units, each far below the sum.
+                    const float y = l - l_low[mt][hf], t = l_run[mt][hf] + y;
+                    l_low[mt][hf] = (t - l_run[mt][hf]) - y;
+                    l_run[mt][hf] = t;
                 }
             // O += P V
             {

@@ -460,3 +460,26 @@ def test_many_small_weights_beside_a_large_one(S, n, H, dtype):
     tol = 2 * u * want * 1.01 + 2e-4 * want + ((N - 1) / L * 2.0 ** -32 + 2.0 ** -25 if dtype == FP else 0)
     err = (o.double() - want).abs().max().item()
     assert err <= tol, f"off by {err:.2e} of {want:.2e}, {err / tol:.1f} times the bound"
+
+
+@pytest.mark.parametrize("S,n,H", [(1300, 1, 1), (320, 40, 4)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("d", [64, 128])
+def test_row_sums_of_many_small_weights(S, n, H, dtype, d):
+    """262,143 weights of 2^-25.5 beside one of 1 are 0.008 of lse2, and more than the weights' own steps:
+    32-bit sums that add them one unit at a time must not lose them."""
+    page, N = 65536, 262144
+    kc = torch.zeros(4, 1, page, d, dtype=dtype, device="cuda")
+    q = torch.zeros(S * n, H, d, dtype=dtype, device="cuda")
+    q[..., 0] = 8.0
+    kc[0, 0, 0, 0] = 17.625
+    bt = torch.arange(4, dtype=torch.int32, device="cuda").expand(S, 4).contiguous()
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda") * n
+    kv = torch.full((S,), N, dtype=torch.int32, device="cuda")
+    _, lse2 = clis.attention_paged(q, kc, kc, bt, cu, kv, n, softmax_scale=0.125, causal=False, return_lse=True)
+    top = 8.0 * 17.625 / 8.0 / math.log(2.0)
+    want = top + math.log2(1.0 + (N - 1) * 2.0 ** -top)
+    # as check_attention; the chunk kernel adds a key tile's sum at a time: half a step of the row sum each
+    tol = 1.5e-4 + 2.0 ** -23 * top + (N / 128 * 2.0 ** -24 / math.log(2.0) if n > 1 else 0)
+    err = (lse2.double() - want).abs().max().item()
+    assert err <= tol, f"off by {err:.2e}, {err / tol:.1f} times the bound"
