@@ -727,6 +727,8 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
                 const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
                 if (grow) m_run = m_new;
                 l_run *= alpha;
+                // (stores to TMEM are asynchronous: the weights that these replace must be in place)
+                if (begun) tmem_wait_st();
                 l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
                 if (begun) {
                     if (!mbar_wait(smem_u32(&c.pv_done[t]), (g - 1) & 1, ab, err, kErrSoftmax)) return;
