@@ -483,3 +483,49 @@ def test_row_sums_of_many_small_weights(S, n, H, dtype, d):
     tol = 1.5e-4 + 2.0 ** -23 * top + (N / 128 * 2.0 ** -24 / math.log(2.0) if n > 1 else 0)
     err = (lse2.double() - want).abs().max().item()
     assert err <= tol, f"off by {err:.2e}, {err / tol:.1f} times the bound"
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.02, 0.37])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (FP, 64)])
+def test_softmax_scales(scale, dtype, d):
+    """Scales other than 1 / sqrt(d), single tokens and chunks; large ones make one weight of a row stand out."""
+    for new in ([1, 2, 1], [1, 130, 0]):
+        b = make_batch([300, 70, 900], new, 8, 2, d, 32, dtype, seed=81)
+        b["q"] = (b["q"].float() * (1.0 / (8.0 * scale))).to(dtype)   # scores of the usual size, which the bounds are for
+        o, lse2 = run(b, softmax_scale=scale)
+        check_attention(o, lse2, b, scale=scale)
+
+
+@pytest.mark.parametrize("page", [512, 4096, 65536])
+@pytest.mark.parametrize("new", [[1, 3], [200, 1]])
+def test_large_pages(page, new):
+    b = make_batch([700, page + 100], new, 4, 2, 128, page, BF, seed=83)
+    check_attention(*run(b), b)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_the_longest_sequence(n, dtype):
+    """2^26 - 3 keys (one page, 1,024 times over) in one sequence, shared out over the whole GPU."""
+    page, times, d = 65536, 1024, 64
+    gen = torch.Generator(device="cuda").manual_seed(85)
+    kc, vc = (torch.randn((1, 1, page, d), generator=gen, device="cuda").to(dtype) for _ in range(2))
+    q = torch.randn((n, 4, d), generator=gen, device="cuda").to(dtype)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    o, lse2 = clis.attention_paged(q, kc, vc, torch.zeros(1, times, dtype=torch.int32, device="cuda"), i32([0, n]),
+                                   i32([page * times - 3]), n, causal=True, return_lse=True)
+    count = torch.full((n, page), float(times), dtype=torch.float64, device="cuda")
+    for i in range(n):                                  # query i is key 2^26 - 3 - n + i
+        count[i, page - 3 - n + i + 1:] -= 1
+    x = q.double().transpose(0, 1) @ kc[0, 0].double().T / 8.0
+    m = x.amax(-1, keepdim=True)
+    p = torch.exp(x - m) * count
+    L = p.sum(-1, keepdim=True)
+    v = vc[0, 0].double()
+    want, A = ((p @ t / L).transpose(0, 1) for t in (v, v.abs()))
+    u = HALF_STEP[dtype]
+    # as check_attention; 32-bit sums: a run is at most 2^26 / 152 keys, 16 to a product, each of which may cut off 2^-23
+    tol = u * (want.abs() + A) * 1.01 + 2e-4 * A + want.abs() * (2.0 ** 26 / 152 / 16 * 2.0 ** -23) + 2.0 ** -25
+    assert ((o.double() - want).abs() <= tol).all()
+    e = (lse2.double() - ((m + L.log())[..., 0] / math.log(2.0)).transpose(0, 1)).abs().max().item()
+    assert e <= 1.5e-4 + 2.0 ** -23 * 32 + 2.0 ** 26 / 152 / 128 * 2.0 ** -24 / math.log(2.0), e

@@ -374,3 +374,19 @@ def test_given_stream_leaves_memory_that_is_still_read(op):
         assert (y == 7).all(), "the dropped tensor's memory was written before it was read"
         assert torch.equal(got, want)
         del got, y
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_gradients_in_fp16(interleaved):
+    """Against the formula, with the positions of a long text, all pairs and part of them."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    B, H, Hk, N, d = 1, 3, 1, 77, 128
+    for pairs in (64, 24):
+        q, k = (torch.randn((B, h, N, d), generator=g, device="cuda").to(FP).requires_grad_() for h in (H, Hk))
+        gq, gk = (torch.randn((B, h, N, d), generator=g, device="cuda").to(FP) for h in (H, Hk))
+        pos = torch.randint(0, 10 ** 6, (N, 1), generator=g, device="cuda", dtype=torch.int32)
+        inv, axis = table(pairs, 1)
+        dq, dk = torch.autograd.grad(clis.rope_autograd(q, k, pos, inv, axis, interleaved), (q, k), (gq, gk))
+        check(dq, turned(gq, pos, inv, axis, interleaved, -1.0), gq)
+        check(dk, turned(gk, pos, inv, axis, interleaved, -1.0), gk)
+        assert dq.dtype == FP and torch.equal(dq[..., 2 * pairs:], gq[..., 2 * pairs:])
