@@ -3,8 +3,8 @@
 // call of the library each, and the rotation's autograd node.
 //
 // These calls are made once or more per layer and token, and at a few tokens the
-// kernels take a few microseconds: marshalled in Python a call took 25 to 35 us of
-// host time, here it takes about 5.  Everything that computes is in libclis.so.
+// kernels take a few microseconds: marshalled in Python a call took 25 to 36 us of
+// host time, here 4 to 9.  Everything that computes is in libclis.so.
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>

@@ -182,6 +182,9 @@ Split split_of(const clis_paged_t *p, int64_t max_q, int nsm)
     // length counts too (24 sequences of up to 8,000 keys 84 us against 94, 40 119
     // against 112, 64 of 16,000 260 against 219): at most 96 tiles per SM by what the
     // block table can hold, which the host knows.
+    // S counts sequences without a token too, which the host cannot tell apart: 3 chunks and
+    // 9 single tokens take 92 us with 12 or 64 rows in the table, 132 with 256.  All of
+    // these have 8 key/value heads.
     const int64_t items = p->S * p->Hkv;
     const int64_t per = (p->width * p->page_size + clis::kChunkKeys - 1) / clis::kChunkKeys;
     if (s.chunk && items <= 4 * nsm && (p->d == 128 || items * per <= 96 * nsm)) s.row_tiles = 0;

@@ -46,10 +46,13 @@
 // 707 us: each further wait and commit of the MMA warp is a gap in the tensor pipe,
 // which takes only a few products in advance.)
 //
-// 2,048 tokens behind 30,011 (32 query and 8 key/value heads, d = 128): 690 us, 1,510
-// TFLOP/s, the tensor pipe active 66% of the time; a key tile takes 1.45 us, of which
+// 2,048 tokens behind 30,011 (32 query and 8 key/value heads): at d = 128 686 to 690 us
+// alone, 726 to 755 among other calls (1,380 to 1,520 TFLOP/s; the tensor pipe active 66%
+// of the time), at d = 64 511 us (1,020).  At d = 128 a key tile takes 1.45 us, of which
 // the chain of one row tile is 1.4 (scores 0.28, weights 0.6, product 0.28, and the
-// barriers between them).
+// barriers between them).  256 items of 243 key tiles on average are 409 such steps on
+// each of 152 SMs, 593 us; the rest (first tiles, joins, page lookups, 84 bytes of
+// registers that the softmax warps spill at d = 128) has not been taken apart.
 //
 // Every wait is bounded.
 #include <cuda_bf16.h>

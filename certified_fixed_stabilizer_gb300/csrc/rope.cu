@@ -22,7 +22,8 @@
 // of 8,192 tokens into a cache (201 MB) 39.3 us, 5.1 TB/s (a plain copy 37.0: what
 // fits the L2 twice over does not reach the rate of long copies).  More loads in
 // flight make it slower (blocks of 128 threads, 8 an SM: 45.2; two heads a thread
-// at a time, 5 blocks an SM: 50.2; eight, 2 blocks: 39.9).
+// at a time, 5 blocks an SM: 50.2; eight, 2 blocks: 39.9).  At three blocks an SM the
+// kernels that write the cache spill 32 bytes of registers; the plain ones do not.
 #include <cuda_bf16.h>
 
 #include "clis_internal.h"

@@ -466,7 +466,7 @@ CLIS_API clis_status_t clis_attn_bwd(const clis_shape_t *shape, const void *q, c
  * interleaved; elements from 2 * pairs on are copied.  inverse = 1 turns back:
  * the gradient of the rotation.  Angles are exact to fp32 for positions of any
  * size and sign; products are rounded once, to the data type.
- *   B, Hq, Hk, N, d   q [B, Hq, N, d], k [B, Hk, N, d]; d 64 or 128
+ *   B, Hq, Hk, N, d   q [B, Hq, N, d], k [B, Hk, N, d]; d 64 or 128; B * N up to 2^27
  *   pairs             a multiple of 8, 8 .. d / 2
  *   axes              1 .. 4
  *   q_s*, k_s*        strides of q and k (may be 0: broadcast); qo_s*, ko_s* of
@@ -570,7 +570,7 @@ CLIS_API clis_status_t clis_paged_plan(const clis_paged_t *desc, const int32_t *
                                        int32_t *positions, clis_stream_t stream);
 
 /* New keys and values into the cache, rotated on the way, and q rotated beside
- * them, in one launch.
+ * them, in one launch.  T up to 2^27.
  *   rope       desc for the rotation: N = T, B = 1, Hq = H (0: no q), Hk = Hkv, d,
  *              strides of q, q_out, k and positions (ko_s* are ignored: k goes to
  *              the cache); dtype as in desc; inverse must be 0
