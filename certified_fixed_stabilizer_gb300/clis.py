@@ -71,6 +71,8 @@ class _Unloaded:
     until the first of them loads it.  Everything else needs libclis.so alone."""
 
     def __getattr__(self, name):
+        if name.startswith("__"):  # (what looks objects over, not a call)
+            raise AttributeError(name)
         return getattr(load_binding(), name)
 
 

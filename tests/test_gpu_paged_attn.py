@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from certified_fixed_stabilizer_gb300 import clis
-from paged_util import HALF_STEP, check_attention, make_batch
+from paged_util import check_attention, make_batch
+from paged_util import HALF_STEP
 
 pytestmark = pytest.mark.gpu
 

@@ -8,7 +8,8 @@ import torch
 from certified_fixed_stabilizer_gb300 import clis
 
 FAKE = 1 << 20  # never followed: every call below is refused, or has nothing to do
-OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA = 0, 1, 2, 3, 4, 5
+OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = 0, 1, 2, 3, 4
+CUDA = 5  # (what a call that would be made says on a machine without a GPU)
 
 
 def rope_desc(**kw):
