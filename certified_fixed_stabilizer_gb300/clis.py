@@ -50,6 +50,10 @@ class Cert(ctypes.Structure):
 CERT_WORDS = ctypes.sizeof(Cert) // 4  # a certificate is 8 32-bit words
 
 
+class QuantDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("code", "ks_sp", "ks_sh", "ks_sn", "vs_sp", "vs_sh", "vs_sn")]
+
+
 class RopeDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in (
         "B", "Hq", "Hk", "N", "d", "pairs", "axes", "interleaved", "inverse",
@@ -154,6 +158,15 @@ def load_library():
     lib.clis_attn_paged_workspace_size.restype = i32
     lib.clis_attn_fwd_paged.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, i64, f32, i32, vp, sz, vp]
     lib.clis_attn_fwd_paged.restype = i32
+    zp = ctypes.POINTER(QuantDesc)
+    lib.clis_paged_append_q8.argtypes = [pp, zp, rp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.clis_paged_append_q8.restype = i32
+    lib.clis_paged_read.argtypes = [pp, zp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp, i64, i64, vp]
+    lib.clis_paged_read.restype = i32
+    lib.clis_attn_paged_q8_workspace_size.argtypes = [pp, zp, i64, ctypes.POINTER(sz)]
+    lib.clis_attn_paged_q8_workspace_size.restype = i32
+    lib.clis_attn_fwd_paged_q8.argtypes = [pp, zp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, f32, i32, vp, sz, vp]
+    lib.clis_attn_fwd_paged_q8.restype = i32
     _lib = lib
     return lib
 
@@ -860,40 +873,67 @@ paged_plan = clis_paged_plan
 
 
 def clis_paged_append(k, v, k_cache, v_cache, slots, q=None, positions=None, inv_freq=None, axis=None,
-                      interleaved: bool = False, q_out=None, stream=None):
+                      interleaved: bool = False, q_out=None, stream=None, k_scale=None, v_scale=None):
     """Writes k, v [T, H_kv, d] into the caches [pages, H_kv, page_size, d] at their
     slots (int64 [T], page * page_size + row; negative: nowhere; distinct),
     rotated by ``positions`` (int32 [T, axes] or [T]) if given, and returns q
     [T, H, d] rotated by them (None without q).  Any strides with a contiguous last
-    dimension; q_out may be q."""
-    return _native.paged_append(k, v, k_cache, v_cache, slots, q, positions, inv_freq, axis, interleaved, q_out,
-                                _raw(stream))
+    dimension; q_out may be q.
+
+    With ``k_scale``, ``v_scale`` (float32 [pages, H_kv, page_size]) the caches hold codes
+    (int8 or float8_e4m3fn): each row's scale is its largest magnitude over 127 or 448, and
+    the codes are its values over the scale, rounded to nearest.  k is rotated in fp32
+    and not rounded before.  A row with a non-finite value reads back as NaN."""
+    return _native.paged_append(k, v, k_cache, v_cache, slots, q, positions, inv_freq, axis, interleaved, q_out, k_scale,
+                                v_scale, _raw(stream))
 
 
 paged_append = clis_paged_append
 
 
 def clis_attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: int, scale_log2: float,
-                        causal: bool = True, out=None, lse2=None, workspace=None, stream=None):
+                        causal: bool = True, out=None, lse2=None, workspace=None, stream=None, k_scale=None,
+                        v_scale=None):
     """Attention of the new tokens q [T, H, d] (those of sequence s are rows cu_q[s] ..
     cu_q[s + 1] - 1) over their sequences' cached keys; returns ``out``.  ``lse2``:
-    optional float32 [T, H].  Rows that belong to no sequence are not written."""
+    optional float32 [T, H].  Rows that belong to no sequence are not written.  Caches of
+    codes come with their scales (:func:`paged_append`)."""
     return _native.attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, scale_log2, causal, out, lse2,
-                                   False, workspace, _raw(stream))[0]
+                                   False, workspace, k_scale, v_scale, _raw(stream))[0]
 
 
 def attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: int | None = None,
-                    softmax_scale: float | None = None, causal: bool = True, out=None, return_lse: bool = False):
+                    softmax_scale: float | None = None, causal: bool = True, out=None, return_lse: bool = False,
+                    k_scale=None, v_scale=None):
     """Attention of new tokens over a paged cache: any mix of single tokens, drafted
     tokens and chunks in one call (grouped-query heads by q's and the caches'
     head counts).  max_q: the most new tokens of a sequence (default: all rows of q).  It
     is what the kernels are chosen by: give it for batches of single or drafted tokens, which
     the default takes for possible chunks (64 single tokens over 1,000 to 16,000 keys: 318 us
     with max_q = 1, 362 without).  With ``return_lse``: (out, lse2 float32 [T, H]).
-    No autograd graph is recorded."""
+    Caches of codes (int8 or float8_e4m3fn) come with ``k_scale`` and ``v_scale``; a max_q that
+    allows for more than 64 query rows per key/value head then takes a workspace of a
+    16-bit copy of the caches that are passed.  No autograd graph is recorded."""
     r = _native.attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q or max(1, q.shape[0]),
-                                scale_log2_for(q.shape[-1], softmax_scale), causal, out, None, return_lse, None, None)
+                                scale_log2_for(q.shape[-1], softmax_scale), causal, out, None, return_lse, None, k_scale,
+                                v_scale, None)
     return r if return_lse else r[0]
+
+
+def clis_paged_read(k_cache, v_cache, block_table, cu, num_tokens: int, start=None, k_scale=None, v_scale=None,
+                    dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+    """Cached tokens as rows again: (k, v) [num_tokens, H_kv, d], where rows cu[s] ..
+    cu[s + 1] - 1 (cu int32 [S + 1]) are tokens start[s], start[s] + 1, ... of sequence s
+    (start int32 [S], default 0).  With ``k_scale`` and ``v_scale`` the caches hold codes, and
+    the rows are their values in ``dtype`` (bfloat16 or float16); without, they are copied
+    (``dtype`` has no effect).  Rows that belong to no sequence are not written."""
+    if dtype not in DTYPE:
+        raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+    return _native.paged_read(k_cache, v_cache, block_table, cu, num_tokens, start, k_scale, v_scale, dtype == torch.float16,
+                              k_out, v_out, _raw(stream))
+
+
+paged_read = clis_paged_read
 
 
 class PagedCache:

@@ -242,32 +242,69 @@ std::vector<Tensor> plan(const Tensor &ctx_len, const Tensor &new_len, const Ten
 
 // --------------------------------------------------------- cache and attention
 
-clis_paged_t cache_desc(const Tensor &kc, const Tensor &vc, const Tensor &like)
+bool is_codes(const Tensor &t) { return t.scalar_type() == at::kChar || t.scalar_type() == at::kFloat8_e4m3fn; }
+
+// The caches' part of the descriptor.
+clis_paged_t cache_desc(const Tensor &kc, const Tensor &vc)
 {
-    TORCH_CHECK_VALUE(kc.dim() == 4 && kc.sizes() == vc.sizes() && kc.size(3) == like.size(2),
-                      "k_cache and v_cache must be [pages, H_kv, page_size, d]");
-    TORCH_CHECK_VALUE(kc.scalar_type() == like.scalar_type() && vc.scalar_type() == like.scalar_type(),
-                      "the caches must have the dtype of q, k and v");
-    TORCH_CHECK_VALUE(kc.device() == like.device() && vc.device() == like.device(),
-                      "the caches must be on the device of q, k and v");
+    TORCH_CHECK_VALUE(kc.dim() == 4 && kc.sizes() == vc.sizes() && kc.scalar_type() == vc.scalar_type() &&
+                          kc.device() == vc.device(),
+                      "k_cache and v_cache must be [pages, H_kv, page_size, d], of one dtype and on one device");
     TORCH_CHECK_VALUE(kc.stride(3) == 1 && vc.stride(3) == 1, "the caches must have a contiguous last dimension");
     clis_paged_t d = {};
-    d.T = like.size(0);
-    d.d = like.size(2);
+    d.d = kc.size(3);
     d.Hkv = kc.size(1);
     d.page_size = kc.size(2);
     d.num_pages = kc.size(0);
     d.width = 1;
     d.kc_sp = st(kc, 0), d.kc_sh = st(kc, 1), d.kc_sn = st(kc, 2);
     d.vc_sp = st(vc, 0), d.vc_sh = st(vc, 1), d.vc_sn = st(vc, 2);
+    return d;
+}
+
+// The caches beside q, k or v; with scales they hold codes.
+clis_paged_t cache_desc(const Tensor &kc, const Tensor &vc, const Tensor &like, bool codes)
+{
+    TORCH_CHECK_VALUE(kc.dim() == 4 && kc.sizes() == vc.sizes() && kc.size(3) == like.size(2),
+                      "k_cache and v_cache must be [pages, H_kv, page_size, d]");
+    if (codes) {
+        TORCH_CHECK_VALUE(is_codes(kc) && kc.scalar_type() == vc.scalar_type(),
+                          "caches with scales must be int8 or float8_e4m3fn");
+    } else {
+        TORCH_CHECK_VALUE(kc.scalar_type() == like.scalar_type() && vc.scalar_type() == like.scalar_type(),
+                          "the caches must have the dtype of q, k and v", is_codes(kc) ? " (codes need k_scale and v_scale)" : "");
+    }
+    TORCH_CHECK_VALUE(kc.device() == like.device() && vc.device() == like.device(),
+                      "the caches must be on the device of q, k and v");
+    clis_paged_t d = cache_desc(kc, vc);
+    d.T = like.size(0);
     d.dtype = dtype_of(like);
     return d;
 }
 
+// The scales of a cache of codes.
+clis_quant_t quant_desc(const Tensor &kc, const std::optional<Tensor> &ks, const std::optional<Tensor> &vs)
+{
+    clis_quant_t z = {};
+    TORCH_CHECK_VALUE(ks.has_value() == vs.has_value(), "k_scale and v_scale belong together");
+    if (!ks) return z;
+    for (const Tensor *t : {&*ks, &*vs})
+        TORCH_CHECK_VALUE(t->scalar_type() == at::kFloat && t->device() == kc.device() && t->sizes() == kc.sizes().slice(0, 3),
+                          "k_scale and v_scale must be float32 [pages, H_kv, page_size] on the caches' device");
+    z.code = kc.scalar_type() == at::kChar ? CLIS_CODE_INT8 : CLIS_CODE_E4M3;
+    auto step = [](const Tensor &t, int64_t i) { return t.size(i) == 1 ? 1 : t.stride(i); };
+    z.ks_sp = step(*ks, 0), z.ks_sh = step(*ks, 1), z.ks_sn = step(*ks, 2);
+    z.vs_sp = step(*vs, 0), z.vs_sh = step(*vs, 1), z.vs_sn = step(*vs, 2);
+    return z;
+}
+
+float *floats(const std::optional<Tensor> &t) { return t ? static_cast<float *>(t->data_ptr()) : nullptr; }
+
 std::optional<Tensor> append(const Tensor &k, const Tensor &v, const Tensor &kc, const Tensor &vc, const Tensor &slots,
                              const std::optional<Tensor> &q, const std::optional<Tensor> &positions,
                              const std::optional<Tensor> &inv_freq, const std::optional<Tensor> &axis, bool interleaved,
-                             std::optional<Tensor> q_out, std::optional<uintptr_t> raw)
+                             std::optional<Tensor> q_out, const std::optional<Tensor> &ks, const std::optional<Tensor> &vs,
+                             std::optional<uintptr_t> raw)
 {
     TORCH_CHECK_VALUE(k.is_cuda() && k.dim() == 3 && elem(k) && k.stride(2) == 1,
                       "k must be a bfloat16 or float16 device tensor [T, H_kv, d] with a contiguous last dimension");
@@ -275,7 +312,8 @@ std::optional<Tensor> append(const Tensor &k, const Tensor &v, const Tensor &kc,
     TORCH_CHECK_VALUE(v.sizes() == k.sizes() && v.scalar_type() == k.scalar_type() && v.device() == k.device() &&
                           v.stride(2) == 1,
                       "v must match k");
-    clis_paged_t desc = cache_desc(kc, vc, k);
+    clis_paged_t desc = cache_desc(kc, vc, k, ks.has_value());
+    const clis_quant_t z = quant_desc(kc, ks, vs);
     TORCH_CHECK_VALUE(desc.Hkv == Hk, "the caches must have k's number of heads");
     check_ints(slots, at::kLong, {T}, k.device(), "slots");
     Place at_(k, raw);
@@ -310,13 +348,19 @@ std::optional<Tensor> append(const Tensor &k, const Tensor &v, const Tensor &kc,
         r.p_sn = positions->stride(0);
         r.p_sa = positions->dim() == 2 ? positions->stride(1) : 0;
     }
-    ok("clis_paged_append",
-       clis_paged_append(&desc, &r, q ? q->data_ptr() : nullptr, k.data_ptr(), v.data_ptr(), st(v, 0), st(v, 1),
-                         q ? q_out->data_ptr() : nullptr, kc.data_ptr(), vc.data_ptr(),
-                         static_cast<const int64_t *>(slots.data_ptr()),
-                         positions ? static_cast<const int32_t *>(positions->data_ptr()) : nullptr,
-                         positions ? static_cast<const double *>(inv_freq->data_ptr()) : nullptr,
-                         positions ? static_cast<const int32_t *>(axis->data_ptr()) : nullptr, at_.stream));
+    const void *qp = q ? q->data_ptr() : nullptr;
+    void *qo = q ? q_out->data_ptr() : nullptr;
+    const auto *sl = static_cast<const int64_t *>(slots.data_ptr());
+    const auto *pos = positions ? static_cast<const int32_t *>(positions->data_ptr()) : nullptr;
+    const auto *inv = positions ? static_cast<const double *>(inv_freq->data_ptr()) : nullptr;
+    const auto *ax = positions ? static_cast<const int32_t *>(axis->data_ptr()) : nullptr;
+    if (ks)
+        ok("clis_paged_append_q8",
+           clis_paged_append_q8(&desc, &z, &r, qp, k.data_ptr(), v.data_ptr(), st(v, 0), st(v, 1), qo, kc.data_ptr(), vc.data_ptr(),
+                                floats(ks), floats(vs), sl, pos, inv, ax, at_.stream));
+    else
+        ok("clis_paged_append", clis_paged_append(&desc, &r, qp, k.data_ptr(), v.data_ptr(), st(v, 0), st(v, 1), qo, kc.data_ptr(),
+                                                  vc.data_ptr(), sl, pos, inv, ax, at_.stream));
     return q ? q_out : std::nullopt;
 }
 
@@ -324,12 +368,13 @@ std::optional<Tensor> append(const Tensor &k, const Tensor &v, const Tensor &kc,
 std::vector<Tensor> attention(const Tensor &q, const Tensor &kc, const Tensor &vc, const Tensor &table, const Tensor &cu,
                               const Tensor &kv, int64_t max_q, double scale_log2, bool causal, std::optional<Tensor> out,
                               std::optional<Tensor> lse2, bool with_lse, std::optional<Tensor> workspace,
-                              std::optional<uintptr_t> raw)
+                              const std::optional<Tensor> &ks, const std::optional<Tensor> &vs, std::optional<uintptr_t> raw)
 {
     TORCH_CHECK_VALUE(q.is_cuda() && q.dim() == 3 && elem(q) && q.stride(2) == 1,
                       "q must be a bfloat16 or float16 device tensor [T, H, d] with a contiguous last dimension");
     const at::Device dev = q.device();
-    clis_paged_t d = cache_desc(kc, vc, q);
+    clis_paged_t d = cache_desc(kc, vc, q, ks.has_value());
+    const clis_quant_t z = quant_desc(kc, ks, vs);
     d.H = q.size(1);
     TORCH_CHECK_VALUE(table.dim() == 2 && table.scalar_type() == at::kInt && table.device() == dev && table.stride(1) == 1,
                       "block_table must be an int32 tensor [S, width] with contiguous rows on the device of q");
@@ -346,16 +391,62 @@ std::vector<Tensor> attention(const Tensor &q, const Tensor &kc, const Tensor &v
     d.q_st = st(q, 0), d.q_sh = st(q, 1);
     d.o_st = st(*out, 0), d.o_sh = st(*out, 1);
     size_t need = 0;
-    ok("clis_attn_paged_workspace_size", clis_attn_paged_workspace_size(&d, max_q, &need));
+    if (ks) ok("clis_attn_paged_q8_workspace_size", clis_attn_paged_q8_workspace_size(&d, &z, max_q, &need));
+    else ok("clis_attn_paged_workspace_size", clis_attn_paged_workspace_size(&d, max_q, &need));
     if (!workspace) workspace = empty({static_cast<int64_t>(need)}, at::kByte, dev);
     TORCH_CHECK_VALUE(workspace->device() == dev && workspace->is_contiguous(),
                       "the workspace must be contiguous and on the device of q");
-    ok("clis_attn_fwd_paged",
-       clis_attn_fwd_paged(&d, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), static_cast<const int32_t *>(table.data_ptr()),
-                           static_cast<const int32_t *>(cu.data_ptr()), static_cast<const int32_t *>(kv.data_ptr()),
-                           out->data_ptr(), lse2 ? static_cast<float *>(lse2->data_ptr()) : nullptr, max_q,
-                           static_cast<float>(scale_log2), causal, workspace->data_ptr(), workspace->nbytes(), at_.stream));
+    const auto *tb = static_cast<const int32_t *>(table.data_ptr()), *cq = static_cast<const int32_t *>(cu.data_ptr()),
+               *kl = static_cast<const int32_t *>(kv.data_ptr());
+    if (ks)
+        ok("clis_attn_fwd_paged_q8",
+           clis_attn_fwd_paged_q8(&d, &z, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), floats(ks), floats(vs), tb, cq, kl,
+                                  out->data_ptr(), floats(lse2), max_q, static_cast<float>(scale_log2), causal,
+                                  workspace->data_ptr(), workspace->nbytes(), at_.stream));
+    else
+        ok("clis_attn_fwd_paged",
+           clis_attn_fwd_paged(&d, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), tb, cq, kl, out->data_ptr(), floats(lse2), max_q,
+                               static_cast<float>(scale_log2), causal, workspace->data_ptr(), workspace->nbytes(), at_.stream));
     return {*out, lse2 ? *lse2 : Tensor()};
+}
+
+// Cached tokens as rows [T, Hkv, d]; type: of the rows, that of the caches without scales.
+std::vector<Tensor> read(const Tensor &kc, const Tensor &vc, const Tensor &table, const Tensor &cu, int64_t T,
+                         const std::optional<Tensor> &start, const std::optional<Tensor> &ks, const std::optional<Tensor> &vs,
+                         bool half, std::optional<Tensor> k_out, std::optional<Tensor> v_out, std::optional<uintptr_t> raw)
+{
+    TORCH_CHECK_VALUE(kc.is_cuda(), "k_cache must be a device tensor [pages, H_kv, page_size, d]");
+    const at::Device dev = kc.device();
+    clis_paged_t d = cache_desc(kc, vc);
+    const clis_quant_t z = quant_desc(kc, ks, vs);
+    TORCH_CHECK_VALUE(ks ? is_codes(kc) : elem(kc), ks ? "caches with scales must be int8 or float8_e4m3fn"
+                                                      : "caches without scales must be bfloat16 or float16");
+    const at::ScalarType type = ks ? (half ? at::kHalf : at::kBFloat16) : kc.scalar_type();
+    TORCH_CHECK_VALUE(table.dim() == 2 && table.scalar_type() == at::kInt && table.device() == dev && table.stride(1) == 1,
+                      "block_table must be an int32 tensor [S, width] with contiguous rows on the caches' device");
+    TORCH_CHECK_VALUE(T >= 0, "num_tokens must not be negative");
+    d.S = table.size(0);
+    d.T = T;
+    d.H = d.Hkv;
+    d.width = table.size(1);
+    d.bt_ss = d.S > 1 ? table.stride(0) : 0;
+    d.dtype = type == at::kHalf ? CLIS_DT_FP16 : CLIS_DT_BF16;
+    check_ints(cu, at::kInt, {d.S + 1}, dev, "cu");
+    if (start) check_ints(*start, at::kInt, {d.S}, dev, "start");
+    Place at_(kc, raw);
+    for (auto *t : {&k_out, &v_out}) {
+        if (!*t) *t = at_.result(empty({T, d.Hkv, d.d}, type, dev));
+        const Tensor &x = **t;
+        TORCH_CHECK_VALUE(x.dim() == 3 && x.size(0) == T && x.size(1) == d.Hkv && x.size(2) == d.d && x.scalar_type() == type &&
+                              x.device() == dev && x.stride(2) == 1,
+                          "k_out and v_out must be [num_tokens, H_kv, d] of the rows' dtype with a contiguous last dimension");
+    }
+    ok("clis_paged_read",
+       clis_paged_read(&d, ks ? &z : nullptr, kc.data_ptr(), vc.data_ptr(), floats(ks), floats(vs),
+                       static_cast<const int32_t *>(table.data_ptr()), static_cast<const int32_t *>(cu.data_ptr()),
+                       start ? static_cast<const int32_t *>(start->data_ptr()) : nullptr, k_out->data_ptr(), st(*k_out, 0),
+                       st(*k_out, 1), v_out->data_ptr(), st(*v_out, 0), st(*v_out, 1), at_.stream));
+    return {*k_out, *v_out};
 }
 
 // -------------------------------------------------------------- Python objects
@@ -477,10 +568,11 @@ PyObject *py_plan(PyObject *, PyObject *const *a, Py_ssize_t n)
 
 PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    return call(n, 12, [&]() -> PyObject * {
+    return call(n, 14, [&]() -> PyObject * {
         const auto q = append(tensor(a[0], "k"), tensor(a[1], "v"), tensor(a[2], "k_cache"), tensor(a[3], "v_cache"),
                               tensor(a[4], "slots"), maybe(a[5], "q"), maybe(a[6], "positions"), maybe(a[7], "inv_freq"),
-                              maybe(a[8], "axis"), truth(a[9]), maybe(a[10], "q_out"), stream_of(a[11]));
+                              maybe(a[8], "axis"), truth(a[9]), maybe(a[10], "q_out"), maybe(a[11], "k_scale"),
+                              maybe(a[12], "v_scale"), stream_of(a[13]));
         if (q) return THPVariable_Wrap(*q);
         Py_RETURN_NONE;
     });
@@ -488,11 +580,20 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n)
 
 PyObject *py_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    return call(n, 14, [&] {
+    return call(n, 16, [&] {
         return wrap(attention(tensor(a[0], "q"), tensor(a[1], "k_cache"), tensor(a[2], "v_cache"), tensor(a[3], "block_table"),
                               tensor(a[4], "cu_q"), tensor(a[5], "kv_len"), integer(a[6]), real(a[7]), truth(a[8]),
                               maybe(a[9], "out"), maybe(a[10], "lse2"), truth(a[11]), maybe(a[12], "workspace"),
-                              stream_of(a[13])));
+                              maybe(a[13], "k_scale"), maybe(a[14], "v_scale"), stream_of(a[15])));
+    });
+}
+
+PyObject *py_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return call(n, 12, [&] {
+        return wrap(read(tensor(a[0], "k_cache"), tensor(a[1], "v_cache"), tensor(a[2], "block_table"), tensor(a[3], "cu"),
+                         integer(a[4]), maybe(a[5], "start"), maybe(a[6], "k_scale"), maybe(a[7], "v_scale"), truth(a[8]),
+                         maybe(a[9], "k_out"), maybe(a[10], "v_out"), stream_of(a[11])));
     });
 }
 
@@ -510,6 +611,7 @@ PyMethodDef g_methods[] = {
     {"paged_plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_plan)), METH_FASTCALL, nullptr},
     {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_append)), METH_FASTCALL, nullptr},
     {"attention_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_attention)), METH_FASTCALL, nullptr},
+    {"paged_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_read)), METH_FASTCALL, nullptr},
     {"set_error_class", py_set_error_class, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

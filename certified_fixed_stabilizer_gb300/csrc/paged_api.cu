@@ -115,6 +115,22 @@ clis_status_t check_cache(const clis_paged_t *p, bool written)
     return CLIS_OK;
 }
 
+// The codes' strides count bytes here; a thread moves 16 of them.
+clis_status_t check_quant(const clis_paged_t *p, const clis_quant_t *z, bool written)
+{
+    if (z->code != CLIS_CODE_INT8 && z->code != CLIS_CODE_E4M3) return CLIS_ERR_INVALID_ARG;
+    for (int64_t s : {p->kc_sp, p->kc_sh, p->kc_sn, p->vc_sp, p->vc_sh, p->vc_sn})
+        if (s & 15) return CLIS_ERR_MISALIGNED;
+    for (int64_t s : {z->ks_sp, z->ks_sh, z->ks_sn, z->vs_sp, z->vs_sh, z->vs_sn}) {
+        if (s < 0) return CLIS_ERR_INVALID_ARG;
+        if (s >= (int64_t(1) << 38)) return CLIS_ERR_UNSUPPORTED;
+    }
+    const int64_t kd[3][2] = {{p->num_pages, z->ks_sp}, {p->Hkv, z->ks_sh}, {p->page_size, z->ks_sn}};
+    const int64_t vd[3][2] = {{p->num_pages, z->vs_sp}, {p->Hkv, z->vs_sh}, {p->page_size, z->vs_sn}};
+    if (written && (overlapping(1, kd, 3) || overlapping(1, vd, 3))) return CLIS_ERR_INVALID_ARG;
+    return CLIS_OK;
+}
+
 // Everything of the attention call but its pointers.
 clis_status_t check_attn(const clis_paged_t *p, int64_t max_q)
 {
@@ -191,6 +207,56 @@ Split split_of(const clis_paged_t *p, int64_t max_q, int nsm)
     return s;
 }
 
+// Over a quantised cache: the kernel for few rows takes up to 64, and batches with chunks
+// always launch both kernels (the chunk kernel's keys are unpacked to 16 bits first, so
+// a single token costs it five times the bytes).
+Split split_q8(const clis_paged_t *p, int64_t max_q)
+{
+    const int g = static_cast<int>(p->H / p->Hkv);
+    const int64_t mq = max_q < p->T ? max_q : p->T;
+    Split s;
+    s.row_tiles = clis::paged_q8_row_tiles(mq, g);
+    s.chunk = mq * g > 16 * s.row_tiles;
+    return s;
+}
+
+// Bytes of one of the two 16-bit copies that the chunk kernel works on, a multiple of 256.
+size_t pages_bytes(const clis_paged_t *p)
+{
+    return (static_cast<size_t>(p->num_pages) * p->Hkv * p->page_size * p->d * 2 + 255) & ~size_t(255);
+}
+
+size_t scales_bytes(const clis_paged_t *p)
+{
+    return (static_cast<size_t>(p->num_pages) * p->Hkv * p->page_size * 4 + 255) & ~size_t(255);
+}
+
+clis_status_t check_attn_q8(const clis_paged_t *p, const clis_quant_t *z, int64_t max_q)
+{
+    clis_status_t st = check_attn(p, max_q);
+    if (st == CLIS_OK) st = check_quant(p, z, false);
+    if (st != CLIS_OK) return st;
+    if (static_cast<double>(p->num_pages) * p->Hkv * p->page_size * p->d >= 1099511627776.0) return CLIS_ERR_UNSUPPORTED;  // 2^40
+    return CLIS_OK;
+}
+
+clis::QuantArgs quant_args(const clis_quant_t *z, const void *kc, const void *vc, const float *ks, const float *vs)
+{
+    clis::QuantArgs q{};
+    q.kc = static_cast<const uint8_t *>(kc);
+    q.vc = static_cast<const uint8_t *>(vc);
+    q.ks = ks;
+    q.vs = vs;
+    q.ks_sp = z->ks_sp;
+    q.ks_sh = z->ks_sh;
+    q.ks_sn = z->ks_sn;
+    q.vs_sp = z->vs_sp;
+    q.vs_sh = z->vs_sh;
+    q.vs_sn = z->vs_sn;
+    q.code = static_cast<int>(z->code);
+    return q;
+}
+
 bool sm_count(int *n)
 {
     int dev = 0;
@@ -227,6 +293,76 @@ clis::RotArgs rot_args(const clis_rope_t *r)
     a.inverse = static_cast<int>(r->inverse);
     a.dtype = static_cast<int>(r->dtype);
     return a;
+}
+
+// The write into a cache of 16-bit values, or with quant of codes.
+clis_status_t append(const clis_paged_t *desc, const clis_quant_t *quant, const clis_rope_t *rope, const void *q, const void *k,
+                     const void *v, int64_t v_st, int64_t v_sh, void *q_out, void *k_cache, void *v_cache, float *k_scale,
+                     float *v_scale, const int64_t *slots, const int32_t *positions, const double *inv_freq,
+                     const int32_t *axis, clis_stream_t stream)
+{
+    if (!desc || !rope) return CLIS_ERR_INVALID_ARG;
+    clis_status_t st = check_cache(desc, true);
+    if (st == CLIS_OK && quant) st = check_quant(desc, quant, true);
+    if (st != CLIS_OK) return st;
+    clis_rope_t r = *rope;
+    const bool turn = r.pairs != 0;
+    if (!turn) {  // the rotation's other fields are not read then
+        r.pairs = 8;
+        r.axes = 1;
+        r.interleaved = r.inverse = 0;
+        r.Hq = 0;
+        r.q_sb = r.q_sh = r.q_sn = r.qo_sb = r.qo_sh = r.qo_sn = 0;
+        if (q) return CLIS_ERR_INVALID_ARG;
+    }
+    r.ko_sb = r.ko_sh = r.ko_sn = 0;
+    if (r.B != 1 || r.N != desc->T || r.Hk != desc->Hkv || r.d != desc->d || r.dtype != desc->dtype || r.inverse ||
+        (r.Hq != 0 && r.Hq != desc->H))
+        return CLIS_ERR_INVALID_ARG;
+    if ((st = check_rope(&r, false)) != CLIS_OK) return st;
+    if ((st = check_strides({v_st, v_sh})) != CLIS_OK) return st;
+    if (desc->T == 0) return CLIS_OK;
+    if (!k || !v || !k_cache || !v_cache || !slots || (r.Hq > 0 && (!q || !q_out))) return CLIS_ERR_INVALID_ARG;
+    if (turn && (!positions || !inv_freq || !axis)) return CLIS_ERR_INVALID_ARG;
+    if (quant && (!k_scale || !v_scale)) return CLIS_ERR_INVALID_ARG;
+    if ((r.Hq > 0 && (!aligned(q, 16) || !aligned(q_out, 16))) || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 8) || !aligned(positions, 4) ||
+        !aligned(inv_freq, 8) || !aligned(axis, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return CLIS_ERR_MISALIGNED;
+    clis::RotArgs a = rot_args(&r);
+    if (!turn) a.pairs = 0;
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.v_sn = v_st;
+    a.v_sh = v_sh;
+    a.qo = static_cast<uint16_t *>(q_out);
+    a.ko = static_cast<uint16_t *>(k_cache);
+    a.ko_sb = desc->kc_sp;
+    a.ko_sh = desc->kc_sh;
+    a.ko_sn = desc->kc_sn;
+    a.vo = static_cast<uint16_t *>(v_cache);
+    a.vo_sb = desc->vc_sp;
+    a.vo_sh = desc->vc_sh;
+    a.vo_sn = desc->vc_sn;
+    a.pos = positions;
+    a.inv_freq = inv_freq;
+    a.axis = axis;
+    a.slots = slots;
+    a.num_slots = desc->num_pages * desc->page_size;
+    a.page_shift = page_shift(desc->page_size);
+    if (quant) {
+        a.code = static_cast<int>(quant->code);
+        a.ks = k_scale;
+        a.ks_sp = quant->ks_sp;
+        a.ks_sh = quant->ks_sh;
+        a.ks_sn = quant->ks_sn;
+        a.vs = v_scale;
+        a.vs_sp = quant->vs_sp;
+        a.vs_sh = quant->vs_sh;
+        a.vs_sn = quant->vs_sn;
+    }
+    return clis::launch_rot(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -300,55 +436,71 @@ clis_status_t clis_paged_append(const clis_paged_t *desc, const clis_rope_t *rop
                                 const int64_t *slots, const int32_t *positions, const double *inv_freq,
                                 const int32_t *axis, clis_stream_t stream)
 {
-    if (!desc || !rope) return CLIS_ERR_INVALID_ARG;
-    clis_status_t st = check_cache(desc, true);
+    return append(desc, nullptr, rope, q, k, v, v_st, v_sh, q_out, k_cache, v_cache, nullptr, nullptr, slots, positions,
+                  inv_freq, axis, stream);
+}
+
+clis_status_t clis_paged_append_q8(const clis_paged_t *desc, const clis_quant_t *quant, const clis_rope_t *rope,
+                                   const void *q, const void *k, const void *v, int64_t v_st, int64_t v_sh, void *q_out,
+                                   void *k_codes, void *v_codes, float *k_scale, float *v_scale, const int64_t *slots,
+                                   const int32_t *positions, const double *inv_freq, const int32_t *axis,
+                                   clis_stream_t stream)
+{
+    if (!quant) return CLIS_ERR_INVALID_ARG;
+    return append(desc, quant, rope, q, k, v, v_st, v_sh, q_out, k_codes, v_codes, k_scale, v_scale, slots, positions,
+                  inv_freq, axis, stream);
+}
+
+clis_status_t clis_paged_read(const clis_paged_t *desc, const clis_quant_t *quant, const void *k_cache, const void *v_cache,
+                              const float *k_scale, const float *v_scale, const int32_t *block_table, const int32_t *cu,
+                              const int32_t *start, void *k_out, int64_t k_st, int64_t k_sh, void *v_out, int64_t v_st,
+                              int64_t v_sh, clis_stream_t stream)
+{
+    if (!desc) return CLIS_ERR_INVALID_ARG;
+    clis_paged_t p = *desc;
+    p.H = p.Hkv;  // (q's heads are not read)
+    clis_status_t st = check_cache(&p, false);
+    if (st == CLIS_OK && quant) st = check_quant(&p, quant, false);
+    if (st == CLIS_OK) st = check_strides({k_st, k_sh, v_st, v_sh});
     if (st != CLIS_OK) return st;
-    clis_rope_t r = *rope;
-    const bool turn = r.pairs != 0;
-    if (!turn) {  // the rotation's other fields are not read then
-        r.pairs = 8;
-        r.axes = 1;
-        r.interleaved = r.inverse = 0;
-        r.Hq = 0;
-        r.q_sb = r.q_sh = r.q_sn = r.qo_sb = r.qo_sh = r.qo_sn = 0;
-        if (q) return CLIS_ERR_INVALID_ARG;
-    }
-    r.ko_sb = r.ko_sh = r.ko_sn = 0;
-    if (r.B != 1 || r.N != desc->T || r.Hk != desc->Hkv || r.d != desc->d || r.dtype != desc->dtype || r.inverse ||
-        (r.Hq != 0 && r.Hq != desc->H))
+    if (p.T > kMaxTokens / 8) return CLIS_ERR_UNSUPPORTED;
+    const int64_t kd[2][2] = {{p.T, k_st}, {p.Hkv, k_sh}}, vd[2][2] = {{p.T, v_st}, {p.Hkv, v_sh}};
+    if (overlapping(p.d, kd, 2) || overlapping(p.d, vd, 2)) return CLIS_ERR_INVALID_ARG;
+    if (p.S == 0 || p.T == 0) return CLIS_OK;
+    if (!k_cache || !v_cache || !block_table || !cu || !k_out || !v_out || (quant && (!k_scale || !v_scale)))
         return CLIS_ERR_INVALID_ARG;
-    if ((st = check_rope(&r, false)) != CLIS_OK) return st;
-    if ((st = check_strides({v_st, v_sh})) != CLIS_OK) return st;
-    if (desc->T == 0) return CLIS_OK;
-    if (!k || !v || !k_cache || !v_cache || !slots || (r.Hq > 0 && (!q || !q_out))) return CLIS_ERR_INVALID_ARG;
-    if (turn && (!positions || !inv_freq || !axis)) return CLIS_ERR_INVALID_ARG;
-    if ((r.Hq > 0 && (!aligned(q, 16) || !aligned(q_out, 16))) || !aligned(k, 16) || !aligned(v, 16) ||
-        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 8) || !aligned(positions, 4) ||
-        !aligned(inv_freq, 8) || !aligned(axis, 4))
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+        !aligned(block_table, 4) || !aligned(cu, 4) || !aligned(start, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
         return CLIS_ERR_MISALIGNED;
-    clis::RotArgs a = rot_args(&r);
-    if (!turn) a.pairs = 0;
-    a.q = static_cast<const uint16_t *>(q);
-    a.k = static_cast<const uint16_t *>(k);
-    a.v = static_cast<const uint16_t *>(v);
-    a.v_sn = v_st;
-    a.v_sh = v_sh;
-    a.qo = static_cast<uint16_t *>(q_out);
-    a.ko = static_cast<uint16_t *>(k_cache);
-    a.ko_sb = desc->kc_sp;
-    a.ko_sh = desc->kc_sh;
-    a.ko_sn = desc->kc_sn;
-    a.vo = static_cast<uint16_t *>(v_cache);
-    a.vo_sb = desc->vc_sp;
-    a.vo_sh = desc->vc_sh;
-    a.vo_sn = desc->vc_sn;
-    a.pos = positions;
-    a.inv_freq = inv_freq;
-    a.axis = axis;
-    a.slots = slots;
-    a.num_slots = desc->num_pages * desc->page_size;
-    a.page_shift = page_shift(desc->page_size);
-    return clis::launch_rot(a, reinterpret_cast<cudaStream_t>(stream));
+    clis::ReadArgs a{};
+    const clis_quant_t none = {};
+    a.z = quant_args(quant ? quant : &none, k_cache, v_cache, k_scale, v_scale);
+    if (!quant) a.z.code = -1;
+    a.block_table = block_table;
+    a.cu = cu;
+    a.start = start;
+    a.ko = static_cast<uint16_t *>(k_out);
+    a.vo = static_cast<uint16_t *>(v_out);
+    a.kc_sp = p.kc_sp;
+    a.kc_sh = p.kc_sh;
+    a.kc_sn = p.kc_sn;
+    a.vc_sp = p.vc_sp;
+    a.vc_sh = p.vc_sh;
+    a.vc_sn = p.vc_sn;
+    a.bt_s = p.bt_ss;
+    a.ko_st = k_st;
+    a.ko_sh = k_sh;
+    a.vo_st = v_st;
+    a.vo_sh = v_sh;
+    a.num_pages = p.num_pages;
+    a.S = static_cast<int>(p.S);
+    a.T = static_cast<int>(p.T);
+    a.Hkv = static_cast<int>(p.Hkv);
+    a.d = static_cast<int>(p.d);
+    a.dtype = static_cast<int>(p.dtype);
+    a.page_shift = page_shift(p.page_size);
+    a.width = static_cast<int>(p.width);
+    return clis::launch_paged_read(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 clis_status_t clis_attn_paged_workspace_size(const clis_paged_t *desc, int64_t max_q, size_t *bytes)
@@ -406,6 +558,78 @@ clis_status_t clis_attn_fwd_paged(const clis_paged_t *desc, const void *q, const
     if (e == CLIS_OK && s.row_tiles > 0)
         e = clis::launch_paged_decode(a, s.row_tiles, !s.chunk, s.chunk, workspace, nsm, cs);
     if (e == CLIS_OK && s.chunk) e = clis::launch_paged_chunk(a, 16 * s.row_tiles, cws, nsm, cs);
+    return e;
+}
+
+clis_status_t clis_attn_paged_q8_workspace_size(const clis_paged_t *desc, const clis_quant_t *quant, int64_t max_q,
+                                                size_t *bytes)
+{
+    if (!desc || !quant || !bytes) return CLIS_ERR_INVALID_ARG;
+    const clis_status_t st = check_attn_q8(desc, quant, max_q);
+    if (st != CLIS_OK) return st;
+    *bytes = 0;
+    if (desc->S == 0 || desc->T == 0) return CLIS_OK;
+    int nsm = 0;
+    if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
+    const Split s = split_q8(desc, max_q);
+    *bytes = clis::paged_q8_workspace(static_cast<int>(desc->d), s.row_tiles, nsm) +
+             (s.chunk ? clis::paged_chunk_workspace(attn_args(desc), nsm) + 2 * pages_bytes(desc) + scales_bytes(desc) : 0);
+    return CLIS_OK;
+}
+
+clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_t *quant, const void *q, const void *k_codes,
+                                     const void *v_codes, const float *k_scale, const float *v_scale,
+                                     const int32_t *block_table, const int32_t *cu_q, const int32_t *kv_len, void *o,
+                                     float *lse2, int64_t max_q, float scale_log2, int causal, void *workspace,
+                                     size_t ws_bytes, clis_stream_t stream)
+{
+    if (!desc || !quant) return CLIS_ERR_INVALID_ARG;
+    const clis_status_t st = check_attn_q8(desc, quant, max_q);
+    if (st != CLIS_OK) return st;
+    if (!std::isfinite(scale_log2) || !(scale_log2 > 0.f)) return CLIS_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return CLIS_ERR_INVALID_ARG;
+    if (desc->S == 0 || desc->T == 0) return CLIS_OK;
+    if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !block_table || !cu_q || !kv_len || !o) return CLIS_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(o, 16) || !aligned(k_scale, 4) ||
+        !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(lse2, 4))
+        return CLIS_ERR_MISALIGNED;
+    int nsm = 0;
+    if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
+    const Split s = split_q8(desc, max_q);
+    clis::PagedArgs a = attn_args(desc);
+    const size_t few = clis::paged_q8_workspace(a.d, s.row_tiles, nsm);
+    const size_t chunk = s.chunk ? clis::paged_chunk_workspace(a, nsm) : 0;
+    const size_t need = few + chunk + (s.chunk ? 2 * pages_bytes(desc) + scales_bytes(desc) : 0);
+    if (need > 0 && (!workspace || ws_bytes < need)) return CLIS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return CLIS_ERR_MISALIGNED;
+    const clis::QuantArgs z = quant_args(quant, k_codes, v_codes, k_scale, v_scale);
+    a.q = static_cast<const uint16_t *>(q);
+    a.o = static_cast<uint16_t *>(o);
+    a.lse2 = lse2;
+    a.block_table = block_table;
+    a.cu_q = cu_q;
+    a.kv_len = kv_len;
+    a.scale_log2 = scale_log2;
+    a.causal = causal;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    char *w = static_cast<char *>(workspace);
+    if (!s.chunk) return clis::launch_paged_q8(a, z, s.row_tiles, true, false, w, nsm, cs);
+    // The chunk kernel works on 16-bit copies of its sequences' pages.
+    clis::PagedArgs b = a;
+    uint16_t *kp = reinterpret_cast<uint16_t *>(w + few + chunk);
+    uint16_t *vp = reinterpret_cast<uint16_t *>(w + few + chunk + pages_bytes(desc));
+    float *ks = reinterpret_cast<float *>(w + few + chunk + 2 * pages_bytes(desc));
+    b.kc = kp;
+    b.vc = vp;
+    b.ks = ks;
+    b.kc_sn = b.vc_sn = a.d;
+    b.kc_sh = b.vc_sh = desc->page_size * a.d;
+    b.kc_sp = b.vc_sp = desc->Hkv * desc->page_size * a.d;
+    const int rows_small = 16 * s.row_tiles;
+    clis_status_t e = clis::launch_paged_unpack(a, z, rows_small, kp, ks, vp, nsm, cs);
+    if (e == CLIS_OK) e = clis::launch_paged_chunk_schedule(b, rows_small, w + few, nsm, cs);
+    if (e == CLIS_OK && s.row_tiles > 0) e = clis::launch_paged_q8(a, z, s.row_tiles, false, true, w, nsm, cs);
+    if (e == CLIS_OK) e = clis::launch_paged_chunk(b, rows_small, w + few, nsm, cs);
     return e;
 }
 

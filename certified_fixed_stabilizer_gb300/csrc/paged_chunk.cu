@@ -54,6 +54,15 @@
 // each of 152 SMs, 593 us; the rest (first tiles, joins, page lookups, 84 bytes of
 // registers that the softmax warps spill at d = 128) has not been taken apart.
 //
+// Over a cache of 8-bit codes (KS) K's pages hold the codes themselves, exact in 16 bits,
+// and a key's scale multiplies its scores: in the weights' multiply-add scale_log2
+// becomes a factor per key, and the maximum costs a multiplication per score, off the
+// chain.  (With the values rounded to bf16 first, the outputs of 2,048 tokens behind 30,011
+// were off by 4.4e-3, rounding the keys alone 3.6e-3.)  The K/V producer brings the scales
+// into a ring of kScaleTiles tiles of shared memory.  K of tile n is loaded when the scores of
+// tile n - NSTAGE / 2 have been computed, so both softmax groups are done with tile n - 3 -
+// NSTAGE / 2 at least, and its place in the ring of scales is free.
+//
 // Every wait is bounded.
 #include <cuda_bf16.h>
 
@@ -70,6 +79,7 @@ namespace {
 constexpr int BM = kChunkRows, BN = kChunkKeys;
 constexpr int kThreads = 512;
 constexpr int kNStageMax = 8;
+constexpr int kScaleTiles = 8;  // more than 3 + NSTAGE / 2
 constexpr float kTau = 8.0f;
 constexpr int kSchedThreads = 256;
 // Items of three parts or more: every block but the last adds at most one part to
@@ -87,6 +97,7 @@ struct Cfg {
     static constexpr int BOX_BYTES = 128 * 128;
     static constexpr int TILE_BYTES = NBOX * BOX_BYTES;
     static constexpr int SMEM_BYTES = 2 * TILE_BYTES + NSTAGE * TILE_BYTES + 1024;
+    static constexpr int SCALE_BYTES = kScaleTiles * BN * 4;  // behind them
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t TM_S0 = 0, TM_S1 = 128, TM_O0 = 256, TM_O1 = 256 + D;
 };
@@ -320,11 +331,12 @@ abort:
         if (wt[t] > 0) drain_wait(smem_u32(&c.q_full[t]), (wt[t] - 1) & 1);
 }
 
-template <int D>
+template <int D, bool KS>
 __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
-                              uint32_t sKV, const Run &R)
+                              uint32_t sKV, float *scales, const Run &R)
 {
     using C = Cfg<D>;
+    static_assert(kScaleTiles > 3 + C::NSTAGE / 2, "a tile's scales are in use when others replace them");
     const PagedArgs &a = p.a;
     volatile int *ab = &c.abort_flag;
     unsigned *err = &g_chunk_error_word;
@@ -334,9 +346,35 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
     const uint64_t pol = policy_evict_last();
     uint32_t it = 0, gq = 0;
     unsigned int bad = 0;
+    uint32_t kt_all = 0;  // K tiles so far
     CLIS_FOR_WORK(K)
     {
         const ChunkItem &T = K.t;
+        // Scales of the lane's four keys of key tile kt (a page holds at least eight): their
+        // page two tiles ahead, themselves one.  Keys behind the last, and those of pages
+        // out of range, get a scale all the same: -inf times it is -inf.
+        auto scale_page = [&](int kt) -> int {
+            const int key = kt * BN + lane * 4;
+            return key < T.kv && kt < K.start + K.n ? __ldg(a.block_table + T.s * a.bt_s + (key >> a.page_shift)) : -1;
+        };
+        auto scale_of = [&](int kt, int pg) -> float4 {
+            float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
+            const int key = kt * BN + lane * 4;
+            if (pg < 0 || pg >= a.num_pages) return x;
+            const float4 y = __ldg(reinterpret_cast<const float4 *>(
+                a.ks + ((static_cast<int64_t>(pg) * a.Hkv + T.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))));
+            x.x = y.x;
+            if (key + 1 < T.kv) x.y = y.y;
+            if (key + 2 < T.kv) x.z = y.z;
+            if (key + 3 < T.kv) x.w = y.w;
+            return x;
+        };
+        float4 sc = make_float4(1.f, 1.f, 1.f, 1.f);
+        int sc_page = -1;
+        if constexpr (KS) {
+            sc = scale_of(K.start, scale_page(K.start));
+            sc_page = scale_page(K.start + 1);
+        }
         // Whether the lane has rows of key tile kt to load (none behind the last key), and
         // their page.  What the table holds is looked at when it is used, a tile later (any
         // number can stand there, so none can say that there is nothing to load).
@@ -358,6 +396,17 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
                     goto abort;
             }
             const uint32_t bar = smem_u32(&c.kv_full[gq % C::NSTAGE]);
+            if constexpr (KS) {
+                if (has_k) {  // (before the arrival on the group's barrier)
+                    const float lo = 1.17549435e-38f, sl2 = a.scale_log2;
+                    *reinterpret_cast<float4 *>(scales + (kt_all % kScaleTiles) * BN + lane * 4) =
+                        make_float4(fmaxf(sc.x * sl2, lo), fmaxf(sc.y * sl2, lo), fmaxf(sc.z * sl2, lo), fmaxf(sc.w * sl2, lo));
+                    ++kt_all;
+                    sc = scale_of(K.start + gi + 1, sc_page);
+                    sc_page = scale_page(K.start + gi + 2);
+                    __syncwarp();
+                }
+            }
             const int live = __popc(__ballot_sync(~0u, rows_v)) + __popc(__ballot_sync(~0u, rows_k));
             if (lane == 0) mbar_arrive_expect_tx(bar, live * C::NBOX * box_bytes);
             __syncwarp();
@@ -647,16 +696,23 @@ abort:
 // Weights of a row's 128 scores for a shift, p = 2^(scale_log2 s - shift), packed in
 // pairs over the first 64 columns of the scores, all of which have been read;
 // returns their sum (before rounding).
-template <int DT>
-__device__ __forceinline__ float weights128(const uint32_t *s, float sl2, float nshift, uint32_t tP)
+// KS: scale_log2 times the key's scale is read from ks.
+template <int DT, bool KS>
+__device__ __forceinline__ float weights128(const uint32_t *s, float sl2, const float *ks, float nshift, uint32_t tP)
 {
-    const float2 sc2 = make_float2(sl2, sl2), sh2 = make_float2(nshift, nshift);
+    float2 sc2 = make_float2(sl2, sl2);
+    const float2 sh2 = make_float2(nshift, nshift);
+    float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f);
     float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c32 = 0; c32 < BN / 32; c32++) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; e++) {
+            if constexpr (KS) {
+                if (e % 2 == 0) k4 = *reinterpret_cast<const float4 *>(ks + c32 * 32 + 2 * e);
+                sc2 = e % 2 == 0 ? make_float2(k4.x, k4.y) : make_float2(k4.z, k4.w);
+            }
             const float2 x = ffma2(
                 make_float2(__uint_as_float(s[c32 * 32 + 2 * e]), __uint_as_float(s[c32 * 32 + 2 * e + 1])), sc2, sh2);
             const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
@@ -670,8 +726,8 @@ __device__ __forceinline__ float weights128(const uint32_t *s, float sl2, float 
     return l.x + l.y;
 }
 
-template <int D, int DT>
-__device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int warp, int lane, const Run &R)
+template <int D, int DT, bool KS>
+__device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, const float *scales, int warp, int lane, const Run &R)
 {
     using C = Cfg<D>;
     volatile int *ab = &c.abort_flag;
@@ -686,6 +742,7 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
     const int row_tok = rl / p.g;  // token within the row tile
     uint32_t g = 0;
     int w = 0;
+    uint32_t kt_all = 0;  // K tiles of the items before
     CLIS_FOR_WORK(K)
     {
         const ChunkItem &T = K.t;
@@ -712,16 +769,20 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
                 for (int cc = 0; cc < BN; cc++)
                     if (key0 + cc >= lim) s[cc] = 0xFF800000u;  // -inf
             }
+            const float *ks = scales + ((kt_all + j) % kScaleTiles) * BN;
             float l = 0.f;
-            if (begun) l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
+            if (begun) l = weights128<DT, KS>(s, sl2, ks, (m_run == -INFINITY) ? 0.f : -m_run, tS);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int cc = 0; cc < BN; cc += 8) {
 #pragma unroll
-                for (int q4 = 0; q4 < 4; q4++)
-                    mx[q4] = fmax3(mx[q4], __uint_as_float(s[cc + 2 * q4]), __uint_as_float(s[cc + 2 * q4 + 1]));
+                for (int q4 = 0; q4 < 4; q4++) {
+                    float2 x = make_float2(__uint_as_float(s[cc + 2 * q4]), __uint_as_float(s[cc + 2 * q4 + 1]));
+                    if constexpr (KS) x = fmul2(x, *reinterpret_cast<const float2 *>(ks + cc + 2 * q4));
+                    mx[q4] = fmax3(mx[q4], x.x, x.y);
+                }
             }
-            const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+            const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (KS ? 1.f : sl2);
             const bool grow = m_tile > m_run + (kTau + weight_room(DT));  // always true where a row's first visible key is
             if (__any_sync(0xFFFFFFFFu, grow) || !begun) {
                 // Raise the shift, compute the tile's weights (again), and shrink O once the
@@ -732,7 +793,7 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
                 l_run *= alpha;
                 // (stores to TMEM are asynchronous: the weights that these replace must be in place)
                 if (begun) tmem_wait_st();
-                l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
+                l = weights128<DT, KS>(s, sl2, ks, (m_run == -INFINITY) ? 0.f : -m_run, tS);
                 if (begun) {
                     if (!mbar_wait(smem_u32(&c.pv_done[t]), (g - 1) & 1, ab, err, kErrSoftmax)) return;
                     tc_fence_after();
@@ -765,6 +826,7 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, int wa
         c.epi_l[t][rl] = l_run;
         c.epi_shift[t][rl] = m_run;
         mbar_arrive(smem_u32(&c.epi_full[t]));
+        kt_all += K.n;
         ++w;
     }
 }
@@ -1061,7 +1123,7 @@ __device__ void epilogue_role(const ChunkParams &p, Ctl &c, uint32_t tmem, uint3
 
 // -------------------------------------------------------------------- kernel
 
-template <int D, int DT>
+template <int D, int DT, bool KS>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const ChunkParams p)
@@ -1072,6 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sbase = (smem_u32(dsmem) + 1023u) & ~1023u;
     const uint32_t sQ0 = sbase;
     const uint32_t sKV = sbase + 2 * C::TILE_BYTES;
+    float *scales = reinterpret_cast<float *>(dsmem + (sKV + C::NSTAGE * C::TILE_BYTES - smem_u32(dsmem)));  // (KS)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -1126,13 +1189,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // epilogue 128 x 80, the other four warps 128 x 80.
     if (warp < 8) {
         setmaxnreg_inc<176>();
-        softmax_role<D, DT>(p, ctl, tmem, warp, lane, R);
+        softmax_role<D, DT, KS>(p, ctl, tmem, scales, warp, lane, R);
     } else if (warp < 12) {
         setmaxnreg_dec<80>();
         epilogue_role<D, DT>(p, ctl, tmem, sKV, warp, lane, R);
     } else {
         setmaxnreg_dec<80>();
-        if (warp == 12) producer_role<D>(p, ctl, &tm_k, &tm_v, sKV, R);
+        if (warp == 12) producer_role<D, KS>(p, ctl, &tm_k, &tm_v, sKV, scales, R);
         if (warp == 13) mma_role<D, DT>(p, ctl, tmem, sQ0, sKV, R);
         if (warp == 14) q_producer_role<D>(p, ctl, &tm_q, sQ0, R);
         if (warp == 15) edge_role<D, DT>(p, ctl, sKV, R);
@@ -1269,13 +1332,13 @@ size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 int64_t max_items(const PagedArgs &a) { return chunk_list(a.T, a.S, a.H / a.Hkv, a.Hkv); }
 
-template <int D, int DT>
+template <int D, int DT, bool KS>
 clis_status_t launch_impl(const ChunkParams &p, cudaStream_t stream)
 {
     using C = Cfg<D>;
     const PagedArgs &a = p.a;
-    if (cudaFuncSetAttribute(paged_chunk_kernel<D, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
-        cudaSuccess)
+    constexpr int smem = C::SMEM_BYTES + (KS ? C::SCALE_BYTES : 0);
+    if (cudaFuncSetAttribute(paged_chunk_kernel<D, DT, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return CLIS_ERR_CUDA;
     CUtensorMap mq, mk, mv;
     {
@@ -1291,7 +1354,7 @@ clis_status_t launch_impl(const ChunkParams &p, cudaStream_t stream)
         const int64_t ks[3] = {a.kc_sn, a.kc_sh, a.kc_sp}, vs[3] = {a.vc_sn, a.vc_sh, a.vc_sp};
         if (!encode(&mk, a.kc, DT, 4, dims, ks, box) || !encode(&mv, a.vc, DT, 4, dims, vs, box)) return CLIS_ERR_CUDA;
     }
-    if (launch_pdl(paged_chunk_kernel<D, DT>, dim3(p.grid), kThreads, C::SMEM_BYTES, stream, mq, mk, mv, p) != cudaSuccess)
+    if (launch_pdl(paged_chunk_kernel<D, DT, KS>, dim3(p.grid), kThreads, smem, stream, mq, mk, mv, p) != cudaSuccess)
         return CLIS_ERR_CUDA;
     // One wave of blocks over the list; mostly it is short or empty.
     const int64_t items = max_items(a), wave = p.grid / 8;
@@ -1362,8 +1425,12 @@ clis_status_t launch_paged_chunk(const PagedArgs &a, int rows_small, void *works
 {
     const ChunkParams p = chunk_params(a, rows_small, workspace, nsm);
     const bool f16 = a.dtype == CLIS_DT_FP16;
-    if (a.d == 128) return f16 ? launch_impl<128, 1>(p, stream) : launch_impl<128, 0>(p, stream);
-    return f16 ? launch_impl<64, 1>(p, stream) : launch_impl<64, 0>(p, stream);
+    if (a.ks) {
+        if (a.d == 128) return f16 ? launch_impl<128, 1, true>(p, stream) : launch_impl<128, 0, true>(p, stream);
+        return f16 ? launch_impl<64, 1, true>(p, stream) : launch_impl<64, 0, true>(p, stream);
+    }
+    if (a.d == 128) return f16 ? launch_impl<128, 1, false>(p, stream) : launch_impl<128, 0, false>(p, stream);
+    return f16 ? launch_impl<64, 1, false>(p, stream) : launch_impl<64, 0, false>(p, stream);
 }
 
 clis_status_t read_chunk_error(uint32_t *code)

@@ -32,9 +32,7 @@
 // us with the join (5 us), 97 to 100% of the measured copy rate.
 #include <cuda_bf16.h>
 
-#include "clis_internal.h"
-#include "paged_internal.h"
-#include "sm103_ptx.cuh"
+#include "paged_warp.cuh"
 
 namespace clis {
 
@@ -42,10 +40,9 @@ __device__ unsigned int g_decode_error_word = 0;
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = kDecodeWarps;
+constexpr int kThreads = kDecodeThreads;
 constexpr float kTau = 8.0f;
-constexpr int kJoinThreads = 256;
 
 template <int D>
 struct DCfg {
@@ -56,58 +53,6 @@ struct DCfg {
     static constexpr int STAGE = 2 * HALF;
     static constexpr int SMEM = kWarps * NST * STAGE;
 };
-
-struct DecodeParams {
-    PagedArgs a;
-    int g, rows_max, least;
-    int workers;     // warps of the grid
-    int strict;  // no chunk kernel follows: a sequence of more rows is an error
-    float *part_o;   // [2 * workers][rows_max][D]: place 2 c + 1 if worker c starts the item, 2 c if it goes on with it
-    float2 *part_ml; // [2 * workers][rows_max]
-    int4 *meta;      // [workers] {parts, first row of q, new tokens, head} of the item the worker starts and does not finish
-};
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t *r)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t *r)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-template <int DT>
-__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
-{
-    if (DT)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 // Clears the non-finite halves of a pair; true if there was one.
 template <int DT>
@@ -120,39 +65,6 @@ __device__ __forceinline__ bool scrub(uint32_t &u)
     u &= keep;
     return keep != 0xFFFFFFFFu;
 }
-
-__device__ __forceinline__ SeqLen seq_len(const PagedArgs &a, int s)
-{
-    return clip_seq(__ldg(a.cu_q + s), __ldg(a.cu_q + s + 1), __ldg(a.kv_len + s), a.T, a.width << a.page_shift);
-}
-
-// Position in the block's run: unit j of item (s, h).
-struct Pos {
-    int s, h, j, units;
-    SeqLen q;
-    uint32_t left;  // units of the run from this one on
-
-    __device__ __forceinline__ void set(const PagedArgs &a, int seq)
-    {
-        s = seq;
-        q = seq_len(a, s);
-        units = decode_units(q, decode_keys(a.d));
-    }
-    // The next item of the run (there is one if units are left).
-    __device__ __forceinline__ void next_item(const PagedArgs &a, int g, int rows_max)
-    {
-        j = 0;
-        if (++h < a.Hkv) return;
-        h = 0;
-        int n = s + 1;
-        while (n < a.S) {
-            set(a, n);
-            if (is_decode(q, g, rows_max)) return;
-            ++n;
-        }
-        left = 0;  // not reached while the run's units are counted alike
-    }
-};
 
 template <int D, int DT, int MT>
 __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeParams p)
@@ -167,51 +79,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     unsigned int bad = 0;
     pdl_launch();
 
-    // ---- the four warps' runs of units (neighbouring runs go to different blocks)
-    const int per = (a.S + kThreads - 1) / kThreads;
-    const int sb = min(a.S, tid * per), se = min(a.S, sb + per);
-    uint64_t mine = 0;
-    for (int s = sb; s < se; s++) {
-        const SeqLen q = seq_len(a, s);
-        if (q.bad) bad |= CLIS_PAGED_LENGTH_BIT;
-        if (is_decode(q, p.g, p.rows_max)) mine += static_cast<uint64_t>(a.Hkv) * decode_units(q, C::TK);
-        else if (p.strict && q.n > 0) bad |= CLIS_PAGED_LENGTH_BIT;
-    }
-    uint64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t up = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += up;
-    }
-    if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
-    uint64_t U = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-        if (w < warp) before += s_sum[w];
-        U += s_sum[w];
-    }
-    const uint64_t excl = before + incl - mine;
-    const int nb = decode_workers(U, p.workers, p.least);
-    for (int w = 0; w < kWarps; w++) {
-        const int cw = w * gridDim.x + blockIdx.x;
-        if (cw >= nb) break;
-        const uint64_t u = decode_cut(U, nb, cw);
-        if (u < excl || u >= excl + mine) continue;
-        uint64_t rel = u - excl;
-        for (int s = sb; s < se; s++) {
-            const SeqLen q = seq_len(a, s);
-            if (!is_decode(q, p.g, p.rows_max)) continue;
-            const uint64_t n = static_cast<uint64_t>(a.Hkv) * decode_units(q, C::TK);
-            if (rel < n) {
-                s_seq[w] = s;
-                s_rel[w] = rel;
-                break;
-            }
-            rel -= n;
-        }
-    }
-    __syncthreads();
+    const Runs runs = block_runs<C::TK, kWarps>(p, s_sum, s_seq, s_rel, bad);
+    const uint64_t U = runs.U;
+    const int nb = runs.nb;
     const int c = warp * gridDim.x + blockIdx.x;  // this worker
     if (lane == 0) p.meta[c] = make_int4(0, 0, 0, 0);
     if (bad && blockIdx.x == 0) atomicOr(&g_decode_error_word, bad);
@@ -222,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     }
     const uint64_t u0 = decode_cut(U, nb, c), u1 = decode_cut(U, nb, c + 1);
 
-    Pos cur;
+    Pos<C::TK> cur;
     cur.set(a, s_seq[warp]);
     cur.h = static_cast<int>(div64(s_rel[warp], cur.units));
     cur.j = static_cast<int>(s_rel[warp] - static_cast<uint64_t>(cur.h) * cur.units);
@@ -235,13 +105,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     const uint32_t ring = smem_u32(smem) + warp * C::NST * C::STAGE;
     const int key_mask = (1 << a.page_shift) - 1;
     const int lrow = lane / CPR, lchunk = lane % CPR;
-    Pos ld = cur;
+    Pos<C::TK> ld = cur;
     int ld_stage = 0;
     // Page of the lane's key of the tile that the loader is at, read one unit ahead.  What
     // the table holds is looked at when it is used (any number can stand there, so none
     // can say that there is no key: `lane_key` does).
-    auto lane_key = [&](const Pos &q) { return q.j * C::TK + (lane & (C::TK - 1)); };
-    auto page_at = [&](const Pos &q) -> int {
+    auto lane_key = [&](const Pos<C::TK> &q) { return q.j * C::TK + (lane & (C::TK - 1)); };
+    auto page_at = [&](const Pos<C::TK> &q) -> int {
         const int key = lane_key(q);
         if (q.left == 0 || key >= q.q.kv) return -1;
         return __ldg(a.block_table + q.s * a.bt_s + (key >> a.page_shift));
@@ -492,12 +362,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
                 }
             }
         if (!whole && j0 == 0 && lane == 0) {
-            // The item's remaining units lie in the next workers' runs; how many workers:
+            // The item's remaining units lie in the next workers' runs.
             const uint64_t end = u1 - cur.left + cur.units - 1;  // the item's last unit
-            int ce = static_cast<int>(div64(end * static_cast<uint32_t>(nb), U));
-            while (ce > c && decode_cut(U, nb, ce) > end) ce--;
-            while (ce + 1 < nb && decode_cut(U, nb, ce + 1) <= end) ce++;
-            p.meta[c] = make_int4(ce - c + 1, q0, n, cur.h);
+            p.meta[c] = make_int4(item_parts(runs, c, end), q0, n, cur.h);
         }
         cur.left -= j1 - j0;
         cur.j = j1;
@@ -506,106 +373,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     cp_async_wait<0>();
     if (bad) atomicOr(&g_decode_error_word, bad);
     pdl_wait();  // (the schedule kernel, whose results only later kernels read)
-}
-
-// Adds the partial results of the items that workers of the decode kernel started
-// and did not finish: worker c's own and those at the start of the following
-// workers' runs, a few, or a hundred where there are few sequences.  A block looks
-// after kJoinEach neighbouring workers; its warps share out the rows of the items
-// that those started, and where there are fewer rows than warps the parts of each
-// row too (by counts alone, and added in a fixed order: reruns agree bit for bit).
-// blockIdx.y: where an item has many rows, blocks take turns.
-constexpr int kJoinEach = 8;
-
-template <int D, int DT>
-__global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const DecodeParams p)
-{
-    constexpr int V = D / 32, W = kJoinThreads / 32, B = 8;  // columns per lane, warps, loads in flight
-    __shared__ int4 s_meta[kJoinEach];
-    __shared__ float s_o[W][D];
-    __shared__ float2 s_ml[W];
-    const PagedArgs &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int c0 = blockIdx.x * kJoinEach;
-    pdl_wait();
-    pdl_launch();
-    if (tid < kJoinEach) s_meta[tid] = c0 + tid < p.workers ? p.meta[c0 + tid] : make_int4(0, 0, 0, 0);
-    __syncthreads();
-    int rows = 0;
-#pragma unroll
-    for (int i = 0; i < kJoinEach; i++) rows += s_meta[i].x ? s_meta[i].z * p.g : 0;
-    const int mine = (rows + gridDim.y - 1) / gridDim.y;  // rows of this block
-    int per = W;                                          // warps per row
-    while (per > 1 && mine * per > W) per /= 2;
-    for (int r0 = blockIdx.y * (W / per); r0 < rows; r0 += gridDim.y * (W / per)) {
-        const int sub = warp % per;
-        int row = r0 + warp / per, i = 0;
-        const bool live = row < rows;
-        if (live)
-            while (true) {  // the item that the row belongs to
-                const int n = s_meta[i].x ? s_meta[i].z * p.g : 0;
-                if (row < n) break;
-                row -= n;
-                i++;
-            }
-        const int4 mt = s_meta[live ? i : 0];
-        const int c = c0 + i;
-        float M = -INFINITY, l = 0.f, o[V];
-#pragma unroll
-        for (int e = 0; e < V; e++) o[e] = 0.f;
-        auto add = [&](float m1, float l1, const float *x) {
-            if (l1 == 0.f) return;  // a part none of whose keys the row sees
-            const float m = fmaxf(M, m1), w = ex2_approx(m1 - m);
-            const bool none = l == 0.f;
-            const float w0 = none ? 0.f : ex2_approx(M - m);
-            M = m;
-            l = none ? w * l1 : fmaf(l, w0, w * l1);
-#pragma unroll
-            for (int e = 0; e < V; e++) o[e] = none ? w * x[e] : fmaf(o[e], w0, w * x[e]);
-        };
-        if (live) {
-            for (int k0 = sub; k0 < mt.x; k0 += B * per) {
-                float2 ml[B];
-                float x[B][V];
-#pragma unroll
-                for (int e = 0; e < B; e++) {
-                    const int k = k0 + e * per;
-                    ml[e] = make_float2(0.f, 0.f);
-                    if (k >= mt.x) continue;
-                    const int64_t at = static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * p.rows_max + row;
-                    ml[e] = p.part_ml[at];
-                    if constexpr (V == 4) {
-                        const float4 u = reinterpret_cast<const float4 *>(p.part_o + at * D)[lane];
-                        x[e][0] = u.x; x[e][1] = u.y; x[e][2] = u.z; x[e][3] = u.w;
-                    } else {
-                        const float2 u = reinterpret_cast<const float2 *>(p.part_o + at * D)[lane];
-                        x[e][0] = u.x; x[e][1] = u.y;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < B; e++) add(ml[e].x, ml[e].y, x[e]);
-            }
-        }
-        if (per > 1) {
-#pragma unroll
-            for (int e = 0; e < V; e++) s_o[warp][lane * V + e] = o[e];
-            if (lane == 0) s_ml[warp] = make_float2(M, l);
-            __syncthreads();
-            if (sub == 0)
-                for (int w = 1; w < per; w++) add(s_ml[warp + w].x, s_ml[warp + w].y, &s_o[warp + w][lane * V]);
-            __syncthreads();
-        }
-        if (live && sub == 0) {
-            const float inv = 1.f / l;
-            const int tok = row / p.g, hd = mt.w * p.g + (row - tok * p.g);
-            uint16_t *dst = a.o + static_cast<int64_t>(mt.y + tok) * a.o_st + hd * a.o_sh + lane * V;
-#pragma unroll
-            for (int e = 0; e < V; e += 2)  // (zeros for a row that sees no key)
-                *reinterpret_cast<uint32_t *>(dst + e) = l == 0.f ? 0u : pack2<DT>(o[e] * inv, o[e + 1] * inv);
-            if (lane == 0 && a.lse2)
-                a.lse2[static_cast<int64_t>(mt.y + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
-        }
-    }
 }
 
 template <int D, int DT, int MT>
@@ -621,13 +388,8 @@ clis_status_t launch_impl(const DecodeParams &p, int grid, bool after_schedule, 
         paged_decode_kernel<D, DT, MT><<<grid, kThreads, DCfg<D>::SMEM, stream>>>(p);
         if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
     }
-    return launch_pdl(paged_decode_join_kernel<D, DT>, dim3((p.workers + kJoinEach - 1) / kJoinEach, p.rows_max / 4), kJoinThreads, 0,
-                      stream, p) == cudaSuccess
-               ? CLIS_OK
-               : CLIS_ERR_CUDA;
+    return launch_join<D, DT>(p, stream) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
-
-size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
@@ -644,29 +406,19 @@ int paged_decode_row_tiles(int64_t max_q, int g, int d)
 size_t paged_decode_workspace(int d, int row_tiles, int nsm)
 {
     if (row_tiles == 0) return 0;
-    const size_t workers = 2 * static_cast<size_t>(nsm) * kWarps, rows = 16 * static_cast<size_t>(row_tiles);
-    return up256(workers * sizeof(int4)) + up256(2 * workers * rows * sizeof(float2)) +
-           up256(2 * workers * rows * d * sizeof(float));
+    return parts_workspace(2 * static_cast<size_t>(nsm) * kWarps, 16 * static_cast<size_t>(row_tiles), d);
 }
 
 clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, bool after_schedule, void *workspace,
                                   int nsm, cudaStream_t stream)
 {
     const int grid = 2 * nsm;  // two blocks fit an SM
-    const size_t workers = static_cast<size_t>(grid) * kWarps, rows = 16 * static_cast<size_t>(row_tiles);
     DecodeParams p;
     p.a = a;
     p.g = a.H / a.Hkv;
-    p.rows_max = static_cast<int>(rows);
     p.least = 2;  // units of a worker's run: one token over 301 keys 12.8 us with 2, 14 with 1 or 4, 16.5 with 8
-    p.workers = static_cast<int>(workers);
     p.strict = strict;
-    char *w = static_cast<char *>(workspace);
-    p.meta = reinterpret_cast<int4 *>(w);
-    w += up256(workers * sizeof(int4));
-    p.part_ml = reinterpret_cast<float2 *>(w);
-    w += up256(2 * workers * rows * sizeof(float2));
-    p.part_o = reinterpret_cast<float *>(w);
+    place_parts(p, static_cast<size_t>(grid) * kWarps, 16 * static_cast<size_t>(row_tiles), workspace);
 #define CLIS_DECODE(D, MT)                                                  \
     return a.dtype == CLIS_DT_FP16 ? launch_impl<D, 1, MT>(p, grid, after_schedule, stream) \
                                    : launch_impl<D, 0, MT>(p, grid, after_schedule, stream)

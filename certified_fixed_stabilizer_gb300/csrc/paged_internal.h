@@ -33,6 +33,11 @@ struct RotArgs {
     int pairs, axes;
     int interleaved, inverse;
     int dtype;
+    // A quantised cache (code >= 0, a clis_code_t): ko and vo hold codes (their strides
+    // count bytes), and every row written has a scale.
+    int code = -1;
+    float *ks, *vs;
+    int64_t ks_sp, ks_sh, ks_sn, vs_sp, vs_sh, vs_sn;
 };
 
 clis_status_t launch_rot(const RotArgs &a, cudaStream_t stream);
@@ -68,7 +73,38 @@ struct PagedArgs {
     int S, T, H, Hkv, d, dtype, page_shift, width;
     float scale_log2;
     int causal;
+    // The chunk kernel over unpacked codes: K's pages hold codes, ks [num_pages][Hkv][page
+    // size] their scales, positive and finite.  nullptr: K's pages hold values.
+    const float *ks = nullptr;
 };
+
+// A quantised cache: codes (strides in PagedArgs, in bytes) and their scales.
+struct QuantArgs {
+    const uint8_t *kc, *vc;
+    const float *ks, *vs;
+    int64_t ks_sp, ks_sh, ks_sn, vs_sp, vs_sh, vs_sn;
+    int code;
+};
+
+// Cached tokens as 16-bit rows.  z.code < 0: the cache holds 16-bit values (z.kc, z.vc,
+// strides in elements).
+struct ReadArgs {
+    QuantArgs z;
+    const int32_t *block_table, *cu, *start;  // start: nullptr, or the first token of each sequence
+    uint16_t *ko, *vo;
+    int64_t kc_sp, kc_sh, kc_sn, vc_sp, vc_sh, vc_sn, bt_s;
+    int64_t ko_st, ko_sh, vo_st, vo_sh;
+    int64_t num_pages;
+    int S, T, Hkv, d, dtype, page_shift, width;
+};
+
+clis_status_t launch_paged_read(const ReadArgs &a, cudaStream_t stream);
+// Every key and value of the sequences that the chunk kernel works on, in 16 bits in
+// pages of the same numbers, [num_pages][Hkv][page size][d] each: K's codes as they are
+// with their scales in k_scale [num_pages][Hkv][page size], V's values.  A K row whose scale
+// is below 2^-100, above 2^100 or no number is given as values, with the scale 1.
+clis_status_t launch_paged_unpack(const PagedArgs &a, const QuantArgs &z, int rows_small, uint16_t *k_pages, float *k_scale,
+                                  uint16_t *v_pages, int nsm, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Programmatic dependent launch.  A kernel launched by launch_pdl may start while
@@ -105,6 +141,11 @@ size_t paged_decode_workspace(int d, int row_tiles, int nsm);
 // does not read.
 clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, bool after_schedule, void *workspace,
                                   int nsm, cudaStream_t stream);
+// The same over a quantised cache: row tiles 1, 2, 4 or 0.
+int paged_q8_row_tiles(int64_t max_q, int g);
+size_t paged_q8_workspace(int d, int row_tiles, int nsm);
+clis_status_t launch_paged_q8(const PagedArgs &a, const QuantArgs &z, int row_tiles, bool strict, bool after_schedule,
+                              void *workspace, int nsm, cudaStream_t stream);
 size_t paged_chunk_workspace(const PagedArgs &a, int nsm);
 // Sequences of at most rows_small query rows are left to the decode kernel.
 // Schedule first, then (with rows_small > 0) the decode kernel, then the chunk kernel:
@@ -124,5 +165,9 @@ clis_status_t read_decode_error(uint32_t *code);
 clis_status_t clear_decode_error();
 clis_status_t read_chunk_error(uint32_t *code);
 clis_status_t clear_chunk_error();
+clis_status_t read_q8_error(uint32_t *code);
+clis_status_t clear_q8_error();
+clis_status_t read_read_error(uint32_t *code);
+clis_status_t clear_read_error();
 
 }  // namespace clis

@@ -72,12 +72,93 @@ __device__ __forceinline__ void rotate8(uint4 &u0, uint4 &u1, const float *cs, c
     u1 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// NC: 16-element chunks per row (d / 16).  hg: heads per block row of the grid.
+// The same in fp32, unrounded: f0, f1 are the values of u0 and u1.
+template <int DT>
+__device__ __forceinline__ void rotate8f(const uint4 &u0, const uint4 &u1, float *f0, float *f1, const float *cs, const float *sn,
+                                         bool interleaved, bool first, bool second)
+{
+    const uint32_t a[4] = {u0.x, u0.y, u0.z, u0.w}, b[4] = {u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const float p0 = elem_lo<DT>(a[e]), q0 = elem_hi<DT>(a[e]), p1 = elem_lo<DT>(b[e]), q1 = elem_hi<DT>(b[e]);
+        f0[2 * e] = p0;
+        f0[2 * e + 1] = q0;
+        f1[2 * e] = p1;
+        f1[2 * e + 1] = q1;
+        if (interleaved) {
+            if (first) {
+                f0[2 * e] = fmaf(p0, cs[e], -q0 * sn[e]);
+                f0[2 * e + 1] = fmaf(q0, cs[e], p0 * sn[e]);
+            }
+            if (second) {
+                f1[2 * e] = fmaf(p1, cs[4 + e], -q1 * sn[4 + e]);
+                f1[2 * e + 1] = fmaf(q1, cs[4 + e], p1 * sn[4 + e]);
+            }
+        } else if (first) {
+            f0[2 * e] = fmaf(p0, cs[2 * e], -p1 * sn[2 * e]);
+            f0[2 * e + 1] = fmaf(q0, cs[2 * e + 1], -q1 * sn[2 * e + 1]);
+            f1[2 * e] = fmaf(p1, cs[2 * e], p0 * sn[2 * e]);
+            f1[2 * e + 1] = fmaf(q1, cs[2 * e + 1], q0 * sn[2 * e + 1]);
+        }
+    }
+}
+
+// Eight values times `mul` as codes.  int8: adding 1.5 * 2^23 leaves the nearest whole
+// number (ties to even) in the low bits; |value * mul| is at most 127.
+template <int CODE>
+__device__ __forceinline__ uint2 codes8(const float *f, float mul)
+{
+    if (CODE == CLIS_CODE_E4M3)
+        return make_uint2(pack_e4m3x4(f[0] * mul, f[1] * mul, f[2] * mul, f[3] * mul),
+                          pack_e4m3x4(f[4] * mul, f[5] * mul, f[6] * mul, f[7] * mul));
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) w[e] = __float_as_uint(fmaf(f[e], mul, 12582912.f));
+    return make_uint2(__byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
+}
+
+// A row's 16 values of this thread (the row lies in NC neighbouring lanes) into codes
+// at dst + e0 and dst + e1, and its scale.  The scale is the row's largest magnitude over
+// that of the codes; a row below 2^-100 becomes zeros (1 / scale would overflow), one that
+// holds a non-finite value gets the scale NaN and the codes 0, so it reads back as NaN.
+template <int CODE, int NC>
+__device__ __forceinline__ void store_codes(const float *f0, const float *f1, uint8_t *dst, int e0, int e1, float *scale)
+{
+    uint32_t top = 0;  // (bits of magnitudes are ordered, infinity and NaN above the numbers)
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        top = max(top, max(__float_as_uint(f0[e]) & 0x7FFFFFFFu, __float_as_uint(f1[e]) & 0x7FFFFFFFu));
+    const int lane = threadIdx.x & 31;
+    const unsigned mask = ((1u << NC) - 1u) << (lane & ~(NC - 1));
+#pragma unroll
+    for (int o = 1; o < NC; o <<= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+    constexpr float kTop = CODE == CLIS_CODE_INT8 ? 127.f : 448.f;
+    const float t = __uint_as_float(top);
+    uint2 c0 = make_uint2(0u, 0u), c1 = c0;
+    float sc = 0.f;
+    if (top >= 0x7F800000u) {
+        sc = __uint_as_float(0x7FC00000u);
+    } else if (t >= 7.888609052210118e-31f) {  // 2^-100
+        const float mul = kTop / t;
+        sc = t / kTop;
+        c0 = codes8<CODE>(f0, mul);
+        c1 = codes8<CODE>(f1, mul);
+    }
+    *reinterpret_cast<uint2 *>(dst + e0) = c0;
+    *reinterpret_cast<uint2 *>(dst + e1) = c1;
+    if ((lane & (NC - 1)) == 0) *scale = sc;
+}
+
+// NC: 16-element chunks per row (d / 16).  MODE: 0 rotation, 1 into a
+// cache, 2 + c into a cache of codes of kind c.  hg: heads per block row of the grid.
 // The first heads are loaded before the angles are computed, so that the chain
 // frequency -> turn -> sin, cos runs beside them.
-template <int DT, int NC, bool APPEND>
-__global__ void __launch_bounds__(kRotThreads, 3) rot_kernel(const RotArgs a, const int hg)
+template <int DT, int NC, int MODE>
+__global__ void __launch_bounds__(kRotThreads, MODE > 1 ? 2 : 3) rot_kernel(const RotArgs a, const int hg)
 {
+    constexpr bool APPEND = MODE > 0;
+    constexpr int CODE = MODE - 2;
     __shared__ unsigned long long s_step[kMaxPairs];
     __shared__ int s_axis[kMaxPairs];
     const int idx = blockIdx.x * kRotThreads + threadIdx.x;
@@ -167,6 +248,18 @@ __global__ void __launch_bounds__(kRotThreads, 3) rot_kernel(const RotArgs a, co
             } else {
                 if (!write_kv) continue;
                 const int kh = hh - a.Hq;
+                if constexpr (CODE >= 0) {
+                    const bool is_k = kh < a.Hk;
+                    const int vh = kh - a.Hk;
+                    float f0[8], f1[8];
+                    rotate8f<DT>(u0[i], u1[i], f0, f1, cs, sn, inter, is_k && turn0, is_k && turn1);
+                    uint8_t *to = is_k ? reinterpret_cast<uint8_t *>(a.ko) + page * a.ko_sb + kh * a.ko_sh + in_page * a.ko_sn
+                                       : reinterpret_cast<uint8_t *>(a.vo) + page * a.vo_sb + vh * a.vo_sh + in_page * a.vo_sn;
+                    float *sc = is_k ? a.ks + page * a.ks_sp + kh * a.ks_sh + in_page * a.ks_sn
+                                     : a.vs + page * a.vs_sp + vh * a.vs_sh + in_page * a.vs_sn;
+                    store_codes<CODE, NC>(f0, f1, to, e0, e1, sc);
+                    continue;
+                }
                 if (kh < a.Hk) {
                     dst = a.ko + page * a.ko_sb + kh * a.ko_sh + in_page * a.ko_sn;
                 } else {  // v is copied as it is
@@ -185,10 +278,14 @@ __global__ void __launch_bounds__(kRotThreads, 3) rot_kernel(const RotArgs a, co
 template <int DT, int NC>
 cudaError_t launch_rot_impl(const RotArgs &a, dim3 grid, int hg, cudaStream_t stream)
 {
-    if (a.slots)
-        rot_kernel<DT, NC, true><<<grid, kRotThreads, 0, stream>>>(a, hg);
+    if (!a.slots)
+        rot_kernel<DT, NC, 0><<<grid, kRotThreads, 0, stream>>>(a, hg);
+    else if (a.code < 0)
+        rot_kernel<DT, NC, 1><<<grid, kRotThreads, 0, stream>>>(a, hg);
+    else if (a.code == CLIS_CODE_INT8)
+        rot_kernel<DT, NC, 2><<<grid, kRotThreads, 0, stream>>>(a, hg);
     else
-        rot_kernel<DT, NC, false><<<grid, kRotThreads, 0, stream>>>(a, hg);
+        rot_kernel<DT, NC, 3><<<grid, kRotThreads, 0, stream>>>(a, hg);
     return cudaGetLastError();
 }
 

@@ -626,6 +626,72 @@ CLIS_API clis_status_t clis_attn_fwd_paged(const clis_paged_t *desc, const void 
                                            const int32_t *kv_len, void *o, float *lse2, int64_t max_q, float scale_log2,
                                            int causal, void *workspace, size_t ws_bytes, clis_stream_t stream);
 
+/* The same cache in 8 bits.  A row (one token and key/value head of K or of V) is d
+ * codes of one byte and one fp32 scale; its values are code * scale.  The codes lie in
+ * k_codes, v_codes [num_pages, Hkv, page_size, d] with the strides kc_s*, vc_s* of
+ * clis_paged_t (here bytes, multiples of 16), the scales in k_scale, v_scale [num_pages,
+ * Hkv, page_size] with strides of their own.  dtype is that of q, k, v and outputs.
+ * Scales are zero or positive. */
+typedef enum { CLIS_CODE_INT8 = 0, CLIS_CODE_E4M3 = 1 } clis_code_t;
+
+typedef struct {
+    int64_t code;                 /* clis_code_t */
+    int64_t ks_sp, ks_sh, ks_sn;  /* strides of k_scale: page, head, row (any, >= 0) */
+    int64_t vs_sp, vs_sh, vs_sn;
+} clis_quant_t;
+
+/* clis_paged_append into a cache of codes.  k is rotated in fp32 and not rounded
+ * before it is quantised.  Each row's scale is its largest magnitude over 127 (int8) or
+ * 448 (E4M3), and a value's code the nearest one to value / scale (ties to even), so a
+ * value is off by at most half a step: scale / 2 in int8; in E4M3 2^-4 of the value, or
+ * scale * 2^-10 below scale * 2^-6.  A row below 2^-100 becomes zeros; one that holds a value that
+ * is not finite gets the scale NaN and reads back as NaN throughout.  Other arguments
+ * and errors as for clis_paged_append; rows of scales must not overlap. */
+CLIS_API clis_status_t clis_paged_append_q8(const clis_paged_t *desc, const clis_quant_t *quant, const clis_rope_t *rope,
+                                            const void *q, const void *k, const void *v, int64_t v_st, int64_t v_sh,
+                                            void *q_out, void *k_codes, void *v_codes, float *k_scale, float *v_scale,
+                                            const int64_t *slots, const int32_t *positions, const double *inv_freq,
+                                            const int32_t *axis, clis_stream_t stream);
+
+/* Cached keys and values as 16-bit rows again: rows cu[s] .. cu[s + 1] - 1 of k_out and
+ * v_out are tokens start[s], start[s] + 1, ... of sequence s.
+ *   desc        S, T (rows of the outputs), Hkv, d, page_size, num_pages, width, kc_s*,
+ *               vc_s*, bt_ss, dtype; T up to 2^27
+ *   quant       NULL: a cache of 16-bit values, which are copied (scales may be NULL);
+ *               else codes: code * scale, rounded once
+ *   cu          device int32 [S + 1], from 0 on, not falling
+ *   start       device int32 [S], or NULL (0)
+ *   k_out, v_out  device [T, Hkv, d], strides k_st, k_sh, v_st, v_sh; must not overlap
+ *               the cache or each other
+ * Rows that belong to no sequence are left as they are.  Tokens outside of a
+ * block-table row (CLIS_PAGED_LENGTH_BIT) and those of pages out of range
+ * (CLIS_PAGED_INDEX_BIT) read as zeros.  One launch.  Errors as for clis_attn_fwd. */
+CLIS_API clis_status_t clis_paged_read(const clis_paged_t *desc, const clis_quant_t *quant, const void *k_cache,
+                                       const void *v_cache, const float *k_scale, const float *v_scale,
+                                       const int32_t *block_table, const int32_t *cu, const int32_t *start, void *k_out,
+                                       int64_t k_st, int64_t k_sh, void *v_out, int64_t v_st, int64_t v_sh,
+                                       clis_stream_t stream);
+
+/* clis_attn_fwd_paged over a cache of codes: x_ij = scale_log2 * q_i . k_j and o_i with the
+ * values code * scale.  Sequences of up to 64 query rows (n * H / Hkv; single tokens, or
+ * with max_q * H / Hkv <= 64 drafted ones) run a kernel bound by the codes' bytes: codes
+ * are exact in its products, the weights times V's scale are rounded to fp16 (off by up to 2^-11
+ * of each, at least 2^-32 of the row's largest), q is exact where it is within 2^-30 of its
+ * row's largest value.  Longer chunks are unpacked to 16 bits first (K's codes, exact, its scales
+ * applied to the scores; V's values, rounded once to the data type) and run the chunk kernel of
+ * clis_attn_fwd_paged; where max_q allows for them the workspace holds a 16-bit copy of
+ * the whole cache that is passed (one layer's).
+ * A NaN code of E4M3 stands for NaN.  Masked places, padding, reruns and errors as for
+ * clis_attn_fwd_paged. */
+CLIS_API clis_status_t clis_attn_paged_q8_workspace_size(const clis_paged_t *desc, const clis_quant_t *quant, int64_t max_q,
+                                                         size_t *bytes);
+CLIS_API clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_t *quant, const void *q,
+                                              const void *k_codes, const void *v_codes, const float *k_scale,
+                                              const float *v_scale, const int32_t *block_table, const int32_t *cu_q,
+                                              const int32_t *kv_len, void *o, float *lse2, int64_t max_q,
+                                              float scale_log2, int causal, void *workspace, size_t ws_bytes,
+                                              clis_stream_t stream);
+
 /* Static description of a status code (never NULL). */
 CLIS_API const char *clis_status_string(clis_status_t status);
 

@@ -1,0 +1,352 @@
+"""A paged cache held in 8 bits: the quantising write, reading back, and attention over the codes."""
+import math
+
+import pytest
+import torch
+
+from certified_fixed_stabilizer_gb300 import clis
+from q8_util import CODES, TOP, check_q8, make_q8, raw
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    clis.clis_clear_device_error()
+    yield
+    torch.cuda.synchronize()
+    assert clis.clis_get_device_error() == 0
+
+
+def attend(b, **kw):
+    return clis.attention_paged(b["q"], b["k_cache"], b["v_cache"], b["block_table"], b["cu_q"], b["kv_len"],
+                                kw.pop("max_q", b["max_q"]), k_scale=b["k_scale"], v_scale=b["v_scale"], **kw)
+
+
+# ------------------------------------------------------------------ attention
+
+SHAPES = [  # ctx, new, H, Hkv, d, page
+    ([0], [1], 1, 1, 128, 8),                                   # one key
+    ([300], [1], 32, 8, 128, 16),
+    ([31, 32, 33, 0, 95, 1000], [1] * 6, 8, 8, 128, 16),        # around a unit's 32 keys
+    ([63, 64, 65, 0, 127, 1000], [1] * 6, 8, 2, 64, 32),        # and 64 at d = 64
+    ([700, 0, 5, 2000], [1, 0, 1, 1], 12, 4, 64, 8),            # a sequence without a token
+    ([500, 3, 90], [5, 2, 0], 16, 4, 128, 64),                  # drafted tokens: 20 rows
+    ([500, 3, 90, 1500], [5, 1, 4, 5], 32, 4, 128, 16),         # 40 rows
+    ([77, 1200], [13, 16], 16, 4, 64, 128),                     # 64 rows
+    ([40, 0], [2, 3], 128, 8, 128, 8),                          # 16 heads a key: 48 rows
+    ([10], [1], 128, 1, 64, 16),                                # 128 query heads a key: the chunk kernel
+    ([200, 0, 33], [70, 129, 1], 8, 2, 128, 16),                # chunks and a single token
+    ([200, 5, 300, 17], [17, 300, 1, 2], 4, 4, 64, 8),
+    ([4000], [9], 40, 8, 128, 256),
+]
+
+
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+@pytest.mark.parametrize("dtype,code", [(BF, "int8"), (HF, "int8"), (BF, "e4m3"), (HF, "e4m3")])
+def test_attention(shape, dtype, code):
+    ctx, new, H, Hkv, d, page = SHAPES[shape]
+    b = make_q8(ctx, new, H, Hkv, d, page, dtype, code, seed=shape, extra_rows=2, layout="hnd" if shape % 2 else "nhd")
+    causal = shape % 3 != 2
+    out = torch.full_like(b["q"], 7.0)
+    o, lse = attend(b, causal=causal, out=out, return_lse=True)
+    check_q8(o, lse, b, causal, what=f"{SHAPES[shape]}")
+    assert (o[sum(new):] == 7.0).all()  # rows of no sequence
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("new,H", [([1] * 9, 8), ([4, 1, 3, 2, 4, 1, 1, 4, 2], 16)])
+def test_many_lengths_and_joins(code, new, H):
+    ctx = [1, 5000, 17, 900, 0, 12000, 333, 64, 2047]
+    b = make_q8(ctx, new, H, 2, 128, 32, BF, code, seed=3)
+    o, lse = attend(b, return_lse=True)
+    check_q8(o, lse, b)
+    assert torch.equal(o, attend(b))  # reruns agree bit for bit
+
+
+def test_hundreds_of_sequences():
+    ctx = [(37 * i) % 211 for i in range(700)]
+    b = make_q8(ctx, [1] * 700, 8, 4, 64, 16, HF, "int8", seed=5)
+    check_q8(attend(b), None, b)
+
+
+@pytest.mark.parametrize("spread", [4.0, 12.0])
+@pytest.mark.parametrize("new", [[1, 1], [3, 2]])
+def test_scales_of_any_size(spread, new):
+    """V's scales span many powers of two (log2: 4 * 1.44 * 3 each way, or 50), K's are ordinary."""
+    b = make_q8([800, 50], new, 8, 2, 128, 16, BF, "int8", seed=7)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for s in range(2):
+        (kc, ks), (vc, vs) = b["keys"][s]
+        vs *= torch.exp(spread * torch.randn(vs.shape, generator=g, device="cuda"))
+        b["keys"][s] = [(kc, ks), (vc, vs)]
+        for i in range(vs.shape[0]):
+            b["v_scale"][b["block_table"][s, i // 16], :, i % 16] = vs[i]
+    check_q8(attend(b), None, b)
+
+
+def test_chunk_with_scales_of_zero_and_of_any_size():
+    """K's scales of 0, 2^-110, 2^-60 and 2^20 among a chunk's: scores of no and of great size."""
+    b = make_q8([300, 11], [70, 90], 4, 2, 64, 8, BF, "e4m3", seed=15)
+    (kc, ks), (vc, vs) = b["keys"][0]
+    for i, x in ((3, 0.0), (50, 2.0 ** -110), (120, 2.0 ** -60), (310, 0.0), (330, 2.0 ** -110)):
+        ks[i] = x
+        b["k_scale"][b["block_table"][0, i // 8], :, i % 8] = x
+    check_q8(attend(b), None, b)
+    b["k_scale"][b["block_table"][0, 4].long(), 1, 3] = 2.0 ** 20  # key 35 of the second head takes all or nothing
+    o = attend(b)
+    assert torch.isfinite(o).all()
+    sign = (b["q"][:70, 2:].double() @ kc[35, 1].float().double()) > 0
+    v = (vc[35, 1].float() * vs[35, 1]).to(BF)
+    # Weight 2^e of one key, e the rounding of its score (up to half a step of 2^28, not 0): rounded to bf16 for the
+    # product, not for the row sum, and the output is rounded: two half steps.
+    assert ((o[:70, 2:][sign].double() - v.double()).abs() <= 2.0 ** -7 * 1.01 * v.double().abs()).all()
+
+
+def test_zero_scales_and_rows():
+    b = make_q8([40, 3], [1, 1], 4, 2, 64, 16, BF, "int8", seed=8)
+    for t in (b["v_scale"], b["k_scale"]):
+        t[b["block_table"][1, 0]] = 0.0
+    for s in ("v_scale",):
+        b[s][b["block_table"][0, 0].long(), :, :5] = 0.0
+    o = attend(b)
+    assert (o[1] == 0).all() and torch.isfinite(o).all()
+    (kc, ks), (vc, vs) = b["keys"][0]
+    vs[:5] = 0.0
+    b["keys"] = b["keys"][:1]
+    b["ctx"], b["new"] = [40], [1]
+    check_q8(o, None, b)
+
+
+def test_no_keys():
+    b = make_q8([5, 6], [1, 2], 4, 2, 128, 16, BF, "e4m3", seed=9)
+    b["kv_len"].zero_()
+    o, lse = attend(b, return_lse=True)
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("what", ["k_scale", "v_scale", "v_inf", "k_code", "v_code"])
+@pytest.mark.parametrize("new,H", [(3, 4), (5, 16), (40, 4)])
+def test_non_finite_where_some_rows_do_not_see_it(code, what, new, H):
+    """The last new token's key is no number: earlier rows are as without it, the last row is NaN."""
+    if what.endswith("code") and code == "int8":
+        pytest.skip("int8 codes are numbers")
+    b = make_q8([61, 30], [new, new], H, 2, 64, 16, BF, code, seed=10)
+    want = attend(b)
+    at = 61 + new - 1
+    page, row = b["block_table"][0, at // 16].long(), at % 16
+    if what.endswith("scale"):
+        b[what][page, :, row] = math.nan
+    elif what == "v_inf":
+        b["v_scale"][page, :, row] = math.inf
+    else:
+        raw(b["k_cache" if what == "k_code" else "v_cache"])[page, :, row, ::3] = 127
+    got = attend(b)
+    assert torch.equal(got[:new - 1], want[:new - 1]) and torch.equal(got[new:], want[new:])
+    last = got[new - 1]
+    if what == "v_code":
+        assert torch.isnan(last[:, ::3]).all()
+        rest = torch.ones(64, dtype=torch.bool, device="cuda")
+        rest[::3] = False
+        assert torch.isfinite(last[:, rest]).all()
+    else:
+        assert not torch.isfinite(last).any()
+
+
+def test_strides_of_caches_scales_and_rows():
+    """Caches and scales that are parts of larger tensors, q and out with rows apart, one head of many."""
+    b = make_q8([100, 45], [2, 1], 8, 2, 128, 16, HF, "int8", seed=11)
+    big = lambda t: torch.zeros((t.shape[0], 3, *t.shape[1:]), dtype=t.dtype, device="cuda")  # noqa: E731
+    for n in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        w = big(raw(b[n]) if n.endswith("cache") else b[n])
+        w[:, 1] = raw(b[n]) if n.endswith("cache") else b[n]
+        b[n] = w[:, 1].view(b[n].dtype) if n.endswith("cache") else w[:, 1]
+    wide = torch.zeros((3, 8, 256), dtype=HF, device="cuda")
+    wide[..., :128] = b["q"]
+    b["q"] = wide[..., :128]
+    out = torch.zeros((3, 16, 128), dtype=HF, device="cuda")[:, ::2]
+    check_q8(attend(b, out=out), None, b)
+
+
+def test_large_queries():
+    """bf16 queries far outside of fp16's range, and rows with values 2^-20 of their largest."""
+    b = make_q8([90, 7], [1, 1], 4, 2, 128, 16, BF, "int8", seed=12)
+    b["q"] *= 2.0 ** 40
+    b["q"][:, :, 3] *= 2.0 ** -20
+    check_q8(attend(b, softmax_scale=2.0 ** -40 / math.sqrt(128)), None, b, scale=2.0 ** -40 / math.sqrt(128))
+    b["q"] *= 2.0 ** -100
+    check_q8(attend(b, softmax_scale=2.0 ** 60 / math.sqrt(128)), None, b, scale=2.0 ** 60 / math.sqrt(128))
+
+
+def test_bad_pages_and_lengths_are_recorded():
+    b = make_q8([40, 20], [1, 1], 4, 2, 64, 16, BF, "int8", seed=13)
+    b["block_table"][0, 1] = 1 << 29
+    o = attend(b)
+    torch.cuda.synchronize()
+    assert clis.clis_get_device_error() == clis.PAGED_INDEX_BIT and torch.isfinite(o).all()
+    clis.clis_clear_device_error()
+    b["kv_len"][1] = 1 << 20
+    attend(b)
+    assert clis.clis_get_device_error() & clis.PAGED_LENGTH_BIT
+    clis.clis_clear_device_error()
+    # more new tokens than max_q says
+    b = make_q8([40], [40], 4, 2, 64, 16, BF, "int8", seed=13)
+    attend(b, max_q=1)
+    assert clis.clis_get_device_error() == clis.PAGED_LENGTH_BIT
+    clis.clis_clear_device_error()
+
+
+def test_graph_replays_other_lengths():
+    b = make_q8([300, 40], [1, 1], 8, 2, 128, 16, BF, "int8", seed=14)
+    o = torch.empty_like(b["q"])
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    call = lambda: clis.clis_attn_fwd_paged(b["q"], b["k_cache"], b["v_cache"], b["block_table"], b["cu_q"], b["kv_len"], 1,  # noqa: E731
+                                            clis.scale_log2_for(128), out=o, workspace=ws, k_scale=b["k_scale"], v_scale=b["v_scale"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for cut in (0, 7, 33):
+        b["kv_len"].sub_(cut)
+        want = attend(b)
+        o.zero_()
+        graph.replay()
+        assert torch.equal(o, want)
+        b["kv_len"].add_(cut)
+
+
+# --------------------------------------------------------------- write, read
+
+
+def turned(x, pos, inv, axis, inter):
+    """x [T, H, d] rotated in 64 bits."""
+    P = inv.numel()
+    a = (pos.double()[:, axis.long()] * inv)[:, None]
+    c, s = a.cos(), a.sin()
+    x = x.double()
+    y = x.clone()
+    i0, i1 = (slice(0, 2 * P, 2), slice(1, 2 * P, 2)) if inter else (slice(0, P), slice(P, 2 * P))
+    y[..., i0] = x[..., i0] * c - x[..., i1] * s
+    y[..., i1] = x[..., i1] * c + x[..., i0] * s
+    return y
+
+
+def check_rows(got_codes, got_scale, x, code, turn):
+    """Codes and scales of rows x (64 bits).  The scale: the largest magnitude, 2^-24 of it (and of the rotation's
+    products, 2 * 2^-24, with sin and cos off by 2^-23) off, then one division: 2^-21 in all.  A value: half a step of its
+    code, and what the scale's error makes of it."""
+    top = x.abs().amax(-1)
+    want = torch.where(top < 2.0 ** -100, 0.0, top / TOP[code])
+    assert ((got_scale.double() - want).abs() <= 2.0 ** (-21 if turn else -23) * want).all()
+    v = got_codes.float().double()
+    assert (v.abs() <= TOP[code]).all()
+    unit = want[..., None]
+    half = 0.5 * unit if code == "int8" else torch.maximum(x.abs() * 2.0 ** -4, unit * 2.0 ** -10)
+    x = torch.where(unit > 0, x, 0.0)
+    assert ((v * got_scale.double()[..., None] - x).abs() <= half * (1 + 2.0 ** -16) + 2.0 ** -20 * unit * TOP[code]).all()
+
+
+@pytest.mark.parametrize("T,H,Hk,d,page,pairs,axes,inter", [
+    (1, 1, 1, 64, 8, 8, 1, False), (7, 16, 2, 64, 16, 32, 2, True), (65, 32, 8, 128, 16, 64, 3, True),
+    (130, 6, 3, 128, 64, 24, 4, False), (33, 5, 5, 64, 32, 0, 1, False), (2049, 8, 4, 128, 8, 64, 1, False)])
+@pytest.mark.parametrize("dtype,code", [(BF, "int8"), (HF, "int8"), (BF, "e4m3"), (HF, "e4m3")])
+def test_write(T, H, Hk, d, page, pairs, axes, inter, dtype, code):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    q, k, v = r(T, H, d), r(T, Hk, d), r(T, Hk, d)
+    k[..., 5] *= 30
+    k[0, 0] = 0.0
+    if T > 5:
+        v[3] *= 2.0 ** -14
+        v[4, -1] = 0.0
+    pages = -(-T // page) + 3
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:T].contiguous()
+    if T > 2:
+        slots[T // 2] = -1
+    kc, vc = (torch.full((pages, Hk, page, d), 5, dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((pages, Hk, page), -1.0, device="cuda") for _ in range(2))
+    inv = 10000.0 ** (-torch.arange(max(pairs, 1), dtype=torch.float64, device="cuda") / max(pairs, 1))
+    axis = (torch.arange(max(pairs, 1), device="cuda") % axes).int()
+    pos = torch.randint(0, 100000, (T, axes), generator=g, device="cuda", dtype=torch.int32)
+    kw = {"q": q, "positions": pos, "inv_freq": inv, "axis": axis, "interleaved": inter} if pairs else {}
+    got = clis.paged_append(k, v, kc.view(CODES[code]), vc.view(CODES[code]), slots, k_scale=ks, v_scale=vs, **kw)
+    if pairs:
+        want_q = clis.paged_append(k, v, *(torch.zeros((pages, Hk, page, d), dtype=dtype, device="cuda") for _ in range(2)), slots, **kw)
+        assert torch.equal(got, want_q)  # (as beside a cache of 16-bit values)
+    live = slots >= 0
+    at = slots[live]
+    for x, c, s, turn in ((turned(k, pos, inv, axis, inter) if pairs else k.double(), kc, ks, pairs > 0), (v.double(), vc, vs, False)):
+        check_rows(c[at // page, :, at % page].view(CODES[code]), s[at // page, :, at % page], x[live], code, turn)
+        rest = torch.ones((pages, page), dtype=torch.bool, device="cuda")
+        rest[at // page, at % page] = False
+        assert (c.transpose(1, 2)[rest] == 5).all() and (s.transpose(1, 2)[rest] == -1.0).all()
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_write_of_non_finite_rows(code):
+    k = torch.randn(6, 2, 64, device="cuda").to(BF)
+    v = k.clone()
+    k[1, 0, 7], k[2, 1, 63], v[3, 0, 0], v[4, 1, 30] = math.nan, math.inf, -math.inf, math.nan
+    k[5] = 2.0 ** -120
+    v[5] = 2.0 ** -99
+    kc, vc = (torch.full((1, 2, 8, 64), 9, dtype=torch.int8, device="cuda").view(CODES[code]) for _ in range(2))
+    ks, vs = (torch.zeros((1, 2, 8), device="cuda") for _ in range(2))
+    clis.paged_append(k, v, kc, vc, torch.arange(6, device="cuda"), k_scale=ks, v_scale=vs)
+    bt = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    k2, v2 = clis.paged_read(kc, vc, bt, cu, 6, k_scale=ks, v_scale=vs)
+    for x, y in ((k, k2), (v, v2)):
+        bad = ~torch.isfinite(x.float()).all(-1)
+        assert torch.isnan(y[bad]).all() and torch.isfinite(y[~bad]).all()
+    assert (k2[5] == 0).all() and (v2[5] == 2.0 ** -99).all()
+
+
+@pytest.mark.parametrize("S,ctx,Hk,d,page,dtype,code", [
+    (1, 1, 1, 64, 8, BF, "int8"), (3, 71, 4, 64, 16, HF, "e4m3"), (5, 1000, 3, 128, 32, BF, "e4m3"),
+    (40, 130, 8, 128, 16, HF, "int8"), (4, 300, 2, 128, 64, BF, ""), (2, 5000, 8, 64, 8, HF, "")])
+def test_read(S, ctx, Hk, d, page, dtype, code):
+    lens = [ctx - (i * 37) % ctx for i in range(S)]
+    lens[S // 2] = 0 if S > 2 else lens[S // 2]
+    b = make_q8(lens, [0] * S, Hk, Hk, d, page, dtype, code or "int8", seed=S, layout="nhd" if S % 2 else "hnd")
+    start = torch.tensor([n // 3 for n in lens], dtype=torch.int32, device="cuda")
+    cnt = [n - n // 3 for n in lens]
+    cu = torch.tensor([sum(cnt[:i]) for i in range(S + 1)], dtype=torch.int32, device="cuda")
+    T = sum(cnt)
+    if code:
+        k, v = clis.paged_read(b["k_cache"], b["v_cache"], b["block_table"], cu, T, start=start, k_scale=b["k_scale"],
+                               v_scale=b["v_scale"], dtype=dtype)
+        want = [torch.cat([(c.float() * x[..., None]).to(dtype)[n // 3:] for (c, x), n in zip(w, lens)])
+                for w in zip(*b["keys"])]
+    else:
+        kc, vc = (torch.randn(b["k_cache"].shape, device="cuda").to(dtype) for _ in range(2))
+        k, v = clis.paged_read(kc, vc, b["block_table"], cu, T, start=start)
+        seq = torch.repeat_interleave(torch.arange(S, device="cuda"), torch.tensor(cnt, device="cuda"))
+        at = start.long()[seq] + torch.arange(T, device="cuda") - cu.long()[seq]
+        pg = b["block_table"].long()[seq, at // page]
+        want = [kc[pg, :, at % page], vc[pg, :, at % page]]
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+def test_read_leaves_other_rows_and_records_bad_places():
+    b = make_q8([20, 9], [0, 0], 2, 2, 64, 8, BF, "int8", seed=1)
+    cu = torch.tensor([0, 20, 29], dtype=torch.int32, device="cuda")
+    ko, vo = (torch.full((33, 4, 64), 3.0, dtype=BF, device="cuda")[:, ::2] for _ in range(2))
+    kw = {"k_scale": b["k_scale"], "v_scale": b["v_scale"]}
+    k, v = clis.paged_read(b["k_cache"], b["v_cache"], b["block_table"], cu, 33, k_out=ko, v_out=vo, **kw)
+    assert k is ko and (ko[29:] == 3.0).all() and (ko[:29] != 3.0).any()
+    b["block_table"][0, 1] = -5
+    k2, _ = clis.paged_read(b["k_cache"], b["v_cache"], b["block_table"], cu, 29, **kw)
+    assert clis.clis_get_device_error() == clis.PAGED_INDEX_BIT
+    assert (k2[8:16] == 0).all() and torch.equal(k2[:8], ko[:8]) and torch.equal(k2[16:], ko[16:29])
+    clis.clis_clear_device_error()
+    start = torch.tensor([0, 1 << 30], dtype=torch.int32, device="cuda")
+    b["block_table"][0, 1] = 0
+    k3, _ = clis.paged_read(b["k_cache"], b["v_cache"], b["block_table"], cu, 29, start=start, **kw)
+    assert clis.clis_get_device_error() == clis.PAGED_LENGTH_BIT and (k3[20:] == 0).all()
+    clis.clis_clear_device_error()
