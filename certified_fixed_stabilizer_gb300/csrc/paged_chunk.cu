@@ -55,9 +55,7 @@
 // registers that the softmax warps spill at d = 128) has not been taken apart.
 //
 // Over a cache of 8-bit codes (KS) K's pages hold the codes themselves, exact in 16 bits,
-// and a key's scale multiplies its scores: in the weights' multiply-add scale_log2
-// becomes a factor per key, and the maximum costs a multiplication per score, off the
-// chain.  (With the values rounded to bf16 first, the outputs of 2,048 tokens behind 30,011
+// and a key's scale multiplies its scores as they come from TMEM.  (With the values rounded to bf16 first, the outputs of 2,048 tokens behind 30,011
 // were off by 4.4e-3, rounding the keys alone 3.6e-3.)  The K/V producer brings the scales
 // into a ring of kScaleTiles tiles of shared memory.  K of tile n is loaded when the scores of
 // tile n - NSTAGE / 2 have been computed, so both softmax groups are done with tile n - 3 -
@@ -352,7 +350,7 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
         const ChunkItem &T = K.t;
         // Scales of the lane's four keys of key tile kt (a page holds at least eight): their
         // page two tiles ahead, themselves one.  Keys behind the last, and those of pages
-        // out of range, get a scale all the same: -inf times it is -inf.
+        // out of range, get the scale 1.
         auto scale_page = [&](int kt) -> int {
             const int key = kt * BN + lane * 4;
             return key < T.kv && kt < K.start + K.n ? __ldg(a.block_table + T.s * a.bt_s + (key >> a.page_shift)) : -1;
@@ -398,9 +396,7 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
             const uint32_t bar = smem_u32(&c.kv_full[gq % C::NSTAGE]);
             if constexpr (KS) {
                 if (has_k) {  // (before the arrival on the group's barrier)
-                    const float lo = 1.17549435e-38f, sl2 = a.scale_log2;
-                    *reinterpret_cast<float4 *>(scales + (kt_all % kScaleTiles) * BN + lane * 4) =
-                        make_float4(fmaxf(sc.x * sl2, lo), fmaxf(sc.y * sl2, lo), fmaxf(sc.z * sl2, lo), fmaxf(sc.w * sl2, lo));
+                    *reinterpret_cast<float4 *>(scales + (kt_all % kScaleTiles) * BN + lane * 4) = sc;
                     ++kt_all;
                     sc = scale_of(K.start + gi + 1, sc_page);
                     sc_page = scale_page(K.start + gi + 2);
@@ -696,23 +692,16 @@ abort:
 // Weights of a row's 128 scores for a shift, p = 2^(scale_log2 s - shift), packed in
 // pairs over the first 64 columns of the scores, all of which have been read;
 // returns their sum (before rounding).
-// KS: scale_log2 times the key's scale is read from ks.
-template <int DT, bool KS>
-__device__ __forceinline__ float weights128(const uint32_t *s, float sl2, const float *ks, float nshift, uint32_t tP)
+template <int DT>
+__device__ __forceinline__ float weights128(const uint32_t *s, float sl2, float nshift, uint32_t tP)
 {
-    float2 sc2 = make_float2(sl2, sl2);
-    const float2 sh2 = make_float2(nshift, nshift);
-    float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float2 sc2 = make_float2(sl2, sl2), sh2 = make_float2(nshift, nshift);
     float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c32 = 0; c32 < BN / 32; c32++) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; e++) {
-            if constexpr (KS) {
-                if (e % 2 == 0) k4 = *reinterpret_cast<const float4 *>(ks + c32 * 32 + 2 * e);
-                sc2 = e % 2 == 0 ? make_float2(k4.x, k4.y) : make_float2(k4.z, k4.w);
-            }
             const float2 x = ffma2(
                 make_float2(__uint_as_float(s[c32 * 32 + 2 * e]), __uint_as_float(s[c32 * 32 + 2 * e + 1])), sc2, sh2);
             const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
@@ -764,25 +753,34 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, const 
             tmem_ld32(tS + 96, s + 96);
             tmem_wait_ld();
             const int key0 = (K.start + j) * BN;
+            if constexpr (KS) {
+                const float4 *ks = reinterpret_cast<const float4 *>(scales + ((kt_all + j) % kScaleTiles) * BN);
+#pragma unroll
+                for (int cc = 0; cc < BN; cc += 4) {
+                    const float4 k4 = ks[cc / 4];
+                    const float2 x = fmul2(make_float2(__uint_as_float(s[cc]), __uint_as_float(s[cc + 1])), make_float2(k4.x, k4.y));
+                    const float2 y = fmul2(make_float2(__uint_as_float(s[cc + 2]), __uint_as_float(s[cc + 3])), make_float2(k4.z, k4.w));
+                    s[cc] = __float_as_uint(x.x);
+                    s[cc + 1] = __float_as_uint(x.y);
+                    s[cc + 2] = __float_as_uint(y.x);
+                    s[cc + 3] = __float_as_uint(y.y);
+                }
+            }
             if (key0 + BN > lim) {
 #pragma unroll
                 for (int cc = 0; cc < BN; cc++)
                     if (key0 + cc >= lim) s[cc] = 0xFF800000u;  // -inf
             }
-            const float *ks = scales + ((kt_all + j) % kScaleTiles) * BN;
             float l = 0.f;
-            if (begun) l = weights128<DT, KS>(s, sl2, ks, (m_run == -INFINITY) ? 0.f : -m_run, tS);
+            if (begun) l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int cc = 0; cc < BN; cc += 8) {
 #pragma unroll
-                for (int q4 = 0; q4 < 4; q4++) {
-                    float2 x = make_float2(__uint_as_float(s[cc + 2 * q4]), __uint_as_float(s[cc + 2 * q4 + 1]));
-                    if constexpr (KS) x = fmul2(x, *reinterpret_cast<const float2 *>(ks + cc + 2 * q4));
-                    mx[q4] = fmax3(mx[q4], x.x, x.y);
-                }
+                for (int q4 = 0; q4 < 4; q4++)
+                    mx[q4] = fmax3(mx[q4], __uint_as_float(s[cc + 2 * q4]), __uint_as_float(s[cc + 2 * q4 + 1]));
             }
-            const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (KS ? 1.f : sl2);
+            const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
             const bool grow = m_tile > m_run + (kTau + weight_room(DT));  // always true where a row's first visible key is
             if (__any_sync(0xFFFFFFFFu, grow) || !begun) {
                 // Raise the shift, compute the tile's weights (again), and shrink O once the
@@ -793,7 +791,7 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, const 
                 l_run *= alpha;
                 // (stores to TMEM are asynchronous: the weights that these replace must be in place)
                 if (begun) tmem_wait_st();
-                l = weights128<DT, KS>(s, sl2, ks, (m_run == -INFINITY) ? 0.f : -m_run, tS);
+                l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
                 if (begun) {
                     if (!mbar_wait(smem_u32(&c.pv_done[t]), (g - 1) & 1, ab, err, kErrSoftmax)) return;
                     tc_fence_after();

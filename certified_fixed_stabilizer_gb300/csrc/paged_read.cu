@@ -240,9 +240,8 @@ __global__ void __launch_bounds__(kReadThreads) paged_unpack_kernel(const Unpack
 #pragma unroll
             for (int b = 0; b < kBatch; b++) {
                 if (to[b] < 0) continue;
-                const bool plain = k[b].scale >= 7.888609052210118e-31f && k[b].scale <= 1.2676506002282294e30f;  // 2^-100, 2^100
-                if ((to[b] & (a.d - 1)) == 0) p.ks[to[b] / a.d] = plain ? k[b].scale : 1.f;
-                if (plain) k[b].scale = 1.f;  // (the codes as they are)
+                if ((to[b] & (a.d - 1)) == 0) p.ks[to[b] / a.d] = k[b].scale;
+                k[b].scale = 1.f;  // (the codes as they are)
                 store_piece<CODE, DT>(k[b], p.ko + to[b]);
                 store_piece<CODE, DT>(v[b], p.vo + to[b]);
             }
