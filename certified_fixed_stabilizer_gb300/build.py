@@ -22,7 +22,8 @@ TORCH_EXT = os.path.join(OUT_DIR, "_clis_torch.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["clis_api.cu", "certify.cu", "attn_fwd.cu", "attn_bwd.cu", "host_attention.cu", "rope.cu",
-           "paged_plan.cu", "paged_decode.cu", "paged_q8.cu", "paged_read.cu", "paged_chunk.cu", "paged_api.cu"]
+           "paged_plan.cu", "paged_decode.cu", "paged_q8.cu", "paged_read.cu", "paged_chunk.cu", "paged_api.cu",
+           "beam.cu", "reorder.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-fvisibility=hidden"]

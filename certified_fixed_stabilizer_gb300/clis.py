@@ -158,6 +158,14 @@ def load_library():
     lib.clis_attn_paged_workspace_size.restype = i32
     lib.clis_attn_fwd_paged.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, i64, f32, i32, vp, sz, vp]
     lib.clis_attn_fwd_paged.restype = i32
+    lib.clis_beam_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    lib.clis_beam_workspace_size.restype = i32
+    lib.clis_beam_select.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.clis_beam_select.restype = i32
+    lib.clis_paged_reorder_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    lib.clis_paged_reorder_workspace_size.restype = i32
+    lib.clis_paged_reorder.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]
+    lib.clis_paged_reorder.restype = i32
     zp = ctypes.POINTER(QuantDesc)
     lib.clis_paged_append_q8.argtypes = [pp, zp, rp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.clis_paged_append_q8.restype = i32
@@ -936,6 +944,61 @@ def clis_paged_read(k_cache, v_cache, block_table, cu, num_tokens: int, start=No
 paged_read = clis_paged_read
 
 
+# -------------------------------------------------------------- beam search
+
+
+class BeamChoice(NamedTuple):
+    """The best continuations of each request, best first: ``scores`` float32 [R, K], the
+    beam that each goes on from (``parent`` int32 [R, K], -1: none left) and its ``token`` int32."""
+    scores: torch.Tensor
+    parent: torch.Tensor
+    token: torch.Tensor
+
+
+def clis_beam_select(logits, scores, num: int, workspace=None, stream=None) -> BeamChoice:
+    """Of each request's continuations (beam w, token v) the ``num`` best by scores[r, w] +
+    log_softmax(logits[r, w])[v]; ties go to the lowest w * V + v.  logits [R, W, V] in bfloat16,
+    float16 or float32 (any row strides), scores float32 [R, W] (-inf: a beam not in use; -inf
+    logits: masked tokens).  At most 64 beams and 64 continuations.  With beams that end at a
+    token, ask for twice as many as go on.  Where fewer are left, scores are -inf, parent and
+    token -1."""
+    return BeamChoice(*_native.beam_select(logits, scores, num, workspace, _raw(stream)))
+
+
+def beam_select(logits, scores, num: int | None = None) -> BeamChoice:
+    """:func:`clis_beam_select`; ``num``: default the number of beams."""
+    return clis_beam_select(logits, scores, logits.shape[1] if num is None else num)
+
+
+class Reordered(NamedTuple):
+    """What :func:`paged_reorder` returns: the new ``block_table``, ``lens`` int32 [S], ``ring_state``
+    int64 [2] and ``done`` int32 [requests] (0: the request stayed as it was)."""
+    block_table: torch.Tensor
+    lens: torch.Tensor
+    ring_state: torch.Tensor
+    done: torch.Tensor
+
+
+def clis_paged_reorder(lens, parent, block_table, ring, ring_state, caches=(), scales=(), page_size: int | None = None, out=None,
+                       workspace=None, stream=None) -> Reordered:
+    """The beams' block-table rows after a selection: row r * W + w (of parent [R, W]) goes on
+    from row r * W + parent[r, w], or ends where that is negative.  Rows share their full
+    pages; a partly filled last page that several rows go on from is copied into pages of
+    the ring for all but the first.  Pages that no row of a request names any more go back to
+    the ring (written in place; ring_state is not changed).  caches: tensors [layers, pages,
+    H_kv, page_size, d] (or without layers) whose rows are copied, scales: [layers, pages, H_kv, page_size].
+    out: the new table (default: a new tensor; may be block_table itself).  page_size is needed
+    without caches.  A request that the ring has too few pages for stays as it was
+    (PAGED_POOL_BIT in the device error word, ``done`` 0): call again when there are pages."""
+    if page_size is None and not len(caches) and not len(scales):
+        raise ValueError("page_size is needed without caches")
+    return Reordered(*_native.paged_reorder(lens, parent, block_table, ring, ring_state, caches, scales, page_size or 0, out,
+                                            workspace, _raw(stream)))
+
+
+paged_reorder = clis_paged_reorder
+
+
 class PagedCache:
     """Paged key/value cache of a model's layers with its block tables and its ring
     of free pages, all on the device: a step is :meth:`begin` with the new tokens
@@ -946,6 +1009,11 @@ class PagedCache:
         plan = cache.begin(new_len, num_tokens)          # int32 [max_seqs], rows of the packed batch
         for i in range(2):
             o = cache.attend(i, q[i], k[i], v[i], plan, max_q, rope=(inv_freq, axis, False))
+
+    With ``dtype`` int8 or float8_e4m3fn the keys and values are held as codes with a scale
+    per token and head (``k_scale``, ``v_scale`` [layers, pages, H_kv, page_size]); q, k and v stay
+    bfloat16 or float16.  :meth:`read` gives cached tokens back, :meth:`reorder` moves the
+    states of a beam search.
     """
 
     def __init__(self, layers: int, num_pages: int, num_kv_heads: int, d: int, max_seqs: int, max_len: int,
@@ -955,11 +1023,17 @@ class PagedCache:
             dev = torch.device("cuda", torch.cuda.current_device())
         shape = (layers, num_pages, num_kv_heads, page_size, d)
         self.k, self.v = (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
+        self.k_scale = self.v_scale = None
+        if dtype in (torch.int8, torch.float8_e4m3fn):
+            self.k_scale, self.v_scale = (torch.empty(shape[:-1], dtype=torch.float32, device=dev) for _ in range(2))
         self.page_size = page_size
         self.block_table = torch.full((max_seqs, -(-max_len // page_size)), -1, dtype=torch.int32, device=dev)
         self.ring = torch.arange(num_pages, dtype=torch.int32, device=dev)
         self.ring_state = torch.tensor([0, num_pages], dtype=torch.int64, device=dev)
         self.lens = torch.zeros(max_seqs, dtype=torch.int32, device=dev)
+
+    def _scales(self, layer: int) -> dict:
+        return {} if self.k_scale is None else {"k_scale": self.k_scale[layer], "v_scale": self.v_scale[layer]}
 
     def begin(self, new_len, num_tokens: int) -> PagedPlan:
         """Plan of a step that adds new_len[s] tokens to sequence s (0: not part of
@@ -981,13 +1055,31 @@ class PagedCache:
         the attention of q [T, H, d] over it.  ``max_q``: as for :func:`attention_paged`
         (give it).  ``rope``: (inv_freq, axis, interleaved) rotates q and k by ``positions``
         (int32 [T, axes], default the tokens' places in their sequences)."""
-        kc, vc = self.k[layer], self.v[layer]
+        kc, vc, sc = self.k[layer], self.v[layer], self._scales(layer)
         if rope is not None:
             q = clis_paged_append(k, v, kc, vc, plan.slots, q=q, positions=plan.positions if positions is None else positions,
-                                  inv_freq=rope[0], axis=rope[1], interleaved=rope[2] if len(rope) > 2 else False)
+                                  inv_freq=rope[0], axis=rope[1], interleaved=rope[2] if len(rope) > 2 else False, **sc)
         else:
-            clis_paged_append(k, v, kc, vc, plan.slots)
-        return attention_paged(q, kc, vc, self.block_table, plan.cu_q, plan.kv_len, max_q, softmax_scale, causal, out)
+            clis_paged_append(k, v, kc, vc, plan.slots, **sc)
+        return attention_paged(q, kc, vc, self.block_table, plan.cu_q, plan.kv_len, max_q, softmax_scale, causal, out, **sc)
+
+    def read(self, layer: int, cu, num_tokens: int, start=None, dtype=torch.bfloat16):
+        """Cached tokens of ``layer`` as rows (k, v) [num_tokens, H_kv, d]; see :func:`paged_read`."""
+        return clis_paged_read(self.k[layer], self.v[layer], self.block_table, cu, num_tokens, start=start, dtype=dtype,
+                               **self._scales(layer))
+
+    def reorder(self, parent) -> torch.Tensor:
+        """The beams' states after a selection (parent int32 [requests, beams], requests * beams =
+        max_seqs: row r * beams + w goes on from row r * beams + parent[r, w], or ends where that is
+        negative); see :func:`paged_reorder`.  Returns ``done`` int32 [requests].  Rows of beams are ended
+        here, not by a negative new_len of :meth:`begin`, while they share pages; a prompt is read by
+        one beam (new_len 0 for the others), and parent 0 for all then starts the search."""
+        scales = [] if self.k_scale is None else [self.k_scale, self.v_scale]
+        r = clis_paged_reorder(self.lens, parent, self.block_table, self.ring, self.ring_state, [self.k, self.v], scales,
+                               out=self.block_table)
+        self.lens.copy_(r.lens)
+        self.ring_state.copy_(r.ring_state)
+        return r.done
 
 
 load_library()

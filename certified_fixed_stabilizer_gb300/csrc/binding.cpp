@@ -449,6 +449,114 @@ std::vector<Tensor> read(const Tensor &kc, const Tensor &vc, const Tensor &table
     return {*k_out, *v_out};
 }
 
+// --------------------------------------------------------------- beam search
+
+std::vector<Tensor> beam(const Tensor &logits, const Tensor &scores, int64_t K, std::optional<Tensor> workspace,
+                         std::optional<uintptr_t> raw)
+{
+    TORCH_CHECK_VALUE(logits.is_cuda() && logits.dim() == 3 && (elem(logits) || logits.scalar_type() == at::kFloat) &&
+                          (logits.size(2) < 2 || logits.stride(2) == 1),
+                      "logits must be a bfloat16, float16 or float32 device tensor [R, W, V] with a contiguous last dimension");
+    const at::Device dev = logits.device();
+    const int64_t R = logits.size(0), W = logits.size(1);
+    TORCH_CHECK_VALUE(R == 0 || (W > 0 && logits.size(2) > 0), "logits must have beams and tokens");
+    check_ints(scores, at::kFloat, {R, W}, dev, "scores");
+    TORCH_CHECK_VALUE(K > 0, "num must be positive");
+    Place at_(logits, raw);
+    Tensor best = at_.result(empty({R, K}, at::kFloat, dev)), parent = at_.result(empty({R, K}, at::kInt, dev)),
+           token = at_.result(empty({R, K}, at::kInt, dev));
+    if (R > 0) {
+        clis_beam_t d = {};
+        d.R = R, d.W = W, d.V = logits.size(2), d.K = K;
+        d.dtype = logits.scalar_type() == at::kFloat ? 2 : dtype_of(logits);
+        d.l_sr = R == 1 ? 0 : logits.stride(0), d.l_sw = W == 1 ? 0 : logits.stride(1);
+        size_t need = 0;
+        ok("clis_beam_workspace_size", clis_beam_workspace_size(&d, &need));
+        if (!workspace) workspace = empty({static_cast<int64_t>(need)}, at::kByte, dev);
+        TORCH_CHECK_VALUE(workspace->device() == dev && workspace->is_contiguous(),
+                          "the workspace must be contiguous and on the device of the logits");
+        ok("clis_beam_select",
+           clis_beam_select(&d, logits.data_ptr(), static_cast<const float *>(scores.data_ptr()), static_cast<float *>(best.data_ptr()),
+                            static_cast<int32_t *>(parent.data_ptr()), static_cast<int32_t *>(token.data_ptr()),
+                            workspace->data_ptr(), workspace->nbytes(), at_.stream));
+    }
+    return {best, parent, token};
+}
+
+// A cache tensor [layers, pages, H_kv, page_size, d], or scales without the last
+// dimension; both also without the first.
+clis_pages_t pages_desc(const Tensor &t, int64_t tail, int64_t pages, int64_t page_size, const at::Device &dev)
+{
+    const int64_t n = t.dim(), first = n - 3 - tail;
+    TORCH_CHECK_VALUE(t.device() == dev && (first == 0 || first == 1) && t.size(first) == pages && t.size(first + 2) == page_size &&
+                          (tail == 0 || t.stride(n - 1) == 1),
+                      "caches must be [layers, pages, H_kv, page_size, d] or [pages, H_kv, page_size, d], scales the same without "
+                      "d, all of one size of pages on the device of the block table");
+    const int64_t e = t.element_size();
+    auto step = [&](int64_t i) { return (t.size(i) == 1 ? (tail ? t.size(n - 1) : 1) : t.stride(i)) * e; };
+    clis_pages_t p = {};
+    p.base = t.data_ptr();
+    p.layers = first ? t.size(0) : 1;
+    p.heads = t.size(first + 1);
+    p.row_bytes = (tail ? t.size(n - 1) : 1) * e;
+    p.sl = first ? step(0) : 0;
+    p.sp = step(first), p.sh = step(first + 1), p.sn = step(first + 2);
+    return p;
+}
+
+std::vector<Tensor> reorder(const Tensor &lens, const Tensor &parent, const Tensor &table, const Tensor &ring,
+                            const Tensor &ring_state, const std::vector<Tensor> &caches, const std::vector<Tensor> &scales,
+                            int64_t page_size, std::optional<Tensor> out, std::optional<Tensor> workspace,
+                            std::optional<uintptr_t> raw)
+{
+    TORCH_CHECK_VALUE(parent.is_cuda() && parent.dim() == 2, "parent must be an int32 device tensor [requests, beams]");
+    const at::Device dev = parent.device();
+    const int64_t R = parent.size(0), W = parent.size(1), S = R * W;
+    TORCH_CHECK_VALUE(W > 0, "parent must have beams");
+    check_ints(parent, at::kInt, {R, W}, dev, "parent");
+    check_ints(lens, at::kInt, {S}, dev, "lens");
+    check_ints(ring_state, at::kLong, {2}, dev, "ring_state");
+    TORCH_CHECK_VALUE(ring.dim() == 1, "ring must be an int32 tensor [ring size]");
+    check_ints(ring, at::kInt, ring.sizes(), dev, "ring");
+    for (const Tensor *t : {&table, out ? &*out : &table})
+        TORCH_CHECK_VALUE(t->dim() == 2 && t->scalar_type() == at::kInt && t->device() == dev && t->size(0) == S &&
+                              t->size(1) == table.size(1) && t->stride(1) == 1,
+                          "block_table and out must be int32 [requests * beams, width] with contiguous rows on one device");
+    clis_reorder_t d = {};
+    d.groups = R, d.beams = W, d.width = table.size(1), d.num_pages = ring.size(0);
+    std::vector<clis_pages_t> tensors;
+    for (const auto *list : {&caches, &scales})
+        for (const Tensor &t : *list) {
+            const int64_t tail = list == &caches ? 1 : 0;
+            TORCH_CHECK_VALUE(t.dim() == 3 + tail || t.dim() == 4 + tail, list == &caches ? "a cache must have 4 or 5 dimensions"
+                                                                                         : "scales must have 3 or 4 dimensions");
+            if (tensors.empty()) {
+                d.num_pages = t.size(t.dim() - 3 - tail);
+                page_size = t.size(t.dim() - 1 - tail);
+            }
+            tensors.push_back(pages_desc(t, tail, d.num_pages, page_size, dev));
+        }
+    d.page_size = page_size;
+    d.bt_ss = S > 1 ? table.stride(0) : table.size(1);
+    Place at_(parent, raw);
+    if (!out) out = at_.result(empty(table.sizes(), at::kInt, dev));
+    d.bo_ss = S > 1 ? out->stride(0) : out->size(1);
+    Tensor lens_out = at_.result(empty({S}, at::kInt, dev)), state = at_.result(empty({2}, at::kLong, dev)),
+           done = at_.result(empty({R}, at::kInt, dev));
+    size_t need = 0;
+    ok("clis_paged_reorder_workspace_size", clis_paged_reorder_workspace_size(&d, &need));
+    if (!workspace) workspace = empty({static_cast<int64_t>(need)}, at::kByte, dev);
+    TORCH_CHECK_VALUE(workspace->device() == dev && workspace->is_contiguous(),
+                      "the workspace must be contiguous and on the device of parent");
+    auto i32 = [](const Tensor &t) { return static_cast<int32_t *>(t.data_ptr()); };
+    auto i64 = [](const Tensor &t) { return static_cast<int64_t *>(t.data_ptr()); };
+    ok("clis_paged_reorder",
+       clis_paged_reorder(&d, i32(lens), i32(parent), i32(table), i32(*out), i32(ring), ring.size(0), i64(ring_state), i64(state),
+                          i32(lens_out), i32(done), tensors.data(), static_cast<int64_t>(tensors.size()), workspace->data_ptr(),
+                          workspace->nbytes(), at_.stream));
+    return {*out, lens_out, state, done};
+}
+
 // -------------------------------------------------------------- Python objects
 
 Tensor tensor(PyObject *o, const char *name)
@@ -597,6 +705,40 @@ PyObject *py_read(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+std::vector<Tensor> tensors(PyObject *o, const char *name)
+{
+    std::vector<Tensor> v;
+    PyObject *seq = PySequence_Fast(o, name);
+    if (!seq) throw python_error();
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+    for (Py_ssize_t i = 0; i < n; i++) {
+        PyObject *x = PySequence_Fast_GET_ITEM(seq, i);
+        if (!THPVariable_Check(x)) {
+            Py_DECREF(seq);
+            TORCH_CHECK_TYPE(false, name, " must hold tensors");
+        }
+        v.push_back(THPVariable_Unpack(x));
+    }
+    Py_DECREF(seq);
+    return v;
+}
+
+PyObject *py_beam(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return call(n, 5, [&] {
+        return wrap(beam(tensor(a[0], "logits"), tensor(a[1], "scores"), integer(a[2]), maybe(a[3], "workspace"), stream_of(a[4])));
+    });
+}
+
+PyObject *py_reorder(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return call(n, 11, [&] {
+        return wrap(reorder(tensor(a[0], "lens"), tensor(a[1], "parent"), tensor(a[2], "block_table"), tensor(a[3], "ring"),
+                            tensor(a[4], "ring_state"), tensors(a[5], "caches"), tensors(a[6], "scales"), integer(a[7]),
+                            maybe(a[8], "out"), maybe(a[9], "workspace"), stream_of(a[10])));
+    });
+}
+
 PyObject *py_set_error_class(PyObject *, PyObject *c)
 {
     Py_INCREF(c);
@@ -612,6 +754,8 @@ PyMethodDef g_methods[] = {
     {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_append)), METH_FASTCALL, nullptr},
     {"attention_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_attention)), METH_FASTCALL, nullptr},
     {"paged_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_read)), METH_FASTCALL, nullptr},
+    {"beam_select", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_beam)), METH_FASTCALL, nullptr},
+    {"paged_reorder", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(py_reorder)), METH_FASTCALL, nullptr},
     {"set_error_class", py_set_error_class, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

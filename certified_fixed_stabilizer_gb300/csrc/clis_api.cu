@@ -567,12 +567,13 @@ clis_status_t clis_get_device_error(uint32_t *code)
     clis_status_t st = clis::read_device_error(&fwd);
     if (st == CLIS_ERR_CUDA) return st;
     if (clis::read_bwd_error(&bwd) != CLIS_OK) return CLIS_ERR_CUDA;
-    uint32_t rot = 0, plan = 0, dec = 0, chunk = 0, q8 = 0, read = 0;
+    uint32_t rot = 0, plan = 0, dec = 0, chunk = 0, q8 = 0, read = 0, reorder = 0;
     if (clis::read_rot_error(&rot) != CLIS_OK || clis::read_plan_error(&plan) != CLIS_OK ||
         clis::read_decode_error(&dec) != CLIS_OK || clis::read_chunk_error(&chunk) != CLIS_OK ||
-        clis::read_q8_error(&q8) != CLIS_OK || clis::read_read_error(&read) != CLIS_OK)
+        clis::read_q8_error(&q8) != CLIS_OK || clis::read_read_error(&read) != CLIS_OK ||
+        clis::read_reorder_error(&reorder) != CLIS_OK)
         return CLIS_ERR_CUDA;
-    *code = fwd | bwd | rot | plan | dec | chunk | q8 | read;
+    *code = fwd | bwd | rot | plan | dec | chunk | q8 | read | reorder;
     if (*code & ~(CLIS_PAGED_INDEX_BIT | CLIS_PAGED_POOL_BIT | CLIS_PAGED_LENGTH_BIT)) return CLIS_ERR_TIMEOUT;
     return *code ? CLIS_ERR_DATA : CLIS_OK;
 }
@@ -586,6 +587,7 @@ clis_status_t clis_clear_device_error(void)
     if (st == CLIS_OK) st = clis::clear_decode_error();
     if (st == CLIS_OK) st = clis::clear_q8_error();
     if (st == CLIS_OK) st = clis::clear_read_error();
+    if (st == CLIS_OK) st = clis::clear_reorder_error();
     return st != CLIS_OK ? st : clis::clear_chunk_error();
 }
 

@@ -365,6 +365,43 @@ clis_status_t append(const clis_paged_t *desc, const clis_quant_t *quant, const 
     return clis::launch_rot(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+clis_status_t check_beam(const clis_beam_t *b, clis::BeamArgs *a)
+{
+    if (b->R < 0 || b->W < 1 || b->V < 1 || b->K < 1 || b->l_sr < 0 || b->l_sw < 0) return CLIS_ERR_INVALID_ARG;
+    if (b->dtype < 0 || b->dtype > 2) return CLIS_ERR_INVALID_ARG;
+    if (b->W > clis::kMaxBeams || b->K > clis::kMaxPicks || b->R > 65535 || b->R * b->W > 65535 || b->V > INT32_MAX ||
+        b->W * b->V > INT32_MAX || b->l_sr >= (int64_t(1) << 38) || b->l_sw >= (int64_t(1) << 38))
+        return CLIS_ERR_UNSUPPORTED;
+    *a = clis::BeamArgs{};
+    a->R = static_cast<int>(b->R);
+    a->W = static_cast<int>(b->W);
+    a->V = static_cast<int>(b->V);
+    a->K = static_cast<int>(b->K);
+    a->dtype = static_cast<int>(b->dtype);
+    a->l_sr = b->l_sr;
+    a->l_sw = b->l_sw;
+    return clis::beam_fits(*a) ? CLIS_OK : CLIS_ERR_UNSUPPORTED;
+}
+
+clis_status_t check_reorder(const clis_reorder_t *r, clis::ReorderArgs *a)
+{
+    if (r->groups < 0 || r->beams < 1 || r->width < 1 || r->num_pages < 1 || r->bt_ss < 0 || r->bo_ss < 0 || r->page_size < 1)
+        return CLIS_ERR_INVALID_ARG;
+    if (page_shift(r->page_size) < 0 || r->beams > clis::kMaxBeams || r->groups > kMaxSeqs || r->groups * r->beams > kMaxSeqs ||
+        r->num_pages > kMaxN || r->width > kMaxKeys / r->page_size || r->bt_ss >= (int64_t(1) << 38) || r->bo_ss >= (int64_t(1) << 38))
+        return CLIS_ERR_UNSUPPORTED;
+    if (r->groups * r->beams > 1 && r->bo_ss < r->width) return CLIS_ERR_INVALID_ARG;  // rows are written
+    *a = clis::ReorderArgs{};
+    a->R = static_cast<int>(r->groups);
+    a->W = static_cast<int>(r->beams);
+    a->width = static_cast<int>(r->width);
+    a->page_shift = page_shift(r->page_size);
+    a->num_pages = r->num_pages;
+    a->bt_s = r->bt_ss;
+    a->bo_s = r->bo_ss;
+    return CLIS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -631,6 +668,106 @@ clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_
     if (e == CLIS_OK && s.row_tiles > 0) e = clis::launch_paged_q8(a, z, s.row_tiles, false, true, w, nsm, cs);
     if (e == CLIS_OK) e = clis::launch_paged_chunk(b, rows_small, w + few, nsm, cs);
     return e;
+}
+
+clis_status_t clis_beam_workspace_size(const clis_beam_t *desc, size_t *bytes)
+{
+    if (!desc || !bytes) return CLIS_ERR_INVALID_ARG;
+    clis::BeamArgs a;
+    const clis_status_t st = check_beam(desc, &a);
+    if (st != CLIS_OK) return st;
+    *bytes = 0;
+    if (a.R == 0) return CLIS_OK;
+    int nsm = 0;
+    if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
+    *bytes = clis::beam_workspace(a, nsm);
+    return CLIS_OK;
+}
+
+clis_status_t clis_beam_select(const clis_beam_t *desc, const void *logits, const float *scores, float *out_scores,
+                               int32_t *parent, int32_t *token, void *workspace, size_t ws_bytes, clis_stream_t stream)
+{
+    if (!desc) return CLIS_ERR_INVALID_ARG;
+    clis::BeamArgs a;
+    const clis_status_t st = check_beam(desc, &a);
+    if (st != CLIS_OK) return st;
+    if (a.R == 0) return CLIS_OK;
+    if (!logits || !scores || !out_scores || !parent || !token) return CLIS_ERR_INVALID_ARG;
+    if (!aligned(logits, a.dtype == 2 ? 4 : 2) || !aligned(scores, 4) || !aligned(out_scores, 4) || !aligned(parent, 4) ||
+        !aligned(token, 4))
+        return CLIS_ERR_MISALIGNED;
+    int nsm = 0;
+    if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
+    if (!workspace || ws_bytes < clis::beam_workspace(a, nsm)) return CLIS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return CLIS_ERR_MISALIGNED;
+    a.logits = logits;
+    a.scores = scores;
+    a.out_scores = out_scores;
+    a.parent = parent;
+    a.token = token;
+    return clis::launch_beam(a, workspace, nsm, reinterpret_cast<cudaStream_t>(stream));
+}
+
+clis_status_t clis_paged_reorder_workspace_size(const clis_reorder_t *desc, size_t *bytes)
+{
+    if (!desc || !bytes) return CLIS_ERR_INVALID_ARG;
+    clis::ReorderArgs a;
+    const clis_status_t st = check_reorder(desc, &a);
+    if (st == CLIS_OK) *bytes = a.R == 0 ? 0 : clis::reorder_workspace(a);
+    return st;
+}
+
+clis_status_t clis_paged_reorder(const clis_reorder_t *desc, const int32_t *lens, const int32_t *parent,
+                                 const int32_t *block_table, int32_t *new_table, int32_t *ring, int64_t ring_size,
+                                 const int64_t *state_in, int64_t *state_out, int32_t *lens_out, int32_t *done,
+                                 const clis_pages_t *tensors, int64_t n, void *workspace, size_t ws_bytes,
+                                 clis_stream_t stream)
+{
+    if (!desc) return CLIS_ERR_INVALID_ARG;
+    clis::ReorderArgs a;
+    const clis_status_t st = check_reorder(desc, &a);
+    if (st != CLIS_OK) return st;
+    if (n < 0 || ring_size < 1 || (n > 0 && !tensors)) return CLIS_ERR_INVALID_ARG;
+    if (n > clis::kMaxPageTensors || ring_size > kMaxN) return CLIS_ERR_UNSUPPORTED;
+    for (int64_t i = 0; i < n; i++) {
+        const clis_pages_t &t = tensors[i];
+        if (t.layers < 0 || t.heads < 0 || t.row_bytes < 4 || t.sl < 0 || t.sp < 0 || t.sh < 0 || t.sn < t.row_bytes)
+            return CLIS_ERR_INVALID_ARG;
+        if (t.layers > 65536 || t.heads > 65536 || t.row_bytes > 65536 || t.heads * desc->page_size * t.row_bytes > INT32_MAX)
+            return CLIS_ERR_UNSUPPORTED;
+        for (int64_t s : {t.sl, t.sp, t.sh, t.sn})
+            if (s >= (int64_t(1) << 40)) return CLIS_ERR_UNSUPPORTED;
+        if (t.layers > 0 && t.heads > 0 && !t.base) return CLIS_ERR_INVALID_ARG;
+        if (((t.row_bytes | t.sl | t.sp | t.sh | t.sn) & 3) || !aligned(t.base, 4)) return CLIS_ERR_MISALIGNED;
+        a.t[i] = t;
+        a.vec[i] = !((t.row_bytes | t.sl | t.sp | t.sh | t.sn) & 15) && aligned(t.base, 16);
+    }
+    a.tensors = static_cast<int>(n);
+    if (!ring || !state_in || !state_out || state_in == state_out) return CLIS_ERR_INVALID_ARG;
+    if (a.R > 0 && (!lens || !parent || !block_table || !new_table || !lens_out || !done)) return CLIS_ERR_INVALID_ARG;
+    if (a.R > 0 && new_table == block_table && a.R * a.W > 1 && a.bt_s != a.bo_s) return CLIS_ERR_INVALID_ARG;
+    if (!aligned(lens, 4) || !aligned(parent, 4) || !aligned(block_table, 4) || !aligned(new_table, 4) || !aligned(ring, 4) ||
+        !aligned(state_in, 8) || !aligned(state_out, 8) || !aligned(lens_out, 4) || !aligned(done, 4))
+        return CLIS_ERR_MISALIGNED;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (a.R == 0)  // nothing but the ring's state
+        return cudaMemcpyAsync(state_out, state_in, 2 * sizeof(int64_t), cudaMemcpyDeviceToDevice, cs) == cudaSuccess ? CLIS_OK
+                                                                                                                    : CLIS_ERR_CUDA;
+    if (!workspace || ws_bytes < clis::reorder_workspace(a)) return CLIS_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return CLIS_ERR_MISALIGNED;
+    int nsm = 0;
+    if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
+    a.lens = lens;
+    a.parent = parent;
+    a.table_in = block_table;
+    a.table_out = new_table;
+    a.lens_out = lens_out;
+    a.done = done;
+    a.ring = ring;
+    a.ring_size = ring_size;
+    a.state_in = state_in;
+    a.state_out = state_out;
+    return clis::launch_reorder(a, workspace, nsm, cs);
 }
 
 }  // extern "C"

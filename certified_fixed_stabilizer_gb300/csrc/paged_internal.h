@@ -154,6 +154,44 @@ clis_status_t launch_paged_chunk_schedule(const PagedArgs &a, int rows_small, vo
                                           cudaStream_t stream);
 clis_status_t launch_paged_chunk(const PagedArgs &a, int rows_small, void *workspace, int nsm, cudaStream_t stream);
 
+// -------------------------------------------------------------- beam search
+
+constexpr int kMaxBeams = 64;             // of a request
+constexpr int kMaxPicks = 64;             // candidates of a request
+constexpr int64_t kMaxBeamChunks = 49152;  // chunks of 512 logits of a request (shared memory)
+
+struct BeamArgs {
+    const void *logits;
+    int64_t l_sr, l_sw;
+    const float *scores;
+    float *out_scores;
+    int32_t *parent, *token;
+    int R, W, V, K;
+    int dtype;  // clis_dtype_t, or 2: fp32
+};
+
+bool beam_fits(const BeamArgs &a);
+size_t beam_workspace(const BeamArgs &a, int nsm);
+clis_status_t launch_beam(const BeamArgs &a, void *workspace, int nsm, cudaStream_t stream);
+
+constexpr int kMaxPageTensors = 8;
+
+struct ReorderArgs {
+    const int32_t *lens, *parent, *table_in;
+    int32_t *table_out, *lens_out, *done, *ring;
+    const int64_t *state_in;
+    int64_t *state_out;
+    int64_t bt_s, bo_s, ring_size, num_pages;
+    int R, W, width, page_shift, tensors;
+    clis_pages_t t[kMaxPageTensors];
+    int vec[kMaxPageTensors];  // rows are copied 16 bytes at a time
+};
+
+size_t reorder_workspace(const ReorderArgs &a);
+clis_status_t launch_reorder(const ReorderArgs &a, void *workspace, int nsm, cudaStream_t stream);
+clis_status_t read_reorder_error(uint32_t *code);
+clis_status_t clear_reorder_error();
+
 // Device error words of these kernels (CLIS_PAGED_* bits and wait bits), one
 // per translation unit; read after a device synchronisation.
 clis_status_t read_rot_error(uint32_t *code);

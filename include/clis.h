@@ -692,6 +692,86 @@ CLIS_API clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const cl
                                               float scale_log2, int causal, void *workspace, size_t ws_bytes,
                                               clis_stream_t stream);
 
+/* Selection of a beam search.  Of the W * V continuations (beam w, token v) of each
+ * request the K best by
+ *   scores[r, w] + logits[r, w, v] - log sum_u e^(logits[r, w, u]),
+ * best first, ties to the lowest w * V + v.  A continuation whose value is not finite is
+ * none (a masked token, -inf; every token of a beam whose score is -inf, or whose logits
+ * hold a NaN or +inf); where fewer than K are left, the places behind get the score
+ * -inf, parent -1 and token -1.
+ *   R, W, V, K   R * W up to 65535, W and K up to 64, W * V up to 2^31 - 1 and
+ *                W * ceil(V / 512) up to 49152 (25 million continuations of a request)
+ *   dtype        0 bf16, 1 fp16 (clis_dtype_t), 2 fp32
+ *   l_sr, l_sw   strides of the logits in elements, any >= 0 (rows need no alignment
+ *                beyond their type's)
+ *   logits       device [R, W, V], tokens contiguous
+ *   scores       device fp32 [R, W]
+ *   out_scores, parent, token  device fp32, int32, int32 [R, K]
+ *   workspace    device scratch of clis_beam_workspace_size() bytes (on the current
+ *                device), 256-byte aligned; not shared by calls that may run at the same time
+ * Values are compared in 64 bits with a logarithm off by about 1e-7.  Reruns agree bit
+ * for bit.  Errors as for clis_attn_fwd; CLIS_ERR_WORKSPACE. */
+typedef struct {
+    int64_t R, W, V, K;
+    int64_t dtype;
+    int64_t l_sr, l_sw;
+} clis_beam_t;
+
+CLIS_API clis_status_t clis_beam_workspace_size(const clis_beam_t *desc, size_t *bytes);
+CLIS_API clis_status_t clis_beam_select(const clis_beam_t *desc, const void *logits, const float *scores,
+                                        float *out_scores, int32_t *parent, int32_t *token, void *workspace,
+                                        size_t ws_bytes, clis_stream_t stream);
+
+/* The beams' block tables after a selection: row g * W + w (beam w of request g) goes on
+ * from row g * W + parent[g, w]; a negative parent ends the row.  Rows share pages: the
+ * new row names the pages of the one it goes on from, except that where a partly filled last
+ * page is gone on from more than once, all but the first (lowest w) get a page of
+ * the ring with a copy of its rows.  Pages that no row of the request names any more go
+ * back to the ring.  So the last page of a row is never shared unless it is full, and
+ * clis_paged_plan and clis_paged_append go on as ever (a beam's row must not be given back
+ * by a negative new_len there while it shares pages: end it here).
+ *   groups, beams  requests and W (up to 64); groups * beams up to 16384
+ *   width, page_size, num_pages  as in clis_paged_t
+ *   bt_ss, bo_ss   strides of rows of block_table and new_table
+ *   lens         device int32 [groups * beams]: tokens of each row
+ *   parent       device int32 [groups, beams], below beams
+ *   block_table, new_table  device int32 [groups * beams, width]; new_table may be
+ *                block_table itself (same stride), no other overlap.  Columns
+ *                behind a row's pages become -1.
+ *   ring, ring_size, state_in, state_out  as for clis_paged_plan: pages are taken from the
+ *                head on in the order of requests and beams, pages that go back
+ *                follow the tail in the order of requests, columns and beams
+ *   lens_out     device int32 [groups * beams]: tokens of the new rows
+ *   done         device int32 [groups]: 0 for a request that stays as it was: the ring has too
+ *                few pages for it and those before (CLIS_PAGED_POOL_BIT), a parent is out
+ *                of range (CLIS_PAGED_INDEX_BIT) or a length (CLIS_PAGED_LENGTH_BIT)
+ *   tensors, n   host array of the caches (values, codes, scales of K and V; up to 8) whose
+ *                rows are copied
+ *   workspace    device scratch of clis_paged_reorder_workspace_size() bytes, 256-byte
+ *                aligned; not shared by calls that may run at the same time
+ * Pages may be shared only within a request and in the same column, as this call makes
+ * them.  Two launches; reruns agree bit for bit.  Errors as for clis_paged_plan;
+ * CLIS_ERR_WORKSPACE. */
+typedef struct {
+    int64_t groups, beams, width, page_size, num_pages;
+    int64_t bt_ss, bo_ss;
+} clis_reorder_t;
+
+/* One tensor of a cache, all layers: row r of page p, head h, layer l lies at base + l * sl + p *
+ * sp + h * sh + r * sn (bytes) and has row_bytes bytes; all multiples of 4. */
+typedef struct {
+    void *base;
+    int64_t layers, heads, row_bytes;
+    int64_t sl, sp, sh, sn;
+} clis_pages_t;
+
+CLIS_API clis_status_t clis_paged_reorder_workspace_size(const clis_reorder_t *desc, size_t *bytes);
+CLIS_API clis_status_t clis_paged_reorder(const clis_reorder_t *desc, const int32_t *lens, const int32_t *parent,
+                                          const int32_t *block_table, int32_t *new_table, int32_t *ring,
+                                          int64_t ring_size, const int64_t *state_in, int64_t *state_out,
+                                          int32_t *lens_out, int32_t *done, const clis_pages_t *tensors, int64_t n,
+                                          void *workspace, size_t ws_bytes, clis_stream_t stream);
+
 /* Static description of a status code (never NULL). */
 CLIS_API const char *clis_status_string(clis_status_t status);
 
