@@ -210,13 +210,18 @@ Split split_of(const clis_paged_t *p, int64_t max_q, int nsm)
 // Over a quantised cache: the kernel for few rows takes up to 64, and batches with chunks
 // always launch both kernels (the chunk kernel's keys are unpacked to 16 bits first, so
 // a single token costs it five times the bytes).
-Split split_q8(const clis_paged_t *p, int64_t max_q)
+struct SplitQ8 {
+    int rows;    // of the kernel for few rows, 0: not launched
+    bool chunk;  // the chunk kernel is launched
+};
+
+SplitQ8 split_q8(const clis_paged_t *p, int64_t max_q)
 {
     const int g = static_cast<int>(p->H / p->Hkv);
     const int64_t mq = max_q < p->T ? max_q : p->T;
-    Split s;
-    s.row_tiles = clis::paged_q8_row_tiles(mq, g);
-    s.chunk = mq * g > 16 * s.row_tiles;
+    SplitQ8 s;
+    s.rows = clis::paged_q8_rows(mq, g);
+    s.chunk = mq * g > s.rows;
     return s;
 }
 
@@ -608,8 +613,8 @@ clis_status_t clis_attn_paged_q8_workspace_size(const clis_paged_t *desc, const 
     if (desc->S == 0 || desc->T == 0) return CLIS_OK;
     int nsm = 0;
     if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
-    const Split s = split_q8(desc, max_q);
-    *bytes = clis::paged_q8_workspace(static_cast<int>(desc->d), s.row_tiles, nsm) +
+    const SplitQ8 s = split_q8(desc, max_q);
+    *bytes = clis::paged_q8_workspace(static_cast<int>(desc->d), s.rows, nsm) +
              (s.chunk ? clis::paged_chunk_workspace(attn_args(desc), nsm) + 2 * pages_bytes(desc) + scales_bytes(desc) : 0);
     return CLIS_OK;
 }
@@ -632,9 +637,9 @@ clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_
         return CLIS_ERR_MISALIGNED;
     int nsm = 0;
     if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
-    const Split s = split_q8(desc, max_q);
+    const SplitQ8 s = split_q8(desc, max_q);
     clis::PagedArgs a = attn_args(desc);
-    const size_t few = clis::paged_q8_workspace(a.d, s.row_tiles, nsm);
+    const size_t few = clis::paged_q8_workspace(a.d, s.rows, nsm);
     const size_t chunk = s.chunk ? clis::paged_chunk_workspace(a, nsm) : 0;
     const size_t need = few + chunk + (s.chunk ? 2 * pages_bytes(desc) + scales_bytes(desc) : 0);
     if (need > 0 && (!workspace || ws_bytes < need)) return CLIS_ERR_WORKSPACE;
@@ -650,7 +655,7 @@ clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_
     a.causal = causal;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     char *w = static_cast<char *>(workspace);
-    if (!s.chunk) return clis::launch_paged_q8(a, z, s.row_tiles, true, false, w, nsm, cs);
+    if (!s.chunk) return clis::launch_paged_q8(a, z, s.rows, true, false, w, nsm, cs);
     // The chunk kernel works on 16-bit copies of its sequences' pages.
     clis::PagedArgs b = a;
     uint16_t *kp = reinterpret_cast<uint16_t *>(w + few + chunk);
@@ -662,10 +667,10 @@ clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_
     b.kc_sn = b.vc_sn = a.d;
     b.kc_sh = b.vc_sh = desc->page_size * a.d;
     b.kc_sp = b.vc_sp = desc->Hkv * desc->page_size * a.d;
-    const int rows_small = 16 * s.row_tiles;
+    const int rows_small = s.rows;
     clis_status_t e = clis::launch_paged_unpack(a, z, rows_small, kp, ks, vp, nsm, cs);
     if (e == CLIS_OK) e = clis::launch_paged_chunk_schedule(b, rows_small, w + few, nsm, cs);
-    if (e == CLIS_OK && s.row_tiles > 0) e = clis::launch_paged_q8(a, z, s.row_tiles, false, true, w, nsm, cs);
+    if (e == CLIS_OK && s.rows > 0) e = clis::launch_paged_q8(a, z, s.rows, false, true, w, nsm, cs);
     if (e == CLIS_OK) e = clis::launch_paged_chunk(b, rows_small, w + few, nsm, cs);
     return e;
 }

@@ -1294,7 +1294,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_chunk_join_kernel(const
 
 // ------------------------------------------------------------------ host side
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn()
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     if (!fn) {
@@ -1308,10 +1310,12 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn()
     return fn;
 }
 
+namespace {
+
 bool encode(CUtensorMap *map, const void *base, int dtype, int rank, const cuuint64_t *dims, const int64_t *elem_strides,
             const cuuint32_t *box)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t strides[3];
     for (int i = 0; i + 1 < rank; i++) {

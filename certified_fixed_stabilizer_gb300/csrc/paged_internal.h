@@ -3,6 +3,8 @@
 // the plan of a serving step, and attention over the cache.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
@@ -140,12 +142,13 @@ size_t paged_decode_workspace(int d, int row_tiles, int nsm);
 // does not read.
 clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, bool after_schedule, void *workspace,
                                   int nsm, cudaStream_t stream);
-// The same over a quantised cache: row tiles 1, 2, 4 or 0.
-int paged_q8_row_tiles(int64_t max_q, int g);
-size_t paged_q8_workspace(int d, int row_tiles, int nsm);
-clis_status_t launch_paged_q8(const PagedArgs &a, const QuantArgs &z, int row_tiles, bool strict, bool after_schedule,
+// The same over a quantised cache: query rows per sequence 8, 16, 32, 64 or 0 (not used).
+int paged_q8_rows(int64_t max_q, int g);
+size_t paged_q8_workspace(int d, int rows, int nsm);
+clis_status_t launch_paged_q8(const PagedArgs &a, const QuantArgs &z, int rows, bool strict, bool after_schedule,
                               void *workspace, int nsm, cudaStream_t stream);
 size_t paged_chunk_workspace(const PagedArgs &a, int nsm);
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // nullptr on failure
 // Sequences of at most rows_small query rows are left to the decode kernel.
 // Schedule first, then (with rows_small > 0) the decode kernel, then the chunk kernel:
 // each of these kernels but the first may be set up while the one before it

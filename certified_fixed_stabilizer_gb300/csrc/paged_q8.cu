@@ -9,26 +9,32 @@
 // to the weights, one multiplication per query row and key instead of one per element.
 //
 // Bound: the cache's bytes, half of those of paged_decode.cu, and then the issue
-// slots: per 8 KB of codes (32 keys at d = 128) a warp spends about 600 instructions
-// on 16 query rows, two thirds of them on turning codes into fp16 pairs, about half of
-// what an SM can issue while these bytes arrive.
+// slots: turning 8 KB of codes into fp16 pairs alone takes a warp some 320 instructions.
 //
-//  * Work, runs and joins: as in paged_decode.cu.  A team of RT = 1, 2 or 4 warps
-//    (16 query rows each) shares one ring of stages, so 17 to 64 rows (drafted tokens)
-//    read the cache once as well; RT = 1 needs no barrier.
+//  * Work, runs and joins: as in paged_decode.cu.  A warp holds 8 query rows or 16
+//    (NT = 1, 2), a team of RT = 1, 2 or 4 warps that share one ring of stages up to 64, so
+//    drafted tokens read the cache once as well.
+//  * The products are taken transposed, S^T = KC Q^T and O^T += VC^T W^T: codes are the
+//    16-row operand, query rows the 8-column one.  A single token's g query heads fill
+//    4 or 8 of 8 places instead of 16, which halves the products, the weights and the
+//    registers of O.  W^T comes out of S^T's registers by one 8 x 8 transposition each.
 //  * int8 to fp16: the byte with its sign bit flipped is put below 0x64, which reads
 //    1024 + 128 + code, and 1152 is subtracted: exact, and the byte permutation does
 //    the transposition of V's pairs on the way.  E4M3 has its own instruction.
 //  * The contraction over d takes the elements in the order in which a thread's
 //    16-byte load of codes holds them; q's fragments are laid out the same way.
+//  * Loads: one warp of a team fetches its stages by TMA, page by page (a unit is 8 KB of
+//    codes), the scales by 4-byte copies that arrive on the same barrier.  With 16-byte
+//    copies by all lanes the addresses alone were a sixth of all instructions.
 //  * q is scaled by a power of two per row so that its largest magnitude is between
 //    2^14 and 2^15 and goes into fp16: exact for fp16 and bf16 values down to 2^-30 of
 //    the row's largest.
-//  * The weights of V carry vs_j, whose range has nothing to do with the softmax's, so
-//    they have a shift of their own: w_ij = 2^(x_ij + log2(vs_j) - m'_i) with the running
-//    maximum m'_i of the exponent, next to m_i for the row sum.  Both are raised
-//    lazily.  w is rounded to fp16 as the matrix instructions take it (off by up to
-//    2^-11, and by 2^-32 of the row's largest below that: weight_room in paged_sched.h).
+//  * The weights of V carry vs_j, whose range has nothing to do with the softmax's: with
+//    p_ij = 2^(x_ij - m_i) for the row sum, w_ij = p_ij vs_j 2^(e_i), where e_i follows the
+//    largest p vs of the row: it stands at 2^7 when it is set, and e_i is lowered (and O with
+//    it) when it has outgrown 2^15.  When m_i is raised, e_i goes along, so that w stays what
+//    it was.  w is rounded to fp16 as the matrix instructions take it (off by up to 2^-11,
+//    and by 2^-32 of the row's largest below that).
 #include <cuda_fp16.h>
 
 #include "paged_warp.cuh"
@@ -40,30 +46,26 @@ __device__ unsigned int g_q8_error_word = 0;
 namespace {
 
 constexpr float kTau = 8.0f;
-constexpr float kRoom = weight_room(1);
+constexpr unsigned kErrLoad = 1u << 0;  // a wait for a stage gave up (the forward kernel's producer bit)
 
-template <int D, int RT>
+template <int D, int NT, int RT>
 struct QCfg {
     static constexpr int TK = 4096 / D;                  // keys per unit: 8 KB of codes
     static constexpr int TEAMS = kDecodeWarps / RT;
-    static constexpr int NST = 3 * RT;
+    static constexpr int BLOCKS = NT == 1 ? 3 : 2;       // of an SM (registers)
+    static constexpr int NST = (NT == 1 ? 2 : 3) * RT;
+    static constexpr int AHEAD = RT == 1 ? NST - 1 : NST - 2;
     static constexpr int HALF = TK * D;                  // bytes of K (or V) of a stage
-    static constexpr int SCALES = 2 * HALF;              // [2][TK] floats behind the codes
-    static constexpr int STAGE = 2 * HALF + 2 * TK * 4;
-    static constexpr int SMEM = TEAMS * NST * STAGE;
+    static constexpr int STAGE = 2 * HALF;
+    static constexpr int SCALE = 2 * TK;                 // floats of a stage: K's, V's
+    static constexpr int SMEM = TEAMS * NST * (STAGE + SCALE * 4) + 1024;
 };
 
-// Place of a 16-byte chunk of a row of codes in its stage.  K is read by 16-byte loads
-// of four threads per row, V by ldmatrix (8 rows, one chunk): either way a quarter warp
-// touches all banks once.
+// Place of a 16-byte chunk of a row of codes in its stage, as TMA's 128- and 64-byte swizzles
+// leave it.  ldmatrix (8 rows, one chunk) touches all banks once, K's 16-byte loads of
+// four threads per row twice at d = 128.
 template <int D>
-__device__ __forceinline__ uint32_t at_k(int row, int chunk)
-{
-    return row * D + ((D == 128 ? chunk ^ ((row & 1) << 2) : chunk) << 4);
-}
-
-template <int D>
-__device__ __forceinline__ uint32_t at_v(int row, int chunk)
+__device__ __forceinline__ uint32_t at_row(int row, int chunk)
 {
     return row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
 }
@@ -73,11 +75,18 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int byt
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ float lg2_approx(float x)
+__device__ __forceinline__ float lds32(uint32_t at)
 {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
+    return x;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
 }
 
 __device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b)
@@ -110,40 +119,58 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t &a, uint32_t &b)
     }
 }
 
-// Clears the NaN halves of an fp16 pair; true if there was one.
-__device__ __forceinline__ bool scrub(uint32_t &u)
+// An fp16 pair of E4M3 values with 448 in the place of NaN.
+__device__ __forceinline__ uint32_t no_nan(uint32_t u)
 {
-    uint32_t keep = 0xFFFFFFFFu;
-    if ((u & 0x7C00u) == 0x7C00u) keep &= 0xFFFF0000u;
-    if (((u >> 16) & 0x7C00u) == 0x7C00u) keep &= 0x0000FFFFu;
-    u &= keep;
-    return keep != 0xFFFFFFFFu;
+    uint32_t r;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0x5F005F00u));
+    return r;
 }
 
-template <int RT>
-__device__ __forceinline__ void team_sync(int team)
+// Whether a word of E4M3 codes holds a NaN (0x7F or 0xFF).
+__device__ __forceinline__ bool has_nan(uint32_t w)
 {
-    if (RT == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(RT * 32) : "memory");
+    const uint32_t y = (w & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu;
+    return ((y - 0x01010101u) & ~y & 0x80808080u) != 0;
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit values held by a warp.
+__device__ __forceinline__ uint32_t transposed(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 
-template <int D, int DT, int CODE, int RT>
-__global__ void __launch_bounds__(kDecodeThreads, 2) paged_q8_kernel(const DecodeParams p, const QuantArgs z)
+template <int D, int DT, int CODE, int NT, int RT>
+__global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT, RT>::BLOCKS)
+    paged_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeParams p,
+                    const QuantArgs z, const int box_shift)
 {
-    using C = QCfg<D, RT>;
-    constexpr int TK = C::TK, NB = TK / 8, KB = TK / 16;
+    using C = QCfg<D, NT, RT>;
+    constexpr int TK = C::TK, KM = TK / 16;  // key tiles of 16
     const PagedArgs &a = p.a;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t s_sum[kDecodeWarps];
     __shared__ int s_seq[C::TEAMS];
     __shared__ uint64_t s_rel[C::TEAMS];
+    __shared__ __align__(8) uint64_t s_full[C::TEAMS * C::NST], s_empty[C::TEAMS * C::NST];
+    __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int team = warp / RT, mt = warp % RT;  // this warp has rows 16 mt .. 16 mt + 15 of its team's items
+    const int team = warp / RT, mt = warp % RT;  // this warp has rows 8 NT mt .. 8 NT (mt + 1) - 1 of its team's items
     unsigned int bad = 0;
     pdl_launch();
+    if (tid == 0) {
+        for (int i = 0; i < C::TEAMS * C::NST; i++) {
+            mbar_init(smem_u32(&s_full[i]), 33);  // the bytes that TMA brings, and 32 lanes' scales
+            mbar_init(smem_u32(&s_empty[i]), RT);
+        }
+        s_abort = 0;
+        fence_mbar_init();
+    }
 
     const Runs runs = block_runs<TK, C::TEAMS>(p, s_sum, s_seq, s_rel, bad);
     const int c = team * gridDim.x + blockIdx.x;  // this worker
@@ -162,315 +189,406 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) paged_q8_kernel(const Decod
     cur.j = static_cast<int>(s_rel[team] - static_cast<uint64_t>(cur.h) * cur.units);
     cur.left = static_cast<uint32_t>(u1 - u0);
 
-    // ---- loader: one stage per unit, `ld` runs NST - 1 units ahead of `cur`; the team's
-    // warps share out the rows
-    constexpr int CPR = D / 16;           // 16-byte chunks per row
-    constexpr int RPI = 32 / CPR;         // rows per copy instruction
-    constexpr int NCP = TK / RT / RPI;
-    constexpr int KPL = TK / 32;          // keys per lane of the page lookup (one page: at least 8 keys)
-    const uint32_t ring = smem_u32(smem) + team * C::NST * C::STAGE;
-    const uint8_t *ring_ptr = smem + team * C::NST * C::STAGE;
-    const int key_mask = (1 << a.page_shift) - 1;
-    const int lrow = mt * (TK / RT) + lane / CPR, lchunk = lane % CPR;
+    // ---- the ring; the team's first warp fetches a unit per stage, AHEAD units before `cur`
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t ring = base + team * C::NST * C::STAGE;
+    const uint32_t ring_scales = base + C::TEAMS * C::NST * C::STAGE + team * C::NST * C::SCALE * 4;
+    const uint32_t full = smem_u32(&s_full[team * C::NST]), empty = smem_u32(&s_empty[team * C::NST]);
+    volatile int *ab = &s_abort;
+    constexpr int KPL = TK / 32;  // keys per lane of the scales (of one page: it has at least 8)
+    const int box = 1 << box_shift, boxes = TK >> box_shift;  // rows of a TMA box, boxes of a unit
+    const uint64_t pol = policy_evict_first();
     Pos<TK> ld = cur;
     int ld_stage = 0;
-    auto lane_key = [&](const Pos<TK> &q) { return q.j * TK + lane * KPL; };
+    uint32_t ld_phase = 0, loads = 0;
+    // Page of the lane's box of the unit that is fetched next.  What the table holds is looked
+    // at when it is used (any number can stand there, so none can say that there is no key).
+    auto has_box = [&](const Pos<TK> &q) { return q.left > 0 && lane < boxes && q.j * TK + lane * box < q.q.kv; };
     auto page_at = [&](const Pos<TK> &q) -> int {
-        const int key = lane_key(q);
-        if (q.left == 0 || key >= q.q.kv) return -1;
-        return __ldg(a.block_table + q.s * a.bt_s + (key >> a.page_shift));
+        return has_box(q) ? __ldg(a.block_table + q.s * a.bt_s + ((q.j * TK + lane * box) >> a.page_shift)) : -1;
     };
-    int page = page_at(ld);
-    auto load_step = [&]() {
-        if (ld.left > 0) {
-            if (page < 0 || page >= a.num_pages) {
-                if (lane_key(ld) < ld.q.kv) bad |= CLIS_PAGED_INDEX_BIT;
-                page = -1;  // its keys read as zeros
-            }
-            const uint32_t dst = ring + ld_stage * C::STAGE;
-            const int key0 = ld.j * TK;
-#pragma unroll
-            for (int i = 0; i < NCP; i++) {
-                const int row = i * RPI + lrow;
-                const int pg = __shfl_sync(~0u, page, row / KPL);
-                const bool ok = pg >= 0 && key0 + row < ld.q.kv;
-                const int64_t pi = ok ? pg : 0;
-                const int in = ok ? (key0 + row) & key_mask : 0;
-                cp_async16(dst + at_k<D>(row, lchunk), z.kc + pi * a.kc_sp + ld.h * a.kc_sh + in * a.kc_sn + lchunk * 16, ok ? 16 : 0);
-                cp_async16(dst + C::HALF + at_v<D>(row, lchunk), z.vc + pi * a.vc_sp + ld.h * a.vc_sh + in * a.vc_sn + lchunk * 16,
-                           ok ? 16 : 0);
-            }
-            // Scales: K's by the team's first warp, V's by its last.
-#pragma unroll
-            for (int i = 0; i < KPL; i++) {
-                const bool ok = page >= 0 && key0 + lane * KPL + i < ld.q.kv;
-                const int64_t pi = ok ? page : 0;
-                const int in = ok ? (key0 + lane * KPL + i) & key_mask : 0;
-                const uint32_t to = dst + C::SCALES + (lane * KPL + i) * 4;
-                if (mt == 0) cp_async4(to, z.ks + pi * z.ks_sp + ld.h * z.ks_sh + in * z.ks_sn, ok ? 4 : 0);
-                if (mt == RT - 1) cp_async4(to + TK * 4, z.vs + pi * z.vs_sp + ld.h * z.vs_sh + in * z.vs_sn, ok ? 4 : 0);
-            }
-            ld_stage = ld_stage + 1 == C::NST ? 0 : ld_stage + 1;
-            ld.left--;
-            if (++ld.j == ld.units && ld.left > 0) ld.next_item(a, p.g, p.rows_max);
-            page = page_at(ld);
+    int page = mt == 0 ? page_at(ld) : -1;
+    auto load_step = [&]() -> bool {  // (the team's first warp alone)
+        if (ld.left == 0) return true;
+        if (RT > 1 && loads >= C::NST)  // the stage's last unit has been read by all warps
+            if (!mbar_wait_warp(empty + 8 * ld_stage, ld_phase ^ 1, ab, &g_q8_error_word, kErrLoad)) return false;
+        const bool has = has_box(ld);
+        if (has && (page < 0 || page >= a.num_pages)) {
+            bad |= CLIS_PAGED_INDEX_BIT;
+            page = static_cast<int>(a.num_pages);  // out of the map: its keys read as zeros
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        const uint32_t bar = full + 8 * ld_stage;
+        const int live = __popc(__ballot_sync(~0u, has)), key0 = ld.j * TK;
+        if (lane == 0) mbar_arrive_expect_tx(bar, live * 2 * (D << box_shift));
+        __syncwarp();
+        if (has) {
+            const uint32_t dst = ring + ld_stage * C::STAGE + lane * (D << box_shift);
+            const int row = (key0 + lane * box) & ((1 << a.page_shift) - 1);
+            tma_load_4d_hint(dst, &tm_k, bar, 0, row, ld.h, page, pol);
+            tma_load_4d_hint(dst + C::HALF, &tm_v, bar, 0, row, ld.h, page, pol);
+        }
+        const int pg = __shfl_sync(~0u, page, (lane * KPL) >> box_shift);
+#pragma unroll
+        for (int i = 0; i < KPL; i++) {
+            const int key = key0 + lane * KPL + i;
+            const bool ok = key < ld.q.kv && pg < a.num_pages;
+            const int64_t pi = ok ? pg : 0;
+            const int in = ok ? key & ((1 << a.page_shift) - 1) : 0;
+            const uint32_t to = ring_scales + (ld_stage * C::SCALE + lane * KPL + i) * 4;
+            cp_async4(to, z.ks + pi * z.ks_sp + ld.h * z.ks_sh + in * z.ks_sn, ok ? 4 : 0);
+            cp_async4(to + TK * 4, z.vs + pi * z.vs_sp + ld.h * z.vs_sh + in * z.vs_sn, ok ? 4 : 0);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        ++loads;
+        if (++ld_stage == C::NST) {
+            ld_stage = 0;
+            ld_phase ^= 1;
+        }
+        ld.left--;
+        if (++ld.j == ld.units && ld.left > 0) ld.next_item(a, p.g, p.rows_max);
+        page = page_at(ld);
+        return true;
     };
+    uint32_t done = 0;  // units read
+    bool fine = true;
+    if (mt == 0)
 #pragma unroll 1
-    for (int i = 0; i < C::NST - 1; i++) load_step();
+        for (int i = 0; i < C::AHEAD; i++) fine = fine && load_step();
 
     const int r4 = lane >> 2, t4 = lane & 3, c2 = t4 * 2;
+    const int key_mask = (1 << a.page_shift) - 1;
     int stage = 0;
+    uint32_t phase = 0;
 
-    while (cur.left > 0) {
+    while (fine && cur.left > 0) {
         // ---- one item, units j0 .. j1 - 1 of it
         const int j0 = cur.j;
         const int j1 = static_cast<int>(min(static_cast<uint32_t>(cur.units), j0 + cur.left));
         const int n = cur.q.n, kv = cur.q.kv, R = n * p.g, q0 = cur.q.q0;
         const int lim0 = visible_keys(n, kv, 0, a.causal);  // keys that every row sees
-        const bool live = mt * 16 < R;                      // (the team's barriers are met either way)
+        const int row0 = mt * 8 * NT;
+        const bool live = row0 < R;  // (the team's barriers are met either way)
 
-        // q's rows r4 and r4 + 8 of this tile: word w of a row's thread t4 holds elements
-        // 16 t4 + 4 w .. (w < 4) or 64 + 16 t4 + 4 (w - 4) .. of d.
-        uint32_t qf[D / 16][4];
-        int lim[2];
-        float cs[2];  // scale_log2 over the power of two that q's row was multiplied by
+        // q's row r4 of each column tile: word w of thread t4 holds elements 16 t4 + 4 w ..
+        // (w < 4) or 64 + 16 t4 + 4 (w - 4) .. of d.
+        uint32_t qf[NT][D / 16][2];
+        float2 cs[NT];     // of rows c2, c2 + 1: scale_log2 over the power of two that q's row was multiplied by
+        int lim[NT][2];
 #pragma unroll
-        for (int hf = 0; hf < 2; hf++) {
-            const int row = mt * 16 + hf * 8 + r4;
+        for (int nt = 0; nt < NT; nt++) {
+            const int row = row0 + nt * 8 + r4;
             const bool ok = row < R;
             const int tok = ok ? row / p.g : 0, hd = cur.h * p.g + (ok ? row - tok * p.g : 0);
-            lim[hf] = ok ? visible_keys(n, kv, tok, a.causal) : 0;
             const uint16_t *src = a.q + static_cast<int64_t>(q0 + tok) * a.q_st + hd * a.q_sh + t4 * 16;
-            uint32_t u[D / 16][2];
+            uint32_t top = 0;  // the row's largest magnitude: bits of non-negative floats are ordered
 #pragma unroll
             for (int w = 0; w < D / 16; w += 2) {
                 const uint4 v = ok ? __ldg(reinterpret_cast<const uint4 *>(src + (w >> 2) * 64 + (w & 3) * 4)) : make_uint4(0, 0, 0, 0);
-                u[w][0] = v.x;
-                u[w][1] = v.y;
-                u[w + 1][0] = v.z;
-                u[w + 1][1] = v.w;
+                qf[nt][w][0] = v.x;
+                qf[nt][w][1] = v.y;
+                qf[nt][w + 1][0] = v.z;
+                qf[nt][w + 1][1] = v.w;
             }
-            uint32_t top = 0;  // the row's largest magnitude: bits of non-negative floats are ordered
 #pragma unroll
             for (int w = 0; w < D / 16; w++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    top = max(top, __float_as_uint(elem_lo<DT>(u[w][e])) & 0x7FFFFFFFu);
-                    top = max(top, __float_as_uint(elem_hi<DT>(u[w][e])) & 0x7FFFFFFFu);
+                    top = max(top, __float_as_uint(elem_lo<DT>(qf[nt][w][e])) & 0x7FFFFFFFu);
+                    top = max(top, __float_as_uint(elem_hi<DT>(qf[nt][w][e])) & 0x7FFFFFFFu);
                 }
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
             // (a row of zeros or with something non-finite is taken as it is)
             const int e = top == 0 || top >= 0x7F800000u ? 0 : min(14 - (static_cast<int>(top >> 23) - 127), 126);
-            const float f = exp2_int(e);
-            cs[hf] = a.scale_log2 * exp2_int(-e);
+            const float f = exp2_int(e), s1 = a.scale_log2 * exp2_int(-e);
 #pragma unroll
-            for (int w = 0; w < D / 16; w++) {
-                qf[w][hf] = pack2<1>(elem_lo<DT>(u[w][0]) * f, elem_hi<DT>(u[w][0]) * f);
-                qf[w][hf + 2] = pack2<1>(elem_lo<DT>(u[w][1]) * f, elem_hi<DT>(u[w][1]) * f);
+            for (int w = 0; w < D / 16; w++)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    qf[nt][w][h] = pack2<1>(elem_lo<DT>(qf[nt][w][h]) * f, elem_hi<DT>(qf[nt][w][h]) * f);
+            cs[nt] = make_float2(__shfl_sync(~0u, s1, c2 * 4), __shfl_sync(~0u, s1, c2 * 4 + 4));
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int r = row0 + nt * 8 + c2 + h;
+                lim[nt][h] = r < R ? visible_keys(n, kv, r / p.g, a.causal) : 0;
             }
         }
-        // o[2 i], o[2 i + 1]: columns 16 i + 4 t4 + {0, 2} and + {1, 3} of rows r4 and r4 + 8.
-        float o[D / 8][4];
-        float m_run[2], l_run[2], l_low[2];  // l_low: what the last addition to l_run gained by rounding
-        float m_val[2];                      // the shift of the weights of V
-        m_run[0] = m_run[1] = m_val[0] = m_val[1] = -INFINITY;
-        l_run[0] = l_run[1] = l_low[0] = l_low[1] = 0.f;
+        // o[i][nt]: d = 16 i + 2 r4 of rows c2, c2 + 1, then d + 1 of them.
+        float o[D / 16][NT][4];
+        float2 m_run[NT], l_run[NT], l_low[NT];  // l_low: what the last addition to l_run gained by rounding
+        float2 ev[NT], fv[NT];                   // the weights of V: exponent and factor 2^exponent
 #pragma unroll
-        for (int i = 0; i < D / 8; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        for (int nt = 0; nt < NT; nt++) {
+            m_run[nt] = ev[nt] = make_float2(-INFINITY, -INFINITY);
+            l_run[nt] = l_low[nt] = fv[nt] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+        }
         bool dirty = false;
 
 #pragma unroll 1
         for (int j = j0; j < j1; j++) {
-            cp_async_wait<C::NST - 2>();
-            team_sync<RT>(team);
-            load_step();  // into the stage that the previous unit has been read from
+            __syncwarp();
+            if (mt == 0 && !load_step()) {  // (RT = 1: into the stage that the previous unit has been read from)
+                fine = false;
+                break;
+            }
+            if (!mbar_wait_warp(full + 8 * stage, phase, ab, &g_q8_error_word, kErrLoad)) {
+                fine = false;
+                break;
+            }
+            ++done;
             const int key0 = j * TK;
-            const uint8_t *sK = ring_ptr + stage * C::STAGE;
-            const uint32_t sV = ring + stage * C::STAGE + C::HALF;
-            const float *sS = reinterpret_cast<const float *>(sK + C::SCALES);
-            stage = stage + 1 == C::NST ? 0 : stage + 1;
-            if (key0 >= kv || !live) continue;
-
-            // S = Q KC^T: 16 rows x TK keys
-            float s[NB][4];
-#pragma unroll
-            for (int i = 0; i < NB; i++) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll
-            for (int hh = 0; hh < D / 64; hh++)
-#pragma unroll
-                for (int i0 = 0; i0 < NB; i0 += 4) {
-                    uint4 kw[4];
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        kw[i] = *reinterpret_cast<const uint4 *>(sK + at_k<D>((i0 + i) * 8 + r4, hh * 4 + t4));
-#pragma unroll
-                    for (int w = 0; w < 4; w++)
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            uint32_t b0, b1;
-                            unpack<CODE, false>(w == 0 ? kw[i].x : w == 1 ? kw[i].y : w == 2 ? kw[i].z : kw[i].w, b0, b1);
-                            mma16816<1>(s[i0 + i], qf[hh * 4 + w], b0, b1);
-                        }
-                }
-            const bool edge = key0 + TK > lim0;  // some row does not see some key
-            float mx[2] = {-INFINITY, -INFINITY}, my[2] = {-INFINITY, -INFINITY}, lv[NB][2];
-#pragma unroll
-            for (int i = 0; i < NB; i++) {
-                const float2 ks = *reinterpret_cast<const float2 *>(sS + i * 8 + c2);
-                const float2 vs = *reinterpret_cast<const float2 *>(sS + TK + i * 8 + c2);
-                lv[i][0] = lg2_approx(vs.x);
-                lv[i][1] = lg2_approx(vs.y);
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    s[i][e] *= e & 1 ? ks.y : ks.x;
-                    if (edge && key0 + i * 8 + c2 + (e & 1) >= lim[e >> 1]) s[i][e] = -INFINITY;
-                }
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                    mx[hf] = fmax3(mx[hf], s[i][2 * hf], s[i][2 * hf + 1]);
-                    const float y0 = fmaf(s[i][2 * hf], cs[hf], lv[i][0]), y1 = fmaf(s[i][2 * hf + 1], cs[hf], lv[i][1]);
-                    my[hf] = fmax3(my[hf], s[i][2 * hf] == -INFINITY ? -INFINITY : y0, s[i][2 * hf + 1] == -INFINITY ? -INFINITY : y1);
-                }
+            const uint32_t sK = ring + stage * C::STAGE, sV = sK + C::HALF;
+            const uint32_t sS = ring_scales + stage * C::SCALE * 4;
+            const uint32_t freed = empty + 8 * stage;
+            if (++stage == C::NST) {
+                stage = 0;
+                phase ^= 1;
             }
-            bool grow = false;
+            if (key0 < kv && live) {
+                // S^T = KC Q^T: TK keys x 8 rows per column tile
+                float s[KM][NT][4];
 #pragma unroll
-            for (int hf = 0; hf < 2; hf++) {
-                mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(~0u, mx[hf], 1));
-                my[hf] = fmaxf(my[hf], __shfl_xor_sync(~0u, my[hf], 1));
-                mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(~0u, mx[hf], 2)) * cs[hf];
-                my[hf] = fmaxf(my[hf], __shfl_xor_sync(~0u, my[hf], 2));
-                grow |= mx[hf] > m_run[hf] + kTau || my[hf] > m_val[hf] + (kTau + kRoom);
-            }
-            if (__any_sync(~0u, grow)) {
+                for (int km = 0; km < KM; km++)
 #pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                    if (mx[hf] > m_run[hf] + kTau) {
-                        const float al = ex2_approx(m_run[hf] - mx[hf]);
-                        m_run[hf] = mx[hf];
-                        l_run[hf] *= al;
-                        l_low[hf] *= al;
+                    for (int nt = 0; nt < NT; nt++) s[km][nt][0] = s[km][nt][1] = s[km][nt][2] = s[km][nt][3] = 0.f;
+#pragma unroll
+                for (int hh = 0; hh < D / 64; hh++)
+#pragma unroll
+                    for (int k0 = 0; k0 < KM; k0 += 2) {
+                        uint4 kw[2][2];
+#pragma unroll
+                        for (int i = 0; i < 2; i++)
+#pragma unroll
+                            for (int h = 0; h < 2; h++) kw[i][h] = lds128(sK + at_row<D>((k0 + i) * 16 + h * 8 + r4, hh * 4 + t4));
+#pragma unroll
+                        for (int w = 0; w < 4; w++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++) {
+                                uint32_t f[4];
+                                unpack<CODE, false>(w == 0 ? kw[i][0].x : w == 1 ? kw[i][0].y : w == 2 ? kw[i][0].z : kw[i][0].w, f[0], f[2]);
+                                unpack<CODE, false>(w == 0 ? kw[i][1].x : w == 1 ? kw[i][1].y : w == 2 ? kw[i][1].z : kw[i][1].w, f[1], f[3]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; nt++)
+                                    mma16816<1>(s[k0 + i][nt], f, qf[nt][hh * 4 + w][0], qf[nt][hh * 4 + w][1]);
+                            }
                     }
-                    if (my[hf] > m_val[hf] + (kTau + kRoom)) {
-                        const float m = my[hf] - kRoom;
-                        const float al = ex2_approx(m_val[hf] - m);
-                        m_val[hf] = m;
+                // The scores' scales, masks and maxima (s[.][.][0], [1]: key r4, rows c2 and c2 + 1;
+                // [2], [3]: key r4 + 8).
+                const bool edge = key0 + TK > lim0;  // some row does not see some key
+                float vs[KM][2];
+                float2 mx[NT];
 #pragma unroll
-                        for (int i = 0; i < D / 8; i++) {
-                            o[i][2 * hf] *= al;
-                            o[i][2 * hf + 1] *= al;
+                for (int nt = 0; nt < NT; nt++) mx[nt] = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+                for (int km = 0; km < KM; km++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int kr = km * 16 + h * 8 + r4;
+                        const float ks = lds32(sS + kr * 4);
+                        vs[km][h] = lds32(sS + (TK + kr) * 4);
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++) {
+                            float2 x = fmul2(make_float2(s[km][nt][2 * h], s[km][nt][2 * h + 1]), make_float2(ks, ks));
+                            if (edge) {
+                                if (key0 + kr >= lim[nt][0]) x.x = -INFINITY;
+                                if (key0 + kr >= lim[nt][1]) x.y = -INFINITY;
+                            }
+                            s[km][nt][2 * h] = x.x;
+                            s[km][nt][2 * h + 1] = x.y;
+                            mx[nt].x = fmaxf(mx[nt].x, x.x);
+                            mx[nt].y = fmaxf(mx[nt].y, x.y);
                         }
                     }
+                bool grow = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    mx[nt] = fmul2(mx[nt], cs[nt]);
+                    grow |= mx[nt].x > m_run[nt].x + kTau || mx[nt].y > m_run[nt].y + kTau;
                 }
-            }
-            uint32_t pf[KB][4];
+                if (__any_sync(~0u, grow)) {
 #pragma unroll
-            for (int hf = 0; hf < 2; hf++) {
-                const float ns = m_run[hf] == -INFINITY ? 0.f : -m_run[hf];
-                const float nv = m_val[hf] == -INFINITY ? 0.f : -m_val[hf];
-                float l = 0.f;
-#pragma unroll
-                for (int i = 0; i < NB; i++) {
-                    const float x0 = s[i][2 * hf], x1 = s[i][2 * hf + 1];
-                    l += ex2_approx(fmaf(x0, cs[hf], ns)) + ex2_approx(fmaf(x1, cs[hf], ns));
-                    float w0 = ex2_approx(fmaf(x0, cs[hf], lv[i][0]) + nv), w1 = ex2_approx(fmaf(x1, cs[hf], lv[i][1]) + nv);
-                    if (edge) {  // (a scale that is no number must not reach a row that does not see its key)
-                        w0 = x0 == -INFINITY ? 0.f : w0;
-                        w1 = x1 == -INFINITY ? 0.f : w1;
+                    for (int nt = 0; nt < NT; nt++) {
+                        auto raise = [&](float v, float &m, float &l, float &low, float &e, float &f) {
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                            if (!(v > m + kTau)) return;
+                            const float al = ex2_approx(m - v);
+                            l *= al;
+                            low *= al;
+                            if (m != -INFINITY) {  // w stays what it was
+                                e += v - m;
+                                f = ex2_approx(fminf(e, 100.f));
+                            }
+                            m = v;
+                        };
+                        raise(mx[nt].x, m_run[nt].x, l_run[nt].x, l_low[nt].x, ev[nt].x, fv[nt].x);
+                        raise(mx[nt].y, m_run[nt].y, l_run[nt].y, l_low[nt].y, ev[nt].y, fv[nt].y);
                     }
-                    pf[i >> 1][2 * (i & 1) + hf] = pack2<1>(w0, w1);
                 }
-                // Compensated: a run may be many thousands of units, each far below the sum.
-                const float y = l - l_low[hf], t = l_run[hf] + y;
-                l_low[hf] = (t - l_run[hf]) - y;
-                l_run[hf] = t;
-            }
-            // O += W VC: a transposed load gives 32 keys of 16 columns, in each word the codes
-            // of two neighbouring columns and two neighbouring keys.
-            auto pv = [&](bool clean) {
+                // p, its sum, and p times V's scale
+                grow = false;
 #pragma unroll
-                for (int kb = 0; kb < KB; kb += 2)
+                for (int nt = 0; nt < NT; nt++) {
+                    const float2 ns = make_float2(m_run[nt].x == -INFINITY ? 0.f : -m_run[nt].x, m_run[nt].y == -INFINITY ? 0.f : -m_run[nt].y);
+                    float2 l = make_float2(0.f, 0.f), tx = l;
 #pragma unroll
-                    for (int i = 0; i < D / 16; i++) {
-                        uint32_t vw[4], b0[4], b1[4];
-                        ldsm4_t(sV + at_v<D>(kb * 16 + lane, i), vw);
+                    for (int km = 0; km < KM; km++)
 #pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            unpack<CODE, true>(vw[e], b0[e], b1[e]);
-                            if (CODE != CLIS_CODE_INT8 && clean) {
-                                dirty |= scrub(b0[e]);
-                                dirty |= scrub(b1[e]);
+                        for (int h = 0; h < 2; h++) {
+                            const float2 x = ffma2(make_float2(s[km][nt][2 * h], s[km][nt][2 * h + 1]), cs[nt], ns);
+                            const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                            l = fadd2(l, pp);
+                            float2 t = fmul2(pp, make_float2(vs[km][h], vs[km][h]));
+                            if (edge) {  // (a scale that is no number must not reach a row that does not see its key)
+                                if (s[km][nt][2 * h] == -INFINITY) t.x = 0.f;
+                                if (s[km][nt][2 * h + 1] == -INFINITY) t.y = 0.f;
+                            }
+                            s[km][nt][2 * h] = t.x;
+                            s[km][nt][2 * h + 1] = t.y;
+                            tx.x = fmaxf(tx.x, t.x);
+                            tx.y = fmaxf(tx.y, t.y);
+                        }
+                    // Compensated: a run may be many thousands of units, each far below the sum.
+                    const float2 minus = make_float2(-1.f, -1.f);
+                    const float2 y = ffma2(l_low[nt], minus, l), t = fadd2(l_run[nt], y);
+                    l_low[nt] = ffma2(y, minus, ffma2(l_run[nt], minus, t));
+                    l_run[nt] = t;
+                    mx[nt] = tx;
+                    const float2 g = fmul2(tx, fv[nt]);
+                    grow |= g.x > 32768.f || g.y > 32768.f || (ev[nt].x == -INFINITY && tx.x > 0.f) || (ev[nt].y == -INFINITY && tx.y > 0.f) ||
+                            ev[nt].x > 100.f || ev[nt].y > 100.f;
+                }
+                if (__any_sync(~0u, grow)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) {
+                        auto lower = [&](float v, float &e, float &f, int h) {
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                            const bool none = e == -INFINITY;
+                            float to = fminf(e, 100.f);
+                            if (v > 0.f && (none || v * ex2_approx(to) > 32768.f)) {
+                                const int x = static_cast<int>(__float_as_uint(v) >> 23) - 127;
+                                to = static_cast<float>(max(-100, min(100, 7 - x)));
+                            }
+                            if (to == e || v == 0.f && none) return;
+                            const float al = none ? 0.f : ex2_approx(to - e);
+                            e = to;
+                            f = ex2_approx(to);
+#pragma unroll
+                            for (int i = 0; i < D / 16; i++) {
+                                o[i][nt][h] *= al;
+                                o[i][nt][2 + h] *= al;
+                            }
+                        };
+                        lower(mx[nt].x, ev[nt].x, fv[nt].x, 0);
+                        lower(mx[nt].y, ev[nt].y, fv[nt].y, 1);
+                    }
+                }
+                uint32_t wf[KM][NT][2];
+#pragma unroll
+                for (int km = 0; km < KM; km++)
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const float2 w = fmul2(make_float2(s[km][nt][2 * h], s[km][nt][2 * h + 1]), fv[nt]);
+                            wf[km][nt][h] = transposed(pack2<1>(w.x, w.y));
+                        }
+                // O^T += VC^T W^T: a transposed load gives 32 keys of 16 columns, in each word the
+                // codes of two neighbouring columns and two neighbouring keys.
+                auto pv = [&](bool clean) {
+#pragma unroll
+                    for (int k0 = 0; k0 < KM; k0 += 2)
+#pragma unroll
+                        for (int i = 0; i < D / 16; i++) {
+                            uint32_t vw[4], f[2][4];
+                            ldsm4_t(sV + at_row<D>(k0 * 16 + lane, i), vw);
+#pragma unroll
+                            for (int e = 0; e < 4; e++) unpack<CODE, true>(vw[e], f[e >> 1][2 * (e & 1)], f[e >> 1][2 * (e & 1) + 1]);
+                            if (CODE != CLIS_CODE_INT8 && clean)
+#pragma unroll
+                                for (int e = 0; e < 8; e++) f[e >> 2][e & 3] = no_nan(f[e >> 2][e & 3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; nt++) {
+                                mma16816<1>(o[i][nt], f[0], wf[k0][nt][0], wf[k0][nt][1]);
+                                mma16816<1>(o[i][nt], f[1], wf[k0 + 1][nt][0], wf[k0 + 1][nt][1]);
                             }
                         }
-                        mma16816<1>(o[2 * i], pf[kb], b0[0], b0[1]);
-                        mma16816<1>(o[2 * i + 1], pf[kb], b1[0], b1[1]);
-                        mma16816<1>(o[2 * i], pf[kb + 1], b0[2], b0[3]);
-                        mma16816<1>(o[2 * i + 1], pf[kb + 1], b1[2], b1[3]);
+                };
+                // Where a key is masked for some rows, or the stage's rows behind the last key hold
+                // whatever was there, a NaN code must not reach the output as 0 * NaN: it takes part as a
+                // number, and the rows that see it get a NaN at the end.
+                if (CODE != CLIS_CODE_INT8 && edge) {
+#pragma unroll 1
+                    for (int i = lane; i < C::HALF / 16; i += 32) {
+                        const uint4 u = lds128(sV + i * 16);
+                        dirty |= has_nan(u.x) || has_nan(u.y) || has_nan(u.z) || has_nan(u.w);
                     }
-            };
-            // Where a key is masked for some rows only, a NaN code of it must not reach them as
-            // 0 * NaN: it is left out of the product and given to the rows that see it at the end.
-            if (CODE != CLIS_CODE_INT8 && edge && lim0 < kv) pv(true);
-            else pv(false);
+                    pv(true);
+                } else {
+                    pv(false);
+                }
+            }
+            if (RT > 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(freed);
+            }
         }
+        if (!fine) break;
 
         // ---- write the rows: final, or partial
         const bool any_dirty = __any_sync(~0u, dirty);
         const bool whole = j0 == 0 && j1 == cur.units;
         const int64_t slot = 2 * static_cast<int64_t>(c) + (j0 == 0 ? 1 : 0);
 #pragma unroll
-        for (int hf = 0; hf < 2; hf++) {
-            const int row = mt * 16 + hf * 8 + r4;
-            float l = l_run[hf];
-            l += __shfl_xor_sync(~0u, l, 1);
-            l += __shfl_xor_sync(~0u, l, 2);
-            if (row >= R) continue;
-            const int tok = row / p.g, hd = cur.h * p.g + (row - tok * p.g);
-            if (CODE != CLIS_CODE_INT8 && any_dirty) {
-                const int see = min(lim[hf], j1 * TK);
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int row = row0 + nt * 8 + c2 + h;
+                float l = h ? l_run[nt].y : l_run[nt].x;
+                l += __shfl_xor_sync(~0u, l, 4);
+                l += __shfl_xor_sync(~0u, l, 8);
+                l += __shfl_xor_sync(~0u, l, 16);
+                if (row >= R) continue;
+                const int tok = row / p.g, hd = cur.h * p.g + (row - tok * p.g);
+                if (CODE != CLIS_CODE_INT8 && any_dirty) {
+                    const int see = min(lim[nt][h], j1 * TK);
 #pragma unroll 1
-                for (int key = max(lim0 / TK * TK, j0 * TK); key < see; key++) {
-                    const int pg = __ldg(a.block_table + cur.s * a.bt_s + (key >> a.page_shift));
-                    if (pg < 0 || pg >= a.num_pages) continue;
-                    const uint8_t *vs = z.vc + static_cast<int64_t>(pg) * a.vc_sp + cur.h * a.vc_sh +
-                                        static_cast<int64_t>(key & key_mask) * a.vc_sn + 4 * t4;
+                    for (int key = max(lim0 / TK * TK, j0 * TK); key < see; key++) {
+                        const int pg = __ldg(a.block_table + cur.s * a.bt_s + (key >> a.page_shift));
+                        if (pg < 0 || pg >= a.num_pages) continue;
+                        const uint8_t *v = z.vc + static_cast<int64_t>(pg) * a.vc_sp + cur.h * a.vc_sh +
+                                           static_cast<int64_t>(key & key_mask) * a.vc_sn + 2 * r4;
 #pragma unroll
-                    for (int i = 0; i < D / 16; i++) {
-                        const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(vs + i * 16));
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            if (((u >> (8 * e)) & 0x7Fu) == 0x7Fu) o[2 * i + (e & 1)][2 * hf + (e >> 1)] = NAN;
+                        for (int i = 0; i < D / 16; i++) {
+                            const uint32_t u = __ldg(reinterpret_cast<const unsigned short *>(v + i * 16));
+                            if ((u & 0x7Fu) == 0x7Fu) o[i][nt][h] = NAN;
+                            if (((u >> 8) & 0x7Fu) == 0x7Fu) o[i][nt][2 + h] = NAN;
+                        }
                     }
                 }
-            }
-            const float m = m_run[hf];
-            // From the weights' shift to the row's.
-            const float back = m_val[hf] == -INFINITY ? 0.f : ex2_approx(m_val[hf] - m);
-            if (whole) {
-                const float inv = l == 0.f ? 0.f : back / l;
-                uint16_t *dst = a.o + static_cast<int64_t>(q0 + tok) * a.o_st + hd * a.o_sh + 4 * t4;
+                const float m = h ? m_run[nt].y : m_run[nt].x, e = h ? ev[nt].y : ev[nt].x;
+                const float back = e == -INFINITY ? 0.f : ex2_approx(-e);  // (O is 0 then)
+                if (whole) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    uint16_t *dst = a.o + static_cast<int64_t>(q0 + tok) * a.o_st + hd * a.o_sh + 2 * r4;
 #pragma unroll
-                for (int i = 0; i < D / 16; i++) {  // (zeros for a row that sees no key)
-                    uint2 u = make_uint2(0u, 0u);
-                    if (l != 0.f) {
-                        u.x = pack2<DT>(o[2 * i][2 * hf] * inv, o[2 * i + 1][2 * hf] * inv);
-                        u.y = pack2<DT>(o[2 * i][2 * hf + 1] * inv, o[2 * i + 1][2 * hf + 1] * inv);
-                    }
-                    *reinterpret_cast<uint2 *>(dst + i * 16) = u;
+                    for (int i = 0; i < D / 16; i++)  // (zeros for a row that sees no key)
+                        *reinterpret_cast<uint32_t *>(dst + i * 16) =
+                            l == 0.f ? 0u : pack2<DT>(o[i][nt][h] * back * inv, o[i][nt][2 + h] * back * inv);
+                    if (r4 == 0 && a.lse2) a.lse2[static_cast<int64_t>(q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : m + log2f(l);
+                } else {
+                    float *dst = p.part_o + (slot * p.rows_max + row) * D + 2 * r4;
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++)
+                        *reinterpret_cast<float2 *>(dst + i * 16) = make_float2(o[i][nt][h] * back, o[i][nt][2 + h] * back);
+                    if (r4 == 0) p.part_ml[slot * p.rows_max + row] = make_float2(m, l);
                 }
-                if (t4 == 0 && a.lse2) a.lse2[static_cast<int64_t>(q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : m + log2f(l);
-            } else {
-                float *dst = p.part_o + (slot * p.rows_max + row) * D + 4 * t4;
-#pragma unroll
-                for (int i = 0; i < D / 16; i++)
-                    *reinterpret_cast<float4 *>(dst + i * 16) =
-                        make_float4(o[2 * i][2 * hf] * back, o[2 * i + 1][2 * hf] * back, o[2 * i][2 * hf + 1] * back,
-                                    o[2 * i + 1][2 * hf + 1] * back);
-                if (t4 == 0) p.part_ml[slot * p.rows_max + row] = make_float2(m, l);
             }
-        }
         if (!whole && j0 == 0 && lane == 0 && mt == 0) {
             const uint64_t end = u1 - cur.left + cur.units - 1;  // the item's last unit
             p.meta[c] = make_int4(item_parts(runs, c, end), q0, n, cur.h);
@@ -479,74 +597,109 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) paged_q8_kernel(const Decod
         cur.j = j1;
         if (cur.left > 0) cur.next_item(a, p.g, p.rows_max);
     }
-    cp_async_wait<0>();
+    if (!fine && mt == 0) {
+        // A wait gave up: the copies in flight end before the block does (or are given up too).
+        for (uint32_t k = done; k < loads; k++) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(full + 8 * (k % C::NST), (k / C::NST) & 1) && globaltimer_ns() - t0 < 200000000ull) {
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
     if (bad) atomicOr(&g_q8_error_word, bad);
     pdl_wait();
 }
 
-template <int D, int DT, int CODE, int RT>
-clis_status_t launch_impl(const DecodeParams &p, const QuantArgs &z, int grid, bool after_schedule, cudaStream_t stream)
+bool encode_codes(CUtensorMap *map, const uint8_t *base, const PagedArgs &a, int64_t sp, int64_t sh, int64_t sn, int box_rows)
 {
-    constexpr int smem = QCfg<D, RT>::SMEM;
-    if (cudaFuncSetAttribute(paged_q8_kernel<D, DT, CODE, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return CLIS_ERR_CUDA;
-    if (after_schedule) {
-        if (launch_pdl(paged_q8_kernel<D, DT, CODE, RT>, dim3(grid), kDecodeThreads, smem, stream, p, z) != cudaSuccess)
-            return CLIS_ERR_CUDA;
-    } else {
-        paged_q8_kernel<D, DT, CODE, RT><<<grid, kDecodeThreads, smem, stream>>>(p, z);
-        if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
-    }
-    return launch_join<D, DT>(p, stream) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.d), static_cast<cuuint64_t>(1) << a.page_shift, static_cast<cuuint64_t>(a.Hkv),
+                                static_cast<cuuint64_t>(a.num_pages)};
+    // (a stride of a size-1 dimension is never used; it gets a canonical value)
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(sn), static_cast<cuuint64_t>(a.Hkv == 1 ? a.d : sh),
+                                   static_cast<cuuint64_t>(a.num_pages == 1 ? a.d : sp)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(a.d), static_cast<cuuint32_t>(box_rows), 1, 1}, step[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(base), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, a.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int DT, int CODE>
-clis_status_t launch_rows(const DecodeParams &p, const QuantArgs &z, int row_tiles, int grid, bool after_schedule, cudaStream_t stream)
+template <int D, int DT, int CODE, int NT, int RT>
+clis_status_t launch_impl(const PagedArgs &a, const QuantArgs &z, bool strict, bool after_schedule, void *workspace, int nsm,
+                          cudaStream_t stream)
 {
-    if (row_tiles == 1) return launch_impl<D, DT, CODE, 1>(p, z, grid, after_schedule, stream);
-    if (row_tiles == 2) return launch_impl<D, DT, CODE, 2>(p, z, grid, after_schedule, stream);
-    return launch_impl<D, DT, CODE, 4>(p, z, grid, after_schedule, stream);
-}
-
-template <int D>
-clis_status_t launch_types(const DecodeParams &p, const QuantArgs &z, int row_tiles, int grid, bool after_schedule, cudaStream_t stream)
-{
-    const bool half = p.a.dtype == CLIS_DT_FP16;
-    if (z.code == CLIS_CODE_INT8)
-        return half ? launch_rows<D, 1, CLIS_CODE_INT8>(p, z, row_tiles, grid, after_schedule, stream)
-                    : launch_rows<D, 0, CLIS_CODE_INT8>(p, z, row_tiles, grid, after_schedule, stream);
-    return half ? launch_rows<D, 1, CLIS_CODE_E4M3>(p, z, row_tiles, grid, after_schedule, stream)
-                : launch_rows<D, 0, CLIS_CODE_E4M3>(p, z, row_tiles, grid, after_schedule, stream);
-}
-
-}  // namespace
-
-int paged_q8_row_tiles(int64_t max_q, int g)
-{
-    // Rows of the largest sequence if it is small; else those of single tokens.
-    constexpr int most = 64;
-    const int64_t rows = max_q <= most && max_q * g <= most ? max_q * g : g;
-    return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= most ? 4 : 0;
-}
-
-size_t paged_q8_workspace(int d, int row_tiles, int nsm)
-{
-    if (row_tiles == 0) return 0;
-    return parts_workspace(2 * static_cast<size_t>(nsm) * kDecodeWarps / row_tiles, 16 * static_cast<size_t>(row_tiles), d);
-}
-
-clis_status_t launch_paged_q8(const PagedArgs &a, const QuantArgs &z, int row_tiles, bool strict, bool after_schedule,
-                              void *workspace, int nsm, cudaStream_t stream)
-{
-    const int grid = 2 * nsm;  // two blocks fit an SM
+    using C = QCfg<D, NT, RT>;
+    const auto kernel = paged_q8_kernel<D, DT, CODE, NT, RT>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return CLIS_ERR_CUDA;
+    const int grid = C::BLOCKS * nsm;
     DecodeParams p;
     p.a = a;
     p.g = a.H / a.Hkv;
     p.least = 2;
     p.strict = strict;
-    place_parts(p, static_cast<size_t>(grid) * kDecodeWarps / row_tiles, 16 * static_cast<size_t>(row_tiles), workspace);
-    return a.d == 128 ? launch_types<128>(p, z, row_tiles, grid, after_schedule, stream)
-                      : launch_types<64>(p, z, row_tiles, grid, after_schedule, stream);
+    place_parts(p, static_cast<size_t>(grid) * C::TEAMS, 8 * NT * RT, workspace);
+    int box_shift = 0;
+    while ((1 << box_shift) < C::TK && box_shift < a.page_shift) box_shift++;
+    CUtensorMap mk, mv;
+    if (!encode_codes(&mk, z.kc, a, a.kc_sp, a.kc_sh, a.kc_sn, 1 << box_shift) ||
+        !encode_codes(&mv, z.vc, a, a.vc_sp, a.vc_sh, a.vc_sn, 1 << box_shift))
+        return CLIS_ERR_CUDA;
+    if (after_schedule) {
+        if (launch_pdl(kernel, dim3(grid), kDecodeThreads, C::SMEM, stream, mk, mv, p, z, box_shift) != cudaSuccess) return CLIS_ERR_CUDA;
+    } else {
+        kernel<<<grid, kDecodeThreads, C::SMEM, stream>>>(mk, mv, p, z, box_shift);
+        if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
+    }
+    return launch_join<D, DT>(p, stream) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
+}
+
+// Query rows that the kernels are built for: 8, 16, 32 and 64.
+template <int D, int DT, int CODE, typename... A>
+clis_status_t launch_rows(int rows, const A &...args)
+{
+    if (rows == 8) return launch_impl<D, DT, CODE, 1, 1>(args...);
+    if (rows == 16) return launch_impl<D, DT, CODE, 2, 1>(args...);
+    if (rows == 32) return launch_impl<D, DT, CODE, 2, 2>(args...);
+    return launch_impl<D, DT, CODE, 2, 4>(args...);
+}
+
+template <int D, typename... A>
+clis_status_t launch_types(bool half, bool int8, int rows, const A &...args)
+{
+    if (int8) return half ? launch_rows<D, 1, CLIS_CODE_INT8>(rows, args...) : launch_rows<D, 0, CLIS_CODE_INT8>(rows, args...);
+    return half ? launch_rows<D, 1, CLIS_CODE_E4M3>(rows, args...) : launch_rows<D, 0, CLIS_CODE_E4M3>(rows, args...);
+}
+
+template <int NT, int RT>
+size_t workspace_of(int d, int nsm)
+{
+    // (the same for both widths)
+    return parts_workspace(static_cast<size_t>(QCfg<128, NT, RT>::BLOCKS) * nsm * QCfg<128, NT, RT>::TEAMS, 8 * NT * RT, d);
+}
+
+}  // namespace
+
+int paged_q8_rows(int64_t max_q, int g)
+{
+    // Rows of the largest sequence if it is small; else those of single tokens.
+    constexpr int most = 64;
+    const int64_t rows = max_q <= most && max_q * g <= most ? max_q * g : g;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= most ? 64 : 0;
+}
+
+size_t paged_q8_workspace(int d, int rows, int nsm)
+{
+    return rows == 0 ? 0 : rows == 8 ? workspace_of<1, 1>(d, nsm) : rows == 16 ? workspace_of<2, 1>(d, nsm)
+           : rows == 32 ? workspace_of<2, 2>(d, nsm) : workspace_of<2, 4>(d, nsm);
+}
+
+clis_status_t launch_paged_q8(const PagedArgs &a, const QuantArgs &z, int rows, bool strict, bool after_schedule,
+                              void *workspace, int nsm, cudaStream_t stream)
+{
+    const bool half = a.dtype == CLIS_DT_FP16, int8 = z.code == CLIS_CODE_INT8;
+    return a.d == 128 ? launch_types<128>(half, int8, rows, a, z, strict, after_schedule, workspace, nsm, stream)
+                      : launch_types<64>(half, int8, rows, a, z, strict, after_schedule, workspace, nsm, stream);
 }
 
 clis_status_t read_q8_error(uint32_t *code)
