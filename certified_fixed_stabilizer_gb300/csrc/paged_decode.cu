@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const DecodeP
     const uint64_t u0 = decode_cut(U, nb, c), u1 = decode_cut(U, nb, c + 1);
 
     Pos<C::TK> cur;
-    cur.set(a, s_seq[warp]);
+    cur.set(a, s_seq[warp], p.g);
     cur.h = static_cast<int>(div64(s_rel[warp], cur.units));
     cur.j = static_cast<int>(s_rel[warp] - static_cast<uint64_t>(cur.h) * cur.units);
     cur.left = static_cast<uint32_t>(u1 - u0);

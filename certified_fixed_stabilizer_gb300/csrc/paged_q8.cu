@@ -11,9 +11,14 @@
 // Bound: the cache's bytes, half of those of paged_decode.cu, and then the issue
 // slots: turning 8 KB of codes into fp16 pairs alone takes a warp some 320 instructions.
 //
-//  * Work, runs and joins: as in paged_decode.cu.  A warp holds 8 query rows or 16
-//    (NT = 1, 2), a team of RT = 1, 2 or 4 warps that share one ring of stages up to 64, so
-//    drafted tokens read the cache once as well.
+//  * Work, runs and joins: as in paged_decode.cu.  A warp works alone, on 8, 16 or (d = 64)
+//    32 query rows, NT = 1, 2 or 4 column tiles; a sequence of up to 64 rows (drafted tokens) is
+//    several items that read the same keys, one after the other, mostly from L2.  From 16
+//    rows on what a warp does per unit is the time (850 instructions at NT = 2, two warps per
+//    scheduler).  Tiles of 32 rows at d = 128 spill registers (16, 32 and 64 rows of the 64 requests
+//    below: 231, 460 and 920 us with tiles of 16; 413 and 783 with 32 of int8, but 526 and 979
+//    of E4M3); at d = 64 they pay (32 rows 282 -> 230).  Teams of four warps that convert a unit
+//    together into fp16 tiles in shared memory took 607 and 798.
 //  * The products are taken transposed, S^T = KC Q^T and O^T += VC^T W^T: codes are the
 //    16-row operand, query rows the 8-column one.  A single token's g query heads fill
 //    4 or 8 of 8 places instead of 16, which halves the products, the weights and the
@@ -48,17 +53,17 @@ namespace {
 constexpr float kTau = 8.0f;
 constexpr unsigned kErrLoad = 1u << 0;  // a wait for a stage gave up (the forward kernel's producer bit)
 
-template <int D, int NT, int RT>
+template <int D, int NT>
 struct QCfg {
-    static constexpr int TK = 4096 / D;                  // keys per unit: 8 KB of codes
-    static constexpr int TEAMS = kDecodeWarps / RT;
-    static constexpr int BLOCKS = NT == 1 ? 3 : 2;       // of an SM (registers)
-    static constexpr int NST = (NT == 1 ? 2 : 3) * RT;
-    static constexpr int AHEAD = RT == 1 ? NST - 1 : NST - 2;
-    static constexpr int HALF = TK * D;                  // bytes of K (or V) of a stage
+    static constexpr int TK = 4096 / D;             // keys per unit: 8 KB of codes
+    static constexpr int BLOCKS = NT == 1 ? 3 : 2;  // of an SM (registers)
+    static constexpr int NST = NT == 1 ? 2 : 3;     // stages of a warp
+    static constexpr int HALF = TK * D;             // bytes of K (or V) of a stage
     static constexpr int STAGE = 2 * HALF;
-    static constexpr int SCALE = 2 * TK;                 // floats of a stage: K's, V's
-    static constexpr int SMEM = TEAMS * NST * (STAGE + SCALE * 4) + 1024;
+    static constexpr int SCALE = 2 * TK;            // floats of a stage: K's, V's
+    static constexpr int TR = 8 * NT;               // query rows of an item
+    static constexpr int PER_WARP = NST * (STAGE + SCALE * 4);
+    static constexpr int SMEM = kDecodeWarps * PER_WARP + 1024;
 };
 
 // Place of a 16-byte chunk of a row of codes in its stage, as TMA's 128- and 64-byte swizzles
@@ -87,6 +92,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t at)
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
     return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 __device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b)
@@ -145,87 +155,47 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x)
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 
-template <int D, int DT, int CODE, int NT, int RT>
-__global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT, RT>::BLOCKS)
-    paged_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeParams p,
-                    const QuantArgs z, const int box_shift)
-{
-    using C = QCfg<D, NT, RT>;
-    constexpr int TK = C::TK, KM = TK / 16;  // key tiles of 16
-    const PagedArgs &a = p.a;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t s_sum[kDecodeWarps];
-    __shared__ int s_seq[C::TEAMS];
-    __shared__ uint64_t s_rel[C::TEAMS];
-    __shared__ __align__(8) uint64_t s_full[C::TEAMS * C::NST], s_empty[C::TEAMS * C::NST];
-    __shared__ int s_abort;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int team = warp / RT, mt = warp % RT;  // this warp has rows 8 NT mt .. 8 NT (mt + 1) - 1 of its team's items
-    unsigned int bad = 0;
-    pdl_launch();
-    if (tid == 0) {
-        for (int i = 0; i < C::TEAMS * C::NST; i++) {
-            mbar_init(smem_u32(&s_full[i]), 33);  // the bytes that TMA brings, and 32 lanes' scales
-            mbar_init(smem_u32(&s_empty[i]), RT);
-        }
-        s_abort = 0;
-        fence_mbar_init();
+// A warp's stages, and the fetching of units into them.
+template <int D, int NST, int TR>
+struct Loader {
+    static constexpr int TK = 4096 / D, KPL = TK / 32;  // keys per lane of the scales (of one page: it has at least 8)
+    Pos<TK, TR> ld;
+    uint32_t ring, scales, full;  // shared addresses: stages, their scales, their barriers
+    uint64_t pol;
+    uint32_t loads;
+    int stage, page, box_shift;
+
+    // Whether the lane has a TMA box of the unit at hand, and its page.  What the table holds
+    // is looked at when it is used (any number can stand there, so none can say that there
+    // is no key).
+    __device__ __forceinline__ bool has_box(int lane) const
+    {
+        return ld.left > 0 && lane < (TK >> box_shift) && ld.j * TK + (lane << box_shift) < ld.q.kv;
     }
-
-    const Runs runs = block_runs<TK, C::TEAMS>(p, s_sum, s_seq, s_rel, bad);
-    const int c = team * gridDim.x + blockIdx.x;  // this worker
-    if (lane == 0 && mt == 0) p.meta[c] = make_int4(0, 0, 0, 0);
-    if (bad && blockIdx.x == 0) atomicOr(&g_q8_error_word, bad);
-    bad = 0;
-    if (c >= runs.nb) {  // nothing for this team (U = 0 included)
-        pdl_wait();
-        return;
+    __device__ __forceinline__ void look_up(const PagedArgs &a, int lane)
+    {
+        page = has_box(lane) ? __ldg(a.block_table + ld.s * a.bt_s + ((ld.j * TK + (lane << box_shift)) >> a.page_shift)) : -1;
     }
-    const uint64_t u0 = decode_cut(runs.U, runs.nb, c), u1 = decode_cut(runs.U, runs.nb, c + 1);
-
-    Pos<TK> cur;
-    cur.set(a, s_seq[team]);
-    cur.h = static_cast<int>(div64(s_rel[team], cur.units));
-    cur.j = static_cast<int>(s_rel[team] - static_cast<uint64_t>(cur.h) * cur.units);
-    cur.left = static_cast<uint32_t>(u1 - u0);
-
-    // ---- the ring; the team's first warp fetches a unit per stage, AHEAD units before `cur`
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t ring = base + team * C::NST * C::STAGE;
-    const uint32_t ring_scales = base + C::TEAMS * C::NST * C::STAGE + team * C::NST * C::SCALE * 4;
-    const uint32_t full = smem_u32(&s_full[team * C::NST]), empty = smem_u32(&s_empty[team * C::NST]);
-    volatile int *ab = &s_abort;
-    constexpr int KPL = TK / 32;  // keys per lane of the scales (of one page: it has at least 8)
-    const int box = 1 << box_shift, boxes = TK >> box_shift;  // rows of a TMA box, boxes of a unit
-    const uint64_t pol = policy_evict_first();
-    Pos<TK> ld = cur;
-    int ld_stage = 0;
-    uint32_t ld_phase = 0, loads = 0;
-    // Page of the lane's box of the unit that is fetched next.  What the table holds is looked
-    // at when it is used (any number can stand there, so none can say that there is no key).
-    auto has_box = [&](const Pos<TK> &q) { return q.left > 0 && lane < boxes && q.j * TK + lane * box < q.q.kv; };
-    auto page_at = [&](const Pos<TK> &q) -> int {
-        return has_box(q) ? __ldg(a.block_table + q.s * a.bt_s + ((q.j * TK + lane * box) >> a.page_shift)) : -1;
-    };
-    int page = mt == 0 ? page_at(ld) : -1;
-    auto load_step = [&]() -> bool {  // (the team's first warp alone)
-        if (ld.left == 0) return true;
-        if (RT > 1 && loads >= C::NST)  // the stage's last unit has been read by all warps
-            if (!mbar_wait_warp(empty + 8 * ld_stage, ld_phase ^ 1, ab, &g_q8_error_word, kErrLoad)) return false;
-        const bool has = has_box(ld);
+    // The next unit of the run into the next stage, which has been read.
+    __device__ __forceinline__ void step(const CUtensorMap *tm_k, const CUtensorMap *tm_v, const DecodeParams &p, const QuantArgs &z,
+                                         int lane, unsigned int &bad)
+    {
+        const PagedArgs &a = p.a;
+        if (ld.left == 0) return;
+        const bool has = has_box(lane);
         if (has && (page < 0 || page >= a.num_pages)) {
             bad |= CLIS_PAGED_INDEX_BIT;
             page = static_cast<int>(a.num_pages);  // out of the map: its keys read as zeros
         }
-        const uint32_t bar = full + 8 * ld_stage;
+        const uint32_t bar = full + 8 * stage;
         const int live = __popc(__ballot_sync(~0u, has)), key0 = ld.j * TK;
         if (lane == 0) mbar_arrive_expect_tx(bar, live * 2 * (D << box_shift));
         __syncwarp();
         if (has) {
-            const uint32_t dst = ring + ld_stage * C::STAGE + lane * (D << box_shift);
-            const int row = (key0 + lane * box) & ((1 << a.page_shift) - 1);
-            tma_load_4d_hint(dst, &tm_k, bar, 0, row, ld.h, page, pol);
-            tma_load_4d_hint(dst + C::HALF, &tm_v, bar, 0, row, ld.h, page, pol);
+            const uint32_t dst = ring + stage * (2 * TK * D) + lane * (D << box_shift);
+            const int row = (key0 + (lane << box_shift)) & ((1 << a.page_shift) - 1);
+            tma_load_4d_hint(dst, tm_k, bar, 0, row, ld.h, page, pol);
+            tma_load_4d_hint(dst + TK * D, tm_v, bar, 0, row, ld.h, page, pol);
         }
         const int pg = __shfl_sync(~0u, page, (lane * KPL) >> box_shift);
 #pragma unroll
@@ -234,335 +204,274 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT, RT>::BLOCKS)
             const bool ok = key < ld.q.kv && pg < a.num_pages;
             const int64_t pi = ok ? pg : 0;
             const int in = ok ? key & ((1 << a.page_shift) - 1) : 0;
-            const uint32_t to = ring_scales + (ld_stage * C::SCALE + lane * KPL + i) * 4;
+            const uint32_t to = scales + (stage * (2 * TK) + lane * KPL + i) * 4;
             cp_async4(to, z.ks + pi * z.ks_sp + ld.h * z.ks_sh + in * z.ks_sn, ok ? 4 : 0);
             cp_async4(to + TK * 4, z.vs + pi * z.vs_sp + ld.h * z.vs_sh + in * z.vs_sn, ok ? 4 : 0);
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
         ++loads;
-        if (++ld_stage == C::NST) {
-            ld_stage = 0;
-            ld_phase ^= 1;
-        }
+        if (++stage == NST) stage = 0;
         ld.left--;
-        if (++ld.j == ld.units && ld.left > 0) ld.next_item(a, p.g, p.rows_max);
-        page = page_at(ld);
-        return true;
-    };
-    uint32_t done = 0;  // units read
-    bool fine = true;
-    if (mt == 0)
-#pragma unroll 1
-        for (int i = 0; i < C::AHEAD; i++) fine = fine && load_step();
+        if (++ld.j == ld.units && ld.left > 0) ld.next_item(a, p.g, p.limit);
+        look_up(a, lane);
+    }
+    // A wait gave up: the copies in flight end before the block does (or are given up too).
+    __device__ __forceinline__ void drain(uint32_t done)
+    {
+        for (uint32_t k = done; k < loads; k++) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(full + 8 * (k % NST), (k / NST) & 1) && globaltimer_ns() - t0 < 200000000ull) {
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+};
 
-    const int r4 = lane >> 2, t4 = lane & 3, c2 = t4 * 2;
-    const int key_mask = (1 << a.page_shift) - 1;
-    int stage = 0;
-    uint32_t phase = 0;
+// The query rows of a warp: rows row0 + 8 nt + r of the item.  A thread loads row
+// 8 nt + lane / 4 and keeps what belongs to the columns 2 (lane % 4), + 1 of its products.
+template <int D, int NT>
+struct Rows {
+    uint32_t qf[NT][D / 16][2];
+    float2 cs[NT];   // scale_log2 over the power of two that q's row was multiplied by
+    float2 m[NT], l[NT], low[NT];  // low: what the last addition to l gained by rounding
+    float2 e[NT], f[NT];           // the weights of V: exponent, and 2^exponent
+    float o[D / 16][NT][4];        // d = 16 i + 2 (lane / 4) of two rows, then d + 1 of them
 
-    while (fine && cur.left > 0) {
-        // ---- one item, units j0 .. j1 - 1 of it
-        const int j0 = cur.j;
-        const int j1 = static_cast<int>(min(static_cast<uint32_t>(cur.units), j0 + cur.left));
-        const int n = cur.q.n, kv = cur.q.kv, R = n * p.g, q0 = cur.q.q0;
-        const int lim0 = visible_keys(n, kv, 0, a.causal);  // keys that every row sees
-        const int row0 = mt * 8 * NT;
-        const bool live = row0 < R;  // (the team's barriers are met either way)
-
-        // q's row r4 of each column tile: word w of thread t4 holds elements 16 t4 + 4 w ..
-        // (w < 4) or 64 + 16 t4 + 4 (w - 4) .. of d.
-        uint32_t qf[NT][D / 16][2];
-        float2 cs[NT];     // of rows c2, c2 + 1: scale_log2 over the power of two that q's row was multiplied by
-        int lim[NT][2];
+    // Word w of thread t holds elements 16 t + 4 w .. (w < 4) or 64 + 16 t + 4 (w - 4) .. of d,
+    // as the loads of codes do.
+    template <int DT>
+    __device__ __forceinline__ void load(const DecodeParams &p, const SeqLen &q, int head, int row0, int lane)
+    {
+        const PagedArgs &a = p.a;
+        const int R = q.n * p.g, r4 = lane >> 2, t4 = lane & 3;
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
             const int row = row0 + nt * 8 + r4;
             const bool ok = row < R;
-            const int tok = ok ? row / p.g : 0, hd = cur.h * p.g + (ok ? row - tok * p.g : 0);
-            const uint16_t *src = a.q + static_cast<int64_t>(q0 + tok) * a.q_st + hd * a.q_sh + t4 * 16;
-            uint32_t top = 0;  // the row's largest magnitude: bits of non-negative floats are ordered
+            const int tok = ok ? row / p.g : 0, hd = head * p.g + (ok ? row - tok * p.g : 0);
+            const uint16_t *src = a.q + static_cast<int64_t>(q.q0 + tok) * a.q_st + hd * a.q_sh;
 #pragma unroll
             for (int w = 0; w < D / 16; w += 2) {
-                const uint4 v = ok ? __ldg(reinterpret_cast<const uint4 *>(src + (w >> 2) * 64 + (w & 3) * 4)) : make_uint4(0, 0, 0, 0);
+                const uint4 v = ok ? __ldg(reinterpret_cast<const uint4 *>(src + t4 * 16 + (w >> 2) * 64 + (w & 3) * 4)) : make_uint4(0, 0, 0, 0);
                 qf[nt][w][0] = v.x;
                 qf[nt][w][1] = v.y;
                 qf[nt][w + 1][0] = v.z;
                 qf[nt][w + 1][1] = v.w;
             }
+            uint32_t top = 0;  // the row's largest magnitude: bits of non-negative floats are ordered
 #pragma unroll
             for (int w = 0; w < D / 16; w++)
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    top = max(top, __float_as_uint(elem_lo<DT>(qf[nt][w][e])) & 0x7FFFFFFFu);
-                    top = max(top, __float_as_uint(elem_hi<DT>(qf[nt][w][e])) & 0x7FFFFFFFu);
+                for (int h = 0; h < 2; h++) {
+                    top = max(top, __float_as_uint(elem_lo<DT>(qf[nt][w][h])) & 0x7FFFFFFFu);
+                    top = max(top, __float_as_uint(elem_hi<DT>(qf[nt][w][h])) & 0x7FFFFFFFu);
                 }
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
             // (a row of zeros or with something non-finite is taken as it is)
-            const int e = top == 0 || top >= 0x7F800000u ? 0 : min(14 - (static_cast<int>(top >> 23) - 127), 126);
-            const float f = exp2_int(e), s1 = a.scale_log2 * exp2_int(-e);
+            const int ex = top == 0 || top >= 0x7F800000u ? 0 : min(14 - (static_cast<int>(top >> 23) - 127), 126);
+            const float by = exp2_int(ex), s1 = a.scale_log2 * exp2_int(-ex);
 #pragma unroll
             for (int w = 0; w < D / 16; w++)
 #pragma unroll
                 for (int h = 0; h < 2; h++)
-                    qf[nt][w][h] = pack2<1>(elem_lo<DT>(qf[nt][w][h]) * f, elem_hi<DT>(qf[nt][w][h]) * f);
-            cs[nt] = make_float2(__shfl_sync(~0u, s1, c2 * 4), __shfl_sync(~0u, s1, c2 * 4 + 4));
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int r = row0 + nt * 8 + c2 + h;
-                lim[nt][h] = r < R ? visible_keys(n, kv, r / p.g, a.causal) : 0;
-            }
-        }
-        // o[i][nt]: d = 16 i + 2 r4 of rows c2, c2 + 1, then d + 1 of them.
-        float o[D / 16][NT][4];
-        float2 m_run[NT], l_run[NT], l_low[NT];  // l_low: what the last addition to l_run gained by rounding
-        float2 ev[NT], fv[NT];                   // the weights of V: exponent and factor 2^exponent
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-            m_run[nt] = ev[nt] = make_float2(-INFINITY, -INFINITY);
-            l_run[nt] = l_low[nt] = fv[nt] = make_float2(0.f, 0.f);
+                    qf[nt][w][h] = pack2<1>(elem_lo<DT>(qf[nt][w][h]) * by, elem_hi<DT>(qf[nt][w][h]) * by);
+            cs[nt] = make_float2(__shfl_sync(~0u, s1, t4 * 8), __shfl_sync(~0u, s1, t4 * 8 + 4));
+            m[nt] = e[nt] = make_float2(-INFINITY, -INFINITY);
+            l[nt] = low[nt] = f[nt] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < D / 16; i++) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
         }
-        bool dirty = false;
+    }
 
-#pragma unroll 1
-        for (int j = j0; j < j1; j++) {
-            __syncwarp();
-            if (mt == 0 && !load_step()) {  // (RT = 1: into the stage that the previous unit has been read from)
-                fine = false;
-                break;
-            }
-            if (!mbar_wait_warp(full + 8 * stage, phase, ab, &g_q8_error_word, kErrLoad)) {
-                fine = false;
-                break;
-            }
-            ++done;
-            const int key0 = j * TK;
-            const uint32_t sK = ring + stage * C::STAGE, sV = sK + C::HALF;
-            const uint32_t sS = ring_scales + stage * C::SCALE * 4;
-            const uint32_t freed = empty + 8 * stage;
-            if (++stage == C::NST) {
-                stage = 0;
-                phase ^= 1;
-            }
-            if (key0 < kv && live) {
-                // S^T = KC Q^T: TK keys x 8 rows per column tile
-                float s[KM][NT][4];
+    // Keys that row 8 nt + 2 (lane % 4) + h sees.
+    static __device__ __forceinline__ int limit(const DecodeParams &p, const SeqLen &q, int row0, int nt, int h, int lane)
+    {
+        const int r = row0 + nt * 8 + 2 * (lane & 3) + h;
+        return r < q.n * p.g ? visible_keys(q.n, q.kv, r / p.g, p.a.causal) : 0;
+    }
+
+    // Products of a unit's codes, s[km][nt][0], [1]: key 16 km + lane / 4 and two rows, [2], [3]:
+    // 8 keys on, into the weights of V's codes, wf: two keys' of row lane / 4.
+    // sS: the unit's scales.
+    // EDGE: some row does not see some key.  (A constant: as a condition at each score it
+    // was a branch there.)
+    template <bool EDGE, int KM>
+    __device__ __forceinline__ void weights(const DecodeParams &p, const SeqLen &q, int row0, float (&s)[KM][NT][4], uint32_t sS, int key0,
+                                            int lane, uint32_t (&wf)[KM][NT][2])
+    {
+        constexpr int TK = KM * 16;
+        const int r4 = lane >> 2;
+        if (EDGE) {  // (before the scales, which may be no numbers: below)
 #pragma unroll
-                for (int km = 0; km < KM; km++)
+            for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++) s[km][nt][0] = s[km][nt][1] = s[km][nt][2] = s[km][nt][3] = 0.f;
-#pragma unroll
-                for (int hh = 0; hh < D / 64; hh++)
-#pragma unroll
-                    for (int k0 = 0; k0 < KM; k0 += 2) {
-                        uint4 kw[2][2];
-#pragma unroll
-                        for (int i = 0; i < 2; i++)
-#pragma unroll
-                            for (int h = 0; h < 2; h++) kw[i][h] = lds128(sK + at_row<D>((k0 + i) * 16 + h * 8 + r4, hh * 4 + t4));
-#pragma unroll
-                        for (int w = 0; w < 4; w++)
-#pragma unroll
-                            for (int i = 0; i < 2; i++) {
-                                uint32_t f[4];
-                                unpack<CODE, false>(w == 0 ? kw[i][0].x : w == 1 ? kw[i][0].y : w == 2 ? kw[i][0].z : kw[i][0].w, f[0], f[2]);
-                                unpack<CODE, false>(w == 0 ? kw[i][1].x : w == 1 ? kw[i][1].y : w == 2 ? kw[i][1].z : kw[i][1].w, f[1], f[3]);
-#pragma unroll
-                                for (int nt = 0; nt < NT; nt++)
-                                    mma16816<1>(s[k0 + i][nt], f, qf[nt][hh * 4 + w][0], qf[nt][hh * 4 + w][1]);
-                            }
-                    }
-                // The scores' scales, masks and maxima (s[.][.][0], [1]: key r4, rows c2 and c2 + 1;
-                // [2], [3]: key r4 + 8).
-                const bool edge = key0 + TK > lim0;  // some row does not see some key
-                float vs[KM][2];
-                float2 mx[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) mx[nt] = make_float2(-INFINITY, -INFINITY);
-#pragma unroll
-                for (int km = 0; km < KM; km++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const int kr = km * 16 + h * 8 + r4;
-                        const float ks = lds32(sS + kr * 4);
-                        vs[km][h] = lds32(sS + (TK + kr) * 4);
-#pragma unroll
-                        for (int nt = 0; nt < NT; nt++) {
-                            float2 x = fmul2(make_float2(s[km][nt][2 * h], s[km][nt][2 * h + 1]), make_float2(ks, ks));
-                            if (edge) {
-                                if (key0 + kr >= lim[nt][0]) x.x = -INFINITY;
-                                if (key0 + kr >= lim[nt][1]) x.y = -INFINITY;
-                            }
-                            s[km][nt][2 * h] = x.x;
-                            s[km][nt][2 * h + 1] = x.y;
-                            mx[nt].x = fmaxf(mx[nt].x, x.x);
-                            mx[nt].y = fmaxf(mx[nt].y, x.y);
-                        }
-                    }
-                bool grow = false;
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    mx[nt] = fmul2(mx[nt], cs[nt]);
-                    grow |= mx[nt].x > m_run[nt].x + kTau || mx[nt].y > m_run[nt].y + kTau;
-                }
-                if (__any_sync(~0u, grow)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++) {
-                        auto raise = [&](float v, float &m, float &l, float &low, float &e, float &f) {
-                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
-                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
-                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-                            if (!(v > m + kTau)) return;
-                            const float al = ex2_approx(m - v);
-                            l *= al;
-                            low *= al;
-                            if (m != -INFINITY) {  // w stays what it was
-                                e += v - m;
-                                f = ex2_approx(fminf(e, 100.f));
-                            }
-                            m = v;
-                        };
-                        raise(mx[nt].x, m_run[nt].x, l_run[nt].x, l_low[nt].x, ev[nt].x, fv[nt].x);
-                        raise(mx[nt].y, m_run[nt].y, l_run[nt].y, l_low[nt].y, ev[nt].y, fv[nt].y);
-                    }
-                }
-                // p, its sum, and p times V's scale
-                grow = false;
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    const float2 ns = make_float2(m_run[nt].x == -INFINITY ? 0.f : -m_run[nt].x, m_run[nt].y == -INFINITY ? 0.f : -m_run[nt].y);
-                    float2 l = make_float2(0.f, 0.f), tx = l;
+                for (int h = 0; h < 2; h++) {
+                    const int lim = limit(p, q, row0, nt, h, lane);
 #pragma unroll
                     for (int km = 0; km < KM; km++)
 #pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const float2 x = ffma2(make_float2(s[km][nt][2 * h], s[km][nt][2 * h + 1]), cs[nt], ns);
-                            const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                            l = fadd2(l, pp);
-                            float2 t = fmul2(pp, make_float2(vs[km][h], vs[km][h]));
-                            if (edge) {  // (a scale that is no number must not reach a row that does not see its key)
-                                if (s[km][nt][2 * h] == -INFINITY) t.x = 0.f;
-                                if (s[km][nt][2 * h + 1] == -INFINITY) t.y = 0.f;
-                            }
-                            s[km][nt][2 * h] = t.x;
-                            s[km][nt][2 * h + 1] = t.y;
-                            tx.x = fmaxf(tx.x, t.x);
-                            tx.y = fmaxf(tx.y, t.y);
-                        }
-                    // Compensated: a run may be many thousands of units, each far below the sum.
-                    const float2 minus = make_float2(-1.f, -1.f);
-                    const float2 y = ffma2(l_low[nt], minus, l), t = fadd2(l_run[nt], y);
-                    l_low[nt] = ffma2(y, minus, ffma2(l_run[nt], minus, t));
-                    l_run[nt] = t;
-                    mx[nt] = tx;
-                    const float2 g = fmul2(tx, fv[nt]);
-                    grow |= g.x > 32768.f || g.y > 32768.f || (ev[nt].x == -INFINITY && tx.x > 0.f) || (ev[nt].y == -INFINITY && tx.y > 0.f) ||
-                            ev[nt].x > 100.f || ev[nt].y > 100.f;
+                        for (int b = 0; b < 2; b++)
+                            if (key0 + km * 16 + b * 8 + r4 >= lim) s[km][nt][2 * b + h] = -INFINITY;
                 }
-                if (__any_sync(~0u, grow)) {
+        }
+        float vs[KM][2];
+        float2 mx[NT];
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++) {
-                        auto lower = [&](float v, float &e, float &f, int h) {
-                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
-                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
-                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-                            const bool none = e == -INFINITY;
-                            float to = fminf(e, 100.f);
-                            if (v > 0.f && (none || v * ex2_approx(to) > 32768.f)) {
-                                const int x = static_cast<int>(__float_as_uint(v) >> 23) - 127;
-                                to = static_cast<float>(max(-100, min(100, 7 - x)));
-                            }
-                            if (to == e || v == 0.f && none) return;
-                            const float al = none ? 0.f : ex2_approx(to - e);
-                            e = to;
-                            f = ex2_approx(to);
+        for (int nt = 0; nt < NT; nt++) mx[nt] = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-                            for (int i = 0; i < D / 16; i++) {
-                                o[i][nt][h] *= al;
-                                o[i][nt][2 + h] *= al;
-                            }
-                        };
-                        lower(mx[nt].x, ev[nt].x, fv[nt].x, 0);
-                        lower(mx[nt].y, ev[nt].y, fv[nt].y, 1);
+        for (int km = 0; km < KM; km++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int kr = km * 16 + h * 8 + r4;
+                const float ks = lds32(sS + kr * 4);
+                vs[km][h] = lds32(sS + (TK + kr) * 4);
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    float2 x = fmul2(make_float2(s[km][nt][2 * h], s[km][nt][2 * h + 1]), make_float2(ks, ks));
+                    if (EDGE) {
+                        if (s[km][nt][2 * h] == -INFINITY) x.x = -INFINITY;
+                        if (s[km][nt][2 * h + 1] == -INFINITY) x.y = -INFINITY;
                     }
-                }
-                uint32_t wf[KM][NT][2];
-#pragma unroll
-                for (int km = 0; km < KM; km++)
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const float2 w = fmul2(make_float2(s[km][nt][2 * h], s[km][nt][2 * h + 1]), fv[nt]);
-                            wf[km][nt][h] = transposed(pack2<1>(w.x, w.y));
-                        }
-                // O^T += VC^T W^T: a transposed load gives 32 keys of 16 columns, in each word the
-                // codes of two neighbouring columns and two neighbouring keys.
-                auto pv = [&](bool clean) {
-#pragma unroll
-                    for (int k0 = 0; k0 < KM; k0 += 2)
-#pragma unroll
-                        for (int i = 0; i < D / 16; i++) {
-                            uint32_t vw[4], f[2][4];
-                            ldsm4_t(sV + at_row<D>(k0 * 16 + lane, i), vw);
-#pragma unroll
-                            for (int e = 0; e < 4; e++) unpack<CODE, true>(vw[e], f[e >> 1][2 * (e & 1)], f[e >> 1][2 * (e & 1) + 1]);
-                            if (CODE != CLIS_CODE_INT8 && clean)
-#pragma unroll
-                                for (int e = 0; e < 8; e++) f[e >> 2][e & 3] = no_nan(f[e >> 2][e & 3]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; nt++) {
-                                mma16816<1>(o[i][nt], f[0], wf[k0][nt][0], wf[k0][nt][1]);
-                                mma16816<1>(o[i][nt], f[1], wf[k0 + 1][nt][0], wf[k0 + 1][nt][1]);
-                            }
-                        }
-                };
-                // Where a key is masked for some rows, or the stage's rows behind the last key hold
-                // whatever was there, a NaN code must not reach the output as 0 * NaN: it takes part as a
-                // number, and the rows that see it get a NaN at the end.
-                if (CODE != CLIS_CODE_INT8 && edge) {
-#pragma unroll 1
-                    for (int i = lane; i < C::HALF / 16; i += 32) {
-                        const uint4 u = lds128(sV + i * 16);
-                        dirty |= has_nan(u.x) || has_nan(u.y) || has_nan(u.z) || has_nan(u.w);
-                    }
-                    pv(true);
-                } else {
-                    pv(false);
+                    s[km][nt][2 * h] = x.x;
+                    s[km][nt][2 * h + 1] = x.y;
+                    mx[nt].x = fmaxf(mx[nt].x, x.x);
+                    mx[nt].y = fmaxf(mx[nt].y, x.y);
                 }
             }
-            if (RT > 1) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(freed);
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            mx[nt] = fmul2(mx[nt], cs[nt]);
+            grow |= mx[nt].x > m[nt].x + kTau || mx[nt].y > m[nt].y + kTau;
+        }
+        if (__any_sync(~0u, grow)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+                raise(mx[nt].x, m[nt].x, l[nt].x, low[nt].x, e[nt].x, f[nt].x);
+                raise(mx[nt].y, m[nt].y, l[nt].y, low[nt].y, e[nt].y, f[nt].y);
             }
         }
-        if (!fine) break;
+        // p, its sum, and p times V's scale
+        grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            const float2 ns = make_float2(m[nt].x == -INFINITY ? 0.f : -m[nt].x, m[nt].y == -INFINITY ? 0.f : -m[nt].y);
+            float2 sum = make_float2(0.f, 0.f), tx = sum;
+#pragma unroll
+            for (int km = 0; km < KM; km++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float2 x = ffma2(make_float2(s[km][nt][2 * h], s[km][nt][2 * h + 1]), cs[nt], ns);
+                    const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                    sum = fadd2(sum, pp);
+                    float2 t = fmul2(pp, make_float2(vs[km][h], vs[km][h]));
+                    if (EDGE) {  // (a scale that is no number must not reach a row that does not see its key)
+                        if (s[km][nt][2 * h] == -INFINITY) t.x = 0.f;
+                        if (s[km][nt][2 * h + 1] == -INFINITY) t.y = 0.f;
+                    }
+                    s[km][nt][2 * h] = t.x;
+                    s[km][nt][2 * h + 1] = t.y;
+                    tx.x = fmaxf(tx.x, t.x);
+                    tx.y = fmaxf(tx.y, t.y);
+                }
+            // Compensated: a run may be many thousands of units, each far below the sum.
+            const float2 minus = make_float2(-1.f, -1.f);
+            const float2 y = ffma2(low[nt], minus, sum), t = fadd2(l[nt], y);
+            low[nt] = ffma2(y, minus, ffma2(l[nt], minus, t));
+            l[nt] = t;
+            mx[nt] = tx;
+            const float2 g = fmul2(tx, f[nt]);
+            grow |= g.x > 32768.f || g.y > 32768.f || (e[nt].x == -INFINITY && tx.x > 0.f) || (e[nt].y == -INFINITY && tx.y > 0.f) ||
+                    e[nt].x > 100.f || e[nt].y > 100.f;
+        }
+        if (__any_sync(~0u, grow)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+                lower(mx[nt].x, e[nt].x, f[nt].x, nt, 0);
+                lower(mx[nt].y, e[nt].y, f[nt].y, nt, 1);
+            }
+        }
+#pragma unroll
+        for (int km = 0; km < KM; km++)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float2 w = fmul2(make_float2(s[km][nt][2 * h], s[km][nt][2 * h + 1]), f[nt]);
+                    wf[km][nt][h] = transposed(pack2<1>(w.x, w.y));
+                }
+    }
 
-        // ---- write the rows: final, or partial
-        const bool any_dirty = __any_sync(~0u, dirty);
-        const bool whole = j0 == 0 && j1 == cur.units;
-        const int64_t slot = 2 * static_cast<int64_t>(c) + (j0 == 0 ? 1 : 0);
+    // The largest over the lanes that share a row.
+    static __device__ __forceinline__ float row_max(float v)
+    {
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+        return fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+    }
+
+    static __device__ __forceinline__ void raise(float v, float &m, float &l, float &low, float &e, float &f)
+    {
+        v = row_max(v);
+        if (!(v > m + kTau)) return;
+        const float al = ex2_approx(m - v);
+        l *= al;
+        low *= al;
+        if (m != -INFINITY) {  // w stays what it was
+            e += v - m;
+            f = ex2_approx(fminf(e, 100.f));
+        }
+        m = v;
+    }
+
+    __device__ __forceinline__ void lower(float v, float &e, float &f, int nt, int h)
+    {
+        v = row_max(v);
+        const bool none = e == -INFINITY;
+        float to = fminf(e, 100.f);
+        if (v > 0.f && (none || v * ex2_approx(to) > 32768.f)) {
+            const int x = static_cast<int>(__float_as_uint(v) >> 23) - 127;
+            to = static_cast<float>(max(-100, min(100, 7 - x)));
+        }
+        if (to == e) return;
+        const float al = none ? 0.f : ex2_approx(to - e);
+        e = to;
+        f = ex2_approx(to);
+#pragma unroll
+        for (int i = 0; i < D / 16; i++) {
+            o[i][nt][h] *= al;
+            o[i][nt][2 + h] *= al;
+        }
+    }
+
+    // The item's rows, final (slot < 0) or partial.  nan_from >= 0: E4M3 codes of V that are NaN and
+    // lie at keys [nan_from, nan_to) took part as numbers; rows that see them become NaN.
+    template <int DT>
+    __device__ __forceinline__ void write(const DecodeParams &p, const QuantArgs &z, const SeqLen &q, int s, int head, int row0, int64_t slot,
+                                          int nan_from, int nan_to, int lane)
+    {
+        const PagedArgs &a = p.a;
+        const int R = q.n * p.g, r4 = lane >> 2, c2 = 2 * (lane & 3);
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const int row = row0 + nt * 8 + c2 + h;
-                float l = h ? l_run[nt].y : l_run[nt].x;
-                l += __shfl_xor_sync(~0u, l, 4);
-                l += __shfl_xor_sync(~0u, l, 8);
-                l += __shfl_xor_sync(~0u, l, 16);
+                float sum = h ? l[nt].y : l[nt].x;
+                sum += __shfl_xor_sync(~0u, sum, 4);
+                sum += __shfl_xor_sync(~0u, sum, 8);
+                sum += __shfl_xor_sync(~0u, sum, 16);
                 if (row >= R) continue;
-                const int tok = row / p.g, hd = cur.h * p.g + (row - tok * p.g);
-                if (CODE != CLIS_CODE_INT8 && any_dirty) {
-                    const int see = min(lim[nt][h], j1 * TK);
+                const int tok = row / p.g, hd = head * p.g + (row - tok * p.g);
+                if (nan_from >= 0) {
+                    const int see = min(limit(p, q, row0, nt, h, lane), nan_to);
 #pragma unroll 1
-                    for (int key = max(lim0 / TK * TK, j0 * TK); key < see; key++) {
-                        const int pg = __ldg(a.block_table + cur.s * a.bt_s + (key >> a.page_shift));
+                    for (int key = nan_from; key < see; key++) {
+                        const int pg = __ldg(a.block_table + s * a.bt_s + (key >> a.page_shift));
                         if (pg < 0 || pg >= a.num_pages) continue;
-                        const uint8_t *v = z.vc + static_cast<int64_t>(pg) * a.vc_sp + cur.h * a.vc_sh +
-                                           static_cast<int64_t>(key & key_mask) * a.vc_sn + 2 * r4;
+                        const uint8_t *v = z.vc + static_cast<int64_t>(pg) * a.vc_sp + head * a.vc_sh +
+                                           static_cast<int64_t>(key & ((1 << a.page_shift) - 1)) * a.vc_sn + 2 * r4;
 #pragma unroll
                         for (int i = 0; i < D / 16; i++) {
                             const uint32_t u = __ldg(reinterpret_cast<const unsigned short *>(v + i * 16));
@@ -571,41 +480,186 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT, RT>::BLOCKS)
                         }
                     }
                 }
-                const float m = h ? m_run[nt].y : m_run[nt].x, e = h ? ev[nt].y : ev[nt].x;
-                const float back = e == -INFINITY ? 0.f : ex2_approx(-e);  // (O is 0 then)
-                if (whole) {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    uint16_t *dst = a.o + static_cast<int64_t>(q0 + tok) * a.o_st + hd * a.o_sh + 2 * r4;
+                const float mm = h ? m[nt].y : m[nt].x, ee = h ? e[nt].y : e[nt].x;
+                const float back = ee == -INFINITY ? 0.f : ex2_approx(-ee);  // (O is 0 then)
+                if (slot < 0) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    uint16_t *dst = a.o + static_cast<int64_t>(q.q0 + tok) * a.o_st + hd * a.o_sh + 2 * r4;
 #pragma unroll
                     for (int i = 0; i < D / 16; i++)  // (zeros for a row that sees no key)
                         *reinterpret_cast<uint32_t *>(dst + i * 16) =
-                            l == 0.f ? 0u : pack2<DT>(o[i][nt][h] * back * inv, o[i][nt][2 + h] * back * inv);
-                    if (r4 == 0 && a.lse2) a.lse2[static_cast<int64_t>(q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : m + log2f(l);
+                            sum == 0.f ? 0u : pack2<DT>(o[i][nt][h] * back * inv, o[i][nt][2 + h] * back * inv);
+                    if (r4 == 0 && a.lse2) a.lse2[static_cast<int64_t>(q.q0 + tok) * a.H + hd] = sum == 0.f ? -INFINITY : mm + log2f(sum);
                 } else {
-                    float *dst = p.part_o + (slot * p.rows_max + row) * D + 2 * r4;
+                    float *dst = p.part_o + (slot * p.rows_max + row - row0) * D + 2 * r4;
 #pragma unroll
                     for (int i = 0; i < D / 16; i++)
                         *reinterpret_cast<float2 *>(dst + i * 16) = make_float2(o[i][nt][h] * back, o[i][nt][2 + h] * back);
-                    if (r4 == 0) p.part_ml[slot * p.rows_max + row] = make_float2(m, l);
+                    if (r4 == 0) p.part_ml[slot * p.rows_max + row - row0] = make_float2(mm, sum);
                 }
             }
-        if (!whole && j0 == 0 && lane == 0 && mt == 0) {
-            const uint64_t end = u1 - cur.left + cur.units - 1;  // the item's last unit
-            p.meta[c] = make_int4(item_parts(runs, c, end), q0, n, cur.h);
-        }
-        cur.left -= j1 - j0;
-        cur.j = j1;
-        if (cur.left > 0) cur.next_item(a, p.g, p.rows_max);
     }
-    if (!fine && mt == 0) {
-        // A wait gave up: the copies in flight end before the block does (or are given up too).
-        for (uint32_t k = done; k < loads; k++) {
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(full + 8 * (k % C::NST), (k / C::NST) & 1) && globaltimer_ns() - t0 < 200000000ull) {
+};
+
+template <int D, int DT, int CODE, int NT>
+__global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
+    paged_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeParams p,
+                    const QuantArgs z, const int box_shift)
+{
+    using C = QCfg<D, NT>;
+    constexpr int TK = C::TK, KM = TK / 16;  // key tiles of 16
+    const PagedArgs &a = p.a;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t s_sum[kDecodeWarps], s_rel[kDecodeWarps];
+    __shared__ int s_seq[kDecodeWarps];
+    __shared__ __align__(8) uint64_t s_full[kDecodeWarps * C::NST];
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned int bad = 0;
+    pdl_launch();
+    if (tid == 0) {
+        for (int i = 0; i < kDecodeWarps * C::NST; i++) mbar_init(smem_u32(&s_full[i]), 33);  // TMA's bytes, and 32 lanes' scales
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    const Runs runs = block_runs<TK, kDecodeWarps, C::TR>(p, s_sum, s_seq, s_rel, bad);
+    const int c = warp * gridDim.x + blockIdx.x;  // this worker
+    if (lane == 0) p.meta[c] = make_int4(0, 0, 0, 0);
+    if (bad && blockIdx.x == 0) atomicOr(&g_q8_error_word, bad);
+    bad = 0;
+    if (c >= runs.nb) {  // nothing for this warp (U = 0 included)
+        pdl_wait();
+        return;
+    }
+    const uint64_t u1 = decode_cut(runs.U, runs.nb, c + 1);
+    Pos<TK, C::TR> cur;
+    cur.set(a, s_seq[warp], p.g);
+    const int item = static_cast<int>(div64(s_rel[warp], cur.units));
+    cur.h = item / cur.tiles;
+    cur.tile = item - cur.h * cur.tiles;
+    cur.j = static_cast<int>(s_rel[warp] - static_cast<uint64_t>(item) * cur.units);
+    cur.left = static_cast<uint32_t>(u1 - decode_cut(runs.U, runs.nb, c));
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    Loader<D, C::NST, C::TR> load;
+    load.ld = cur;
+    load.ring = base + warp * C::NST * C::STAGE;
+    load.scales = base + kDecodeWarps * C::NST * C::STAGE + warp * C::NST * C::SCALE * 4;
+    load.full = smem_u32(&s_full[warp * C::NST]);
+    load.pol = policy_evict_first();
+    load.loads = load.stage = 0;
+    load.box_shift = box_shift;
+    load.look_up(a, lane);
+#pragma unroll 1
+    for (int i = 0; i < C::NST - 1; i++) load.step(&tm_k, &tm_v, p, z, lane, bad);
+
+    const int r4 = lane >> 2, t4 = lane & 3;
+    uint32_t done = 0, phase = 0;  // units read
+    int stage = 0;
+    bool fine = true;
+    Rows<D, NT> w;
+    while (fine && cur.left > 0) {
+        // ---- one item, units j0 .. j1 - 1 of it
+        const int j0 = cur.j;
+        const int j1 = static_cast<int>(min(static_cast<uint32_t>(cur.units), j0 + cur.left));
+        const int kv = cur.q.kv, lim0 = visible_keys(cur.q.n, kv, 0, a.causal);  // keys that every row sees
+        const int row0 = cur.tile * C::TR;
+        w.template load<DT>(p, cur.q, cur.h, row0, lane);
+        bool dirty = false;
+#pragma unroll 1
+        for (int j = j0; j < j1; j++) {
+            __syncwarp();
+            load.step(&tm_k, &tm_v, p, z, lane, bad);  // into the stage that the previous unit has been read from
+            if (!mbar_wait_warp(load.full + 8 * stage, phase, &s_abort, &g_q8_error_word, kErrLoad)) {
+                fine = false;
+                break;
+            }
+            ++done;
+            const int key0 = j * TK;
+            const uint32_t sK = load.ring + stage * C::STAGE, sV = sK + C::HALF;
+            const uint32_t sS = load.scales + stage * C::SCALE * 4;
+            if (++stage == C::NST) {
+                stage = 0;
+                phase ^= 1;
+            }
+            if (key0 >= kv) continue;
+            // S^T = KC Q^T: TK keys x 8 rows per column tile
+            float s[KM][NT][4];
+#pragma unroll
+            for (int km = 0; km < KM; km++)
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) s[km][nt][0] = s[km][nt][1] = s[km][nt][2] = s[km][nt][3] = 0.f;
+#pragma unroll
+            for (int hh = 0; hh < D / 64; hh++)
+#pragma unroll
+                for (int k0 = 0; k0 < KM; k0 += 2) {
+                    uint4 kw[2][2];
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) kw[i][h] = lds128(sK + at_row<D>((k0 + i) * 16 + h * 8 + r4, hh * 4 + t4));
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            uint32_t f[4];
+                            unpack<CODE, false>(x == 0 ? kw[i][0].x : x == 1 ? kw[i][0].y : x == 2 ? kw[i][0].z : kw[i][0].w, f[0], f[2]);
+                            unpack<CODE, false>(x == 0 ? kw[i][1].x : x == 1 ? kw[i][1].y : x == 2 ? kw[i][1].z : kw[i][1].w, f[1], f[3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; nt++)
+                                mma16816<1>(s[k0 + i][nt], f, w.qf[nt][hh * 4 + x][0], w.qf[nt][hh * 4 + x][1]);
+                        }
+                }
+            const bool edge = key0 + TK > lim0;  // some row does not see some key
+            uint32_t wf[KM][NT][2];
+            if (edge) w.template weights<true, KM>(p, cur.q, row0, s, sS, key0, lane, wf);
+            else w.template weights<false, KM>(p, cur.q, row0, s, sS, key0, lane, wf);
+            // O^T += VC^T W^T: a transposed load gives 32 keys of 16 columns, in each word the
+            // codes of two neighbouring columns and two neighbouring keys.
+            auto pv = [&](bool clean) {
+#pragma unroll
+                for (int k0 = 0; k0 < KM; k0 += 2)
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++) {
+                        uint32_t vw[4], f[2][4];
+                        ldsm4_t(sV + at_row<D>(k0 * 16 + lane, i), vw);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) unpack<CODE, true>(vw[e], f[e >> 1][2 * (e & 1)], f[e >> 1][2 * (e & 1) + 1]);
+                        if (CODE != CLIS_CODE_INT8 && clean)
+#pragma unroll
+                            for (int e = 0; e < 8; e++) f[e >> 2][e & 3] = no_nan(f[e >> 2][e & 3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++) {
+                            mma16816<1>(w.o[i][nt], f[0], wf[k0][nt][0], wf[k0][nt][1]);
+                            mma16816<1>(w.o[i][nt], f[1], wf[k0 + 1][nt][0], wf[k0 + 1][nt][1]);
+                        }
+                    }
+            };
+            // Where a key is masked for some rows, or the stage's rows behind the last key hold
+            // whatever was there, a NaN code must not reach the output as 0 * NaN: it takes part as a
+            // number, and the rows that see it get a NaN at the end.
+            if (CODE != CLIS_CODE_INT8 && edge) {
+#pragma unroll 1
+                for (int i = lane; i < C::HALF / 16; i += 32) {
+                    const uint4 u = lds128(sV + i * 16);
+                    dirty |= has_nan(u.x) || has_nan(u.y) || has_nan(u.z) || has_nan(u.w);
+                }
+                pv(true);
+            } else {
+                pv(false);
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!fine) break;
+        const bool any_dirty = CODE != CLIS_CODE_INT8 && __any_sync(~0u, dirty);
+        const bool whole = j0 == 0 && j1 == cur.units;
+        w.template write<DT>(p, z, cur.q, cur.s, cur.h, row0, whole ? -1 : 2 * static_cast<int64_t>(c) + (j0 == 0 ? 1 : 0),
+                             any_dirty ? max(lim0 / TK * TK, j0 * TK) : -1, j1 * TK, lane);
+        if (!whole && j0 == 0 && lane == 0)
+            p.meta[c] = make_int4(item_parts(runs, c, u1 - cur.left + cur.units - 1), cur.q.q0, cur.q.n | row0 << 16, cur.h);
+        cur.left -= j1 - j0;
+        cur.j = j1;
+        if (cur.left > 0) cur.next_item(a, p.g, p.limit);
     }
+    if (!fine) load.drain(done);
     if (bad) atomicOr(&g_q8_error_word, bad);
     pdl_wait();
 }
@@ -625,12 +679,12 @@ bool encode_codes(CUtensorMap *map, const uint8_t *base, const PagedArgs &a, int
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int DT, int CODE, int NT, int RT>
-clis_status_t launch_impl(const PagedArgs &a, const QuantArgs &z, bool strict, bool after_schedule, void *workspace, int nsm,
-                          cudaStream_t stream)
+template <int D, int DT, int CODE, int NT>
+clis_status_t launch_impl(int rows, const PagedArgs &a, const QuantArgs &z, bool strict, bool after_schedule, void *workspace,
+                          int nsm, cudaStream_t stream)
 {
-    using C = QCfg<D, NT, RT>;
-    const auto kernel = paged_q8_kernel<D, DT, CODE, NT, RT>;
+    using C = QCfg<D, NT>;
+    const auto kernel = paged_q8_kernel<D, DT, CODE, NT>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return CLIS_ERR_CUDA;
     const int grid = C::BLOCKS * nsm;
     DecodeParams p;
@@ -638,7 +692,8 @@ clis_status_t launch_impl(const PagedArgs &a, const QuantArgs &z, bool strict, b
     p.g = a.H / a.Hkv;
     p.least = 2;
     p.strict = strict;
-    place_parts(p, static_cast<size_t>(grid) * C::TEAMS, 8 * NT * RT, workspace);
+    place_parts(p, static_cast<size_t>(grid) * kDecodeWarps, C::TR, workspace);
+    p.limit = rows;
     int box_shift = 0;
     while ((1 << box_shift) < C::TK && box_shift < a.page_shift) box_shift++;
     CUtensorMap mk, mv;
@@ -654,14 +709,13 @@ clis_status_t launch_impl(const PagedArgs &a, const QuantArgs &z, bool strict, b
     return launch_join<D, DT>(p, stream) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
 
-// Query rows that the kernels are built for: 8, 16, 32 and 64.
 template <int D, int DT, int CODE, typename... A>
 clis_status_t launch_rows(int rows, const A &...args)
 {
-    if (rows == 8) return launch_impl<D, DT, CODE, 1, 1>(args...);
-    if (rows == 16) return launch_impl<D, DT, CODE, 2, 1>(args...);
-    if (rows == 32) return launch_impl<D, DT, CODE, 2, 2>(args...);
-    return launch_impl<D, DT, CODE, 2, 4>(args...);
+    if (rows <= 8) return launch_impl<D, DT, CODE, 1>(rows, args...);
+    if constexpr (D == 64)
+        if (rows > 16) return launch_impl<D, DT, CODE, 4>(rows, args...);
+    return launch_impl<D, DT, CODE, 2>(rows, args...);
 }
 
 template <int D, typename... A>
@@ -671,13 +725,6 @@ clis_status_t launch_types(bool half, bool int8, int rows, const A &...args)
     return half ? launch_rows<D, 1, CLIS_CODE_E4M3>(rows, args...) : launch_rows<D, 0, CLIS_CODE_E4M3>(rows, args...);
 }
 
-template <int NT, int RT>
-size_t workspace_of(int d, int nsm)
-{
-    // (the same for both widths)
-    return parts_workspace(static_cast<size_t>(QCfg<128, NT, RT>::BLOCKS) * nsm * QCfg<128, NT, RT>::TEAMS, 8 * NT * RT, d);
-}
-
 }  // namespace
 
 int paged_q8_rows(int64_t max_q, int g)
@@ -685,13 +732,16 @@ int paged_q8_rows(int64_t max_q, int g)
     // Rows of the largest sequence if it is small; else those of single tokens.
     constexpr int most = 64;
     const int64_t rows = max_q <= most && max_q * g <= most ? max_q * g : g;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= most ? 64 : 0;
+    return rows <= most ? static_cast<int>(rows) : 0;
 }
 
 size_t paged_q8_workspace(int d, int rows, int nsm)
 {
-    return rows == 0 ? 0 : rows == 8 ? workspace_of<1, 1>(d, nsm) : rows == 16 ? workspace_of<2, 1>(d, nsm)
-           : rows == 32 ? workspace_of<2, 2>(d, nsm) : workspace_of<2, 4>(d, nsm);
+    if (rows == 0) return 0;
+    const int nt = rows <= 8 ? 1 : d == 64 && rows > 16 ? 4 : 2;
+    const int of_sm = kDecodeWarps * (nt == 1 ? QCfg<128, 1>::BLOCKS : QCfg<128, 2>::BLOCKS);  // (the same for both widths)
+    static_assert(QCfg<64, 4>::BLOCKS == QCfg<128, 2>::BLOCKS, "one number of blocks");
+    return parts_workspace(static_cast<size_t>(of_sm) * nsm, 8 * nt, d);
 }
 
 clis_status_t launch_paged_q8(const PagedArgs &a, const QuantArgs &z, int rows, bool strict, bool after_schedule,

@@ -20,11 +20,13 @@ constexpr int kJoinThreads = 256;
 struct DecodeParams {
     PagedArgs a;
     int g, rows_max, least;
+    int limit;   // query rows that a sequence may have (rows_max of them in an item)
     int workers;     // warps (paged_q8.cu: teams of warps) of the grid
     int strict;  // no chunk kernel follows: a sequence of more rows is an error
     float *part_o;   // [2 * workers][rows_max][D]: place 2 c + 1 if worker c starts the item, 2 c if it goes on with it
     float2 *part_ml; // [2 * workers][rows_max]
-    int4 *meta;      // [workers] {parts, first row of q, new tokens, head} of the item the worker starts and does not finish
+    int4 *meta;      // [workers] {parts, first row of q, new tokens and 2^16 times the item's first row, head} of the item
+                     // the worker starts and does not finish
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
@@ -75,28 +77,36 @@ __device__ __forceinline__ SeqLen seq_len(const PagedArgs &a, int s)
 }
 
 // Position in the block's run: unit j of item (s, h).
-template <int TK>
+// TR: an item has up to TR of a sequence's query rows, `tile` says which (0: all of them).
+template <int TK, int TR = 0>
 struct Pos {
     int s, h, j, units;
+    int tile, tiles;
     SeqLen q;
     uint32_t left;  // units of the run from this one on
 
-    __device__ __forceinline__ void set(const PagedArgs &a, int seq)
+    __device__ __forceinline__ void set(const PagedArgs &a, int seq, int g)
     {
         s = seq;
         q = seq_len(a, s);
         units = decode_units(q, TK);
+        tile = 0;
+        tiles = TR ? ceil_div(q.n * g, TR) : 1;
     }
     // The next item of the run (there is one if units are left).
-    __device__ __forceinline__ void next_item(const PagedArgs &a, int g, int rows_max)
+    __device__ __forceinline__ void next_item(const PagedArgs &a, int g, int limit)
     {
         j = 0;
+        if (TR) {
+            if (++tile < tiles) return;
+            tile = 0;
+        }
         if (++h < a.Hkv) return;
         h = 0;
         int n = s + 1;
         while (n < a.S) {
-            set(a, n);
-            if (is_decode(q, g, rows_max)) return;
+            set(a, n, g);
+            if (is_decode(q, g, limit)) return;
             ++n;
         }
         left = 0;  // not reached while the run's units are counted alike
@@ -111,7 +121,7 @@ struct Runs {
     int nb;      // workers that take part
 };
 
-template <int TK, int NW>
+template <int TK, int NW, int TR = 0>
 __device__ __forceinline__ Runs block_runs(const DecodeParams &p, uint64_t *s_sum, int *s_seq, uint64_t *s_rel, unsigned int &bad)
 {
     const PagedArgs &a = p.a;
@@ -122,7 +132,7 @@ __device__ __forceinline__ Runs block_runs(const DecodeParams &p, uint64_t *s_su
     for (int s = sb; s < se; s++) {
         const SeqLen q = seq_len(a, s);
         if (q.bad) bad |= CLIS_PAGED_LENGTH_BIT;
-        if (is_decode(q, p.g, p.rows_max)) mine += static_cast<uint64_t>(a.Hkv) * decode_units(q, TK);
+        if (is_decode(q, p.g, p.limit)) mine += static_cast<uint64_t>(a.Hkv * (TR ? ceil_div(q.n * p.g, TR) : 1)) * decode_units(q, TK);
         else if (p.strict && q.n > 0) bad |= CLIS_PAGED_LENGTH_BIT;
     }
     uint64_t incl = mine;
@@ -149,8 +159,8 @@ __device__ __forceinline__ Runs block_runs(const DecodeParams &p, uint64_t *s_su
         uint64_t rel = u - excl;
         for (int s = sb; s < se; s++) {
             const SeqLen q = seq_len(a, s);
-            if (!is_decode(q, p.g, p.rows_max)) continue;
-            const uint64_t n = static_cast<uint64_t>(a.Hkv) * decode_units(q, TK);
+            if (!is_decode(q, p.g, p.limit)) continue;
+            const uint64_t n = static_cast<uint64_t>(a.Hkv * (TR ? ceil_div(q.n * p.g, TR) : 1)) * decode_units(q, TK);
             if (rel < n) {
                 s_seq[w] = s;
                 s_rel[w] = rel;
@@ -186,9 +196,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
     pdl_launch();
     if (tid < kJoinEach) s_meta[tid] = c0 + tid < p.workers ? p.meta[c0 + tid] : make_int4(0, 0, 0, 0);
     __syncthreads();
+    auto rows_of = [&](int i) { return s_meta[i].x ? min((s_meta[i].z & 0xFFFF) * p.g - (s_meta[i].z >> 16), p.rows_max) : 0; };
     int rows = 0;
 #pragma unroll
-    for (int i = 0; i < kJoinEach; i++) rows += s_meta[i].x ? s_meta[i].z * p.g : 0;
+    for (int i = 0; i < kJoinEach; i++) rows += rows_of(i);
     const int mine = (rows + gridDim.y - 1) / gridDim.y;  // rows of this block
     int per = W;                                          // warps per row
     while (per > 1 && mine * per > W) per /= 2;
@@ -198,7 +209,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
         const bool live = row < rows;
         if (live)
             while (true) {  // the item that the row belongs to
-                const int n = s_meta[i].x ? s_meta[i].z * p.g : 0;
+                const int n = rows_of(i);
                 if (row < n) break;
                 row -= n;
                 i++;
@@ -252,7 +263,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join_kernel(const D
         }
         if (live && sub == 0) {
             const float inv = 1.f / l;
-            const int tok = row / p.g, hd = mt.w * p.g + (row - tok * p.g);
+            const int of = row + (mt.z >> 16), tok = of / p.g, hd = mt.w * p.g + (of - tok * p.g);
             uint16_t *dst = a.o + static_cast<int64_t>(mt.y + tok) * a.o_st + hd * a.o_sh + lane * V;
 #pragma unroll
             for (int e = 0; e < V; e += 2)  // (zeros for a row that sees no key)
@@ -286,7 +297,7 @@ inline void place_parts(DecodeParams &p, size_t workers, size_t rows, void *work
 {
     char *w = static_cast<char *>(workspace);
     p.workers = static_cast<int>(workers);
-    p.rows_max = static_cast<int>(rows);
+    p.rows_max = p.limit = static_cast<int>(rows);
     p.meta = reinterpret_cast<int4 *>(w);
     w += up256(workers * sizeof(int4));
     p.part_ml = reinterpret_cast<float2 *>(w);

@@ -59,7 +59,7 @@ def make_q8(ctx, new, H, Hkv, d, page, dtype, code, seed=0, device="cuda", extra
 def is_few(n, max_q, g):
     """Whether a sequence of n new tokens runs the kernel for few rows (include/clis.h)."""
     limit = max_q * g if max_q * g <= 64 else g
-    limit = 8 if limit <= 8 else 16 if limit <= 16 else 32 if limit <= 32 else 64 if limit <= 64 else 0
+    limit = limit if limit <= 64 else 0
     return n * g <= limit
 
 
