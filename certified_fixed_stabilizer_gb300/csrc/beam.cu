@@ -9,13 +9,19 @@
 // first kernel leaves each chunk's largest logit and the row's maximum and sum.  At most K
 // chunks can hold one of the K best: those whose largest logit leads to the K best such
 // values, so the second kernel (a block per request) picks them, reads them again (a
-// few KB, still in L2) and picks the K best of what they hold.  Either pick is K rounds of
-// a maximum over the block, each thread offering the best of what it has left: exact in
-// the order of (value, index), whatever ties.
+// few KB, still in L2) and picks the K best of what they hold:
 //
-//  * Values are compared in 64 bits: score and logit as they are, the logarithm of the
-//    sum from 32-bit terms, off by about 1e-7.  Within a beam the order is that of the
-//    logits alone; fp64 is one addition per thread and round.
+//  * Mostly no pick has to be exact but the last.  The K-th largest of 64 groups' leaders is
+//    no more than the K-th best value; chunks and then logits below it are left out, which leaves
+//    little more than K candidates, and each counts those that are better (13 us for 8 requests of
+//    4 beams and K = 8 with the other way).  Where more are left (many ties, few chunks), warps
+//    sort candidates 32 at a time and merge their lists in a tree.  Either way the order is
+//    exactly that of (value, index).  (K rounds of a maximum over the block took 38 us for 96
+//    requests of 8 beams and K = 16.)
+//  * A value is a pair of fp32 numbers (their sum, to 48 bits): exact sums of score, logit and
+//    the logarithm, which comes from 32-bit terms and is off by about 1e-7.  fp64 is a
+//    fiftieth of fp32's rate here: with doubles the picks took 28 us for 8 requests of 4
+//    beams and K = 8.  Within a beam the order is that of the logits alone.
 //  * Sums are taken in an order that depends on the places in the row alone, not on the
 //    row's alignment: equal rows have equal sums, and ties between beams stay ties.
 #include <cuda_bf16.h>
@@ -32,7 +38,9 @@ namespace {
 
 constexpr int kChunk = 512, kPer = kChunk / 32;  // logits of a chunk, of a lane
 constexpr int kScanThreads = 256, kScanWarps = kScanThreads / 32;
-constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32;
+constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
+constexpr int kGroups = kMaxPicks;  // of leaders, for the bound
+constexpr int kPool = kPickThreads; // candidates that are ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BeamParams {
@@ -87,48 +95,56 @@ __device__ __forceinline__ uint4 shifted_by(const uint4 &lo, const uint4 &hi, in
     }
 }
 
-// A lane's logits of the chunk at `first`, the e-th at place(lane, e); -inf behind the
-// row's end.  A row that is not 16-byte aligned is read in aligned pieces, each lane two
+// What a lane loads of a chunk: its logits (the e-th at place(lane, e)) as they lie in
+// memory.  A row that is not 16-byte aligned is read in aligned pieces, each lane two
 // neighbouring ones; its first and last chunk one logit at a time, so that nothing outside
 // of the row is touched.
-template <int DT>
-__device__ __forceinline__ void load_chunk(const void *row, int64_t first, int V, int lane, float *x)
-{
-    constexpr int SIZE = DT == 2 ? 4 : 2, N = 16 / SIZE;
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
-    if (off == 0 ? first + kChunk <= V : first > 0 && first + kChunk + N <= V) {
+template <int DT, bool ALIGNED>
+struct Raw {
+    static constexpr int SIZE = DT == 2 ? 4 : 2, N = 16 / SIZE, P = kPer / N;
+    uint4 v[P], u[ALIGNED ? 1 : P];
+    bool whole;
+
+    __device__ __forceinline__ void load(const void *row, int64_t first, int V, int lane)
+    {
+        const int off = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+        whole = off == 0 ? first + kChunk <= V : first > 0 && first + kChunk + N <= V;
+        if (!whole) return;
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) + first * SIZE - off);
-        uint4 v[kPer / N];
 #pragma unroll
-        for (int j = 0; j < kPer / N; j++) v[j] = __ldg(src + j * 32 + lane);
-        if (off != 0) {
-            uint4 u[kPer / N];
+        for (int j = 0; j < P; j++) v[j] = __ldg(src + j * 32 + lane);
+        if (!ALIGNED && off != 0)
 #pragma unroll
-            for (int j = 0; j < kPer / N; j++) u[j] = __ldg(src + j * 32 + lane + 1);
+            for (int j = 0; j < P; j++) u[ALIGNED ? 0 : j] = __ldg(src + j * 32 + lane + 1);
+    }
+    // The logits; -inf behind the row's end.
+    __device__ __forceinline__ void values(const void *row, int64_t first, int V, int lane, float *x) const
+    {
+        if (!whole) {
 #pragma unroll
-            for (int j = 0; j < kPer / N; j++) v[j] = shifted_by(v[j], u[j], off);
+            for (int e = 0; e < kPer; e++) {
+                const int64_t i = first + place<DT>(lane, e);
+                x[e] = i < V ? logit(row, DT, i) : -INFINITY;
+            }
+            return;
         }
+        const int off = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
 #pragma unroll
-        for (int j = 0; j < kPer / N; j++) {
-            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        for (int j = 0; j < P; j++) {
+            const uint4 y = ALIGNED ? v[j] : shifted_by(v[j], u[ALIGNED ? 0 : j], off);
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                if (DT == 2) {
+                if constexpr (DT == 2) {
                     x[j * N + e] = __uint_as_float(w[e]);
                 } else {
-                    x[j * N + 2 * e] = elem_lo<DT == 2 ? 0 : DT>(w[e]);
-                    x[j * N + 2 * e + 1] = elem_hi<DT == 2 ? 0 : DT>(w[e]);
+                    x[j * N + 2 * e] = elem_lo<DT>(w[e]);
+                    x[j * N + 2 * e + 1] = elem_hi<DT>(w[e]);
                 }
             }
         }
-        return;
     }
-#pragma unroll
-    for (int e = 0; e < kPer; e++) {
-        const int64_t i = first + place<DT>(lane, e);
-        x[e] = i < V ? logit(row, DT, i) : -INFINITY;
-    }
-}
+};
 
 // Floats as unsigned numbers of the same order.
 __device__ __forceinline__ uint32_t ordered(float x)
@@ -154,7 +170,7 @@ __device__ __forceinline__ void merge(float &m, float &s, float m1, float s1)
     m = mm;
 }
 
-template <int DT>
+template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParams p)
 {
     const BeamArgs &a = p.a;
@@ -162,23 +178,27 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParam
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = blockIdx.y, split = blockIdx.x;
     pdl_launch();
-    if (!isfinite(__ldg(a.scores + r))) return;  // a beam not in use
+    const float score = __ldg(a.scores + r);
     const int req = r / a.W, w = r - req * a.W;
     const void *row = static_cast<const uint8_t *>(a.logits) + (req * a.l_sr + w * a.l_sw) * (DT == 2 ? 4 : 2);
     const int c0 = (split * kScanWarps + warp) * p.per_warp, c1 = min(p.chunks, c0 + p.per_warp);
-    float m = -INFINITY, s = 0.f;  // the warp's maximum, the lane's sum
-    constexpr int B = 2;           // chunks in flight
-    for (int c = c0; c < c1; c += B) {
-        float x[B][kPer];
+    float m = -INFINITY, s = 0.f;       // the warp's maximum, the lane's sum
+    constexpr int B = DT == 2 || !ALIGNED ? 2 : 4;  // chunks on their way
+    Raw<DT, ALIGNED> raw[B];
 #pragma unroll
-        for (int b = 0; b < B; b++)
-            if (c + b < c1) load_chunk<DT>(row, static_cast<int64_t>(c + b) * kChunk, a.V, lane, x[b]);
+    for (int b = 0; b < B; b++)
+        if (c0 + b < c1) raw[b].load(row, static_cast<int64_t>(c0 + b) * kChunk, a.V, lane);
+    if (!isfinite(score)) return;  // a beam not in use (known only now: the loads do not wait for it)
+    for (int c = c0; c < c1; c += B) {
 #pragma unroll
         for (int b = 0; b < B; b++) {
             if (c + b >= c1) continue;
-            float mx = x[b][0];
+            float x[kPer];
+            raw[b].values(row, static_cast<int64_t>(c + b) * kChunk, a.V, lane, x);
+            if (c + b + B < c1) raw[b].load(row, static_cast<int64_t>(c + b + B) * kChunk, a.V, lane);
+            float mx = x[0];
 #pragma unroll
-            for (int e = 1; e < kPer; e++) mx = fmaxf(mx, x[b][e]);  // (a NaN is left to the sum)
+            for (int e = 1; e < kPer; e++) mx = fmaxf(mx, x[e]);  // (a NaN is left to the sum)
             mx = from_ordered(__reduce_max_sync(~0u, ordered(mx)));
             if (lane == 0) p.lead[static_cast<int64_t>(r) * p.chunks + c + b] = mx;
             if (mx > m) {
@@ -189,7 +209,7 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParam
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < kPer; e += 2) {
-                const float2 d = fmul2(fadd2(make_float2(x[b][e], x[b][e + 1]), make_float2(base, base)), make_float2(kLog2e, kLog2e));
+                const float2 d = fmul2(fadd2(make_float2(x[e], x[e + 1]), make_float2(base, base)), make_float2(kLog2e, kLog2e));
                 sum = fadd2(sum, make_float2(ex2_approx(d.x), ex2_approx(d.y)));
             }
             s += sum.x + sum.y;
@@ -205,77 +225,184 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParam
     }
 }
 
-// A candidate: its value as an unsigned number of the same order (0: none), and its place.
-struct Best {
-    uint32_t hi, lo, at;
+// hi + lo, exact sums of two numbers and of such pairs (to 48 bits).
+struct Pair {
+    float hi, lo;
 };
 
-__device__ __forceinline__ Best best_of(double v, uint32_t at)
+__device__ __forceinline__ Pair two_sum(float a, float b)
 {
-    uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
-    u = u >> 63 ? ~u : u | (uint64_t(1) << 63);
-    if (!isfinite(v)) u = 0;
-    return {static_cast<uint32_t>(u >> 32), static_cast<uint32_t>(u), at};
+    const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
 }
 
-__device__ __forceinline__ double value_of(const Best &b)
+__device__ __forceinline__ Pair plus(const Pair &a, float b)
 {
-    uint64_t u = (static_cast<uint64_t>(b.hi) << 32) | b.lo;
-    u = u >> 63 ? u & ~(uint64_t(1) << 63) : ~u;
-    return __longlong_as_double(static_cast<long long>(u));
+    const Pair t = two_sum(a.hi, b);
+    const float e = __fadd_rn(t.lo, a.lo), s = __fadd_rn(t.hi, e);
+    return {s, __fsub_rn(e, __fsub_rn(s, t.hi))};
 }
 
-__device__ __forceinline__ bool none(const Best &b) { return (b.hi | b.lo) == 0; }
-__device__ __forceinline__ bool better(const Best &a, const Best &b)
+// m + log(s), s a positive number: s = f 2^k with f in [0.7, 1.42), so that logf(f) is off by
+// little, and k log 2 as a pair.
+__device__ __forceinline__ Pair log_sum(float m, float s)
 {
-    return a.hi != b.hi ? a.hi > b.hi : a.lo != b.lo ? a.lo > b.lo : a.at < b.at;
+    int k = static_cast<int>(__float_as_uint(s) >> 23) - 127;
+    float f = __uint_as_float((__float_as_uint(s) & 0x7FFFFFu) | 0x3F800000u);  // (sums are normal numbers)
+    if (f > 1.41421356f) {
+        f *= 0.5f;
+        k++;
+    }
+    const float ln2 = 0.693147182f, rest = -1.90465429e-9f;  // log 2 - ln2
+    const float x = static_cast<float>(k), p = __fmul_rn(x, ln2);
+    const Pair t = plus(two_sum(m, p), __fmaf_rn(x, ln2, -p));
+    return plus(t, __fmaf_rn(x, rest, logf(f)));
 }
 
-__device__ __forceinline__ Best warp_best(const Best &b)
+// score + (x - lse)
+__device__ __forceinline__ Pair value(float score, float x, const Pair &lse)
 {
-    Best r;
-    r.hi = __reduce_max_sync(~0u, b.hi);
-    r.lo = __reduce_max_sync(~0u, b.hi == r.hi ? b.lo : 0u);
-    r.at = __reduce_min_sync(~0u, b.hi == r.hi && b.lo == r.lo ? b.at : ~0u);
-    return r;
+    const Pair t = plus({-lse.hi, -lse.lo}, x);
+    return plus(t, score);
 }
 
-// Of all threads' candidates; one barrier (the places alternate).
-__device__ __forceinline__ Best block_best(const Best &b, Best (*places)[kPickWarps], int round)
+// A candidate: its value as an unsigned number of the same order (0: none), and its place.
+struct Best {
+    uint64_t v;
+    uint32_t at;
+};
+
+__device__ __forceinline__ Best no_one() { return {0ull, ~0u}; }
+
+__device__ __forceinline__ Best best_of(const Pair &v, uint32_t at)
+{
+    // (no -0)
+    return {isfinite(v.hi) ? static_cast<uint64_t>(ordered(v.hi + 0.f)) << 32 | ordered(v.lo + 0.f) : 0ull, at};
+}
+
+__device__ __forceinline__ bool better(const Best &a, const Best &b) { return a.v > b.v || (a.v == b.v && a.at < b.at); }
+__device__ __forceinline__ Best from_lane(const Best &b, int l) { return {__shfl_sync(~0u, b.v, l), __shfl_sync(~0u, b.at, l)}; }
+
+// One comparison of a sorting network: lanes whose bit o is clear keep the better one
+// (down), or the worse.
+__device__ __forceinline__ void exchange(Best &b, int o, bool down, int lane)
+{
+    const Best x = {__shfl_xor_sync(~0u, b.v, o), __shfl_xor_sync(~0u, b.at, o)};
+    if (better(x, b) == (((lane & o) == 0) == down)) b = x;
+}
+
+// A bitonic sequence of 32, best first.  (Loops, not unrolled: a kernel this short waits for
+// its instructions.)
+__device__ __forceinline__ void sort_bitonic(Best &b, int lane)
+{
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) exchange(b, o, true, lane);
+}
+
+__device__ __forceinline__ void sort32(Best &b, int lane)
+{
+#pragma unroll 1
+    for (int n = 2; n <= 32; n *= 2)
+#pragma unroll 1
+        for (int o = n / 2; o > 0; o >>= 1) exchange(b, o, (lane & n) == 0, lane);
+}
+
+// The K best of what a warp has seen, best first: lane i has the i-th and, where K is
+// beyond 32, the (32 + i)-th.
+struct Top {
+    Best b[2];
+    int K;
+
+    // 32 sorted candidates join.
+    __device__ __forceinline__ void join(const Best &sorted, int lane)
+    {
+        Best x = from_lane(sorted, 31 - lane);
+        const bool take = better(x, b[0]);
+        Best rest = take ? b[0] : x;
+        if (take) b[0] = x;
+        sort_bitonic(b[0], lane);
+        if (K <= 32) return;
+        sort_bitonic(rest, lane);
+        x = from_lane(rest, 31 - lane);
+        if (better(x, b[1])) b[1] = x;
+        sort_bitonic(b[1], lane);
+    }
+    __device__ __forceinline__ void add(Best x, int lane)
+    {
+        // (nothing to do where no candidate is better than the K-th)
+        const Best worst = K <= 32 ? from_lane(b[0], K - 1) : from_lane(b[1], K - 33);
+        if (!__any_sync(~0u, better(x, worst))) return;
+        sort32(x, lane);
+        join(x, lane);
+    }
+};
+
+// The lists of the block's first n warps (all threads call) become the first warp's.
+__device__ __forceinline__ void join_warps(Top &top, int n, Best (*lists)[64])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Best w = warp_best(b);
-    if (lane == 0) places[round & 1][warp] = w;
-    __syncthreads();
-    return warp_best(places[round & 1][lane]);
+    for (int d = 1; d < n; d *= 2) {
+        if (warp < n && (warp & (2 * d - 1)) == d) {
+            lists[warp][lane] = top.b[0];
+            if (top.K > 32) lists[warp][32 + lane] = top.b[1];
+        }
+        __syncthreads();
+        if ((warp & (2 * d - 1)) == 0 && warp + d < n) {
+            top.join(lists[warp + d][lane], lane);
+            if (top.K > 32) top.join(lists[warp + d][32 + lane], lane);
+        }
+    }
 }
+
+struct Outputs {
+    const BeamArgs &a;
+    int64_t first;
+    __device__ __forceinline__ void put(int k, const Best &b) const
+    {
+        const bool gone = b.v == 0;
+        a.out_scores[first + k] = gone ? -INFINITY : from_ordered(static_cast<uint32_t>(b.v >> 32));
+        a.parent[first + k] = gone ? -1 : static_cast<int>(b.at / static_cast<uint32_t>(a.V));
+        a.token[first + k] = gone ? -1 : static_cast<int>(b.at % static_cast<uint32_t>(a.V));
+    }
+};
 
 template <int DT>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParams p)
 {
     const BeamArgs &a = p.a;
-    extern __shared__ float s_lead[];  // [W][chunks]
-    __shared__ double s_score[kMaxBeams], s_lse[kMaxBeams];
+    __shared__ Best s_lists[kPickWarps][64];
+    __shared__ float s_score[kMaxBeams];
+    __shared__ Pair s_lse[kMaxBeams];
     __shared__ bool s_ok[kMaxBeams];
-    __shared__ Best s_best[2][kPickWarps];
-    __shared__ int2 s_pick[kMaxPicks];  // beam and chunk
+    __shared__ Best s_pick[kMaxPicks];  // at: beam * chunks + chunk
+    __shared__ uint32_t s_group[kGroups];
+    __shared__ uint32_t s_bound;
+    __shared__ int s_chunks, s_cands, s_chunk[kPool];
+    Best *pool = &s_lists[0][0];  // [kPool]
+    static_assert(kPool <= kPickWarps * 64, "the pool lies in the lists' place");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int req = blockIdx.x;
+    if (tid < kGroups) s_group[tid] = 0;
+    if (tid == 0) s_chunks = s_cands = 0;
     pdl_wait();
+    const int leads = a.W * p.chunks;
+    const float *lead = p.lead + static_cast<int64_t>(req) * leads;
+    const Outputs out{a, static_cast<int64_t>(req) * a.K};
+    const float ahead = tid < leads ? lead[tid] : 0.f;  // (beside the rows' sums; a beam not in use may hold anything)
 
     // ---- the rows' logarithms, in the order of the splits
     for (int w = warp; w < a.W; w += kPickWarps) {
         const int r = req * a.W + w;
         const float score = __ldg(a.scores + r);
-        bool ok = isfinite(score);
         float m = -INFINITY, s = 0.f;
+        for (int i = lane; i < p.splits; i += 32) {
+            const float2 v = p.part[static_cast<int64_t>(r) * p.splits + i];
+            merge(m, s, v.x, v.y);
+        }
+        bool ok = isfinite(score);
         if (ok) {
-            for (int i = lane; i < p.splits; i += 32) {
-                const float2 v = p.part[static_cast<int64_t>(r) * p.splits + i];
-                merge(m, s, v.x, v.y);
-            }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {  // (lane l with l + o: the same order in every lane that counts)
+            for (int o = 16; o > 0; o >>= 1) {
                 const float m1 = __shfl_down_sync(~0u, m, o), s1 = __shfl_down_sync(~0u, s, o);
                 merge(m, s, m1, s1);
             }
@@ -286,107 +413,118 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
         if (lane == 0) {
             s_ok[w] = ok;
             s_score[w] = score;
-            s_lse[w] = ok ? static_cast<double>(m) + log(static_cast<double>(s)) : 0.0;
+            s_lse[w] = ok ? log_sum(m, s) : Pair{0.f, 0.f};
         }
     }
-    for (int i = tid; i < a.W * p.chunks; i += kPickThreads)
-        s_lead[i] = p.lead[static_cast<int64_t>(req) * a.W * p.chunks + i];
     __syncthreads();
 
-    // ---- the chunks: a thread has every tpr-th of one beam
-    const int tpr = kPickThreads / a.W;
-    const int w = tid / tpr, sub = tid - w * tpr;
-    const bool mine = w < a.W && s_ok[w < a.W ? w : 0];
-    auto next_lead = [&]() -> Best {
-        float top = -INFINITY;
-        int at = -1;
-        if (mine)
-            for (int c = sub; c < p.chunks; c += tpr) {
-                const float x = s_lead[w * p.chunks + c];
-                if (x > top) {
-                    top = x;
-                    at = c;
-                }
-            }
-        if (at < 0) return {0u, 0u, ~0u};
-        return best_of(s_score[w] + (static_cast<double>(top) - s_lse[w]), static_cast<uint32_t>(w * p.chunks + at));
+    // The value of a chunk's leader as an unsigned number of its order (0: none).
+    auto leader = [&](int i, float x) -> Best {
+        const int w = i / p.chunks;
+        return s_ok[w] && x != -INFINITY ? best_of(value(s_score[w], x, s_lse[w]), static_cast<uint32_t>(i)) : no_one();
     };
-    Best have = next_lead();
+    // A quarter of a chunk: this lane's kChunk / 128 logits, their places w * V + v from `at` on in steps of 32.
+    constexpr int E = kChunk / 128;
+    auto quarter = [&](int chunk, int q, float *x, int &w, uint32_t &at) {
+        w = chunk / p.chunks;
+        const int64_t first = static_cast<int64_t>(chunk - w * p.chunks) * kChunk + q * 128 + lane;
+        const void *row = static_cast<const uint8_t *>(a.logits) + (req * a.l_sr + w * a.l_sw) * (DT == 2 ? 4 : 2);
+#pragma unroll
+        for (int e = 0; e < E; e++) x[e] = first + e * 32 < a.V ? logit(row, DT, first + e * 32) : -INFINITY;
+        at = static_cast<uint32_t>(static_cast<int64_t>(w) * a.V + first);
+    };
+
+    // ---- the bound, the chunks that reach it, the logits that do
+#pragma unroll 1
+    for (int i = tid; i < leads; i += kPickThreads)
+        atomicMax(&s_group[i % kGroups], static_cast<uint32_t>(leader(i, i == tid ? ahead : lead[i]).v >> 32));
+    __syncthreads();
+    if (tid < kGroups) {
+        const uint32_t mine = s_group[tid];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < kGroups; j++) rank += s_group[j] > mine || (s_group[j] == mine && j < tid);
+        if (rank == a.K - 1) s_bound = max(mine, 1u);
+    }
+    __syncthreads();
+    const uint32_t bound = s_bound;
+#pragma unroll 1
+    for (int i = tid; i < leads; i += kPickThreads)
+        if ((leader(i, i == tid ? ahead : lead[i]).v >> 32) >= bound) {
+            const int k = atomicAdd(&s_chunks, 1);
+            if (k < kPool) s_chunk[k] = i;
+        }
+    __syncthreads();
+    const int found = s_chunks;
+    if (found <= kPool) {
+#pragma unroll 1
+        for (int t = warp; t < 4 * found; t += kPickWarps) {
+            float x[E];
+            int w;
+            uint32_t at;
+            quarter(s_chunk[t >> 2], t & 3, x, w, at);
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                const Best b = x[e] == -INFINITY ? no_one() : best_of(value(s_score[w], x[e], s_lse[w]), at + e * 32);
+                if ((b.v >> 32) < bound) continue;
+                const int k = atomicAdd(&s_cands, 1);
+                if (k < kPool) pool[k] = b;
+            }
+            if (s_cands > kPool) break;  // (only to save time: looked at again below)
+        }
+        __syncthreads();
+        const int n = s_cands;
+        if (n <= kPool) {
+            const Best mine = tid < n ? pool[tid] : no_one();
+            if (tid < n) {
+                int rank = 0;
+#pragma unroll 4
+                for (int j = 0; j < n; j++) rank += better(pool[j], mine);
+                if (rank < a.K) out.put(rank, mine);
+            }
+            if (tid >= n && tid < a.K) out.put(tid, no_one());
+            return;
+        }
+    }
+    __syncthreads();  // (the pool's place is written again)
+
+    // ---- the other way: the K best leaders, exactly
+    Top top;
+    top.K = a.K;
+    top.b[0] = top.b[1] = no_one();
+#pragma unroll 1
+    for (int i0 = warp * 32; i0 < leads; i0 += kPickThreads) top.add(i0 + lane < leads ? leader(i0 + lane, lead[i0 + lane]) : no_one(), lane);
+    join_warps(top, min((leads + 31) / 32, kPickWarps), s_lists);
+    if (warp == 0) {
+        if (lane < a.K) s_pick[lane] = top.b[0];
+        if (32 + lane < a.K) s_pick[32 + lane] = top.b[1];
+    }
+    __syncthreads();
+
+    // ---- what they hold, no worse than the last of their leaders: quarters of chunks
     int picks = 0;
-    for (; picks < a.K; picks++) {
-        const Best b = block_best(have, s_best, picks);
-        if (none(b)) break;
-        if (tid == 0) s_pick[picks] = make_int2(static_cast<int>(b.at) / p.chunks, static_cast<int>(b.at) % p.chunks);
-        if (have.at == b.at && !none(have)) {
-            s_lead[b.at] = -INFINITY;
-            have = next_lead();
+    while (picks < a.K && s_pick[picks].v != 0) picks++;
+    const Best last = picks == a.K ? s_pick[picks - 1] : no_one();
+    top.b[0] = top.b[1] = no_one();
+#pragma unroll 1
+    for (int t = warp; t < 4 * picks; t += kPickWarps) {
+        float x[E];
+        int w;
+        uint32_t at;
+        quarter(static_cast<int>(s_pick[t >> 2].at), t & 3, x, w, at);
+#pragma unroll 1
+        for (int e = 0; e < E; e++) {
+            Best b = x[0] == -INFINITY ? no_one() : best_of(value(s_score[w], x[0], s_lse[w]), at + e * 32);
+            if (b.v < last.v) b = no_one();
+            top.add(b, lane);
+#pragma unroll
+            for (int i = 1; i < E; i++) x[i - 1] = x[i];
         }
     }
-    __syncthreads();
-
-    // ---- what they hold: up to two chunks a warp
-    constexpr int Q = kMaxPicks / kPickWarps;
-    float x[Q][kPer];
-    Best own[Q];
-    int beam[Q] = {};
-    int64_t first[Q] = {};
-    auto next_own = [&](int q) {
-        float top = -INFINITY;
-        int at = -1;
-#pragma unroll
-        for (int e = 0; e < kPer; e++)
-            if (x[q][e] > top) {  // (the first of equal ones: places rise with e)
-                top = x[q][e];
-                at = e;
-            }
-        own[q] = at < 0 ? Best{0u, 0u, ~0u}
-                        : best_of(s_score[beam[q]] + (static_cast<double>(top) - s_lse[beam[q]]),
-                                  static_cast<uint32_t>(static_cast<int64_t>(beam[q]) * a.V + first[q] + place<DT>(lane, at)));
-    };
-#pragma unroll
-    for (int q = 0; q < Q; q++) {
-        const int i = q * kPickWarps + warp;
-        const bool some = i < picks;
-        const int2 pk = some ? s_pick[i] : make_int2(0, 0);
-        beam[q] = pk.x;
-        first[q] = static_cast<int64_t>(pk.y) * kChunk;
-        const void *row = static_cast<const uint8_t *>(a.logits) + (req * a.l_sr + pk.x * a.l_sw) * (DT == 2 ? 4 : 2);
-        if (some) load_chunk<DT>(row, first[q], a.V, lane, x[q]);
-        else
-#pragma unroll
-            for (int e = 0; e < kPer; e++) x[q][e] = -INFINITY;
-        next_own(q);
-    }
-    for (int k = 0; k < a.K; k++) {
-        Best mineb = own[0];
-#pragma unroll
-        for (int q = 1; q < Q; q++)
-            if (better(own[q], mineb)) mineb = own[q];
-        const Best b = block_best(mineb, s_best, picks + 1 + k);
-        const int64_t out = static_cast<int64_t>(req) * a.K + k;
-        if (none(b)) {
-            for (int i = k + tid; i < a.K; i += kPickThreads) {
-                a.out_scores[out + i - k] = -INFINITY;
-                a.parent[out + i - k] = -1;
-                a.token[out + i - k] = -1;
-            }
-            break;
-        }
-        if (tid == 0) {
-            a.out_scores[out] = static_cast<float>(value_of(b));
-            a.parent[out] = static_cast<int>(b.at / static_cast<uint32_t>(a.V));
-            a.token[out] = static_cast<int>(b.at % static_cast<uint32_t>(a.V));
-        }
-#pragma unroll
-        for (int q = 0; q < Q; q++)
-            if (own[q].at == b.at && !none(own[q])) {
-                const int64_t at = static_cast<int64_t>(b.at) - static_cast<int64_t>(beam[q]) * a.V - first[q];
-#pragma unroll
-                for (int e = 0; e < kPer; e++)
-                    if (place<DT>(lane, e) == at) x[q][e] = -INFINITY;
-                next_own(q);
-            }
-    }
+    join_warps(top, min(4 * picks, kPickWarps), s_lists);
+    if (warp > 0) return;
+    if (lane < a.K) out.put(lane, top.b[0]);
+    if (32 + lane < a.K) out.put(32 + lane, top.b[1]);
 }
 
 int chunks_of(const BeamArgs &a) { return (a.V + kChunk - 1) / kChunk; }
@@ -398,30 +536,32 @@ void plan(const BeamArgs &a, int nsm, BeamParams &p)
     p.chunks = chunks_of(a);
     const int64_t rows = static_cast<int64_t>(a.R) * a.W;
     p.per_warp = 1;
-    while (p.per_warp < 8 && rows * p.chunks / (2 * p.per_warp) >= static_cast<int64_t>(nsm) * 32) p.per_warp *= 2;
+    while (p.per_warp < 16 && rows * p.chunks / (2 * p.per_warp) >= static_cast<int64_t>(nsm) * 32) p.per_warp *= 2;
     const int per_block = kScanWarps * p.per_warp;
     p.splits = (p.chunks + per_block - 1) / per_block;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-template <int DT>
-cudaError_t launch_impl(const BeamParams &p, size_t smem, cudaStream_t stream)
+template <int DT, bool ALIGNED>
+cudaError_t launch_impl(const BeamParams &p, cudaStream_t stream)
 {
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(beam_pick_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
-    beam_scan_kernel<DT><<<dim3(p.splits, p.a.R * p.a.W), kScanThreads, 0, stream>>>(p);
+    beam_scan_kernel<DT, ALIGNED><<<dim3(p.splits, p.a.R * p.a.W), kScanThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_pdl(beam_pick_kernel<DT>, dim3(p.a.R), kPickThreads, smem, stream, p);
+    return launch_pdl(beam_pick_kernel<DT>, dim3(p.a.R), kPickThreads, 0, stream, p);
+}
+
+template <int DT>
+cudaError_t launch_type(const BeamParams &p, cudaStream_t stream)
+{
+    constexpr int64_t size = DT == 2 ? 4 : 2;
+    const BeamArgs &a = p.a;
+    const bool aligned = !((reinterpret_cast<uintptr_t>(a.logits) | a.l_sr * size | a.l_sw * size) & 15);
+    return aligned ? launch_impl<DT, true>(p, stream) : launch_impl<DT, false>(p, stream);
 }
 
 }  // namespace
-
-bool beam_fits(const BeamArgs &a) { return static_cast<int64_t>(a.W) * chunks_of(a) <= kMaxBeamChunks; }
 
 size_t beam_workspace(const BeamArgs &a, int nsm)
 {
@@ -438,10 +578,9 @@ clis_status_t launch_beam(const BeamArgs &a, void *workspace, int nsm, cudaStrea
     const size_t rows = static_cast<size_t>(a.R) * a.W;
     p.lead = static_cast<float *>(workspace);
     p.part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + up256(rows * p.chunks * sizeof(float)));
-    const size_t smem = static_cast<size_t>(a.W) * p.chunks * sizeof(float);
-    const cudaError_t e = a.dtype == CLIS_DT_BF16 ? launch_impl<CLIS_DT_BF16>(p, smem, stream)
-                          : a.dtype == CLIS_DT_FP16 ? launch_impl<CLIS_DT_FP16>(p, smem, stream)
-                                                    : launch_impl<2>(p, smem, stream);
+    const cudaError_t e = a.dtype == CLIS_DT_BF16 ? launch_type<CLIS_DT_BF16>(p, stream)
+                          : a.dtype == CLIS_DT_FP16 ? launch_type<CLIS_DT_FP16>(p, stream)
+                                                    : launch_type<2>(p, stream);
     return e == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
 

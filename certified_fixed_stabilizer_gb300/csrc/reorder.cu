@@ -34,28 +34,20 @@ struct ReorderParams {
     int *back;    // [R][W * width] pages that go back
 };
 
-// What a request wants: pages for copies, and whether its inputs make sense.
-struct Wish {
-    int need;
-    unsigned int bad;
-};
-
-__device__ __forceinline__ Wish wish_of(const ReorderArgs &a, int g)
+// Whether row i wants a page for a copy: an earlier beam of its request goes on from the same
+// one, whose last page is not full.  No row of a request with a number out of range does.
+__device__ __forceinline__ bool wants(const ReorderArgs &a, int i)
 {
-    Wish r = {0, 0u};
     const int cap = a.width << a.page_shift, mask = (1 << a.page_shift) - 1;
-    const int32_t *parent = a.parent + static_cast<int64_t>(g) * a.W, *lens = a.lens + static_cast<int64_t>(g) * a.W;
-    unsigned long long seen = 0;  // beams that some beam has gone on from
-    for (int w = 0; w < a.W; w++) {
-        const int p = __ldg(parent + w), n = __ldg(lens + w);
-        if (n < 0 || n > cap) r.bad |= CLIS_PAGED_LENGTH_BIT;
-        if (p >= a.W) r.bad |= CLIS_PAGED_INDEX_BIT;
-        if (p < 0 || p >= a.W) continue;
-        if ((seen >> p & 1) && (__ldg(lens + p) & mask)) r.need++;
-        seen |= 1ull << p;
+    const int g0 = i - i % a.W, mine = __ldg(a.parent + i);
+    bool bad = false, again = false;
+#pragma unroll 4
+    for (int v = 0; v < a.W; v++) {
+        const int p = __ldg(a.parent + g0 + v), n = __ldg(a.lens + g0 + v);
+        bad |= n < 0 || n > cap || p >= a.W;
+        again |= p == mine && g0 + v < i;
     }
-    if (r.bad) r.need = 0;
-    return r;
+    return !bad && again && mine >= 0 && (__ldg(a.lens + g0 + mine) & mask) != 0;
 }
 
 __device__ __forceinline__ long long warp_sum(long long x)
@@ -74,61 +66,62 @@ __global__ void __launch_bounds__(kTableThreads) reorder_table_kernel(const Reor
     __shared__ int s_src[kMaxBeams], s_len[kMaxBeams], s_have[kMaxBeams], s_pages[kMaxBeams];
     __shared__ int s_copy[kMaxBeams], s_fresh[kMaxBeams];  // place in the list of copies (-1: none), page
     __shared__ bool s_kept[kMaxBeams], s_again[kMaxBeams];
-    __shared__ int s_done, s_rows;
-    __shared__ long long s_before;
+    __shared__ int s_rows;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x, W = a.W;
     const int mask = (1 << a.page_shift) - 1;
     unsigned int bad = 0;
     pdl_launch();
 
-    // ---- pages that the requests before this one take
+    // ---- pages that the requests before this one take, and this one's rows
+    const int64_t row0 = static_cast<int64_t>(g) * W;
+    const int64_t head = a.state_in[0], held = a.state_in[1] - head, F = a.ring_size;
     long long before = 0;
-    for (int i = tid; i < g; i += kTableThreads) before += wish_of(a, i).need;
+    for (int i = tid; i < static_cast<int>(row0); i += kTableThreads) before += wants(a, i);
     before = warp_sum(before);
     if (lane == 0) s_sum[warp] = before;
-    __syncthreads();
-    const int64_t head = a.state_in[0], held = a.state_in[1] - head, F = a.ring_size;
-    if (tid == 0) {
-        before = 0;
-        for (int i = 0; i < kTableWarps; i++) before += s_sum[i];
-        const Wish mine = wish_of(a, g);
-        const bool sane = held >= 0 && held <= F;
-        s_done = !mine.bad && (mine.need == 0 || (sane && before + mine.need <= held));
-        if (!sane || (!mine.bad && !s_done)) bad |= CLIS_PAGED_POOL_BIT;
-        bad |= mine.bad;
-        s_before = before;
-        s_rows = 0;
-        a.done[g] = s_done;
-        p.count[g].x = s_done ? mine.need : 0;
-    }
-    __syncthreads();
-    // A thread per beam: whom it goes on from, and whether it needs a copy.
-    const int64_t row0 = static_cast<int64_t>(g) * W;
-    int src = -1, len = 0;
-    if (tid < W) {
-        const int n = __ldg(a.lens + row0 + tid), ok = min(max(n, 0), a.width << a.page_shift);
+    int parent = -1, n = 0;
+    bool wrong = false;
+    if (tid < W) {  // a thread per beam
+        parent = __ldg(a.parent + row0 + tid);
+        n = __ldg(a.lens + row0 + tid);
+        s_src[tid] = parent;
         s_len[tid] = n;
+        const int cap = a.width << a.page_shift, ok = min(max(n, 0), cap);
+        if (n != ok) bad |= CLIS_PAGED_LENGTH_BIT;
+        if (parent >= W) bad |= CLIS_PAGED_INDEX_BIT;
+        wrong = bad != 0;
         s_have[tid] = (ok >> a.page_shift) + ((ok & mask) ? 1 : 0);
-        atomicMax(&s_rows, s_have[tid]);
-        src = s_done ? __ldg(a.parent + row0 + tid) : tid;
-        s_src[tid] = src;
         s_kept[tid] = false;
     }
-    __syncthreads();
+    wrong = __syncthreads_or(wrong);
+    before = 0;
+    for (int i = 0; i < kTableWarps; i++) before += s_sum[i];
+    bool again = false;
+    if (tid < W && !wrong && parent >= 0 && (s_len[parent] & mask) != 0)
+        for (int v = 0; v < tid; v++) again |= s_src[v] == parent;
+    const int need = __syncthreads_count(again);
+    const bool sane = held >= 0 && held <= F;
+    const bool done = !wrong && (need == 0 || (sane && before + need <= held));
+    if (tid == 0) {
+        if (!sane || (!wrong && !done)) bad |= CLIS_PAGED_POOL_BIT;
+        a.done[g] = done;
+        p.count[g].x = done ? need : 0;
+        s_rows = 0;
+    }
     if (tid < W) {
-        len = src < 0 ? 0 : s_len[src];
-        a.lens_out[row0 + tid] = len;
-        s_pages[tid] = src < 0 ? 0 : s_have[src];
-        bool again = false;
-        for (int v = 0; v < tid; v++) again |= s_src[v] == src;
-        if (src >= 0) s_kept[src] = true;  // (several threads write the same)
-        s_again[tid] = again && src >= 0 && (len & mask) != 0 && s_done;
+        s_again[tid] = again && done;
+        if (!done) s_src[tid] = tid;
     }
     __syncthreads();
     if (tid < W) {
+        atomicMax(&s_rows, s_have[tid]);
+        const int src = s_src[tid], len = src < 0 ? 0 : s_len[src];
+        a.lens_out[row0 + tid] = len;
+        s_pages[tid] = src < 0 ? 0 : s_have[src];
+        if (src >= 0) s_kept[src] = true;  // (several threads write the same)
         s_copy[tid] = -1;
         if (s_again[tid]) {
-            long long i = s_before;
+            long long i = before;
             for (int v = 0; v < tid; v++) i += s_again[v];
             // (i is below the number of pages that the ring holds)
             const int page = __ldg(a.ring + (((head % F) + F) % F + i) % F);
@@ -141,7 +134,6 @@ __global__ void __launch_bounds__(kTableThreads) reorder_table_kernel(const Reor
     __syncthreads();
 
     // ---- the tables, a tile of columns at a time
-    const bool done = s_done != 0;
     int base = 0;  // pages that went back in the columns before
     for (int c0 = 0; c0 < a.width; c0 += p.tile) {
         const int cols = min(p.tile, a.width - c0);
@@ -153,17 +145,22 @@ __global__ void __launch_bounds__(kTableThreads) reorder_table_kernel(const Reor
         __syncthreads();
         // (a thread has at most one column: tile <= kTableThreads)
         const int c = tid, col = c0 + c;
-        auto gone = [&](int w) -> bool {  // beam w's page of this column goes back, and beam w says so
-            if (s_kept[w] || col >= s_have[w]) return false;
-            const int page = s_tab[w * p.tile + c];
-            for (int v = 0; v < W; v++)
-                if (v != w && col < s_have[v] && s_tab[v * p.tile + c] == page && (s_kept[v] || v < w)) return false;
-            return true;
-        };
+        // Beams whose page of this column goes back, each page once: no beam that somebody goes on
+        // from names it, nor an earlier one.
+        uint64_t gone = 0;
         int mine = 0;
         if (c < cols) {
             if (done && c0 < s_rows)
-                for (int w = 0; w < W; w++) mine += gone(w);
+                for (int w = 0; w < W; w++) {
+                    if (s_kept[w] || col >= s_have[w]) continue;
+                    const int page = s_tab[w * p.tile + c];
+                    bool stays = false;
+#pragma unroll 4
+                    for (int v = 0; v < W; v++)
+                        stays |= v != w && col < s_have[v] && (s_kept[v] || v < w) && s_tab[v * p.tile + c] == page;
+                    gone |= static_cast<uint64_t>(!stays) << w;
+                }
+            mine = __popcll(gone);
             for (int w = 0; w < W; w++) {
                 int page = -1;
                 if (col < s_pages[w]) {
@@ -190,13 +187,11 @@ __global__ void __launch_bounds__(kTableThreads) reorder_table_kernel(const Reor
             if (i < warp) at += s_scan[i];
             base += s_scan[i];
         }
-        if (mine > 0)
-            for (int w = 0; w < W; w++)
-                if (gone(w)) {
-                    const int page = s_tab[w * p.tile + c];
-                    if (page < 0 || page >= a.num_pages) bad |= CLIS_PAGED_INDEX_BIT;
-                    p.back[static_cast<int64_t>(g) * W * a.width + at++] = page;
-                }
+        for (; gone; gone &= gone - 1) {
+            const int page = s_tab[(__ffsll(gone) - 1) * p.tile + c];
+            if (page < 0 || page >= a.num_pages) bad |= CLIS_PAGED_INDEX_BIT;
+            p.back[static_cast<int64_t>(g) * W * a.width + at++] = page;
+        }
         __syncthreads();  // (the tile is loaded again)
     }
     if (tid == 0) p.count[g].y = base;
@@ -227,6 +222,29 @@ __device__ __forceinline__ longlong2 counts_before(const ReorderParams &p, int g
         r.y += s[i][1];
     }
     return r;
+}
+
+// The first `rows` rows of all heads of a page, by a block; four pieces a thread in flight.
+template <typename T>
+__device__ __forceinline__ void copy_rows(const uint8_t *from, uint8_t *to, const clis_pages_t &x, int rows, int tid)
+{
+    const uint32_t per = static_cast<uint32_t>(x.row_bytes) / sizeof(T), one = rows * per, total = static_cast<uint32_t>(x.heads) * one;
+    constexpr int B = 4;
+    for (uint32_t i0 = tid; i0 < total; i0 += B * kCopyThreads) {
+        T v[B];
+        int64_t at[B];
+#pragma unroll
+        for (int b = 0; b < B; b++) {
+            const uint32_t i = i0 + b * kCopyThreads;
+            if (i >= total) continue;
+            const uint32_t h = i / one, e = i - h * one, r = e / per;
+            at[b] = h * x.sh + r * x.sn + (e - r * per) * sizeof(T);
+            v[b] = *reinterpret_cast<const T *>(from + at[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < B; b++)
+            if (i0 + b * kCopyThreads < total) *reinterpret_cast<T *>(to + at[b]) = v[b];
+    }
 }
 
 __global__ void __launch_bounds__(kCopyThreads) reorder_copy_kernel(const ReorderParams p)
@@ -267,15 +285,8 @@ __global__ void __launch_bounds__(kCopyThreads) reorder_copy_kernel(const Reorde
         const clis_pages_t &x = a.t[t];
         const uint8_t *from = static_cast<const uint8_t *>(x.base) + l * x.sl + c.x * x.sp;
         uint8_t *to = static_cast<uint8_t *>(x.base) + l * x.sl + c.y * x.sp;
-        const bool vec = a.vec[t] != 0;
-        const int size = vec ? 16 : 4, per = static_cast<int>(x.row_bytes) / size, one = c.z * per;
-        const int total = static_cast<int>(x.heads) * one;
-        for (int i = tid; i < total; i += kCopyThreads) {
-            const int h = i / one, e = i - h * one, r = e / per;
-            const int64_t at = h * x.sh + r * x.sn + (e - r * per) * size;
-            if (vec) *reinterpret_cast<uint4 *>(to + at) = *reinterpret_cast<const uint4 *>(from + at);
-            else *reinterpret_cast<uint32_t *>(to + at) = *reinterpret_cast<const uint32_t *>(from + at);
-        }
+        if (a.vec[t]) copy_rows<uint4>(from, to, x, c.z, tid);
+        else copy_rows<uint32_t>(from, to, x, c.z, tid);
     }
     if (bad) atomicOr(&g_reorder_error_word, bad);
 }
@@ -305,7 +316,7 @@ clis_status_t launch_reorder(const ReorderArgs &a, void *workspace, int nsm, cud
     reorder_table_kernel<<<a.R, kTableThreads, p.tile * a.W * sizeof(int), stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
     // (blocks without a copy or a request of their own end at once)
-    return launch_pdl(reorder_copy_kernel, dim3(4 * nsm), kCopyThreads, 0, stream, p) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
+    return launch_pdl(reorder_copy_kernel, dim3(8 * nsm), kCopyThreads, 0, stream, p) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
 
 clis_status_t read_reorder_error(uint32_t *code)

@@ -699,8 +699,7 @@ CLIS_API clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const cl
  * none (a masked token, -inf; every token of a beam whose score is -inf, or whose logits
  * hold a NaN or +inf); where fewer than K are left, the places behind get the score
  * -inf, parent -1 and token -1.
- *   R, W, V, K   R * W up to 65535, W and K up to 64, W * V up to 2^31 - 1 and
- *                W * ceil(V / 512) up to 49152 (25 million continuations of a request)
+ *   R, W, V, K   R * W up to 65535, W and K up to 64, W * V up to 2^31 - 1
  *   dtype        0 bf16, 1 fp16 (clis_dtype_t), 2 fp32
  *   l_sr, l_sw   strides of the logits in elements, any >= 0 (rows need no alignment
  *                beyond their type's)
@@ -709,7 +708,7 @@ CLIS_API clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const cl
  *   out_scores, parent, token  device fp32, int32, int32 [R, K]
  *   workspace    device scratch of clis_beam_workspace_size() bytes (on the current
  *                device), 256-byte aligned; not shared by calls that may run at the same time
- * Values are compared in 64 bits with a logarithm off by about 1e-7.  Reruns agree bit
+ * Values are compared to 48 bits, with a logarithm off by about 1e-7.  Reruns agree bit
  * for bit.  Errors as for clis_attn_fwd; CLIS_ERR_WORKSPACE. */
 typedef struct {
     int64_t R, W, V, K;
