@@ -4,8 +4,9 @@
 //
 //   x = code * scale, rounded once to the data type (a cache of 16-bit values is copied)
 //
-// Bound: bytes, d + 4 read and 2 d written per row.  A thread turns 16 codes into two
-// 16-byte stores; four such pieces are in flight at a time.
+// Bound: bytes, d + 4 read and 2 d written per row.  A thread turns 8 codes into one 16-byte
+// store, so that a warp's stores fill whole lines (16 codes and two stores a thread: 124 us
+// for 120,000 rows of 8 heads, K and V, 600 MB); eight such pieces are in flight at a time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -21,7 +22,7 @@ namespace {
 
 constexpr int kReadThreads = 256;
 constexpr int kReadTokens = 32;  // of a block: a warp looks up their places
-constexpr int kBatch = 4;        // pieces in flight
+constexpr int kBatch = 8;        // pieces in flight
 
 __device__ __forceinline__ float2 e4m3_floats(uint32_t lo16)
 {
@@ -48,21 +49,21 @@ __device__ __forceinline__ void values4(uint32_t w, float scale, float *f)
     }
 }
 
-// A piece: 16 elements of a row.
+// A piece: 8 elements of a row.
 struct Piece {
-    uint4 u, w;  // codes in u; 16-bit values in u and w
+    uint4 u;  // codes in x and y, or 16-bit values
     float scale;
 };
 
 template <int CODE>
-__device__ __forceinline__ void load_piece(Piece &x, const uint8_t *row, const float *scale, int chunk)
+__device__ __forceinline__ void load_piece(Piece &x, const uint8_t *row, const float *scale, int piece)
 {
     if (CODE < 0) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(row + chunk * 32);
-        x.u = __ldg(src);
-        x.w = __ldg(src + 1);
+        x.u = __ldg(reinterpret_cast<const uint4 *>(row) + piece);
     } else {
-        x.u = __ldg(reinterpret_cast<const uint4 *>(row + chunk * 16));
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row) + piece);
+        x.u.x = v.x;
+        x.u.y = v.y;
         x.scale = __ldg(scale);
     }
 }
@@ -70,25 +71,77 @@ __device__ __forceinline__ void load_piece(Piece &x, const uint8_t *row, const f
 template <int CODE, int DT>
 __device__ __forceinline__ void store_piece(const Piece &x, uint16_t *dst)
 {
-    uint4 y0 = x.u, y1 = x.w;
+    uint4 y = x.u;
     if (CODE >= 0) {
-        float f[16];
+        float f[8];
         values4<CODE>(x.u.x, x.scale, f);
         values4<CODE>(x.u.y, x.scale, f + 4);
-        values4<CODE>(x.u.z, x.scale, f + 8);
-        values4<CODE>(x.u.w, x.scale, f + 12);
-        y0 = make_uint4(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]), pack2<DT>(f[4], f[5]), pack2<DT>(f[6], f[7]));
-        y1 = make_uint4(pack2<DT>(f[8], f[9]), pack2<DT>(f[10], f[11]), pack2<DT>(f[12], f[13]), pack2<DT>(f[14], f[15]));
+        y = make_uint4(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]), pack2<DT>(f[4], f[5]), pack2<DT>(f[6], f[7]));
     }
-    reinterpret_cast<uint4 *>(dst)[0] = y0;
-    reinterpret_cast<uint4 *>(dst)[1] = y1;
+    *reinterpret_cast<uint4 *>(dst) = y;
 }
 
-// A token's place: page (-1: reads as zeros, -2: not written) and row of it.
-template <int CODE, int DT>
+// 32 tokens of both caches by a block.  Iteration `it` is head it / IPH of K's heads, then of V's;
+// a thread has one piece of a token in it, of the same IPH tokens throughout, so that their
+// places are looked up and multiplied out once.
+template <int D>
+struct Split {
+    static constexpr int PPR = D / 8, IPH = kReadTokens * PPR / kReadThreads;  // pieces of a row, iterations of a head
+    static constexpr int PER = kReadTokens / IPH;                             // tokens of an iteration
+};
+
+// One token's rows: where they lie in the caches and where they go.  from: 0 nowhere (reads as
+// zeros), 1 there; to: whether they are written.
+struct Token {
+    int64_t kc, vc, ks, vs, ko, vo;
+    bool from, to;
+};
+
+// Heads it0 / IPH .. of the block's tokens, kBatch pieces in flight.  SCALED: K's values (else its
+// codes as they are, and its scales to k_scale at their offset `ko` / D of the row).
+template <int CODE, int DT, int D, bool SCALED>
+__device__ __forceinline__ void convert(const uint8_t *kc, const uint8_t *vc, const float *ks, const float *vs, int64_t kc_sh, int64_t vc_sh,
+                                        int64_t ks_sh, int64_t vs_sh, uint16_t *ko, uint16_t *vo, int64_t ko_sh, int64_t vo_sh, float *k_scale,
+                                        int64_t k_scale_sh, int Hkv, const Token *tok, int it0, int step)
+{
+    using S = Split<D>;
+    constexpr int B = CODE < 0 ? 2 : 1;
+    const int piece = threadIdx.x & (S::PPR - 1);
+    for (; it0 < 2 * Hkv * S::IPH; it0 += step) {
+        Piece x[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; b++) {
+            const int hh = (it0 + b) / S::IPH;
+            const Token &t = tok[b % S::IPH];
+            x[b].u = make_uint4(0, 0, 0, 0);
+            x[b].scale = 0.f;
+            if (hh >= 2 * Hkv || !t.from || !t.to) continue;
+            if (hh < Hkv) load_piece<CODE>(x[b], kc + (t.kc + hh * kc_sh) * B, ks + t.ks + hh * ks_sh, piece);
+            else load_piece<CODE>(x[b], vc + (t.vc + (hh - Hkv) * vc_sh) * B, vs + t.vs + (hh - Hkv) * vs_sh, piece);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; b++) {
+            const int hh = (it0 + b) / S::IPH;
+            const Token &t = tok[b % S::IPH];
+            if (hh >= 2 * Hkv || !t.to) continue;
+            if (hh < Hkv) {
+                if (!SCALED) {
+                    if (piece == 0) k_scale[t.ko / D + hh * k_scale_sh] = x[b].scale;
+                    x[b].scale = 1.f;
+                }
+                store_piece<CODE, DT>(x[b], ko + t.ko + hh * ko_sh + piece * 8);
+            } else {
+                store_piece<CODE, DT>(x[b], vo + t.vo + (hh - Hkv) * vo_sh + piece * 8);
+            }
+        }
+    }
+}
+
+template <int CODE, int DT, int D>
 __global__ void __launch_bounds__(kReadThreads) paged_read_kernel(const ReadArgs a)
 {
-    __shared__ int2 s_at[kReadTokens];
+    using S = Split<D>;
+    __shared__ int2 s_at[kReadTokens];  // page (-1: reads as zeros, -2: not written) and row of it
     const int t0 = blockIdx.x * kReadTokens;
     if (threadIdx.x < kReadTokens) {
         const int t = t0 + threadIdx.x;
@@ -124,40 +177,23 @@ __global__ void __launch_bounds__(kReadThreads) paged_read_kernel(const ReadArgs
         if (bad) atomicOr(&g_read_error_word, bad);
     }
     __syncthreads();
-    const int cpr = a.d >> 4, shift = a.d == 128 ? 3 : 2;  // pieces of a row
-    const int all = kReadTokens * cpr * a.Hkv;
-    for (int i0 = blockIdx.y * kReadThreads * kBatch + threadIdx.x; i0 < all; i0 += gridDim.y * kReadThreads * kBatch) {
-        Piece k[kBatch], v[kBatch];
-        int2 at[kBatch];
+    Token tok[S::IPH];
 #pragma unroll
-        for (int b = 0; b < kBatch; b++) {
-            const int i = i0 + b * kReadThreads, chunk = i & (cpr - 1), t = (i >> shift) & (kReadTokens - 1), h = (i >> shift) / kReadTokens;
-            at[b] = i < all ? s_at[t] : make_int2(-2, 0);
-            k[b].u = k[b].w = v[b].u = v[b].w = make_uint4(0, 0, 0, 0);
-            k[b].scale = v[b].scale = 0.f;
-            if (at[b].x < 0) continue;
-            const int64_t pg = at[b].x, in = at[b].y;
-            constexpr int B = CODE < 0 ? 2 : 1;
-            load_piece<CODE>(k[b], a.z.kc + (pg * a.kc_sp + h * a.kc_sh + in * a.kc_sn) * B,
-                             a.z.ks + pg * a.z.ks_sp + h * a.z.ks_sh + in * a.z.ks_sn, chunk);
-            load_piece<CODE>(v[b], a.z.vc + (pg * a.vc_sp + h * a.vc_sh + in * a.vc_sn) * B,
-                             a.z.vs + pg * a.z.vs_sp + h * a.z.vs_sh + in * a.z.vs_sn, chunk);
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; b++) {
-            if (at[b].x == -2) continue;
-            const int i = i0 + b * kReadThreads, chunk = i & (cpr - 1), t = (i >> shift) & (kReadTokens - 1), h = (i >> shift) / kReadTokens;
-            const int64_t row = t0 + t;
-            store_piece<CODE, DT>(k[b], a.ko + row * a.ko_st + h * a.ko_sh + chunk * 16);
-            store_piece<CODE, DT>(v[b], a.vo + row * a.vo_st + h * a.vo_sh + chunk * 16);
-        }
+    for (int i = 0; i < S::IPH; i++) {
+        const int t = i * S::PER + threadIdx.x / S::PPR;
+        const int2 at = s_at[t];
+        const int64_t pg = max(at.x, 0), in = at.y, row = t0 + t;
+        tok[i] = {pg * a.kc_sp + in * a.kc_sn, pg * a.vc_sp + in * a.vc_sn, pg * a.z.ks_sp + in * a.z.ks_sn, pg * a.z.vs_sp + in * a.z.vs_sn,
+                  row * a.ko_st, row * a.vo_st, at.x >= 0, at.x != -2};
     }
+    convert<CODE, DT, D, true>(a.z.kc, a.z.vc, a.z.ks, a.z.vs, a.kc_sh, a.vc_sh, a.z.ks_sh, a.z.vs_sh, a.ko, a.vo, a.ko_sh, a.vo_sh, nullptr, 0,
+                               a.Hkv, tok, blockIdx.y * kBatch, gridDim.y * kBatch);
 }
 
 // Whole pages, for the chunk kernel (K's codes stay unscaled: its softmax applies the scales).  Units of 32 keys (all heads) of the sequences that
 // it works on, laid end to end and cut into equal runs, one per block.  Two sequences
 // that share a page write the same bits.
-constexpr int kUnitKeys = 32;
+constexpr int kUnitKeys = kReadTokens;
 
 struct UnpackParams {
     PagedArgs a;
@@ -167,7 +203,7 @@ struct UnpackParams {
     int g, rows_small;
 };
 
-template <int CODE, int DT>
+template <int CODE, int DT, int D>
 __global__ void __launch_bounds__(kReadThreads) paged_unpack_kernel(const UnpackParams p)
 {
     const PagedArgs &a = p.a;
@@ -216,36 +252,22 @@ __global__ void __launch_bounds__(kReadThreads) paged_unpack_kernel(const Unpack
     __syncthreads();
     if (u0 >= u1) return;
     int s = s_seq, j = s_unit, n = units(s), kv = seq_len(s).kv;
-    const int cpr = a.d >> 4, shift = a.d == 128 ? 3 : 2, page = 1 << a.page_shift;
-    const int all = kUnitKeys * cpr * a.Hkv;
+    using S = Split<D>;
+    const int mask = (1 << a.page_shift) - 1;
+    const int64_t head = static_cast<int64_t>(D) << a.page_shift;  // values of a head's page
     for (unsigned long long u = u0; u < u1; u++) {
-        for (int i0 = tid; i0 < all; i0 += kReadThreads * kBatch) {
-            Piece k[kBatch], v[kBatch];
-            int64_t to[kBatch];
+        Token tok[S::IPH];
 #pragma unroll
-            for (int b = 0; b < kBatch; b++) {
-                const int i = i0 + b * kReadThreads, chunk = i & (cpr - 1), h = (i >> shift) / kUnitKeys;
-                const int key = j * kUnitKeys + ((i >> shift) & (kUnitKeys - 1));
-                to[b] = -1;
-                if (i >= all || key >= kv) continue;
-                const int pg = __ldg(a.block_table + s * a.bt_s + (key >> a.page_shift));
-                if (pg < 0 || pg >= a.num_pages) continue;  // (the chunk kernel records it)
-                const int64_t in = key & (page - 1);
-                load_piece<CODE>(k[b], z.kc + pg * a.kc_sp + h * a.kc_sh + in * a.kc_sn, z.ks + pg * z.ks_sp + h * z.ks_sh + in * z.ks_sn,
-                                 chunk);
-                load_piece<CODE>(v[b], z.vc + pg * a.vc_sp + h * a.vc_sh + in * a.vc_sn, z.vs + pg * z.vs_sp + h * z.vs_sh + in * z.vs_sn,
-                                 chunk);
-                to[b] = (((static_cast<int64_t>(pg) * a.Hkv + h) << a.page_shift) + in) * a.d + chunk * 16;
-            }
-#pragma unroll
-            for (int b = 0; b < kBatch; b++) {
-                if (to[b] < 0) continue;
-                if ((to[b] & (a.d - 1)) == 0) p.ks[to[b] / a.d] = k[b].scale;
-                k[b].scale = 1.f;  // (the codes as they are)
-                store_piece<CODE, DT>(k[b], p.ko + to[b]);
-                store_piece<CODE, DT>(v[b], p.vo + to[b]);
-            }
+        for (int i = 0; i < S::IPH; i++) {
+            const int key = j * kUnitKeys + i * S::PER + threadIdx.x / S::PPR;
+            const int page = key < kv ? __ldg(a.block_table + s * a.bt_s + (key >> a.page_shift)) : -1;
+            const bool ok = page >= 0 && page < a.num_pages;  // (the chunk kernel records the others)
+            const int64_t pg = ok ? page : 0, in = key & mask, to = pg * a.Hkv * head + in * D;
+            tok[i] = {pg * a.kc_sp + in * a.kc_sn, pg * a.vc_sp + in * a.vc_sn, pg * z.ks_sp + in * z.ks_sn, pg * z.vs_sp + in * z.vs_sn,
+                      to, to, ok, ok};
         }
+        convert<CODE, DT, D, false>(z.kc, z.vc, z.ks, z.vs, a.kc_sh, a.vc_sh, z.ks_sh, z.vs_sh, p.ko, p.vo, head, head, p.ks, mask + 1, a.Hkv,
+                                    tok, 0, kBatch);
         if (++j == n && u + 1 < u1) {
             do s++;
             while (s + 1 < a.S && units(s) == 0);
@@ -256,19 +278,19 @@ __global__ void __launch_bounds__(kReadThreads) paged_unpack_kernel(const Unpack
     }
 }
 
-template <int CODE>
+template <int CODE, int DT>
 cudaError_t launch_read_impl(const ReadArgs &a, dim3 grid, cudaStream_t stream)
 {
-    if (a.dtype == CLIS_DT_FP16 || CODE < 0) paged_read_kernel<CODE, 1><<<grid, kReadThreads, 0, stream>>>(a);
-    else paged_read_kernel<CODE, 0><<<grid, kReadThreads, 0, stream>>>(a);
+    if (a.d == 128) paged_read_kernel<CODE, DT, 128><<<grid, kReadThreads, 0, stream>>>(a);
+    else paged_read_kernel<CODE, DT, 64><<<grid, kReadThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
-template <int CODE>
+template <int CODE, int DT>
 cudaError_t launch_unpack_impl(const UnpackParams &p, int grid, cudaStream_t stream)
 {
-    if (p.a.dtype == CLIS_DT_FP16) paged_unpack_kernel<CODE, 1><<<grid, kReadThreads, 0, stream>>>(p);
-    else paged_unpack_kernel<CODE, 0><<<grid, kReadThreads, 0, stream>>>(p);
+    if (p.a.d == 128) paged_unpack_kernel<CODE, DT, 128><<<grid, kReadThreads, 0, stream>>>(p);
+    else paged_unpack_kernel<CODE, DT, 64><<<grid, kReadThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -278,13 +300,15 @@ clis_status_t launch_paged_read(const ReadArgs &a, cudaStream_t stream)
 {
     const int64_t blocks = (static_cast<int64_t>(a.T) + kReadTokens - 1) / kReadTokens;
     // Blocks share out a token group's heads where there are few groups.
-    const int pieces = kReadTokens * (a.d >> 4) * a.Hkv;
-    int split = (pieces + kReadThreads * kBatch - 1) / (kReadThreads * kBatch);
-    if (blocks >= 152 * 8) split = 1;
+    const int its = 2 * a.Hkv * kReadTokens * (a.d / 8) / kReadThreads;
+    const int split = blocks >= 152 * 8 ? 1 : (its + kBatch - 1) / kBatch;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
-    const cudaError_t e = a.z.code < 0 ? launch_read_impl<-1>(a, grid, stream)
-                          : a.z.code == CLIS_CODE_INT8 ? launch_read_impl<CLIS_CODE_INT8>(a, grid, stream)
-                                                       : launch_read_impl<CLIS_CODE_E4M3>(a, grid, stream);
+    const bool half = a.dtype == CLIS_DT_FP16;
+    const cudaError_t e = a.z.code < 0                 ? launch_read_impl<-1, 0>(a, grid, stream)  // (the type does not matter)
+                          : a.z.code == CLIS_CODE_INT8 ? (half ? launch_read_impl<CLIS_CODE_INT8, 1>(a, grid, stream)
+                                                               : launch_read_impl<CLIS_CODE_INT8, 0>(a, grid, stream))
+                                                       : (half ? launch_read_impl<CLIS_CODE_E4M3, 1>(a, grid, stream)
+                                                               : launch_read_impl<CLIS_CODE_E4M3, 0>(a, grid, stream));
     return e == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
 
@@ -293,8 +317,11 @@ clis_status_t launch_paged_unpack(const PagedArgs &a, const QuantArgs &z, int ro
 {
     const UnpackParams p{a, z, k_pages, v_pages, k_scale, a.H / a.Hkv, rows_small};
     const int grid = 8 * nsm;
-    const cudaError_t e = z.code == CLIS_CODE_INT8 ? launch_unpack_impl<CLIS_CODE_INT8>(p, grid, stream)
-                                                   : launch_unpack_impl<CLIS_CODE_E4M3>(p, grid, stream);
+    const bool half = a.dtype == CLIS_DT_FP16;
+    const cudaError_t e = z.code == CLIS_CODE_INT8 ? (half ? launch_unpack_impl<CLIS_CODE_INT8, 1>(p, grid, stream)
+                                                           : launch_unpack_impl<CLIS_CODE_INT8, 0>(p, grid, stream))
+                                                   : (half ? launch_unpack_impl<CLIS_CODE_E4M3, 1>(p, grid, stream)
+                                                           : launch_unpack_impl<CLIS_CODE_E4M3, 0>(p, grid, stream));
     return e == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
 

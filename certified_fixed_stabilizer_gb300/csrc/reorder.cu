@@ -224,26 +224,31 @@ __device__ __forceinline__ longlong2 counts_before(const ReorderParams &p, int g
     return r;
 }
 
-// The first `rows` rows of all heads of a page, by a block; four pieces a thread in flight.
+// The first `rows` rows of all heads of a page, by a block: a warp per head, four pieces a
+// lane in flight.
 template <typename T>
 __device__ __forceinline__ void copy_rows(const uint8_t *from, uint8_t *to, const clis_pages_t &x, int rows, int tid)
 {
-    const uint32_t per = static_cast<uint32_t>(x.row_bytes) / sizeof(T), one = rows * per, total = static_cast<uint32_t>(x.heads) * one;
+    const uint32_t per = static_cast<uint32_t>(x.row_bytes) / sizeof(T), one = rows * per;
+    const bool dense = x.sn == x.row_bytes;  // rows follow each other
     constexpr int B = 4;
-    for (uint32_t i0 = tid; i0 < total; i0 += B * kCopyThreads) {
-        T v[B];
-        int64_t at[B];
+    for (int h = tid >> 5; h < x.heads; h += kCopyWarps) {
+        const int64_t head = h * x.sh;
+        for (uint32_t i0 = tid & 31; i0 < one; i0 += B * 32) {
+            T v[B];
+            int64_t at[B];
 #pragma unroll
-        for (int b = 0; b < B; b++) {
-            const uint32_t i = i0 + b * kCopyThreads;
-            if (i >= total) continue;
-            const uint32_t h = i / one, e = i - h * one, r = e / per;
-            at[b] = h * x.sh + r * x.sn + (e - r * per) * sizeof(T);
-            v[b] = *reinterpret_cast<const T *>(from + at[b]);
+            for (int b = 0; b < B; b++) {
+                const uint32_t i = i0 + b * 32;
+                if (i >= one) continue;
+                const uint32_t r = dense ? 0 : i / per;
+                at[b] = head + r * x.sn + (i - r * per) * sizeof(T);
+                v[b] = *reinterpret_cast<const T *>(from + at[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < B; b++)
+                if (i0 + b * 32 < one) *reinterpret_cast<T *>(to + at[b]) = v[b];
         }
-#pragma unroll
-        for (int b = 0; b < B; b++)
-            if (i0 + b * kCopyThreads < total) *reinterpret_cast<T *>(to + at[b]) = v[b];
     }
 }
 
