@@ -54,6 +54,18 @@ class QuantDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("code", "ks_sp", "ks_sh", "ks_sn", "vs_sp", "vs_sh", "vs_sn")]
 
 
+class BeamDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("R", "W", "V", "K", "dtype", "l_sr", "l_sw")]
+
+
+class ReorderDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("groups", "beams", "width", "page_size", "num_pages", "bt_ss", "bo_ss")]
+
+
+class PagesDesc(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("layers", "heads", "row_bytes", "sl", "sp", "sh", "sn")]
+
+
 class RopeDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in (
         "B", "Hq", "Hk", "N", "d", "pairs", "axes", "interleaved", "inverse",
@@ -158,13 +170,14 @@ def load_library():
     lib.clis_attn_paged_workspace_size.restype = i32
     lib.clis_attn_fwd_paged.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, vp, i64, f32, i32, vp, sz, vp]
     lib.clis_attn_fwd_paged.restype = i32
-    lib.clis_beam_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    bp, op, gp = ctypes.POINTER(BeamDesc), ctypes.POINTER(ReorderDesc), ctypes.POINTER(PagesDesc)
+    lib.clis_beam_workspace_size.argtypes = [bp, ctypes.POINTER(sz)]
     lib.clis_beam_workspace_size.restype = i32
-    lib.clis_beam_select.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.clis_beam_select.argtypes = [bp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.clis_beam_select.restype = i32
-    lib.clis_paged_reorder_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    lib.clis_paged_reorder_workspace_size.argtypes = [op, ctypes.POINTER(sz)]
     lib.clis_paged_reorder_workspace_size.restype = i32
-    lib.clis_paged_reorder.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, vp, sz, vp]
+    lib.clis_paged_reorder.argtypes = [op, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, gp, i64, vp, sz, vp]
     lib.clis_paged_reorder.restype = i32
     zp = ctypes.POINTER(QuantDesc)
     lib.clis_paged_append_q8.argtypes = [pp, zp, rp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -180,7 +193,8 @@ def load_library():
 
 
 def load_binding():
-    """Load the torch binding of rope, paged_plan, paged_append and attention_paged
+    """Load the torch binding of rope, paged_plan, paged_append, paged_read, attention_paged,
+    beam_select and paged_reorder
     (building it first when it is missing, older than its source or built against another
     torch; there is no fallback: without it these calls raise)."""
     global _native
@@ -957,7 +971,7 @@ class BeamChoice(NamedTuple):
 
 def clis_beam_select(logits, scores, num: int, workspace=None, stream=None) -> BeamChoice:
     """Of each request's continuations (beam w, token v) the ``num`` best by scores[r, w] +
-    log_softmax(logits[r, w])[v]; ties go to the lowest w * V + v.  logits [R, W, V] in bfloat16,
+    logits[r, w, v] - logsumexp(logits[r, w]); ties go to the lowest w * V + v.  logits [R, W, V] in bfloat16,
     float16 or float32 (any row strides), scores float32 [R, W] (-inf: a beam not in use; -inf
     logits: masked tokens).  At most 64 beams and 64 continuations.  With beams that end at a
     token, ask for twice as many as go on.  Where fewer are left, scores are -inf, parent and

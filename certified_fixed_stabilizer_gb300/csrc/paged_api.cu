@@ -121,6 +121,9 @@ clis_status_t check_quant(const clis_paged_t *p, const clis_quant_t *z, bool wri
     if (z->code != CLIS_CODE_INT8 && z->code != CLIS_CODE_E4M3) return CLIS_ERR_INVALID_ARG;
     for (int64_t s : {p->kc_sp, p->kc_sh, p->kc_sn, p->vc_sp, p->vc_sh, p->vc_sn})
         if (s & 15) return CLIS_ERR_MISALIGNED;
+    const int64_t kc[3][2] = {{p->num_pages, p->kc_sp}, {p->Hkv, p->kc_sh}, {p->page_size, p->kc_sn}};
+    const int64_t vc[3][2] = {{p->num_pages, p->vc_sp}, {p->Hkv, p->vc_sh}, {p->page_size, p->vc_sn}};
+    if (overlapping(p->d, kc, 3) || overlapping(p->d, vc, 3)) return CLIS_ERR_INVALID_ARG;
     for (int64_t s : {z->ks_sp, z->ks_sh, z->ks_sn, z->vs_sp, z->vs_sh, z->vs_sn}) {
         if (s < 0) return CLIS_ERR_INVALID_ARG;
         if (s >= (int64_t(1) << 38)) return CLIS_ERR_UNSUPPORTED;

@@ -94,11 +94,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t at)
     return v;
 }
 
-__device__ __forceinline__ void sts128(uint32_t at, uint4 v)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 __device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b)
 {
     uint32_t r;

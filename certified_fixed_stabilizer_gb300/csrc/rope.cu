@@ -104,7 +104,8 @@ __device__ __forceinline__ void rotate8f(const uint4 &u0, const uint4 &u1, float
 }
 
 // Eight values times `mul` as codes.  int8: adding 1.5 * 2^23 leaves the nearest whole
-// number (ties to even) in the low bits; |value * mul| is at most 127.
+// number (ties to even) in the low bits; |value * mul| is at most 127.  The product is rounded
+// first: ties (16-bit values meet them) are then those of value * mul in fp32.
 template <int CODE>
 __device__ __forceinline__ uint2 codes8(const float *f, float mul)
 {
@@ -113,7 +114,7 @@ __device__ __forceinline__ uint2 codes8(const float *f, float mul)
                           pack_e4m3x4(f[4] * mul, f[5] * mul, f[6] * mul, f[7] * mul));
     uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < 8; e++) w[e] = __float_as_uint(fmaf(f[e], mul, 12582912.f));
+    for (int e = 0; e < 8; e++) w[e] = __float_as_uint(__fadd_rn(__fmul_rn(f[e], mul), 12582912.f));
     return make_uint2(__byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410),
                       __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
 }

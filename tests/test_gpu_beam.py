@@ -401,3 +401,79 @@ def test_a_search(dtype):
     head_, tail = cache.ring_state.tolist()
     assert tail - head_ == 200 and cache.lens.tolist() == [0] * (R * W)
     assert sorted(cache.ring[(head_ + torch.arange(200, device="cuda")) % 200].tolist()) == list(range(200))
+
+
+def test_a_step_of_the_search_in_a_graph():
+    """Plan, write, attention, selection and reordering captured once and replayed, against the same steps made one by one."""
+    R, W, H, Hk, d, V = 2, 3, 4, 2, 64, 1000
+    g = torch.Generator(device="cuda").manual_seed(41)
+    emb = torch.randn((V, (H + 2 * Hk) * d), generator=g, device="cuda").to(torch.bfloat16)
+    head = 0.2 * torch.randn((H * d, V), generator=g, device="cuda")
+
+    def fresh():
+        cache = clis.PagedCache(layers=1, num_pages=60, num_kv_heads=Hk, d=d, max_seqs=R * W, max_len=64, page_size=8, dtype=torch.int8)
+        x = emb[:20].reshape(20, H + 2 * Hk, d)
+        plan = cache.begin(torch.tensor([9, 0, 0, 11, 0, 0], dtype=torch.int32, device="cuda"), 20)
+        cache.attend(0, *(t.contiguous() for t in x.split([H, Hk, Hk], 1)), plan, 11)
+        cache.reorder(torch.zeros((R, W), dtype=torch.int32, device="cuda"))
+        return cache, torch.arange(R * W, device="cuda"), torch.zeros((R, W), device="cuda")
+
+    one = torch.ones(R * W, dtype=torch.int32, device="cuda")
+
+    def step(cache, token, scores):
+        x = emb[token].reshape(R * W, H + 2 * Hk, d)
+        plan = cache.begin(one, R * W)
+        o = cache.attend(0, *(t.contiguous() for t in x.split([H, Hk, Hk], 1)), plan, 1)
+        got = clis.beam_select((o.reshape(R * W, -1).float() @ head).reshape(R, W, V), scores, W)
+        cache.reorder(got.parent)
+        token.copy_(got.token.reshape(-1))
+        scores.copy_(got.scores)
+
+    a, b = fresh(), fresh()
+    warm = fresh()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*warm)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*b)
+    for _ in range(8):
+        step(*a)
+        graph.replay()
+        assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2]) and torch.equal(a[0].lens, b[0].lens)
+        assert torch.equal(a[0].block_table, b[0].block_table) and torch.equal(a[0].ring_state, b[0].ring_state)
+
+
+def test_logits_beyond_32_bits():
+    """2.2 * 10^9 logits in all: the last request's place is past 2^32 bytes and 2^31 values."""
+    R, W, V = 70, 8, 4000037
+    logits = torch.empty((R, W, V), dtype=torch.bfloat16, device="cuda").fill_(-3.0)
+    g = torch.Generator(device="cuda").manual_seed(42)
+    scores = -torch.rand((R, W), generator=g, device="cuda")
+    logits[::23] = torch.randn((W, V), generator=g, device="cuda").to(torch.bfloat16)
+    logits[R - 1] = torch.randn((W, V), generator=g, device="cuda").to(torch.bfloat16)
+    got = clis.beam_select(logits, scores, 9)
+    for r in (0, 1, 46, R - 1):
+        check(logits[r:r + 1], scores[r:r + 1], 9, clis.BeamChoice(*(t[r:r + 1] for t in got)))
+
+
+def test_refusals_on_the_host():
+    x, s = torch.zeros((2, 3, 50), device="cuda"), torch.zeros((2, 3), device="cuda")
+    for logits, scores, num, match in ((x[..., ::2], s, 3, "contiguous last"), (x.double(), s, 3, "bfloat16, float16 or float32"),
+                                       (x, s[:1], 3, "scores"), (x, s.double(), 3, "scores"), (x, s, 0, "positive"), (x, s, 65, "UNSUPPORTED"),
+                                       (x[:, :0], s[:, :0], 3, "beams and tokens")):
+        with pytest.raises((ValueError, clis.ClisError), match=match):
+            clis.beam_select(logits, scores, num)
+    i = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    st = torch.tensor([0, 10], dtype=torch.int64, device="cuda")
+    k = torch.zeros((10, 2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    for args, kw, match in (((i(6), i(2, 3), i(6, 4), i(10), st, [k[0]]), {}, "4 or 5"), ((i(5), i(2, 3), i(6, 4), i(10), st, [k]), {}, "lens"),
+                            ((i(6), i(2, 3), i(5, 4), i(10), st, [k]), {}, "block_table"), ((i(6), i(2, 3), i(6, 4), i(10), st, [k, k[:5]]), {}, "one size"),
+                            ((i(6), i(2, 3), i(6, 4), i(10), st.int(), [k]), {}, "ring_state"), ((i(6), i(2, 3), i(6, 4), i(10), st, [k]), {"out": i(6, 5)}, "out"),
+                            ((i(6), i(2, 3), i(6, 4), i(10), st, [k], [k[..., 0]]), {}, "MISALIGNED|multiple|aligned|INVALID")):
+        with pytest.raises((ValueError, clis.ClisError), match=match):
+            clis.paged_reorder(*args, **kw)
+    with pytest.raises(TypeError):
+        clis.paged_reorder(i(6), i(2, 3), i(6, 4), i(10), st, [1])

@@ -350,3 +350,104 @@ def test_read_leaves_other_rows_and_records_bad_places():
     k3, _ = clis.paged_read(b["k_cache"], b["v_cache"], b["block_table"], cu, 29, start=start, **kw)
     assert clis.clis_get_device_error() == clis.PAGED_LENGTH_BIT and (k3[20:] == 0).all()
     clis.clis_clear_device_error()
+
+
+# ------------------------------------------------------------ sizes, streams, refusals
+
+
+@pytest.mark.parametrize("n", [1, 5, 80])
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_the_longest_sequence(n, code):
+    """2^26 - 3 keys (one page, 1,024 times over) in one sequence, shared out over the whole GPU."""
+    page, times, d = 65536, 1024, 64
+    b = make_q8([page], [0], 4, 1, d, page, BF, code, seed=16, poison=False)
+    q = torch.randn((n, 4, d), device="cuda").to(BF)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    at = b["block_table"][0, 0].item()
+    o, lse2 = clis.attention_paged(q, b["k_cache"], b["v_cache"], torch.full((1, times), at, dtype=torch.int32, device="cuda"), i32([0, n]),
+                                   i32([page * times - 3]), n, causal=True, return_lse=True, k_scale=b["k_scale"], v_scale=b["v_scale"])
+    (kc, ks), (vc, vs) = b["keys"][0]
+    k, v = (c[:, 0].float().double() * s.double() for c, s in ((kc, ks), (vc, vs)))
+    count = torch.full((n, page), float(times), dtype=torch.float64, device="cuda")
+    for i in range(n):                                  # query i is key 2^26 - 3 - n + i
+        count[i, page - 3 - n + i + 1:] -= 1
+    x = q.double().transpose(0, 1) @ k.T / 8.0
+    m = x.amax(-1, keepdim=True)
+    p = torch.exp(x - m) * count
+    L = p.sum(-1, keepdim=True)
+    want, A = ((p @ t / L).transpose(0, 1) for t in (v, v.abs()))
+    # As check_q8, for chunks also V's rounding (2^-8 of A); 32-bit sums: a run is at most 2^26 / 152 keys, 16 to a product,
+    # each of which may cut off 2^-23 of the sum.
+    tol = 2.0 ** -8 * (want.abs() + (2 * A if 4 * n > 64 else 0)) + (2.0 ** -11 + 6e-4) * A * 1.01
+    tol = tol + want.abs() * (2.0 ** 26 / 152 / 16 * 2.0 ** -23) + 2.0 ** -32 * (vs.max() / vs.min()) * A
+    assert ((o.double() - want).abs() <= tol).all()
+    e = (lse2.double() - ((m + L.log())[..., 0] / math.log(2.0)).transpose(0, 1)).abs().max().item()
+    assert e <= 6e-4 + 2.0 ** -22 * 32 + 2.0 ** 26 / 152 / 128 * 2.0 ** -24 / math.log(2.0), e
+
+
+def test_caches_beyond_32_bits():
+    """Pages past 2^31 bytes and past 2^31 rows' worth of offsets: written, read back and attended."""
+    page, Hk, d, pages = 64, 8, 128, 36000  # 2.36 GB of codes each
+    kc, vc = (torch.empty((pages, Hk, page, d), dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty((pages, Hk, page), device="cuda") for _ in range(2))
+    T = 200
+    k, v = (torch.randn((T, Hk, d), device="cuda").to(BF) for _ in range(2))
+    bt = torch.tensor([[35999, 3, 35990, 35000, 0]], dtype=torch.int32, device="cuda")
+    at = torch.arange(T, device="cuda")
+    slots = bt[0].long()[at // page] * page + at % page
+    clis.paged_append(k, v, kc, vc, slots, k_scale=ks, v_scale=vs)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    k2, v2 = clis.paged_read(kc, vc, bt, i32([0, T]), T, k_scale=ks, v_scale=vs)
+    for x, y in ((k, k2), (v, v2)):  # half a step of the code, and the rounding of the value read
+        top = x.float().abs().amax(-1, keepdim=True)
+        assert ((x.float() - y.float()).abs() <= top / 254 * 1.001 + 2.0 ** -8 * y.float().abs()).all()
+    held = [(c[bt[0].long()[at // page], :, at % page], x[bt[0].long()[at // page], :, at % page]) for c, x in ((kc, ks), (vc, vs))]
+    for n in (1, 3, 20):
+        b = {"q": torch.randn((n, 32, d), device="cuda").to(BF), "k_cache": kc, "v_cache": vc, "k_scale": ks, "v_scale": vs, "block_table": bt,
+             "cu_q": i32([0, n]), "kv_len": i32([T]), "keys": [held], "ctx": [T - n], "new": [n], "max_q": n}
+        check_q8(attend(b), None, b)
+
+
+def test_given_stream_and_workspace():
+    b = make_q8([500, 90], [1, 1], 8, 2, 128, 16, BF, "int8", seed=17)
+    want = attend(b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o = clis.clis_attn_fwd_paged(b["q"], b["k_cache"], b["v_cache"], b["block_table"], b["cu_q"], b["kv_len"], 1, clis.scale_log2_for(128),
+                                 stream=side, k_scale=b["k_scale"], v_scale=b["v_scale"])
+    k, v = clis.clis_paged_read(b["k_cache"], b["v_cache"], b["block_table"], torch.tensor([0, 501, 592], dtype=torch.int32, device="cuda"), 592,
+                                k_scale=b["k_scale"], v_scale=b["v_scale"], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(o, want)
+    (kc, ks), _ = b["keys"][0]
+    assert torch.equal(k[:501], (kc.float() * ks[..., None]).to(BF))
+
+
+def test_refusals_on_the_host():
+    b = make_q8([50], [1], 8, 2, 64, 16, BF, "int8", seed=18)
+    kw = {"k_scale": b["k_scale"], "v_scale": b["v_scale"]}
+    args = [b["q"], b["k_cache"], b["v_cache"], b["block_table"], b["cu_q"], b["kv_len"], 1]
+
+    def no(match, **change):
+        a, k = list(args), dict(kw)
+        for n, x in change.items():
+            if n in k:
+                k[n] = x
+            else:
+                a[int(n[1:])] = x
+        with pytest.raises((ValueError, clis.ClisError), match=match):
+            clis.attention_paged(*a, **k)
+
+    no("belong together", v_scale=None)
+    no("codes need k_scale", k_scale=None, v_scale=None)
+    no("float32", k_scale=b["k_scale"].double())
+    no("float32", k_scale=b["k_scale"][:1])
+    no("int8 or float8", _1=b["k_cache"].float().to(BF), _2=b["v_cache"].float().to(BF))
+    no("int8 or float8", _2=b["v_cache"].view(torch.float8_e4m3fn))
+    no("MISALIGNED|multiple|aligned", _1=raw(b["k_cache"])[..., 8:].contiguous().new_zeros((b["k_cache"].shape[0], 2, 16, 72))[..., :64])
+    with pytest.raises(ValueError, match="dtype"):
+        clis.paged_read(b["k_cache"], b["v_cache"], b["block_table"], b["cu_q"], 1, dtype=torch.float32, **kw)
+    with pytest.raises(ValueError, match="without scales"):
+        clis.paged_read(b["k_cache"], b["v_cache"], b["block_table"], b["cu_q"], 1)
+    with pytest.raises(ValueError, match="k_out and v_out"):
+        clis.paged_read(b["k_cache"], b["v_cache"], b["block_table"], b["cu_q"], 1, k_out=torch.empty((1, 2, 64), device="cuda"), **kw)
