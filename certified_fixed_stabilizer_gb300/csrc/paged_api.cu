@@ -210,21 +210,24 @@ Split split_of(const clis_paged_t *p, int64_t max_q, int nsm)
     return s;
 }
 
-// Over a quantised cache: the kernel for few rows takes up to 64, and batches with chunks
-// always launch both kernels (the chunk kernel's keys are unpacked to 16 bits first, so
-// a single token costs it five times the bytes).
+// Over a quantised cache: the kernel for few rows takes up to 64.  The chunk kernel's keys are
+// unpacked to 16 bits first, so a single token costs it five times the bytes, and a batch with
+// chunks launches both kernels; but where its whole tables can hold no more than 16 MB of
+// codes, the bytes are cheaper than two more launches.
 struct SplitQ8 {
     int rows;    // of the kernel for few rows, 0: not launched
     bool chunk;  // the chunk kernel is launched
 };
 
-SplitQ8 split_q8(const clis_paged_t *p, int64_t max_q)
+SplitQ8 split_q8(const clis_paged_t *p, int64_t max_q, int nsm)
 {
     const int g = static_cast<int>(p->H / p->Hkv);
     const int64_t mq = max_q < p->T ? max_q : p->T;
     SplitQ8 s;
     s.rows = clis::paged_q8_rows(mq, g);
     s.chunk = mq * g > s.rows;
+    const double codes = 2.0 * static_cast<double>(p->S) * p->Hkv * p->width * p->page_size * p->d;
+    if (s.chunk && p->S * p->Hkv <= 4 * nsm && codes <= 16.0 * (1 << 20)) s.rows = 0;
     return s;
 }
 
@@ -616,7 +619,7 @@ clis_status_t clis_attn_paged_q8_workspace_size(const clis_paged_t *desc, const 
     if (desc->S == 0 || desc->T == 0) return CLIS_OK;
     int nsm = 0;
     if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
-    const SplitQ8 s = split_q8(desc, max_q);
+    const SplitQ8 s = split_q8(desc, max_q, nsm);
     *bytes = clis::paged_q8_workspace(static_cast<int>(desc->d), s.rows, nsm) +
              (s.chunk ? clis::paged_chunk_workspace(attn_args(desc), nsm) + 2 * pages_bytes(desc) + scales_bytes(desc) : 0);
     return CLIS_OK;
@@ -640,7 +643,7 @@ clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_
         return CLIS_ERR_MISALIGNED;
     int nsm = 0;
     if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
-    const SplitQ8 s = split_q8(desc, max_q);
+    const SplitQ8 s = split_q8(desc, max_q, nsm);
     clis::PagedArgs a = attn_args(desc);
     const size_t few = clis::paged_q8_workspace(a.d, s.rows, nsm);
     const size_t chunk = s.chunk ? clis::paged_chunk_workspace(a, nsm) : 0;
@@ -671,8 +674,8 @@ clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_
     b.kc_sh = b.vc_sh = desc->page_size * a.d;
     b.kc_sp = b.vc_sp = desc->Hkv * desc->page_size * a.d;
     const int rows_small = s.rows;
-    clis_status_t e = clis::launch_paged_unpack(a, z, rows_small, kp, ks, vp, nsm, cs);
-    if (e == CLIS_OK) e = clis::launch_paged_chunk_schedule(b, rows_small, w + few, nsm, cs);
+    clis_status_t e = clis::launch_paged_chunk_schedule(b, rows_small, w + few, nsm, cs);
+    if (e == CLIS_OK) e = clis::launch_paged_unpack(a, z, rows_small, kp, ks, vp, nsm, cs);
     if (e == CLIS_OK && s.rows > 0) e = clis::launch_paged_q8(a, z, s.rows, false, true, w, nsm, cs);
     if (e == CLIS_OK) e = clis::launch_paged_chunk(b, rows_small, w + few, nsm, cs);
     return e;

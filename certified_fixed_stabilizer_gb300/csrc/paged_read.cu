@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kReadThreads) paged_unpack_kernel(const Unpack
     __shared__ unsigned long long s_sum[kReadThreads / 32];
     __shared__ int s_seq, s_unit;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch();
     auto seq_len = [&](int s) {
         return clip_seq(__ldg(a.cu_q + s), __ldg(a.cu_q + s + 1), __ldg(a.kv_len + s), a.T, a.width << a.page_shift);
     };
@@ -250,7 +251,10 @@ __global__ void __launch_bounds__(kReadThreads) paged_unpack_kernel(const Unpack
         }
     }
     __syncthreads();
-    if (u0 >= u1) return;
+    if (u0 >= u1) {
+        pdl_wait();
+        return;
+    }
     int s = s_seq, j = s_unit, n = units(s), kv = seq_len(s).kv;
     using S = Split<D>;
     const int mask = (1 << a.page_shift) - 1;
@@ -276,6 +280,7 @@ __global__ void __launch_bounds__(kReadThreads) paged_unpack_kernel(const Unpack
             kv = seq_len(s).kv;
         }
     }
+    pdl_wait();  // (the schedule kernel, whose results only later kernels read)
 }
 
 template <int CODE, int DT>
@@ -289,9 +294,7 @@ cudaError_t launch_read_impl(const ReadArgs &a, dim3 grid, cudaStream_t stream)
 template <int CODE, int DT>
 cudaError_t launch_unpack_impl(const UnpackParams &p, int grid, cudaStream_t stream)
 {
-    if (p.a.d == 128) paged_unpack_kernel<CODE, DT, 128><<<grid, kReadThreads, 0, stream>>>(p);
-    else paged_unpack_kernel<CODE, DT, 64><<<grid, kReadThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(p.a.d == 128 ? paged_unpack_kernel<CODE, DT, 128> : paged_unpack_kernel<CODE, DT, 64>, dim3(grid), kReadThreads, 0, stream, p);
 }
 
 }  // namespace

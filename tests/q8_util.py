@@ -56,11 +56,16 @@ def make_q8(ctx, new, H, Hkv, d, page, dtype, code, seed=0, device="cuda", extra
             "max_q": max(new + [1]), "code": code}
 
 
-def is_few(n, max_q, g):
-    """Whether a sequence of n new tokens runs the kernel for few rows (include/clis.h)."""
-    limit = max_q * g if max_q * g <= 64 else g
-    limit = limit if limit <= 64 else 0
-    return n * g <= limit
+def few_rows(b):
+    """Query rows up to which a sequence of the batch runs the kernel for few rows (include/clis.h)."""
+    S, width = b["block_table"].shape
+    pages, Hkv, page, d = b["k_cache"].shape
+    g, max_q = b["q"].shape[1] // Hkv, min(b["max_q"], b["q"].shape[0])
+    limit = max_q * g if max_q * g <= 64 else g if g <= 64 else 0
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if max_q * g > limit and S * Hkv <= 4 * sms and 2 * S * Hkv * width * page * d <= 16 << 20:
+        return 0
+    return limit
 
 
 def check_q8(got_o, got_lse2, b, causal=True, scale=None, what=""):
@@ -83,7 +88,7 @@ def check_q8(got_o, got_lse2, b, causal=True, scale=None, what=""):
     for s, (c, n) in enumerate(zip(b["ctx"], b["new"])):
         if n == 0:
             continue
-        few = is_few(n, b["max_q"], g)
+        few = n * g <= few_rows(b)
         (kc, ks), (vc, vs) = b["keys"][s]
         k, v = kc.float().double() * ks.double()[..., None], vc.float().double() * vs.double()[..., None]
         if not few:
