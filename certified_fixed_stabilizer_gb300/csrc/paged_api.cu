@@ -224,7 +224,7 @@ SplitQ8 split_q8(const clis_paged_t *p, int64_t max_q, int nsm)
     const int g = static_cast<int>(p->H / p->Hkv);
     const int64_t mq = max_q < p->T ? max_q : p->T;
     SplitQ8 s;
-    s.rows = clis::paged_q8_rows(mq, g);
+    s.rows = clis::paged_q8_rows(attn_args(p), mq, nsm);
     s.chunk = mq * g > s.rows;
     const double codes = 2.0 * static_cast<double>(p->S) * p->Hkv * p->width * p->page_size * p->d;
     if (s.chunk && p->S * p->Hkv <= 4 * nsm && codes <= 16.0 * (1 << 20)) s.rows = 0;

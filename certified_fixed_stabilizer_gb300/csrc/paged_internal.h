@@ -144,7 +144,7 @@ size_t paged_decode_workspace(int d, int row_tiles, int nsm);
 clis_status_t launch_paged_decode(const PagedArgs &a, int row_tiles, bool strict, bool after_schedule, void *workspace,
                                   int nsm, cudaStream_t stream);
 // The same over a quantised cache: query rows of a sequence, at most, or 0 (not used).
-int paged_q8_rows(int64_t max_q, int g);
+int paged_q8_rows(const PagedArgs &a, int64_t max_q, int nsm);
 size_t paged_q8_workspace(int d, int rows, int nsm);
 clis_status_t launch_paged_q8(const PagedArgs &a, const QuantArgs &z, int rows, bool strict, bool after_schedule,
                               void *workspace, int nsm, cudaStream_t stream);

@@ -12,8 +12,8 @@
 // slots: turning 8 KB of codes into fp16 pairs alone takes a warp some 320 instructions.
 //
 //  * Work, runs and joins: as in paged_decode.cu.  A warp works alone, on 8, 16 or (d = 64)
-//    32 query rows, NT = 1, 2 or 4 column tiles; a sequence of up to 64 rows (drafted tokens) is
-//    several items that read the same keys, one after the other, mostly from L2.  From 16
+//    32 query rows, NT = 1, 2 or 4 column tiles; a sequence of more rows (drafted tokens,
+//    small chunks) is several items that read the same keys, one after the other, mostly from L2.  From 16
 //    rows on what a warp does per unit is the time (850 instructions at NT = 2, two warps per
 //    scheduler).  Tiles of 32 rows at d = 128 spill registers (16, 32 and 64 rows of the 64 requests
 //    below: 231, 460 and 920 us with tiles of 16; 413 and 783 with 32 of int8, but 526 and 979
@@ -722,12 +722,21 @@ clis_status_t launch_types(bool half, bool int8, int rows, const A &...args)
 
 }  // namespace
 
-int paged_q8_rows(int64_t max_q, int g)
+int paged_q8_rows(const PagedArgs &a, int64_t max_q, int nsm)
 {
-    // Rows of the largest sequence if it is small; else those of single tokens.
-    constexpr int most = 64;
-    const int64_t rows = max_q <= most && max_q * g <= most ? max_q * g : g;
-    return rows <= most ? static_cast<int>(rows) : 0;
+    // Rows of the largest sequence if it is small; else those of single tokens.  Small: up to 64
+    // rows; up to 2048 where the tables can hold no more than 12 units (d = 64, where tiles of 32
+    // rows cost twice as much: 3) for each of 1,216 workers.  (The chunk kernel with what it needs
+    // takes 32 us at least: 72 rows over 509 keys, d = 64, 2 heads 21 us here against 32; 80 rows
+    // over 2 x 4,020 keys of 8 heads, 8 units, 34 against 54; 800 rows over 1,200 keys, 12.5 units, 45
+    // against 63; 19 units 68 against 53; at d = 64 3.4 units 43 against 49, 4.4 units 54 against 40.)
+    const int g = a.H / a.Hkv, tile = a.d == 64 ? 32 : 16, keys = 4096 / a.d;
+    const int64_t rows = max_q <= 2048 ? max_q * g : 2049;
+    if (rows <= 64) return static_cast<int>(rows);
+    const int64_t items = static_cast<int64_t>(a.S) * a.Hkv * ((rows + tile - 1) / tile);
+    const int64_t units = ((static_cast<int64_t>(a.width) << a.page_shift) + keys - 1) / keys * items;
+    if (rows <= 2048 && units <= static_cast<int64_t>(a.d == 64 ? 3 : 12) * nsm * 2 * kDecodeWarps) return static_cast<int>(rows);
+    return g <= 64 ? g : 0;
 }
 
 size_t paged_q8_workspace(int d, int rows, int nsm)

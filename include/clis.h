@@ -673,15 +673,16 @@ CLIS_API clis_status_t clis_paged_read(const clis_paged_t *desc, const clis_quan
                                        clis_stream_t stream);
 
 /* clis_attn_fwd_paged over a cache of codes: x_ij = scale_log2 * q_i . k_j and o_i with the
- * values code * scale.  Sequences of up to 64 query rows (n * H / Hkv; single tokens, or
- * with max_q * H / Hkv <= 64 drafted ones) run a kernel bound by the codes' bytes: codes
- * are exact in its products, the weights times V's scale are rounded to fp16 (off by up to 2^-11
- * of each, at least 2^-32 of the row's largest), q is exact where it is within 2^-30 of its
- * row's largest value.  Longer chunks, and with them the other sequences of a batch whose
- * table can hold no more than 16 MB of codes, are unpacked to 16 bits first (K's codes, exact, its
- * scales applied to the scores; V's values, rounded once to the data type) and run the
- * chunk kernel of clis_attn_fwd_paged; where max_q allows for them the workspace holds
- * a 16-bit copy of the whole cache that is passed (one layer's).
+ * values code * scale.  Where max_q allows for no more than 64 query rows of a sequence
+ * (max_q * H / Hkv; single and drafted tokens), or the tables can hold little enough to go
+ * with them, one kernel does it all, bound by the codes' bytes: codes are exact in its
+ * products, the weights times V's scale are rounded to fp16 (off by up to 2^-11 of each, at
+ * least 2^-32 of the row's largest), q is exact where it is within 2^-30 of its row's largest
+ * value.  Else that kernel serves single tokens, and the other sequences (all of them
+ * where the tables can hold no more than 16 MB of codes) are unpacked to 16 bits first (K's
+ * codes, exact, its scales applied to the scores; V's values, rounded once to the data type)
+ * and run the chunk kernel of clis_attn_fwd_paged; the workspace then holds a 16-bit copy
+ * of the whole cache that is passed (one layer's).
  * A NaN code of E4M3 stands for NaN.  Masked places, padding, reruns and errors as for
  * clis_attn_fwd_paged. */
 CLIS_API clis_status_t clis_attn_paged_q8_workspace_size(const clis_paged_t *desc, const clis_quant_t *quant, int64_t max_q,

@@ -15,10 +15,11 @@ def raw(t):
     return t.view(torch.int8)
 
 
-def make_q8(ctx, new, H, Hkv, d, page, dtype, code, seed=0, device="cuda", extra_rows=0, layout="hnd", spread=0.4, poison=True):
+def make_q8(ctx, new, H, Hkv, d, page, dtype, code, seed=0, device="cuda", extra_rows=0, layout="hnd", spread=0.4, poison=True,
+            columns=0):
     """Random batch over a paged cache of codes.  Pages are scattered; with ``poison`` the scales (and E4M3 codes)
     of rows that hold no key are NaN, int8 codes 111, and unused block-table entries out of range.  ``spread``: of
-    the scales' logarithm."""
+    the scales' logarithm.  ``columns``: further ones of the block table (by what it can hold a batch's kernels are chosen)."""
     g = torch.Generator(device=device).manual_seed(seed)
     rng = random.Random(seed)
     S, kv = len(ctx), [c + n for c, n in zip(ctx, new)]
@@ -26,7 +27,7 @@ def make_q8(ctx, new, H, Hkv, d, page, dtype, code, seed=0, device="cuda", extra
     pages = sum(need) + 3
     ids = list(range(pages))
     rng.shuffle(ids)
-    bt = torch.full((S, max(need + [0]) + 2), 0x3FFFFFFF if poison else -1, dtype=torch.int32)
+    bt = torch.full((S, max(need + [0]) + 2 + columns), 0x3FFFFFFF if poison else -1, dtype=torch.int32)
     shape = (pages, Hkv, page, d) if layout == "hnd" else (pages, page, Hkv, d)
     fill = 127 if code == "e4m3" else 111
     kc, vc = (torch.full(shape, fill if poison else 0, dtype=torch.int8, device=device) for _ in range(2))
@@ -61,11 +62,16 @@ def few_rows(b):
     S, width = b["block_table"].shape
     pages, Hkv, page, d = b["k_cache"].shape
     g, max_q = b["q"].shape[1] // Hkv, min(b["max_q"], b["q"].shape[0])
-    limit = max_q * g if max_q * g <= 64 else g if g <= 64 else 0
+    rows, tile, keys = max_q * g, 32 if d == 64 else 16, 4096 // d
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    if max_q * g > limit and S * Hkv <= 4 * sms and 2 * S * Hkv * width * page * d <= 16 << 20:
+    if rows <= 64:
+        return rows
+    units = -(-width * page // keys) * S * Hkv * -(-rows // tile)
+    if max_q <= 2048 and rows <= 2048 and units <= (3 if d == 64 else 12) * sms * 8:
+        return rows
+    if S * Hkv <= 4 * sms and 2 * S * Hkv * width * page * d <= 16 << 20:
         return 0
-    return limit
+    return g if g <= 64 else 0
 
 
 def check_q8(got_o, got_lse2, b, causal=True, scale=None, what=""):

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from certified_fixed_stabilizer_gb300 import clis
-from q8_util import CODES, TOP, check_q8, make_q8, raw
+from q8_util import CODES, TOP, check_q8, few_rows, make_q8, raw
 
 pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
@@ -36,18 +36,35 @@ SHAPES = [  # ctx, new, H, Hkv, d, page
     ([500, 3, 90, 1500], [5, 1, 4, 5], 32, 4, 128, 16),         # 40 rows
     ([77, 1200], [13, 16], 16, 4, 64, 128),                     # 64 rows
     ([40, 0], [2, 3], 128, 8, 128, 8),                          # 16 heads a key: 48 rows
-    ([10], [1], 128, 1, 64, 16),                                # 128 query heads a key: the chunk kernel
-    ([200, 0, 33], [70, 129, 1], 8, 2, 128, 16),                # chunks and a single token
+    ([10], [1], 128, 1, 64, 16),                                # 128 query heads a key
+    ([200, 0, 33], [70, 129, 1], 8, 2, 128, 16),                # small chunks and a single token: 516 rows
     ([200, 5, 300, 17], [17, 300, 1, 2], 4, 4, 64, 8),
     ([4000], [9], 40, 8, 128, 256),
+    # the same with tables that can hold far more: the chunk kernel
+    ([10], [1], 128, 1, 64, 16, 30000),
+    ([200, 0, 33], [70, 129, 1], 8, 2, 128, 16, 20000),
+    ([200, 5, 300, 17], [17, 300, 1, 2], 4, 4, 64, 8, 30000),
+    ([4000, 70], [20, 1], 40, 8, 128, 256, 1000),
+    ([300, 20], [600, 1], 16, 4, 128, 32),                      # 2,400 rows: the chunk kernel for the single token too
 ]
+
+
+def which(b):
+    """The kernels that the batch's sequences run."""
+    g = b["q"].shape[1] // b["k_cache"].shape[1]
+    return {"few" if n * g <= few_rows(b) else "chunk" for n in b["new"] if n}
+
+
+def test_the_shapes_cover_the_ways():
+    ways = [which(make_q8(*s[:6], BF, "int8", columns=s[6] if len(s) > 6 else 0)) for s in SHAPES]
+    assert {"few"} in ways and {"chunk"} in ways and {"few", "chunk"} in ways
 
 
 @pytest.mark.parametrize("shape", range(len(SHAPES)))
 @pytest.mark.parametrize("dtype,code", [(BF, "int8"), (HF, "int8"), (BF, "e4m3"), (HF, "e4m3")])
 def test_attention(shape, dtype, code):
-    ctx, new, H, Hkv, d, page = SHAPES[shape]
-    b = make_q8(ctx, new, H, Hkv, d, page, dtype, code, seed=shape, extra_rows=2, layout="hnd" if shape % 2 else "nhd")
+    ctx, new, H, Hkv, d, page, *columns = SHAPES[shape]
+    b = make_q8(ctx, new, H, Hkv, d, page, dtype, code, seed=shape, extra_rows=2, layout="hnd" if shape % 2 else "nhd", columns=sum(columns))
     causal = shape % 3 != 2
     out = torch.full_like(b["q"], 7.0)
     o, lse = attend(b, causal=causal, out=out, return_lse=True)
@@ -88,7 +105,8 @@ def test_scales_of_any_size(spread, new):
 
 def test_chunk_with_scales_of_zero_and_of_any_size():
     """K's scales of 0, 2^-110, 2^-60 and 2^20 among a chunk's: scores of no and of great size."""
-    b = make_q8([300, 11], [70, 90], 4, 2, 64, 8, BF, "e4m3", seed=15)
+    b = make_q8([300, 11], [70, 90], 4, 2, 64, 8, BF, "e4m3", seed=15, columns=50000)
+    assert which(b) == {"chunk"}
     (kc, ks), (vc, vs) = b["keys"][0]
     for i, x in ((3, 0.0), (50, 2.0 ** -110), (120, 2.0 ** -60), (310, 0.0), (330, 2.0 ** -110)):
         ks[i] = x
@@ -128,12 +146,13 @@ def test_no_keys():
 
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
 @pytest.mark.parametrize("what", ["k_scale", "v_scale", "v_inf", "k_code", "v_code"])
-@pytest.mark.parametrize("new,H", [(3, 4), (5, 16), (40, 4)])
-def test_non_finite_where_some_rows_do_not_see_it(code, what, new, H):
+@pytest.mark.parametrize("new,H,columns", [(3, 4, 0), (5, 16, 0), (40, 4, 0), (40, 4, 20000)])
+def test_non_finite_where_some_rows_do_not_see_it(code, what, new, H, columns):
     """The last new token's key is no number: earlier rows are as without it, the last row is NaN."""
     if what.endswith("code") and code == "int8":
         pytest.skip("int8 codes are numbers")
-    b = make_q8([61, 30], [new, new], H, 2, 64, 16, BF, code, seed=10)
+    b = make_q8([61, 30], [new, new], H, 2, 64, 16, BF, code, seed=10, columns=columns)
+    assert which(b) == {"chunk" if columns else "few"}
     want = attend(b)
     at = 61 + new - 1
     page, row = b["block_table"][0, at // 16].long(), at % 16
