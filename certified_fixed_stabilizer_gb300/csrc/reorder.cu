@@ -252,7 +252,7 @@ __device__ __forceinline__ void copy_rows(const uint8_t *from, uint8_t *to, cons
     }
 }
 
-__global__ void __launch_bounds__(kCopyThreads) reorder_copy_kernel(const ReorderParams p)
+__global__ void __launch_bounds__(kCopyThreads, 4) reorder_copy_kernel(const ReorderParams p)
 {
     const ReorderArgs &a = p.a;
     __shared__ long long s_sum[kCopyWarps][2];
@@ -277,11 +277,13 @@ __global__ void __launch_bounds__(kCopyThreads) reorder_copy_kernel(const Reorde
         }
     }
     // Copies: (page, tensor, layer) by blocks.
-    int64_t layers = 0;
-    for (int t = 0; t < a.tensors; t++) layers += a.t[t].layers;
-    for (int64_t u = blockIdx.x; u < all.x * layers; u += gridDim.x) {
-        const int4 c = p.copy[u / layers];
-        int l = static_cast<int>(u % layers), t = 0;
+    uint32_t layers = 0;
+    for (int t = 0; t < a.tensors; t++) layers += static_cast<uint32_t>(a.t[t].layers);
+    const uint64_t units = static_cast<uint64_t>(all.x) * layers;
+    for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const uint64_t which = div64(u, layers);
+        const int4 c = p.copy[which];
+        int l = static_cast<int>(u - which * layers), t = 0;
         while (l >= a.t[t].layers) l -= static_cast<int>(a.t[t++].layers);
         if (c.x < 0 || c.x >= a.num_pages || c.y < 0 || c.y >= a.num_pages) {
             bad |= CLIS_PAGED_INDEX_BIT;
