@@ -1,5 +1,5 @@
 """Builds libclis.so (CUDA for sm_103a) in-tree with nvcc, and _clis_torch.so, the
-torch binding of the calls around a paged cache, with the C++ compiler.
+torch binding of the calls around a paged cache and of beam search, with the C++ compiler.
 
 Each translation unit is compiled in parallel to an object file, then linked
 into ``certified_fixed_stabilizer_gb300/_lib/libclis.so``.  The CUDA runtime is

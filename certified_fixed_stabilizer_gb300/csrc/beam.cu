@@ -5,7 +5,9 @@
 //
 // best first, ties to the lowest w * V + v.
 //
-// Bound: the logits' bytes, read once.  A row is cut into chunks of 512 logits.  The
+// Bound: the logits' bytes, read once (96 requests of 8 beams, 128,000 tokens, bf16, a fifth of the
+// beams not in use: 59 us, of which the first kernel 38, whatever the loads in flight, 23 by the
+// copy rate; 8 requests of 4 beams and 32,003 tokens: 13 us, two dependent launches).  A row is cut into chunks of 512 logits.  The
 // first kernel leaves each chunk's largest logit and the row's maximum and sum.  At most K
 // chunks can hold one of the K best: those whose largest logit leads to the K best such
 // values, so the second kernel (a block per request) picks them, reads them again (a

@@ -1,5 +1,5 @@
 // binding.cpp -- torch tensors into the calls around a paged key/value cache
-// (include/clis.h): argument checks, output allocation, the current stream, one
+// and beam search over it (include/clis.h): argument checks, output allocation, the current stream, one
 // call of the library each, and the rotation's autograd node.
 //
 // These calls are made once or more per layer and token, and at a few tokens the

@@ -54,12 +54,14 @@
 // each of 152 SMs, 593 us; the rest (first tiles, joins, page lookups, 84 bytes of
 // registers that the softmax warps spill at d = 128) has not been taken apart.
 //
-// Over a cache of 8-bit codes (KS) K's pages hold the codes themselves, exact in 16 bits,
-// and a key's scale multiplies its scores as they come from TMEM.  (With the values rounded to bf16 first, the outputs of 2,048 tokens behind 30,011
-// were off by 4.4e-3, rounding the keys alone 3.6e-3.)  The K/V producer brings the scales
-// into a ring of kScaleTiles tiles of shared memory.  K of tile n is loaded when the scores of
-// tile n - NSTAGE / 2 have been computed, so both softmax groups are done with tile n - 3 -
-// NSTAGE / 2 at least, and its place in the ring of scales is free.
+// Over a cache of 8-bit codes (KS) K's pages hold the codes themselves, exact in 16 bits, and a
+// key's scale multiplies its scores as they come from TMEM.  The call of 2,048 tokens behind
+// 30,011 takes 869 to 893 us (40 of them unpacking, paged_read.cu), off by 2.5e-3.  With the
+// values of K and V rounded to bf16 it took 808 and was off by 4.4e-3; with the scales
+// multiplied in at both uses of a score, read from shared memory each time, 1,015.  The K/V
+// producer brings the scales into a ring of kScaleTiles tiles of shared memory.  K of tile n is
+// loaded when the scores of tile n - NSTAGE / 2 have been computed, so both softmax groups are
+// done with tile n - 3 - NSTAGE / 2 at least, and its place in the ring of scales is free.
 //
 // Every wait is bounded.
 #include <cuda_bf16.h>

@@ -5,8 +5,9 @@
 //   x = code * scale, rounded once to the data type (a cache of 16-bit values is copied)
 //
 // Bound: bytes, d + 4 read and 2 d written per row.  A thread turns 8 codes into one 16-byte
-// store, so that a warp's stores fill whole lines (16 codes and two stores a thread: 124 us
-// for 120,000 rows of 8 heads, K and V, 600 MB); eight such pieces are in flight at a time.
+// store, so that a warp's stores fill whole lines; eight such pieces are in flight at a time,
+// and places are multiplied out once per token.  120,000 tokens of 8 heads, K and V, 600 MB: 99 us,
+// 89% of the measured copy rate (16 codes and two stores a thread 124, places per piece 110).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
