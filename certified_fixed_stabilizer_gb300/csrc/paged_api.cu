@@ -756,6 +756,7 @@ clis_status_t clis_paged_reorder(const clis_reorder_t *desc, const int32_t *lens
     a.tensors = static_cast<int>(n);
     if (!ring || !state_in || !state_out || state_in == state_out) return CLIS_ERR_INVALID_ARG;
     if (a.R > 0 && (!lens || !parent || !block_table || !new_table || !lens_out || !done)) return CLIS_ERR_INVALID_ARG;
+    if (a.R > 0 && (lens_out == lens || lens_out == parent)) return CLIS_ERR_INVALID_ARG;  // all blocks read them
     if (a.R > 0 && new_table == block_table && a.R * a.W > 1 && a.bt_s != a.bo_s) return CLIS_ERR_INVALID_ARG;
     if (!aligned(lens, 4) || !aligned(parent, 4) || !aligned(block_table, 4) || !aligned(new_table, 4) || !aligned(ring, 4) ||
         !aligned(state_in, 8) || !aligned(state_out, 8) || !aligned(lens_out, 4) || !aligned(done, 4))

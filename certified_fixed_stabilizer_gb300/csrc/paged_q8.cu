@@ -12,13 +12,12 @@
 // slots: turning 8 KB of codes into fp16 pairs alone takes a warp some 320 instructions.
 //
 //  * Work, runs and joins: as in paged_decode.cu.  A warp works alone, on 8, 16 or (d = 64)
-//    32 query rows, NT = 1, 2 or 4 column tiles; a sequence of more rows (drafted tokens,
+//    24 query rows, NT = 1, 2 or 3 column tiles; a sequence of more rows (drafted tokens,
 //    small chunks) is several items that read the same keys, one after the other, mostly from L2.  From 16
 //    rows on what a warp does per unit is the time (850 instructions at NT = 2, two warps per
-//    scheduler).  Tiles of 32 rows at d = 128 spill registers (16, 32 and 64 rows of the 64 requests
-//    below: 231, 460 and 920 us with tiles of 16; 413 and 783 with 32 of int8, but 526 and 979
-//    of E4M3); at d = 64 they pay (32 rows 282 -> 230 us).  Teams of four warps that convert a unit
-//    together into fp16 tiles in shared memory took 607 and 798.
+//    scheduler).  Larger tiles spill registers: 16, 32 and 64 rows of the 64 requests below 231, 460
+//    and 920 us with tiles of 16; 413 and 783 with 32 of int8, but 526 and 979 of E4M3.  Teams of
+//    four warps that convert a unit together into fp16 tiles in shared memory took 607 and 798.
 //  * The products are taken transposed, S^T = KC Q^T and O^T += VC^T W^T: codes are the
 //    16-row operand, query rows the 8-column one.  A single token's g query heads fill
 //    4 or 8 of 8 places instead of 16, which halves the products, the weights and the
@@ -561,8 +560,8 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
         // ---- one item, units j0 .. j1 - 1 of it
         const int j0 = cur.j;
         const int j1 = static_cast<int>(min(static_cast<uint32_t>(cur.units), j0 + cur.left));
-        const int kv = cur.q.kv, lim0 = visible_keys(cur.q.n, kv, 0, a.causal);  // keys that every row sees
-        const int row0 = cur.tile * C::TR;
+        const int kv = cur.q.kv, row0 = cur.tile * C::TR;
+        const int lim0 = visible_keys(cur.q.n, kv, row0 / p.g, a.causal);  // keys that every row sees
         w.template load<DT>(p, cur.q, cur.h, row0, lane);
         bool dirty = false;
 #pragma unroll 1
@@ -709,12 +708,19 @@ clis_status_t launch_impl(int rows, const PagedArgs &a, const QuantArgs &z, bool
     return launch_join<D, DT>(p, stream) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
 
+// Column tiles of 8 query rows that a warp takes.  Three only at d = 64 (at d = 128 they spill
+// registers: 20 rows 168 us instead of 141 with two tiles of 16), where a tile of 24 rows costs 1.25 times
+// one of 16: 20 rows over 64 requests 88 us, 40 166; with two they are 2 and 3 tiles, with four
+// (registers spilled) 132 and 245.  25 to 32 rows fill two tiles of 16.
+int column_tiles(int d, int rows) { return rows <= 8 ? 1 : d == 64 && rows > 16 && (rows <= 24 || rows > 32) ? 3 : 2; }
+
 template <int D, int DT, int CODE, typename... A>
 clis_status_t launch_rows(int rows, const A &...args)
 {
-    if (rows <= 8) return launch_impl<D, DT, CODE, 1>(rows, args...);
+    const int nt = column_tiles(D, rows);
+    if (nt == 1) return launch_impl<D, DT, CODE, 1>(rows, args...);
     if constexpr (D == 64)
-        if (rows > 16) return launch_impl<D, DT, CODE, 4>(rows, args...);
+        if (nt == 3) return launch_impl<D, DT, CODE, 3>(rows, args...);
     return launch_impl<D, DT, CODE, 2>(rows, args...);
 }
 
@@ -730,26 +736,26 @@ clis_status_t launch_types(bool half, bool int8, int rows, const A &...args)
 int paged_q8_rows(const PagedArgs &a, int64_t max_q, int nsm)
 {
     // Rows of the largest sequence if it is small; else those of single tokens.  Small: up to 64
-    // rows; up to 2048 where the tables can hold no more than 12 units (d = 64, where tiles of 32
-    // rows cost twice as much: 3) for each of 1,216 workers.  (The chunk kernel with what it needs
-    // takes 32 us at least: 72 rows over 509 keys, d = 64, 2 heads 21 us here against 32; 80 rows
-    // over 2 x 4,020 keys of 8 heads, 8 units, 34 against 54; 800 rows over 1,200 keys, 12.5 units, 45
-    // against 63; 19 units 68 against 53; at d = 64 3.4 units 43 against 49, 4.4 units 54 against 40.)
-    const int g = a.H / a.Hkv, tile = a.d == 64 ? 32 : 16, keys = 4096 / a.d;
+    // rows; up to 2048 where the tables can hold no more than 17 units (d = 64, where the chunk
+    // kernel costs half: 6) for each of 1,216 workers.  (The chunk kernel with what it needs takes 40
+    // to 55 us at least.  d = 128: 80 rows over 16,080 keys of 8 heads, 16.5 units, 51 us here
+    // against 68; 160 rows of 4 x 4,040 keys, 16.7, 43 against 56; 2,048 rows over 712 keys, 19.4, 69
+    // against 54.  d = 64: 160 rows, 5.9, 35 against 42; 2,048 rows, 6.8, 48 against 41.)
+    const int g = a.H / a.Hkv, tile = a.d == 64 ? 24 : 16, keys = 4096 / a.d;
     const int64_t rows = max_q <= 2048 ? max_q * g : 2049;
     if (rows <= 64) return static_cast<int>(rows);
     const int64_t items = static_cast<int64_t>(a.S) * a.Hkv * ((rows + tile - 1) / tile);
     const int64_t units = ((static_cast<int64_t>(a.width) << a.page_shift) + keys - 1) / keys * items;
-    if (rows <= 2048 && units <= static_cast<int64_t>(a.d == 64 ? 3 : 12) * nsm * 2 * kDecodeWarps) return static_cast<int>(rows);
+    if (rows <= 2048 && units <= static_cast<int64_t>(a.d == 64 ? 6 : 17) * nsm * 2 * kDecodeWarps) return static_cast<int>(rows);
     return g <= 64 ? g : 0;
 }
 
 size_t paged_q8_workspace(int d, int rows, int nsm)
 {
     if (rows == 0) return 0;
-    const int nt = rows <= 8 ? 1 : d == 64 && rows > 16 ? 4 : 2;
+    const int nt = column_tiles(d, rows);
     const int of_sm = kDecodeWarps * (nt == 1 ? QCfg<128, 1>::BLOCKS : QCfg<128, 2>::BLOCKS);  // (the same for both widths)
-    static_assert(QCfg<64, 4>::BLOCKS == QCfg<128, 2>::BLOCKS, "one number of blocks");
+    static_assert(QCfg<64, 3>::BLOCKS == QCfg<128, 2>::BLOCKS, "one number of blocks");
     return parts_workspace(static_cast<size_t>(of_sm) * nsm, 8 * nt, d);
 }
 

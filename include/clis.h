@@ -742,7 +742,7 @@ CLIS_API clis_status_t clis_beam_select(const clis_beam_t *desc, const void *log
  *   ring, ring_size, state_in, state_out  as for clis_paged_plan: pages are taken from the
  *                head on in the order of requests and beams, pages that go back
  *                follow the tail in the order of requests, columns and beams
- *   lens_out     device int32 [groups * beams]: tokens of the new rows
+ *   lens_out     device int32 [groups * beams]: tokens of the new rows; not lens or parent itself
  *   done         device int32 [groups]: 0 for a request that stays as it was: the ring has too
  *                few pages for it and those before (CLIS_PAGED_POOL_BIT), a parent is out
  *                of range (CLIS_PAGED_INDEX_BIT) or a length (CLIS_PAGED_LENGTH_BIT)

@@ -62,12 +62,12 @@ def few_rows(b):
     S, width = b["block_table"].shape
     pages, Hkv, page, d = b["k_cache"].shape
     g, max_q = b["q"].shape[1] // Hkv, min(b["max_q"], b["q"].shape[0])
-    rows, tile, keys = max_q * g, 32 if d == 64 else 16, 4096 // d
+    rows, tile, keys = max_q * g, 24 if d == 64 else 16, 4096 // d
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     if rows <= 64:
         return rows
     units = -(-width * page // keys) * S * Hkv * -(-rows // tile)
-    if max_q <= 2048 and rows <= 2048 and units <= (3 if d == 64 else 12) * sms * 8:
+    if max_q <= 2048 and rows <= 2048 and units <= (6 if d == 64 else 17) * sms * 8:
         return rows
     if S * Hkv <= 4 * sms and 2 * S * Hkv * width * page * d <= 16 << 20:
         return 0

@@ -46,6 +46,9 @@ SHAPES = [  # ctx, new, H, Hkv, d, page
     ([200, 5, 300, 17], [17, 300, 1, 2], 4, 4, 64, 8, 30000),
     ([4000, 70], [20, 1], 40, 8, 128, 256, 1000),
     ([300, 20], [600, 1], 16, 4, 128, 32),                      # 2,400 rows: the chunk kernel for the single token too
+    ([500, 3, 90, 3000], [3, 1, 2, 3], 32, 4, 64, 16),          # 24 rows at d = 64
+    ([500, 3, 900], [3, 0, 7], 8, 2, 64, 8),                    # 28 rows
+    ([2500, 64, 1], [10, 7, 1], 20, 4, 64, 64),                 # 50 rows
 ]
 
 

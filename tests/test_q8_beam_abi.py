@@ -150,7 +150,7 @@ def reorder_desc(**kw):
 
 
 def reorder(desc, ring_size=50, tensors=None, n=0, ws=FAKE, ws_bytes=1 << 50, **p):
-    a = dict(lens=FAKE, parent=FAKE, bt=FAKE, out=FAKE + 4096, ring=FAKE, size=ring_size, st=FAKE, so=FAKE + 64, lo=FAKE, done=FAKE)
+    a = dict(lens=FAKE, parent=FAKE, bt=FAKE, out=FAKE + 4096, ring=FAKE, size=ring_size, st=FAKE, so=FAKE + 64, lo=FAKE + 128, done=FAKE)
     a.update(p)
     return clis.load_library().clis_paged_reorder(desc, *a.values(), tensors, n, ws, ws_bytes, None)
 
@@ -169,6 +169,8 @@ def test_reorder_refusals():
         assert reorder(reorder_desc(), **{p: FAKE + 2}) == MISALIGNED, p
     assert reorder(reorder_desc(), so=FAKE) == INVALID and reorder(reorder_desc(), st=FAKE + 4) == MISALIGNED
     assert reorder(reorder_desc(bt_ss=16), out=FAKE) == INVALID  # in place with another stride
+    for p in ("lens", "parent"):  # inputs of all blocks
+        assert reorder(reorder_desc(), **{p: FAKE + 64}, lo=FAKE + 64) == INVALID
     assert reorder(reorder_desc(), n=-1) == INVALID and reorder(reorder_desc(), n=1) == INVALID
     assert reorder(reorder_desc(), tensors=pages(), n=9) == UNSUPPORTED
     for kw, st in ((dict(base=None), INVALID), (dict(layers=-1), INVALID), (dict(heads=-1), INVALID), (dict(row_bytes=0), INVALID),
