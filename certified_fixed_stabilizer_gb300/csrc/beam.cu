@@ -6,8 +6,8 @@
 // best first, ties to the lowest w * V + v.
 //
 // Bound: the logits' bytes, read once (96 requests of 8 beams, 128,000 tokens, bf16, a fifth of the
-// beams not in use: 59 us, of which the first kernel 38, whatever the loads in flight, 23 by the
-// copy rate; 8 requests of 4 beams and 32,003 tokens: 13 us, two dependent launches).  A row is cut into chunks of 512 logits.  The
+// beams not in use: 52 us, of which the first kernel 36, whatever the loads in flight, 23 by the
+// copy rate; 8 requests of 4 beams and 32,003 tokens: 12.5 us, two dependent launches).  A row is cut into chunks of 512 logits.  The
 // first kernel leaves each chunk's largest logit and the row's maximum and sum.  At most K
 // chunks can hold one of the K best: those whose largest logit leads to the K best such
 // values, so the second kernel (a block per request) picks them, reads them again (a
@@ -43,6 +43,7 @@ constexpr int kScanThreads = 256, kScanWarps = kScanThreads / 32;
 constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
 constexpr int kGroups = kMaxPicks;  // of leaders, for the bound
 constexpr int kPool = kPickThreads; // candidates that are ranked by counting
+constexpr int kAhead = 4;             // leaders of a thread that are loaded at once
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BeamParams {
@@ -97,6 +98,14 @@ __device__ __forceinline__ uint4 shifted_by(const uint4 &lo, const uint4 &hi, in
     }
 }
 
+// Logits that are read once (without a place in L1: 2 us less for 96 requests of 8 beams).
+__device__ __forceinline__ uint4 ldg_stream(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // What a lane loads of a chunk: its logits (the e-th at place(lane, e)) as they lie in
 // memory.  A row that is not 16-byte aligned is read in aligned pieces, each lane two
 // neighbouring ones; its first and last chunk one logit at a time, so that nothing outside
@@ -114,7 +123,7 @@ struct Raw {
         if (!whole) return;
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) + first * SIZE - off);
 #pragma unroll
-        for (int j = 0; j < P; j++) v[j] = __ldg(src + j * 32 + lane);
+        for (int j = 0; j < P; j++) v[j] = ldg_stream(src + j * 32 + lane);
         if (!ALIGNED && off != 0)
 #pragma unroll
             for (int j = 0; j < P; j++) u[ALIGNED ? 0 : j] = __ldg(src + j * 32 + lane + 1);
@@ -390,7 +399,9 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     const int leads = a.W * p.chunks;
     const float *lead = p.lead + static_cast<int64_t>(req) * leads;
     const Outputs out{a, static_cast<int64_t>(req) * a.K};
-    const float ahead = tid < leads ? lead[tid] : 0.f;  // (beside the rows' sums; a beam not in use may hold anything)
+    float ahead[kAhead];  // this thread's first leaders, beside the rows' sums (a beam not in use may hold anything)
+#pragma unroll
+    for (int j = 0; j < kAhead; j++) ahead[j] = tid + j * kPickThreads < leads ? lead[tid + j * kPickThreads] : 0.f;
 
     // ---- the rows' logarithms, in the order of the splits
     for (int w = warp; w < a.W; w += kPickWarps) {
@@ -437,9 +448,16 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     };
 
     // ---- the bound, the chunks that reach it, the logits that do
+    uint32_t first[kAhead];  // the first leaders' values
+#pragma unroll
+    for (int j = 0; j < kAhead; j++) {
+        const int i = tid + j * kPickThreads;
+        first[j] = i < leads ? static_cast<uint32_t>(leader(i, ahead[j]).v >> 32) : 0u;
+        if (first[j]) atomicMax(&s_group[i % kGroups], first[j]);
+    }
 #pragma unroll 1
-    for (int i = tid; i < leads; i += kPickThreads)
-        atomicMax(&s_group[i % kGroups], static_cast<uint32_t>(leader(i, i == tid ? ahead : lead[i]).v >> 32));
+    for (int i = tid + kAhead * kPickThreads; i < leads; i += kPickThreads)
+        atomicMax(&s_group[i % kGroups], static_cast<uint32_t>(leader(i, lead[i]).v >> 32));
     __syncthreads();
     if (tid < kGroups) {
         const uint32_t mine = s_group[tid];
@@ -450,27 +468,39 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     }
     __syncthreads();
     const uint32_t bound = s_bound;
+    auto found_one = [&](int i) {
+        const int k = atomicAdd(&s_chunks, 1);
+        if (k < kPool) s_chunk[k] = i;
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; j++)
+        if (first[j] >= bound) found_one(tid + j * kPickThreads);
 #pragma unroll 1
-    for (int i = tid; i < leads; i += kPickThreads)
-        if ((leader(i, i == tid ? ahead : lead[i]).v >> 32) >= bound) {
-            const int k = atomicAdd(&s_chunks, 1);
-            if (k < kPool) s_chunk[k] = i;
-        }
+    for (int i = tid + kAhead * kPickThreads; i < leads; i += kPickThreads)
+        if ((leader(i, lead[i]).v >> 32) >= bound) found_one(i);
     __syncthreads();
     const int found = s_chunks;
     if (found <= kPool) {
 #pragma unroll 1
-        for (int t = warp; t < 4 * found; t += kPickWarps) {
-            float x[E];
-            int w;
-            uint32_t at;
-            quarter(s_chunk[t >> 2], t & 3, x, w, at);
+        for (int t = warp; t < 4 * found; t += kAhead * kPickWarps) {
+            float x[kAhead][E];  // four quarters on their way
+            int w[kAhead];
+            uint32_t at[kAhead];
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                const Best b = x[e] == -INFINITY ? no_one() : best_of(value(s_score[w], x[e], s_lse[w]), at + e * 32);
-                if ((b.v >> 32) < bound) continue;
-                const int k = atomicAdd(&s_cands, 1);
-                if (k < kPool) pool[k] = b;
+            for (int j = 0; j < kAhead; j++) {
+                const int u = t + j * kPickWarps;
+                if (u < 4 * found) quarter(s_chunk[u >> 2], u & 3, x[j], w[j], at[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; j++) {
+                if (t + j * kPickWarps >= 4 * found) break;
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    const Best b = x[j][e] == -INFINITY ? no_one() : best_of(value(s_score[w[j]], x[j][e], s_lse[w[j]]), at[j] + e * 32);
+                    if ((b.v >> 32) < bound) continue;
+                    const int k = atomicAdd(&s_cands, 1);
+                    if (k < kPool) pool[k] = b;
+                }
             }
             if (s_cands > kPool) break;  // (only to save time: looked at again below)
         }
