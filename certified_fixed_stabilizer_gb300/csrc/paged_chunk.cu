@@ -55,11 +55,15 @@
 // registers that the softmax warps spill at d = 128) has not been taken apart.
 //
 // Over a cache of 8-bit codes (KS) K's pages hold the codes themselves, exact in 16 bits, and a
-// key's scale multiplies its scores as they come from TMEM.  The call of 2,048 tokens behind
-// 30,011 takes 869 to 893 us (40 of them unpacking, paged_read.cu), off by 2.5e-3.  With the
-// values of K and V rounded to bf16 it took 808 and was off by 4.4e-3; with the scales
-// multiplied in at both uses of a score, read from shared memory each time, 1,015.  The K/V
-// producer brings the scales into a ring of kScaleTiles tiles of shared memory.  K of tile n is
+// key's scale (with scale_log2) multiplies its scores as they come from TMEM, in the same
+// instruction that subtracts the shift: what the weights take is then ready, and the first half is
+// scaled while the second is on its way.  The call of 2,048 tokens behind 30,011 takes 823 us
+// (40 of them unpacking, paged_read.cu; without the multiplications 739), off by 2.5e-3.  With
+// scales multiplied in by themselves, all scores loaded before, it took 851; with the values of K
+// and V rounded to bf16 808, off by 4.4e-3.  A thread reads 128 scales a tile, 128 cycles of the
+// register file's port for each of 8 warps, which is what is left of the difference.
+// The K/V producer copies the scales into a ring of kScaleTiles tiles of shared memory,
+// asynchronously, on the barrier of the tile (through registers: 831).  K of tile n is
 // loaded when the scores of tile n - NSTAGE / 2 have been computed, so both softmax groups are
 // done with tile n - 3 - NSTAGE / 2 at least, and its place in the ring of scales is free.
 //
@@ -331,6 +335,12 @@ abort:
         if (wt[t] > 0) drain_wait(smem_u32(&c.q_full[t]), (wt[t] - 1) & 1);
 }
 
+// 16 bytes, of which the first `bytes` are read and the others zeros.
+__device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 template <int D, bool KS>
 __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
                               uint32_t sKV, float *scales, const Run &R)
@@ -350,30 +360,16 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
     CLIS_FOR_WORK(K)
     {
         const ChunkItem &T = K.t;
-        // Scales of the lane's four keys of key tile kt (a page holds at least eight): their
-        // page two tiles ahead, themselves one.  Keys behind the last, and those of pages
-        // out of range, get the scale 1.
+        // Page of the lane's four keys of key tile kt, whose scales it copies (a page holds at least
+        // eight); looked up two tiles ahead.
         auto scale_page = [&](int kt) -> int {
             const int key = kt * BN + lane * 4;
             return key < T.kv && kt < K.start + K.n ? __ldg(a.block_table + T.s * a.bt_s + (key >> a.page_shift)) : -1;
         };
-        auto scale_of = [&](int kt, int pg) -> float4 {
-            float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
-            const int key = kt * BN + lane * 4;
-            if (pg < 0 || pg >= a.num_pages) return x;
-            const float4 y = __ldg(reinterpret_cast<const float4 *>(
-                a.ks + ((static_cast<int64_t>(pg) * a.Hkv + T.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))));
-            x.x = y.x;
-            if (key + 1 < T.kv) x.y = y.y;
-            if (key + 2 < T.kv) x.z = y.z;
-            if (key + 3 < T.kv) x.w = y.w;
-            return x;
-        };
-        float4 sc = make_float4(1.f, 1.f, 1.f, 1.f);
-        int sc_page = -1;
+        int sc_page = -1, sc_next = -1;
         if constexpr (KS) {
-            sc = scale_of(K.start, scale_page(K.start));
-            sc_page = scale_page(K.start + 1);
+            sc_page = scale_page(K.start);
+            sc_next = scale_page(K.start + 1);
         }
         // Whether the lane has rows of key tile kt to load (none behind the last key), and
         // their page.  What the table holds is looked at when it is used, a tile later (any
@@ -396,18 +392,22 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
                     goto abort;
             }
             const uint32_t bar = smem_u32(&c.kv_full[gq % C::NSTAGE]);
-            if constexpr (KS) {
-                if (has_k) {  // (before the arrival on the group's barrier)
-                    *reinterpret_cast<float4 *>(scales + (kt_all % kScaleTiles) * BN + lane * 4) = sc;
-                    ++kt_all;
-                    sc = scale_of(K.start + gi + 1, sc_page);
-                    sc_page = scale_page(K.start + gi + 2);
-                    __syncwarp();
-                }
-            }
             const int live = __popc(__ballot_sync(~0u, rows_v)) + __popc(__ballot_sync(~0u, rows_k));
             if (lane == 0) mbar_arrive_expect_tx(bar, live * C::NBOX * box_bytes);
             __syncwarp();
+            if constexpr (KS) {
+                if (has_k) {  // (zeros for keys behind the last and those of pages out of range)
+                    const int key = (K.start + gi) * BN + lane * 4;
+                    const bool ok = sc_page >= 0 && sc_page < a.num_pages;
+                    const float *src = a.ks + ((((ok ? static_cast<int64_t>(sc_page) : 0) * a.Hkv + T.h) << a.page_shift) +
+                                               (ok ? key & ((1 << a.page_shift) - 1) : 0));
+                    cp_async16_fill(smem_u32(scales + (kt_all % kScaleTiles) * BN + lane * 4), src, ok ? 4 * min(4, T.kv - key) : 0);
+                    ++kt_all;
+                    sc_page = sc_next;
+                    sc_next = scale_page(K.start + gi + 2);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+            }
 #pragma unroll
             for (int l = 0; l < 2; l++) {
                 const bool is_v = l == 0;
@@ -438,6 +438,7 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
 abort:
     for (uint32_t k = (gq > C::NSTAGE ? gq - C::NSTAGE : 0); k < gq; k++)
         drain_wait(smem_u32(&c.kv_full[k % C::NSTAGE]), (k / C::NSTAGE) & 1);
+    if constexpr (KS) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- edge tiles
@@ -693,8 +694,9 @@ abort:
 
 // Weights of a row's 128 scores for a shift, p = 2^(scale_log2 s - shift), packed in
 // pairs over the first 64 columns of the scores, all of which have been read;
-// returns their sum (before rounding).
-template <int DT>
+// returns their sum (before rounding).  FORM 0; 1: the scores have their factors and the shift
+// already; 2: their factors.
+template <int DT, int FORM>
 __device__ __forceinline__ float weights128(const uint32_t *s, float sl2, float nshift, uint32_t tP)
 {
     const float2 sc2 = make_float2(sl2, sl2), sh2 = make_float2(nshift, nshift);
@@ -704,8 +706,9 @@ __device__ __forceinline__ float weights128(const uint32_t *s, float sl2, float 
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; e++) {
-            const float2 x = ffma2(
-                make_float2(__uint_as_float(s[c32 * 32 + 2 * e]), __uint_as_float(s[c32 * 32 + 2 * e + 1])), sc2, sh2);
+            float2 x = make_float2(__uint_as_float(s[c32 * 32 + 2 * e]), __uint_as_float(s[c32 * 32 + 2 * e + 1]));
+            if (FORM == 0) x = ffma2(x, sc2, sh2);
+            if (FORM == 2) x = fadd2(x, sh2);
             const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             if (e & 1) lb = fadd2(lb, pp);
             else la = fadd2(la, pp);
@@ -749,19 +752,26 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, const 
             if (!mbar_wait(smem_u32(&c.s_full[t]), g & 1, ab, err, kErrSoftmax)) return;
             tc_fence_after();
             uint32_t s[BN];
+            const int key0 = (K.start + j) * BN;
             tmem_ld32(tS + 0, s + 0);
             tmem_ld32(tS + 32, s + 32);
-            tmem_ld32(tS + 64, s + 64);
-            tmem_ld32(tS + 96, s + 96);
-            tmem_wait_ld();
-            const int key0 = (K.start + j) * BN;
-            if constexpr (KS) {
+            if constexpr (!KS) {
+                tmem_ld32(tS + 64, s + 64);
+                tmem_ld32(tS + 96, s + 96);
+                tmem_wait_ld();
+            } else {  // (the scales with scale_log2; the shift of the tile before comes off at once)
+                const float sh = m_run == -INFINITY ? 0.f : -m_run;
+                const float2 sh2 = make_float2(sh, sh);
                 const float4 *ks = reinterpret_cast<const float4 *>(scales + ((kt_all + j) % kScaleTiles) * BN);
+                tmem_wait_ld();
+                tmem_ld32(tS + 64, s + 64);
+                tmem_ld32(tS + 96, s + 96);
 #pragma unroll
                 for (int cc = 0; cc < BN; cc += 4) {
+                    if (cc == BN / 2) tmem_wait_ld();
                     const float4 k4 = ks[cc / 4];
-                    const float2 x = fmul2(make_float2(__uint_as_float(s[cc]), __uint_as_float(s[cc + 1])), make_float2(k4.x, k4.y));
-                    const float2 y = fmul2(make_float2(__uint_as_float(s[cc + 2]), __uint_as_float(s[cc + 3])), make_float2(k4.z, k4.w));
+                    const float2 x = ffma2(make_float2(__uint_as_float(s[cc]), __uint_as_float(s[cc + 1])), make_float2(k4.x, k4.y), sh2);
+                    const float2 y = ffma2(make_float2(__uint_as_float(s[cc + 2]), __uint_as_float(s[cc + 3])), make_float2(k4.z, k4.w), sh2);
                     s[cc] = __float_as_uint(x.x);
                     s[cc + 1] = __float_as_uint(x.y);
                     s[cc + 2] = __float_as_uint(y.x);
@@ -774,7 +784,7 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, const 
                     if (key0 + cc >= lim) s[cc] = 0xFF800000u;  // -inf
             }
             float l = 0.f;
-            if (begun) l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
+            if (begun) l = weights128<DT, KS ? 1 : 0>(s, sl2, m_run == -INFINITY ? 0.f : -m_run, tS);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int cc = 0; cc < BN; cc += 8) {
@@ -782,18 +792,20 @@ __device__ void softmax_role(const ChunkParams &p, Ctl &c, uint32_t tmem, const 
                 for (int q4 = 0; q4 < 4; q4++)
                     mx[q4] = fmax3(mx[q4], __uint_as_float(s[cc + 2 * q4]), __uint_as_float(s[cc + 2 * q4 + 1]));
             }
-            const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float m_tile = KS ? (m_run == -INFINITY ? top : top + m_run) : top * sl2;
             const bool grow = m_tile > m_run + (kTau + weight_room(DT));  // always true where a row's first visible key is
             if (__any_sync(0xFFFFFFFFu, grow) || !begun) {
                 // Raise the shift, compute the tile's weights (again), and shrink O once the
                 // last product is in it.
                 const float m_new = m_tile - weight_room(DT);
-                const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
+                const float m_old = m_run, alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
                 if (grow) m_run = m_new;
                 l_run *= alpha;
+                const float back = KS && m_old != -INFINITY ? m_old : 0.f;  // (what came off already)
                 // (stores to TMEM are asynchronous: the weights that these replace must be in place)
                 if (begun) tmem_wait_st();
-                l = weights128<DT>(s, sl2, (m_run == -INFINITY) ? 0.f : -m_run, tS);
+                l = weights128<DT, KS ? 2 : 0>(s, sl2, m_run == -INFINITY ? 0.f : back - m_run, tS);
                 if (begun) {
                     if (!mbar_wait(smem_u32(&c.pv_done[t]), (g - 1) & 1, ab, err, kErrSoftmax)) return;
                     tc_fence_after();
@@ -1148,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ctl.epi_full[t]), BM);
         }
         for (int s = 0; s < C::NSTAGE; s++) {
-            mbar_init(smem_u32(&ctl.kv_full[s]), 1);
+            mbar_init(smem_u32(&ctl.kv_full[s]), KS ? 33 : 1);  // TMA's bytes, and 32 lanes' scales
             mbar_init(smem_u32(&ctl.kv_empty[s]), 1);
         }
         mbar_init(smem_u32(&ctl.edge_go), 1);

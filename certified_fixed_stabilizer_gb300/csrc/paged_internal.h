@@ -76,7 +76,7 @@ struct PagedArgs {
     float scale_log2;
     int causal;
     // The chunk kernel over unpacked codes: K's pages hold codes, ks [num_pages][Hkv][page
-    // size] their scales.  nullptr: K's pages hold values.
+    // size] their scales times scale_log2.  nullptr: K's pages hold values.
     const float *ks = nullptr;
 };
 
@@ -103,7 +103,7 @@ struct ReadArgs {
 clis_status_t launch_paged_read(const ReadArgs &a, cudaStream_t stream);
 // Every key and value of the sequences that the chunk kernel works on, in 16 bits in
 // pages of the same numbers, [num_pages][Hkv][page size][d] each: K's codes as they are
-// with their scales in k_scale [num_pages][Hkv][page size], V's values.
+// with their scales times a.scale_log2 in k_scale [num_pages][Hkv][page size], V's values.
 // Launched behind launch_paged_chunk_schedule, beside which it may run.
 clis_status_t launch_paged_unpack(const PagedArgs &a, const QuantArgs &z, int rows_small, uint16_t *k_pages, float *k_scale,
                                   uint16_t *v_pages, int nsm, cudaStream_t stream);

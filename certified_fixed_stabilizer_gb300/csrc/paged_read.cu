@@ -99,11 +99,11 @@ struct Token {
 };
 
 // Heads it0 / IPH .. of the block's tokens, kBatch pieces in flight.  SCALED: K's values (else its
-// codes as they are, and its scales to k_scale at their offset `ko` / D of the row).
+// codes as they are, and its scales times k_times to k_scale at their offset `ko` / D of the row).
 template <int CODE, int DT, int D, bool SCALED>
 __device__ __forceinline__ void convert(const uint8_t *kc, const uint8_t *vc, const float *ks, const float *vs, int64_t kc_sh, int64_t vc_sh,
                                         int64_t ks_sh, int64_t vs_sh, uint16_t *ko, uint16_t *vo, int64_t ko_sh, int64_t vo_sh, float *k_scale,
-                                        int64_t k_scale_sh, int Hkv, const Token *tok, int it0, int step)
+                                        int64_t k_scale_sh, float k_times, int Hkv, const Token *tok, int it0, int step)
 {
     using S = Split<D>;
     constexpr int B = CODE < 0 ? 2 : 1;
@@ -127,7 +127,7 @@ __device__ __forceinline__ void convert(const uint8_t *kc, const uint8_t *vc, co
             if (hh >= 2 * Hkv || !t.to) continue;
             if (hh < Hkv) {
                 if (!SCALED) {
-                    if (piece == 0) k_scale[t.ko / D + hh * k_scale_sh] = x[b].scale;
+                    if (piece == 0) k_scale[t.ko / D + hh * k_scale_sh] = x[b].scale * k_times;
                     x[b].scale = 1.f;
                 }
                 store_piece<CODE, DT>(x[b], ko + t.ko + hh * ko_sh + piece * 8);
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kReadThreads) paged_read_kernel(const ReadArgs
         tok[i] = {pg * a.kc_sp + in * a.kc_sn, pg * a.vc_sp + in * a.vc_sn, pg * a.z.ks_sp + in * a.z.ks_sn, pg * a.z.vs_sp + in * a.z.vs_sn,
                   row * a.ko_st, row * a.vo_st, at.x >= 0, at.x != -2};
     }
-    convert<CODE, DT, D, true>(a.z.kc, a.z.vc, a.z.ks, a.z.vs, a.kc_sh, a.vc_sh, a.z.ks_sh, a.z.vs_sh, a.ko, a.vo, a.ko_sh, a.vo_sh, nullptr, 0,
+    convert<CODE, DT, D, true>(a.z.kc, a.z.vc, a.z.ks, a.z.vs, a.kc_sh, a.vc_sh, a.z.ks_sh, a.z.vs_sh, a.ko, a.vo, a.ko_sh, a.vo_sh, nullptr, 0, 1.f,
                                a.Hkv, tok, blockIdx.y * kBatch, gridDim.y * kBatch);
 }
 
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kReadThreads) paged_unpack_kernel(const Unpack
             tok[i] = {pg * a.kc_sp + in * a.kc_sn, pg * a.vc_sp + in * a.vc_sn, pg * z.ks_sp + in * z.ks_sn, pg * z.vs_sp + in * z.vs_sn,
                       to, to, ok, ok};
         }
-        convert<CODE, DT, D, false>(z.kc, z.vc, z.ks, z.vs, a.kc_sh, a.vc_sh, z.ks_sh, z.vs_sh, p.ko, p.vo, head, head, p.ks, mask + 1, a.Hkv,
+        convert<CODE, DT, D, false>(z.kc, z.vc, z.ks, z.vs, a.kc_sh, a.vc_sh, z.ks_sh, z.vs_sh, p.ko, p.vo, head, head, p.ks, mask + 1, a.scale_log2, a.Hkv,
                                     tok, 0, kBatch);
         if (++j == n && u + 1 < u1) {
             do s++;
