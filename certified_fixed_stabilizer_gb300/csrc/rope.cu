@@ -26,9 +26,9 @@
 // kernels that write the cache spill 32 bytes of registers; the plain ones do not.
 //
 // Into a cache of codes a row's scale needs its largest magnitude: its 4 or 8 threads
-// exchange it by shuffles and each writes its 16 codes.  The same chunk (185 MB) takes 45 us, 27
-// by the copy rate: two blocks an SM (three, with spills, 51; 4, 8, 12, 24 or 48 heads a block
-// 60, 49, 47, 47 and 47).
+// exchange it by shuffles and each writes its 16 codes.  The same chunk (185 MB) takes 43 us, 27
+// by the copy rate: two blocks an SM (three, with spills, 51; in one launch with q's rotation 45 with 16
+// heads a block, 60, 49, 47, 47 and 47 with 4, 8, 12, 24 and 48).
 #include <cuda_bf16.h>
 
 #include "clis_internal.h"
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kRotThreads, MODE > 1 ? 2 : 3) rot_kernel(cons
     constexpr bool APPEND = MODE > 0;
     constexpr int CODE = MODE - 2;
     __shared__ unsigned long long s_step[kMaxPairs];
+    if (MODE > 1) pdl_launch();
     __shared__ int s_axis[kMaxPairs];
     const int idx = blockIdx.x * kRotThreads + threadIdx.x;
     const bool live = idx < a.B * a.N * NC;
@@ -279,11 +280,32 @@ __global__ void __launch_bounds__(kRotThreads, MODE > 1 ? 2 : 3) rot_kernel(cons
         }
         load(h + kHeadBatch);
     }
+    if (MODE == 0) pdl_wait();  // (a write of codes beside it)
+}
+
+// A write of codes beside q's rotation: a launch each, since q's kernel has three blocks an SM
+// and the other two.  Worth a second launch from 32 blocks of rows on where q has most of the
+// heads (32 and 8, d = 128: 1,024 rows 12.6 us together, 11.2 apart; 8,192 45.4 and 42.8; 512 rows 8.5
+// and 10.5; 8,192 rows of 32 and 32 heads 85.6 and 86.8).
+template <int DT, int NC>
+cudaError_t launch_codes_and_q(const RotArgs &a, int blocks, cudaStream_t stream)
+{
+    constexpr int KV = 8, Q = 16;  // heads per thread
+    RotArgs kv = a, q = a;
+    kv.Hq = 0;
+    q.Hk = 0;
+    q.slots = nullptr;
+    const auto codes = a.code == CLIS_CODE_INT8 ? rot_kernel<DT, NC, 2> : rot_kernel<DT, NC, 3>;
+    codes<<<dim3(blocks, (2 * a.Hk + KV - 1) / KV), kRotThreads, 0, stream>>>(kv, KV);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(rot_kernel<DT, NC, 0>, dim3(blocks, (a.Hq + Q - 1) / Q), kRotThreads, 0, stream, q, Q);
 }
 
 template <int DT, int NC>
 cudaError_t launch_rot_impl(const RotArgs &a, dim3 grid, int hg, cudaStream_t stream)
 {
+    if (a.slots && a.code >= 0 && a.Hq >= 4 * a.Hk && grid.x >= 32) return launch_codes_and_q<DT, NC>(a, grid.x, stream);
     if (!a.slots)
         rot_kernel<DT, NC, 0><<<grid, kRotThreads, 0, stream>>>(a, hg);
     else if (a.code < 0)
