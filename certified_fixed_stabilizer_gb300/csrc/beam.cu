@@ -6,8 +6,8 @@
 // best first, ties to the lowest w * V + v.
 //
 // Bound: the logits' bytes, read once (96 requests of 8 beams, 128,000 tokens, bf16, a fifth of the
-// beams not in use: 52 us, of which the first kernel 36, whatever the loads in flight, 23 by the
-// copy rate; 8 requests of 4 beams and 32,003 tokens: 12.5 us, two dependent launches).  A row is cut into chunks of 512 logits.  The
+// beams not in use: 47 us, of which the second kernel 11; 23 by the copy rate.  8 requests of 4 beams and
+// 32,003 tokens: 12.4 us, two dependent launches).  A row is cut into chunks of 512 logits.  The
 // first kernel leaves each chunk's largest logit and the row's maximum and sum.  At most K
 // chunks can hold one of the K best: those whose largest logit leads to the K best such
 // values, so the second kernel (a block per request) picks them, reads them again (a
@@ -40,6 +40,10 @@ namespace {
 
 constexpr int kChunk = 512, kPer = kChunk / 32;  // logits of a chunk, of a lane
 constexpr int kScanThreads = 256, kScanWarps = kScanThreads / 32;
+// Chunks of a segment, on their way at a time, and blocks of an SM (registers).
+constexpr int max_seg(int dtype) { return dtype == 2 ? 1 : 2; }
+constexpr int scan_blocks(bool aligned) { return aligned ? 4 : 3; }
+constexpr int kMaxListed = 8192; // rows
 constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
 constexpr int kGroups = kMaxPicks;  // of leaders, for the bound
 constexpr int kPool = kPickThreads; // candidates that are ranked by counting
@@ -49,10 +53,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct BeamParams {
     BeamArgs a;
     int chunks;     // of a row
-    int per_warp;   // chunks that a warp of the first kernel takes
-    int splits;     // blocks of a row
+    int seg;        // chunks of a segment
+    int segs;       // segments of a row
+    bool listed;    // runs of segments of the beams in use; else a warp per segment
     float *lead;    // [R * W][chunks] largest logit
-    float2 *part;   // [R * W][splits] maximum and sum
+    float2 *part;   // [R * W][segs] maximum and sum
 };
 
 __device__ __forceinline__ float logit(const void *row, int dtype, int64_t i)
@@ -181,35 +186,97 @@ __device__ __forceinline__ void merge(float &m, float &s, float m1, float s1)
     m = mm;
 }
 
+// The rows of beams in use, in order, in s_rows; returns their number.
+__device__ __forceinline__ int list_rows(const float *scores, int rows, uint16_t *s_rows, uint32_t *s_mask, int *s_sum)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, words = (rows + 31) / 32;
+    for (int j = warp; j < words; j += kScanWarps) {
+        const int r = j * 32 + lane;
+        const uint32_t mask = __ballot_sync(~0u, r < rows && isfinite(__ldg(scores + min(r, rows - 1))));
+        if (lane == 0) s_mask[j] = mask;
+    }
+    __syncthreads();
+    static_assert(kMaxListed / 32 <= kScanThreads, "a thread per word");
+    const int n = threadIdx.x < words ? __popc(s_mask[threadIdx.x]) : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int at = incl - n, total = 0;
+    for (int i = 0; i < kScanWarps; i++) {
+        if (i < warp) at += s_sum[i];
+        total += s_sum[i];
+    }
+    if (threadIdx.x < words)
+        for (uint32_t mask = s_mask[threadIdx.x]; mask; mask &= mask - 1) s_rows[at++] = static_cast<uint16_t>(threadIdx.x * 32 + __ffs(mask) - 1);
+    __syncthreads();
+    return total;
+}
+
+// A warp reads segments of one or two chunks, the next one's chunks on their way as those of the one
+// at hand have been looked at, also from row to row: runs of segments of the beams in use,
+// as many for each warp (few logits: a warp per segment).  A block per 128 chunks of a row,
+// which began and ended without loads on their way, took 5 us more for 96 requests of 8 beams;
+// segments of four chunks with three blocks an SM 1.5, two blocks an SM 10: it is warps that hide
+// a chunk's chain of instructions.
 template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParams p)
+__global__ void __launch_bounds__(kScanThreads, scan_blocks(ALIGNED)) beam_scan_kernel(const BeamParams p)
 {
     const BeamArgs &a = p.a;
-    __shared__ float2 s_part[kScanWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r = blockIdx.y, split = blockIdx.x;
+    __shared__ uint16_t s_rows[kMaxListed];
+    __shared__ uint32_t s_mask[kMaxListed / 32];
+    __shared__ int s_sum[kScanWarps];
+    const int lane = threadIdx.x & 31, worker = blockIdx.x * kScanWarps + (threadIdx.x >> 5), rows = a.R * a.W;
     pdl_launch();
-    const float score = __ldg(a.scores + r);
-    const int req = r / a.W, w = r - req * a.W;
-    const void *row = static_cast<const uint8_t *>(a.logits) + (req * a.l_sr + w * a.l_sw) * (DT == 2 ? 4 : 2);
-    const int c0 = (split * kScanWarps + warp) * p.per_warp, c1 = min(p.chunks, c0 + p.per_warp);
-    float m = -INFINITY, s = 0.f;       // the warp's maximum, the lane's sum
-    constexpr int B = DT == 2 || !ALIGNED ? 2 : 4;  // chunks on their way
+    int64_t u = worker;  // its first segment
+    int left = 1;        // and how many
+    const bool list = p.listed && rows <= kMaxListed;  // (else those of beams not in use are read as well)
+    if (p.listed) {
+        const int64_t n = static_cast<int64_t>(list ? list_rows(a.scores, rows, s_rows, s_mask, s_sum) : rows) * p.segs;
+        const int workers = gridDim.x * kScanWarps;
+        u = n * worker / workers;
+        left = static_cast<int>(n * (worker + 1) / workers - u);
+    }
+    if (left <= 0 || (!p.listed && u >= static_cast<int64_t>(rows) * p.segs)) return;
+    int rank = static_cast<int>(u / p.segs), c = static_cast<int>(u - static_cast<int64_t>(rank) * p.segs) * p.seg;  // its first chunk
+    int r = list ? s_rows[rank] : rank;
+    auto row_of = [&](int i) {
+        const int req = i / a.W, w = i - req * a.W;
+        return static_cast<const uint8_t *>(a.logits) + (req * a.l_sr + w * a.l_sw) * (DT == 2 ? 4 : 2);
+    };
+    const uint8_t *row = row_of(r);
+    constexpr int B = max_seg(DT);
     Raw<DT, ALIGNED> raw[B];
 #pragma unroll
     for (int b = 0; b < B; b++)
-        if (c0 + b < c1) raw[b].load(row, static_cast<int64_t>(c0 + b) * kChunk, a.V, lane);
-    if (!isfinite(score)) return;  // a beam not in use (known only now: the loads do not wait for it)
-    for (int c = c0; c < c1; c += B) {
+        if (b < p.seg && c + b < p.chunks) raw[b].load(row, static_cast<int64_t>(c + b) * kChunk, a.V, lane);
+    if (!p.listed && !isfinite(__ldg(a.scores + r))) return;  // a beam not in use (known only now: the loads do not wait for it)
+    while (true) {
+        // the segment after this one
+        const uint8_t *row1 = row;
+        int r1 = r, c1 = c + p.seg;
+        if (left > 1 && c1 >= p.chunks) {
+            rank++;
+            r1 = list ? s_rows[rank] : rank;
+            row1 = row_of(r1);
+            c1 = 0;
+        }
+        float m = -INFINITY, s = 0.f;  // the segment's maximum, the lane's sum
 #pragma unroll
         for (int b = 0; b < B; b++) {
-            if (c + b >= c1) continue;
+            if (b >= p.seg) continue;
             float x[kPer];
-            raw[b].values(row, static_cast<int64_t>(c + b) * kChunk, a.V, lane, x);
-            if (c + b + B < c1) raw[b].load(row, static_cast<int64_t>(c + b + B) * kChunk, a.V, lane);
-            float mx = x[0];
+            const bool has = c + b < p.chunks;
+            if (has) raw[b].values(row, static_cast<int64_t>(c + b) * kChunk, a.V, lane, x);
+            if (left > 1 && c1 + b < p.chunks) raw[b].load(row1, static_cast<int64_t>(c1 + b) * kChunk, a.V, lane);
+            if (!has) continue;
+            float mx = fmaxf(x[0], x[1]);  // (a NaN is left to the sum)
 #pragma unroll
-            for (int e = 1; e < kPer; e++) mx = fmaxf(mx, x[e]);  // (a NaN is left to the sum)
+            for (int e = 2; e < kPer; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
             mx = from_ordered(__reduce_max_sync(~0u, ordered(mx)));
             if (lane == 0) p.lead[static_cast<int64_t>(r) * p.chunks + c + b] = mx;
             if (mx > m) {
@@ -225,14 +292,13 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParam
             }
             s += sum.x + sum.y;
         }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    if (lane == 0) s_part[warp] = make_float2(m, s);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kScanWarps; i++) merge(m, s, s_part[i].x, s_part[i].y);
-        p.part[static_cast<int64_t>(r) * p.splits + split] = make_float2(m, s);
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+        if (lane == 0) p.part[static_cast<int64_t>(r) * p.segs + c / p.seg] = make_float2(m, s);
+        if (--left == 0) break;
+        r = r1;
+        c = c1;
+        row = row1;
     }
 }
 
@@ -403,14 +469,20 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
 #pragma unroll
     for (int j = 0; j < kAhead; j++) ahead[j] = tid + j * kPickThreads < leads ? lead[tid + j * kPickThreads] : 0.f;
 
-    // ---- the rows' logarithms, in the order of the splits
+    // ---- the rows' logarithms, in the order of the segments
     for (int w = warp; w < a.W; w += kPickWarps) {
         const int r = req * a.W + w;
         const float score = __ldg(a.scores + r);
         float m = -INFINITY, s = 0.f;
-        for (int i = lane; i < p.splits; i += 32) {
-            const float2 v = p.part[static_cast<int64_t>(r) * p.splits + i];
-            merge(m, s, v.x, v.y);
+        for (int i0 = 0; i0 < p.segs; i0 += 32 * kAhead) {
+            float2 v[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; j++) {
+                const int i = i0 + j * 32 + lane;
+                v[j] = i < p.segs ? p.part[static_cast<int64_t>(r) * p.segs + i] : make_float2(-INFINITY, 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; j++) merge(m, s, v[j].x, v[j].y);
         }
         bool ok = isfinite(score);
         if (ok) {
@@ -561,36 +633,33 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
 
 int chunks_of(const BeamArgs &a) { return (a.V + kChunk - 1) / kChunk; }
 
-// Chunks per warp of the first kernel: about 16 warps a SM or more, up to 8 chunks each.
+// Segments of one chunk and a warp for each while the GPU holds them all.
 void plan(const BeamArgs &a, int nsm, BeamParams &p)
 {
     p.a = a;
     p.chunks = chunks_of(a);
-    const int64_t rows = static_cast<int64_t>(a.R) * a.W;
-    p.per_warp = 1;
-    while (p.per_warp < 16 && rows * p.chunks / (2 * p.per_warp) >= static_cast<int64_t>(nsm) * 32) p.per_warp *= 2;
-    const int per_block = kScanWarps * p.per_warp;
-    p.splits = (p.chunks + per_block - 1) / per_block;
+    const int64_t rows = static_cast<int64_t>(a.R) * a.W, workers = static_cast<int64_t>(scan_blocks(false)) * nsm * kScanWarps;
+    p.listed = rows * p.chunks > workers;
+    p.seg = p.listed ? max_seg(a.dtype) : 1;
+    p.segs = (p.chunks + p.seg - 1) / p.seg;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 template <int DT, bool ALIGNED>
-cudaError_t launch_impl(const BeamParams &p, cudaStream_t stream)
+cudaError_t launch_impl(const BeamParams &p, int nsm, cudaStream_t stream)
 {
-    beam_scan_kernel<DT, ALIGNED><<<dim3(p.splits, p.a.R * p.a.W), kScanThreads, 0, stream>>>(p);
+    const int64_t units = static_cast<int64_t>(p.a.R) * p.a.W * p.segs, blocks = (units + kScanWarps - 1) / kScanWarps, most = scan_blocks(ALIGNED) * nsm;
+    beam_scan_kernel<DT, ALIGNED><<<static_cast<unsigned>(blocks < most ? blocks : most), kScanThreads, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_pdl(beam_pick_kernel<DT>, dim3(p.a.R), kPickThreads, 0, stream, p);
 }
 
 template <int DT>
-cudaError_t launch_type(const BeamParams &p, cudaStream_t stream)
+cudaError_t launch_type(const BeamParams &p, bool aligned, int nsm, cudaStream_t stream)
 {
-    constexpr int64_t size = DT == 2 ? 4 : 2;
-    const BeamArgs &a = p.a;
-    const bool aligned = !((reinterpret_cast<uintptr_t>(a.logits) | a.l_sr * size | a.l_sw * size) & 15);
-    return aligned ? launch_impl<DT, true>(p, stream) : launch_impl<DT, false>(p, stream);
+    return aligned ? launch_impl<DT, true>(p, nsm, stream) : launch_impl<DT, false>(p, nsm, stream);
 }
 
 }  // namespace
@@ -600,19 +669,21 @@ size_t beam_workspace(const BeamArgs &a, int nsm)
     BeamParams p;
     plan(a, nsm, p);
     const size_t rows = static_cast<size_t>(a.R) * a.W;
-    return up256(rows * p.chunks * sizeof(float)) + up256(rows * p.splits * sizeof(float2));
+    return up256(rows * p.chunks * sizeof(float)) + up256(rows * p.segs * sizeof(float2));
 }
 
 clis_status_t launch_beam(const BeamArgs &a, void *workspace, int nsm, cudaStream_t stream)
 {
     BeamParams p;
+    const int64_t size = a.dtype == 2 ? 4 : 2;
+    const bool aligned = !((reinterpret_cast<uintptr_t>(a.logits) | a.l_sr * size | a.l_sw * size) & 15);
     plan(a, nsm, p);
     const size_t rows = static_cast<size_t>(a.R) * a.W;
     p.lead = static_cast<float *>(workspace);
     p.part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + up256(rows * p.chunks * sizeof(float)));
-    const cudaError_t e = a.dtype == CLIS_DT_BF16 ? launch_type<CLIS_DT_BF16>(p, stream)
-                          : a.dtype == CLIS_DT_FP16 ? launch_type<CLIS_DT_FP16>(p, stream)
-                                                    : launch_type<2>(p, stream);
+    const cudaError_t e = a.dtype == CLIS_DT_BF16 ? launch_type<CLIS_DT_BF16>(p, aligned, nsm, stream)
+                          : a.dtype == CLIS_DT_FP16 ? launch_type<CLIS_DT_FP16>(p, aligned, nsm, stream)
+                                                    : launch_type<2>(p, aligned, nsm, stream);
     return e == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
 

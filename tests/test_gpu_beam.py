@@ -94,6 +94,22 @@ def test_masked_tokens_and_beams_not_in_use():
     assert got.token[1].tolist() == [7] + [-1] * 7 and got.parent[2].tolist() == [-1] * 8
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("R,V", [(60, 20001), (60, 16384), (1100, 600)])
+def test_runs_of_beams_in_use(R, V, dtype):
+    """More logits than the GPU holds warps for: the beams in use are shared out among them, of up to 8,192 rows;
+    a third is not in use, with NaN where nobody looks, among them the first and last rows and whole requests."""
+    g = torch.Generator(device="cuda").manual_seed(R + V)
+    logits = (3 * torch.randn((R, 8, V), generator=g, device="cuda")).to(DT[dtype])
+    scores = -5 * torch.rand((R, 8), generator=g, device="cuda")
+    dead = torch.rand((R, 8), generator=g, device="cuda") < 0.33
+    dead[0, 0] = dead[-1, -1] = True
+    dead[R // 2] = dead[R // 2 + 1] = True
+    scores[dead] = -math.inf
+    logits[dead] = math.nan
+    check(logits, scores, 4)
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_rows_that_are_no_distribution(bad):
     g = torch.Generator(device="cuda").manual_seed(7)
