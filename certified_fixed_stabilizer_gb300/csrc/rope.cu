@@ -26,7 +26,7 @@
 // kernels that write the cache spill 32 bytes of registers; the plain ones do not.
 //
 // Into a cache of codes a row's scale needs its largest magnitude: its 4 or 8 threads
-// exchange it by shuffles and each writes its 16 codes.  The same chunk (185 MB) takes 43 us, 27
+// exchange it by shuffles and each writes its 16 codes.  The same chunk (185 MB) takes 41 us, 27
 // by the copy rate: two blocks an SM (three, with spills, 51; in one launch with q's rotation 45 with 16
 // heads a block, 60, 49, 47, 47 and 47 with 4, 8, 12, 24 and 48).
 #include <cuda_bf16.h>
@@ -202,10 +202,11 @@ __global__ void __launch_bounds__(kRotThreads, MODE > 1 ? 2 : 3) rot_kernel(cons
         }
     };
     load(h0);
+    const bool angles = MODE < 2 || h0 < a.Hq + a.Hk;  // (a block of V's heads alone turns nothing)
     int pos[kMaxAxes];
 #pragma unroll
     for (int x = 0; x < kMaxAxes; x++)
-        pos[x] = x < a.axes && a.pairs > 0 ? __ldg(a.pos + b * a.p_sb + n * a.p_sn + x * a.p_sa) : 0;
+        pos[x] = x < a.axes && a.pairs > 0 && angles ? __ldg(a.pos + b * a.p_sb + n * a.p_sn + x * a.p_sa) : 0;
     int64_t page = 0, in_page = 0;
     bool write_kv = true;
     if (APPEND) {
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kRotThreads, MODE > 1 ? 2 : 3) rot_kernel(cons
         page = slot >> a.page_shift;
         in_page = slot & ((int64_t(1) << a.page_shift) - 1);
     }
-    for (int i = threadIdx.x; i < a.pairs; i += kRotThreads) {
+    for (int i = angles ? threadIdx.x : a.pairs; i < a.pairs; i += kRotThreads) {
         // Frequency as a fraction of a turn per position, 64-bit fixed point.
         double t = a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
         t -= floor(t);
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kRotThreads, MODE > 1 ? 2 : 3) rot_kernel(cons
     for (int e = 0; e < 8; e++) {
         cs[e] = 1.f;
         sn[e] = 0.f;
-        if (e < 4 ? !turn0 : !turn1) continue;
+        if (!angles || (e < 4 ? !turn0 : !turn1)) continue;
         const int pr = e < 4 ? p0 + e : p1 + e - 4;
         const int ax = s_axis[pr];
         // (an axis index out of range turns by nothing)
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kRotThreads, MODE > 1 ? 2 : 3) rot_kernel(cons
 
 // A write of codes beside q's rotation: a launch each, since q's kernel has three blocks an SM
 // and the other two.  Worth a second launch from 32 blocks of rows on where q has most of the
-// heads (32 and 8, d = 128: 1,024 rows 12.6 us together, 11.2 apart; 8,192 45.4 and 42.8; 512 rows 8.5
+// heads (32 and 8, d = 128: 1,024 rows 12.6 us together, 11.2 apart; 8,192 45.4 and 41.2; 512 rows 8.5
 // and 10.5; 8,192 rows of 32 and 32 heads 85.6 and 86.8).
 template <int DT, int NC>
 cudaError_t launch_codes_and_q(const RotArgs &a, int blocks, cudaStream_t stream)
