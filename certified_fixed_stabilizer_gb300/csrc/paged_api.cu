@@ -231,15 +231,26 @@ SplitQ8 split_q8(const clis_paged_t *p, int64_t max_q, int nsm)
     return s;
 }
 
-// Bytes of one of the two 16-bit copies that the chunk kernel works on, a multiple of 256.
-size_t pages_bytes(const clis_paged_t *p)
-{
-    return (static_cast<size_t>(p->num_pages) * p->Hkv * p->page_size * p->d * 2 + 255) & ~size_t(255);
-}
+// The 16-bit copies that the chunk kernel works on: pages of the same numbers, or, where the
+// tables have fewer places than the cache pages, a page for each place and a table of them.
+struct Copies {
+    int64_t pages;
+    bool listed;
+    size_t of_values, of_scales, table;  // bytes, multiples of 256
+    size_t all() const { return 2 * of_values + of_scales + table; }
+};
 
-size_t scales_bytes(const clis_paged_t *p)
+Copies copies_of(const clis_paged_t *p)
 {
-    return (static_cast<size_t>(p->num_pages) * p->Hkv * p->page_size * 4 + 255) & ~size_t(255);
+    auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+    Copies c;
+    c.listed = p->S * p->width < p->num_pages;
+    c.pages = c.listed ? p->S * p->width : p->num_pages;
+    const size_t rows = static_cast<size_t>(c.pages) * p->Hkv * p->page_size;
+    c.of_values = up(rows * p->d * 2);
+    c.of_scales = up(rows * 4);
+    c.table = c.listed ? up(static_cast<size_t>(c.pages) * 4) : 0;
+    return c;
 }
 
 clis_status_t check_attn_q8(const clis_paged_t *p, const clis_quant_t *z, int64_t max_q)
@@ -621,7 +632,7 @@ clis_status_t clis_attn_paged_q8_workspace_size(const clis_paged_t *desc, const 
     if (!sm_count(&nsm)) return CLIS_ERR_CUDA;
     const SplitQ8 s = split_q8(desc, max_q, nsm);
     *bytes = clis::paged_q8_workspace(static_cast<int>(desc->d), s.rows, nsm) +
-             (s.chunk ? clis::paged_chunk_workspace(attn_args(desc), nsm) + 2 * pages_bytes(desc) + scales_bytes(desc) : 0);
+             (s.chunk ? clis::paged_chunk_workspace(attn_args(desc), nsm) + copies_of(desc).all() : 0);
     return CLIS_OK;
 }
 
@@ -647,7 +658,8 @@ clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_
     clis::PagedArgs a = attn_args(desc);
     const size_t few = clis::paged_q8_workspace(a.d, s.rows, nsm);
     const size_t chunk = s.chunk ? clis::paged_chunk_workspace(a, nsm) : 0;
-    const size_t need = few + chunk + (s.chunk ? 2 * pages_bytes(desc) + scales_bytes(desc) : 0);
+    const Copies copies = copies_of(desc);
+    const size_t need = few + chunk + (s.chunk ? copies.all() : 0);
     if (need > 0 && (!workspace || ws_bytes < need)) return CLIS_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return CLIS_ERR_MISALIGNED;
     const clis::QuantArgs z = quant_args(quant, k_codes, v_codes, k_scale, v_scale);
@@ -665,8 +677,14 @@ clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_
     // The chunk kernel works on 16-bit copies of its sequences' pages.
     clis::PagedArgs b = a;
     uint16_t *kp = reinterpret_cast<uint16_t *>(w + few + chunk);
-    uint16_t *vp = reinterpret_cast<uint16_t *>(w + few + chunk + pages_bytes(desc));
-    float *ks = reinterpret_cast<float *>(w + few + chunk + 2 * pages_bytes(desc));
+    uint16_t *vp = reinterpret_cast<uint16_t *>(w + few + chunk + copies.of_values);
+    float *ks = reinterpret_cast<float *>(w + few + chunk + 2 * copies.of_values);
+    int32_t *table = copies.listed ? reinterpret_cast<int32_t *>(w + need - copies.table) : nullptr;
+    if (table) {
+        b.block_table = table;
+        b.bt_s = desc->width;
+        b.num_pages = copies.pages;
+    }
     b.kc = kp;
     b.vc = vp;
     b.ks = ks;
@@ -675,7 +693,7 @@ clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const clis_quant_
     b.kc_sp = b.vc_sp = desc->Hkv * desc->page_size * a.d;
     const int rows_small = s.rows;
     clis_status_t e = clis::launch_paged_chunk_schedule(b, rows_small, w + few, nsm, cs);
-    if (e == CLIS_OK) e = clis::launch_paged_unpack(a, z, rows_small, kp, ks, vp, nsm, cs);
+    if (e == CLIS_OK) e = clis::launch_paged_unpack(a, z, rows_small, kp, ks, vp, table, nsm, cs);
     if (e == CLIS_OK && s.rows > 0) e = clis::launch_paged_q8(a, z, s.rows, false, true, w, nsm, cs);
     if (e == CLIS_OK) e = clis::launch_paged_chunk(b, rows_small, w + few, nsm, cs);
     return e;

@@ -364,7 +364,7 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
         // eight); looked up two tiles ahead.
         auto scale_page = [&](int kt) -> int {
             const int key = kt * BN + lane * 4;
-            return key < T.kv && kt < K.start + K.n ? __ldg(a.block_table + T.s * a.bt_s + (key >> a.page_shift)) : -1;
+            return key < T.kv && kt < K.start + K.n ? __ldcg(a.block_table + T.s * a.bt_s + (key >> a.page_shift)) : -1;
         };
         int sc_page = -1, sc_next = -1;
         if constexpr (KS) {
@@ -376,7 +376,8 @@ __device__ void producer_role(const ChunkParams &p, Ctl &c, const CUtensorMap *t
         // number can stand there, so none can say that there is nothing to load).
         auto has_rows = [&](int kt) { return lane < npg && kt * BN + lane * p.box_rows < T.kv; };
         auto page_of = [&](int kt) -> int {
-            return has_rows(kt) ? __ldg(a.block_table + T.s * a.bt_s + ((kt * BN + lane * p.box_rows) >> a.page_shift)) : -1;
+            const int32_t *at = a.block_table + T.s * a.bt_s + ((kt * BN + lane * p.box_rows) >> a.page_shift);
+            return has_rows(kt) ? (KS ? __ldcg(at) : __ldg(at)) : -1;  // (KS: the launch before may have written it)
         };
         int pg_k = page_of(K.start), pg_v = -1;
         // Groups of loads as the MMA warp needs them: {K_0}, {V_0, K_1}, ..., {V_{n-1}}.
@@ -852,14 +853,14 @@ __device__ __forceinline__ void add_not_finite(float *o, const ChunkItem &T, int
     const PagedArgs &a = p.a;
 #pragma unroll 1
     for (int key = from; key < see; key++) {
-        const int pg = __ldg(a.block_table + T.s * a.bt_s + (key >> a.page_shift));
+        const int pg = __ldcg(a.block_table + T.s * a.bt_s + (key >> a.page_shift));  // (as V, maybe written by the launch before)
         if (pg < 0 || pg >= a.num_pages) continue;
         const uint32_t *vs = reinterpret_cast<const uint32_t *>(
             a.vc + static_cast<int64_t>(pg) * a.vc_sp + T.h * a.vc_sh +
             static_cast<int64_t>(key & ((1 << a.page_shift) - 1)) * a.vc_sn + col);
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const uint32_t u = __ldg(vs + e);
+            const uint32_t u = __ldcg(vs + e);
             const float lo = elem_lo<DT>(u), hi = elem_hi<DT>(u);
             if (!isfinite(lo)) o[2 * e] += lo;
             if (!isfinite(hi)) o[2 * e + 1] += hi;

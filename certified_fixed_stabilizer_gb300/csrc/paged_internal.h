@@ -102,11 +102,12 @@ struct ReadArgs {
 
 clis_status_t launch_paged_read(const ReadArgs &a, cudaStream_t stream);
 // Every key and value of the sequences that the chunk kernel works on, in 16 bits in
-// pages of the same numbers, [num_pages][Hkv][page size][d] each: K's codes as they are
-// with their scales times a.scale_log2 in k_scale [num_pages][Hkv][page size], V's values.
+// pages [pages][Hkv][page size][d] each: K's codes as they are with their scales times a.scale_log2
+// in k_scale [pages][Hkv][page size], V's values.  The pages have the numbers of the cache, or with
+// `table` [S][width] those of their places in it, which it then lists (-1: out of range).
 // Launched behind launch_paged_chunk_schedule, beside which it may run.
 clis_status_t launch_paged_unpack(const PagedArgs &a, const QuantArgs &z, int rows_small, uint16_t *k_pages, float *k_scale,
-                                  uint16_t *v_pages, int nsm, cudaStream_t stream);
+                                  uint16_t *v_pages, int32_t *table, int nsm, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Programmatic dependent launch.  A kernel launched by launch_pdl may start while

@@ -201,6 +201,7 @@ struct UnpackParams {
     QuantArgs z;
     uint16_t *ko, *vo;
     float *ks;
+    int32_t *table;  // nullptr: the cache's page numbers
     int g, rows_small;
 };
 
@@ -267,7 +268,10 @@ __global__ void __launch_bounds__(kReadThreads) paged_unpack_kernel(const Unpack
             const int key = j * kUnitKeys + i * S::PER + threadIdx.x / S::PPR;
             const int page = key < kv ? __ldg(a.block_table + s * a.bt_s + (key >> a.page_shift)) : -1;
             const bool ok = page >= 0 && page < a.num_pages;  // (the chunk kernel records the others)
-            const int64_t pg = ok ? page : 0, in = key & mask, to = pg * a.Hkv * head + in * D;
+            const int64_t pg = ok ? page : 0, in = key & mask;
+            const int64_t place = p.table ? static_cast<int64_t>(s) * a.width + (key >> a.page_shift) : pg;
+            const int64_t to = place * a.Hkv * head + in * D;
+            if (p.table && in == 0 && key < kv && (threadIdx.x & (S::PPR - 1)) == 0) p.table[place] = ok ? static_cast<int>(place) : -1;
             tok[i] = {pg * a.kc_sp + in * a.kc_sn, pg * a.vc_sp + in * a.vc_sn, pg * z.ks_sp + in * z.ks_sn, pg * z.vs_sp + in * z.vs_sn,
                       to, to, ok, ok};
         }
@@ -317,9 +321,9 @@ clis_status_t launch_paged_read(const ReadArgs &a, cudaStream_t stream)
 }
 
 clis_status_t launch_paged_unpack(const PagedArgs &a, const QuantArgs &z, int rows_small, uint16_t *k_pages, float *k_scale,
-                                  uint16_t *v_pages, int nsm, cudaStream_t stream)
+                                  uint16_t *v_pages, int32_t *table, int nsm, cudaStream_t stream)
 {
-    const UnpackParams p{a, z, k_pages, v_pages, k_scale, a.H / a.Hkv, rows_small};
+    const UnpackParams p{a, z, k_pages, v_pages, k_scale, table, a.H / a.Hkv, rows_small};
     const int grid = 8 * nsm;
     const bool half = a.dtype == CLIS_DT_FP16;
     const cudaError_t e = z.code == CLIS_CODE_INT8 ? (half ? launch_unpack_impl<CLIS_CODE_INT8, 1>(p, grid, stream)

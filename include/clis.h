@@ -682,7 +682,8 @@ CLIS_API clis_status_t clis_paged_read(const clis_paged_t *desc, const clis_quan
  * where the tables can hold no more than 16 MB of codes) are unpacked to 16 bits first (K's
  * codes, exact, its scales applied to the scores; V's values, rounded once to the data type)
  * and run the chunk kernel of clis_attn_fwd_paged; the workspace then holds a 16-bit copy
- * of the whole cache that is passed (one layer's).
+ * of as many pages as the tables have places (S * width) or the cache has (one layer's), whichever
+ * is less.
  * A NaN code of E4M3 stands for NaN.  Masked places, padding, reruns and errors as for
  * clis_attn_fwd_paged. */
 CLIS_API clis_status_t clis_attn_paged_q8_workspace_size(const clis_paged_t *desc, const clis_quant_t *quant, int64_t max_q,

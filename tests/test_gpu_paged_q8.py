@@ -407,6 +407,42 @@ def test_the_longest_sequence(n, code):
     assert e <= 6e-4 + 2.0 ** -22 * 32 + 2.0 ** 26 / 152 / 128 * 2.0 ** -24 / math.log(2.0), e
 
 
+@pytest.mark.parametrize("d,page", [(128, 16), (64, 8), (128, 64), (64, 256)])
+@pytest.mark.parametrize("dtype,code", [(BF, "int8"), (HF, "e4m3")])
+def test_chunks_in_a_cache_of_many_pages(d, page, dtype, code):
+    """Where the tables have fewer places than the cache pages, the chunk kernel's copies are by place: the same bits, a
+    fraction of the workspace, and pages out of range are recorded as ever."""
+    b = make_q8([300, 20, 0, 64], [600, 1, 0, 40], 16, 4, d, page, dtype, code, seed=page)
+    assert which(b) == {"chunk"}
+    check_q8(attend(b), None, b)
+    wide = dict(b)
+    for name in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        t = b[name]
+        more = torch.full((5000, *t.shape[1:]), 1, dtype=torch.int8, device="cuda").view(t.dtype) if t.dtype != torch.float32 else \
+            torch.full((5000, *t.shape[1:]), math.nan, device="cuda")
+        raw_t, raw_more = (raw(t), raw(more)) if t.dtype != torch.float32 else (t, more)
+        wide[name] = torch.cat([raw_t, raw_more]).view(t.dtype)
+    bad = b["block_table"].clone()
+    bad[0, 1] = 1 << 29
+    for table in (b["block_table"], bad):
+        o = [attend(dict(x, block_table=table), return_lse=True) for x in (b, wide)]
+        assert torch.equal(o[0][0], o[1][0]) and torch.equal(o[0][1], o[1][1])
+    torch.cuda.synchronize()
+    assert clis.clis_get_device_error() == clis.PAGED_INDEX_BIT
+    clis.clis_clear_device_error()
+    # Both calls take the same output and the same workspace for parts of items (some 50 MB); the copies of the second have
+    # S * width pages instead of the first's, 2 * 2 d + 4 bytes a row, and a table, rounded to 256 bytes (torch: 2 MB a tensor).
+    used = []
+    for x in (b, wide):
+        torch.cuda.empty_cache()
+        torch.cuda.reset_peak_memory_stats()
+        held = torch.cuda.memory_allocated()
+        attend(x)
+        used.append(torch.cuda.max_memory_allocated() - held)
+    places, pages = b["block_table"].numel(), b["k_cache"].shape[0]
+    assert used[1] - used[0] <= (places - pages) * 4 * page * (4 * d + 4) + 4 * places + (5 << 20)
+
+
 def test_caches_beyond_32_bits():
     """Pages past 2^31 bytes and past 2^31 rows' worth of offsets: written, read back and attended."""
     page, Hk, d, pages = 64, 8, 128, 36000  # 2.36 GB of codes each
