@@ -27,7 +27,7 @@
 //    the transposition of V's pairs on the way.  E4M3 has its own instruction.
 //  * The contraction over d takes the elements in the order in which a thread's
 //    16-byte load of codes holds them; q's fragments are laid out the same way.
-//  * Loads: one warp of a team fetches its stages by TMA, page by page (a unit is 8 KB of
+//  * Loads: a warp fetches its stages by TMA, page by page (a unit is 8 KB of
 //    codes), the scales by 4-byte copies that arrive on the same barrier.  With 16-byte
 //    copies by all lanes the addresses alone were a sixth of all instructions.
 //  * q is scaled by a power of two per row so that its largest magnitude is between

@@ -21,7 +21,7 @@ struct DecodeParams {
     PagedArgs a;
     int g, rows_max, least;
     int limit;   // query rows that a sequence may have (rows_max of them in an item)
-    int workers;     // warps (paged_q8.cu: teams of warps) of the grid
+    int workers; // warps of the grid
     int strict;  // no chunk kernel follows: a sequence of more rows is an error
     float *part_o;   // [2 * workers][rows_max][D]: place 2 c + 1 if worker c starts the item, 2 c if it goes on with it
     float2 *part_ml; // [2 * workers][rows_max]
