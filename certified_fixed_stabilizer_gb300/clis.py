@@ -936,7 +936,8 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q: int |
     Caches of codes (int8 or float8_e4m3fn) come with ``k_scale`` and ``v_scale``; where max_q
     allows for long chunks (more than 64 query rows per key/value head, unless the tables
     are small) the call takes a workspace of a 16-bit copy of as many pages as the block tables have
-    places, or the caches pages if these are fewer: pass the rows and columns that a step needs.
+    places, or the caches pages if these are fewer: pass the rows and columns that a step needs
+    (few columns also save short single tokens a launch).
     No autograd graph is recorded."""
     r = _native.attention_paged(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q or max(1, q.shape[0]),
                                 scale_log2_for(q.shape[-1], softmax_scale), causal, out, None, return_lse, None, k_scale,

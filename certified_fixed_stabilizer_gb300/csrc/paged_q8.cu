@@ -18,6 +18,8 @@
 //    scheduler).  Larger tiles spill registers: 16, 32 and 64 rows of the 64 requests below 231, 460
 //    and 920 us with tiles of 16; 413 and 783 with 32 of int8, but 526 and 979 of E4M3.  Teams of
 //    four warps that convert a unit together into fp16 tiles in shared memory took 607 and 798.
+//    Where the tables hold little, a block takes an item, each warp a quarter of its units, and
+//    joins it in shared memory: no second launch.
 //  * The products are taken transposed, S^T = KC Q^T and O^T += VC^T W^T: codes are the
 //    16-row operand, query rows the 8-column one.  A single token's g query heads fill
 //    4 or 8 of 8 places instead of 16, which halves the products, the weights and the
@@ -448,7 +450,7 @@ struct Rows {
     // lie at keys [nan_from, nan_to) took part as numbers; rows that see them become NaN.
     template <int DT>
     __device__ __forceinline__ void write(const DecodeParams &p, const QuantArgs &z, const SeqLen &q, int s, int head, int row0, int64_t slot,
-                                          int nan_from, int nan_to, int lane)
+                                          float *part_o, float2 *part_ml, int nan_from, int nan_to, int lane)
     {
         const PagedArgs &a = p.a;
         const int R = q.n * p.g, r4 = lane >> 2, c2 = 2 * (lane & 3);
@@ -490,15 +492,90 @@ struct Rows {
                             sum == 0.f ? 0u : pack2<DT>(o[i][nt][h] * back * inv, o[i][nt][2 + h] * back * inv);
                     if (r4 == 0 && a.lse2) a.lse2[static_cast<int64_t>(q.q0 + tok) * a.H + hd] = sum == 0.f ? -INFINITY : mm + log2f(sum);
                 } else {
-                    float *dst = p.part_o + (slot * p.rows_max + row - row0) * D + 2 * r4;
+                    float *dst = part_o + (slot * p.rows_max + row - row0) * D + 2 * r4;
 #pragma unroll
                     for (int i = 0; i < D / 16; i++)
                         *reinterpret_cast<float2 *>(dst + i * 16) = make_float2(o[i][nt][h] * back, o[i][nt][2 + h] * back);
-                    if (r4 == 0) p.part_ml[slot * p.rows_max + row - row0] = make_float2(mm, sum);
+                    if (r4 == 0) part_ml[slot * p.rows_max + row - row0] = make_float2(mm, sum);
                 }
             }
     }
 };
+
+// Item blockIdx.x of the batch, if it has as many (all threads take part; ends with a
+// barrier): item s_rel[0] of sequence s_seq[0].
+template <int TR>
+__device__ __forceinline__ bool block_item(const DecodeParams &p, uint64_t *s_sum, int *s_seq, uint64_t *s_rel, unsigned int &bad)
+{
+    const PagedArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (a.S + kDecodeThreads - 1) / kDecodeThreads;
+    const int sb = min(a.S, tid * per), se = min(a.S, sb + per);
+    auto items = [&](const SeqLen &q) { return is_decode(q, p.g, p.limit) ? a.Hkv * ceil_div(q.n * p.g, TR) : 0; };
+    int n = 0;
+    for (int s = sb; s < se; s++) {
+        const SeqLen q = seq_len(a, s);
+        if (q.bad || (p.strict && q.n > 0 && !is_decode(q, p.g, p.limit))) bad |= CLIS_PAGED_LENGTH_BIT;
+        n += items(q);
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - n, all = 0;
+    for (int i = 0; i < kDecodeWarps; i++) {
+        if (i < warp) before += static_cast<int>(s_sum[i]);
+        all += static_cast<int>(s_sum[i]);
+    }
+    int rel = static_cast<int>(blockIdx.x) - before;
+    if (rel >= 0 && rel < n)
+        for (int s = sb; s < se; s++) {
+            const int k = items(seq_len(a, s));
+            if (rel < k) {
+                s_seq[0] = s;
+                s_rel[0] = rel;
+                break;
+            }
+            rel -= k;
+        }
+    __syncthreads();
+    return static_cast<int>(blockIdx.x) < all;
+}
+
+// The output rows of an item from its warps' parts, in the order of the keys.
+template <int D, int DT, int TR>
+__device__ __forceinline__ void join_quarters(const DecodeParams &p, const SeqLen &q, int head, int row0, const float *sO, const float2 *s_ml)
+{
+    constexpr int V = D / 32;
+    const PagedArgs &a = p.a;
+    const int lane = threadIdx.x & 31, rows = min(TR, q.n * p.g - row0);
+    for (int r = threadIdx.x >> 5; r < rows; r += kDecodeWarps) {
+        float M = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+        for (int i = 0; i < kDecodeWarps; i++) M = fmaxf(M, s_ml[i * TR + r].x);
+#pragma unroll
+        for (int e = 0; e < V; e++) o[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kDecodeWarps; i++) {
+            const float2 ml = s_ml[i * TR + r];
+            if (ml.y == 0.f) continue;  // a part none of whose keys the row sees
+            const float w = ex2_approx(ml.x - M);
+            l = fmaf(w, ml.y, l);
+#pragma unroll
+            for (int e = 0; e < V; e++) o[e] = fmaf(w, sO[(i * TR + r) * D + lane * V + e], o[e]);
+        }
+        const int tok = (row0 + r) / p.g, hd = head * p.g + (row0 + r - tok * p.g);
+        const float inv = 1.f / l;
+        uint16_t *dst = a.o + static_cast<int64_t>(q.q0 + tok) * a.o_st + hd * a.o_sh + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; e += 2)  // (zeros for a row that sees no key)
+            *reinterpret_cast<uint32_t *>(dst + e) = l == 0.f ? 0u : pack2<DT>(o[e] * inv, o[e + 1] * inv);
+        if (lane == 0 && a.lse2) a.lse2[static_cast<int64_t>(q.q0 + tok) * a.H + hd] = l == 0.f ? -INFINITY : M + log2f(l);
+    }
+}
 
 template <int D, int DT, int CODE, int NT>
 __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
@@ -513,6 +590,7 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
     __shared__ int s_seq[kDecodeWarps];
     __shared__ __align__(8) uint64_t s_full[kDecodeWarps * C::NST];
     __shared__ int s_abort;
+    __shared__ float2 s_ml[kDecodeWarps * C::TR];  // (one)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned int bad = 0;
     pdl_launch();
@@ -521,23 +599,42 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
         s_abort = 0;
         fence_mbar_init();
     }
-    const Runs runs = block_runs<TK, kDecodeWarps, C::TR>(p, s_sum, s_seq, s_rel, bad);
     const int c = warp * gridDim.x + blockIdx.x;  // this worker
-    if (lane == 0) p.meta[c] = make_int4(0, 0, 0, 0);
+    Runs runs{};
+    uint64_t u1 = 0;
+    bool mine = true;
+    Pos<TK, C::TR> cur;
+    if (p.one) {
+        mine = block_item<C::TR>(p, s_sum, s_seq, s_rel, bad);
+    } else {
+        runs = block_runs<TK, kDecodeWarps, C::TR>(p, s_sum, s_seq, s_rel, bad);
+        if (lane == 0) p.meta[c] = make_int4(0, 0, 0, 0);
+        mine = c < runs.nb;
+    }
     if (bad && blockIdx.x == 0) atomicOr(&g_q8_error_word, bad);
     bad = 0;
-    if (c >= runs.nb) {  // nothing for this warp (U = 0 included)
+    if (!mine) {  // nothing for this warp (U = 0 included)
         pdl_wait();
         return;
     }
-    const uint64_t u1 = decode_cut(runs.U, runs.nb, c + 1);
-    Pos<TK, C::TR> cur;
-    cur.set(a, s_seq[warp], p.g);
-    const int item = static_cast<int>(div64(s_rel[warp], cur.units));
-    cur.h = item / cur.tiles;
-    cur.tile = item - cur.h * cur.tiles;
-    cur.j = static_cast<int>(s_rel[warp] - static_cast<uint64_t>(item) * cur.units);
-    cur.left = static_cast<uint32_t>(u1 - decode_cut(runs.U, runs.nb, c));
+    if (p.one) {  // a quarter of the item's units
+        cur.set(a, s_seq[0], p.g);
+        const int item = static_cast<int>(s_rel[0]);
+        cur.h = item / cur.tiles;
+        cur.tile = item - cur.h * cur.tiles;
+        cur.j = cur.units * warp / kDecodeWarps;
+        cur.left = cur.units * (warp + 1) / kDecodeWarps - cur.j;
+    } else {
+        u1 = decode_cut(runs.U, runs.nb, c + 1);
+        cur.set(a, s_seq[warp], p.g);
+        const int item = static_cast<int>(div64(s_rel[warp], cur.units));
+        cur.h = item / cur.tiles;
+        cur.tile = item - cur.h * cur.tiles;
+        cur.j = static_cast<int>(s_rel[warp] - static_cast<uint64_t>(item) * cur.units);
+        cur.left = static_cast<uint32_t>(u1 - decode_cut(runs.U, runs.nb, c));
+    }
+    const SeqLen q0 = cur.q;  // (one)
+    const int head0 = cur.h, row00 = cur.tile * C::TR;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     Loader<D, C::NST, C::TR> load;
     load.ld = cur;
@@ -554,7 +651,8 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
     const int r4 = lane >> 2, t4 = lane & 3;
     uint32_t done = 0, phase = 0;  // units read
     int stage = 0;
-    bool fine = true;
+    bool fine = true, some = false;
+    float *const sO = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)));  // (one: the stages, all read by then)
     Rows<D, NT> w;
     while (fine && cur.left > 0) {
         // ---- one item, units j0 .. j1 - 1 of it
@@ -650,8 +748,15 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
         if (!fine) break;
         const bool any_dirty = CODE != CLIS_CODE_INT8 && __any_sync(~0u, dirty);
         const bool whole = j0 == 0 && j1 == cur.units;
-        w.template write<DT>(p, z, cur.q, cur.s, cur.h, row0, whole ? -1 : 2 * static_cast<int64_t>(c) + (j0 == 0 ? 1 : 0),
-                             any_dirty ? max(lim0 / TK * TK, j0 * TK) : -1, j1 * TK, lane);
+        const int nan_from = any_dirty ? max(lim0 / TK * TK, j0 * TK) : -1;
+        if (p.one) {
+            __syncthreads();
+            w.template write<DT>(p, z, cur.q, cur.s, cur.h, row0, warp, sO, s_ml, nan_from, j1 * TK, lane);
+            some = true;
+            break;
+        }
+        w.template write<DT>(p, z, cur.q, cur.s, cur.h, row0, whole ? -1 : 2 * static_cast<int64_t>(c) + (j0 == 0 ? 1 : 0), p.part_o,
+                             p.part_ml, nan_from, j1 * TK, lane);
         if (!whole && j0 == 0 && lane == 0)
             p.meta[c] = make_int4(item_parts(runs, c, u1 - cur.left + cur.units - 1), cur.q.q0, cur.q.n | row0 << 16, cur.h);
         cur.left -= j1 - j0;
@@ -660,6 +765,14 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
     }
     if (!fine) load.drain(done);
     if (bad) atomicOr(&g_q8_error_word, bad);
+    if (p.one) {
+        if (!some) {
+            __syncthreads();
+            if (lane < C::TR) s_ml[warp * C::TR + lane] = make_float2(-INFINITY, 0.f);
+        }
+        __syncthreads();
+        join_quarters<D, DT, C::TR>(p, q0, head0, row00, sO, s_ml);
+    }
     pdl_wait();
 }
 
@@ -678,6 +791,26 @@ bool encode_codes(CUtensorMap *map, const uint8_t *base, const PagedArgs &a, int
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Column tiles of 8 query rows that a warp takes.  Three only at d = 64 (at d = 128 they spill
+// registers: 20 rows 168 us instead of 141 with two tiles of 16), where a tile of 24 rows costs 1.25 times
+// one of 16: 20 rows over 64 requests 88 us, 40 166; with two they are 2 and 3 tiles, with four
+// (registers spilled) 132 and 245.  25 to 32 rows fill two tiles of 16.
+int column_tiles(int d, int rows) { return rows <= 8 ? 1 : d == 64 && rows > 16 && (rows <= 24 || rows > 32) ? 3 : 2; }
+
+// Blocks of the form without a second launch, or 0: where the GPU holds a block for each item that
+// the batch can have, and the tables no more than 16 units of each, or 32 where runs would not be
+// much shorter (64 items).  (d = 128, 4 query heads a key, 8 key/value heads, runs and join against a block
+// per item: one request of 300 keys 12.4 and 10.4 us, of 60 12.5 and 7.4, 40 of 480 22.8 and 15.1, 8 of
+// 900 18.4 and 16.6, one of 900 16.3 and 16.2, 8 of 1,900 22.1 and 24.9; d = 64: one of 900 14.9 and
+// 11.1, of 1,900, 30 units, 13.7 and 16.6.)
+int64_t one_item_blocks(const PagedArgs &a, int rows, int nsm)
+{
+    const int nt = column_tiles(a.d, rows), tk = 4096 / a.d;
+    const int64_t items = static_cast<int64_t>(a.S) * a.Hkv * ((rows + 8 * nt - 1) / (8 * nt));
+    const int64_t units = ((static_cast<int64_t>(a.width) << a.page_shift) + tk - 1) / tk;
+    return items <= (nt == 1 ? QCfg<128, 1>::BLOCKS : QCfg<128, 2>::BLOCKS) * nsm && units <= (items >= 64 ? 32 : 16) ? items : 0;
+}
+
 template <int D, int DT, int CODE, int NT>
 clis_status_t launch_impl(int rows, const PagedArgs &a, const QuantArgs &z, bool strict, bool after_schedule, void *workspace,
                           int nsm, cudaStream_t stream)
@@ -685,9 +818,11 @@ clis_status_t launch_impl(int rows, const PagedArgs &a, const QuantArgs &z, bool
     using C = QCfg<D, NT>;
     const auto kernel = paged_q8_kernel<D, DT, CODE, NT>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return CLIS_ERR_CUDA;
-    const int grid = C::BLOCKS * nsm;
+    const int64_t items = one_item_blocks(a, rows, nsm);
+    const int grid = items > 0 ? static_cast<int>(items) : C::BLOCKS * nsm;
     DecodeParams p;
     p.a = a;
+    p.one = items > 0;
     p.g = a.H / a.Hkv;
     p.least = 2;
     p.strict = strict;
@@ -705,14 +840,9 @@ clis_status_t launch_impl(int rows, const PagedArgs &a, const QuantArgs &z, bool
         kernel<<<grid, kDecodeThreads, C::SMEM, stream>>>(mk, mv, p, z, box_shift);
         if (cudaGetLastError() != cudaSuccess) return CLIS_ERR_CUDA;
     }
+    if (p.one) return CLIS_OK;
     return launch_join<D, DT>(p, stream) == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
-
-// Column tiles of 8 query rows that a warp takes.  Three only at d = 64 (at d = 128 they spill
-// registers: 20 rows 168 us instead of 141 with two tiles of 16), where a tile of 24 rows costs 1.25 times
-// one of 16: 20 rows over 64 requests 88 us, 40 166; with two they are 2 and 3 tiles, with four
-// (registers spilled) 132 and 245.  25 to 32 rows fill two tiles of 16.
-int column_tiles(int d, int rows) { return rows <= 8 ? 1 : d == 64 && rows > 16 && (rows <= 24 || rows > 32) ? 3 : 2; }
 
 template <int D, int DT, int CODE, typename... A>
 clis_status_t launch_rows(int rows, const A &...args)

@@ -23,6 +23,7 @@ struct DecodeParams {
     int limit;   // query rows that a sequence may have (rows_max of them in an item)
     int workers; // warps of the grid
     int strict;  // no chunk kernel follows: a sequence of more rows is an error
+    int one;     // (paged_q8.cu) a block per item, no parts
     float *part_o;   // [2 * workers][rows_max][D]: place 2 c + 1 if worker c starts the item, 2 c if it goes on with it
     float2 *part_ml; // [2 * workers][rows_max]
     int4 *meta;      // [workers] {parts, first row of q, new tokens and 2^16 times the item's first row, head} of the item

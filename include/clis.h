@@ -675,7 +675,8 @@ CLIS_API clis_status_t clis_paged_read(const clis_paged_t *desc, const clis_quan
 /* clis_attn_fwd_paged over a cache of codes: x_ij = scale_log2 * q_i . k_j and o_i with the
  * values code * scale.  Where max_q allows for no more than 64 query rows of a sequence
  * (max_q * H / Hkv; single and drafted tokens), or the tables can hold little enough to go
- * with them, one kernel does it all, bound by the codes' bytes: codes are exact in its
+ * with them, one kernel (and a second one that joins what it split, unless the tables are
+ * small) does it all, bound by the codes' bytes: codes are exact in its
  * products, the weights times V's scale are rounded to fp16 (off by up to 2^-11 of each, at
  * least 2^-32 of the row's largest), q is exact where it is within 2^-30 of its row's largest
  * value.  Else that kernel serves single tokens, and the other sequences (all of them

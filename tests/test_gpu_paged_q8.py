@@ -75,6 +75,26 @@ def test_attention(shape, dtype, code):
     assert (o[sum(new):] == 7.0).all()  # rows of no sequence
 
 
+@pytest.mark.parametrize("shape", [i for i, s in enumerate(SHAPES) if len(s) == 6 and max(s[1]) * s[2] // s[3] <= 64])
+@pytest.mark.parametrize("dtype,code", [(BF, "int8"), (HF, "e4m3")])
+def test_short_sequences_in_long_tables(shape, dtype, code):
+    """Few rows: with short tables a block takes an item, with long ones runs of units are joined by a second launch."""
+    ctx, new, H, Hkv, d, page = SHAPES[shape]
+    b = make_q8(ctx, new, H, Hkv, d, page, dtype, code, seed=100 + shape, columns=4096 // page)
+    o, lse = attend(b, return_lse=True)
+    check_q8(o, lse, b, what=f"{SHAPES[shape]}")
+    short = dict(b, block_table=b["block_table"][:, :-4096 // page].contiguous())
+    o, lse = attend(short, return_lse=True)
+    check_q8(o, lse, short, what=f"{SHAPES[shape]}, short tables")
+
+
+@pytest.mark.parametrize("d,ctx", [(128, 127), (128, 1000), (64, 1000), (64, 2040)])
+@pytest.mark.parametrize("new", [1, 2, 5])
+def test_sixty_four_items_of_up_to_32_units(d, ctx, new):
+    b = make_q8([ctx - 7 * i for i in range(16)], [new] * 16, 16, 4, d, 8, BF, "int8", seed=ctx + new)
+    check_q8(attend(b), None, b)
+
+
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
 @pytest.mark.parametrize("new,H", [([1] * 9, 8), ([4, 1, 3, 2, 4, 1, 1, 4, 2], 16)])
 def test_many_lengths_and_joins(code, new, H):
