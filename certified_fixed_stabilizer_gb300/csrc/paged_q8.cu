@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
             // number, and the rows that see it get a NaN at the end.
             if (CODE != CLIS_CODE_INT8 && edge) {
 #pragma unroll 1
-                for (int i = lane; i < C::HALF / 16; i += 32) {
+                for (int i = lane; i < C::HALF / 16 && key0 + i / (D / 16) < kv; i += 32) {  // (not what lies behind the last key)
                     const uint4 u = lds128(sV + i * 16);
                     dirty |= has_nan(u.x) || has_nan(u.y) || has_nan(u.z) || has_nan(u.w);
                 }
