@@ -13,12 +13,14 @@
 // values, so the second kernel (a block per request) picks them, reads them again (a
 // few KB, still in L2) and picks the K best of what they hold:
 //
-//  * Mostly no pick has to be exact but the last.  The K-th largest of 64 groups' leaders is
-//    no more than the K-th best value; chunks and then logits below it are left out, which leaves
-//    little more than K candidates, and each counts those that are better (13 us for 8 requests of
-//    4 beams and K = 8 with the other way).  Where more are left (many ties, few chunks), warps
-//    sort candidates 32 at a time and merge their lists in a tree.  Either way the order is
-//    exactly that of (value, index).  (K rounds of a maximum over the block took 38 us for 96
+//  * Mostly no pick has to be exact but the last.  The K-th largest of 64 (K above 16: 256) groups'
+//    leaders is no more than the K-th best value; chunks and then logits below it are left out,
+//    which leaves little more than K candidates, and each counts those that are better.  Where many
+//    are left (few chunks), a second such bound comes from groups of the logits themselves; where that
+//    does not do either (ties), warps sort candidates 32 at a time and merge their lists in a tree.
+//    Either way the order is exactly that of (value, index).  (Without the second bound 37 requests
+//    of 7 beams and 2,397 tokens took 35 us, now 19; with 64 groups for all K 8 requests of 4 beams
+//    and K = 64 took 87, now 38.  K rounds of a maximum over the block took 38 us for 96
 //    requests of 8 beams and K = 16.)
 //  * A value is a pair of fp32 numbers (their sum, to 48 bits): exact sums of score, logit and
 //    the logarithm, which comes from 32-bit terms and is off by about 1e-7.  fp64 is a
@@ -45,7 +47,8 @@ constexpr int max_seg(int dtype) { return dtype == 2 ? 1 : 2; }
 constexpr int scan_blocks(bool aligned) { return aligned ? 4 : 3; }
 constexpr int kMaxListed = 8192; // rows
 constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
-constexpr int kGroups = kMaxPicks;  // of leaders, for the bound
+constexpr int kGroups = 256;        // for the bounds, at most
+constexpr int kFew = 128;           // candidates that are ranked at once
 constexpr int kPool = kPickThreads; // candidates that are ranked by counting
 constexpr int kAhead = 4;             // leaders of a thread that are loaded at once
 constexpr float kLog2e = 1.4426950408889634f;
@@ -443,6 +446,25 @@ struct Outputs {
     }
 };
 
+// The K-th largest of N groups (1: there are fewer); the block's first N threads take part.
+template <int N>
+__device__ __forceinline__ void kth_group(const uint32_t *group, int K, uint32_t *bound)
+{
+    const int tid = threadIdx.x;
+    if (tid >= N) return;
+    const uint32_t mine = group[tid];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < N; j += 4) {
+        const uint4 g = *reinterpret_cast<const uint4 *>(group + j);
+        rank += g.x > mine || (g.x == mine && j < tid);
+        rank += g.y > mine || (g.y == mine && j + 1 < tid);
+        rank += g.z > mine || (g.z == mine && j + 2 < tid);
+        rank += g.w > mine || (g.w == mine && j + 3 < tid);
+    }
+    if (rank == K - 1) *bound = max(mine, 1u);
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParams p)
 {
@@ -452,13 +474,14 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
     __shared__ Pair s_lse[kMaxBeams];
     __shared__ bool s_ok[kMaxBeams];
     __shared__ Best s_pick[kMaxPicks];  // at: beam * chunks + chunk
-    __shared__ uint32_t s_group[kGroups];
+    __shared__ __align__(16) uint32_t s_group[kGroups];
     __shared__ uint32_t s_bound;
     __shared__ int s_chunks, s_cands, s_chunk[kPool];
     Best *pool = &s_lists[0][0];  // [kPool]
     static_assert(kPool <= kPickWarps * 64, "the pool lies in the lists' place");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int req = blockIdx.x;
+    const int groups = a.K <= 16 ? 64 : kGroups;  // of leaders (more take longer to rank)
     if (tid < kGroups) s_group[tid] = 0;
     if (tid == 0) s_chunks = s_cands = 0;
     pdl_wait();
@@ -519,27 +542,34 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
         at = static_cast<uint32_t>(static_cast<int64_t>(w) * a.V + first);
     };
 
+    // The K best of n candidates, each by the number of those that are better.
+    auto rank_pool = [&](int n) {
+        const Best mine = tid < n ? pool[tid] : no_one();
+        if (tid < n) {
+            int rank = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; j++) rank += better(pool[j], mine);
+            if (rank < a.K) out.put(rank, mine);
+        }
+        if (tid >= n && tid < a.K) out.put(tid, no_one());
+    };
+
     // ---- the bound, the chunks that reach it, the logits that do
     uint32_t first[kAhead];  // the first leaders' values
 #pragma unroll
     for (int j = 0; j < kAhead; j++) {
         const int i = tid + j * kPickThreads;
         first[j] = i < leads ? static_cast<uint32_t>(leader(i, ahead[j]).v >> 32) : 0u;
-        if (first[j]) atomicMax(&s_group[i % kGroups], first[j]);
+        if (first[j]) atomicMax(&s_group[i & (groups - 1)], first[j]);
     }
 #pragma unroll 1
     for (int i = tid + kAhead * kPickThreads; i < leads; i += kPickThreads)
-        atomicMax(&s_group[i % kGroups], static_cast<uint32_t>(leader(i, lead[i]).v >> 32));
+        atomicMax(&s_group[i & (groups - 1)], static_cast<uint32_t>(leader(i, lead[i]).v >> 32));
     __syncthreads();
-    if (tid < kGroups) {
-        const uint32_t mine = s_group[tid];
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < kGroups; j++) rank += s_group[j] > mine || (s_group[j] == mine && j < tid);
-        if (rank == a.K - 1) s_bound = max(mine, 1u);
-    }
+    if (groups == 64) kth_group<64>(s_group, a.K, &s_bound);
+    else kth_group<kGroups>(s_group, a.K, &s_bound);
     __syncthreads();
-    const uint32_t bound = s_bound;
+    uint32_t bound = s_bound;
     auto found_one = [&](int i) {
         const int k = atomicAdd(&s_chunks, 1);
         if (k < kPool) s_chunk[k] = i;
@@ -578,19 +608,52 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamParam
         }
         __syncthreads();
         const int n = s_cands;
-        if (n <= kPool) {
-            const Best mine = tid < n ? pool[tid] : no_one();
-            if (tid < n) {
-                int rank = 0;
-#pragma unroll 4
-                for (int j = 0; j < n; j++) rank += better(pool[j], mine);
-                if (rank < a.K) out.put(rank, mine);
-            }
-            if (tid >= n && tid < a.K) out.put(tid, no_one());
+        if (n <= kFew) {
+            rank_pool(n);
             return;
         }
     }
-    __syncthreads();  // (the pool's place is written again)
+    __syncthreads();  // (s_cands and the pool's place are written again)
+
+    // ---- many logits reach it (leaders are few in a small vocabulary): the K-th largest of 128 groups
+    // of those logits is the next bound
+    if (found <= kPool) {
+        auto logits = [&](auto use) {
+#pragma unroll 1
+            for (int t = warp; t < 4 * found; t += kPickWarps) {
+                float x[E];
+                int w;
+                uint32_t at;
+                quarter(s_chunk[t >> 2], t & 3, x, w, at);
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    if (x[e] != -INFINITY) use(best_of(value(s_score[w], x[e], s_lse[w]), at + e * 32));
+            }
+        };
+        uint32_t top = 0;
+        logits([&](const Best &b) { top = max(top, static_cast<uint32_t>(b.v >> 32)); });
+        top = max(top, __shfl_xor_sync(~0u, top, 1));
+        top = max(top, __shfl_xor_sync(~0u, top, 2));
+        static_assert(kPickThreads / 4 <= kGroups, "a group for four threads");
+        if ((tid & 3) == 0) s_group[tid >> 2] = top;
+        if (tid == 0) s_cands = 0;
+        __syncthreads();
+        kth_group<kPickThreads / 4>(s_group, a.K, &s_bound);
+        __syncthreads();
+        bound = max(bound, s_bound);
+        logits([&](const Best &b) {
+            if ((b.v >> 32) < bound || *static_cast<volatile int *>(&s_cands) > kPool) return;
+            const int k = atomicAdd(&s_cands, 1);
+            if (k < kPool) pool[k] = b;
+        });
+        __syncthreads();
+        const int n = s_cands;
+        if (n <= kPool) {
+            rank_pool(n);
+            return;
+        }
+        __syncthreads();  // (the pool's place is written again)
+    }
 
     // ---- the other way: the K best leaders, exactly
     Top top;

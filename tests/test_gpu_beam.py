@@ -51,7 +51,8 @@ def check(logits, scores, K, got=None):
 
 @pytest.mark.parametrize("R,W,V,K", [
     (1, 1, 1, 1), (1, 1, 1, 3), (2, 3, 2, 9), (3, 4, 511, 8), (2, 4, 512, 8), (2, 4, 513, 8), (1, 5, 1031, 10),
-    (8, 4, 32003, 8), (2, 16, 50000, 32), (1, 64, 3000, 64), (3, 1, 131072, 64), (65, 8, 8192, 16), (1, 2, 300007, 4)])
+    (8, 4, 32003, 8), (2, 16, 50000, 32), (1, 64, 3000, 64), (3, 1, 131072, 64), (65, 8, 8192, 16), (1, 2, 300007, 4),
+    (11, 15, 35, 14), (37, 7, 2397, 12), (8, 4, 50257, 64), (3, 14, 8, 17), (9, 40, 700, 40)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_selection(R, W, V, K, dtype):
     g = torch.Generator(device="cuda").manual_seed(R * 1000 + V)
