@@ -95,6 +95,16 @@ def test_sixty_four_items_of_up_to_32_units(d, ctx, new):
     check_q8(attend(b), None, b)
 
 
+@pytest.mark.parametrize("dtype,code", [(BF, "int8"), (HF, "e4m3")])
+def test_blocks_of_single_tokens_beside_a_chunk(dtype, code):
+    """Tables of fewer than 32 units but more than 16 MB of codes: a block per item between unpacking and the chunk kernel."""
+    b = make_q8([900 - 13 * i for i in range(47)] + [600], [1] * 47 + [300], 32, 8, 128, 16, dtype, code, seed=48)
+    assert which(b) == {"few", "chunk"}
+    o, lse = attend(b, return_lse=True)
+    check_q8(o, lse, b)
+    assert torch.equal(attend(b), o)
+
+
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
 @pytest.mark.parametrize("new,H", [([1] * 9, 8), ([4, 1, 3, 2, 4, 1, 1, 4, 2], 16)])
 def test_many_lengths_and_joins(code, new, H):
