@@ -113,7 +113,10 @@ __global__ void __launch_bounds__(kTableThreads) reorder_table_kernel(const Reor
     }
     if (tid < W) {
         s_again[tid] = again && done;
-        if (!done) s_src[tid] = tid;
+        if (!done) {  // the request stays as it was: its rows whole, whatever their lengths say
+            s_src[tid] = tid;
+            s_have[tid] = a.width;
+        }
     }
     __syncthreads();
     if (tid < W) {

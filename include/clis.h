@@ -745,9 +745,10 @@ CLIS_API clis_status_t clis_beam_select(const clis_beam_t *desc, const void *log
  *                head on in the order of requests and beams, pages that go back
  *                follow the tail in the order of requests, columns and beams
  *   lens_out     device int32 [groups * beams]: tokens of the new rows; not lens or parent itself
- *   done         device int32 [groups]: 0 for a request that stays as it was: the ring has too
- *                few pages for it and those before (CLIS_PAGED_POOL_BIT), a parent is out
- *                of range (CLIS_PAGED_INDEX_BIT) or a length (CLIS_PAGED_LENGTH_BIT)
+ *   done         device int32 [groups]: 0 for a request that stays as it was (whole rows of its
+ *                table, and its lens): the ring has too few pages for it and those before
+ *                (CLIS_PAGED_POOL_BIT), a parent is out of range (CLIS_PAGED_INDEX_BIT) or a
+ *                length (CLIS_PAGED_LENGTH_BIT)
  *   tensors, n   host array of the caches (values, codes, scales of K and V; up to 8) whose
  *                rows are copied
  *   workspace    device scratch of clis_paged_reorder_workspace_size() bytes, 256-byte

@@ -324,6 +324,28 @@ def test_bad_inputs_leave_a_request_as_it_was():
     clis.clis_clear_device_error()
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("what", ["negative length", "long", "parent", "pool"])
+def test_a_refused_request_keeps_its_rows(what, in_place):
+    """Whole rows, whatever is wrong with the request; its neighbours go on."""
+    b = beams(3, 4, 8, 6, 5, free=0 if what == "pool" else 20)
+    b["lens"][:] = torch.tensor([20, 20, 17, 9] * 3)
+    b["table"][4:8, 3:] = torch.arange(12, dtype=torch.int32, device="cuda").view(4, 3)  # (behind the pages: kept as well)
+    par = torch.tensor([[0, 1, 2, 3], [0, 0, 3, 1], [3, 2, 1, 0]], dtype=torch.int32, device="cuda")
+    if what == "parent":
+        par[1, 2] = 4
+    elif what != "pool":
+        b["lens"][6] = -3 if what == "negative length" else 49
+    table, lens = b["table"].clone(), b["lens"].clone()
+    r = clis.paged_reorder(b["lens"], par, b["table"], b["ring"], b["state"], page_size=8, out=b["table"] if in_place else None)
+    assert clis.clis_get_device_error() == {"parent": clis.PAGED_INDEX_BIT, "pool": clis.PAGED_POOL_BIT}.get(what, clis.PAGED_LENGTH_BIT)
+    assert r.done.tolist() == [1, 0, 1]
+    assert torch.equal(r.block_table[4:8], table[4:8]) and torch.equal(r.lens[4:8], lens[4:8])
+    assert torch.equal(r.lens[8:], lens[8:].flip(0)) and torch.equal(r.block_table[8:, :2], table[8:, :2].flip(0))
+    assert torch.equal(r.ring_state, b["state"])
+    clis.clis_clear_device_error()
+
+
 def test_strided_caches():
     """[pages, page_size, H, d] order, one layer of several, rows of 4-byte multiples only."""
     page, W = 8, 3
