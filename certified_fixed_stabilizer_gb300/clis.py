@@ -164,6 +164,8 @@ def load_library():
     lib.clis_rope.restype = i32
     lib.clis_paged_plan.argtypes = [pp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp]
     lib.clis_paged_plan.restype = i32
+    lib.clis_paged_plan_beams.argtypes = [pp, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+    lib.clis_paged_plan_beams.restype = i32
     lib.clis_paged_append.argtypes = [pp, rp, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.clis_paged_append.restype = i32
     lib.clis_attn_paged_workspace_size.argtypes = [pp, i64, ctypes.POINTER(sz)]
@@ -879,16 +881,18 @@ class PagedPlan(NamedTuple):
 
 
 def clis_paged_plan(ctx_len, new_len, block_table, ring, ring_state, page_size: int, num_tokens: int,
-                    num_pages: int | None = None, stream=None) -> PagedPlan:
+                    num_pages: int | None = None, stream=None, beams: int = 1) -> PagedPlan:
     """Block tables, slots and positions of a step from the lengths of its
     sequences, on the GPU: ctx_len, new_len int32 [S] (cached and new tokens; new
     < 0: the sequence is finished and gives its pages back), block_table int32
     [S, width] (completed in place), ring int32 [ring size] (free pages; pages
     given back are written into it), ring_state int64 [2] (its head and tail,
     not changed).  num_tokens: rows of the packed batch, at least the sum of the
-    new tokens.  num_pages: pages of the cache (default: the ring's size)."""
+    new tokens.  num_pages: pages of the cache (default: the ring's size).  beams: rows of a
+    request that share pages (:func:`paged_reorder`); a finished one then gives back only
+    the pages that no other row of its request names."""
     return PagedPlan(*_native.paged_plan(ctx_len, new_len, block_table, ring, ring_state, page_size, num_tokens, num_pages,
-                                         _raw(stream)))
+                                         beams, _raw(stream)))
 
 
 paged_plan = clis_paged_plan
@@ -1030,11 +1034,12 @@ class PagedCache:
     With ``dtype`` int8 or float8_e4m3fn the keys and values are held as codes with a scale
     per token and head (``k_scale``, ``v_scale`` [layers, pages, H_kv, page_size]); q, k and v stay
     bfloat16 or float16.  :meth:`read` gives cached tokens back, :meth:`reorder` moves the
-    states of a beam search.
+    states of a beam search.  ``beams``: rows of a request (default 1, :meth:`reorder` raises it);
+    needed only where a graph with :meth:`begin` is captured before the first :meth:`reorder`.
     """
 
     def __init__(self, layers: int, num_pages: int, num_kv_heads: int, d: int, max_seqs: int, max_len: int,
-                 page_size: int = 64, dtype=torch.bfloat16, device="cuda"):
+                 page_size: int = 64, dtype=torch.bfloat16, device="cuda", beams: int = 1):
         dev = torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
@@ -1048,20 +1053,21 @@ class PagedCache:
         self.ring = torch.arange(num_pages, dtype=torch.int32, device=dev)
         self.ring_state = torch.tensor([0, num_pages], dtype=torch.int64, device=dev)
         self.lens = torch.zeros(max_seqs, dtype=torch.int32, device=dev)
+        self.beams = beams
 
     def _scales(self, layer: int) -> dict:
         return {} if self.k_scale is None else {"k_scale": self.k_scale[layer], "v_scale": self.v_scale[layer]}
 
     def begin(self, new_len, num_tokens: int) -> PagedPlan:
         """Plan of a step that adds new_len[s] tokens to sequence s (0: not part of
-        the step, negative: finished, its pages are free again), ``num_tokens``
-        rows in all (rows behind the last token are padding).  A sequence that too few
+        the step, negative: finished, its pages are free again; those that other beams of its
+        request share with it when the last of them ends), ``num_tokens`` rows in all (rows behind the last token are padding).  A sequence that too few
         pages are left for stays as it was (PAGED_POOL_BIT in the device error word; its
         rows of the step mean nothing): bring its tokens again when others have finished.
         So does one that would outgrow ``max_len``, rounded up to pages (PAGED_LENGTH_BIT);
         the others go on as if it had not taken part."""
         plan = clis_paged_plan(self.lens, new_len, self.block_table, self.ring, self.ring_state, self.page_size,
-                               num_tokens)
+                               num_tokens, beams=self.beams)
         self.lens.copy_(plan.kv_len)
         self.ring_state.copy_(plan.ring_state)
         return plan
@@ -1089,11 +1095,12 @@ class PagedCache:
         """The beams' states after a selection (parent int32 [requests, beams], requests * beams =
         max_seqs: row r * beams + w goes on from row r * beams + parent[r, w], or ends where that is
         negative); see :func:`paged_reorder`.  Returns ``done`` int32 [requests].  Rows of beams are ended
-        here, not by a negative new_len of :meth:`begin`, while they share pages; a prompt is read by
-        one beam (new_len 0 for the others), and parent 0 for all then starts the search."""
+        here or by a negative new_len of :meth:`begin`; a prompt is read by one beam (new_len 0 for
+        the others), and parent 0 for all then starts the search."""
         scales = [] if self.k_scale is None else [self.k_scale, self.v_scale]
         r = clis_paged_reorder(self.lens, parent, self.block_table, self.ring, self.ring_state, [self.k, self.v], scales,
                                out=self.block_table)
+        self.beams = max(self.beams, parent.shape[1])
         self.lens.copy_(r.lens)
         self.ring_state.copy_(r.ring_state)
         return r.done

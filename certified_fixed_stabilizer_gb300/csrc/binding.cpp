@@ -209,7 +209,7 @@ struct RopeNode : torch::autograd::Function<RopeNode> {
 
 std::vector<Tensor> plan(const Tensor &ctx_len, const Tensor &new_len, const Tensor &table, const Tensor &ring,
                          const Tensor &ring_state, int64_t page_size, int64_t T, std::optional<int64_t> num_pages,
-                         std::optional<uintptr_t> raw)
+                         int64_t beams, std::optional<uintptr_t> raw)
 {
     TORCH_CHECK_VALUE(ctx_len.is_cuda() && ctx_len.dim() == 1, "ctx_len must be an int32 device tensor [S]");
     const at::Device dev = ctx_len.device();
@@ -223,6 +223,7 @@ std::vector<Tensor> plan(const Tensor &ctx_len, const Tensor &new_len, const Ten
                           table.stride(1) == 1,
                       "block_table must be an int32 tensor [S, width] with contiguous rows on the same device");
     TORCH_CHECK_VALUE(T >= 0, "num_tokens must not be negative");
+    TORCH_CHECK_VALUE(beams > 0 && S % beams == 0, "the sequences must be requests of `beams` rows each");
     Place at_(ctx_len, raw);
     Tensor cu = empty({S + 1}, at::kInt, dev), kv = empty({S}, at::kInt, dev), slots = empty({T}, at::kLong, dev),
            pos = empty({T}, at::kInt, dev), state = empty({2}, at::kLong, dev);
@@ -235,8 +236,9 @@ std::vector<Tensor> plan(const Tensor &ctx_len, const Tensor &new_len, const Ten
     d.bt_ss = S > 1 ? table.stride(0) : table.size(1);
     auto i32 = [](const Tensor &t) { return static_cast<int32_t *>(t.data_ptr()); };
     auto i64 = [](const Tensor &t) { return static_cast<int64_t *>(t.data_ptr()); };
-    ok("clis_paged_plan", clis_paged_plan(&d, i32(ctx_len), i32(new_len), i32(table), i32(ring), ring.size(0),
-                                          i64(ring_state), i64(state), i32(cu), i32(kv), i64(slots), i32(pos), at_.stream));
+    ok(beams == 1 ? "clis_paged_plan" : "clis_paged_plan_beams",
+       clis_paged_plan_beams(&d, beams, i32(ctx_len), i32(new_len), i32(table), i32(ring), ring.size(0), i64(ring_state),
+                             i64(state), i32(cu), i32(kv), i64(slots), i32(pos), at_.stream));
     return {at_.result(cu), at_.result(kv), at_.result(slots), at_.result(pos), at_.result(state)};
 }
 
@@ -668,9 +670,9 @@ PyObject *py_rope_autograd(PyObject *, PyObject *const *a, Py_ssize_t n)
 
 PyObject *py_plan(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    return call(n, 9, [&] {
+    return call(n, 10, [&] {
         return wrap(plan(tensor(a[0], "ctx_len"), tensor(a[1], "new_len"), tensor(a[2], "block_table"), tensor(a[3], "ring"),
-                         tensor(a[4], "ring_state"), integer(a[5]), integer(a[6]), maybe_int(a[7]), stream_of(a[8])));
+                         tensor(a[4], "ring_state"), integer(a[5]), integer(a[6]), maybe_int(a[7]), integer(a[8]), stream_of(a[9])));
     });
 }
 

@@ -456,9 +456,20 @@ clis_status_t clis_paged_plan(const clis_paged_t *desc, const int32_t *ctx_len, 
                               int64_t *state_out, int32_t *cu_q, int32_t *kv_len, int64_t *slots, int32_t *positions,
                               clis_stream_t stream)
 {
+    return clis_paged_plan_beams(desc, 1, ctx_len, new_len, block_table, ring, ring_size, state_in, state_out, cu_q, kv_len,
+                                 slots, positions, stream);
+}
+
+clis_status_t clis_paged_plan_beams(const clis_paged_t *desc, int64_t beams, const int32_t *ctx_len, const int32_t *new_len,
+                                    int32_t *block_table, int32_t *ring, int64_t ring_size, const int64_t *state_in,
+                                    int64_t *state_out, int32_t *cu_q, int32_t *kv_len, int64_t *slots, int32_t *positions,
+                                    clis_stream_t stream)
+{
     if (!desc) return CLIS_ERR_INVALID_ARG;
     const clis_status_t st = check_table(desc);
     if (st != CLIS_OK) return st;
+    if (beams < 1 || desc->S % beams) return CLIS_ERR_INVALID_ARG;
+    if (beams > clis::kMaxBeams) return CLIS_ERR_UNSUPPORTED;
     if (desc->S > 1 && desc->bt_ss < desc->width) return CLIS_ERR_INVALID_ARG;  // rows are written
     if (ring_size < 1) return CLIS_ERR_INVALID_ARG;
     if (ring_size > kMaxN) return CLIS_ERR_UNSUPPORTED;
@@ -487,6 +498,7 @@ clis_status_t clis_paged_plan(const clis_paged_t *desc, const int32_t *ctx_len, 
     a.width = static_cast<int>(desc->width);
     a.page_shift = page_shift(desc->page_size);
     a.num_pages = desc->num_pages;
+    a.beams = static_cast<int>(beams);
     return clis::launch_paged_plan(a, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -59,6 +59,7 @@ struct PlanArgs {
     int32_t *pos;
     int S, T, width, page_shift;
     int64_t num_pages;
+    int beams;  // that many neighbouring rows may name the same pages, in their first columns
 };
 
 clis_status_t launch_paged_plan(const PlanArgs &a, cudaStream_t stream);

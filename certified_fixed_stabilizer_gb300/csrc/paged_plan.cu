@@ -62,10 +62,33 @@ __device__ __forceinline__ Seq read_seq(const PlanArgs &a, int s)
     return q;
 }
 
-__device__ __forceinline__ Sums sums_of(const Seq &q)
+// Pages of finished sequence s that stay, because another row of its request (`beams` rows)
+// names them: one that goes on, or an earlier finished one, which gives them back.  Beams that
+// share a page share all before it, so rows agree up to a column, found by halving (the
+// columns read are pages held, which this step does not write).
+__device__ __forceinline__ int shared_pages(const PlanArgs &a, int s, const Seq &q)
+{
+    const int s0 = s - s % a.beams;
+    int most = 0;
+    for (int v = s0; v < s0 + a.beams; v++) {
+        if (v == s) continue;
+        const Seq o = read_seq(a, v);
+        if (o.gone && v > s) continue;
+        int lo = 0, hi = min(q.have, o.have);  // the first lo columns agree, those from hi on do not
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.block_table[s * a.bt_s + mid] == a.block_table[v * a.bt_s + mid]) lo = mid + 1;
+            else hi = mid;
+        }
+        most = max(most, lo);
+    }
+    return most;
+}
+
+__device__ __forceinline__ Sums sums_of(const PlanArgs &a, int s, const Seq &q)
 {
     return {min(static_cast<uint32_t>(q.n), kCap), static_cast<uint32_t>(q.need - q.have),
-            q.gone ? static_cast<uint32_t>(q.have) : 0u};
+            q.gone ? static_cast<uint32_t>(q.have - (a.beams > 1 ? shared_pages(a, s, q) : 0)) : 0u};
 }
 
 // Last s with first[s] <= i, for i < first[S] (first is non-decreasing).
@@ -95,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
     for (int s = s0; s < s1; s++) {
         const Seq q = read_seq(a, s);
         if (q.full) bad |= CLIS_PAGED_LENGTH_BIT;
-        mine = add(mine, sums_of(q));
+        mine = add(mine, sums_of(a, s, q));
     }
     Sums incl = mine;
 #pragma unroll
@@ -117,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
         s_tok[s] = run.tok;
         s_taken[s] = run.taken;
         s_back[s] = run.back;
-        run = add(run, sums_of(read_seq(a, s)));
+        run = add(run, sums_of(a, s, read_seq(a, s)));
     }
     // (the totals: from the thread with the last sequence, or zeros without any)
     if ((s0 < a.S && s1 == a.S) || (a.S == 0 && tid == 0)) {
@@ -184,7 +207,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
             bad |= CLIS_PAGED_POOL_BIT;
             continue;
         }
-        const int page = a.block_table[s * a.bt_s + (i - s_back[s])];
+        int col = static_cast<int>(i - s_back[s]);
+        if (a.beams > 1) col += read_seq(a, s).have - static_cast<int>(s_back[s + 1] - s_back[s]);  // (behind those that stay)
+        const int page = a.block_table[s * a.bt_s + col];
         if (page < 0 || page >= a.num_pages) bad |= CLIS_PAGED_INDEX_BIT;
         a.ring[(tm + i) % Fu] = page;
     }

@@ -569,6 +569,17 @@ CLIS_API clis_status_t clis_paged_plan(const clis_paged_t *desc, const int32_t *
                                        int64_t *state_out, int32_t *cu_q, int32_t *kv_len, int64_t *slots,
                                        int32_t *positions, clis_stream_t stream);
 
+/* The same where rows share pages, as clis_paged_reorder leaves them: rows r * beams .. r * beams
+ * + beams - 1 of the table are the beams of request r.  A finished row gives back the pages that
+ * no row of its request names any more that goes on or is finished before it; clis_paged_plan
+ * (beams = 1) would give a shared page back once for each row.
+ *   beams        1 .. 64 (CLIS_ERR_UNSUPPORTED), S a multiple of it (CLIS_ERR_INVALID_ARG) */
+CLIS_API clis_status_t clis_paged_plan_beams(const clis_paged_t *desc, int64_t beams, const int32_t *ctx_len,
+                                             const int32_t *new_len, int32_t *block_table, int32_t *ring,
+                                             int64_t ring_size, const int64_t *state_in, int64_t *state_out,
+                                             int32_t *cu_q, int32_t *kv_len, int64_t *slots, int32_t *positions,
+                                             clis_stream_t stream);
+
 /* New keys and values into the cache, rotated on the way, and q rotated beside
  * them, in one launch.  T up to 2^27.
  *   rope       desc for the rotation: N = T, B = 1, Hq = H (0: no q), Hk = Hkv, d,
@@ -731,8 +742,9 @@ CLIS_API clis_status_t clis_beam_select(const clis_beam_t *desc, const void *log
  * page is gone on from more than once, all but the first (lowest w) get a page of
  * the ring with a copy of its rows.  Pages that no row of the request names any more go
  * back to the ring.  So the last page of a row is never shared unless it is full, and
- * clis_paged_plan and clis_paged_append go on as ever (a beam's row must not be given back
- * by a negative new_len there while it shares pages: end it here).
+ * clis_paged_plan and clis_paged_append go on as ever; a beam's row that shares pages is ended
+ * here, or by a negative new_len of clis_paged_plan_beams (not of clis_paged_plan, which does not
+ * know that other rows name its pages).
  *   groups, beams  requests and W (up to 64); groups * beams up to 16384
  *   width, page_size, num_pages  as in clis_paged_t
  *   bt_ss, bo_ss   strides of rows of block_table and new_table

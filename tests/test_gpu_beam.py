@@ -442,6 +442,73 @@ def test_a_search(dtype):
     assert sorted(cache.ring[(head_ + torch.arange(200, device="cuda")) % 200].tolist()) == list(range(200))
 
 
+def check_pages(cache):
+    """Every page is free once or held by a row, and not both; rows share pages only in the same column."""
+    page, (head, tail) = cache.page_size, cache.ring_state.tolist()
+    F = cache.ring.numel()
+    free = [cache.ring[i % F].item() for i in range(head, tail)]
+    held = {(p, c) for n, row in zip(cache.lens.tolist(), cache.block_table.tolist()) for c, p in enumerate(row[:-(-n // page)])}
+    assert sorted(free + [p for p, _ in held]) == list(range(F))
+
+
+def test_beams_ended_by_the_plan():
+    """Beams that share pages end by a negative length of the next step, some of them or all: a page is free once its last
+    row has ended, and free once."""
+    R, W = 2, 4
+    cache = clis.PagedCache(layers=1, num_pages=50, num_kv_heads=1, d=64, max_seqs=R * W, max_len=64, page_size=8)
+
+    def begin(*new):
+        cache.begin(torch.tensor(new, dtype=torch.int32, device="cuda"), 40)
+        check_pages(cache)
+
+    def reorder(*parent):
+        assert cache.reorder(torch.tensor(parent, dtype=torch.int32, device="cuda").view(R, W)).tolist() == [1] * R
+        check_pages(cache)
+
+    begin(21, 0, 0, 0, 16, 0, 0, 0)
+    reorder(*[0] * 8)
+    for _ in range(4):
+        begin(*[1] * 8)
+    reorder(0, 0, 2, 2, 1, 1, 1, 1)
+    for _ in range(4):
+        begin(*[1] * 8)
+    begin(1, -1, 1, 1, -1, -1, 1, -1)                     # one of two that share, three of four, beside others that go on
+    begin(-1, 0, -1, -1, 0, 0, 1, 0)                      # the rest of a request, one of them the last to name a page
+    reorder(-1, -1, -1, -1, 2, 2, -1, 2)
+    begin(5, 0, 0, 0, -2, -1, 0, 1)
+    begin(-1, -1, -1, -1, -1, -1, -1, -1)
+    assert cache.lens.tolist() == [0] * 8 and (cache.ring_state[1] - cache.ring_state[0]).item() == 50
+
+
+@pytest.mark.parametrize("R,W,page,width", [(1, 2, 8, 3), (7, 4, 16, 9), (40, 8, 8, 30), (3, 64, 8, 6), (300, 3, 8, 5)])
+def test_plan_of_beams_against_a_host_loop(R, W, page, width):
+    """Pages given back, in the order of rows and columns: those that no row of the request names any more that goes on
+    or is finished before; rows that go on take theirs as ever."""
+    for seed in range(3):
+        rng = random.Random(seed)
+        b = beams(R, W, page, width, seed + 100 * R, free=R * W + 1)
+        cap, lens, table = width * page, b["lens"].tolist(), b["table"].tolist()
+        new = [rng.choice([-1, -1, 0, min(rng.randint(0, page), cap - n)]) for n in lens]
+        if seed == 2:
+            new = [-1] * (R * W)
+        have, (head, tail), F = [-(-n // page) for n in lens], b["state"].tolist(), b["pages"]
+        ring, h = b["ring"].tolist(), head
+        for s, n in enumerate(new):
+            for c in range(have[s], -(-(lens[s] + n) // page) if n > 0 else 0):
+                table[s][c] = ring[h % F]
+                h += 1
+        for s, n in enumerate(new):
+            r0 = s - s % W
+            for c in range(have[s] if n < 0 else 0):
+                if not any(v != s and (new[v] >= 0 or v < s) and c < have[v] and table[v][c] == table[s][c] for v in range(r0, r0 + W)):
+                    ring[tail % F] = table[s][c]
+                    tail += 1
+        p = clis.paged_plan(b["lens"], torch.tensor(new, dtype=torch.int32, device="cuda"), b["table"], b["ring"], b["state"], page,
+                            sum(max(n, 0) for n in new), beams=W)
+        assert p.ring_state.tolist() == [h, tail] and b["ring"].tolist() == ring and b["table"].tolist() == table
+        assert p.kv_len.tolist() == [n + m if m >= 0 else 0 for n, m in zip(lens, new)]
+
+
 def test_a_step_of_the_search_in_a_graph():
     """Plan, write, attention, selection and reordering captured once and replayed, against the same steps made one by one."""
     R, W, H, Hk, d, V = 2, 3, 4, 2, 64, 1000

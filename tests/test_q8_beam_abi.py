@@ -105,6 +105,15 @@ def test_attention_refusals():
     assert size(paged_desc(), quant(), 4, None) == INVALID and size(paged_desc(), quant(), 0, ctypes.byref(n)) == INVALID
 
 
+def test_plan_of_beams_refusals():
+    def plan(desc, beams):
+        return clis.load_library().clis_paged_plan_beams(desc, beams, *[FAKE + 64 * i for i in range(4)], 50, *[FAKE + 64 * i for i in range(4, 10)], None)
+
+    for beams, S, st in ((0, 3, INVALID), (-1, 3, INVALID), (2, 3, INVALID), (4, 6, INVALID), (65, 130, UNSUPPORTED)):
+        assert plan(paged_desc(S=S), beams) == st, beams
+    assert plan(None, 1) == INVALID
+
+
 def beam(desc, ws=FAKE, ws_bytes=1 << 50, **p):
     a = dict(logits=FAKE, scores=FAKE, out=FAKE, parent=FAKE, token=FAKE)
     a.update(p)
