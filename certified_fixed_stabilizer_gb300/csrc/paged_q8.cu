@@ -33,8 +33,8 @@
 //    codes), the scales by 4-byte copies that arrive on the same barrier.  With 16-byte
 //    copies by all lanes the addresses alone were a sixth of all instructions.
 //  * q is scaled by a power of two per row so that its largest magnitude is between
-//    2^14 and 2^15 and goes into fp16: exact for fp16 and bf16 values down to 2^-30 of
-//    the row's largest.
+//    2^15 and 2^16 (at most 65,504 in fp16 and 65,280 in bf16) and goes into fp16: exact for
+//    fp16 values, which are never scaled down, and for bf16 values down to 2^-32 of the row's largest.
 //  * The weights of V carry vs_j, whose range has nothing to do with the softmax's: with
 //    p_ij = 2^(x_ij - m_i) for the row sum, w_ij = p_ij vs_j 2^(e_i), where e_i follows the
 //    largest p vs of the row: it stands at 2^7 when it is set, and e_i is lowered (and O with
@@ -270,7 +270,7 @@ struct Rows {
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
             // (a row of zeros or with something non-finite is taken as it is)
-            const int ex = top == 0 || top >= 0x7F800000u ? 0 : min(14 - (static_cast<int>(top >> 23) - 127), 126);
+            const int ex = top == 0 || top >= 0x7F800000u ? 0 : min(15 - (static_cast<int>(top >> 23) - 127), 126);
             const float by = exp2_int(ex), s1 = a.scale_log2 * exp2_int(-ex);
 #pragma unroll
             for (int w = 0; w < D / 16; w++)

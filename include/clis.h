@@ -689,8 +689,8 @@ CLIS_API clis_status_t clis_paged_read(const clis_paged_t *desc, const clis_quan
  * with them, one kernel (and a second one that joins what it split, unless the tables are
  * small) does it all, bound by the codes' bytes: codes are exact in its
  * products, the weights times V's scale are rounded to fp16 (off by up to 2^-11 of each, at
- * least 2^-32 of the row's largest), q is exact where it is within 2^-30 of its row's largest
- * value.  Else that kernel serves single tokens, and the other sequences (all of them
+ * least 2^-32 of the row's largest), q is exact in fp16, and in bf16 where it is within 2^-32 of
+ * its row's largest value.  Else that kernel serves single tokens, and the other sequences (all of them
  * where the tables can hold no more than 16 MB of codes) are unpacked to 16 bits first (K's
  * codes, exact, its scales applied to the scores; V's values, rounded once to the data type)
  * and run the chunk kernel of clis_attn_fwd_paged; the workspace then holds a 16-bit copy

@@ -136,6 +136,24 @@ def test_scales_of_any_size(spread, new):
     check_q8(attend(b), None, b)
 
 
+@pytest.mark.parametrize("H", [2, 12])
+def test_fp16_queries_are_exact(H):
+    """Rows of fp16 with its largest and its smallest numbers: what the small ones add to a score is not rounded."""
+    b = make_q8([0], [1], H, 1, 64, 8, HF, "int8", seed=8)
+    (kc, ks), _ = b["keys"][0]
+    kc.fill_(101)
+    kc[..., 0] = 0
+    ks.fill_(2.0 ** 12)
+    b["k_cache"][b["block_table"][0, 0], :, 0] = kc[0]
+    b["k_scale"][b["block_table"][0, 0], :, 0] = 2.0 ** 12
+    b["q"][:] = (2 * torch.arange(64, device="cuda") + 1) * 2.0 ** -24   # (odd multiples of the smallest number)
+    b["q"][..., 0] = 60000.0
+    _, lse = attend(b, softmax_scale=1.0, return_lse=True)
+    want = (b["q"][0].double() * kc[0, 0].double()).sum(-1) * 2.0 ** 12 / math.log(2)
+    # a product is exact, their sum rounded in 32 bits: 64 additions; then two factors, one of them rounded itself
+    assert ((lse[0].double() - want).abs() <= 67 * 2.0 ** -24 * want).all()
+
+
 def test_chunk_with_scales_of_zero_and_of_any_size():
     """K's scales of 0, 2^-110, 2^-60 and 2^20 among a chunk's: scores of no and of great size."""
     b = make_q8([300, 11], [70, 90], 4, 2, 64, 8, BF, "e4m3", seed=15, columns=50000)
