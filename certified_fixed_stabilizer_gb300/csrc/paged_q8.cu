@@ -35,6 +35,9 @@
 //  * q is scaled by a power of two per row so that its largest magnitude is between
 //    2^15 and 2^16 (at most 65,504 in fp16 and 65,280 in bf16) and goes into fp16: exact for
 //    fp16 values, which are never scaled down, and for bf16 values down to 2^-32 of the row's largest.
+//    Scores of such rows are up to 2^32, and K's scales in bf16 up to 2^121: where rows were scaled up, a
+//    power of two common to a warp's rows is taken off the scales as they are read (two or four
+//    multiplications a lane and unit) and goes into the rows' factors, so that nothing overflows but a score.
 //  * The weights of V carry vs_j, whose range has nothing to do with the softmax's: with
 //    p_ij = 2^(x_ij - m_i) for the row sum, w_ij = p_ij vs_j 2^(e_i), where e_i follows the
 //    largest p vs of the row: it stands at 2^7 when it is set, and e_i is lowered (and O with
@@ -68,7 +71,8 @@ struct QCfg {
     static constexpr int STAGE = 2 * HALF;
     static constexpr int SCALE = 2 * TK;            // floats of a stage: K's, V's
     static constexpr int TR = 8 * NT;               // query rows of an item
-    static constexpr int PER_WARP = NST * (STAGE + SCALE * 4);
+    static constexpr int SCALES = NST * SCALE * 4 + 16;  // bytes of a warp, and what K's are multiplied by
+    static constexpr int PER_WARP = NST * STAGE + SCALES;
     static constexpr int SMEM = kDecodeWarps * PER_WARP + 1024;
 };
 
@@ -233,18 +237,19 @@ struct Loader {
 template <int D, int NT>
 struct Rows {
     uint32_t qf[NT][D / 16][2];
-    float2 cs[NT];   // scale_log2 over the power of two that q's row was multiplied by
+    float2 cs[NT];   // scale_log2 over the powers of two that q's row and K's scales were multiplied by
     float2 m[NT], l[NT], low[NT];  // low: what the last addition to l gained by rounding
     float2 e[NT], f[NT];           // the weights of V: exponent, and 2^exponent
     float o[D / 16][NT][4];        // d = 16 i + 2 (lane / 4) of two rows, then d + 1 of them
 
     // Word w of thread t holds elements 16 t + 4 w .. (w < 4) or 64 + 16 t + 4 (w - 4) .. of d,
-    // as the loads of codes do.
+    // as the loads of codes do.  s_down: shared address of what K's scales are to be multiplied by.
     template <int DT>
-    __device__ __forceinline__ void load(const DecodeParams &p, const SeqLen &q, int head, int row0, int lane)
+    __device__ __forceinline__ void load(const DecodeParams &p, const SeqLen &q, int head, int row0, int lane, uint32_t s_down)
     {
         const PagedArgs &a = p.a;
         const int R = q.n * p.g, r4 = lane >> 2, t4 = lane & 3;
+        int exps[NT], least = 1000, most = -1000;  // of the rows' powers of two
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
             const int row = row0 + nt * 8 + r4;
@@ -270,19 +275,37 @@ struct Rows {
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
             // (a row of zeros or with something non-finite is taken as it is)
-            const int ex = top == 0 || top >= 0x7F800000u ? 0 : min(15 - (static_cast<int>(top >> 23) - 127), 126);
-            const float by = exp2_int(ex), s1 = a.scale_log2 * exp2_int(-ex);
+            const bool plain = top == 0 || top >= 0x7F800000u;
+            const int ex = plain ? 0 : min(15 - (static_cast<int>(top >> 23) - 127), 126);
+            const float by = exp2_int(ex);
+            exps[nt] = plain ? -1000 : ex;
+            if (!plain) {
+                least = min(least, ex);
+                most = max(most, ex);
+            }
 #pragma unroll
             for (int w = 0; w < D / 16; w++)
 #pragma unroll
                 for (int h = 0; h < 2; h++)
                     qf[nt][w][h] = pack2<1>(elem_lo<DT>(qf[nt][w][h]) * by, elem_hi<DT>(qf[nt][w][h]) * by);
-            cs[nt] = make_float2(__shfl_sync(~0u, s1, t4 * 8), __shfl_sync(~0u, s1, t4 * 8 + 4));
             m[nt] = e[nt] = make_float2(-INFINITY, -INFINITY);
             l[nt] = low[nt] = f[nt] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < D / 16; i++) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
         }
+        // Off K's scales: what the smallest row was scaled up by, but no more than leaves those of
+        // the largest row's scores above 2^-28.
+        least = __reduce_min_sync(~0u, least);
+        most = __reduce_max_sync(~0u, most);
+        const int down = max(0, min(most, least + 90));
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            const float s1 = exps[nt] == -1000 ? a.scale_log2 : a.scale_log2 * exp2_int(down - exps[nt]);
+            cs[nt] = make_float2(__shfl_sync(~0u, s1, t4 * 8), __shfl_sync(~0u, s1, t4 * 8 + 4));
+        }
+        __syncwarp();
+        if (lane == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_down), "f"(exp2_int(-down)) : "memory");
+        __syncwarp();
     }
 
     // Keys that row 8 nt + 2 (lane % 4) + h sees.
@@ -294,12 +317,12 @@ struct Rows {
 
     // Products of a unit's codes, s[km][nt][0], [1]: key 16 km + lane / 4 and two rows, [2], [3]:
     // 8 keys on, into the weights of V's codes, wf: two keys' of row lane / 4.
-    // sS: the unit's scales.
+    // sS: the unit's scales; down: what K's are multiplied by.
     // EDGE: some row does not see some key.  (A constant: as a condition at each score it
     // was a branch there.)
     template <bool EDGE, int KM>
-    __device__ __forceinline__ void weights(const DecodeParams &p, const SeqLen &q, int row0, float (&s)[KM][NT][4], uint32_t sS, int key0,
-                                            int lane, uint32_t (&wf)[KM][NT][2])
+    __device__ __forceinline__ void weights(const DecodeParams &p, const SeqLen &q, int row0, float (&s)[KM][NT][4], uint32_t sS, float down,
+                                            int key0, int lane, uint32_t (&wf)[KM][NT][2])
     {
         constexpr int TK = KM * 16;
         const int r4 = lane >> 2;
@@ -325,7 +348,7 @@ struct Rows {
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const int kr = km * 16 + h * 8 + r4;
-                const float ks = lds32(sS + kr * 4);
+                const float ks = lds32(sS + kr * 4) * down;
                 vs[km][h] = lds32(sS + (TK + kr) * 4);
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
@@ -639,7 +662,8 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
     Loader<D, C::NST, C::TR> load;
     load.ld = cur;
     load.ring = base + warp * C::NST * C::STAGE;
-    load.scales = base + kDecodeWarps * C::NST * C::STAGE + warp * C::NST * C::SCALE * 4;
+    load.scales = base + kDecodeWarps * C::NST * C::STAGE + warp * C::SCALES;
+    const uint32_t s_down = load.scales + C::SCALES - 16;
     load.full = smem_u32(&s_full[warp * C::NST]);
     load.pol = policy_evict_first();
     load.loads = load.stage = 0;
@@ -660,7 +684,7 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
         const int j1 = static_cast<int>(min(static_cast<uint32_t>(cur.units), j0 + cur.left));
         const int kv = cur.q.kv, row0 = cur.tile * C::TR;
         const int lim0 = visible_keys(cur.q.n, kv, row0 / p.g, a.causal);  // keys that every row sees
-        w.template load<DT>(p, cur.q, cur.h, row0, lane);
+        w.template load<DT>(p, cur.q, cur.h, row0, lane, s_down);
         bool dirty = false;
 #pragma unroll 1
         for (int j = j0; j < j1; j++) {
@@ -708,8 +732,9 @@ __global__ void __launch_bounds__(kDecodeThreads, QCfg<D, NT>::BLOCKS)
                 }
             const bool edge = key0 + TK > lim0;  // some row does not see some key
             uint32_t wf[KM][NT][2];
-            if (edge) w.template weights<true, KM>(p, cur.q, row0, s, sS, key0, lane, wf);
-            else w.template weights<false, KM>(p, cur.q, row0, s, sS, key0, lane, wf);
+            const float down = lds32(s_down);
+            if (edge) w.template weights<true, KM>(p, cur.q, row0, s, sS, down, key0, lane, wf);
+            else w.template weights<false, KM>(p, cur.q, row0, s, sS, down, key0, lane, wf);
             // O^T += VC^T W^T: a transposed load gives 32 keys of 16 columns, in each word the
             // codes of two neighbouring columns and two neighbouring keys.
             auto pv = [&](bool clean) {

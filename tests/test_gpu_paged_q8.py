@@ -136,6 +136,42 @@ def test_scales_of_any_size(spread, new):
     check_q8(attend(b), None, b)
 
 
+def scaled(b, q=1.0, k=1.0):
+    """The batch with its rows of q times `q` (a number, or one per row and head) and K's scales times `k`."""
+    b["q"] = (b["q"].float() * q).to(b["q"].dtype)
+    b["k_scale"] = b["k_scale"] * k
+    b["keys"] = [[(kc, ks * k), v] for (kc, ks), v in b["keys"]]
+    return b
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("power", [-112, -60, 60, 112])
+@pytest.mark.parametrize("new,H,d,columns", [(1, 4, 128, 0), (5, 16, 128, 0), (6, 8, 64, 0), (90, 4, 128, 0), (90, 4, 128, 20000)])
+def test_key_scales_of_any_size(new, H, d, columns, power, code):
+    """Keys far larger or smaller than ordinary ones and queries the other way round: the scores are the ordinary ones."""
+    b = make_q8([900, 40], [new, 1], H, 2, d, 16, BF, code, seed=3, columns=columns)
+    check_q8(*attend(scaled(b, 2.0 ** -power, 2.0 ** power), return_lse=True), b)
+
+
+@pytest.mark.parametrize("d,new", [(128, 1), (128, 4), (64, 6)])
+def test_query_rows_of_different_sizes(d, new):
+    """Some heads' queries are 2^-112, 2^-115 or zero, and K's scales 2^112; a head of ordinary numbers among them, whose scores
+    are beyond any sense, changes nothing for the others."""
+    b = make_q8([300, 40], [new, 1], 8, 2, d, 16, BF, "int8", seed=4)
+    size = torch.full((new + 1, 8, 1), 2.0 ** -112, device="cuda")
+    size[:, 1] = 0.0
+    size[:, 5] = 2.0 ** -115
+    size[:, 6] = 0.0
+    q = b["q"]
+    o, lse = attend(scaled(b, size, 2.0 ** 112), return_lse=True)
+    check_q8(o, lse, b)
+    b["q"] = b["q"].clone()
+    b["q"][:, 1] = q[:, 1]
+    o2, lse2 = attend(b, return_lse=True)
+    others = [h for h in range(8) if h != 1]
+    assert torch.equal(o[:, others], o2[:, others]) and torch.equal(lse[:, others], lse2[:, others])
+
+
 @pytest.mark.parametrize("H", [2, 12])
 def test_fp16_queries_are_exact(H):
     """Rows of fp16 with its largest and its smallest numbers: what the small ones add to a score is not rounded."""
