@@ -60,6 +60,9 @@ __device__ unsigned int g_q8_error_word = 0;
 namespace {
 
 constexpr float kTau = 8.0f;
+// Exponents of V's weights.  Scales are 2^-109 (the smallest rows that a write keeps, in E4M3) to
+// 2^121: 2^7 over them, and the powers and their inverses are ordinary fp32 numbers.
+constexpr float kMostExp = 118.f, kLeastExp = -118.f;
 constexpr unsigned kErrLoad = 1u << 0;  // a wait for a stage gave up (the forward kernel's producer bit)
 
 template <int D, int NT>
@@ -407,7 +410,7 @@ struct Rows {
             mx[nt] = tx;
             const float2 g = fmul2(tx, f[nt]);
             grow |= g.x > 32768.f || g.y > 32768.f || (e[nt].x == -INFINITY && tx.x > 0.f) || (e[nt].y == -INFINITY && tx.y > 0.f) ||
-                    e[nt].x > 100.f || e[nt].y > 100.f;
+                    e[nt].x > kMostExp || e[nt].y > kMostExp;
         }
         if (__any_sync(~0u, grow)) {
 #pragma unroll
@@ -444,7 +447,7 @@ struct Rows {
         low *= al;
         if (m != -INFINITY) {  // w stays what it was
             e += v - m;
-            f = ex2_approx(fminf(e, 100.f));
+            f = ex2_approx(fminf(e, kMostExp));
         }
         m = v;
     }
@@ -453,10 +456,10 @@ struct Rows {
     {
         v = row_max(v);
         const bool none = e == -INFINITY;
-        float to = fminf(e, 100.f);
+        float to = fminf(e, kMostExp);
         if (v > 0.f && (none || v * ex2_approx(to) > 32768.f)) {
             const int x = static_cast<int>(__float_as_uint(v) >> 23) - 127;
-            to = static_cast<float>(max(-100, min(100, 7 - x)));
+            to = fmaxf(kLeastExp, fminf(kMostExp, static_cast<float>(7 - x)));
         }
         if (to == e) return;
         const float al = none ? 0.f : ex2_approx(to - e);
@@ -512,7 +515,7 @@ struct Rows {
 #pragma unroll
                     for (int i = 0; i < D / 16; i++)  // (zeros for a row that sees no key)
                         *reinterpret_cast<uint32_t *>(dst + i * 16) =
-                            sum == 0.f ? 0u : pack2<DT>(o[i][nt][h] * back * inv, o[i][nt][2 + h] * back * inv);
+                            sum == 0.f ? 0u : pack2<DT>(o[i][nt][h] * inv * back, o[i][nt][2 + h] * inv * back);
                     if (r4 == 0 && a.lse2) a.lse2[static_cast<int64_t>(q.q0 + tok) * a.H + hd] = sum == 0.f ? -INFINITY : mm + log2f(sum);
                 } else {
                     float *dst = part_o + (slot * p.rows_max + row - row0) * D + 2 * r4;

@@ -172,6 +172,47 @@ def test_query_rows_of_different_sizes(d, new):
     assert torch.equal(o[:, others], o2[:, others]) and torch.equal(lse[:, others], lse2[:, others])
 
 
+@pytest.mark.parametrize("H,new,d", [(8, 1, 64), (8, 1, 128), (32, 2, 128)])
+@pytest.mark.parametrize("power", [-107, 0, 100])
+def test_many_small_weights_of_values_of_any_size(H, new, d, power):
+    """One key with a weight of 1 and 30,000 with 2^-20 each, together 3% of a row: they count whatever V's scales are, down to
+    those of the smallest rows that a write keeps (2^-100 over 127).  400 requests of the same pages, so that the runs are long."""
+    N, S = 30000, 400
+    b = make_q8([N], [new], H, 4, d, 64, BF, "int8", seed=6)
+    (kc, ks), (vc, vs) = b["keys"][0]
+    kc.zero_()
+    kc[7, :, 3] = 127
+    ks.fill_(1.0)
+    vc.abs_().clamp_(min=20)
+    vc[7] = -vc[7]
+    vs.fill_(2.0 ** power)
+    at = torch.arange(N + new, device="cuda")
+    pages = b["block_table"][0].long()[at // 64]
+    for cache, scale, (c, x) in ((b["k_cache"], b["k_scale"], (kc, ks)), (b["v_cache"], b["v_scale"], (vc, vs))):
+        cache[pages, :, at % 64] = c
+        scale[pages, :, at % 64] = x
+    b["q"].zero_()
+    b["q"][:, :, 3] = 1.0
+    many = dict(b, q=b["q"].repeat(S, 1, 1), block_table=b["block_table"].repeat(S, 1), kv_len=b["kv_len"].repeat(S),
+                cu_q=torch.arange(0, new * S + 1, new, dtype=torch.int32, device="cuda"))
+    softmax_scale = 20 * math.log(2) / 127
+    o, lse = attend(many, softmax_scale=softmax_scale, return_lse=True)
+    one = dict(b, keys=[[(kc, ks), (vc, torch.ones_like(vs))]])
+    for r in range(0, new * S, new * 57):
+        check_q8(o[r:r + new].double() * 2.0 ** -power, lse[r:r + new], one, scale=softmax_scale)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("power,columns", [(-102, 0), (-102, 300), (125, 0), (125, 300)])
+@pytest.mark.parametrize("new,H,d", [(1, 4, 128), (3, 12, 64)])
+def test_values_of_any_size(new, H, d, power, columns, code):
+    """V's rows near the smallest that a write keeps and near bf16's largest numbers (three keys: their sum must fit 32 bits)."""
+    b = make_q8([2, 1], [new, 1], H, 2, d, 16, BF, code, seed=9, columns=columns, spread=0.0)
+    b["v_scale"] = b["v_scale"] * 2.0 ** power
+    o = attend(b)
+    check_q8(o.double() * 2.0 ** -power, None, b)
+
+
 @pytest.mark.parametrize("H", [2, 12])
 def test_fp16_queries_are_exact(H):
     """Rows of fp16 with its largest and its smallest numbers: what the small ones add to a score is not rounded."""
