@@ -899,7 +899,12 @@ int paged_q8_rows(const PagedArgs &a, int64_t max_q, int nsm)
     // kernel costs half: 6) for each of 1,216 workers.  (The chunk kernel with what it needs takes 40
     // to 55 us at least.  d = 128: 80 rows over 16,080 keys of 8 heads, 16.5 units, 51 us here
     // against 68; 160 rows of 4 x 4,040 keys, 16.7, 43 against 56; 2,048 rows over 712 keys, 19.4, 69
-    // against 54.  d = 64: 160 rows, 5.9, 35 against 42; 2,048 rows, 6.8, 48 against 41.)
+    // against 54.  d = 64: 160 rows, 5.9, 35 against 42; 2,048 rows, 6.8, 48 against 41.  Up to 64 rows, 8
+    // heads, here against there: 64 requests of 1,000 to 16,000 keys, int8, d = 128, 20, 32 and 64 rows 418,
+    // 427 and 831 against 1,011, 998 and 1,001, E4M3 876 for 64 against 993; d = 64 174, 260 and 472 against 625,
+    // 609 and 611.  17 of 562 to 9,001 keys 85, 89 and 158 against 217; 8 of 1,875 to 30,000 113, 113 and 208
+    // against 287; 64 of 125 to 2,000 90, 97 and 168 against 194, and only at d = 64, 64 rows, it is 143
+    // against 135, E4M3 173 against 137.)
     const int g = a.H / a.Hkv, tile = a.d == 64 ? 24 : 16, keys = 4096 / a.d;
     const int64_t rows = max_q <= 2048 ? max_q * g : 2049;
     if (rows <= 64) return static_cast<int>(rows);

@@ -2,7 +2,8 @@
 // ranges of the sequences' tokens (to move, inspect or use them in a dense call), or
 // whole pages for the chunk kernel, which works on 16-bit tiles.
 //
-//   x = code * scale, rounded once to the data type (a cache of 16-bit values is copied)
+//   x = code * scale, rounded to fp32 and then to the data type (a cache of 16-bit values is
+//   copied): off by half a step of the data type and by 2^-24 of the value
 //
 // Bound: bytes, d + 4 read and 2 d written per row.  A thread turns 8 codes into one 16-byte
 // store, so that a warp's stores fill whole lines; eight such pieces are in flight at a time,

@@ -669,7 +669,7 @@ CLIS_API clis_status_t clis_paged_append_q8(const clis_paged_t *desc, const clis
  *   desc        S, T (rows of the outputs), Hkv, d, page_size, num_pages, width, kc_s*,
  *               vc_s*, bt_ss, dtype; T up to 2^27
  *   quant       NULL: a cache of 16-bit values, which are copied (scales may be NULL);
- *               else codes: code * scale, rounded once
+ *               else codes: code * scale, rounded to fp32 and then to the data type
  *   cu          device int32 [S + 1], from 0 on, not falling
  *   start       device int32 [S], or NULL (0)
  *   k_out, v_out  device [T, Hkv, d], strides k_st, k_sh, v_st, v_sh; must not overlap
@@ -692,7 +692,7 @@ CLIS_API clis_status_t clis_paged_read(const clis_paged_t *desc, const clis_quan
  * least 2^-32 of the row's largest), q is exact in fp16, and in bf16 where it is within 2^-32 of
  * its row's largest value.  Else that kernel serves single tokens, and the other sequences (all of them
  * where the tables can hold no more than 16 MB of codes) are unpacked to 16 bits first (K's
- * codes, exact, its scales applied to the scores; V's values, rounded once to the data type)
+ * codes, exact, its scales applied to the scores; V's values, rounded as clis_paged_read does)
  * and run the chunk kernel of clis_attn_fwd_paged; the workspace then holds a 16-bit copy
  * of as many pages as the tables have places (S * width) or the cache has (one layer's), whichever
  * is less.
@@ -723,8 +723,10 @@ CLIS_API clis_status_t clis_attn_fwd_paged_q8(const clis_paged_t *desc, const cl
  *   out_scores, parent, token  device fp32, int32, int32 [R, K]
  *   workspace    device scratch of clis_beam_workspace_size() bytes (on the current
  *                device), 256-byte aligned; not shared by calls that may run at the same time
- * Values are compared to 48 bits, with a logarithm off by about 1e-7.  Reruns agree bit
- * for bit.  Errors as for clis_attn_fwd; CLIS_ERR_WORKSPACE. */
+ * Values are compared to 48 bits, with logarithms off by at most 4e-6 (up to 2^18 tokens; measured
+ * 3e-7).  So the order is that of the logits within a beam (those that differ by less than the 48
+ * bits tie), and between beams that of values further apart than the logarithms' errors; beams of
+ * equal logits have equal logarithms.  Reruns agree bit for bit.  Errors as for clis_attn_fwd; CLIS_ERR_WORKSPACE. */
 typedef struct {
     int64_t R, W, V, K;
     int64_t dtype;
