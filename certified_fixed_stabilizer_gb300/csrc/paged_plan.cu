@@ -85,10 +85,11 @@ __device__ __forceinline__ int shared_pages(const PlanArgs &a, int s, const Seq 
     return most;
 }
 
+template <bool BEAMS>
 __device__ __forceinline__ Sums sums_of(const PlanArgs &a, int s, const Seq &q)
 {
     return {min(static_cast<uint32_t>(q.n), kCap), static_cast<uint32_t>(q.need - q.have),
-            q.gone ? static_cast<uint32_t>(q.have - (a.beams > 1 ? shared_pages(a, s, q) : 0)) : 0u};
+            q.gone ? static_cast<uint32_t>(q.have - (BEAMS ? shared_pages(a, s, q) : 0)) : 0u};
 }
 
 // Last s with first[s] <= i, for i < first[S] (first is non-decreasing).
@@ -103,6 +104,8 @@ __device__ __forceinline__ int find(const uint32_t *first, int S, uint32_t i)
     return lo;
 }
 
+// BEAMS: rows share pages.  (A constant: as a condition it cost plans with finished rows 0.5 us.)
+template <bool BEAMS>
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs a)
 {
     extern __shared__ uint32_t sm[];
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
     for (int s = s0; s < s1; s++) {
         const Seq q = read_seq(a, s);
         if (q.full) bad |= CLIS_PAGED_LENGTH_BIT;
-        mine = add(mine, sums_of(a, s, q));
+        mine = add(mine, sums_of<BEAMS>(a, s, q));
     }
     Sums incl = mine;
 #pragma unroll
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
         s_tok[s] = run.tok;
         s_taken[s] = run.taken;
         s_back[s] = run.back;
-        run = add(run, sums_of(a, s, read_seq(a, s)));
+        run = add(run, sums_of<BEAMS>(a, s, read_seq(a, s)));
     }
     // (the totals: from the thread with the last sequence, or zeros without any)
     if ((s0 < a.S && s1 == a.S) || (a.S == 0 && tid == 0)) {
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
             continue;
         }
         int col = static_cast<int>(i - s_back[s]);
-        if (a.beams > 1) col += read_seq(a, s).have - static_cast<int>(s_back[s + 1] - s_back[s]);  // (behind those that stay)
+        if (BEAMS) col += read_seq(a, s).have - static_cast<int>(s_back[s + 1] - s_back[s]);  // (behind those that stay)
         const int page = a.block_table[s * a.bt_s + col];
         if (page < 0 || page >= a.num_pages) bad |= CLIS_PAGED_INDEX_BIT;
         a.ring[(tm + i) % Fu] = page;
@@ -241,16 +244,16 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 
 clis_status_t launch_paged_plan(const PlanArgs &a, cudaStream_t stream)
 {
+    const auto kernel = a.beams > 1 ? paged_plan_kernel<true> : paged_plan_kernel<false>;
     const size_t smem = 3 * sizeof(uint32_t) * (static_cast<size_t>(a.S) + 1);
     if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return CLIS_ERR_CUDA;
     // About two tokens a thread, one block per SM at most (90,000 tokens: 8.5 us a call with
     // one or two, 10.3 with four).
     int64_t blocks = (static_cast<int64_t>(a.T) + 2 * kPlanThreads - 1) / (2 * kPlanThreads);
     blocks = blocks < 1 ? 1 : blocks > 152 ? 152 : blocks;
-    paged_plan_kernel<<<static_cast<unsigned>(blocks), kPlanThreads, smem, stream>>>(a);
+    kernel<<<static_cast<unsigned>(blocks), kPlanThreads, smem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? CLIS_OK : CLIS_ERR_CUDA;
 }
 
