@@ -136,6 +136,31 @@ def test_far_logits():
     assert ((got.scores.cpu().double() - best).abs() <= 4e-6 + 2.0 ** -24 * best.abs()).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V", [1000, 40009])
+def test_masked_by_the_lowest_value(dtype, V):
+    """Masks of the type's lowest number instead of -inf: such words are candidates behind all others, and a row of
+    nothing else is as good as any constant one, log V below its score (in 64 bits the logarithm is lost beside such numbers,
+    so the reference takes the maximum off first)."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    low = torch.finfo(DT[dtype]).min
+    logits = (3 * torch.randn((3, 4, V), generator=g, device="cuda")).to(DT[dtype])
+    logits[:, :, torch.rand(V, generator=g, device="cuda") < 0.5] = low
+    logits[1, 2] = low
+    logits[2] = low
+    scores = -torch.rand((3, 4), generator=g, device="cuda")
+    scores[1, 2] = 12.0
+    got = clis.beam_select(logits, scores, 40)
+    x = logits.double().cpu()
+    x = x - x.amax(-1, keepdim=True)
+    v = (scores.double().cpu()[..., None] + (x - x.exp().sum(-1, keepdim=True).log())).flatten(1)
+    best, at = torch.sort(v, dim=-1, descending=True, stable=True)
+    best, at = best[:, :40], at[:, :40]
+    assert torch.equal(got.parent.cpu(), (at // V).int()) and torch.equal(got.token.cpu(), (at % V).int())
+    assert (got.parent[1] == 2).any() and got.token[2].tolist() == list(range(40))
+    assert ((got.scores.cpu().double() - best).abs() <= 4e-6 + 2.0 ** -24 * best.abs()).all()
+
+
 def test_strided_logits_and_no_requests():
     g = torch.Generator(device="cuda").manual_seed(9)
     big = torch.randn((3, 6, 2100), generator=g, device="cuda").to(torch.float16)
