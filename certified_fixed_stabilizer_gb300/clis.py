@@ -1100,7 +1100,7 @@ class PagedCache:
         scales = [] if self.k_scale is None else [self.k_scale, self.v_scale]
         r = clis_paged_reorder(self.lens, parent, self.block_table, self.ring, self.ring_state, [self.k, self.v], scales,
                                out=self.block_table)
-        self.beams = max(self.beams, parent.shape[1])
+        self.beams = math.lcm(self.beams, parent.shape[1])  # (requests of another size before: groups that hold both)
         self.lens.copy_(r.lens)
         self.ring_state.copy_(r.ring_state)
         return r.done

@@ -469,7 +469,7 @@ clis_status_t clis_paged_plan_beams(const clis_paged_t *desc, int64_t beams, con
     const clis_status_t st = check_table(desc);
     if (st != CLIS_OK) return st;
     if (beams < 1 || desc->S % beams) return CLIS_ERR_INVALID_ARG;
-    if (beams > clis::kMaxBeams) return CLIS_ERR_UNSUPPORTED;
+    if (beams > kMaxSeqs) return CLIS_ERR_UNSUPPORTED;  // (S = 0)
     if (desc->S > 1 && desc->bt_ss < desc->width) return CLIS_ERR_INVALID_ARG;  // rows are written
     if (ring_size < 1) return CLIS_ERR_INVALID_ARG;
     if (ring_size > kMaxN) return CLIS_ERR_UNSUPPORTED;

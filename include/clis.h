@@ -573,7 +573,8 @@ CLIS_API clis_status_t clis_paged_plan(const clis_paged_t *desc, const int32_t *
  * + beams - 1 of the table are the beams of request r.  A finished row gives back the pages that
  * no row of its request names any more that goes on or is finished before it; clis_paged_plan
  * (beams = 1) would give a shared page back once for each row.
- *   beams        1 .. 64 (CLIS_ERR_UNSUPPORTED), S a multiple of it (CLIS_ERR_INVALID_ARG) */
+ *   beams        rows of a request, or of several (a multiple of its beams will do): S is a
+ *                multiple of it (CLIS_ERR_INVALID_ARG otherwise) */
 CLIS_API clis_status_t clis_paged_plan_beams(const clis_paged_t *desc, int64_t beams, const int32_t *ctx_len,
                                              const int32_t *new_len, int32_t *block_table, int32_t *ring,
                                              int64_t ring_size, const int64_t *state_in, int64_t *state_out,

@@ -534,6 +534,21 @@ def test_plan_of_beams_against_a_host_loop(R, W, page, width):
         assert p.kv_len.tolist() == [n + m if m >= 0 else 0 for n, m in zip(lens, new)]
 
 
+def test_requests_of_another_number_of_beams():
+    """A cache that served requests of three beams serves requests of two: rows 2 and 3 share pages then."""
+    cache = clis.PagedCache(layers=1, num_pages=40, num_kv_heads=1, d=64, max_seqs=6, max_len=64, page_size=8)
+    i32 = {"dtype": torch.int32, "device": "cuda"}
+    for W in (3, 2):
+        cache.begin(torch.tensor([17 if r % W == 0 else 0 for r in range(6)], **i32), 60)
+        assert cache.reorder(torch.zeros((6 // W, W), **i32)).tolist() == [1] * (6 // W)
+        cache.begin(torch.ones(6, **i32), 6)
+        check_pages(cache)
+        cache.begin(torch.tensor([-1, 1, -1, 0, 1, -1], **i32), 6)
+        check_pages(cache)
+        cache.begin(torch.full((6,), -1, **i32), 6)
+        check_pages(cache)
+
+
 def test_a_step_of_the_search_in_a_graph():
     """Plan, write, attention, selection and reordering captured once and replayed, against the same steps made one by one."""
     R, W, H, Hk, d, V = 2, 3, 4, 2, 64, 1000

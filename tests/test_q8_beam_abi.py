@@ -109,7 +109,7 @@ def test_plan_of_beams_refusals():
     def plan(desc, beams):
         return clis.load_library().clis_paged_plan_beams(desc, beams, *[FAKE + 64 * i for i in range(4)], 50, *[FAKE + 64 * i for i in range(4, 10)], None)
 
-    for beams, S, st in ((0, 3, INVALID), (-1, 3, INVALID), (2, 3, INVALID), (4, 6, INVALID), (65, 130, UNSUPPORTED)):
+    for beams, S, st in ((0, 3, INVALID), (-1, 3, INVALID), (2, 3, INVALID), (4, 6, INVALID), (7, 6, INVALID), (16385, 0, UNSUPPORTED)):
         assert plan(paged_desc(S=S), beams) == st, beams
     assert plan(None, 1) == INVALID
 
