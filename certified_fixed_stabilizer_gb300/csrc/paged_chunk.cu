@@ -58,7 +58,7 @@
 // key's scale (with scale_log2) multiplies its scores as they come from TMEM, in the same
 // instruction that subtracts the shift: what the weights take is then ready, and the first half is
 // scaled while the second is on its way.  The call of 2,048 tokens behind 30,011 takes 819
-// to 850 us (40 of them unpacking, paged_read.cu; without the multiplications 739), off by 2.5e-3.  With
+// to 861 us (40 of them unpacking, paged_read.cu; without the multiplications 739), off by 2.5e-3.  With
 // scales multiplied in by themselves, all scores loaded before, it took 851; with the values of K
 // and V rounded to bf16 808, off by 4.4e-3.  A thread reads 128 scales a tile, 128 cycles of the
 // register file's port for each of 8 warps, which is what is left of the difference.

@@ -45,7 +45,7 @@
 //    it was.  w is rounded to fp16 as the matrix instructions take it (off by up to 2^-11,
 //    and by 2^-32 of the row's largest below that).
 //
-// 64 requests of 1,000 to 16,000 keys (8 key/value heads of d = 128, int8, 1.23 GB): 202 to 207 us
+// 64 requests of 1,000 to 16,000 keys (8 key/value heads of d = 128, int8, 1.23 GB): 202 to 209 us
 // with the join for 4 query heads a key (89% of the measured copy rate; 254 with 16-row products
 // of all heads and 16-byte copies), 215 to 231 for 16 rows.  Drafted tokens, 20 or more rows a
 // sequence: 41 us where the bytes alone would take 10.5: a warp spends 2.1 us on a unit.
